@@ -13,11 +13,13 @@ with ``own``, through the library's calls.
 
 The cache is a pool of pages of ``page`` tokens.  A page holds, per key/value head, page/16
 records of 16 tokens; a record of 18 * dim bytes holds the keys' codes, the keys' scales,
-the values' codes and the values' scales (G = dim / 32 blocks of 32 per token and head):
+the values' codes and the values' scales (G = dim / 32 blocks of 32 per token and head, in
+G / I sets of I = min(G, 4); block g is g % I of set g / I):
 
-    key codes    [16 tokens][4 c][G g] uint32: nibble j of a word is dim 32 g + 8 c + j
+    key codes    [set][16 tokens][4 c][I] uint32: nibble j of a word is dim 32 g + 8 c + j
     scales       [8 token pairs][G g][2 tokens] fp16
-    value codes  [8 token pairs][8 r][G g][2 tokens] uint16: nibble j is dim 32 g + 4 r + j
+    value codes  [set][2 halves][8 r][4 pairs of the half][I][2 tokens] uint16: nibble j is
+                 dim 32 g + 4 r + j
 
 A value is (nibble - 8) * scale.
 """
@@ -130,14 +132,16 @@ def quantize(x):
 
 
 def key_bytes(codes):
-    """[..., D] codes -> [..., D / 2] bytes in the order of a key row."""
-    w = codes.unflatten(-1, (-1, 4, 8)).transpose(-3, -2)             # [..., c, g, j]
-    return (w[..., 0::2] | (w[..., 1::2] << 4)).flatten(-3)
+    """[..., D] codes -> [..., set, 4 c, I, 4] bytes: a token's words."""
+    D = codes.shape[-1]
+    w = codes.unflatten(-1, (-1, min(D // 32, 4), 4, 8)).transpose(-3, -2)      # [..., set, c, i, j]
+    return w[..., 0::2] | (w[..., 1::2] << 4)
 
 
 def value_bytes(codes):
-    """[..., D] codes -> [..., 8 r, G, 2] bytes: a token's halfwords."""
-    w = codes.unflatten(-1, (-1, 8, 4)).transpose(-3, -2)             # [..., r, g, j]
+    """[..., D] codes -> [..., set, 8 r, I, 2] bytes: a token's halfwords."""
+    D = codes.shape[-1]
+    w = codes.unflatten(-1, (-1, min(D // 32, 4), 8, 4)).transpose(-3, -2)      # [..., set, r, i, j]
     return w[..., 0::2] | (w[..., 1::2] << 4)
 
 
@@ -151,8 +155,9 @@ def records(k, v):
 
     kc, kd = quantize(k)
     vc, vd = quantize(v)
-    vb = value_bytes(vc).view(n, 8, 2, 8, G, 2).permute(0, 1, 3, 4, 2, 5)
-    return torch.cat([key_bytes(kc).reshape(n, -1), scales(kd), vb.reshape(n, -1), scales(vd)], 1)
+    kb = key_bytes(kc).transpose(1, 2)                                 # [n, set, 16, c, i, 4]
+    vb = value_bytes(vc).unflatten(1, (2, 4, 2)).permute(0, 4, 1, 5, 2, 6, 3, 7)
+    return torch.cat([kb.reshape(n, -1), scales(kd), vb.reshape(n, -1), scales(vd)], 1)
 
 
 def rotations(n_pos, rot, dev):
@@ -332,7 +337,7 @@ def plain_norm_rope_op(s):
 def plain_append(s):
     c = s["case"]
     act, Hk, D, P = ACT[c["act"]], c["kv_heads"], c["dim"], c["page"]
-    G = D // 32
+    G, I = D // 32, min(D // 32, 4)
     q, k, v = plain_norm_rope(s["q"], s["q_weight"], s), plain_norm_rope(s["k"], s["k_weight"], s), s["v"].float()
     kc, kd = quantize(k)
     vc, vd = quantize(v)
@@ -342,8 +347,8 @@ def plain_append(s):
     def part(at, width, *shape):
         return pool[..., at:at + width].unflatten(-1, shape)
 
-    part(0, 8 * D, 16, D // 2)[page, :, rec, t] = key_bytes(kc)
-    part(9 * D, 8 * D, 8, 8, G, 2, 2)[page, :, rec, t // 2, :, :, t % 2] = value_bytes(vc)
+    part(0, 8 * D, G // I, 16, 4, I, 4)[page, :, rec, :, t] = key_bytes(kc)
+    part(9 * D, 8 * D, G // I, 2, 8, 4, I, 2, 2)[page, :, rec, :, t // 8, :, t // 2 % 4, :, t % 2] = value_bytes(vc)
     for at, d in ((8 * D, kd), (17 * D, vd)):
         part(at, D, 8, G, 2, 2)[page, :, rec, t // 2, :, t % 2] = d.contiguous().view(torch.uint8).view(-1, Hk, G, 2)
 
@@ -361,15 +366,17 @@ def plain_cache(s):
     """Keys and values of every request, fp32 [n_req, kv_heads, padded length, D]."""
     c = s["case"]
     Hk, D, P = c["kv_heads"], c["dim"], c["page"]
-    G = D // 32
+    G, I = D // 32, min(D // 32, 4)
     rec = s["pool"].view(-1, Hk, P // 16, 18 * D)[s["table"].clamp(min=0).long()].transpose(1, 2).flatten(2, 3)
 
     def scales(at):
         d = rec[..., at:at + D].contiguous().view(torch.float16).float()
         return d.unflatten(-1, (8, G, 2)).transpose(-1, -2).reshape(*d.shape[:2], -1, G, 1)
 
-    k = nibbles(rec[..., :8 * D].unflatten(-1, (16, 4, G, 4))).transpose(-2, -3).flatten(2, 3).flatten(-2)
-    v = nibbles(rec[..., 9 * D:17 * D].unflatten(-1, (8, 8, G, 2, 2))).permute(0, 1, 2, 3, 6, 5, 4, 7).flatten(2, 4).flatten(-2)
+    # [n, head, record, set, 16, c, i, 8] and [n, head, record, set, half, r, pair, i, 2, 4] -> [n, head, token, G, 32]
+    k = nibbles(rec[..., :8 * D].unflatten(-1, (G // I, 16, 4, I, 4))).permute(0, 1, 2, 4, 3, 6, 5, 7)
+    v = nibbles(rec[..., 9 * D:17 * D].unflatten(-1, (G // I, 2, 8, 4, I, 2, 2))).permute(0, 1, 2, 4, 6, 8, 3, 7, 5, 9)
+    k, v = (x.reshape(*x.shape[:2], -1, G, 32) for x in (k, v))
     k = ((k.float() - 8) * scales(8 * D)).flatten(-2)
     v = ((v.float() - 8) * scales(17 * D)).flatten(-2)
     return k, v
@@ -475,12 +482,13 @@ def exact_attention(s):
     """Request by request, each nibble fetched from its own place in the pool."""
     c = s["case"]
     Hq, Hk, D, P = c["heads"], c["kv_heads"], c["dim"], c["page"]
-    G, dev, pool = D // 32, s["q"].device, s["pool"]
+    G, I, dev, pool = D // 32, min(D // 32, 4), s["q"].device, s["pool"]
     half = pool.view(torch.float16)
     dim = torch.arange(D, device=dev)
     g, rest = dim // 32, dim % 32
-    k_byte, k_shift = ((rest // 8) * G + g) * 4 + rest % 8 // 2, dim % 2 * 4
-    v_byte, v_shift = (rest // 4) * G * 4 + g * 4 + rest % 4 // 2, dim % 2 * 4
+    shift = dim % 2 * 4
+    k_byte = (g // I * 64 + rest // 8) * I * 4 + g % I * 4 + rest % 8 // 2
+    v_byte = (g // I * 64 + rest // 4 * 4) * I * 4 + g % I * 4 + rest % 4 // 2
     outs, lses = [], []
     seq, cu = s["seq_len"].tolist(), s["cu_new"].tolist()
     for r in range(c["n_req"]):
@@ -491,8 +499,8 @@ def exact_attention(s):
         head = torch.arange(Hk, device=dev)[:, None]
         rec = (((page * Hk + head) * (P // 16) + t % P // 16) * 18 * D)[..., None]      # [Hk, keys, 1]
         u = (t % 16)[:, None]
-        k = ((pool[rec + u * (D // 2) + k_byte] >> k_shift) & 15).double() - 8
-        v = ((pool[rec + 9 * D + (u // 2) * 8 * G * 4 + u % 2 * 2 + v_byte] >> v_shift) & 15).double() - 8
+        k = ((pool[rec + u * 16 * I + k_byte] >> shift) & 15).double() - 8
+        v = ((pool[rec + 9 * D + (u // 8 * 32 + u // 2 % 4) * I * 4 + u % 2 * 2 + v_byte] >> shift) & 15).double() - 8
         sc = (u // 2) * G * 2 + g * 2 + u % 2
         k *= half[(rec + 8 * D) // 2 + sc].double()
         v *= half[(rec + 17 * D) // 2 + sc].double()
