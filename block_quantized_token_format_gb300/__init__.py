@@ -26,6 +26,9 @@ __all__ = [
     "QG_DEVICE_BAD_PLAN", "QG_EXPERTS_X_BY_SLOT", "QG_EXPERTS_PLAN_READY",
     "QG_EXPERTS_SWIGLU", "qgemv_expert_layer", "qgemv_expert_layer_workspace_bytes",
     "qg_set_phase_record", "QG_PHASE_WORDS", "QG_PHASE_SLOT_WORDS",
+    "qg_cache", "qg_cache_bytes", "qg_cache_pages", "qg_qk_norm_rope", "qg_cache_append", "qg_attention",
+    "qg_attention_workspace_bytes", "QG_CACHE_MAX", "QG_ATTENTION_ZERO_BYTES", "QG_DEVICE_BAD_PAGE",
+    "QG_DEVICE_BAD_LENGTH", "QG_DEVICE_NO_PAGES", "QG_ACT_F32", "QG_ACT_BF16",
 ]
 
 QG_Q8_0, QG_Q4_0, QG_AFFINE4_G64, QG_BF16, QG_Q5_0 = 0, 1, 2, 3, 4
@@ -61,6 +64,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         pass
     lib = ctypes.CDLL(p)
     i64, vp, sz, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+    u32, f32, cache = ctypes.c_uint, ctypes.c_float, ctypes.POINTER(qg_cache)
     sig = {
         "qg_strerror": (ctypes.c_char_p, [i32]),
         "qg_abi_version": (i32, []),
@@ -87,6 +91,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "qgemv_experts": (i32, [i32, vp, i64, i64, i64, vp, i64, ctypes.c_uint, vp, i64, vp, vp, i64, i64, vp]),
         "qg_describe_expert_tile": (i32, [i32, i64, i64, ctypes.c_char_p, sz]),
         "qgemv_expert_layer_workspace_bytes": (sz, []),
+        "qg_cache_bytes": (sz, [i64, i32, i32, i32]),
+        "qg_cache_pages": (i32, [vp, vp, i32, i32, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, i64, vp]),
+        "qg_qk_norm_rope": (i32, [i32, vp, i64, vp, i64, i64, i32, i32, i32, vp, vp, f32, u32, vp, i64, i32, vp, vp, i64,
+                                  vp, i64, vp]),
+        "qg_cache_append": (i32, [cache, i32, vp, i64, vp, i64, vp, i64, i64, i32, vp, vp, f32, u32, vp, i64, i32, vp, vp,
+                                  vp, i64, vp, vp, vp]),
+        "qg_attention_workspace_bytes": (sz, [i32, i32, i32]),
+        "qg_attention": (i32, [cache, i32, vp, i64, i64, i32, vp, i64, vp, vp, i32, i32, i32, vp, f32, vp, i64, vp, vp, sz,
+                               vp]),
         "qgemv_expert_layer": (i32, [i32, vp, vp, i64, i64, i64, vp, i32, vp, i32, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -95,6 +108,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+class qg_cache(ctypes.Structure):
+    """A paged key/value cache in 4 bits: ``data`` (a CUDA uint8 tensor of ``qg_cache_bytes``
+    bytes, which this object keeps alive, or a device address) and its shape."""
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_tokens", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+    def __init__(self, data, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int):
+        super().__init__(_ptr(data), int(n_pages), int(page_tokens), int(n_kv_heads), int(head_dim))
+        if hasattr(data, "numel"):
+            need = qg_cache_bytes(n_pages, page_tokens, n_kv_heads, head_dim)
+            if need == 0 or data.numel() * data.element_size() < need or not data.is_contiguous():
+                raise ValueError("qg_cache: data must be a contiguous tensor of at least qg_cache_bytes() bytes")
+        self.tensor = data
 
 
 def _ptr(t) -> int | None:
@@ -329,6 +357,161 @@ def qg_device_status(clear: bool = True) -> int:
 def qg_set_wait_limit(polls: int = 0, extra_tx_bytes: int = 0) -> None:
     """Test hook: mbarrier polls before a wait gives up (0 = default) and extra expected bytes."""
     _check(load_library().qg_set_wait_limit(int(polls), int(extra_tx_bytes)), "qg_set_wait_limit")
+
+
+# ------------------------------------------------------------- key/value cache in 4 bits
+
+QG_ACT_F32, QG_ACT_BF16 = 0, 1
+QG_ROPE_INTERLEAVED, QG_NORM_UNIT_OFFSET, QG_NORM_NONE = 1, 2, 4
+QG_CACHE_MAX = 16384.0
+QG_ATTENTION_ZERO_BYTES = 4096
+QG_DEVICE_BAD_PAGE = 8
+QG_DEVICE_BAD_LENGTH = 16
+QG_DEVICE_NO_PAGES = 32
+_ACT = {"torch.float32": QG_ACT_F32, "torch.bfloat16": QG_ACT_BF16}
+
+
+def _act(t) -> int:
+    a = _ACT.get(str(t.dtype))
+    if a is None:
+        raise TypeError(f"activations are float32 or bfloat16 tensors, not {t.dtype}")
+    return a
+
+
+def _heads(t, act: int, name: str):
+    """(address, token stride, tokens, heads, head_dim) of ``[n_tok, heads, head_dim]``
+    activations whose heads are contiguous (a slice of a projection's row is)."""
+    n, h, d = t.shape
+    st = t.stride()
+    if (h > 1 and st[1] != d) or st[2] != 1 or _act(t) != act:
+        raise ValueError(f"{name}: [n_tok, heads, head_dim] of one type, heads contiguous, is needed")
+    return t.data_ptr(), (st[0] if n > 1 else max(st[0], h * d)), n, h, d
+
+
+def _typed(t, dtype: str, name: str, numel: int | None = None):
+    """Address of a contiguous tensor of ``dtype`` with at least ``numel`` entries."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype) not in ("torch." + dtype,) or not t.is_contiguous() or (numel is not None and t.numel() < numel):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if numel is None else f' of {numel} entries'} is needed")
+    return t.data_ptr()
+
+
+def _table(table, n_req: int):
+    if table.dim() != 2 or str(table.dtype) != "torch.int32" or table.shape[0] < n_req or not table.is_contiguous():
+        raise ValueError("table: a contiguous int32 [n_req, width] tensor is needed")
+    return table.data_ptr(), int(table.shape[1])
+
+
+def qg_cache_bytes(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(load_library().qg_cache_bytes(int(n_pages), int(page_tokens), int(n_kv_heads), int(head_dim)))
+
+
+def qg_cache_pages(held, fresh, free_pages, table, seq_len, cu_new, slots, positions, page_tokens: int,
+                   free_begin=None, free_end=None, stream=None) -> None:
+    """Enqueue a step's block table, slots and positions: requests hold ``held`` tokens and add
+    ``fresh`` (int32 ``[n_req]``); pages are dealt from ``free_pages`` (int32) starting at
+    ``free_begin[0]``.  Writes the new entries of ``table`` (int32 ``[n_req, width]``),
+    ``seq_len``, ``cu_new`` (int32 ``[n_req + 1]``), ``slots`` (int64) and ``positions`` (int32)
+    of all new tokens, and ``free_end[0]`` (``free_begin`` itself may be passed)."""
+    n = int(held.shape[0])
+    tp, width = _table(table, n)
+    n_tok = int(slots.numel())
+    st = load_library().qg_cache_pages(
+        _typed(held, "int32", "held"), _typed(fresh, "int32", "fresh", n), n, int(page_tokens),
+        _typed(free_pages, "int32", "free_pages"), int(free_pages.numel()), _typed(free_begin, "int32", "free_begin", 1),
+        _typed(free_end, "int32", "free_end", 1), tp, width, _typed(seq_len, "int32", "seq_len", n), _typed(cu_new, "int32", "cu_new", n + 1), _typed(slots, "int64", "slots"),
+        _typed(positions, "int32", "positions", n_tok), n_tok, _stream(stream))
+    _check(st, "qg_cache_pages")
+
+
+def _rotation(cos_sin, positions, n_tok: int):
+    if cos_sin is None:
+        return None, 0, 0, _typed(positions, "int32", "positions", n_tok)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin: float32 [n_pos, rot_dim] is needed")
+    return (_typed(cos_sin, "float32", "cos_sin"), int(cos_sin.shape[0]), int(cos_sin.shape[1]),
+            _typed(positions, "int32", "positions", n_tok))
+
+
+def _head_flags(norm: bool, unit_offset: bool, interleaved: bool) -> int:
+    return ((QG_ROPE_INTERLEAVED if interleaved else 0) | (QG_NORM_UNIT_OFFSET if unit_offset else 0)
+            | (0 if norm else QG_NORM_NONE))
+
+
+def qg_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    norm: bool = True, unit_offset: bool = False, interleaved: bool = False, stream=None) -> None:
+    """Enqueue the RMS norm of every query and key head (``[n_tok, heads, head_dim]``, float32 or
+    bfloat16; slices of one projection's rows are taken as they are) and the rotation by
+    ``cos_sin[positions]`` (``[n_pos, rot_dim]``: cosines, then sines) in one pass."""
+    act = _act(q)
+    qp, qs, n, hq, d = _heads(q, act, "q")
+    kp, ks, nk, hk, dk = _heads(k, act, "k")
+    qo, qos, nqo, hqo, dqo = _heads(q_out, act, "q_out")
+    ko, kos, nko, hko, dko = _heads(k_out, act, "k_out")
+    if not (n == nk == nqo == nko and d == dk == dqo == dko and hq == hqo and hk == hko):
+        raise ValueError("qg_qk_norm_rope: q, k and their outputs differ in tokens, heads or head_dim")
+    cs, n_pos, rot, pos = _rotation(cos_sin, positions, n)
+    st = load_library().qg_qk_norm_rope(act, qp, qs, kp, ks, n, hq, hk, d, _typed(q_weight, "float32", "q_weight", d),
+                                        _typed(k_weight, "float32", "k_weight", d), eps,
+                                        _head_flags(norm, unit_offset, interleaved), cs, n_pos, rot, pos, qo, qos, ko, kos,
+                                        _stream(stream))
+    _check(st, "qg_qk_norm_rope")
+
+
+def qg_cache_append(cache: qg_cache, k, v, slots, q=None, q_out=None, positions=None, cos_sin=None, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, norm: bool = True, unit_offset: bool = False,
+                    interleaved: bool = False, k_back=None, v_back=None, stream=None) -> None:
+    """Enqueue qg_qk_norm_rope's norm and rotation with the keys and the values (``v``: as they
+    are) quantized into ``cache`` at ``slots`` (int64 ``[n_tok]``, -1 = none); queries go to
+    ``q_out``.  ``k_back`` / ``v_back`` receive the values the cache now stands for."""
+    act = _act(k)
+    kp, ks, n, hk, d = _heads(k, act, "k")
+    vp, vs, nv, hv, dv = _heads(v, act, "v")
+    qp = qs = qo = qos = hq = 0
+    if q is not None:
+        qp, qs, nq, hq, dq = _heads(q, act, "q")
+        qo, qos, nqo, hqo, dqo = _heads(q_out, act, "q_out")
+        if not (nq == nqo == n and dq == dqo == d and hq == hqo):
+            raise ValueError("qg_cache_append: q and q_out differ from k in tokens or head_dim")
+    if not (nv == n and hk == hv == cache.n_kv_heads and d == dv == cache.head_dim):
+        raise ValueError("qg_cache_append: k and v do not fit the cache's heads")
+    for t, name in ((k_back, "k_back"), (v_back, "v_back")):
+        if t is not None and (_act(t) != act or not t.is_contiguous() or t.numel() < n * hk * d):
+            raise ValueError(f"{name}: a contiguous [n_tok, n_kv_heads, head_dim] tensor of k's type is needed")
+    cs, n_pos, rot, pos = _rotation(cos_sin, positions, n)
+    st = load_library().qg_cache_append(cache, act, qp or None, qs, kp, ks, vp, vs, n, hq,
+                                        _typed(q_weight, "float32", "q_weight", d),
+                                        _typed(k_weight, "float32", "k_weight", d), eps,
+                                        _head_flags(norm, unit_offset, interleaved), cs, n_pos, rot, pos,
+                                        _typed(slots, "int64", "slots", n), qo or None, qos, _ptr(k_back), _ptr(v_back),
+                                        _stream(stream))
+    _check(st, "qg_cache_append")
+
+
+def qg_attention_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(load_library().qg_attention_workspace_bytes(int(n_heads), int(n_kv_heads), int(head_dim)))
+
+
+def qg_attention(cache: qg_cache, q, table, seq_len, cu_new, out, workspace, scale: float, max_new: int = 4,
+                 window: int = 0, span_mask=None, lse=None, stream=None) -> None:
+    """Enqueue the attention of ``q`` (``[n_tok, n_heads, head_dim]``, the new tokens of the
+    requests one after the other as in ``cu_new``) over the cache's tokens of each request
+    (``table``, ``seq_len``) into ``out``.  ``window`` > 0: a sliding window; ``span_mask`` (int32
+    bits per new token): a draft tree's visibility among the request's new tokens.
+    ``workspace``: uint8, ``qg_attention_workspace_bytes``, zeroed once."""
+    act = _act(q)
+    qp, qs, n, hq, d = _heads(q, act, "q")
+    op, os_, no, ho, do = _heads(out, act, "out")
+    if not (n == no and hq == ho and d == do == cache.head_dim):
+        raise ValueError("qg_attention: q, out and the cache differ in tokens, heads or head_dim")
+    n_req = int(seq_len.shape[0])
+    tp, width = _table(table, n_req)
+    st = load_library().qg_attention(
+        cache, act, qp, qs, n, hq, tp, width, _typed(seq_len, "int32", "seq_len"), _typed(cu_new, "int32", "cu_new", n_req + 1), n_req, int(max_new),
+        int(window), _typed(span_mask, "int32", "span_mask", n), scale, op, os_, _typed(lse, "float32", "lse", n * hq),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "qg_attention")
 
 
 QG_DEVICE_WAIT_TIMEOUT = 1

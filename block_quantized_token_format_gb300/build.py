@@ -1,7 +1,7 @@
 """Build the CUDA shared library ``_lib/libqgemv.so`` in-tree (sm_103a only).
 
-Compiles the per-format kernel units, the expert kernels, the C ABI and the host
-packer in parallel with nvcc / g++, then links one shared library.  Object files go to
+Compiles the per-format kernel units, the expert kernels, the attention path's units,
+the C ABI and the host packer in parallel with nvcc / g++, then links one shared library.  Object files go to
 ``_build/`` at the repository root.  A stamp of the sources and flags skips
 the work when nothing changed.
 """
@@ -47,6 +47,11 @@ def _units():
         units.append((os.path.join(BUILD, f"qgemv_inst_fmt{f}.o"),
                       [nvcc, *ARCH, *NVCC_FLAGS, f"-DQG_INST_FMT={f}", "-c",
                        os.path.join(CSRC, "qgemv_inst.cu")]))
+    for d in (64, 128, 256):
+        units.append((os.path.join(BUILD, f"attention_inst_{d}.o"),
+                      [nvcc, *ARCH, *NVCC_FLAGS, f"-DQG_ATTN_D={d}", "-c", os.path.join(CSRC, "attention_inst.cu")]))
+    for src in ("attention", "kv_cache"):
+        units.append((os.path.join(BUILD, src + ".o"), [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src + ".cu")]))
     units.append((os.path.join(BUILD, "qgemv_experts.o"),
                   [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, "qgemv_experts.cu")]))
     units.append((os.path.join(BUILD, "qgemv_api.o"),

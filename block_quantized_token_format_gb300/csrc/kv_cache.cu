@@ -1,0 +1,603 @@
+// The cache side of the attention sublayer: block tables and slots from request lengths
+// (qg_cache_pages), norm and rotation of query and key heads (qg_qk_norm_rope), and the same
+// with the quantizing store into the paged 4-bit cache (qg_cache_append).  Formulas, layouts
+// and argument rules are in include/qgemv.h; the record layout in kv_layout.h.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kv_layout.h"
+#include "qgemv_host.h"
+
+namespace qg {
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kMaxPageReq = 16384;      // requests of one qg_cache_pages call (two prefix arrays in shared memory)
+constexpr int kPageThreads = 512;
+
+__device__ __forceinline__ void grid_dependency() {
+    // Let the next kernel start its prologue; this one's inputs may come from the previous.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------------------------ page tables
+
+struct PageArgs {
+    const int32_t* held;
+    const int32_t* fresh;
+    const int32_t* free_pages;
+    const int32_t* free_begin;
+    int32_t* free_end;
+    int32_t* table;
+    int32_t* seq_len;
+    int32_t* cu_new;
+    int64_t* slots;
+    int32_t* positions;
+    long long n_free, table_stride, n_tok;
+    int n_req, page;
+    bool in_place;            // free_end is free_begin: one cluster, which syncs before the write
+    unsigned int* status;
+};
+
+// Prefix sums of new tokens and of new pages over the requests, kept in shared memory by
+// every CTA for itself (n_req values from L2; no CTA waits on another), then one thread per
+// new token: a binary search for its request, its page from the table (a page the request
+// held) or from the free list, its slot and position; the first token of a page writes the
+// table's entry.  Working per token rather than per request spreads one long prompt over the
+// grid as evenly as many short ones.  Bound by latency at decode sizes (one launch, two
+// dependent loads) and by the 12 bytes written per token at prompt sizes.
+__global__ void __launch_bounds__(kPageThreads) cache_pages_kernel(const PageArgs a) {
+    extern __shared__ int32_t prefix[];                  // [n_req + 1] tokens, then [n_req] pages
+    __shared__ long long warp_tok[kPageThreads / 32], warp_pg[kPageThreads / 32];
+    int32_t* const cu = prefix;
+    int32_t* const off = prefix + a.n_req + 1;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    grid_dependency();
+    const long long begin = a.free_begin ? *a.free_begin : 0;
+    bool bad = begin < 0;
+    long long run_tok = 0, run_pg = 0;
+    for (int r0 = 0; r0 < a.n_req; r0 += kPageThreads) {
+        const int r = r0 + tid;
+        long long tok = 0, pg = 0;
+        if (r < a.n_req) {
+            long long h = a.held[r], f = a.fresh[r];
+            if (h < 0 || f < 0 || h + f > 0x7FFFFFFFll) { bad = true; h = f = 0; }
+            tok = f;
+            pg = (h + f + a.page - 1) / a.page - (h + a.page - 1) / a.page;
+            if (blockIdx.x == 0) a.seq_len[r] = int32_t(h + f);
+        }
+        long long st = tok, sp = pg;                     // inclusive scans over the block
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const long long ut = __shfl_up_sync(kAll, st, d), up = __shfl_up_sync(kAll, sp, d);
+            if (lane >= d) { st += ut; sp += up; }
+        }
+        if (lane == 31) { warp_tok[warp] = st; warp_pg[warp] = sp; }
+        __syncthreads();
+        long long bt = run_tok, bp = run_pg;
+        for (int w = 0; w < kPageThreads / 32; ++w) {
+            if (w < warp) { bt += warp_tok[w]; bp += warp_pg[w]; }
+            run_tok += warp_tok[w];
+            run_pg += warp_pg[w];
+        }
+        if (r < a.n_req) {
+            // Clipped to the caller's n_tok (an excess is an error, reported below) and to 31 bits.
+            cu[r] = int32_t(min(bt + st - tok, a.n_tok));
+            off[r] = int32_t(min(bp + sp - pg, 0x7FFFFFFFll));
+        }
+        __syncthreads();
+    }
+    const long long total = min(run_tok, a.n_tok);
+    if (tid == 0) cu[a.n_req] = int32_t(total);
+    if (bad || run_tok > a.n_tok) atomicOr(a.status, kStatusBadLength);
+    __syncthreads();
+    for (long long t = (long long)blockIdx.x * kPageThreads + tid; t < a.n_tok; t += (long long)gridDim.x * kPageThreads) {
+        long long slot = -1;
+        int pos = -1;
+        if (t < total) {
+            int lo = 0, hi = a.n_req;                    // the last r with cu[r] <= t
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= t) lo = mid; else hi = mid;
+            }
+            const int held = a.held[lo];
+            pos = held + int(t - cu[lo]);
+            const int pg = pos / a.page, in = pos - pg * a.page, have = int((unsigned(held) + a.page - 1) / a.page);
+            int32_t* const entry = a.table + (long long)lo * a.table_stride + pg;
+            int page = -1;
+            if (pg >= a.table_stride) {
+                atomicOr(a.status, kStatusBadPage);
+            } else if (pg < have) {
+                page = *entry;
+                if (page < 0) atomicOr(a.status, kStatusBadPage);
+            } else {
+                const long long i = begin + off[lo] + (pg - have);
+                if (begin >= 0 && i < a.n_free) page = a.free_pages[i];
+                else atomicOr(a.status, kStatusNoPages);
+                if (in == 0) *entry = page;
+            }
+            if (page >= 0) slot = (long long)page * a.page + in;
+        }
+        a.slots[t] = slot;
+        a.positions[t] = pos;
+    }
+    if (a.in_place && gridDim.x > 1) {                   // every CTA has read free_begin
+        asm volatile("barrier.cluster.arrive;" ::: "memory");
+        asm volatile("barrier.cluster.wait;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+    if (blockIdx.x == 0) {
+        for (int r = tid; r <= a.n_req; r += kPageThreads) a.cu_new[r] = cu[r];
+        if (tid == 0 && a.free_end) *a.free_end = int32_t(min(max(begin, 0ll) + run_pg, a.n_free));
+    }
+}
+
+// ------------------------------------------------------------------------- heads of a token
+
+struct HeadArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;      // elements
+    const float *q_weight, *k_weight, *cos_sin;
+    const int32_t* positions;
+    const int64_t* slots;
+    void *q_out, *k_out, *v_back;      // k_out: normed keys, or the cache's values when it is written
+    uint8_t* data;                     // the cache, or null
+    long long n_tok, n_pos, n_slots;
+    int n_q, n_k, n_v, page, rot;
+    float eps;
+    unsigned flags;
+    unsigned int* status;
+};
+
+template <typename T, int N> struct Raw;                 // N elements of a lane as one or two words
+template <> struct Raw<float, 2> { float2 v; };
+template <> struct Raw<float, 4> { float4 v; };
+template <> struct Raw<float, 8> { float4 v[2]; };
+template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
+template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
+template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
+
+template <typename T, int N> __device__ __forceinline__ void widen(const Raw<T, N>& raw, float (&x)[N]) {
+    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = float(e[i]);
+}
+
+template <typename T, int N> __device__ __forceinline__ void store(void* at, const float (&x)[N]) {
+    Raw<T, N> raw;
+    T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = T(x[i]);          // nearest even for bf16
+    *static_cast<Raw<T, N>*>(at) = raw;
+}
+
+// Adjacent-pair tree over a warp's D squares: pairs within the lane, then lanes 2i, 2i + 1 and
+// so on.  The order is part of the operator's definition (the sum then does not depend on the
+// kernel), and it is the order a butterfly takes anyway.
+template <int N> __device__ __forceinline__ float square_sum(const float (&x)[N]) {
+    float s[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __fmul_rn(x[i], x[i]);
+#pragma unroll
+    for (int n = N; n > 1; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) s[i] = __fadd_rn(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], d));
+    return s[0];
+}
+
+// Codes and scale of the block this lane's N values belong to (32 / N lanes hold a block).
+template <int N>
+__device__ __forceinline__ void quantize_block(const float (&x)[N], int lane, uint32_t (&code)[N], __half& scale) {
+    float m = x[0];
+    uint32_t top = __float_as_uint(x[0]) & 0x7FFFFFFFu;
+#pragma unroll
+    for (int i = 1; i < N; ++i) {                        // the first of the largest (NaN above all)
+        const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+        if (b > top) { top = b; m = x[i]; }
+    }
+    uint32_t all = top;
+#pragma unroll
+    for (int d = 1; d < 32 / N; d *= 2) all = max(all, __shfl_xor_sync(kAll, all, d));
+    constexpr int kLanes = 32 / N;
+    const uint32_t group = (kLanes == 32 ? kAll : ((1u << kLanes) - 1u)) << (lane & ~(kLanes - 1));
+    const uint32_t who = __ballot_sync(kAll, top == all) & group;
+    m = __shfl_sync(kAll, m, __ffs(int(who)) - 1);
+    const float d = __fmul_rn(m, -0.125f);
+    const bool bad = !(all <= __float_as_uint(QG_CACHE_MAX));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int q = int(roundf(__fdiv_rn(x[i], d))) + 8;
+        code[i] = bad || d == 0.0f ? 8u : uint32_t(min(max(q, 0), 15));
+    }
+    scale = bad ? __ushort_as_half(0x7FFFu) : __float2half_rn(float(__float2bfloat16_rn(d)));
+}
+
+// One warp takes ROWS consecutive heads of a token (queries, then keys, then values), a lane
+// D / 32 neighbouring values of each: every load and store is one contiguous row of a warp, the
+// rows' loads are all issued before the first is used, and the token's cosines and sines are
+// read once for the ROWS heads.  Bound by memory (each element read once and written once) at
+// prompt sizes, by the launch and one load's latency at decode sizes, where ROWS = 1 spreads
+// the heads over more warps.
+template <int D, typename T, int ROWS>
+__global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
+    constexpr int N = D / 32;
+    const int lane = int(threadIdx.x) & 31;
+    const int heads = a.n_q + a.n_k + a.n_v;
+    const int per_tok = (heads + ROWS - 1) / ROWS;
+    const long long id = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    grid_dependency();
+    if (id >= a.n_tok * per_tok) return;
+    const long long tok = id / per_tok;
+    const int h0 = int(id - tok * per_tok) * ROWS;
+
+    Raw<T, N> raw[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+        const int h = h0 + j;
+        if (h >= heads) break;
+        const T* src = h < a.n_q ? static_cast<const T*>(a.q) + tok * a.q_stride + (long long)h * D
+                     : h < a.n_q + a.n_k ? static_cast<const T*>(a.k) + tok * a.k_stride + (long long)(h - a.n_q) * D
+                     : static_cast<const T*>(a.v) + tok * a.v_stride + (long long)(h - a.n_q - a.n_k) * D;
+        raw[j] = *reinterpret_cast<const Raw<T, N>*>(src + lane * N);
+    }
+
+    // The token's rotation: of a lane's values the cosines and sines it needs (half-split: one
+    // per value; interleaved: one per pair).
+    const int half = a.rot / 2, i0 = lane * N;
+    const bool inter = (a.flags & QG_ROPE_INTERLEAVED) != 0;
+    float cs[N], sn[N];
+    bool dead = false, turn = false;
+    if (a.positions) {
+        const int pos = a.positions[tok];
+        dead = pos < 0 || (a.rot > 0 && pos >= a.n_pos);
+        if (pos >= 0 && dead && lane == 0) atomicOr(a.status, kStatusBadLength);
+        if (!dead && a.rot > 0) {
+            const float* row = a.cos_sin + (long long)pos * a.rot;
+            turn = i0 < a.rot;
+            if (turn && inter) {
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) { cs[i] = row[i0 / 2 + i]; sn[i] = row[half + i0 / 2 + i]; }
+            } else if (turn) {
+                const int at = i0 < half ? i0 : i0 - half;
+#pragma unroll
+                for (int i = 0; i < N; ++i) { cs[i] = row[at + i]; sn[i] = row[half + at + i]; }
+            }
+        }
+    }
+    const int reach = half / N;                          // lanes from a value to its partner (half-split)
+    const bool first = lane < reach;
+    const int partner = !turn ? lane : first ? lane + reach : lane - reach;
+
+    long long slot = -1;
+    if (a.data) {
+        slot = a.slots[tok];
+        if (slot >= a.n_slots || slot < -1) {
+            if (lane == 0) atomicOr(a.status, kStatusBadPage);
+            slot = -1;
+        }
+    }
+
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+        const int h = h0 + j;
+        if (h >= heads) break;
+        const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_k;
+        float x[N];
+        widen<T, N>(raw[j], x);
+        if (!is_v) {
+            if (!(a.flags & QG_NORM_NONE)) {
+                const float mean = __fmul_rn(square_sum<N>(x), 1.0f / D);
+                const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, a.eps)));
+                const float* w = is_q ? a.q_weight : a.k_weight;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    x[i] = __fmul_rn(x[i], r);
+                    if (w) {
+                        const float wi = w[i0 + i];
+                        x[i] = __fmul_rn(x[i], a.flags & QG_NORM_UNIT_OFFSET ? __fadd_rn(wi, 1.0f) : wi);
+                    }
+                }
+            }
+            if (a.rot > 0 && !dead) {
+                if (inter) {
+                    if (turn) {
+#pragma unroll
+                        for (int i = 0; i < N / 2; ++i) {
+                            const float u = x[2 * i], v = x[2 * i + 1];
+                            x[2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
+                            x[2 * i + 1] = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const float p = __shfl_sync(kAll, x[i], partner);
+                        if (turn) {
+                            const float own = __fmul_rn(x[i], cs[i]), other = __fmul_rn(p, sn[i]);
+                            x[i] = first ? __fsub_rn(own, other) : __fadd_rn(own, other);
+                        }
+                    }
+                }
+            }
+        }
+        if (dead) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = 0.0f;
+        }
+        if (is_q) {
+            store<T, N>(static_cast<T*>(a.q_out) + tok * a.q_out_stride + (long long)h * D + i0, x);
+            continue;
+        }
+        const int kv = is_v ? h - a.n_q - a.n_k : h - a.n_q;
+        void* out = is_v ? a.v_back : a.k_out;
+        if (a.data) {
+            uint32_t code[N];
+            __half scale;
+            quantize_block<N>(x, lane, code, scale);
+            if (slot >= 0) {
+                const long long page = slot / a.page;
+                const int in = int(slot - page * a.page), t = in % kRecordTokens;
+                uint8_t* rec = a.data + ((page * a.n_k + kv) * (a.page / kRecordTokens) + in / kRecordTokens) * kv_record_bytes(D);
+                const int g = i0 / 32, at = i0 % 32;
+                uint32_t bits = 0;                       // the lane's N nibbles, in order
+#pragma unroll
+                for (int i = 0; i < N; ++i) bits |= code[i] << (4 * i);
+                if (is_v) {
+                    uint8_t* p = rec + kv_v_codes(D) + at % 4 / 2;
+                    const int r = at / 4;
+                    if constexpr (N == 2) p[kv_value_half(D, t, r, g)] = uint8_t(bits);
+                    if constexpr (N == 4) *reinterpret_cast<uint16_t*>(p + kv_value_half(D, t, r, g)) = uint16_t(bits);
+                    if constexpr (N == 8) {
+                        *reinterpret_cast<uint16_t*>(p + kv_value_half(D, t, r, g)) = uint16_t(bits);
+                        *reinterpret_cast<uint16_t*>(p + kv_value_half(D, t, r + 1, g)) = uint16_t(bits >> 16);
+                    }
+                } else {
+                    uint8_t* p = rec + kv_key_word(D, t, at / 8, g) + at % 8 / 2;
+                    if constexpr (N == 2) *p = uint8_t(bits);
+                    if constexpr (N == 4) *reinterpret_cast<uint16_t*>(p) = uint16_t(bits);
+                    if constexpr (N == 8) *reinterpret_cast<uint32_t*>(p) = bits;
+                }
+                if (at == 0)
+                    *reinterpret_cast<__half*>(rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + kv_scale(D, t, g)) = scale;
+            }
+            if (!out) continue;
+            const float d = __half2float(scale);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = __fmul_rn(float(int(code[i]) - 8), d);
+            store<T, N>(static_cast<T*>(out) + (tok * a.n_k + kv) * D + i0, x);
+        } else {
+            store<T, N>(static_cast<T*>(out) + tok * a.k_out_stride + (long long)kv * D + i0, x);
+        }
+    }
+}
+
+// Heads per warp: 4 once that still leaves every SM 32 warps; below, one, so that a few
+// tokens' heads run side by side.
+template <int D, typename T>
+const void* heads_fn(bool wide) { return wide ? (const void*)&heads_kernel<D, T, 4> : (const void*)&heads_kernel<D, T, 1>; }
+
+template <typename T> const void* heads_fn(int D, bool wide) {
+    return D == 64 ? heads_fn<64, T>(wide) : D == 128 ? heads_fn<128, T>(wide) : heads_fn<256, T>(wide);
+}
+
+qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
+    int dev = 0, sms = 0, optin = 0;
+    qg_status st = device_info(&dev, &sms, &optin, &a.status);
+    if (st != QG_OK) return st;
+    const long long heads = a.n_q + a.n_k + a.n_v;
+    if (heads == 0 || a.n_tok == 0) return QG_OK;
+    const bool wide = a.n_tok * heads >= 4ll * 32 * sms;
+    const long long per_tok = wide ? (heads + 3) / 4 : heads;
+    const long long warps = a.n_tok * per_tok;
+    const int in_block = wide ? 8 : 4;
+    const long long grid = (warps + in_block - 1) / in_block;
+    if (grid > 0x7FFFFFFFll) return QG_EUNSUPPORTED;
+    void* params[] = {&a};
+    return launch_early(act == QG_ACT_F32 ? heads_fn<float>(D, wide) : heads_fn<__nv_bfloat16>(D, wide), int(grid),
+                        32 * in_block, 0, 1, params, stream);
+}
+
+constexpr unsigned kHeadFlags = QG_ROPE_INTERLEAVED | QG_NORM_UNIT_OFFSET | QG_NORM_NONE;
+
+// Rows of `heads` heads of D values, `stride` elements apart: 16-byte aligned, not overlapping.
+qg_status check_rows(const void* p, int64_t stride, int64_t heads, int D, qg_act act) {
+    if (!p || stride < heads * D) return QG_EINVAL;
+    const int64_t size = act == QG_ACT_F32 ? 4 : 2;
+    return aligned(p, 16) && stride * size % 16 == 0 ? QG_OK : QG_EALIGN;
+}
+
+qg_status check_heads(qg_act act, int64_t n_tok, int n_heads, int n_kv, int D, const float* qw, const float* kw,
+                      float eps, unsigned flags, const float* cos_sin, int64_t n_pos, int rot,
+                      const int32_t* positions) {
+    if (act != QG_ACT_F32 && act != QG_ACT_BF16) return QG_EINVAL;
+    if (n_tok < 0 || n_tok > (int64_t(1) << 31) - 1 || n_heads < 0 || n_heads > 65535 || n_kv < 0 || n_kv > 65535)
+        return QG_EINVAL;
+    if (!kv_dim_ok(D) || (flags & ~kHeadFlags) || !(eps >= 0.0f)) return QG_EINVAL;
+    if (cos_sin ? (rot < 16 || rot > D || rot % 16 != 0 || n_pos < 1 || !positions) : rot != 0) return QG_EINVAL;
+    return aligned(qw, 4) && aligned(kw, 4) && aligned(cos_sin, 4) && aligned(positions, 4) ? QG_OK : QG_EALIGN;
+}
+
+}  // namespace
+
+qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int cluster, void** params, void* stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (launch_flags() & QG_LAUNCH_EARLY_START) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = unsigned(n);
+    if (cudaLaunchKernelExC(&cfg, fn, params) != cudaSuccess) { cudaGetLastError(); return QG_ECUDA; }
+    return QG_OK;
+}
+
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" {
+
+size_t qg_cache_bytes(int64_t n_pages, int page_tokens, int n_kv_heads, int head_dim) {
+    const qg_cache c = {reinterpret_cast<void*>(16), n_pages, page_tokens, n_kv_heads, head_dim};
+    if (kv_check(&c) != QG_OK) return 0;
+    return size_t(n_pages) * size_t(n_kv_heads) * size_t(page_tokens / kRecordTokens) * size_t(kv_record_bytes(head_dim));
+}
+
+qg_status qg_cache_pages(const int32_t* held, const int32_t* fresh, int n_req, int page_tokens,
+                         const int32_t* free_pages, int64_t n_free, const int32_t* free_begin, int32_t* free_end,
+                         int32_t* table, int64_t table_stride, int32_t* seq_len, int32_t* cu_new, int64_t* slots,
+                         int32_t* positions, int64_t n_tok, void* stream) {
+    const int64_t most = (int64_t(1) << 31) - 1;
+    if (n_req < 0 || page_tokens < 16 || page_tokens > 65536 || page_tokens % kRecordTokens != 0) return QG_EINVAL;
+    if (n_free < 0 || n_free > most || table_stride < 0 || table_stride > most || n_tok < 0 || n_tok > most)
+        return QG_EINVAL;
+    if (!cu_new || (n_free > 0 && !free_pages) || (n_tok > 0 && (!slots || !positions))) return QG_EINVAL;
+    if (n_req > 0 && (!held || !fresh || !table || !seq_len)) return QG_EINVAL;
+    if (n_req > 0 && (seq_len == held || seq_len == fresh || cu_new == held || cu_new == fresh)) return QG_EINVAL;
+    if (n_req > kMaxPageReq) return QG_EUNSUPPORTED;
+    if (!aligned(held, 4) || !aligned(fresh, 4) || !aligned(free_pages, 4) || !aligned(free_begin, 4) ||
+        !aligned(free_end, 4) || !aligned(table, 4) || !aligned(seq_len, 4) || !aligned(cu_new, 4) ||
+        !aligned(slots, 8) || !aligned(positions, 4))
+        return QG_EALIGN;
+    int dev = 0, sms = 0, optin = 0;
+    PageArgs a{};
+    qg_status st = device_info(&dev, &sms, &optin, &a.status);
+    if (st != QG_OK) return st;
+    a.held = held;
+    a.fresh = fresh;
+    a.free_pages = free_pages;
+    a.free_begin = free_begin;
+    a.free_end = free_end;
+    a.table = table;
+    a.seq_len = seq_len;
+    a.cu_new = cu_new;
+    a.slots = slots;
+    a.positions = positions;
+    a.n_free = n_free;
+    a.table_stride = table_stride;
+    a.n_tok = n_tok;
+    a.n_req = n_req;
+    a.page = page_tokens;
+    a.in_place = free_end && free_end == free_begin;
+    const size_t smem = (2 * size_t(n_req) + 1) * sizeof(int32_t);
+    const void* fn = (const void*)&cache_pages_kernel;
+    if (smem > 48 * 1024 && blocks_per_sm(fn, dev, optin, kPageThreads, smem) < 1) return QG_EUNSUPPORTED;
+    int64_t grid = std::max<int64_t>(1, std::min<int64_t>((n_tok + kPageThreads - 1) / kPageThreads, sms));
+    // In place every CTA must have read free_begin before it is written: one cluster, which can wait for itself.
+    const int cluster = a.in_place ? int(grid >= 8 ? 8 : grid) : 1;
+    if (a.in_place) grid = cluster;
+    void* params[] = {&a};
+    return launch_early(fn, int(grid), kPageThreads, smem, cluster, params, stream);
+}
+
+qg_status qg_qk_norm_rope(qg_act act, const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t n_tok,
+                          int n_heads, int n_kv_heads, int head_dim, const float* q_weight, const float* k_weight,
+                          float eps, unsigned int flags, const float* cos_sin, int64_t n_pos, int rot_dim,
+                          const int32_t* positions, void* q_out, int64_t q_out_stride, void* k_out,
+                          int64_t k_out_stride, void* stream) {
+    qg_status st = check_heads(act, n_tok, n_heads, n_kv_heads, head_dim, q_weight, k_weight, eps, flags, cos_sin, n_pos,
+                               rot_dim, positions);
+    if (st != QG_OK) return st;
+    if (n_tok > 0 && n_heads > 0) {
+        if ((st = check_rows(q, q_stride, n_heads, head_dim, act)) != QG_OK) return st;
+        if ((st = check_rows(q_out, q_out_stride, n_heads, head_dim, act)) != QG_OK) return st;
+    }
+    if (n_tok > 0 && n_kv_heads > 0) {
+        if ((st = check_rows(k, k_stride, n_kv_heads, head_dim, act)) != QG_OK) return st;
+        if ((st = check_rows(k_out, k_out_stride, n_kv_heads, head_dim, act)) != QG_OK) return st;
+    }
+    HeadArgs a{};
+    a.q = q;
+    a.k = k;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.cos_sin = cos_sin;
+    a.positions = positions;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.n_tok = n_tok;
+    a.n_pos = n_pos;
+    a.n_q = n_heads;
+    a.n_k = n_kv_heads;
+    a.rot = rot_dim;
+    a.eps = eps;
+    a.flags = flags;
+    return launch_heads(a, act, head_dim, stream);
+}
+
+qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, int64_t n_tok, int n_heads,
+                          const float* q_weight, const float* k_weight, float eps, unsigned int flags,
+                          const float* cos_sin, int64_t n_pos, int rot_dim, const int32_t* positions,
+                          const int64_t* slots, void* q_out, int64_t q_out_stride, void* k_back, void* v_back,
+                          void* stream) {
+    qg_status st = kv_check(cache);
+    if (st != QG_OK) return st;
+    const int D = cache->head_dim, n_kv = cache->n_kv_heads;
+    st = check_heads(act, n_tok, n_heads, n_kv, D, q_weight, k_weight, eps, flags, cos_sin, n_pos, rot_dim, positions);
+    if (st != QG_OK) return st;
+    if (n_tok > 0) {
+        if (!slots) return QG_EINVAL;
+        if (!aligned(slots, 8) || !aligned(k_back, 16) || !aligned(v_back, 16)) return QG_EALIGN;
+        if (n_heads > 0) {
+            if ((st = check_rows(q, q_stride, n_heads, D, act)) != QG_OK) return st;
+            if ((st = check_rows(q_out, q_out_stride, n_heads, D, act)) != QG_OK) return st;
+        }
+        if ((st = check_rows(k, k_stride, n_kv, D, act)) != QG_OK) return st;
+        if ((st = check_rows(v, v_stride, n_kv, D, act)) != QG_OK) return st;
+    }
+    HeadArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.cos_sin = cos_sin;
+    a.positions = positions;
+    a.slots = slots;
+    a.q_out = q_out;
+    a.q_out_stride = q_out_stride;
+    a.k_out = k_back;
+    a.v_back = v_back;
+    a.data = static_cast<uint8_t*>(cache->data);
+    a.n_tok = n_tok;
+    a.n_pos = n_pos;
+    a.n_slots = cache->n_pages * cache->page_tokens;
+    a.n_q = n_heads;
+    a.n_k = n_kv;
+    a.n_v = n_kv;
+    a.page = cache->page_tokens;
+    a.rot = rot_dim;
+    a.eps = eps;
+    a.flags = flags;
+    return launch_heads(a, act, D, stream);
+}
+
+}  // extern "C"

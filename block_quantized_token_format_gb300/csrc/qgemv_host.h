@@ -42,6 +42,9 @@ void read_env_override();
 TileOverride current_override();
 uint64_t override_generation();
 uint32_t wait_limit();
+// A launch of `grid` CTAs (as clusters of `cluster`), with programmatic dependent launch
+// when it is on: the kernel waits for its predecessor before its first access.
+qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int cluster, void** params, void* stream);
 uint32_t test_extra_tx();
 
 }  // namespace qg

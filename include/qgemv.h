@@ -321,6 +321,156 @@ qg_status qgemv_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_
                         int64_t next_n_in, void* stream);
 qg_status qg_describe_expert_tile(qg_fmt fmt, int64_t n_out, int64_t n_in, char* buf, size_t len);
 
+/* ------------------------------------------------- key/value cache held in 4 bits
+ * The attention sublayer of a decode or verify step, between the query/key/value
+ * projection and the output projection (both qgemv): block tables and slots from the
+ * requests' lengths, the norm and rotation of the heads, keys and values into a paged
+ * cache, attention over it.  (The pages leave attention and its cache to the host
+ * program; these calls have no counterpart there.)
+ *
+ * The cache is one device buffer of n_pages pages of page_tokens tokens (a multiple of
+ * 16), for n_kv_heads key/value heads of head_dim (64, 128 or 256) values.  Every 32
+ * values of a head are a block of 18 bytes, as in Q4_0 but with a scale that keeps 8
+ * significant bits:
+ *     m = the value of largest magnitude (first on ties), d' = m / -8 in fp32
+ *     q = clamp(roundf(x / d') + 8, 0, 15)       the codes of qg_quantize(QG_Q4_0)
+ *     d = fp16(bf16(d'));   a block reads back as (q - 8) * d
+ * so every value read back is exactly an fp16 number, which is what lets the tensor cores
+ * multiply it without a rounding.  m = 0 gives d = 0, q = 8.  A block that holds a NaN, an
+ * infinity or a magnitude above QG_CACHE_MAX stores d = NaN: it reads back as NaN (a visible
+ * key or value of that kind makes the outputs that see it NaN), not as a wrong number.
+ *
+ * A slot is page * page_tokens + (token within the page), 64 bits wide.
+ * data: 16-byte aligned, qg_cache_bytes(n_pages, page_tokens, n_kv_heads, head_dim) bytes
+ * (18 * head_dim / 16 bytes per token and head; 0 for invalid arguments); it need not be
+ * cleared.  A page holds per head page_tokens / 16 records of 16 tokens; a record holds, with
+ * G = head_dim / 32 blocks per token in sets of I = min(G, 4):
+ *     key codes    [G / I][16 tokens][4 c][I] uint32, nibble j = dim 32 g + 8 c + j
+ *     key scales   [8 token pairs][G][2 tokens] fp16
+ *     value codes  [G / I][2][8 r][4 token pairs][I][2 tokens] uint16, nibble j = dim 32 g + 4 r + j
+ *     value scales [8 token pairs][G][2 tokens] fp16
+ *
+ * Rules of the four calls: arguments are checked on the host as everywhere in this library;
+ * what only the device can see (lengths, page ids, slots, positions) is checked there:
+ * nothing outside a buffer is read or written, the token or request concerned is left out
+ * or its result is not valid, and a bit is set in the device status word (qg_device_status):
+ *     QG_DEVICE_BAD_PAGE    a page id or slot outside the cache, or a table row too short
+ *     QG_DEVICE_BAD_LENGTH  a negative or inconsistent length, count or position
+ *     QG_DEVICE_NO_PAGES    the list of free pages ran out
+ * act: the type of activations, QG_ACT_F32 or QG_ACT_BF16. */
+typedef enum { QG_ACT_F32 = 0, QG_ACT_BF16 = 1 } qg_act;
+typedef struct {
+    void* data;
+    int64_t n_pages;
+    int page_tokens, n_kv_heads, head_dim;
+} qg_cache;
+#define QG_CACHE_MAX 16384.0f
+#define QG_DEVICE_BAD_PAGE 8u
+#define QG_DEVICE_BAD_LENGTH 16u
+#define QG_DEVICE_NO_PAGES 32u
+size_t qg_cache_bytes(int64_t n_pages, int page_tokens, int n_kv_heads, int head_dim);
+
+/* qg_cache_pages: block table, slots and positions of a step's new tokens.
+ *   held, fresh  device int32 [n_req]: tokens a request has in the cache, tokens it adds.
+ *   free_pages   device int32 [n_free]: pages to deal; free_begin: device int32, the first
+ *                one not dealt yet, or NULL for 0; free_end: device int32, receives the one
+ *                after the last dealt (may be free_begin itself), or NULL.
+ *   table        device int32 [n_req][table_stride]: page i of a request's tokens; the first
+ *                ceil(held / page_tokens) entries of a row are read, the following ones up to
+ *                ceil((held + fresh) / page_tokens) are written: pages are dealt in the order of
+ *                requests, then of pages.  Other entries are left as they are.
+ *   seq_len      device int32 [n_req]: held + fresh.   cu_new: device int32 [n_req + 1]: the
+ *                requests' first tokens and, last, their sum.
+ *   slots        device int64 [n_tok]; positions: device int32 [n_tok]: every new token's slot
+ *                and position (held + j for a request's token j), requests one after the
+ *                other.  Entries past the requests' sum are -1 (padding); tokens without a
+ *                page have slot -1.
+ *   table may have n_req = 0 rows (nothing but padding is written).  n_req <= 16384.
+ *   4-byte aligned (slots 8).  Calls may be repeated: with free_end != free_begin the same
+ *   inputs give the same outputs. */
+qg_status qg_cache_pages(const int32_t* held, const int32_t* fresh, int n_req, int page_tokens,
+                         const int32_t* free_pages, int64_t n_free, const int32_t* free_begin, int32_t* free_end,
+                         int32_t* table, int64_t table_stride, int32_t* seq_len, int32_t* cu_new, int64_t* slots,
+                         int32_t* positions, int64_t n_tok, void* stream);
+
+/* qg_qk_norm_rope: for every token and every query and key head x (head_dim values):
+ *     ss = sum of x^2, r = 1 / sqrt(ss / head_dim + eps), y = (x * r) * w
+ *     the first rot_dim values of y in pairs (a, b) = (y[i], y[i + rot_dim / 2]), or
+ *     (y[2i], y[2i + 1]) with QG_ROPE_INTERLEAVED:  a' = a c_i - b s_i,  b' = b c_i + a s_i
+ *   in fp32, every operation rounded by itself (no fused multiply-add), the squares summed
+ *   as a tree of adjacent pairs; rounded once to act.  qg_cache_append computes the same bits.
+ *   q, k         device act [n_tok][heads][head_dim], tokens q_stride / k_stride elements
+ *                apart (the slices of one projection's row may be passed as they are); q_out,
+ *                k_out likewise.  16-byte aligned, strides a multiple of 16 bytes.  In place
+ *                (q_out = q) is allowed.  n_heads or n_kv_heads may be 0 (its pointers unused).
+ *   q_weight,    device fp32 [head_dim], NULL for ones; QG_NORM_UNIT_OFFSET: the weight is
+ *   k_weight     1 + w.  QG_NORM_NONE: no norm (y = x; weights and eps unused).
+ *   cos_sin      device fp32 [n_pos][rot_dim], row p: the cosines c_i, then the sines s_i of
+ *                position p; NULL (rot_dim 0): no rotation.  rot_dim: a multiple of 16, at most
+ *                head_dim.
+ *   positions    device int32 [n_tok]; negative = padding, its output rows are zero.  A
+ *                position >= n_pos sets QG_DEVICE_BAD_LENGTH, its rows are zero. */
+#define QG_ROPE_INTERLEAVED 1u
+#define QG_NORM_UNIT_OFFSET 2u
+#define QG_NORM_NONE 4u
+qg_status qg_qk_norm_rope(qg_act act, const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t n_tok,
+                          int n_heads, int n_kv_heads, int head_dim, const float* q_weight, const float* k_weight,
+                          float eps, unsigned int flags, const float* cos_sin, int64_t n_pos, int rot_dim,
+                          const int32_t* positions, void* q_out, int64_t q_out_stride, void* k_out,
+                          int64_t k_out_stride, void* stream);
+
+/* qg_cache_append: the norm and rotation of qg_qk_norm_rope, with the keys and the values
+ * (which are neither normed nor rotated) quantized into the cache instead of written out: one
+ * pass from a projection's row to rotated queries and a filled cache.
+ *   k, v         device act [n_tok][n_kv_heads][head_dim] as above; q, q_out: the queries, or
+ *                NULL with n_heads 0.  Keys are quantized from their fp32 values.
+ *   slots        device int64 [n_tok]; -1 = padding (nothing is stored).  Two tokens of a call
+ *                must not have the same slot.
+ *   k_back,      device act [n_tok][n_kv_heads][head_dim], contiguous, 16-byte aligned, or
+ *   v_back       NULL: what the cache now holds for these tokens, as values (a caller that
+ *                attends within a prompt chunk then sees what later steps will read).
+ *   cos_sin NULL: no rotation, positions may be NULL.  Other arguments as in qg_qk_norm_rope. */
+qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, int64_t n_tok, int n_heads,
+                          const float* q_weight, const float* k_weight, float eps, unsigned int flags,
+                          const float* cos_sin, int64_t n_pos, int rot_dim, const int32_t* positions,
+                          const int64_t* slots, void* q_out, int64_t q_out_stride, void* k_back, void* v_back,
+                          void* stream);
+
+/* qg_attention: attention of the new tokens of n_req requests over the cache.
+ *     s_k = scale * q . key_k,   out = sum_k softmax(s)_k value_k,   lse = log sum_k exp(s_k)
+ *   over the visible tokens k of the query's request: query head h reads key/value head
+ *   h / (n_heads / n_kv_heads).  Request r has seq_len[r] tokens in the cache, its new ones
+ *   (rows cu_new[r] .. cu_new[r + 1] of q) the last of them, already appended.  The new token
+ *   at position p sees k <= p; with window > 0 only k > p - window; with span_mask, of the
+ *   request's new tokens exactly those whose bit is set (bit j = the request's new token j, so
+ *   a draft tree's token sees its ancestors and itself; at most 32 new tokens per request
+ *   then).  A query that sees nothing gets out = 0 and lse = -infinity.
+ *   q            device act [n_tok][n_heads][head_dim], tokens q_stride elements apart;
+ *   out          device act, likewise with out_stride.  16-byte aligned, strides a multiple of
+ *                16 bytes.
+ *   lse          device fp32 [n_tok][n_heads] (natural logarithm), or NULL.
+ *   table        device int32 [n_req][table_stride], seq_len, cu_new: as qg_cache_pages leaves
+ *                them.  Table entries past a request's tokens are not read.
+ *   max_new      the largest number of new tokens of a request: chooses the kernel's row tile;
+ *                results are right for any value.
+ *   n_tok        rows of q and out (tokens past cu_new[n_req] are not touched).
+ *   workspace    device, >= qg_attention_workspace_bytes(n_heads, n_kv_heads, head_dim) bytes,
+ *                16-byte aligned, its first QG_ATTENTION_ZERO_BYTES bytes ZEROED by the caller
+ *                once; each call leaves them zeroed.  Calls that share one must be serialized.
+ *                After QG_DEVICE_WAIT_TIMEOUT zero them again.
+ *   n_req <= 4096, n_heads a multiple of n_kv_heads.
+ * fp32 activations: queries and probabilities enter the tensor cores as two fp16 terms (22
+ * bits), sums are fp32; bf16: queries are exact, probabilities one fp16 term.  Outputs are the
+ * same on every run; the order of a sum depends on the lengths of the whole batch and on the
+ * GPU's number of SMs. */
+#define QG_ATTENTION_ZERO_BYTES 4096
+size_t    qg_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim);
+qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t q_stride, int64_t n_tok, int n_heads,
+                       const int32_t* table, int64_t table_stride, const int32_t* seq_len, const int32_t* cu_new,
+                       int n_req, int max_new, int window, const uint32_t* span_mask, float scale, void* out,
+                       int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------- qgemv_argmax_noalloc
  * No counterpart on the source pages: an addition for callers that cannot call
  * cudaMalloc, such as a plugin inside a host framework that owns every device
