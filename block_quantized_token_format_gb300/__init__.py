@@ -363,7 +363,7 @@ def qg_set_wait_limit(polls: int = 0, extra_tx_bytes: int = 0) -> None:
 
 QG_ACT_F32, QG_ACT_BF16 = 0, 1
 QG_ROPE_INTERLEAVED, QG_NORM_UNIT_OFFSET, QG_NORM_NONE = 1, 2, 4
-QG_CACHE_MAX = 16384.0
+QG_CACHE_MAX = 65280.0
 QG_ATTENTION_ZERO_BYTES = 4096
 QG_DEVICE_BAD_PAGE = 8
 QG_DEVICE_BAD_LENGTH = 16

@@ -8,15 +8,15 @@
 
 namespace qg {
 
-AttnKernel attention_lookup_64(int act, int rows);
-AttnKernel attention_lookup_128(int act, int rows);
-AttnKernel attention_lookup_256(int act, int rows);
+AttnKernel attention_lookup_64(int act, int tiles);
+AttnKernel attention_lookup_128(int act, int tiles);
+AttnKernel attention_lookup_256(int act, int tiles);
 
 namespace {
 
-AttnKernel lookup(int act, int D, int rows) {
-    return D == 64 ? attention_lookup_64(act, rows) : D == 128 ? attention_lookup_128(act, rows)
-                                                               : attention_lookup_256(act, rows);
+AttnKernel lookup(int act, int D, int tiles) {
+    return D == 64 ? attention_lookup_64(act, tiles) : D == 128 ? attention_lookup_128(act, tiles)
+                                                               : attention_lookup_256(act, tiles);
 }
 
 // Floats of all partials of a grid of CTAs: two per CTA, one per warp.
@@ -35,8 +35,8 @@ size_t qg_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim) {
         return 0;
     size_t most = 0;
     for (int act = 0; act < 2; ++act)
-        for (int rows = 8; rows <= 16; rows += 8)
-            most = std::max(most, partial_floats(lookup(act, head_dim, rows), kAttnGrid));
+        for (int tiles = 1; tiles <= 4; ++tiles)
+            most = std::max(most, partial_floats(lookup(act, head_dim, tiles), kAttnGrid));
     return size_t(QG_ATTENTION_ZERO_BYTES) + most * sizeof(float);
 }
 
@@ -67,12 +67,21 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     st = device_info(&dev, &sms, &optin, &a.status);
     if (st != QG_OK) return st;
     const int group = n_heads / n_kv;
-    const AttnKernel k = lookup(act, D, int64_t(max_new) * group <= 8 ? 8 : 16);
-    // The deepest ring (up to 8 stages per warp) that fits one CTA per SM.
-    int depth = 8;
-    while (depth > 2 && size_t(k.smem(n_req, depth)) + kStaticSmemReserve > size_t(optin)) --depth;
+    // Column tiles for the rows of a request and key/value head, at most 16 rows at a time.
+    const int64_t rows = std::min<int64_t>(int64_t(max_new) * group, 16);
+    int tiles = int(act == QG_ACT_F32 ? (rows + 3) / 4 : (rows + 7) / 8), depth = 0;
+    AttnKernel k{};
+    auto fits = [&](int d) { return size_t(k.smem(n_req, d)) + kStaticSmemReserve <= size_t(optin); };
+    // The deepest ring (2 to 8 stages per warp) that fits one CTA per SM; a long list of requests
+    // may leave room only for fewer rows at a time.
+    for (; tiles >= 1 && depth < 2; --tiles) {
+        k = lookup(act, D, tiles);
+        for (depth = 8; depth >= 2 && !fits(depth); --depth) {}
+    }
+    if (depth < 2) return QG_EUNSUPPORTED;
     const int smem = k.smem(n_req, depth);
-    if (size_t(smem) + kStaticSmemReserve > size_t(optin)) return QG_EUNSUPPORTED;
+    // Records are numbered with 32 bits on the device.
+    if (cache->n_pages * n_kv > ((int64_t(1) << 32) - 1) / (cache->page_tokens / kRecordTokens)) return QG_EUNSUPPORTED;
     if (blocks_per_sm(k.fn, dev, optin, 32 * k.warps, size_t(smem)) < 1) return QG_EUNSUPPORTED;
     a.data = static_cast<const uint8_t*>(cache->data);
     a.q = q;
@@ -96,7 +105,7 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     a.page_records = cache->page_tokens / kRecordTokens;
     a.window = window;
     a.depth = depth;
-    a.scale_log2 = float(double(scale) * 1.4426950408889634 * 1048576.0);
+    a.scale_log2 = float(double(scale) * 1.4426950408889634);
     a.wait_limit = wait_limit();
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.test_extra_tx = test_extra_tx();

@@ -44,7 +44,7 @@
 namespace qg {
 
 constexpr int kUnit = 32;                 // keys per unit: two records
-constexpr int kMaxAttnReq = 4096;
+constexpr int kMaxAttnReq = 1024;
 constexpr int kAttnGrid = 160;             // most CTAs of a launch (one per SM; the workspace is sized by it)
 static_assert(kAttnGrid * 4 <= QG_ATTENTION_ZERO_BYTES, "one ticket per CTA");
 constexpr float kProbShift = 7.0f;        // probabilities are scaled by 2^7 ...
@@ -63,35 +63,41 @@ struct AttnArgs {
     unsigned int* status;
     long long q_stride, out_stride, table_stride, n_tok, n_pages;
     int n_req, n_heads, n_kv, group, page_records, window, depth;
-    float scale_log2;          // scale * log2(e) * 2^20 (the codes' exponent)
+    float scale_log2;          // scale * log2(e)
     uint32_t wait_limit, drain_limit, test_extra_tx;
 };
 
-template <int D, int ROWS, int TERMS> struct AttnShape {
-    static constexpr bool kPacked = ROWS == 8;
-    static_assert(ROWS == 16 || (ROWS == 8 && TERMS == 2), "8 rows hold both terms in one operand");
 #ifndef QG_W
 #define QG_W 12
 #endif
-    static constexpr int kWarps = D == 256 && ROWS == 16 && TERMS == 2 ? 6 : D == 256 ? 8 : QG_W;
+#ifndef QG_VU
+#define QG_VU 1
+#endif
+// TILES column tiles of 8 query columns: a row takes TERMS of them (its fp16 terms side by
+// side), so a tile holds 4 rows with two terms or 8 with one.
+template <int D, int TILES, int TERMS> struct AttnShape {
+    static constexpr int kLaneRows = 2 / TERMS;                      // rows a lane holds per tile
+    static constexpr int kTileRows = 8 / TERMS;
+    static constexpr int kRows = TILES * kTileRows;
+    static constexpr int kWarps = D == 256 ? 10 - TILES : QG_W;
     static constexpr int kRec = kv_record_bytes(D);
     static constexpr int kStage = 2 * kRec;
-    static constexpr int kQMats = kPacked ? 1 : TERMS;
-    static constexpr int kQBytes = kQMats * (D / 16) * 512;          // queries in operand order
-    static constexpr int kInitBytes = kv_groups(D) * 16 * 4;         // -8 * sum(q) per block and row
-    static constexpr int kPartial = ROWS * (D + 2);                  // floats: [ROWS][D], m[ROWS], l[ROWS]
+    static constexpr int kQBytes = TILES * kv_groups(D) * 512;       // queries in operand order
+    static constexpr int kInitBytes = TILES * (kv_groups(D) + 1) * 32;    // -8 * sum(q) per block and column; factors
+    static constexpr int kPartial = kRows * (D + 2);                 // floats: [rows][D], m[rows], l[rows]
 };
 
 // Shared memory: prefix of units per request, the warps' records of unfinished items, then
 // per warp its barriers, queries and ring.
-struct AttnSmem { int meta_off, warp_off, bar_off, q_off, init_off, ring_off, warp_bytes, total; };
-template <int D, int ROWS, int TERMS> __host__ __device__ inline AttnSmem attn_smem(int n_req, int depth) {
-    using S = AttnShape<D, ROWS, TERMS>;
+struct AttnSmem { int seq_off, new_off, meta_off, warp_off, bar_off, q_off, init_off, warp_bytes, total; };
+template <int D, int TILES, int TERMS> __host__ __device__ inline AttnSmem attn_smem(int n_req, int depth) {
+    using S = AttnShape<D, TILES, TERMS>;
     AttnSmem p;
-    p.meta_off = ((n_req + 1) * 4 + 7) / 8 * 8;
+    p.seq_off = (n_req + 1) * 4;                     // after the prefix: lengths, then first new tokens
+    p.new_off = p.seq_off + n_req * 4;
+    p.meta_off = (p.new_off + (n_req + 1) * 4 + 7) / 8 * 8;
     p.warp_off = (p.meta_off + (4 * S::kWarps + 1) * 4 + 127) / 128 * 128;
-    p.ring_off = 0;
-    p.q_off = depth * S::kStage;
+    p.q_off = depth * S::kStage;                     // a warp's ring comes first
     p.init_off = p.q_off + S::kQBytes;
     p.bar_off = p.init_off + S::kInitBytes;
     p.warp_bytes = (p.bar_off + depth * 8 + 127) / 128 * 128;
@@ -101,13 +107,13 @@ template <int D, int ROWS, int TERMS> __host__ __device__ inline AttnSmem attn_s
 
 // ------------------------------------------------------------------------------ PTX helpers
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
-// d = a b + {c0, c0, c1, c1}: an accumulator of its own, so that a start value costs no moves.
+// d = a b + {c0, c1, c0, c1}: an accumulator of its own, so that a start value costs no moves.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1, float c0, float c1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
@@ -150,6 +156,42 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
     hi = h2_bits(h);
     lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
 }
+// The four pairs of codes of a key word (nibbles i and i + 4), as fp16 code * 2^-20.
+constexpr float kCodeUnit = 1.0f / 1048576.0f;
+__device__ __forceinline__ void key_codes(uint32_t w, uint32_t (&b)[4]) {
+    const uint32_t m = 0x00F000F0u;
+    b[0] = (w << 4) & m;
+    b[1] = w & m;
+    b[2] = (w >> 4) & m;
+    b[3] = (w >> 8) & m;
+}
+// The four value pairs of a word (nibble n of two tokens) times the tokens' scales d: exact.
+__device__ __forceinline__ void value_pairs(uint32_t w, uint32_t d, uint32_t (&v)[4]) {
+    const __half2 e = bits_h2(d);
+#if QG_VU == 1
+    const __half2 less = __hmul2(e, __float2half2_rn(-8.0f));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t t = i ? w >> 8 : w;
+        const __half2 y = bits_h2((t & 0x00FF00FFu) | 0x64006400u), z = bits_h2((t & 0x00F000F0u) | 0x64006400u);
+        v[2 * i] = h2_bits(__hfma2(__hsub2(y, z), e, less));
+        v[2 * i + 1] = h2_bits(__hmul2(__hfma2(z, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f)), e));
+    }
+#else
+    const __half2 less = __hmul2(e, __float2half2_rn(-24.0f));
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const uint32_t t = n == 0 ? w << 6 : n == 1 ? w << 2 : n == 2 ? w >> 2 : w >> 6;
+        v[n] = h2_bits(__hfma2(bits_h2((t & 0x03C003C0u) | 0x4C004C00u), e, less));
+    }
+#endif
+}
+// The transpose of an 8x8 matrix of fp16: lane 4 r + c holds row r, columns 2 c and 2 c + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 template <int N> __device__ __forceinline__ void lds_words(uint32_t a, uint32_t* w) {
     if constexpr (N == 4) {
         const uint4 v = lds128(a);
@@ -158,6 +200,11 @@ template <int N> __device__ __forceinline__ void lds_words(uint32_t a, uint32_t*
         static_assert(N == 2, "two or four blocks of a set");
         asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
     }
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
 }
 __device__ __forceinline__ void load8(const float* p, float* x) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -190,25 +237,23 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float
 struct Request {
     int seq, first_tok, fresh, first_unit, units, tiles;
 };
-template <int ROWS> __device__ __forceinline__ Request request_of(const AttnArgs& a, int r, bool& bad_len, bool& bad_page) {
+template <int ROWS> __device__ __forceinline__ Request request_of(const AttnArgs& a, int seq, int first_tok, int end) {
     Request q;
-    q.seq = a.seq_len[r];
-    q.first_tok = a.cu_new[r];
-    const int end = a.cu_new[r + 1];
-    q.fresh = end - q.first_tok;
-    q.units = q.first_unit = q.tiles = 0;
-    const bool ok = q.seq >= 0 && q.first_tok >= 0 && end >= q.first_tok && end <= a.n_tok &&
-                    !(a.span_mask && q.fresh > 32);
-    bad_len |= !ok;
-    const long long records = ((long long)q.seq + kRecordTokens - 1) / kRecordTokens;
-    const bool fits = records <= a.table_stride * a.page_records;
-    bad_page |= ok && !fits;
-    if (!ok || !fits || q.fresh == 0) { q.fresh = 0; return q; }
-    if (a.window > 0) q.first_unit = max(0, q.seq - q.fresh + 1 - a.window) / kUnit;
-    q.units = max(1, int(((long long)q.seq + kUnit - 1) / kUnit) - q.first_unit);
+    q.seq = seq;
+    q.first_tok = first_tok;
+    q.fresh = end - first_tok;
+    q.first_unit = a.window > 0 ? max(0, seq - q.fresh + 1 - a.window) / kUnit : 0;
+    q.units = max(1, int((unsigned(seq) + kUnit - 1) / kUnit) - q.first_unit);
     q.tiles = int(((long long)q.fresh * a.group + ROWS - 1) / ROWS);
     return q;
 }
+
+// The CTA's view of the batch: units prefixed over the requests, their lengths, their tokens.
+struct Batch {
+    const uint32_t* cum;
+    const int *seq, *first;
+    int n_req;
+};
 
 // An item, decoded from a unit's place in the sequence.
 struct Item {
@@ -216,26 +261,21 @@ struct Item {
     int r, head, tile, unit;       // unit: within the item
     uint32_t start;                // the item's first unit in the sequence: its identity
 };
-template <int ROWS> __device__ __forceinline__ Item item_at(const AttnArgs& a, const uint32_t* cum, int r, uint32_t u) {
-    bool x = false, y = false;
+template <int ROWS> __device__ __forceinline__ Item item_at(const AttnArgs& a, const Batch& b, int r, uint32_t u) {
+    int hi = b.n_req;              // the request whose units hold u, searched from r on (units only grow)
+    while (hi - r > 1) {
+        const int mid = (r + hi) >> 1;
+        if (b.cum[mid] <= u) r = mid; else hi = mid;
+    }
     Item it;
     it.r = r;
-    it.rq = request_of<ROWS>(a, r, x, y);
-    const uint32_t rem = u - cum[r], n = rem / uint32_t(it.rq.units);
+    it.rq = request_of<ROWS>(a, b.seq[r], b.first[r], b.first[r + 1]);
+    const uint32_t rem = u - b.cum[r], n = rem / uint32_t(it.rq.units);
     it.unit = int(rem - n * uint32_t(it.rq.units));
     it.head = int(n / uint32_t(it.rq.tiles));
     it.tile = int(n - uint32_t(it.head) * uint32_t(it.rq.tiles));
     it.start = u - uint32_t(it.unit);
     return it;
-}
-// The request whose units hold u, searched from request r on (units only grow).
-__device__ __forceinline__ int find_request(const uint32_t* cum, int lo, int n_req, uint32_t u) {
-    int hi = n_req;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= u) lo = mid; else hi = mid;
-    }
-    return lo;
 }
 
 // What a row may see: keys in (low, pos], of its request's new tokens those in bits.
@@ -257,18 +297,21 @@ template <int ROWS> __device__ __forceinline__ void row_of(const AttnArgs& a, co
 
 // ------------------------------------------------------------------------------ kernel
 
-template <typename T, int D, int ROWS, int TERMS>
-__global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) attention_kernel(const AttnArgs a) {
-    using S = AttnShape<D, ROWS, TERMS>;
+template <typename T, int D, int TILES, int TERMS>
+__global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) attention_kernel(const AttnArgs a) {
+    using S = AttnShape<D, TILES, TERMS>;
     constexpr int W = S::kWarps, NG = kv_groups(D), GI = kv_set(D), NS = NG / GI;
-    constexpr bool PACKED = S::kPacked;
+    constexpr int ROWS = S::kRows, H = S::kLaneRows;
     extern __shared__ __align__(128) uint8_t smem[];
+    const AttnSmem lay = attn_smem<D, TILES, TERMS>(a.n_req, a.depth);
     uint32_t* const cum = reinterpret_cast<uint32_t*>(smem);
-    const AttnSmem lay = attn_smem<D, ROWS, TERMS>(a.n_req, a.depth);
+    int* const seqs = reinterpret_cast<int*>(smem + lay.seq_off);
+    int* const firsts = reinterpret_cast<int*>(smem + lay.new_off);
+    const Batch batch{cum, seqs, firsts, a.n_req};
     unsigned long long* const wsum = reinterpret_cast<unsigned long long*>(smem + lay.meta_off);   // [W]
     uint32_t* const meta = reinterpret_cast<uint32_t*>(wsum + W);                 // [W][2] item starts, then a flag
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    const int r8 = lane >> 2, c4 = lane & 3;               // operand row (or key column) and column group
+    const int r8 = lane >> 2, c4 = lane & 3;               // operand row and column group
     uint8_t* const mine = smem + lay.warp_off + warp * lay.warp_bytes;
     const uint32_t ring = smem_addr(mine), qmat = ring + lay.q_off, binit = ring + lay.init_off, bars = ring + lay.bar_off;
 
@@ -284,8 +327,19 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
         const int r = r0 + tid;
         unsigned long long n = 0;
         if (r < a.n_req) {
-            const Request q = request_of<ROWS>(a, r, bad_len, bad_page);
-            n = (unsigned long long)q.units * unsigned(q.tiles) * unsigned(a.n_kv);
+            const int seq = a.seq_len[r], first = a.cu_new[r], end = a.cu_new[r + 1];
+            const bool ok = seq >= 0 && first >= 0 && end >= first && end <= a.n_tok && !(a.span_mask && end - first > 32);
+            // Records beyond the table's row cannot be found: such a request is left out whole.
+            const bool fits = ((long long)seq + kRecordTokens - 1) / kRecordTokens <= a.table_stride * a.page_records;
+            bad_len |= !ok;
+            bad_page |= ok && !fits;
+            if (ok && fits && end > first) {
+                const Request q = request_of<ROWS>(a, seq, first, end);
+                n = (unsigned long long)q.units * unsigned(q.tiles) * unsigned(a.n_kv);
+            }
+            seqs[r] = seq;
+            firsts[r] = first;
+            if (r == a.n_req - 1) firsts[r + 1] = end;
         }
         unsigned long long s = n;
 #pragma unroll
@@ -317,37 +371,31 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
     const uint32_t u0 = c0 + uint32_t((unsigned long long)(c1 - c0) * warp / W);
     const uint32_t u1 = c0 + uint32_t((unsigned long long)(c1 - c0) * (warp + 1) / W);
 
-    // ---- page numbers, a batch (up to 16 units of one item) ahead of the copies
-    uint32_t au = u0;                    // next unit to fetch page numbers for
-    int ar = 0;
-    int next_id = -1, next_rec = 0, next_head = 0, next_count = 0;
-    uint64_t src = 0;                    // this lane's record of the current batch (0: none)
-    uint32_t have = 0;
-    int count = 0, at = 0;
+    // ---- records, found a batch (up to 16 units of one item) ahead of their copies: lanes 2 i
+    // and 2 i + 1 hold those of the batch's unit i.  A record past the request's last is replaced
+    // by its first, one of a page that does not exist by the cache's first (and reported): every
+    // unit is two copies, and what they bring is masked or not valid anyway.
+    uint32_t au = u0, next_rec = 0, cur_rec = 0;
+    int ar = 0, next_count = 0, count = 0, at = 0, next_page = 0;
     auto fetch = [&]() {
         next_count = 0;
-        next_id = -1;
         if (au >= u1) return;
-        ar = find_request(cum, ar, a.n_req, au);
-        const Item it = item_at<ROWS>(a, cum, ar, au);
+        const Item it = item_at<ROWS>(a, batch, ar, au);
+        ar = it.r;
         next_count = min(min(16, it.rq.units - it.unit), int(u1 - au));
-        next_head = it.head;
-        next_rec = 2 * (it.rq.first_unit + it.unit) + lane;
-        if (lane < 2 * next_count && (long long)next_rec * kRecordTokens < it.rq.seq) {
-            next_id = a.table[(long long)ar * a.table_stride + next_rec / a.page_records];
-            if (next_id < 0 || next_id >= a.n_pages) {
-                atomicOr(a.status, kStatusBadPage);
-                next_id = -1;
-            }
-        }
+        uint32_t rec = 2 * uint32_t(it.rq.first_unit + it.unit) + lane;
+        if (rec * kRecordTokens >= unsigned(it.rq.seq)) rec = 0;
+        const uint32_t page = rec / uint32_t(a.page_records);
+        next_rec = uint32_t(it.head) * uint32_t(a.page_records) + (rec - page * uint32_t(a.page_records));
+        next_page = it.rq.seq > 0 ? a.table[(long long)ar * a.table_stride + page] : 0;
         au += next_count;
     };
     auto turn_batch = [&]() {
-        src = 0;
-        if (next_id >= 0)
-            src = reinterpret_cast<uint64_t>(a.data) +
-                  (((uint64_t)next_id * a.n_kv + next_head) * a.page_records + next_rec % a.page_records) * uint64_t(S::kRec);
-        have = __ballot_sync(kFull, src != 0);
+        if (next_page < 0 || next_page >= a.n_pages) {
+            atomicOr(a.status, kStatusBadPage);
+            next_page = 0;
+        }
+        cur_rec = uint32_t(next_page) * uint32_t(a.n_kv * a.page_records) + next_rec;
         count = next_count;
         at = 0;
         fetch();
@@ -356,18 +404,14 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
     uint32_t issued = u0;
     int in_stage = 0, out_stage = 0;
     uint32_t out_phase = 0;
-    bool dead = false;
     auto issue = [&]() {
-        if (issued >= u1 || dead) return;
+        if (issued >= u1) return;
         if (at == count) turn_batch();
-        const uint32_t bar = bars + 8 * in_stage;
-        if (lane == 2 * at) {
-            uint32_t bytes = __popc((have >> (2 * at)) & 3u) * S::kRec;
-            if (issued == u0) bytes += a.test_extra_tx;
-            mbar_arrive_expect_tx(bar, bytes);
+        if ((lane >> 1) == at) {
+            const uint32_t bar = bars + 8 * in_stage;
+            if ((lane & 1) == 0) mbar_arrive_expect_tx(bar, S::kStage + (issued == u0 ? a.test_extra_tx : 0u));
+            bulk_load(ring + in_stage * S::kStage + (lane & 1) * S::kRec, a.data + uint64_t(cur_rec) * S::kRec, S::kRec, bar);
         }
-        __syncwarp();
-        if ((lane >> 1) == at && src != 0) bulk_load(ring + in_stage * S::kStage + (lane & 1) * S::kRec, src, S::kRec, bar);
         ++at;
         ++issued;
         in_stage = in_stage + 1 == a.depth ? 0 : in_stage + 1;
@@ -378,25 +422,20 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
     }
 
     // ---- the warp's part, item by item
+    bool dead = false;
     uint32_t u = u0;
     int r = 0;
     while (u < u1) {
-        r = find_request(cum, r, a.n_req, u);
-        const Item it = item_at<ROWS>(a, cum, r, u);
+        const Item it = item_at<ROWS>(a, batch, r, u);
+        r = it.r;
         const int begin = it.rq.seq - it.rq.fresh;
 
-        // Rows: what they see, their queries as matrix operands.
-        Sight sight[PACKED ? 1 : 2];
-        float factor[PACKED ? 1 : 2];
+        // Queries as operand columns: this lane's column is r8, a term of a row (or the row itself),
+        // its values 8 c4 .. 8 c4 + 7 of every block.
 #pragma unroll
-        for (int h = 0; h < (PACKED ? 1 : 2); ++h) {
+        for (int t = 0; t < TILES; ++t) {
             int j, head;
-            row_of<ROWS>(a, it, r8 + 8 * h, j, head);
-            sight[h].pos = begin + j;
-            sight[h].begin = a.span_mask ? begin : 0x7FFFFFFF;
-            sight[h].bits = a.span_mask && j >= 0 ? a.span_mask[it.rq.first_tok + j] : 0u;
-            sight[h].low = a.window > 0 ? sight[h].pos - a.window : -1;
-            if (j < 0) sight[h].pos = -1;
+            row_of<ROWS>(a, it, t * S::kTileRows + r8 / TERMS, j, head);
             float x[NG][8];
             const T* src_row = static_cast<const T*>(a.q) + (long long)(it.rq.first_tok + max(j, 0)) * a.q_stride +
                                (long long)head * D + 8 * c4;
@@ -420,72 +459,56 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
             const int sh = min(141 - e, 126);
             const float up = __uint_as_float(uint32_t(127 + sh) << 23), down = __uint_as_float(uint32_t(127 - sh) << 23);
             const bool finite = e < 255;
-            factor[h] = finite ? a.scale_log2 * down : __uint_as_float(0x7FFFFFFFu);
+            float* const init = reinterpret_cast<float*>(mine + lay.init_off) + t * (NG + 1) * 8;
+            if (c4 == 0) init[NG * 8 + r8] = finite ? a.scale_log2 * (1.0f / kCodeUnit) * down : __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint32_t hi[4], lo[4];
-                float sum_hi = 0.0f, sum_lo = 0.0f;
+                uint32_t v[4];
+                float total_q = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p = finite ? x[g][i] * up : 0.0f, q = finite ? x[g][i + 4] * up : 0.0f;
-                    split_pair(p, q, hi[i], lo[i]);
-                    const float2 fh = __half22float2(bits_h2(hi[i])), fl = __half22float2(bits_h2(lo[i]));
-                    sum_hi += fh.x + fh.y;
-                    sum_lo += fl.x + fl.y;
+                    uint32_t hi, lo;
+                    split_pair(finite ? x[g][i] * up : 0.0f, finite ? x[g][i + 4] * up : 0.0f, hi, lo);
+                    v[i] = TERMS == 2 && (r8 & 1) ? lo : hi;
+                    const float2 f = __half22float2(bits_h2(v[i]));
+                    total_q += f.x + f.y;
                 }
-                if (TERMS == 1) sum_lo = 0.0f;
-                if (!PACKED) sum_hi += sum_lo;
-                sum_hi += __shfl_xor_sync(kFull, sum_hi, 1);
-                sum_hi += __shfl_xor_sync(kFull, sum_hi, 2);
-                if (PACKED) {
-                    sum_lo += __shfl_xor_sync(kFull, sum_lo, 1);
-                    sum_lo += __shfl_xor_sync(kFull, sum_lo, 2);
-                }
-                constexpr float kUlp = -8.0f / 1048576.0f;       // -8 codes of 2^-20
-                float* const init = reinterpret_cast<float*>(mine + lay.init_off) + 16 * g;
-                uint32_t* const m = reinterpret_cast<uint32_t*>(mine + lay.q_off);
-                if (c4 == 0) {
-                    init[r8 + 8 * h] = kUlp * sum_hi;
-                    if (PACKED) init[r8 + 8] = kUlp * sum_lo;
-                }
-                // Operand words: (row, low columns), (row + 8, low), (row, high), (row + 8, high).
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    uint32_t* const w = m + ((2 * g + ks) * 32 + lane) * 4;
-                    w[h] = hi[2 * ks];
-                    w[2 + h] = hi[2 * ks + 1];
-                    if (PACKED) {
-                        w[1] = lo[2 * ks];
-                        w[3] = lo[2 * ks + 1];
-                    } else if (TERMS == 2) {
-                        uint32_t* const l = w + (D / 16) * 128;
-                        l[h] = lo[2 * ks];
-                        l[2 + h] = lo[2 * ks + 1];
-                    }
-                }
+                total_q += __shfl_xor_sync(kFull, total_q, 1);
+                total_q += __shfl_xor_sync(kFull, total_q, 2);
+                if (c4 == 0) init[g * 8 + r8] = -8.0f * kCodeUnit * total_q;
+                *reinterpret_cast<uint4*>(mine + lay.q_off + ((t * NG + g) * 32 + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
         __syncwarp();
         // Keys that every row sees lie in (full_low, full_high]; any row's in (any_low, any_high].
-        int full_high = sight[0].pos, any_high = sight[0].pos;
-        {
-            const int i0 = it.tile * ROWS, i1 = min(i0 + ROWS, it.rq.fresh * a.group) - 1;
-            full_high = begin + i0 / a.group;
-            any_high = begin + i1 / a.group;
-            if (a.span_mask) full_high = min(full_high, begin - 1);
-        }
+        const int i0 = it.tile * ROWS, i1 = min(i0 + ROWS, it.rq.fresh * a.group) - 1;
+        const int any_high = begin + i1 / a.group;
+        const int full_high = a.span_mask ? min(begin + i0 / a.group, begin - 1) : begin + i0 / a.group;
         const int full_low = a.window > 0 ? any_high - a.window : -1;
-        const int any_low = a.window > 0 ? begin + it.tile * ROWS / a.group - a.window : -1;
+        const int any_low = a.window > 0 ? begin + i0 / a.group - a.window : -1;
+        // What this lane's row h of tile t may see (in units that need it).
+        auto sight = [&](int t, int h) {
+            int j, head;
+            row_of<ROWS>(a, it, t * S::kTileRows + H * c4 + h, j, head);
+            Sight s;
+            s.pos = j < 0 ? -1 : begin + j;
+            s.low = a.window > 0 ? begin + j - a.window : -1;
+            s.begin = a.span_mask ? begin : 0x7FFFFFFF;
+            s.bits = a.span_mask && j >= 0 ? a.span_mask[it.rq.first_tok + j] : 0u;
+            return s;
+        };
 
-        constexpr int H = PACKED ? 1 : 2;                  // rows of this lane
-        f2_t o[4 * NG][H];                                 // columns 2 c4, 2 c4 + 1 of the output tiles
+        // Running outputs: of this lane's rows, value 4 r8 + n of block g.
+        float o[TILES][4 * NG][H], ref[TILES][H], sum[TILES][H];
 #pragma unroll
-        for (int n = 0; n < 4 * NG; ++n)
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
-            for (int h = 0; h < H; ++h) o[n][h] = 0ull;
-        float ref[H], sum[H];
+            for (int h = 0; h < H; ++h) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) { ref[h] = -INFINITY; sum[h] = 0.0f; }
+                for (int n = 0; n < 4 * NG; ++n) o[t][n][h] = 0.0f;
+                ref[t][h] = -INFINITY;
+                sum[t][h] = 0.0f;
+            }
 
         const uint32_t item_end = min(it.start + uint32_t(it.rq.units), u1);
         int key0 = (it.rq.first_unit + it.unit) * kUnit;
@@ -505,131 +528,131 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
                 continue;
             }
 
-            // ---- scores of 32 keys: four column tiles of 8
-            uint32_t kw[4][NG], kd[4][NG];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const uint32_t rec = stage + (nt >> 1) * S::kRec;
-#pragma unroll
-                for (int q = 0; q < NS; ++q) {
-                    lds_words<GI>(rec + ((q * 16 + (nt & 1) * 8) * 4 + lane) * GI * 4, &kw[nt][q * GI]);
-                    lds_words<GI>(rec + kv_k_scales(D) + (((nt & 1) * 4 + c4) * NG + q * GI) * 4, &kd[nt][q * GI]);
-                }
-            }
-            f2_t s[4][H];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                for (int h = 0; h < H; ++h) s[nt][h] = 0ull;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const uint4 qa = lds128(qmat + ((2 * g) * 32 + lane) * 16), qb = lds128(qmat + ((2 * g + 1) * 32 + lane) * 16);
-                uint4 la, lb;
-                if (!PACKED && TERMS == 2) {
-                    la = lds128(qmat + ((D / 16 + 2 * g) * 32 + lane) * 16);
-                    lb = lds128(qmat + ((D / 16 + 2 * g + 1) * 32 + lane) * 16);
-                }
-                const float i0 = __uint_as_float(lds32(binit + (16 * g + r8) * 4));
-                const float i1 = __uint_as_float(lds32(binit + (16 * g + r8 + 8) * 4));
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const uint32_t w = kw[nt][g], m = 0x00F000F0u;
-                    const uint32_t b0 = (w << 4) & m, b1 = w & m, b2 = (w >> 4) & m, b3 = (w >> 8) & m;
-                    float acc[4];
-                    mma_f16(acc, qa, b0, b1, i0, i1);
-                    mma_f16(acc, qb, b2, b3);
-                    if (!PACKED && TERMS == 2) {
-                        mma_f16(acc, la, b0, b1);
-                        mma_f16(acc, lb, b2, b3);
-                    }
-                    const f2_t d = f2_of_h2(kd[nt][g]);
-                    if (PACKED) {
-                        s[nt][0] = f2_fma(f2_add(f2_of(acc[0], acc[1]), f2_of(acc[2], acc[3])), d, s[nt][0]);
-                    } else {
-                        s[nt][0] = f2_fma(f2_of(acc[0], acc[1]), d, s[nt][0]);
-                        s[nt][H - 1] = f2_fma(f2_of(acc[2], acc[3]), d, s[nt][H - 1]);
-                    }
-                }
-            }
-            float p[4][H][2];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const float2 t = f2_get(f2_mul(s[nt][h], f2_of(factor[h], factor[h])));
-                    p[nt][h][0] = t.x;
-                    p[nt][h][1] = t.y;
-                }
-            const bool masked = key0 + kUnit - 1 > full_high || key0 <= full_low;
-            if (masked) {
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int h = 0; h < H; ++h)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (!sight[h].sees(key0 + 8 * nt + 2 * c4 + i)) p[nt][h][i] = -INFINITY;
-            }
-
-            // ---- running reference and sum
-            bool grow = false;
-            float top[H];
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                top[h] = fmaxf(p[0][h][0], p[0][h][1]);
-#pragma unroll
-                for (int nt = 1; nt < 4; ++nt) top[h] = fmaxf(top[h], fmaxf(p[nt][h][0], p[nt][h][1]));
-                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
-                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
-                grow |= top[h] > ref[h] + kRefSlack;
-            }
-            float keep[H];                                  // what the outputs so far count for
-#pragma unroll
-            for (int h = 0; h < H; ++h) keep[h] = 1.0f;
-            if (__any_sync(kFull, grow)) {
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const float to = fmaxf(ref[h], top[h]);
-                    if (to != -INFINITY) keep[h] = exp2_fast(ref[h] - to);
-                    ref[h] = to;
-                    sum[h] *= keep[h];
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                const float base = (ref[h] == -INFINITY ? 0.0f : ref[h]) - kProbShift;
-                float add = 0.0f;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        p[nt][h][i] = exp2_fast(p[nt][h][i] - base);
-                        add += p[nt][h][i];
-                    }
-                sum[h] += add;
-            }
-
-            // ---- outputs: the unit's products go into accumulators of their own and are added to
-            // the running outputs in fp32 (the tensor core truncates what it adds to: over a long
-            // cache that bias would grow with the number of units)
-            uint4 pa[2], pl[2];
+            // ---- scores: keys are the product's rows (16 per record: r8 and r8 + 8), query columns
+            // its columns
+            float p[TILES][2][2][H];                       // [record][key r8, r8 + 8]
+            uint32_t kw[2][2][NG];
+            uint32_t kd[2][NG];                            // scales of keys r8 and r8 + 8
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if (PACKED) {
-                    split_pair(p[2 * k][0][0], p[2 * k][0][1], pa[k].x, pa[k].y);
-                    split_pair(p[2 * k + 1][0][0], p[2 * k + 1][0][1], pa[k].z, pa[k].w);
-                } else if (TERMS == 2) {
-                    split_pair(p[2 * k][0][0], p[2 * k][0][1], pa[k].x, pl[k].x);
-                    split_pair(p[2 * k][H - 1][0], p[2 * k][H - 1][1], pa[k].y, pl[k].y);
-                    split_pair(p[2 * k + 1][0][0], p[2 * k + 1][0][1], pa[k].z, pl[k].z);
-                    split_pair(p[2 * k + 1][H - 1][0], p[2 * k + 1][H - 1][1], pa[k].w, pl[k].w);
-                } else {
-                    pa[k].x = h2_bits(__floats2half2_rn(p[2 * k][0][0], p[2 * k][0][1]));
-                    pa[k].y = h2_bits(__floats2half2_rn(p[2 * k][H - 1][0], p[2 * k][H - 1][1]));
-                    pa[k].z = h2_bits(__floats2half2_rn(p[2 * k + 1][0][0], p[2 * k + 1][0][1]));
-                    pa[k].w = h2_bits(__floats2half2_rn(p[2 * k + 1][H - 1][0], p[2 * k + 1][H - 1][1]));
+                const uint32_t rec = stage + k * S::kRec;
+#pragma unroll
+                for (int q = 0; q < NS; ++q) {
+                    uint32_t d0[GI], d1[GI];
+                    lds_words<GI>(rec + ((q * 16) * 4 + lane) * GI * 4, &kw[k][0][q * GI]);
+                    lds_words<GI>(rec + ((q * 16 + 8) * 4 + lane) * GI * 4, &kw[k][1][q * GI]);
+                    lds_words<GI>(rec + kv_k_scales(D) + ((r8 >> 1) * NG + q * GI) * 4, d0);
+                    lds_words<GI>(rec + kv_k_scales(D) + ((4 + (r8 >> 1)) * NG + q * GI) * 4, d1);
+#pragma unroll
+                    for (int i = 0; i < GI; ++i) kd[k][q * GI + i] = __byte_perm(d0[i], d1[i], (r8 & 1) ? 0x7632 : 0x5410);
                 }
             }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint4 qb[TILES];
+                float2 start[TILES];
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    qb[t] = lds128(qmat + ((t * NG + g) * 32 + lane) * 16);
+                    start[t] = lds_f2(binit + ((t * (NG + 1) + g) * 8 + 2 * c4) * 4);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t x[4], y[4];
+                    key_codes(kw[k][0][g], x);
+                    key_codes(kw[k][1][g], y);
+                    const uint4 a0 = make_uint4(x[0], y[0], x[1], y[1]), a1 = make_uint4(x[2], y[2], x[3], y[3]);
+                    const float2 d = __half22float2(bits_h2(kd[k][g]));
+#pragma unroll
+                    for (int t = 0; t < TILES; ++t) {
+                        float acc[4];
+                        mma_f16(acc, a0, qb[t].x, qb[t].y, start[t].x, start[t].y);
+                        mma_f16(acc, a1, qb[t].z, qb[t].w);
+                        float(&to)[2][H] = p[t][k];
+                        if (TERMS == 2) {
+                            const float v = acc[0] + acc[1], w = acc[2] + acc[3];
+                            to[0][0] = g == 0 ? v * d.x : fmaf(v, d.x, to[0][0]);
+                            to[1][0] = g == 0 ? w * d.y : fmaf(w, d.y, to[1][0]);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < H; ++h) {
+                                to[0][h] = g == 0 ? acc[h] * d.x : fmaf(acc[h], d.x, to[0][h]);
+                                to[1][h] = g == 0 ? acc[2 + h] * d.y : fmaf(acc[2 + h], d.y, to[1][h]);
+                            }
+                        }
+                    }
+                }
+            }
+            const bool masked = key0 + kUnit - 1 > full_high || key0 <= full_low;
+            uint32_t pb[TILES][2][2];                      // probabilities as operand columns
+            float keep[TILES][H];                          // what the outputs so far count for
+            bool grow = false;
+            float top[TILES][H];
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                const float2 f = lds_f2(binit + ((t * (NG + 1) + NG) * 8 + 2 * c4) * 4);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) p[t][k][i][h] *= h ? f.y : f.x;
+                    if (masked) {
+                        const Sight s = sight(t, h);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (!s.sees(key0 + 16 * k + 8 * i + r8)) p[t][k][i][h] = -INFINITY;
+                    }
+                    float m = fmaxf(fmaxf(p[t][0][0][h], p[t][0][1][h]), fmaxf(p[t][1][0][h], p[t][1][1][h]));
+                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+                    top[t][h] = m;
+                    grow |= m > ref[t][h] + kRefSlack;
+                    keep[t][h] = 1.0f;
+                }
+            }
+            // ---- running reference and sum
+            if (__any_sync(kFull, grow)) {
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        const float to = fmaxf(ref[t][h], top[t][h]);
+                        if (to != -INFINITY) keep[t][h] = exp2_fast(ref[t][h] - to);
+                        ref[t][h] = to;
+                        sum[t][h] *= keep[t][h];
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const float base = (ref[t][h] == -INFINITY ? 0.0f : ref[t][h]) - kProbShift;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) p[t][k][i][h] = exp2_fast(p[t][k][i][h] - base);
+                    sum[t][h] += (p[t][0][0][h] + p[t][0][1][h]) + (p[t][1][0][h] + p[t][1][1][h]);
+                }
+                // A key's row of operand columns is the transpose of what the product takes.
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float x = p[t][k][i][0];
+                        const __half2 both = TERMS == 2 ? __floats2half2_rn(x, x - __half2float(__float2half_rn(x)))
+                                                        : __floats2half2_rn(x, p[t][k][i][H - 1]);
+                        pb[t][k][i] = transpose8(h2_bits(both));
+                    }
+            }
+
+            // ---- outputs, transposed: values are the product's rows.  The unit's products go into
+            // accumulators of their own and are added to the running outputs in fp32 (the tensor
+            // core truncates what it adds to: over a long cache that bias would grow with the
+            // number of units).
 #pragma unroll
             for (int q = 0; q < NS; ++q) {
                 // Tokens 2 c4, 2 c4 + 1 of each half of each record.
@@ -659,21 +682,20 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
                     if (__any_sync(kFull, odd)) {
 #pragma unroll
                         for (int i = 0; i < GI; ++i) {
-                            bool spoil[H];
 #pragma unroll
-                            for (int h = 0; h < H; ++h) spoil[h] = false;
-                            for (int t = 0; t < kUnit; ++t) {
-                                const uint32_t x = lds16(stage + t / kRecordTokens * S::kRec + kv_v_scales(D) +
-                                                         kv_scale(D, t % kRecordTokens, q * GI + i));
-                                if ((x & 0x7C00u) != 0x7C00u) continue;
+                            for (int t = 0; t < TILES; ++t)
 #pragma unroll
-                                for (int h = 0; h < H; ++h) spoil[h] |= sight[h].sees(key0 + t);
-                            }
+                                for (int h = 0; h < H; ++h) {
+                                    const Sight s = sight(t, h);
+                                    float spoil = 0.0f;
+                                    for (int k = 0; k < kUnit; ++k) {
+                                        const uint32_t x = lds16(stage + k / kRecordTokens * S::kRec + kv_v_scales(D) +
+                                                                 kv_scale(D, k % kRecordTokens, q * GI + i));
+                                        if ((x & 0x7C00u) == 0x7C00u && s.sees(key0 + k)) spoil = NAN;
+                                    }
 #pragma unroll
-                            for (int h = 0; h < H; ++h)
-#pragma unroll
-                                for (int n = 0; n < 4; ++n)
-                                    if (spoil[h]) o[4 * (q * GI + i) + n][h] = f2_of(NAN, NAN);
+                                    for (int n = 0; n < 4; ++n) o[t][4 * (q * GI + i) + n][h] += spoil;
+                                }
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 if ((d[k][i] & 0x7C00u) == 0x7C00u) d[k][i] &= 0xFFFF0000u;
@@ -684,30 +706,30 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
                 }
 #pragma unroll
                 for (int i = 0; i < GI; ++i) {
-                    __half2 less[4];
+                    uint32_t v[4][4];                      // [half][nibble]
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) less[k] = __hmul2(bits_h2(d[k][i]), __float2half2_rn(-24.0f));
+                    for (int k = 0; k < 4; ++k) value_pairs(w[k][i], d[k][i], v[k]);
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        uint32_t v[4];
+                    for (int n = 0; n < 4; n += 2) {
+                        const uint4 a0 = make_uint4(v[0][n], v[0][n + 1], v[1][n], v[1][n + 1]);
+                        const uint4 a1 = make_uint4(v[2][n], v[2][n + 1], v[3][n], v[3][n + 1]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t x = w[k][i], t = n == 0 ? x << 6 : n == 1 ? x << 2 : n == 2 ? x >> 2 : x >> 6;
-                            v[k] = h2_bits(__hfma2(bits_h2((t & 0x03C003C0u) | 0x4C004C00u), bits_h2(d[k][i]), less[k]));
-                        }
-                        float acc[4];
-                        mma_f16(acc, pa[0], v[0], v[1], 0.0f, 0.0f);
-                        mma_f16(acc, pa[1], v[2], v[3]);
-                        if (!PACKED && TERMS == 2) {
-                            mma_f16(acc, pl[0], v[0], v[1]);
-                            mma_f16(acc, pl[1], v[2], v[3]);
-                        }
-                        f2_t(&to)[H] = o[4 * (q * GI + i) + n];
-                        if (PACKED) {
-                            to[0] = f2_fma(to[0], f2_of(keep[0], keep[0]), f2_add(f2_of(acc[0], acc[1]), f2_of(acc[2], acc[3])));
-                        } else {
-                            to[0] = f2_fma(to[0], f2_of(keep[0], keep[0]), f2_of(acc[0], acc[1]));
-                            to[H - 1] = f2_fma(to[H - 1], f2_of(keep[H - 1], keep[H - 1]), f2_of(acc[2], acc[3]));
+                        for (int t = 0; t < TILES; ++t) {
+                            float acc[4];
+                            mma_f16(acc, a0, pb[t][0][0], pb[t][0][1], 0.0f, 0.0f);
+                            mma_f16(acc, a1, pb[t][1][0], pb[t][1][1]);
+                            float(&x)[H] = o[t][4 * (q * GI + i) + n];
+                            float(&y)[H] = o[t][4 * (q * GI + i) + n + 1];
+                            if (TERMS == 2) {
+                                x[0] = fmaf(x[0], keep[t][0], acc[0] + acc[1]);
+                                y[0] = fmaf(y[0], keep[t][0], acc[2] + acc[3]);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < H; ++h) {
+                                    x[h] = fmaf(x[h], keep[t][h], acc[h]);
+                                    y[h] = fmaf(y[h], keep[t][h], acc[2 + h]);
+                                }
+                            }
                         }
                     }
                 }
@@ -719,54 +741,42 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
         }
 
         // ---- the item's end: written out, or left for the join
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            sum[h] += __shfl_xor_sync(kFull, sum[h], 1);
-            sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
-        }
         const bool whole = it.start >= u0 && it.start + uint32_t(it.rq.units) <= u1;
-        if (whole) {
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                int j, head;
-                row_of<ROWS>(a, it, r8 + 8 * h, j, head);
-                if (j < 0) continue;
-                const float inv = sum[h] == 0.0f ? 0.0f : 1.0f / sum[h];
-                const long long tok = it.rq.first_tok + j;
-                T* const dst = static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D + 8 * c4;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float2 x0 = f2_get(o[4 * g][h]), x1 = f2_get(o[4 * g + 1][h]), x2 = f2_get(o[4 * g + 2][h]),
-                                 x3 = f2_get(o[4 * g + 3][h]);
-                    store4(dst + 32 * g, x0.x * inv, x1.x * inv, x2.x * inv, x3.x * inv);
-                    store4(dst + 32 * g + 4, x0.y * inv, x1.y * inv, x2.y * inv, x3.y * inv);
-                }
-                if (a.lse && c4 == 0)
-                    a.lse[tok * a.n_heads + head] = (ref[h] + log2f(sum[h]) - kProbShift) * 0.693147180559945309f;
-            }
-        } else {
-            // The part's last item waits in the warp's ring (every copy into it has been consumed),
-            // an earlier one, whose ring is still in use, in the workspace.
-            const bool last = u == u1;
-            float* const dst = last ? reinterpret_cast<float*>(mine)
+        // The part's last item waits in the warp's ring (every copy into it has been consumed), an
+        // earlier one, whose ring is still in use, in the workspace.
+        const bool last = u == u1;
+        float* const keep_at = last ? reinterpret_cast<float*>(mine)
                                     : a.partial + (2ll * gridDim.x + (long long)blockIdx.x * W + warp) * S::kPartial;
 #pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
             for (int h = 0; h < H; ++h) {
-                const int row = r8 + 8 * h;
+                float l = sum[t][h];
+                l += __shfl_xor_sync(kFull, l, 4);
+                l += __shfl_xor_sync(kFull, l, 8);
+                l += __shfl_xor_sync(kFull, l, 16);
+                const int row = t * S::kTileRows + H * c4 + h;
+                int j, head;
+                row_of<ROWS>(a, it, row, j, head);
+                if (whole && j < 0) continue;
+                const long long tok = it.rq.first_tok + j;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                T* const dst = static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D + 4 * r8;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const float2 x0 = f2_get(o[4 * g][h]), x1 = f2_get(o[4 * g + 1][h]), x2 = f2_get(o[4 * g + 2][h]),
-                                 x3 = f2_get(o[4 * g + 3][h]);
-                    store4(dst + row * D + 32 * g + 8 * c4, x0.x, x1.x, x2.x, x3.x);
-                    store4(dst + row * D + 32 * g + 8 * c4 + 4, x0.y, x1.y, x2.y, x3.y);
+                    const float v0 = o[t][4 * g][h], v1 = o[t][4 * g + 1][h], v2 = o[t][4 * g + 2][h], v3 = o[t][4 * g + 3][h];
+                    if (whole) store4(dst + 32 * g, v0 * inv, v1 * inv, v2 * inv, v3 * inv);
+                    else store4(keep_at + row * D + 32 * g + 4 * r8, v0, v1, v2, v3);
                 }
-                if (c4 == 0) {
-                    dst[ROWS * D + row] = ref[h];
-                    dst[ROWS * D + ROWS + row] = sum[h];
+                if (r8 != 0) continue;
+                if (!whole) {
+                    keep_at[ROWS * D + row] = ref[t][h];
+                    keep_at[ROWS * D + ROWS + row] = l;
+                } else if (a.lse) {
+                    a.lse[tok * a.n_heads + head] = (ref[t][h] + log2f(l) - kProbShift) * 0.693147180559945309f;
                 }
             }
-            if (lane == 0) meta[2 * warp + (last ? 1 : 0)] = it.start;
-        }
+        if (!whole && lane == 0) meta[2 * warp + (last ? 1 : 0)] = it.start;
     }
     __syncthreads();
 
@@ -792,7 +802,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
         if (start == kNoItem) { ++i; continue; }
         int end = i + 1, n = 1;
         while (end < 2 * W && (meta[end] == start || meta[end] == kNoItem)) n += meta[end++] == start;
-        const Item it = item_at<ROWS>(a, cum, find_request(cum, 0, a.n_req, start), start);
+        const Item it = item_at<ROWS>(a, batch, 0, start);
         const bool all = start >= c0 && start + uint32_t(it.rq.units) <= c1;
         float* const dst = a.partial + (2ll * blockIdx.x + (start >= c0 ? 1 : 0)) * S::kPartial;
         for (int e = tid; e < ROWS * D / 4; e += 32 * W) {
@@ -825,7 +835,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS, TERMS>::kWarps, 1) att
     int* const flag = reinterpret_cast<int*>(meta + 2 * W);
     for (int k = 0; k < n_shared; ++k) {
         const uint32_t start = shared_item[k];
-        const Item it = item_at<ROWS>(a, cum, find_request(cum, 0, a.n_req, start), start);
+        const Item it = item_at<ROWS>(a, batch, 0, start);
         const uint32_t first = start / share, last = (start + uint32_t(it.rq.units) - 1) / share;
         const int n = int(last - first) + 1;
         __threadfence();
@@ -878,10 +888,10 @@ struct AttnKernel {
     int warps, partial;
     int (*smem)(int n_req, int depth);
 };
-template <typename T, int D, int ROWS, int TERMS> AttnKernel attn_kernel() {
-    using S = AttnShape<D, ROWS, TERMS>;
-    return {(const void*)&attention_kernel<T, D, ROWS, TERMS>, S::kWarps, S::kPartial,
-            [](int n_req, int depth) { return attn_smem<D, ROWS, TERMS>(n_req, depth).total; }};
+template <typename T, int D, int TILES, int TERMS> AttnKernel attn_kernel() {
+    using S = AttnShape<D, TILES, TERMS>;
+    return {(const void*)&attention_kernel<T, D, TILES, TERMS>, S::kWarps, S::kPartial,
+            [](int n_req, int depth) { return attn_smem<D, TILES, TERMS>(n_req, depth).total; }};
 }
 
 }  // namespace qg

@@ -364,7 +364,7 @@ typedef struct {
     int64_t n_pages;
     int page_tokens, n_kv_heads, head_dim;
 } qg_cache;
-#define QG_CACHE_MAX 16384.0f
+#define QG_CACHE_MAX 65280.0f
 #define QG_DEVICE_BAD_PAGE 8u
 #define QG_DEVICE_BAD_LENGTH 16u
 #define QG_DEVICE_NO_PAGES 32u
@@ -459,7 +459,7 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
  *                16-byte aligned, its first QG_ATTENTION_ZERO_BYTES bytes ZEROED by the caller
  *                once; each call leaves them zeroed.  Calls that share one must be serialized.
  *                After QG_DEVICE_WAIT_TIMEOUT zero them again.
- *   n_req <= 4096, n_heads a multiple of n_kv_heads.
+ *   n_req <= 1024, n_heads a multiple of n_kv_heads.
  * fp32 activations: queries and probabilities enter the tensor cores as two fp16 terms (22
  * bits), sums are fp32; bf16: queries are exact, probabilities one fp16 term.  Outputs are the
  * same on every run; the order of a sum depends on the lengths of the whole batch and on the
