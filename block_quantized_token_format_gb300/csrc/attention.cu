@@ -67,8 +67,9 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     st = device_info(&dev, &sms, &optin, &a.status);
     if (st != QG_OK) return st;
     const int group = n_heads / n_kv;
-    // Column tiles for the rows of a request and key/value head, at most 16 rows at a time.
-    const int64_t rows = std::min<int64_t>(int64_t(max_new) * group, 16);
+    // Column tiles for the rows of a request and key/value head: at most 16 rows at a time, and
+    // equal shares where there are more (24 rows are 12 and 12).
+    const int64_t all_rows = int64_t(max_new) * group, passes = (all_rows + 15) / 16, rows = (all_rows + passes - 1) / passes;
     int tiles = int(act == QG_ACT_F32 ? (rows + 3) / 4 : (rows + 7) / 8), depth = 0;
     AttnKernel k{};
     auto fits = [&](int d) { return size_t(k.smem(n_req, d)) + kStaticSmemReserve <= size_t(optin); };

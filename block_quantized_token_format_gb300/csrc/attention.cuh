@@ -44,6 +44,10 @@
 namespace qg {
 
 constexpr int kUnit = 32;                 // keys per unit: two records
+#ifndef QG_E
+#define QG_E 6
+#endif
+constexpr int kItemCost = QG_E;           // an item's own cost (its queries, its outputs), in units
 constexpr int kMaxAttnReq = 1024;
 constexpr int kAttnGrid = 160;             // most CTAs of a launch (one per SM; the workspace is sized by it)
 static_assert(kAttnGrid * 4 <= QG_ATTENTION_ZERO_BYTES, "one ticket per CTA");
@@ -71,7 +75,7 @@ struct AttnArgs {
 #define QG_W 12
 #endif
 #ifndef QG_VU
-#define QG_VU 1
+#define QG_VU 0
 #endif
 // TILES column tiles of 8 query columns: a row takes TERMS of them (its fp16 terms side by
 // side), so a tile holds 4 rows with two terms or 8 with one.
@@ -95,8 +99,8 @@ template <int D, int TILES, int TERMS> __host__ __device__ inline AttnSmem attn_
     AttnSmem p;
     p.seq_off = (n_req + 1) * 4;                     // after the prefix: lengths, then first new tokens
     p.new_off = p.seq_off + n_req * 4;
-    p.meta_off = (p.new_off + (n_req + 1) * 4 + 7) / 8 * 8;
-    p.warp_off = (p.meta_off + (4 * S::kWarps + 1) * 4 + 127) / 128 * 128;
+    p.meta_off = p.new_off + (n_req + 1) * 4;
+    p.warp_off = (p.meta_off + (3 * S::kWarps + 1) * 4 + 127) / 128 * 128;
     p.q_off = depth * S::kStage;                     // a warp's ring comes first
     p.init_off = p.q_off + S::kQBytes;
     p.bar_off = p.init_off + S::kInitBytes;
@@ -111,6 +115,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" :: "l"(p)); }
 // d = a b + {c0, c1, c0, c1}: an accumulator of its own, so that a start value costs no moves.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1, float c0, float c1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
@@ -230,6 +235,18 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float
     *reinterpret_cast<uint2*>(p) = v;
 }
 
+__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+// Takes a ticket: what the CTA wrote before (and a barrier ordered) is seen by whoever takes a
+// later one, and what others wrote before theirs is seen here.
+__device__ __forceinline__ uint32_t ticket_add(uint32_t* p) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
+}
+
 // ------------------------------------------------------------------------------ work
 
 // A request's share of the work: its visible keys in units (from the first one a window
@@ -255,11 +272,13 @@ struct Batch {
     int n_req;
 };
 
-// An item, decoded from a unit's place in the sequence.
+// An item, decoded from a place in the sequence: kItemCost places that stand for the item's own
+// cost, so that CTAs with many short items get no more work than others, then its units.
 struct Item {
     Request rq;
     int r, head, tile, unit;       // unit: within the item
     uint32_t start;                // the item's first unit in the sequence: its identity
+    uint32_t end;
 };
 template <int ROWS> __device__ __forceinline__ Item item_at(const AttnArgs& a, const Batch& b, int r, uint32_t u) {
     int hi = b.n_req;              // the request whose units hold u, searched from r on (units only grow)
@@ -270,11 +289,12 @@ template <int ROWS> __device__ __forceinline__ Item item_at(const AttnArgs& a, c
     Item it;
     it.r = r;
     it.rq = request_of<ROWS>(a, b.seq[r], b.first[r], b.first[r + 1]);
-    const uint32_t rem = u - b.cum[r], n = rem / uint32_t(it.rq.units);
-    it.unit = int(rem - n * uint32_t(it.rq.units));
+    const uint32_t length = uint32_t(it.rq.units + kItemCost), rem = u - b.cum[r], n = rem / length;
     it.head = int(n / uint32_t(it.rq.tiles));
     it.tile = int(n - uint32_t(it.head) * uint32_t(it.rq.tiles));
-    it.start = u - uint32_t(it.unit);
+    it.start = b.cum[r] + n * length + kItemCost;
+    it.end = it.start + uint32_t(it.rq.units);
+    it.unit = u > it.start ? int(u - it.start) : 0;
     return it;
 }
 
@@ -308,8 +328,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     int* const seqs = reinterpret_cast<int*>(smem + lay.seq_off);
     int* const firsts = reinterpret_cast<int*>(smem + lay.new_off);
     const Batch batch{cum, seqs, firsts, a.n_req};
-    unsigned long long* const wsum = reinterpret_cast<unsigned long long*>(smem + lay.meta_off);   // [W]
-    uint32_t* const meta = reinterpret_cast<uint32_t*>(wsum + W);                 // [W][2] item starts, then a flag
+    uint32_t* const wsum = reinterpret_cast<uint32_t*>(smem + lay.meta_off);      // [W]
+    uint32_t* const meta = wsum + W;                                              // [W][2] item starts, then a flag
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int r8 = lane >> 2, c4 = lane & 3;               // operand row and column group
     uint8_t* const mine = smem + lay.warp_off + warp * lay.warp_bytes;
@@ -321,49 +341,68 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- units per request, prefixed
-    unsigned long long run = 0;
+    uint32_t run = 0;
     bool bad_len = false, bad_page = false;
-    for (int r0 = 0; r0 < a.n_req; r0 += 32 * W) {
-        const int r = r0 + tid;
-        unsigned long long n = 0;
-        if (r < a.n_req) {
-            const int seq = a.seq_len[r], first = a.cu_new[r], end = a.cu_new[r + 1];
-            const bool ok = seq >= 0 && first >= 0 && end >= first && end <= a.n_tok && !(a.span_mask && end - first > 32);
-            // Records beyond the table's row cannot be found: such a request is left out whole.
-            const bool fits = ((long long)seq + kRecordTokens - 1) / kRecordTokens <= a.table_stride * a.page_records;
-            bad_len |= !ok;
-            bad_page |= ok && !fits;
-            if (ok && fits && end > first) {
-                const Request q = request_of<ROWS>(a, seq, first, end);
-                n = (unsigned long long)q.units * unsigned(q.tiles) * unsigned(a.n_kv);
-            }
-            seqs[r] = seq;
-            firsts[r] = first;
-            if (r == a.n_req - 1) firsts[r + 1] = end;
-        }
-        unsigned long long s = n;
+    // A request's units; its lengths go to shared memory for later decoding.
+    auto units_of = [&](int r) -> uint32_t {
+        const int seq = a.seq_len[r], first = a.cu_new[r], end = a.cu_new[r + 1];
+        const bool ok = seq >= 0 && first >= 0 && end >= first && end <= a.n_tok && !(a.span_mask && end - first > 32);
+        // Records beyond the table's row cannot be found: such a request is left out whole.
+        const bool fits = ((long long)seq + kRecordTokens - 1) / kRecordTokens <= a.table_stride * a.page_records;
+        bad_len |= !ok;
+        bad_page |= ok && !fits;
+        seqs[r] = seq;
+        firsts[r] = first;
+        if (r == a.n_req - 1) firsts[r + 1] = end;
+        if (!ok || !fits || end == first) return 0;
+        const Request q = request_of<ROWS>(a, seq, first, end);
+        const unsigned long long n = (unsigned long long)(q.units + kItemCost) * unsigned(q.tiles) * unsigned(a.n_kv);
+        const bool numbered = n < 0x7FFFFFFFull / kMaxAttnReq;       // more than the sequence can number
+        bad_len |= !numbered;
+        return numbered ? uint32_t(n) : 0u;
+    };
+    if (lane < 2) meta[2 * warp + lane] = kNoItem;
+    if (a.n_req <= 32) {
+        // One warp's worth: every warp computes (and writes) the same values, none waits.
+        const uint32_t n = lane < a.n_req ? units_of(lane) : 0u;
+        run = n;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const unsigned long long up = __shfl_up_sync(kFull, s, d);
-            if (lane >= d) s += up;
+            const uint32_t up = __shfl_up_sync(kFull, run, d);
+            if (lane >= d) run += up;
         }
-        if (lane == 31) wsum[warp] = s;
-        __syncthreads();
-        unsigned long long before = run;
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) before += wsum[w];
-            run += wsum[w];
+        if (lane < a.n_req) cum[lane] = run - n;
+        run = __shfl_sync(kFull, run, 31);
+        if (lane == 0) cum[a.n_req] = run;
+        __syncwarp();
+    } else {
+        for (int r0 = 0; r0 < a.n_req; r0 += 32 * W) {
+            const int r = r0 + tid;
+            const uint32_t n = r < a.n_req ? units_of(r) : 0u;
+            uint32_t s = n;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const uint32_t up = __shfl_up_sync(kFull, s, d);
+                if (lane >= d) s += up;
+            }
+            if (lane == 31) wsum[warp] = s;
+            __syncthreads();
+            uint32_t before = run;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const uint32_t x = wsum[w];
+                if (w < warp) before += x;
+                run += x;
+            }
+            if (r < a.n_req) cum[r] = before + s - n;
+            __syncthreads();
         }
-        if (r < a.n_req) cum[r] = uint32_t(before + s - n);
+        if (tid == 0) cum[a.n_req] = run;
         __syncthreads();
     }
-    if (run >= 0x7FFFFFFFull) { bad_len = true; run = 0; }       // more units than the sequence can number
-    if (tid == 0) cum[a.n_req] = uint32_t(run);
-    if (tid < 2 * W) meta[tid] = kNoItem;
     if (blockIdx.x == 0 && bad_len) atomicOr(a.status, kStatusBadLength);
     if (blockIdx.x == 0 && bad_page) atomicOr(a.status, kStatusBadPage);
-    __syncthreads();
-    const uint32_t total = uint32_t(run);
+    const uint32_t total = run;
     // At least one unit per warp: a smaller share would leave warps idle and more CTAs to join.
     const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, uint32_t(W));
     const uint32_t c0 = min(share * blockIdx.x, total), c1 = min(c0 + share, total);
@@ -382,13 +421,23 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         if (au >= u1) return;
         const Item it = item_at<ROWS>(a, batch, ar, au);
         ar = it.r;
-        next_count = min(min(16, it.rq.units - it.unit), int(u1 - au));
+        if (it.start >= u1) return;
+        next_count = min(min(16, it.rq.units - it.unit), int(u1 - max(au, it.start)));
+        au = max(au, it.start) + next_count;
         uint32_t rec = 2 * uint32_t(it.rq.first_unit + it.unit) + lane;
         if (rec * kRecordTokens >= unsigned(it.rq.seq)) rec = 0;
         const uint32_t page = rec / uint32_t(a.page_records);
         next_rec = uint32_t(it.head) * uint32_t(a.page_records) + (rec - page * uint32_t(a.page_records));
         next_page = it.rq.seq > 0 ? a.table[(long long)ar * a.table_stride + page] : 0;
-        au += next_count;
+        if (it.unit == 0) {                    // the item's queries, for when it begins
+            for (int i = lane; i < ROWS * D * int(sizeof(T)) / 128; i += 32) {
+                int j, head;
+                row_of<ROWS>(a, it, i * 128 / (D * int(sizeof(T))), j, head);
+                if (j >= 0)
+                    prefetch_l1(static_cast<const T*>(a.q) + (long long)(it.rq.first_tok + j) * a.q_stride + (long long)head * D +
+                                i * (128 / int(sizeof(T))) % D);
+            }
+        }
     };
     auto turn_batch = [&]() {
         if (next_page < 0 || next_page >= a.n_pages) {
@@ -401,25 +450,24 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         fetch();
     };
     // ---- the ring
-    uint32_t issued = u0;
+    uint32_t issued = 0, consumed = 0;
     int in_stage = 0, out_stage = 0;
     uint32_t out_phase = 0;
     auto issue = [&]() {
-        if (issued >= u1) return;
-        if (at == count) turn_batch();
+        if (at == count) {
+            if (next_count == 0) return;
+            turn_batch();
+        }
         if ((lane >> 1) == at) {
             const uint32_t bar = bars + 8 * in_stage;
-            if ((lane & 1) == 0) mbar_arrive_expect_tx(bar, S::kStage + (issued == u0 ? a.test_extra_tx : 0u));
+            if ((lane & 1) == 0) mbar_arrive_expect_tx(bar, S::kStage + (issued == 0 ? a.test_extra_tx : 0u));
             bulk_load(ring + in_stage * S::kStage + (lane & 1) * S::kRec, a.data + uint64_t(cur_rec) * S::kRec, S::kRec, bar);
         }
         ++at;
         ++issued;
         in_stage = in_stage + 1 == a.depth ? 0 : in_stage + 1;
     };
-    if (u0 < u1) {
-        fetch();
-        for (int i = 0; i < a.depth; ++i) issue();
-    }
+    fetch();
 
     // ---- the warp's part, item by item
     bool dead = false;
@@ -428,29 +476,39 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     while (u < u1) {
         const Item it = item_at<ROWS>(a, batch, r, u);
         r = it.r;
+        u = max(u, it.start);
+        if (u >= u1) break;
         const int begin = it.rq.seq - it.rq.fresh;
 
         // Queries as operand columns: this lane's column is r8, a term of a row (or the row itself),
-        // its values 8 c4 .. 8 c4 + 7 of every block.
+        // its values 8 c4 .. 8 c4 + 7 of every block.  The first item's are requested before the
+        // ring's first copies, behind which they would wait.
+        float x[TILES][NG][8];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
             int j, head;
             row_of<ROWS>(a, it, t * S::kTileRows + r8 / TERMS, j, head);
-            float x[NG][8];
             const T* src_row = static_cast<const T*>(a.q) + (long long)(it.rq.first_tok + max(j, 0)) * a.q_stride +
                                (long long)head * D + 8 * c4;
-            uint32_t top = 0;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 if (j >= 0) {
-                    load8(src_row + 32 * g, x[g]);
+                    load8(src_row + 32 * g, x[t][g]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[g][i] = 0.0f;
+                    for (int i = 0; i < 8; ++i) x[t][g][i] = 0.0f;
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[g][i]) & 0x7FFFFFFFu);
             }
+        }
+        if (issued == 0)
+            for (int i = 0; i < a.depth; ++i) issue();
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[t][g][i]) & 0x7FFFFFFFu);
             top = max(top, __shfl_xor_sync(kFull, top, 1));
             top = max(top, __shfl_xor_sync(kFull, top, 2));
             // 2^s brings the row's largest magnitude to [2^14, 2^15) (s at most 126); a row with a
@@ -468,7 +526,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t hi, lo;
-                    split_pair(finite ? x[g][i] * up : 0.0f, finite ? x[g][i + 4] * up : 0.0f, hi, lo);
+                    split_pair(finite ? x[t][g][i] * up : 0.0f, finite ? x[t][g][i + 4] * up : 0.0f, hi, lo);
                     v[i] = TERMS == 2 && (r8 & 1) ? lo : hi;
                     const float2 f = __half22float2(bits_h2(v[i]));
                     total_q += f.x + f.y;
@@ -510,7 +568,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 sum[t][h] = 0.0f;
             }
 
-        const uint32_t item_end = min(it.start + uint32_t(it.rq.units), u1);
+        const uint32_t item_end = min(it.end, u1);
         int key0 = (it.rq.first_unit + it.unit) * kUnit;
         for (; u < item_end; ++u, key0 += kUnit) {
             const uint32_t stage = ring + out_stage * S::kStage;
@@ -520,7 +578,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 // Gave up: no more copies; the ones in flight land (bounded again) before the
                 // ring is reused or the CTA ends.  The rest of the part is passed over.
                 if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
-                for (uint32_t v = u; v < issued; ++v) {
+                for (; consumed < issued; ++consumed) {
                     mbar_wait(bars + 8 * out_stage, out_phase, a.drain_limit);
                     out_stage = out_stage + 1 == a.depth ? 0 : out_stage + 1;
                     if (out_stage == 0) out_phase ^= 1;
@@ -735,16 +793,17 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 }
             }
             __syncwarp();                                   // every lane has read the stage
+            ++consumed;
             out_stage = out_stage + 1 == a.depth ? 0 : out_stage + 1;
             if (out_stage == 0) out_phase ^= 1;
             issue();
         }
 
         // ---- the item's end: written out, or left for the join
-        const bool whole = it.start >= u0 && it.start + uint32_t(it.rq.units) <= u1;
+        const bool whole = it.start >= u0 && it.end <= u1;
         // The part's last item waits in the warp's ring (every copy into it has been consumed), an
         // earlier one, whose ring is still in use, in the workspace.
-        const bool last = u == u1;
+        const bool last = consumed == issued && at == count && next_count == 0;
         float* const keep_at = last ? reinterpret_cast<float*>(mine)
                                     : a.partial + (2ll * gridDim.x + (long long)blockIdx.x * W + warp) * S::kPartial;
 #pragma unroll
@@ -780,105 +839,121 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     }
     __syncthreads();
 
-    // ---- join the warps' parts, in order; an item that other CTAs share leaves one partial
+    // ---- join the warps' parts, in order.  Part i is warp i / 2's earlier (even) or last one; the
+    // parts of one item are neighbours.  Every warp reads the list for itself.
     auto part = [&](int i) -> const float* {
         return (i & 1) ? reinterpret_cast<const float*>(smem + lay.warp_off + (i >> 1) * lay.warp_bytes)
                        : a.partial + (2ll * gridDim.x + (long long)blockIdx.x * W + (i >> 1)) * S::kPartial;
     };
-    auto put = [&](const Item& it, int row, int col, float4 v, float m, float l) {
+    auto put = [&](const Item& it, int row, int col, float2 v, float m, float l) {
         int j, head;
         row_of<ROWS>(a, it, row, j, head);
         if (j < 0) return;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const long long tok = it.rq.first_tok + j;
-        store4(static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D + col, v.x * inv, v.y * inv, v.z * inv,
-               v.w * inv);
+        store2(static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D + col, v.x * inv, v.y * inv);
         if (a.lse && col == 0) a.lse[tok * a.n_heads + head] = (m + log2f(l) - kProbShift) * 0.693147180559945309f;
     };
+    static_assert(2 * W <= 32, "a lane per part");
+    const uint32_t my_start = lane < 2 * W ? meta[lane] : kNoItem;
+    uint32_t left = __ballot_sync(kFull, my_start != kNoItem);
     uint32_t shared_item[2];
     int n_shared = 0;
-    for (int i = 0; i < 2 * W;) {
-        const uint32_t start = meta[i];
-        if (start == kNoItem) { ++i; continue; }
-        int end = i + 1, n = 1;
-        while (end < 2 * W && (meta[end] == start || meta[end] == kNoItem)) n += meta[end++] == start;
+    while (left != 0) {
+        const uint32_t start = __shfl_sync(kFull, my_start, __ffs(int(left)) - 1);
+        const uint32_t parts = __ballot_sync(kFull, my_start == start);
+        left &= ~parts;
         const Item it = item_at<ROWS>(a, batch, 0, start);
-        const bool all = start >= c0 && start + uint32_t(it.rq.units) <= c1;
+        const bool all = start >= c0 && it.end <= c1;
         float* const dst = a.partial + (2ll * blockIdx.x + (start >= c0 ? 1 : 0)) * S::kPartial;
-        for (int e = tid; e < ROWS * D / 4; e += 32 * W) {
-            const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
-            float m = -INFINITY;
-            for (int k = i; k < end; ++k)
-                if (meta[k] == start) m = fmaxf(m, part(k)[ROWS * D + row]);
-            float l = 0.0f;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int k = i; k < end; ++k) {
-                if (meta[k] != start) continue;
-                const float* const p = part(k);
-                const float f = m == -INFINITY ? 1.0f : exp2_fast(p[ROWS * D + row] - m);
-                const float4 x = *reinterpret_cast<const float4*>(p + row * D + col);
-                l = fmaf(p[ROWS * D + ROWS + row], f, l);
-                v.x = fmaf(x.x, f, v.x); v.y = fmaf(x.y, f, v.y); v.z = fmaf(x.z, f, v.z); v.w = fmaf(x.w, f, v.w);
+        for (int row = warp; row < ROWS; row += W) {
+            // A warp per row: the parts' weights by lane, then the row's values.
+            const bool has = (parts >> lane) & 1u;
+            const float* const p = part(has ? lane : 1);
+            const float mi = has ? p[ROWS * D + row] : -INFINITY, li = has ? p[ROWS * D + ROWS + row] : 0.0f;
+            float m = mi;
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+            const float f = m == -INFINITY ? 1.0f : exp2_fast(mi - m);
+            float l = has ? li * f : 0.0f;
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(kFull, l, d);
+            float2 v[D / 64];
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) v[k] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+            for (uint32_t rest = parts; rest != 0; rest &= rest - 1) {
+                const int i = __ffs(int(rest)) - 1;
+                const float fi = __shfl_sync(kFull, f, i);
+                const float2* const x = reinterpret_cast<const float2*>(part(i) + row * D) + lane;
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k) {
+                    const float2 y = x[32 * k];
+                    v[k].x = fmaf(y.x, fi, v[k].x);
+                    v[k].y = fmaf(y.y, fi, v[k].y);
+                }
             }
-            if (all) {
-                put(it, row, col, v, m, l);
-            } else {
-                *reinterpret_cast<float4*>(dst + row * D + col) = v;
-                if (col == 0) { dst[ROWS * D + row] = m; dst[ROWS * D + ROWS + row] = l; }
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                if (all) put(it, row, 64 * k + 2 * lane, v[k], m, l);
+                else *(reinterpret_cast<float2*>(dst + row * D) + 32 * k + lane) = v[k];
             }
+            if (!all && lane == 0) { dst[ROWS * D + row] = m; dst[ROWS * D + ROWS + row] = l; }
         }
         if (!all && n_shared < 2) shared_item[n_shared++] = start;
-        i = end;
     }
 
     // ---- the last CTA of a shared item joins the CTAs' partials, in order
-    int* const flag = reinterpret_cast<int*>(meta + 2 * W);
+    uint32_t* const flag = meta + 2 * W;
     for (int k = 0; k < n_shared; ++k) {
         const uint32_t start = shared_item[k];
         const Item it = item_at<ROWS>(a, batch, 0, start);
-        const uint32_t first = start / share, last = (start + uint32_t(it.rq.units) - 1) / share;
+        const uint32_t first = start / share, last = (it.end - 1) / share;
         const int n = int(last - first) + 1;
-        __threadfence();
         __syncthreads();
         if (tid == 0) {
-            const bool mine_last = atomicAdd(a.tickets + first, 1u) == uint32_t(n - 1);
+            const bool mine_last = ticket_add(a.tickets + first) == uint32_t(n - 1);
             if (mine_last) a.tickets[first] = 0u;
             *flag = mine_last;
         }
         __syncthreads();
-        if (!*flag) continue;
-        __threadfence();
-        auto cta_part = [&](int i) { return a.partial + (2ll * (first + i) + (i == 0 ? 1 : 0)) * S::kPartial; };
-        // Weights of the partials, per row, where the rings were: [ROWS][n], then m[ROWS], l[ROWS].
-        float* const wt = reinterpret_cast<float*>(smem + lay.warp_off);
-        for (int row = warp; row < ROWS; row += W) {
-            float m = -INFINITY;
-            for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(cta_part(i) + ROWS * D + row));
+        if (*flag == 0) continue;
+        const float* const p0 = a.partial + (2ll * first + 1) * S::kPartial;     // the first CTA's part is its last one
+        const float* const p1 = a.partial + 2ll * (first + 1) * S::kPartial;     // the others' their first
+        for (int e = tid; e < ROWS * D / 2; e += 32 * W) {
+            const int row = e / (D / 2), col = (e - row * (D / 2)) * 2;
+            float m = -INFINITY, l = 0.0f;
+            float2 v = make_float2(0.0f, 0.0f);
+            // Eight partials' loads at a time (one round trip to L2), then their sums in order.
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float mi[8], li[8];
+                float2 x[8];
 #pragma unroll
-            for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-            float l = 0.0f;
-            for (int i = lane; i < n; i += 32) {
-                const float f = m == -INFINITY ? 1.0f : exp2_fast(__ldcg(cta_part(i) + ROWS * D + row) - m);
-                wt[row * n + i] = f;
-                l = fmaf(__ldcg(cta_part(i) + ROWS * D + ROWS + row), f, l);
-            }
+                for (int i = 0; i < 8; ++i) {
+                    const float* const p = i0 + i == 0 ? p0 : p1 + 2ll * (i0 + i - 1) * S::kPartial;
+                    const bool in = i0 + i < n;
+                    mi[i] = in ? __ldcg(p + ROWS * D + row) : -INFINITY;
+                    li[i] = in ? __ldcg(p + ROWS * D + ROWS + row) : 0.0f;
+                    x[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + row * D + col)) : make_float2(0.0f, 0.0f);
+                }
+                float to = m;
 #pragma unroll
-            for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(kFull, l, d);
-            if (lane == 0) { wt[ROWS * n + row] = m; wt[ROWS * n + ROWS + row] = l; }
-        }
-        __syncthreads();
-        for (int e = tid; e < ROWS * D / 4; e += 32 * W) {
-            const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float f = wt[row * n + i];
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(cta_part(i) + row * D + col));
-                v.x = fmaf(x.x, f, v.x); v.y = fmaf(x.y, f, v.y); v.z = fmaf(x.z, f, v.z); v.w = fmaf(x.w, f, v.w);
+                for (int i = 0; i < 8; ++i) to = fmaxf(to, mi[i]);
+                const float f = to == -INFINITY ? 1.0f : exp2_fast(m - to);
+                m = to;
+                l *= f;
+                v.x *= f;
+                v.y *= f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float w = m == -INFINITY ? 1.0f : exp2_fast(mi[i] - m);
+                    l = fmaf(li[i], w, l);
+                    v.x = fmaf(x[i].x, w, v.x);
+                    v.y = fmaf(x[i].y, w, v.y);
+                }
             }
-            put(it, row, col, v, wt[ROWS * n + row], wt[ROWS * n + ROWS + row]);
+            put(it, row, col, v, m, l);
         }
-        __syncthreads();
     }
 }
 
