@@ -74,16 +74,13 @@ struct AttnArgs {
 #ifndef QG_W
 #define QG_W 12
 #endif
-#ifndef QG_VU
-#define QG_VU 0
-#endif
 // TILES column tiles of 8 query columns: a row takes TERMS of them (its fp16 terms side by
 // side), so a tile holds 4 rows with two terms or 8 with one.
 template <int D, int TILES, int TERMS> struct AttnShape {
     static constexpr int kLaneRows = 2 / TERMS;                      // rows a lane holds per tile
     static constexpr int kTileRows = 8 / TERMS;
     static constexpr int kRows = TILES * kTileRows;
-    static constexpr int kWarps = D == 256 ? 10 - TILES : QG_W;
+    static constexpr int kWarps = D == 256 ? 10 - TILES : TILES == 1 ? QG_W : 12;
     static constexpr int kRec = kv_record_bytes(D);
     static constexpr int kStage = 2 * kRec;
     static constexpr int kQBytes = TILES * kv_groups(D) * 512;       // queries in operand order
@@ -170,26 +167,25 @@ __device__ __forceinline__ void key_codes(uint32_t w, uint32_t (&b)[4]) {
     b[2] = (w >> 4) & m;
     b[3] = (w >> 8) & m;
 }
-// The four value pairs of a word (nibble n of two tokens) times the tokens' scales d: exact.
-__device__ __forceinline__ void value_pairs(uint32_t w, uint32_t d, uint32_t (&v)[4]) {
-    const __half2 e = bits_h2(d);
-#if QG_VU == 1
-    const __half2 less = __hmul2(e, __float2half2_rn(-8.0f));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t t = i ? w >> 8 : w;
-        const __half2 y = bits_h2((t & 0x00FF00FFu) | 0x64006400u), z = bits_h2((t & 0x00F000F0u) | 0x64006400u);
-        v[2 * i] = h2_bits(__hfma2(__hsub2(y, z), e, less));
-        v[2 * i + 1] = h2_bits(__hmul2(__hfma2(z, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f)), e));
-    }
-#else
-    const __half2 less = __hmul2(e, __float2half2_rn(-24.0f));
+// The four value pairs of a word (nibble n of two tokens) times the tokens' scales d: with the
+// nibble in bits 6..9 under the exponent of 16, (16 + code) * d - 24 * d in one rounding, of
+// an exact result.  The mask and the exponent come in registers, so that one three-input
+// logic instruction places a pair.
+__device__ __forceinline__ void value_pairs(uint32_t w, uint32_t d, uint32_t mask, uint32_t magic, uint32_t (&v)[4]) {
+    const __half2 e = bits_h2(d), less = __hmul2(e, __float2half2_rn(-24.0f));
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         const uint32_t t = n == 0 ? w << 6 : n == 1 ? w << 2 : n == 2 ? w >> 2 : w >> 6;
-        v[n] = h2_bits(__hfma2(bits_h2((t & 0x03C003C0u) | 0x4C004C00u), e, less));
+        uint32_t x;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(t), "r"(mask), "r"(magic));
+        v[n] = h2_bits(__hfma2(bits_h2(x), e, less));
     }
-#endif
+}
+// A value the compiler does not see through.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    uint32_t y;
+    asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 // The transpose of an 8x8 matrix of fp16: lane 4 r + c holds row r, columns 2 c and 2 c + 1.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -470,6 +466,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     fetch();
 
     // ---- the warp's part, item by item
+    const uint32_t mask = opaque(0x03C003C0u), magic = opaque(0x4C004C00u);
     bool dead = false;
     uint32_t u = u0;
     int r = 0;
@@ -766,7 +763,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 for (int i = 0; i < GI; ++i) {
                     uint32_t v[4][4];                      // [half][nibble]
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) value_pairs(w[k][i], d[k][i], v[k]);
+                    for (int k = 0; k < 4; ++k) value_pairs(w[k][i], d[k][i], mask, magic, v[k]);
 #pragma unroll
                     for (int n = 0; n < 4; n += 2) {
                         const uint4 a0 = make_uint4(v[0][n], v[0][n + 1], v[1][n], v[1][n + 1]);
