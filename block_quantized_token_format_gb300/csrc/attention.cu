@@ -106,7 +106,8 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     a.page_records = cache->page_tokens / kRecordTokens;
     a.window = window;
     a.depth = depth;
-    a.scale_log2 = float(double(scale) * 1.4426950408889634);
+    a.scale_log2 = scale == 0.0f ? 1.0f : float(std::fabs(double(scale)) * 1.4426950408889634);
+    a.scale_sign = scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f;
     a.wait_limit = wait_limit();
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.test_extra_tx = test_extra_tx();

@@ -20,13 +20,10 @@
 // decode step has 1 to 32 rows per key/value head, far below the 64 or 128 rows of a tcgen05
 // tile, and operands that come out of nibbles in registers would have to go back through
 // shared memory for it.  Every operand is exact:
-//  * scores: a key's codes enter as they are, as the fp16 subnormals code * 2^-20 (a shift and
-//    a mask per two codes, no arithmetic); the sum starts at -8 * sum(q) of its block, and the
-//    block's scale multiplies the fp32 result. (Four bits lower, code * 2^-24, would save
-//    half the shifts, but the tensor core aligns products by their exponent fields, and a
-//    subnormal that far down loses 6 bits of the sum: measured 9 ulps against 0.17.) A query is
-//    scaled by a power of two to [2^14, 2^15) and split into two fp16 terms (22 bits; one term
-//    is exact for bf16 queries).
+//  * scores: a key's codes enter as they are, as fp16 subnormals (a shift and a mask per two
+//    codes, no arithmetic); the sum starts at -8 * sum(q) of its block, and the block's scale
+//    multiplies the fp32 result.  A query is scaled by a power of two to [2^14, 2^15) and split
+//    into two fp16 terms (22 bits; one term is exact for bf16 queries).
 //  * outputs: a value is (16 + code) * d - 24 * d in one fp16 FMA, which is exact because
 //    d has 8 significant bits; probabilities are two fp16 terms (one for bf16 outputs), scaled
 //    by 2^7 relative to a reference that follows the running maximum within 2^8, so that the
@@ -53,7 +50,9 @@ constexpr int kAttnGrid = 160;             // most CTAs of a launch (one per SM;
 static_assert(kAttnGrid * 4 <= QG_ATTENTION_ZERO_BYTES, "one ticket per CTA");
 constexpr float kProbShift = 7.0f;        // probabilities are scaled by 2^7 ...
 constexpr float kRefSlack = 8.0f;         // ... and the reference follows the maximum within 2^8: below 2^15
+constexpr float kNoRef = -3.0e38f;        // the reference before the first visible key: any score is above it
 constexpr uint32_t kNoItem = 0xFFFFFFFFu;
+constexpr int kMetaInts = 6;              // of an unfinished item: start, end, first token, new tokens, head, tile
 
 struct AttnArgs {
     const uint8_t* data;
@@ -67,12 +66,13 @@ struct AttnArgs {
     unsigned int* status;
     long long q_stride, out_stride, table_stride, n_tok, n_pages;
     int n_req, n_heads, n_kv, group, page_records, window, depth;
-    float scale_log2;          // scale * log2(e)
+    float scale_log2;          // |scale| * log2(e) (1 where that is 0)
+    float scale_sign;          // the scale's sign (0 for 0), which goes into the queries
     uint32_t wait_limit, drain_limit, test_extra_tx;
 };
 
 #ifndef QG_W
-#define QG_W 12
+#define QG_W 16
 #endif
 // TILES column tiles of 8 query columns: a row takes TERMS of them (its fp16 terms side by
 // side), so a tile holds 4 rows with two terms or 8 with one.
@@ -81,6 +81,8 @@ template <int D, int TILES, int TERMS> struct AttnShape {
     static constexpr int kTileRows = 8 / TERMS;
     static constexpr int kRows = TILES * kTileRows;
     static constexpr int kWarps = D == 256 ? 10 - TILES : TILES == 1 ? QG_W : 12;
+    static constexpr float kCodeUnit = TERMS == 1 ? 1.0f / 16777216.0f : 1.0f / 1048576.0f;    // what a code of 1 stands for
+    static constexpr float kOddScale = TERMS == 1 ? 0.0625f : 1.0f;
     static constexpr int kRec = kv_record_bytes(D);
     static constexpr int kStage = 2 * kRec;
     static constexpr int kQBytes = TILES * kv_groups(D) * 512;       // queries in operand order
@@ -97,7 +99,7 @@ template <int D, int TILES, int TERMS> __host__ __device__ inline AttnSmem attn_
     p.seq_off = (n_req + 1) * 4;                     // after the prefix: lengths, then first new tokens
     p.new_off = p.seq_off + n_req * 4;
     p.meta_off = p.new_off + (n_req + 1) * 4;
-    p.warp_off = (p.meta_off + (3 * S::kWarps + 1) * 4 + 127) / 128 * 128;
+    p.warp_off = (p.meta_off + (S::kWarps + 2 * S::kWarps * kMetaInts + 1) * 4 + 127) / 128 * 128;
     p.q_off = depth * S::kStage;                     // a warp's ring comes first
     p.init_off = p.q_off + S::kQBytes;
     p.bar_off = p.init_off + S::kInitBytes;
@@ -158,14 +160,24 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
     hi = h2_bits(h);
     lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
 }
-// The four pairs of codes of a key word (nibbles i and i + 4), as fp16 code * 2^-20.
-constexpr float kCodeUnit = 1.0f / 1048576.0f;
-__device__ __forceinline__ void key_codes(uint32_t w, uint32_t (&b)[4]) {
+// The four pairs of codes of a key word (nibbles i and i + 4) as fp16 subnormals: code * 2^-20,
+// or with COARSE code * 2^-24 and code * 2^-20 in turn (two shifts less; the queries of the odd
+// pairs then carry 2^-4).  The tensor core aligns products by their exponent fields, so
+// 2^-24 costs 6 bits of the sum (measured 9 ulps rms against 0.17): it serves bf16 only.
+template <bool COARSE> __device__ __forceinline__ void key_codes(uint32_t w, uint32_t (&b)[4]) {
     const uint32_t m = 0x00F000F0u;
-    b[0] = (w << 4) & m;
-    b[1] = w & m;
-    b[2] = (w >> 4) & m;
-    b[3] = (w >> 8) & m;
+    if (COARSE) {
+        const uint32_t v = w >> 8, l = 0x000F000Fu;
+        b[0] = w & l;
+        b[1] = w & m;
+        b[2] = v & l;
+        b[3] = v & m;
+    } else {
+        b[0] = (w << 4) & m;
+        b[1] = w & m;
+        b[2] = (w >> 4) & m;
+        b[3] = (w >> 8) & m;
+    }
 }
 // The four value pairs of a word (nibble n of two tokens) times the tokens' scales d: with the
 // nibble in bits 6..9 under the exponent of 16, (16 + code) * d - 24 * d in one rounding, of
@@ -325,8 +337,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     int* const firsts = reinterpret_cast<int*>(smem + lay.new_off);
     const Batch batch{cum, seqs, firsts, a.n_req};
     uint32_t* const wsum = reinterpret_cast<uint32_t*>(smem + lay.meta_off);      // [W]
-    uint32_t* const meta = wsum + W;                                              // [W][2] item starts, then a flag
-    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    uint32_t* const meta = wsum + W;                                              // [W][2][kMetaInts], then a flag
+    const int tid = int(threadIdx.x), lane = tid & 31;
+    // A warp's place in the CTA's share: neighbours in the share sit on different schedulers, so
+    // that a share of few units is spread over all four.
+    const int warp = W % 4 == 0 ? (tid >> 5) % (W / 4) * 4 + (tid >> 5) / (W / 4) : tid >> 5;
     const int r8 = lane >> 2, c4 = lane & 3;               // operand row and column group
     uint8_t* const mine = smem + lay.warp_off + warp * lay.warp_bytes;
     const uint32_t ring = smem_addr(mine), qmat = ring + lay.q_off, binit = ring + lay.init_off, bars = ring + lay.bar_off;
@@ -357,7 +372,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         bad_len |= !numbered;
         return numbered ? uint32_t(n) : 0u;
     };
-    if (lane < 2) meta[2 * warp + lane] = kNoItem;
+    if (lane < 2) meta[(2 * warp + lane) * kMetaInts] = kNoItem;
     if (a.n_req <= 32) {
         // One warp's worth: every warp computes (and writes) the same values, none waits.
         const uint32_t n = lane < a.n_req ? units_of(lane) : 0u;
@@ -381,13 +396,13 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 const uint32_t up = __shfl_up_sync(kFull, s, d);
                 if (lane >= d) s += up;
             }
-            if (lane == 31) wsum[warp] = s;
+            if (lane == 31) wsum[tid >> 5] = s;
             __syncthreads();
             uint32_t before = run;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 const uint32_t x = wsum[w];
-                if (w < warp) before += x;
+                if (w < (tid >> 5)) before += x;
                 run += x;
             }
             if (r < a.n_req) cum[r] = before + s - n;
@@ -399,8 +414,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     if (blockIdx.x == 0 && bad_len) atomicOr(a.status, kStatusBadLength);
     if (blockIdx.x == 0 && bad_page) atomicOr(a.status, kStatusBadPage);
     const uint32_t total = run;
-    // At least one unit per warp: a smaller share would leave warps idle and more CTAs to join.
-    const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, uint32_t(W));
+#ifndef QG_MS
+#define QG_MS 4
+#endif
+    const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, uint32_t(QG_MS));
     const uint32_t c0 = min(share * blockIdx.x, total), c1 = min(c0 + share, total);
     if (c0 == c1) return;
     const uint32_t u0 = c0 + uint32_t((unsigned long long)(c1 - c0) * warp / W);
@@ -512,10 +529,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             // NaN or an infinity has NaN scores.
             const int e = int(top >> 23);
             const int sh = min(141 - e, 126);
-            const float up = __uint_as_float(uint32_t(127 + sh) << 23), down = __uint_as_float(uint32_t(127 - sh) << 23);
+            const float up = __uint_as_float(uint32_t(127 + sh) << 23) * a.scale_sign, down = __uint_as_float(uint32_t(127 - sh) << 23);
             const bool finite = e < 255;
             float* const init = reinterpret_cast<float*>(mine + lay.init_off) + t * (NG + 1) * 8;
-            if (c4 == 0) init[NG * 8 + r8] = finite ? a.scale_log2 * (1.0f / kCodeUnit) * down : __uint_as_float(0x7FFFFFFFu);
+            if (c4 == 0) init[NG * 8 + r8] = finite ? a.scale_log2 * (1.0f / S::kCodeUnit) * down : __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 uint32_t v[4];
@@ -523,14 +540,15 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t hi, lo;
-                    split_pair(finite ? x[t][g][i] * up : 0.0f, finite ? x[t][g][i + 4] * up : 0.0f, hi, lo);
+                    const float w = (i & 1) ? up * S::kOddScale : up;
+                    split_pair(finite ? x[t][g][i] * w : 0.0f, finite ? x[t][g][i + 4] * w : 0.0f, hi, lo);
                     v[i] = TERMS == 2 && (r8 & 1) ? lo : hi;
                     const float2 f = __half22float2(bits_h2(v[i]));
-                    total_q += f.x + f.y;
+                    total_q += (f.x + f.y) * ((i & 1) ? 1.0f / S::kOddScale : 1.0f);
                 }
                 total_q += __shfl_xor_sync(kFull, total_q, 1);
                 total_q += __shfl_xor_sync(kFull, total_q, 2);
-                if (c4 == 0) init[g * 8 + r8] = -8.0f * kCodeUnit * total_q;
+                if (c4 == 0) init[g * 8 + r8] = -8.0f * S::kCodeUnit * total_q;
                 *reinterpret_cast<uint4*>(mine + lay.q_off + ((t * NG + g) * 32 + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
@@ -561,7 +579,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             for (int h = 0; h < H; ++h) {
 #pragma unroll
                 for (int n = 0; n < 4 * NG; ++n) o[t][n][h] = 0.0f;
-                ref[t][h] = -INFINITY;
+                ref[t][h] = kNoRef;
                 sum[t][h] = 0.0f;
             }
 
@@ -569,18 +587,20 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         int key0 = (it.rq.first_unit + it.unit) * kUnit;
         for (; u < item_end; ++u, key0 += kUnit) {
             const uint32_t stage = ring + out_stage * S::kStage;
-            if (dead) continue;
-            dead = __any_sync(kFull, !mbar_wait(bars + 8 * out_stage, out_phase, a.wait_limit));
-            if (dead) {
-                // Gave up: no more copies; the ones in flight land (bounded again) before the
-                // ring is reused or the CTA ends.  The rest of the part is passed over.
-                if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
-                for (; consumed < issued; ++consumed) {
-                    mbar_wait(bars + 8 * out_stage, out_phase, a.drain_limit);
-                    out_stage = out_stage + 1 == a.depth ? 0 : out_stage + 1;
-                    if (out_stage == 0) out_phase ^= 1;
+            if (!__all_sync(kFull, mbar_try_wait(bars + 8 * out_stage, out_phase))) {
+                if (!dead) dead = __any_sync(kFull, !mbar_wait(bars + 8 * out_stage, out_phase, a.wait_limit));
+                if (dead) {
+                    // Gave up: no more copies; the ones in flight land (bounded again) before the
+                    // ring is reused or the CTA ends.  The rest of the part is passed over.
+                    if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
+                    for (; consumed < issued; ++consumed) {
+                        mbar_wait(bars + 8 * out_stage, out_phase, a.drain_limit);
+                        out_stage = out_stage + 1 == a.depth ? 0 : out_stage + 1;
+                        if (out_stage == 0) out_phase ^= 1;
+                    }
+                    u = u1;
+                    break;
                 }
-                continue;
             }
 
             // ---- scores: keys are the product's rows (16 per record: r8 and r8 + 8), query columns
@@ -614,8 +634,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     uint32_t x[4], y[4];
-                    key_codes(kw[k][0][g], x);
-                    key_codes(kw[k][1][g], y);
+                    key_codes<TERMS == 1>(kw[k][0][g], x);
+                    key_codes<TERMS == 1>(kw[k][1][g], y);
                     const uint4 a0 = make_uint4(x[0], y[0], x[1], y[1]), a1 = make_uint4(x[2], y[2], x[3], y[3]);
                     const float2 d = __half22float2(bits_h2(kd[k][g]));
 #pragma unroll
@@ -640,18 +660,14 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             }
             const bool masked = key0 + kUnit - 1 > full_high || key0 <= full_low;
             uint32_t pb[TILES][2][2];                      // probabilities as operand columns
-            float keep[TILES][H];                          // what the outputs so far count for
             bool grow = false;
-            float top[TILES][H];
+            float top[TILES][H], factor[TILES][H];
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
                 const float2 f = lds_f2(binit + ((t * (NG + 1) + NG) * 8 + 2 * c4) * 4);
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) p[t][k][i][h] *= h ? f.y : f.x;
+                    factor[t][h] = h ? f.y : f.x;
                     if (masked) {
                         const Sight s = sight(t, h);
 #pragma unroll
@@ -664,9 +680,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                     m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-                    top[t][h] = m;
-                    grow |= m > ref[t][h] + kRefSlack;
-                    keep[t][h] = 1.0f;
+                    top[t][h] = m * factor[t][h];
+                    grow |= top[t][h] > ref[t][h] + kRefSlack;
                 }
             }
             // ---- running reference and sum
@@ -675,32 +690,33 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 for (int t = 0; t < TILES; ++t)
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
-                        const float to = fmaxf(ref[t][h], top[t][h]);
-                        if (to != -INFINITY) keep[t][h] = exp2_fast(ref[t][h] - to);
+                        const float to = fmaxf(ref[t][h], top[t][h]), keep = exp2_fast(ref[t][h] - to);
                         ref[t][h] = to;
-                        sum[t][h] *= keep[t][h];
+                        sum[t][h] *= keep;
+#pragma unroll
+                        for (int n = 0; n < 4 * NG; ++n) o[t][n][h] *= keep;
                     }
             }
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    const float base = (ref[t][h] == -INFINITY ? 0.0f : ref[t][h]) - kProbShift;
+                    const float base = kProbShift - ref[t][h];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) p[t][k][i][h] = exp2_fast(p[t][k][i][h] - base);
+                        for (int i = 0; i < 2; ++i) p[t][k][i][h] = exp2_fast(fmaf(p[t][k][i][h], factor[t][h], base));
                     sum[t][h] += (p[t][0][0][h] + p[t][0][1][h]) + (p[t][1][0][h] + p[t][1][1][h]);
                 }
-                // A key's row of operand columns is the transpose of what the product takes.
+                // A key's row of operand columns is the transpose of what the product takes.  The
+                // first term is cut off at 11 bits (exact in fp16), the second is the rest rounded.
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float x = p[t][k][i][0];
-                        const __half2 both = TERMS == 2 ? __floats2half2_rn(x, x - __half2float(__float2half_rn(x)))
-                                                        : __floats2half2_rn(x, p[t][k][i][H - 1]);
-                        pb[t][k][i] = transpose8(h2_bits(both));
+                        const float x = p[t][k][i][0], hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
+                        pb[t][k][i] = transpose8(h2_bits(TERMS == 2 ? __floats2half2_rn(hi, x - hi)
+                                                                    : __floats2half2_rn(x, p[t][k][i][H - 1])));
                     }
             }
 
@@ -776,14 +792,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                             float(&x)[H] = o[t][4 * (q * GI + i) + n];
                             float(&y)[H] = o[t][4 * (q * GI + i) + n + 1];
                             if (TERMS == 2) {
-                                x[0] = fmaf(x[0], keep[t][0], acc[0] + acc[1]);
-                                y[0] = fmaf(y[0], keep[t][0], acc[2] + acc[3]);
+                                x[0] += acc[0] + acc[1];
+                                y[0] += acc[2] + acc[3];
                             } else {
 #pragma unroll
-                                for (int h = 0; h < H; ++h) {
-                                    x[h] = fmaf(x[h], keep[t][h], acc[h]);
-                                    y[h] = fmaf(y[h], keep[t][h], acc[2 + h]);
-                                }
+                                for (int h = 0; h < H; ++h) { x[h] += acc[h]; y[h] += acc[2 + h]; }
                             }
                         }
                     }
@@ -832,7 +845,15 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                     a.lse[tok * a.n_heads + head] = (ref[t][h] + log2f(l) - kProbShift) * 0.693147180559945309f;
                 }
             }
-        if (!whole && lane == 0) meta[2 * warp + (last ? 1 : 0)] = it.start;
+        if (!whole && lane == 0) {
+            uint32_t* const m = meta + (2 * warp + (last ? 1 : 0)) * kMetaInts;
+            m[0] = it.start;
+            m[1] = it.end;
+            m[2] = uint32_t(it.rq.first_tok);
+            m[3] = uint32_t(it.rq.fresh);
+            m[4] = uint32_t(it.head);
+            m[5] = uint32_t(it.tile);
+        }
     }
     __syncthreads();
 
@@ -851,61 +872,84 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         store2(static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D + col, v.x * inv, v.y * inv);
         if (a.lse && col == 0) a.lse[tok * a.n_heads + head] = (m + log2f(l) - kProbShift) * 0.693147180559945309f;
     };
+    auto unfinished = [&](int i) {
+        const uint32_t* const m = meta + i * kMetaInts;
+        Item it;
+        it.start = m[0];
+        it.end = m[1];
+        it.rq.first_tok = int(m[2]);
+        it.rq.fresh = int(m[3]);
+        it.head = int(m[4]);
+        it.tile = int(m[5]);
+        return it;
+    };
+    // Per row: the parts' weights, then by an item's first part its maximum and its sum; where
+    // the queries were.
+    auto weights = [&](int row) {
+        return reinterpret_cast<float*>(smem + lay.warp_off + (row % W) * lay.warp_bytes + lay.q_off) + row / W * 96;
+    };
     static_assert(2 * W <= 32, "a lane per part");
-    const uint32_t my_start = lane < 2 * W ? meta[lane] : kNoItem;
-    uint32_t left = __ballot_sync(kFull, my_start != kNoItem);
-    uint32_t shared_item[2];
-    int n_shared = 0;
-    while (left != 0) {
-        const uint32_t start = __shfl_sync(kFull, my_start, __ffs(int(left)) - 1);
-        const uint32_t parts = __ballot_sync(kFull, my_start == start);
-        left &= ~parts;
-        const Item it = item_at<ROWS>(a, batch, 0, start);
-        const bool all = start >= c0 && it.end <= c1;
-        float* const dst = a.partial + (2ll * blockIdx.x + (start >= c0 ? 1 : 0)) * S::kPartial;
-        for (int row = warp; row < ROWS; row += W) {
-            // A warp per row: the parts' weights by lane, then the row's values.
-            const bool has = (parts >> lane) & 1u;
-            const float* const p = part(has ? lane : 1);
-            const float mi = has ? p[ROWS * D + row] : -INFINITY, li = has ? p[ROWS * D + ROWS + row] : 0.0f;
-            float m = mi;
+    static_assert((ROWS + W - 1) / W * 384 <= S::kQBytes, "the weights fit where the queries were");
+    const uint32_t my_start = lane < 2 * W ? meta[lane * kMetaInts] : kNoItem;
+    const uint32_t listed = __ballot_sync(kFull, my_start != kNoItem);
+    for (int row = warp; row < ROWS; row += W) {
+        const bool has = (listed >> lane) & 1u;
+        const float* const p = part(has ? lane : 1);
+        const float mi = has ? p[ROWS * D + row] : kNoRef, li = has ? p[ROWS * D + ROWS + row] : 0.0f;
+        for (uint32_t left = listed; left != 0;) {
+            const int head = __ffs(int(left)) - 1;
+            const uint32_t start = __shfl_sync(kFull, my_start, head);
+            const bool in = my_start == start;
+            left &= ~__ballot_sync(kFull, in);
+            float m = in ? mi : kNoRef;
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-            const float f = m == -INFINITY ? 1.0f : exp2_fast(mi - m);
-            float l = has ? li * f : 0.0f;
+            const float f = exp2_fast(mi - m);
+            float l = in ? li * f : 0.0f;
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(kFull, l, d);
-            float2 v[D / 64];
-#pragma unroll
-            for (int k = 0; k < D / 64; ++k) v[k] = make_float2(0.0f, 0.0f);
+            float* const w = weights(row);
+            if (in) w[lane] = f;
+            if (lane == head) { w[32 + head] = m; w[64 + head] = l; }
+        }
+    }
+    __syncthreads();
+    int shared_item[2];
+    int n_shared = 0;
+    for (uint32_t left = listed; left != 0;) {
+        const int head = __ffs(int(left)) - 1;
+        const uint32_t parts = __ballot_sync(kFull, my_start == __shfl_sync(kFull, my_start, head));
+        left &= ~parts;
+        const Item it = unfinished(head);
+        const bool all = it.start >= c0 && it.end <= c1;
+        float* const dst = a.partial + (2ll * blockIdx.x + (it.start >= c0 ? 1 : 0)) * S::kPartial;
+        for (int e = tid; e < ROWS * D / 2; e += 32 * W) {
+            const int row = e / (D / 2), col = (e - row * (D / 2)) * 2;
+            const float* const w = weights(row);
+            float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll 4
             for (uint32_t rest = parts; rest != 0; rest &= rest - 1) {
                 const int i = __ffs(int(rest)) - 1;
-                const float fi = __shfl_sync(kFull, f, i);
-                const float2* const x = reinterpret_cast<const float2*>(part(i) + row * D) + lane;
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k) {
-                    const float2 y = x[32 * k];
-                    v[k].x = fmaf(y.x, fi, v[k].x);
-                    v[k].y = fmaf(y.y, fi, v[k].y);
-                }
+                const float2 x = *reinterpret_cast<const float2*>(part(i) + row * D + col);
+                v.x = fmaf(x.x, w[i], v.x);
+                v.y = fmaf(x.y, w[i], v.y);
             }
-#pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-                if (all) put(it, row, 64 * k + 2 * lane, v[k], m, l);
-                else *(reinterpret_cast<float2*>(dst + row * D) + 32 * k + lane) = v[k];
+            const float m = w[32 + head], l = w[64 + head];
+            if (all) {
+                put(it, row, col, v, m, l);
+            } else {
+                *reinterpret_cast<float2*>(dst + row * D + col) = v;
+                if (col == 0) { dst[ROWS * D + row] = m; dst[ROWS * D + ROWS + row] = l; }
             }
-            if (!all && lane == 0) { dst[ROWS * D + row] = m; dst[ROWS * D + ROWS + row] = l; }
         }
-        if (!all && n_shared < 2) shared_item[n_shared++] = start;
+        if (!all && n_shared < 2) shared_item[n_shared++] = head;
     }
 
     // ---- the last CTA of a shared item joins the CTAs' partials, in order
-    uint32_t* const flag = meta + 2 * W;
+    uint32_t* const flag = meta + 2 * W * kMetaInts;
     for (int k = 0; k < n_shared; ++k) {
-        const uint32_t start = shared_item[k];
-        const Item it = item_at<ROWS>(a, batch, 0, start);
-        const uint32_t first = start / share, last = (it.end - 1) / share;
+        const Item it = unfinished(shared_item[k]);
+        const uint32_t first = it.start / share, last = (it.end - 1) / share;
         const int n = int(last - first) + 1;
         __syncthreads();
         if (tid == 0) {
@@ -919,7 +963,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         const float* const p1 = a.partial + 2ll * (first + 1) * S::kPartial;     // the others' their first
         for (int e = tid; e < ROWS * D / 2; e += 32 * W) {
             const int row = e / (D / 2), col = (e - row * (D / 2)) * 2;
-            float m = -INFINITY, l = 0.0f;
+            float m = kNoRef, l = 0.0f;
             float2 v = make_float2(0.0f, 0.0f);
             // Eight partials' loads at a time (one round trip to L2), then their sums in order.
             for (int i0 = 0; i0 < n; i0 += 8) {
@@ -929,21 +973,21 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 for (int i = 0; i < 8; ++i) {
                     const float* const p = i0 + i == 0 ? p0 : p1 + 2ll * (i0 + i - 1) * S::kPartial;
                     const bool in = i0 + i < n;
-                    mi[i] = in ? __ldcg(p + ROWS * D + row) : -INFINITY;
+                    mi[i] = in ? __ldcg(p + ROWS * D + row) : kNoRef;
                     li[i] = in ? __ldcg(p + ROWS * D + ROWS + row) : 0.0f;
                     x[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + row * D + col)) : make_float2(0.0f, 0.0f);
                 }
                 float to = m;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) to = fmaxf(to, mi[i]);
-                const float f = to == -INFINITY ? 1.0f : exp2_fast(m - to);
+                const float f = exp2_fast(m - to);
                 m = to;
                 l *= f;
                 v.x *= f;
                 v.y *= f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float w = m == -INFINITY ? 1.0f : exp2_fast(mi[i] - m);
+                    const float w = exp2_fast(mi[i] - m);
                     l = fmaf(li[i], w, l);
                     v.x = fmaf(x[i].x, w, v.x);
                     v.y = fmaf(x[i].y, w, v.y);
