@@ -59,12 +59,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     if not os.path.exists(p):
         raise RuntimeError(f"CUDA library not built: {p} is missing (run __graft_entry__.build())")
     try:
-        import torch  # noqa: F401  (load torch's CUDA runtime first so one copy is shared)
+        import torch  # (loads torch's CUDA runtime first so one copy is shared)
+        _ACT.update({torch.float32: QG_ACT_F32, torch.bfloat16: QG_ACT_BF16})
+        _DTYPE.update(i32=torch.int32, i64=torch.int64, f32=torch.float32)
     except ImportError:
         pass
     lib = ctypes.CDLL(p)
     i64, vp, sz, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-    u32, f32, cache = ctypes.c_uint, ctypes.c_float, ctypes.POINTER(qg_cache)
+    u32, f32 = ctypes.c_uint, ctypes.c_float
     sig = {
         "qg_strerror": (ctypes.c_char_p, [i32]),
         "qg_abi_version": (i32, []),
@@ -95,10 +97,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "qg_cache_pages": (i32, [vp, vp, i32, i32, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, i64, vp]),
         "qg_qk_norm_rope": (i32, [i32, vp, i64, vp, i64, i64, i32, i32, i32, vp, vp, f32, u32, vp, i64, i32, vp, vp, i64,
                                   vp, i64, vp]),
-        "qg_cache_append": (i32, [cache, i32, vp, i64, vp, i64, vp, i64, i64, i32, vp, vp, f32, u32, vp, i64, i32, vp, vp,
+        "qg_cache_append": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, i64, i32, vp, vp, f32, u32, vp, i64, i32, vp, vp,
                                   vp, i64, vp, vp, vp]),
         "qg_attention_workspace_bytes": (sz, [i32, i32, i32]),
-        "qg_attention": (i32, [cache, i32, vp, i64, i64, i32, vp, i64, vp, vp, i32, i32, i32, vp, f32, vp, i64, vp, vp, sz,
+        "qg_attention": (i32, [vp, i32, vp, i64, i64, i32, vp, i64, vp, vp, i32, i32, i32, vp, f32, vp, i64, vp, vp, sz,
                                vp]),
         "qgemv_expert_layer": (i32, [i32, vp, vp, i64, i64, i64, vp, i32, vp, i32, vp, vp, vp, vp, sz, vp]),
     }
@@ -119,10 +121,12 @@ class qg_cache(ctypes.Structure):
     def __init__(self, data, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int):
         super().__init__(_ptr(data), int(n_pages), int(page_tokens), int(n_kv_heads), int(head_dim))
         if hasattr(data, "numel"):
+            if not data.is_cuda:
+                raise ValueError("qg_cache: data must be a CUDA tensor")
             need = qg_cache_bytes(n_pages, page_tokens, n_kv_heads, head_dim)
             if need == 0 or data.numel() * data.element_size() < need or not data.is_contiguous():
                 raise ValueError("qg_cache: data must be a contiguous tensor of at least qg_cache_bytes() bytes")
-        self.tensor = data
+        self.tensor, self.address = data, ctypes.addressof(self)
 
 
 def _ptr(t) -> int | None:
@@ -138,17 +142,25 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        return _current_stream() or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
 
 
+def _current_stream() -> int:
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    handle = torch.cuda.current_stream().cuda_stream        # (initializes CUDA)
+    if raw is not None and device is not None:              # the same lookup without a Stream object
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return handle
+
+
 def current_stream_handle() -> int:
     """torch's current CUDA stream as a raw ``cudaStream_t`` (0 = the legacy default stream)."""
-    import torch
-    return int(torch.cuda.current_stream().cuda_stream)
+    return int(_current_stream())
 
 
 def _check(status: int, what: str) -> None:
@@ -368,39 +380,44 @@ QG_ATTENTION_ZERO_BYTES = 4096
 QG_DEVICE_BAD_PAGE = 8
 QG_DEVICE_BAD_LENGTH = 16
 QG_DEVICE_NO_PAGES = 32
-_ACT = {"torch.float32": QG_ACT_F32, "torch.bfloat16": QG_ACT_BF16}
+
+
+# The calls below run once per layer and step, where a few microseconds of Python count:
+# their checks look at each tensor once.
+_ACT: dict = {}      # torch dtype -> qg_act, and the dtypes by name; filled when the library loads
+_DTYPE: dict = {}
+
+
+def _heads(t, dtype, name: str):
+    """(address, token stride, tokens, heads, head_dim) of ``[n_tok, heads, head_dim]``
+    activations whose heads are contiguous (a slice of a projection's row is)."""
+    n, h, d = t.shape
+    s, sh, sd = t.stride()
+    if (sh != d and h > 1) or sd != 1 or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA [n_tok, heads, head_dim] tensor of one type, heads contiguous, is needed")
+    return t.data_ptr(), s if n > 1 else max(s, h * d), n, h, d
+
+
+def _typed(t, kind: str, name: str, numel: int = 0):
+    """Address of a contiguous CUDA tensor of type ``kind`` with at least ``numel`` entries."""
+    if t is None:
+        return None
+    if t.dtype is not _DTYPE[kind] or not t.is_contiguous() or t.numel() < numel or not t.is_cuda:
+        raise ValueError(f"{name}: a contiguous CUDA {kind} tensor of at least {numel} entries is needed")
+    return t.data_ptr()
 
 
 def _act(t) -> int:
-    a = _ACT.get(str(t.dtype))
+    a = _ACT.get(t.dtype)
     if a is None:
         raise TypeError(f"activations are float32 or bfloat16 tensors, not {t.dtype}")
     return a
 
 
-def _heads(t, act: int, name: str):
-    """(address, token stride, tokens, heads, head_dim) of ``[n_tok, heads, head_dim]``
-    activations whose heads are contiguous (a slice of a projection's row is)."""
-    n, h, d = t.shape
-    st = t.stride()
-    if (h > 1 and st[1] != d) or st[2] != 1 or _act(t) != act:
-        raise ValueError(f"{name}: [n_tok, heads, head_dim] of one type, heads contiguous, is needed")
-    return t.data_ptr(), (st[0] if n > 1 else max(st[0], h * d)), n, h, d
-
-
-def _typed(t, dtype: str, name: str, numel: int | None = None):
-    """Address of a contiguous tensor of ``dtype`` with at least ``numel`` entries."""
-    if t is None or isinstance(t, int):
-        return t
-    if str(t.dtype) not in ("torch." + dtype,) or not t.is_contiguous() or (numel is not None and t.numel() < numel):
-        raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if numel is None else f' of {numel} entries'} is needed")
-    return t.data_ptr()
-
-
 def _table(table, n_req: int):
-    if table.dim() != 2 or str(table.dtype) != "torch.int32" or table.shape[0] < n_req or not table.is_contiguous():
+    if table.dim() != 2 or table.shape[0] < n_req:
         raise ValueError("table: a contiguous int32 [n_req, width] tensor is needed")
-    return table.data_ptr(), int(table.shape[1])
+    return _typed(table, "i32", "table"), table.shape[1]
 
 
 def qg_cache_bytes(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
@@ -414,24 +431,25 @@ def qg_cache_pages(held, fresh, free_pages, table, seq_len, cu_new, slots, posit
     ``free_begin[0]``.  Writes the new entries of ``table`` (int32 ``[n_req, width]``),
     ``seq_len``, ``cu_new`` (int32 ``[n_req + 1]``), ``slots`` (int64) and ``positions`` (int32)
     of all new tokens, and ``free_end[0]`` (``free_begin`` itself may be passed)."""
-    n = int(held.shape[0])
+    lib = _lib or load_library()
+    n, n_tok = held.shape[0], slots.numel()
     tp, width = _table(table, n)
-    n_tok = int(slots.numel())
-    st = load_library().qg_cache_pages(
-        _typed(held, "int32", "held"), _typed(fresh, "int32", "fresh", n), n, int(page_tokens),
-        _typed(free_pages, "int32", "free_pages"), int(free_pages.numel()), _typed(free_begin, "int32", "free_begin", 1),
-        _typed(free_end, "int32", "free_end", 1), tp, width, _typed(seq_len, "int32", "seq_len", n), _typed(cu_new, "int32", "cu_new", n + 1), _typed(slots, "int64", "slots"),
-        _typed(positions, "int32", "positions", n_tok), n_tok, _stream(stream))
-    _check(st, "qg_cache_pages")
+    st = lib.qg_cache_pages(
+        _typed(held, "i32", "held"), _typed(fresh, "i32", "fresh", n), n, page_tokens,
+        _typed(free_pages, "i32", "free_pages"), free_pages.numel(), _typed(free_begin, "i32", "free_begin", 1),
+        _typed(free_end, "i32", "free_end", 1), tp, width, _typed(seq_len, "i32", "seq_len", n),
+        _typed(cu_new, "i32", "cu_new", n + 1), _typed(slots, "i64", "slots"),
+        _typed(positions, "i32", "positions", n_tok), n_tok, _stream(stream))
+    if st != 0:
+        raise QGError(st, "qg_cache_pages")
 
 
 def _rotation(cos_sin, positions, n_tok: int):
+    pos = _typed(positions, "i32", "positions", n_tok)
     if cos_sin is None:
-        return None, 0, 0, _typed(positions, "int32", "positions", n_tok)
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin: float32 [n_pos, rot_dim] is needed")
-    return (_typed(cos_sin, "float32", "cos_sin"), int(cos_sin.shape[0]), int(cos_sin.shape[1]),
-            _typed(positions, "int32", "positions", n_tok))
+        return None, 0, 0, pos
+    n_pos, rot = cos_sin.shape
+    return _typed(cos_sin, "f32", "cos_sin"), n_pos, rot, pos
 
 
 def _head_flags(norm: bool, unit_offset: bool, interleaved: bool) -> int:
@@ -444,19 +462,20 @@ def qg_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=N
     """Enqueue the RMS norm of every query and key head (``[n_tok, heads, head_dim]``, float32 or
     bfloat16; slices of one projection's rows are taken as they are) and the rotation by
     ``cos_sin[positions]`` (``[n_pos, rot_dim]``: cosines, then sines) in one pass."""
-    act = _act(q)
-    qp, qs, n, hq, d = _heads(q, act, "q")
-    kp, ks, nk, hk, dk = _heads(k, act, "k")
-    qo, qos, nqo, hqo, dqo = _heads(q_out, act, "q_out")
-    ko, kos, nko, hko, dko = _heads(k_out, act, "k_out")
+    lib = _lib or load_library()
+    act, dtype = _act(q), q.dtype
+    qp, qs, n, hq, d = _heads(q, dtype, "q")
+    kp, ks, nk, hk, dk = _heads(k, dtype, "k")
+    qo, qos, nqo, hqo, dqo = _heads(q_out, dtype, "q_out")
+    ko, kos, nko, hko, dko = _heads(k_out, dtype, "k_out")
     if not (n == nk == nqo == nko and d == dk == dqo == dko and hq == hqo and hk == hko):
         raise ValueError("qg_qk_norm_rope: q, k and their outputs differ in tokens, heads or head_dim")
     cs, n_pos, rot, pos = _rotation(cos_sin, positions, n)
-    st = load_library().qg_qk_norm_rope(act, qp, qs, kp, ks, n, hq, hk, d, _typed(q_weight, "float32", "q_weight", d),
-                                        _typed(k_weight, "float32", "k_weight", d), eps,
-                                        _head_flags(norm, unit_offset, interleaved), cs, n_pos, rot, pos, qo, qos, ko, kos,
-                                        _stream(stream))
-    _check(st, "qg_qk_norm_rope")
+    st = lib.qg_qk_norm_rope(act, qp, qs, kp, ks, n, hq, hk, d, _typed(q_weight, "f32", "q_weight", d),
+                             _typed(k_weight, "f32", "k_weight", d), eps, _head_flags(norm, unit_offset, interleaved),
+                             cs, n_pos, rot, pos, qo, qos, ko, kos, _stream(stream))
+    if st != 0:
+        raise QGError(st, "qg_qk_norm_rope")
 
 
 def qg_cache_append(cache: qg_cache, k, v, slots, q=None, q_out=None, positions=None, cos_sin=None, q_weight=None,
@@ -465,28 +484,29 @@ def qg_cache_append(cache: qg_cache, k, v, slots, q=None, q_out=None, positions=
     """Enqueue qg_qk_norm_rope's norm and rotation with the keys and the values (``v``: as they
     are) quantized into ``cache`` at ``slots`` (int64 ``[n_tok]``, -1 = none); queries go to
     ``q_out``.  ``k_back`` / ``v_back`` receive the values the cache now stands for."""
-    act = _act(k)
-    kp, ks, n, hk, d = _heads(k, act, "k")
-    vp, vs, nv, hv, dv = _heads(v, act, "v")
+    lib = _lib or load_library()
+    act, dtype = _act(k), k.dtype
+    kp, ks, n, hk, d = _heads(k, dtype, "k")
+    vp, vs, nv, hv, dv = _heads(v, dtype, "v")
     qp = qs = qo = qos = hq = 0
     if q is not None:
-        qp, qs, nq, hq, dq = _heads(q, act, "q")
-        qo, qos, nqo, hqo, dqo = _heads(q_out, act, "q_out")
+        qp, qs, nq, hq, dq = _heads(q, dtype, "q")
+        qo, qos, nqo, hqo, dqo = _heads(q_out, dtype, "q_out")
         if not (nq == nqo == n and dq == dqo == d and hq == hqo):
             raise ValueError("qg_cache_append: q and q_out differ from k in tokens or head_dim")
     if not (nv == n and hk == hv == cache.n_kv_heads and d == dv == cache.head_dim):
         raise ValueError("qg_cache_append: k and v do not fit the cache's heads")
     for t, name in ((k_back, "k_back"), (v_back, "v_back")):
-        if t is not None and (_act(t) != act or not t.is_contiguous() or t.numel() < n * hk * d):
-            raise ValueError(f"{name}: a contiguous [n_tok, n_kv_heads, head_dim] tensor of k's type is needed")
+        if t is not None and (t.dtype is not dtype or not t.is_contiguous() or t.numel() < n * hk * d or not t.is_cuda):
+            raise ValueError(f"{name}: a contiguous CUDA [n_tok, n_kv_heads, head_dim] tensor of k's type is needed")
     cs, n_pos, rot, pos = _rotation(cos_sin, positions, n)
-    st = load_library().qg_cache_append(cache, act, qp or None, qs, kp, ks, vp, vs, n, hq,
-                                        _typed(q_weight, "float32", "q_weight", d),
-                                        _typed(k_weight, "float32", "k_weight", d), eps,
-                                        _head_flags(norm, unit_offset, interleaved), cs, n_pos, rot, pos,
-                                        _typed(slots, "int64", "slots", n), qo or None, qos, _ptr(k_back), _ptr(v_back),
-                                        _stream(stream))
-    _check(st, "qg_cache_append")
+    st = lib.qg_cache_append(cache.address, act, qp or None, qs, kp, ks, vp, vs, n, hq,
+                             _typed(q_weight, "f32", "q_weight", d), _typed(k_weight, "f32", "k_weight", d), eps,
+                             _head_flags(norm, unit_offset, interleaved), cs, n_pos, rot, pos,
+                             _typed(slots, "i64", "slots", n), qo or None, qos, None if k_back is None else k_back.data_ptr(),
+                             None if v_back is None else v_back.data_ptr(), _stream(stream))
+    if st != 0:
+        raise QGError(st, "qg_cache_append")
 
 
 def qg_attention_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -500,18 +520,22 @@ def qg_attention(cache: qg_cache, q, table, seq_len, cu_new, out, workspace, sca
     (``table``, ``seq_len``) into ``out``.  ``window`` > 0: a sliding window; ``span_mask`` (int32
     bits per new token): a draft tree's visibility among the request's new tokens.
     ``workspace``: uint8, ``qg_attention_workspace_bytes``, zeroed once."""
-    act = _act(q)
-    qp, qs, n, hq, d = _heads(q, act, "q")
-    op, os_, no, ho, do = _heads(out, act, "out")
+    lib = _lib or load_library()
+    act, dtype = _act(q), q.dtype
+    qp, qs, n, hq, d = _heads(q, dtype, "q")
+    op, os_, no, ho, do = _heads(out, dtype, "out")
     if not (n == no and hq == ho and d == do == cache.head_dim):
         raise ValueError("qg_attention: q, out and the cache differ in tokens, heads or head_dim")
-    n_req = int(seq_len.shape[0])
+    n_req = seq_len.shape[0]
     tp, width = _table(table, n_req)
-    st = load_library().qg_attention(
-        cache, act, qp, qs, n, hq, tp, width, _typed(seq_len, "int32", "seq_len"), _typed(cu_new, "int32", "cu_new", n_req + 1), n_req, int(max_new),
-        int(window), _typed(span_mask, "int32", "span_mask", n), scale, op, os_, _typed(lse, "float32", "lse", n * hq),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "qg_attention")
+    if not workspace.is_cuda:
+        raise ValueError("workspace: a CUDA tensor is needed")
+    st = lib.qg_attention(cache.address, act, qp, qs, n, hq, tp, width, _typed(seq_len, "i32", "seq_len"),
+                          _typed(cu_new, "i32", "cu_new", n_req + 1), n_req, max_new, window,
+                          _typed(span_mask, "i32", "span_mask", n), scale, op, os_, _typed(lse, "f32", "lse", n * hq),
+                          workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st != 0:
+        raise QGError(st, "qg_attention")
 
 
 QG_DEVICE_WAIT_TIMEOUT = 1
