@@ -177,19 +177,47 @@ template <typename T, int N> __device__ __forceinline__ void store(void* at, con
     *static_cast<Raw<T, N>*>(at) = raw;
 }
 
-// Adjacent-pair tree over a warp's D squares: pairs within the lane, then lanes 2i, 2i + 1 and
-// so on.  The order is part of the operator's definition (the sum then does not depend on the
-// kernel), and it is the order a butterfly takes anyway.
-template <int N> __device__ __forceinline__ float square_sum(const float (&x)[N]) {
-    float s[N];
+// Sums of squares of G rows of a warp (G a power of two, N values of each per lane), as a tree
+// of adjacent pairs: pairs within the lane, then lanes 2i and 2i + 1, and so on.  The order is
+// part of the operator's definition (the sum then does not depend on the kernel); the first
+// steps halve the rows a lane still carries, so G rows cost G - 1 + 5 - log2(G) shuffles
+// instead of 5 G.  Returns the sum of row `sum_row<G>(lane)`.
+template <int G> __device__ __forceinline__ int sum_row(int lane) {
+    int r = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = __fmul_rn(x[i], x[i]);
+    for (int m = G / 2, bit = 0; m >= 1; m /= 2, ++bit) r += ((lane >> bit) & 1) * m;
+    return r;
+}
+template <int G> __host__ __device__ constexpr int sum_lane(int row) {       // a lane that holds row's sum
+    int l = 0;
+    for (int m = G / 2, bit = 0; m >= 1; m /= 2, ++bit) l |= ((row / m) & 1) << bit;
+    return l;
+}
+template <int N, int G> __device__ __forceinline__ float square_sums(const float (&x)[G][N], int lane) {
+    float s[G];
 #pragma unroll
-    for (int n = N; n > 1; n /= 2)
+    for (int j = 0; j < G; ++j) {
+        float t[N];
 #pragma unroll
-        for (int i = 0; i < n / 2; ++i) s[i] = __fadd_rn(s[2 * i], s[2 * i + 1]);
+        for (int i = 0; i < N; ++i) t[i] = __fmul_rn(x[j][i], x[j][i]);
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], d));
+        for (int n = N; n > 1; n /= 2)
+#pragma unroll
+            for (int i = 0; i < n / 2; ++i) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
+        s[j] = t[0];
+    }
+    int d = 1;
+#pragma unroll
+    for (int m = G / 2; m >= 1; m /= 2, d *= 2) {
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+            const bool up = (lane & d) != 0;
+            const float send = up ? s[i] : s[i + m], mine = up ? s[i + m] : s[i];
+            s[i] = __fadd_rn(mine, __shfl_xor_sync(kAll, send, d));
+        }
+    }
+#pragma unroll
+    for (; d < 32; d *= 2) s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], d));
     return s[0];
 }
 
@@ -211,55 +239,67 @@ __device__ __forceinline__ void quantize_block(const float (&x)[N], int lane, ui
     const uint32_t who = __ballot_sync(kAll, top == all) & group;
     m = __shfl_sync(kAll, m, __ffs(int(who)) - 1);
     const float d = __fmul_rn(m, -0.125f);
-    const bool bad = !(all <= __float_as_uint(QG_CACHE_MAX));
+    const bool bad = !(all <= __float_as_uint(QG_CACHE_MAX)) || d == 0.0f;
+    // x / d through the reciprocal where that cannot change the code (the quotient, within 2^-20
+    // of the true one, is not that near to a half), by the division itself elsewhere.
+    float t[N];
+    const float inv = __frcp_rn(d);
+    bool close = !(fabsf(inv) < 1e30f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int q = int(roundf(__fdiv_rn(x[i], d))) + 8;
-        code[i] = bad || d == 0.0f ? 8u : uint32_t(min(max(q, 0), 15));
+        t[i] = x[i] * inv;
+        const float a = fabsf(t[i]);
+        close |= !(fabsf(a - floorf(a) - 0.5f) > 1e-5f);
     }
-    scale = bad ? __ushort_as_half(0x7FFFu) : __float2half_rn(float(__float2bfloat16_rn(d)));
+    if (close) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) t[i] = __fdiv_rn(x[i], d);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) code[i] = bad ? 8u : uint32_t(min(max(int(roundf(t[i])) + 8, 0), 15));
+    scale = !bad || d == 0.0f ? __float2half_rn(float(__float2bfloat16_rn(d))) : __ushort_as_half(0x7FFFu);
 }
 
-// One warp takes ROWS consecutive heads of a token (queries, then keys, then values), a lane
+// One warp takes ROWS consecutive heads of one kind (queries, keys or values) of a token, a lane
 // D / 32 neighbouring values of each: every load and store is one contiguous row of a warp, the
-// rows' loads are all issued before the first is used, and the token's cosines and sines are
-// read once for the ROWS heads.  Bound by memory (each element read once and written once) at
-// prompt sizes, by the launch and one load's latency at decode sizes, where ROWS = 1 spreads
-// the heads over more warps.
+// rows' loads are all issued before the first is used, and the token's cosines and sines and
+// the weights are read once for the ROWS heads.  Rows are normed G at a time, so that their
+// sums share shuffles and one lane of each computes the root.  Bound by memory (each element
+// read once and written once) at prompt sizes, by the launch and one load's latency at decode
+// sizes, where ROWS = 1 spreads the heads over more warps.
 template <int D, typename T, int ROWS>
 __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
-    constexpr int N = D / 32;
+    constexpr int N = D / 32, G = ROWS < 4 ? ROWS : 4;
     const int lane = int(threadIdx.x) & 31;
-    const int heads = a.n_q + a.n_k + a.n_v;
-    const int per_tok = (heads + ROWS - 1) / ROWS;
+    const int g_q = (a.n_q + ROWS - 1) / ROWS, g_k = (a.n_k + ROWS - 1) / ROWS, g_v = (a.n_v + ROWS - 1) / ROWS;
+    const int per_tok = g_q + g_k + g_v;
     const long long id = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
     grid_dependency();
     if (id >= a.n_tok * per_tok) return;
     const long long tok = id / per_tok;
-    const int h0 = int(id - tok * per_tok) * ROWS;
+    const int group = int(id - tok * per_tok);
+    const bool is_q = group < g_q, is_v = group >= g_q + g_k;
+    const int h0 = (is_q ? group : is_v ? group - g_q - g_k : group - g_q) * ROWS;
+    const int heads = min(ROWS, (is_q ? a.n_q : is_v ? a.n_v : a.n_k) - h0);
 
+    const T* const src = (is_q ? static_cast<const T*>(a.q) + tok * a.q_stride : is_v ? static_cast<const T*>(a.v) + tok * a.v_stride
+                                                                               : static_cast<const T*>(a.k) + tok * a.k_stride) +
+                         (long long)h0 * D + lane * N;
     Raw<T, N> raw[ROWS];
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-        const int h = h0 + j;
-        if (h >= heads) break;
-        const T* src = h < a.n_q ? static_cast<const T*>(a.q) + tok * a.q_stride + (long long)h * D
-                     : h < a.n_q + a.n_k ? static_cast<const T*>(a.k) + tok * a.k_stride + (long long)(h - a.n_q) * D
-                     : static_cast<const T*>(a.v) + tok * a.v_stride + (long long)(h - a.n_q - a.n_k) * D;
-        raw[j] = *reinterpret_cast<const Raw<T, N>*>(src + lane * N);
-    }
+    for (int j = 0; j < ROWS; ++j) raw[j] = *reinterpret_cast<const Raw<T, N>*>(src + (j < heads ? j : 0) * D);
 
     // The token's rotation: of a lane's values the cosines and sines it needs (half-split: one
     // per value; interleaved: one per pair).
     const int half = a.rot / 2, i0 = lane * N;
-    const bool inter = (a.flags & QG_ROPE_INTERLEAVED) != 0;
-    float cs[N], sn[N];
+    const bool inter = (a.flags & QG_ROPE_INTERLEAVED) != 0, norm = !is_v && !(a.flags & QG_NORM_NONE);
+    float cs[N], sn[N], w[N];
     bool dead = false, turn = false;
     if (a.positions) {
         const int pos = a.positions[tok];
         dead = pos < 0 || (a.rot > 0 && pos >= a.n_pos);
         if (pos >= 0 && dead && lane == 0) atomicOr(a.status, kStatusBadLength);
-        if (!dead && a.rot > 0) {
+        if (!dead && a.rot > 0 && !is_v) {
             const float* row = a.cos_sin + (long long)pos * a.rot;
             turn = i0 < a.rot;
             if (turn && inter) {
@@ -275,77 +315,88 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
     const int reach = half / N;                          // lanes from a value to its partner (half-split)
     const bool first = lane < reach;
     const int partner = !turn ? lane : first ? lane + reach : lane - reach;
+    const float* const weight = is_q ? a.q_weight : a.k_weight;
+    const bool weighted = norm && weight;
+    if (weighted) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = a.flags & QG_NORM_UNIT_OFFSET ? __fadd_rn(weight[i0 + i], 1.0f) : weight[i0 + i];
+    }
 
     long long slot = -1;
-    if (a.data) {
+    if (a.data && !is_q) {
         slot = a.slots[tok];
         if (slot >= a.n_slots || slot < -1) {
             if (lane == 0) atomicOr(a.status, kStatusBadPage);
             slot = -1;
         }
     }
+    const long long page = slot >= 0 ? slot / a.page : 0;
+    const int in = slot >= 0 ? int(slot - page * a.page) : 0, t = in % kRecordTokens;
 
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-        const int h = h0 + j;
-        if (h >= heads) break;
-        const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_k;
-        float x[N];
-        widen<T, N>(raw[j], x);
-        if (!is_v) {
-            if (!(a.flags & QG_NORM_NONE)) {
-                const float mean = __fmul_rn(square_sum<N>(x), 1.0f / D);
-                const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, a.eps)));
-                const float* w = is_q ? a.q_weight : a.k_weight;
+    for (int j0 = 0; j0 < ROWS; j0 += G) {
+        if (j0 >= heads) break;
+        float x[G][N];
+#pragma unroll
+        for (int j = 0; j < G; ++j) widen<T, N>(raw[j0 + j], x[j]);
+        if (norm) {
+            const float mean = __fmul_rn(square_sums<N, G>(x, lane), 1.0f / D);
+            const float root = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, a.eps)));
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const float r = G == 1 ? root : __shfl_sync(kAll, root, sum_lane<G>(j));
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    x[i] = __fmul_rn(x[i], r);
-                    if (w) {
-                        const float wi = w[i0 + i];
-                        x[i] = __fmul_rn(x[i], a.flags & QG_NORM_UNIT_OFFSET ? __fadd_rn(wi, 1.0f) : wi);
-                    }
+                    x[j][i] = __fmul_rn(x[j][i], r);
+                    if (weighted) x[j][i] = __fmul_rn(x[j][i], w[i]);
                 }
             }
-            if (a.rot > 0 && !dead) {
+        }
+        if (a.rot > 0 && !dead && !is_v) {
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
                 if (inter) {
                     if (turn) {
 #pragma unroll
                         for (int i = 0; i < N / 2; ++i) {
-                            const float u = x[2 * i], v = x[2 * i + 1];
-                            x[2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
-                            x[2 * i + 1] = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
+                            const float u = x[j][2 * i], v = x[j][2 * i + 1];
+                            x[j][2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
+                            x[j][2 * i + 1] = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
                         }
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const float p = __shfl_sync(kAll, x[i], partner);
+                        const float p = __shfl_sync(kAll, x[j][i], partner);
                         if (turn) {
-                            const float own = __fmul_rn(x[i], cs[i]), other = __fmul_rn(p, sn[i]);
-                            x[i] = first ? __fsub_rn(own, other) : __fadd_rn(own, other);
+                            const float own = __fmul_rn(x[j][i], cs[i]), other = __fmul_rn(p, sn[i]);
+                            x[j][i] = first ? __fsub_rn(own, other) : __fadd_rn(own, other);
                         }
                     }
                 }
             }
         }
-        if (dead) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = 0.0f;
-        }
-        if (is_q) {
-            store<T, N>(static_cast<T*>(a.q_out) + tok * a.q_out_stride + (long long)h * D + i0, x);
-            continue;
-        }
-        const int kv = is_v ? h - a.n_q - a.n_k : h - a.n_q;
-        void* out = is_v ? a.v_back : a.k_out;
-        if (a.data) {
+        for (int j = 0; j < G; ++j) {
+            const int h = h0 + j0 + j;
+            if (j0 + j >= heads) break;
+            if (dead) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) x[j][i] = 0.0f;
+            }
+            if (is_q) {
+                store<T, N>(static_cast<T*>(a.q_out) + tok * a.q_out_stride + (long long)h * D + i0, x[j]);
+                continue;
+            }
+            if (!a.data) {
+                store<T, N>(static_cast<T*>(a.k_out) + tok * a.k_out_stride + (long long)h * D + i0, x[j]);
+                continue;
+            }
             uint32_t code[N];
             __half scale;
-            quantize_block<N>(x, lane, code, scale);
+            quantize_block<N>(x[j], lane, code, scale);
             if (slot >= 0) {
-                const long long page = slot / a.page;
-                const int in = int(slot - page * a.page), t = in % kRecordTokens;
-                uint8_t* rec = a.data + ((page * a.n_k + kv) * (a.page / kRecordTokens) + in / kRecordTokens) * kv_record_bytes(D);
+                uint8_t* rec = a.data + ((page * a.n_k + h) * (a.page / kRecordTokens) + in / kRecordTokens) * kv_record_bytes(D);
                 const int g = i0 / 32, at = i0 % 32;
                 uint32_t bits = 0;                       // the lane's N nibbles, in order
 #pragma unroll
@@ -368,24 +419,32 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
                 if (at == 0)
                     *reinterpret_cast<__half*>(rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + kv_scale(D, t, g)) = scale;
             }
+            void* const out = is_v ? a.v_back : a.k_out;
             if (!out) continue;
             const float d = __half2float(scale);
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = __fmul_rn(float(int(code[i]) - 8), d);
-            store<T, N>(static_cast<T*>(out) + (tok * a.n_k + kv) * D + i0, x);
-        } else {
-            store<T, N>(static_cast<T*>(out) + tok * a.k_out_stride + (long long)kv * D + i0, x);
+            for (int i = 0; i < N; ++i) x[j][i] = __fmul_rn(float(int(code[i]) - 8), d);
+            store<T, N>(static_cast<T*>(out) + (tok * a.n_k + h) * D + i0, x[j]);
         }
     }
 }
 
-// Heads per warp: 4 once that still leaves every SM 32 warps; below, one, so that a few
-// tokens' heads run side by side.
-template <int D, typename T>
-const void* heads_fn(bool wide) { return wide ? (const void*)&heads_kernel<D, T, 4> : (const void*)&heads_kernel<D, T, 1>; }
+// Heads per warp: 2 KB of rows (4 to 8) once that still leaves every SM 32 warps; below, one, so
+// that a few tokens' heads run side by side.
+#ifndef QG_HR
+#define QG_HR (2048 / (D * int(sizeof(T))))
+#endif
+template <typename T, int D> struct HeadShape {
+    static constexpr int kWide = QG_HR < 2 ? 2 : QG_HR > 8 ? 8 : QG_HR;
+};
+template <typename T, int D>
+const void* heads_fn(bool wide, int* rows) {
+    *rows = wide ? HeadShape<T, D>::kWide : 1;
+    return wide ? (const void*)&heads_kernel<D, T, HeadShape<T, D>::kWide> : (const void*)&heads_kernel<D, T, 1>;
+}
 
-template <typename T> const void* heads_fn(int D, bool wide) {
-    return D == 64 ? heads_fn<64, T>(wide) : D == 128 ? heads_fn<128, T>(wide) : heads_fn<256, T>(wide);
+template <typename T> const void* heads_fn(int D, bool wide, int* rows) {
+    return D == 64 ? heads_fn<T, 64>(wide, rows) : D == 128 ? heads_fn<T, 128>(wide, rows) : heads_fn<T, 256>(wide, rows);
 }
 
 qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
@@ -395,14 +454,15 @@ qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
     const long long heads = a.n_q + a.n_k + a.n_v;
     if (heads == 0 || a.n_tok == 0) return QG_OK;
     const bool wide = a.n_tok * heads >= 4ll * 32 * sms;
-    const long long per_tok = wide ? (heads + 3) / 4 : heads;
+    int rows = 1;
+    const void* fn = act == QG_ACT_F32 ? heads_fn<float>(D, wide, &rows) : heads_fn<__nv_bfloat16>(D, wide, &rows);
+    const long long per_tok = (a.n_q + rows - 1) / rows + (a.n_k + rows - 1) / rows + (a.n_v + rows - 1) / rows;
     const long long warps = a.n_tok * per_tok;
     const int in_block = wide ? 8 : 4;
     const long long grid = (warps + in_block - 1) / in_block;
     if (grid > 0x7FFFFFFFll) return QG_EUNSUPPORTED;
     void* params[] = {&a};
-    return launch_early(act == QG_ACT_F32 ? heads_fn<float>(D, wide) : heads_fn<__nv_bfloat16>(D, wide), int(grid),
-                        32 * in_block, 0, 1, params, stream);
+    return launch_early(fn, int(grid), 32 * in_block, 0, 1, params, stream);
 }
 
 constexpr unsigned kHeadFlags = QG_ROPE_INTERLEAVED | QG_NORM_UNIT_OFFSET | QG_NORM_NONE;
