@@ -163,18 +163,33 @@ template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
 template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
 template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
 
-template <typename T, int N> __device__ __forceinline__ void widen(const Raw<T, N>& raw, float (&x)[N]) {
-    const T* e = reinterpret_cast<const T*>(&raw);
+template <int N> __device__ __forceinline__ void widen(const Raw<float, N>& raw, float (&x)[N]) {
+    const float* e = reinterpret_cast<const float*>(&raw);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = float(e[i]);
+    for (int i = 0; i < N; ++i) x[i] = e[i];
+}
+template <int N> __device__ __forceinline__ void widen(const Raw<__nv_bfloat16, N>& raw, float (&x)[N]) {
+    const uint32_t* e = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        x[2 * i] = __uint_as_float(e[i] << 16);
+        x[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
+    }
 }
 
-template <typename T, int N> __device__ __forceinline__ void store(void* at, const float (&x)[N]) {
-    Raw<T, N> raw;
-    T* e = reinterpret_cast<T*>(&raw);
+template <int N> __device__ __forceinline__ void store(float* at, const float (&x)[N]) {
+    Raw<float, N> raw;
+    float* e = reinterpret_cast<float*>(&raw);
 #pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = T(x[i]);          // nearest even for bf16
-    *static_cast<Raw<T, N>*>(at) = raw;
+    for (int i = 0; i < N; ++i) e[i] = x[i];
+    *reinterpret_cast<Raw<float, N>*>(at) = raw;
+}
+template <int N> __device__ __forceinline__ void store(__nv_bfloat16* at, const float (&x)[N]) {
+    Raw<__nv_bfloat16, N> raw;
+    __nv_bfloat162* e = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) e[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);      // nearest even
+    *reinterpret_cast<Raw<__nv_bfloat16, N>*>(at) = raw;
 }
 
 // Sums of squares of G rows of a warp (G a power of two, N values of each per lane), as a tree
@@ -273,11 +288,12 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
     const int lane = int(threadIdx.x) & 31;
     const int g_q = (a.n_q + ROWS - 1) / ROWS, g_k = (a.n_k + ROWS - 1) / ROWS, g_v = (a.n_v + ROWS - 1) / ROWS;
     const int per_tok = g_q + g_k + g_v;
-    const long long id = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    const uint32_t id = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);        // < 2^31 (host)
     grid_dependency();
-    if (id >= a.n_tok * per_tok) return;
-    const long long tok = id / per_tok;
-    const int group = int(id - tok * per_tok);
+    const uint32_t tok32 = id / uint32_t(per_tok);
+    if (tok32 >= a.n_tok) return;
+    const long long tok = tok32;
+    const int group = int(id - tok32 * uint32_t(per_tok));
     const bool is_q = group < g_q, is_v = group >= g_q + g_k;
     const int h0 = (is_q ? group : is_v ? group - g_q - g_k : group - g_q) * ROWS;
     const int heads = min(ROWS, (is_q ? a.n_q : is_v ? a.n_v : a.n_k) - h0);
@@ -287,13 +303,13 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
                          (long long)h0 * D + lane * N;
     Raw<T, N> raw[ROWS];
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) raw[j] = *reinterpret_cast<const Raw<T, N>*>(src + (j < heads ? j : 0) * D);
+    for (int j = 0; j < ROWS; ++j) if (j < heads) raw[j] = *reinterpret_cast<const Raw<T, N>*>(src + j * D);
 
     // The token's rotation: of a lane's values the cosines and sines it needs (half-split: one
     // per value; interleaved: one per pair).
     const int half = a.rot / 2, i0 = lane * N;
     const bool inter = (a.flags & QG_ROPE_INTERLEAVED) != 0, norm = !is_v && !(a.flags & QG_NORM_NONE);
-    float cs[N], sn[N], w[N];
+    float cs[N] = {}, sn[N] = {}, w[N];
     bool dead = false, turn = false;
     if (a.positions) {
         const int pos = a.positions[tok];
@@ -308,13 +324,15 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
             } else if (turn) {
                 const int at = i0 < half ? i0 : i0 - half;
 #pragma unroll
-                for (int i = 0; i < N; ++i) { cs[i] = row[at + i]; sn[i] = row[half + at + i]; }
+                for (int i = 0; i < N; ++i) {            // b' = b c + a s, a' = a c + b (-s)
+                    cs[i] = row[at + i];
+                    sn[i] = i0 < half ? -row[half + at + i] : row[half + at + i];
+                }
             }
         }
     }
     const int reach = half / N;                          // lanes from a value to its partner (half-split)
-    const bool first = lane < reach;
-    const int partner = !turn ? lane : first ? lane + reach : lane - reach;
+    const int partner = !turn ? lane : lane < reach ? lane + reach : lane - reach;
     const float* const weight = is_q ? a.q_weight : a.k_weight;
     const bool weighted = norm && weight;
     if (weighted) {
@@ -338,10 +356,10 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
         if (j0 >= heads) break;
         float x[G][N];
 #pragma unroll
-        for (int j = 0; j < G; ++j) widen<T, N>(raw[j0 + j], x[j]);
+        for (int j = 0; j < G; ++j) widen<N>(raw[j0 + j], x[j]);
         if (norm) {
             const float mean = __fmul_rn(square_sums<N, G>(x, lane), 1.0f / D);
-            const float root = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, a.eps)));
+            const float root = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, a.eps)));
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const float r = G == 1 ? root : __shfl_sync(kAll, root, sum_lane<G>(j));
@@ -368,10 +386,8 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
                         const float p = __shfl_sync(kAll, x[j][i], partner);
-                        if (turn) {
-                            const float own = __fmul_rn(x[j][i], cs[i]), other = __fmul_rn(p, sn[i]);
-                            x[j][i] = first ? __fsub_rn(own, other) : __fadd_rn(own, other);
-                        }
+                        const float y = __fadd_rn(__fmul_rn(x[j][i], cs[i]), __fmul_rn(p, sn[i]));
+                        x[j][i] = turn ? y : x[j][i];
                     }
                 }
             }
@@ -385,11 +401,11 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
                 for (int i = 0; i < N; ++i) x[j][i] = 0.0f;
             }
             if (is_q) {
-                store<T, N>(static_cast<T*>(a.q_out) + tok * a.q_out_stride + (long long)h * D + i0, x[j]);
+                store<N>(static_cast<T*>(a.q_out) + tok * a.q_out_stride + (long long)h * D + i0, x[j]);
                 continue;
             }
             if (!a.data) {
-                store<T, N>(static_cast<T*>(a.k_out) + tok * a.k_out_stride + (long long)h * D + i0, x[j]);
+                store<N>(static_cast<T*>(a.k_out) + tok * a.k_out_stride + (long long)h * D + i0, x[j]);
                 continue;
             }
             uint32_t code[N];
@@ -424,7 +440,7 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
             const float d = __half2float(scale);
 #pragma unroll
             for (int i = 0; i < N; ++i) x[j][i] = __fmul_rn(float(int(code[i]) - 8), d);
-            store<T, N>(static_cast<T*>(out) + (tok * a.n_k + h) * D + i0, x[j]);
+            store<N>(static_cast<T*>(out) + (tok * a.n_k + h) * D + i0, x[j]);
         }
     }
 }
@@ -460,7 +476,7 @@ qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
     const long long warps = a.n_tok * per_tok;
     const int in_block = wide ? 8 : 4;
     const long long grid = (warps + in_block - 1) / in_block;
-    if (grid > 0x7FFFFFFFll) return QG_EUNSUPPORTED;
+    if (warps > 0x7FFFFFFFll - 8) return QG_EUNSUPPORTED;
     void* params[] = {&a};
     return launch_early(fn, int(grid), 32 * in_block, 0, 1, params, stream);
 }
