@@ -283,7 +283,7 @@ __device__ __forceinline__ void quantize_block(const float (&x)[N], int lane, ui
 // read once and written once) at prompt sizes, by the launch and one load's latency at decode
 // sizes, where ROWS = 1 spreads the heads over more warps.
 template <int D, typename T, int ROWS>
-__global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(128, ROWS > 1 ? 8 : 4) heads_kernel(const HeadArgs a) {
     constexpr int N = D / 32, G = ROWS < 4 ? ROWS : 4;
     const int lane = int(threadIdx.x) & 31;
     const int g_q = (a.n_q + ROWS - 1) / ROWS, g_k = (a.n_k + ROWS - 1) / ROWS, g_v = (a.n_v + ROWS - 1) / ROWS;
@@ -445,13 +445,11 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a) {
     }
 }
 
-// Heads per warp: 2 KB of rows (4 to 8) once that still leaves every SM 32 warps; below, one, so
+// Heads per warp: 2 KB of rows (2 to 8; with 1 KB a chunk of 8191 bf16 tokens took 100 us, with
+// 2 KB 87, and 76 once eight CTAs of four warps fit an SM) once that still leaves every SM 32 warps; below, one, so
 // that a few tokens' heads run side by side.
-#ifndef QG_HR
-#define QG_HR (2048 / (D * int(sizeof(T))))
-#endif
 template <typename T, int D> struct HeadShape {
-    static constexpr int kWide = QG_HR < 2 ? 2 : QG_HR > 8 ? 8 : QG_HR;
+    static constexpr int kFit = 2048 / (D * int(sizeof(T))), kWide = kFit > 8 ? 8 : kFit;
 };
 template <typename T, int D>
 const void* heads_fn(bool wide, int* rows) {
@@ -474,7 +472,7 @@ qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
     const void* fn = act == QG_ACT_F32 ? heads_fn<float>(D, wide, &rows) : heads_fn<__nv_bfloat16>(D, wide, &rows);
     const long long per_tok = (a.n_q + rows - 1) / rows + (a.n_k + rows - 1) / rows + (a.n_v + rows - 1) / rows;
     const long long warps = a.n_tok * per_tok;
-    const int in_block = wide ? 8 : 4;
+    const int in_block = 4;
     const long long grid = (warps + in_block - 1) / in_block;
     if (warps > 0x7FFFFFFFll - 8) return QG_EUNSUPPORTED;
     void* params[] = {&a};
