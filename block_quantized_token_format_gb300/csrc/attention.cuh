@@ -71,6 +71,9 @@ struct AttnArgs {
     uint32_t wait_limit, drain_limit, test_extra_tx;
 };
 
+#ifndef QG_W2
+#define QG_W2 12
+#endif
 #ifndef QG_W
 #define QG_W 16
 #endif
@@ -80,7 +83,7 @@ template <int D, int TILES, int TERMS> struct AttnShape {
     static constexpr int kLaneRows = 2 / TERMS;                      // rows a lane holds per tile
     static constexpr int kTileRows = 8 / TERMS;
     static constexpr int kRows = TILES * kTileRows;
-    static constexpr int kWarps = D == 256 ? 10 - TILES : TILES == 1 ? QG_W : 12;
+    static constexpr int kWarps = D == 256 ? 10 - TILES : TILES == 1 ? QG_W : QG_W2;
     static constexpr float kCodeUnit = TERMS == 1 ? 1.0f / 16777216.0f : 1.0f / 1048576.0f;    // what a code of 1 stands for
     static constexpr float kOddScale = TERMS == 1 ? 0.0625f : 1.0f;
     static constexpr int kRec = kv_record_bytes(D);
@@ -153,12 +156,10 @@ __device__ __forceinline__ f2_t f2_of_h2(uint32_t b) {
     const float2 f = __half22float2(bits_h2(b));
     return f2_of(f.x, f.y);
 }
-// A pair as its fp16 rounding and the fp16 rounding of what that leaves.
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(h);
-    hi = h2_bits(h);
-    lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
 // The four pairs of codes of a key word (nibbles i and i + 4) as fp16 subnormals: code * 2^-20,
 // or with COARSE code * 2^-24 and code * 2^-20 in turn (two shifts less; the queries of the odd
@@ -518,38 +519,46 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             for (int i = 0; i < a.depth; ++i) issue();
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            uint32_t top = 0;
+            float top = 0.0f;
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[t][g][i]) & 0x7FFFFFFFu);
-            top = max(top, __shfl_xor_sync(kFull, top, 1));
-            top = max(top, __shfl_xor_sync(kFull, top, 2));
+                for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[t][g][i]));
+            top = max_nan(top, __shfl_xor_sync(kFull, top, 1));
+            top = max_nan(top, __shfl_xor_sync(kFull, top, 2));
             // 2^s brings the row's largest magnitude to [2^14, 2^15) (s at most 126); a row with a
             // NaN or an infinity has NaN scores.
-            const int e = int(top >> 23);
+            const int e = int((__float_as_uint(top) & 0x7FFFFFFFu) >> 23);
             const int sh = min(141 - e, 126);
             const float up = __uint_as_float(uint32_t(127 + sh) << 23) * a.scale_sign, down = __uint_as_float(uint32_t(127 - sh) << 23);
             const bool finite = e < 255;
             float* const init = reinterpret_cast<float*>(mine + lay.init_off) + t * (NG + 1) * 8;
             if (c4 == 0) init[NG * 8 + r8] = finite ? a.scale_log2 * (1.0f / S::kCodeUnit) * down : __uint_as_float(0x7FFFFFFFu);
+            // Of two terms, the even column takes a value cut off at 11 bits, the odd one the rest.
+            const float rest = TERMS == 2 && (r8 & 1) ? 1.0f : 0.0f;
+            const uint32_t minus = TERMS == 2 && (r8 & 1) ? 0x80000000u : 0u;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 uint32_t v[4];
-                float total_q = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t hi, lo;
                     const float w = (i & 1) ? up * S::kOddScale : up;
-                    split_pair(finite ? x[t][g][i] * w : 0.0f, finite ? x[t][g][i + 4] * w : 0.0f, hi, lo);
-                    v[i] = TERMS == 2 && (r8 & 1) ? lo : hi;
-                    const float2 f = __half22float2(bits_h2(v[i]));
-                    total_q += (f.x + f.y) * ((i & 1) ? 1.0f / S::kOddScale : 1.0f);
+                    float p = finite ? x[t][g][i] * w : 0.0f, q = finite ? x[t][g][i + 4] * w : 0.0f;
+                    if (TERMS == 2) {
+                        p = fmaf(rest, p, __uint_as_float((__float_as_uint(p) & 0xFFFFE000u) ^ minus));
+                        q = fmaf(rest, q, __uint_as_float((__float_as_uint(q) & 0xFFFFE000u) ^ minus));
+                    }
+                    v[i] = h2_bits(__floats2half2_rn(p, q));
                 }
-                total_q += __shfl_xor_sync(kFull, total_q, 1);
-                total_q += __shfl_xor_sync(kFull, total_q, 2);
-                if (c4 == 0) init[g * 8 + r8] = -8.0f * S::kCodeUnit * total_q;
                 *reinterpret_cast<uint4*>(mine + lay.q_off + ((t * NG + g) * 32 + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+                // -8 * (sum of the column): a product with a matrix of -8 (-128 where the odd pairs
+                // carry 2^-4), which also puts it where the scores' product wants it.
+                const uint32_t eight = 0xC800C800u, odd8 = TERMS == 1 ? 0xD800D800u : eight;
+                const uint4 a8 = make_uint4(eight, eight, odd8, odd8);
+                float c[4];
+                mma_f16(c, a8, v[0], v[1], 0.0f, 0.0f);
+                mma_f16(c, a8, v[2], v[3]);
+                if (r8 == 0) *reinterpret_cast<float2*>(init + g * 8 + 2 * c4) = make_float2(c[0] * S::kCodeUnit, c[1] * S::kCodeUnit);
             }
         }
         __syncwarp();
@@ -959,41 +968,67 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         }
         __syncthreads();
         if (*flag == 0) continue;
-        const float* const p0 = a.partial + (2ll * first + 1) * S::kPartial;     // the first CTA's part is its last one
-        const float* const p1 = a.partial + 2ll * (first + 1) * S::kPartial;     // the others' their first
-        for (int e = tid; e < ROWS * D / 2; e += 32 * W) {
-            const int row = e / (D / 2), col = (e - row * (D / 2)) * 2;
+        // Weights of the CTAs' partials, per row, then the row's maximum and sum; where the warps'
+        // parts were.
+        auto cta_part = [&](int i) { return a.partial + (2ll * (first + i) + (i == 0 ? 1 : 0)) * S::kPartial; };
+        float* const wt = reinterpret_cast<float*>(smem + lay.warp_off);         // [ROWS][n + 2]
+        for (int row = warp; row < ROWS; row += W) {
             float m = kNoRef, l = 0.0f;
-            float2 v = make_float2(0.0f, 0.0f);
-            // Eight partials' loads at a time (one round trip to L2), then their sums in order.
-            for (int i0 = 0; i0 < n; i0 += 8) {
-                float mi[8], li[8];
-                float2 x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float* const p = i0 + i == 0 ? p0 : p1 + 2ll * (i0 + i - 1) * S::kPartial;
-                    const bool in = i0 + i < n;
-                    mi[i] = in ? __ldcg(p + ROWS * D + row) : kNoRef;
-                    li[i] = in ? __ldcg(p + ROWS * D + ROWS + row) : 0.0f;
-                    x[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + row * D + col)) : make_float2(0.0f, 0.0f);
-                }
-                float to = m;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) to = fmaxf(to, mi[i]);
-                const float f = exp2_fast(m - to);
-                m = to;
-                l *= f;
-                v.x *= f;
-                v.y *= f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float w = exp2_fast(mi[i] - m);
-                    l = fmaf(li[i], w, l);
-                    v.x = fmaf(x[i].x, w, v.x);
-                    v.y = fmaf(x[i].y, w, v.y);
-                }
+            for (int i = lane; i < n; i += 32) {
+                const float mi = __ldcg(cta_part(i) + ROWS * D + row);
+                wt[row * (n + 2) + i] = mi;
+                m = fmaxf(m, mi);
             }
-            put(it, row, col, v, m, l);
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+            for (int i = lane; i < n; i += 32) {
+                const float f = exp2_fast(wt[row * (n + 2) + i] - m);
+                wt[row * (n + 2) + i] = f;
+                l = fmaf(__ldcg(cta_part(i) + ROWS * D + ROWS + row), f, l);
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(kFull, l, d);
+            if (lane == 0) { wt[row * (n + 2) + n] = m; wt[row * (n + 2) + n + 1] = l; }
+        }
+        __syncthreads();
+        // Four values a thread; where there are more threads than that takes, they share the
+        // partials and add up what they have.
+        constexpr int kQuads = ROWS * D / 4, kSplit = 32 * W / kQuads > 1 ? 32 * W / kQuads : 1;
+        float4* const sums = reinterpret_cast<float4*>(smem + lay.warp_off + 8192);
+        const int share_of = tid / kQuads;
+        for (int e = kSplit > 1 ? tid % kQuads : tid; e < kQuads && (kSplit == 1 || share_of < kSplit); e += kSplit > 1 ? kQuads : 32 * W) {
+            const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
+            const float* const w = wt + row * (n + 2);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int i = kSplit > 1 ? share_of : 0; i < n; i += kSplit) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(cta_part(i) + row * D + col));
+                v.x = fmaf(x.x, w[i], v.x);
+                v.y = fmaf(x.y, w[i], v.y);
+                v.z = fmaf(x.z, w[i], v.z);
+                v.w = fmaf(x.w, w[i], v.w);
+            }
+            if (kSplit > 1) {
+                sums[share_of * kQuads + e] = v;
+            } else {
+                put(it, row, col, make_float2(v.x, v.y), w[n], w[n + 1]);
+                put(it, row, col + 2, make_float2(v.z, v.w), w[n], w[n + 1]);
+            }
+        }
+        if (kSplit > 1) {
+            __syncthreads();
+            for (int e = tid; e < kQuads; e += 32 * W) {
+                const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
+                const float* const w = wt + row * (n + 2);
+                float4 v = sums[e];
+#pragma unroll
+                for (int i = 1; i < kSplit; ++i) {
+                    const float4 x = sums[i * kQuads + e];
+                    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+                }
+                put(it, row, col, make_float2(v.x, v.y), w[n], w[n + 1]);
+                put(it, row, col + 2, make_float2(v.z, v.w), w[n], w[n + 1]);
+            }
         }
     }
 }
