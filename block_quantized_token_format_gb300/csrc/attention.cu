@@ -8,15 +8,15 @@
 
 namespace qg {
 
-AttnKernel attention_lookup_64(int act, int tiles);
-AttnKernel attention_lookup_128(int act, int tiles);
-AttnKernel attention_lookup_256(int act, int tiles);
+AttnKernel attention_lookup_64(int act, int rows);
+AttnKernel attention_lookup_128(int act, int rows);
+AttnKernel attention_lookup_256(int act, int rows);
 
 namespace {
 
-AttnKernel lookup(int act, int D, int tiles) {
-    return D == 64 ? attention_lookup_64(act, tiles) : D == 128 ? attention_lookup_128(act, tiles)
-                                                               : attention_lookup_256(act, tiles);
+AttnKernel lookup(int act, int D, int rows) {
+    return D == 64 ? attention_lookup_64(act, rows) : D == 128 ? attention_lookup_128(act, rows)
+                                                               : attention_lookup_256(act, rows);
 }
 
 // Floats of all partials of a grid of CTAs: two per CTA, one per warp.
@@ -35,8 +35,8 @@ size_t qg_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim) {
         return 0;
     size_t most = 0;
     for (int act = 0; act < 2; ++act)
-        for (int tiles = 1; tiles <= 4; ++tiles)
-            most = std::max(most, partial_floats(lookup(act, head_dim, tiles), kAttnGrid));
+        for (int rows = 4; rows <= 16; rows += 4)
+            most = std::max(most, partial_floats(lookup(act, head_dim, rows), kAttnGrid));
     return size_t(QG_ATTENTION_ZERO_BYTES) + most * sizeof(float);
 }
 
@@ -67,16 +67,16 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     st = device_info(&dev, &sms, &optin, &a.status);
     if (st != QG_OK) return st;
     const int group = n_heads / n_kv;
-    // Column tiles for the rows of a request and key/value head: at most 16 rows at a time, and
-    // equal shares where there are more (24 rows are 12 and 12).
-    const int64_t all_rows = int64_t(max_new) * group, passes = (all_rows + 15) / 16, rows = (all_rows + passes - 1) / passes;
-    int tiles = int(act == QG_ACT_F32 ? (rows + 3) / 4 : (rows + 7) / 8), depth = 0;
+    // The rows of a request and key/value head, at most 16 at a time, and equal shares where there
+    // are more (24 rows are 12 and 12).
+    const int64_t all_rows = int64_t(max_new) * group, passes = (all_rows + 15) / 16;
     AttnKernel k{};
+    int depth = 0;
     auto fits = [&](int d) { return size_t(k.smem(n_req, d)) + kStaticSmemReserve <= size_t(optin); };
     // The deepest ring (2 to 8 stages per warp) that fits one CTA per SM; a long list of requests
     // may leave room only for fewer rows at a time.
-    for (; tiles >= 1 && depth < 2; --tiles) {
-        k = lookup(act, D, tiles);
+    for (int rows = int((all_rows + passes - 1) / passes); rows >= 1 && depth < 2; rows -= 4) {
+        k = lookup(act, D, rows);
         for (depth = 8; depth >= 2 && !fits(depth); --depth) {}
     }
     if (depth < 2) return QG_EUNSUPPORTED;

@@ -77,18 +77,23 @@ struct AttnArgs {
 #ifndef QG_W
 #define QG_W 16
 #endif
-// TILES column tiles of 8 query columns: a row takes TERMS of them (its fp16 terms side by
-// side), so a tile holds 4 rows with two terms or 8 with one.
+// How queries and probabilities enter the tensor core's fp16, in tiles of 8 columns:
+//  kOne    one term a row, 8 rows to a tile (bf16 activations)
+//  kSide   two terms side by side, 4 rows to a tile: for up to 4 rows half the products of kTwice
+//  kTwice  two terms one after the other into one accumulator, 8 rows to a tile: as many products
+//          per row in full tiles, without kSide's sums of neighbouring columns
+enum { kOne = 1, kSide = 2, kTwice = 3 };
 template <int D, int TILES, int TERMS> struct AttnShape {
-    static constexpr int kLaneRows = 2 / TERMS;                      // rows a lane holds per tile
-    static constexpr int kTileRows = 8 / TERMS;
+    static constexpr int kLaneRows = TERMS == kSide ? 1 : 2;         // rows a lane holds per tile
+    static constexpr int kTileRows = 4 * kLaneRows;
+    static constexpr int kMats = TERMS == kTwice ? 2 : 1;            // operand matrices
     static constexpr int kRows = TILES * kTileRows;
-    static constexpr int kWarps = D == 256 ? 10 - TILES : TILES == 1 ? QG_W : QG_W2;
-    static constexpr float kCodeUnit = TERMS == 1 ? 1.0f / 16777216.0f : 1.0f / 1048576.0f;    // what a code of 1 stands for
-    static constexpr float kOddScale = TERMS == 1 ? 0.0625f : 1.0f;
+    static constexpr int kWarps = D == 256 ? 10 - kMats * TILES : kMats * TILES == 1 ? QG_W : QG_W2;
+    static constexpr float kCodeUnit = TERMS == kOne ? 1.0f / 16777216.0f : 1.0f / 1048576.0f;    // what a code of 1 stands for
+    static constexpr float kOddScale = TERMS == kOne ? 0.0625f : 1.0f;
     static constexpr int kRec = kv_record_bytes(D);
     static constexpr int kStage = 2 * kRec;
-    static constexpr int kQBytes = TILES * kv_groups(D) * 512;       // queries in operand order
+    static constexpr int kQBytes = kMats * TILES * kv_groups(D) * 512;    // queries in operand order
     static constexpr int kInitBytes = TILES * (kv_groups(D) + 1) * 32;    // -8 * sum(q) per block and column; factors
     static constexpr int kPartial = kRows * (D + 2);                 // floats: [rows][D], m[rows], l[rows]
 };
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
             int j, head;
-            row_of<ROWS>(a, it, t * S::kTileRows + r8 / TERMS, j, head);
+            row_of<ROWS>(a, it, t * S::kTileRows + (TERMS == kSide ? r8 / 2 : r8), j, head);
             const T* src_row = static_cast<const T*>(a.q) + (long long)(it.rq.first_tok + max(j, 0)) * a.q_stride +
                                (long long)head * D + 8 * c4;
 #pragma unroll
@@ -534,30 +539,37 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             const bool finite = e < 255;
             float* const init = reinterpret_cast<float*>(mine + lay.init_off) + t * (NG + 1) * 8;
             if (c4 == 0) init[NG * 8 + r8] = finite ? a.scale_log2 * (1.0f / S::kCodeUnit) * down : __uint_as_float(0x7FFFFFFFu);
-            // Of two terms, the even column takes a value cut off at 11 bits, the odd one the rest.
-            const float rest = TERMS == 2 && (r8 & 1) ? 1.0f : 0.0f;
-            const uint32_t minus = TERMS == 2 && (r8 & 1) ? 0x80000000u : 0u;
+            // The first of two terms is cut off at 11 bits, the second is the rest (kSide: in the odd column).
+            const float rest = TERMS == kSide && (r8 & 1) ? 1.0f : 0.0f;
+            const uint32_t minus = TERMS == kSide && (r8 & 1) ? 0x80000000u : 0u;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint32_t v[4];
+                uint32_t v[S::kMats][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float w = (i & 1) ? up * S::kOddScale : up;
                     float p = finite ? x[t][g][i] * w : 0.0f, q = finite ? x[t][g][i + 4] * w : 0.0f;
-                    if (TERMS == 2) {
-                        p = fmaf(rest, p, __uint_as_float((__float_as_uint(p) & 0xFFFFE000u) ^ minus));
-                        q = fmaf(rest, q, __uint_as_float((__float_as_uint(q) & 0xFFFFE000u) ^ minus));
+                    if (TERMS != kOne) {
+                        const float cp = __uint_as_float((__float_as_uint(p) & 0xFFFFE000u) ^ minus);
+                        const float cq = __uint_as_float((__float_as_uint(q) & 0xFFFFE000u) ^ minus);
+                        if (TERMS == kTwice) v[S::kMats - 1][i] = h2_bits(__floats2half2_rn(p - cp, q - cq));
+                        p = TERMS == kSide ? fmaf(rest, p, cp) : cp;
+                        q = TERMS == kSide ? fmaf(rest, q, cq) : cq;
                     }
-                    v[i] = h2_bits(__floats2half2_rn(p, q));
+                    v[0][i] = h2_bits(__floats2half2_rn(p, q));
                 }
-                *reinterpret_cast<uint4*>(mine + lay.q_off + ((t * NG + g) * 32 + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
                 // -8 * (sum of the column): a product with a matrix of -8 (-128 where the odd pairs
                 // carry 2^-4), which also puts it where the scores' product wants it.
-                const uint32_t eight = 0xC800C800u, odd8 = TERMS == 1 ? 0xD800D800u : eight;
+                const uint32_t eight = 0xC800C800u, odd8 = TERMS == kOne ? 0xD800D800u : eight;
                 const uint4 a8 = make_uint4(eight, eight, odd8, odd8);
-                float c[4];
-                mma_f16(c, a8, v[0], v[1], 0.0f, 0.0f);
-                mma_f16(c, a8, v[2], v[3]);
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int m = S::kMats - 1; m >= 0; --m) {
+                    *reinterpret_cast<uint4*>(mine + lay.q_off + (((m * TILES + t) * NG + g) * 32 + lane) * 16) =
+                        make_uint4(v[m][0], v[m][1], v[m][2], v[m][3]);
+                    mma_f16(c, a8, v[m][0], v[m][1]);
+                    mma_f16(c, a8, v[m][2], v[m][3]);
+                }
                 if (r8 == 0) *reinterpret_cast<float2*>(init + g * 8 + 2 * c4) = make_float2(c[0] * S::kCodeUnit, c[1] * S::kCodeUnit);
             }
         }
@@ -633,18 +645,19 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint4 qb[TILES];
+                uint4 qb[TILES], ql[TILES];
                 float2 start[TILES];
 #pragma unroll
                 for (int t = 0; t < TILES; ++t) {
                     qb[t] = lds128(qmat + ((t * NG + g) * 32 + lane) * 16);
+                    if (TERMS == kTwice) ql[t] = lds128(qmat + (((TILES + t) * NG + g) * 32 + lane) * 16);
                     start[t] = lds_f2(binit + ((t * (NG + 1) + g) * 8 + 2 * c4) * 4);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     uint32_t x[4], y[4];
-                    key_codes<TERMS == 1>(kw[k][0][g], x);
-                    key_codes<TERMS == 1>(kw[k][1][g], y);
+                    key_codes<TERMS == kOne>(kw[k][0][g], x);
+                    key_codes<TERMS == kOne>(kw[k][1][g], y);
                     const uint4 a0 = make_uint4(x[0], y[0], x[1], y[1]), a1 = make_uint4(x[2], y[2], x[3], y[3]);
                     const float2 d = __half22float2(bits_h2(kd[k][g]));
 #pragma unroll
@@ -652,8 +665,12 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                         float acc[4];
                         mma_f16(acc, a0, qb[t].x, qb[t].y, start[t].x, start[t].y);
                         mma_f16(acc, a1, qb[t].z, qb[t].w);
+                        if (TERMS == kTwice) {
+                            mma_f16(acc, a0, ql[t].x, ql[t].y);
+                            mma_f16(acc, a1, ql[t].z, ql[t].w);
+                        }
                         float(&to)[2][H] = p[t][k];
-                        if (TERMS == 2) {
+                        if (TERMS == kSide) {
                             const float v = acc[0] + acc[1], w = acc[2] + acc[3];
                             to[0][0] = g == 0 ? v * d.x : fmaf(v, d.x, to[0][0]);
                             to[1][0] = g == 0 ? w * d.y : fmaf(w, d.y, to[1][0]);
@@ -668,7 +685,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 }
             }
             const bool masked = key0 + kUnit - 1 > full_high || key0 <= full_low;
-            uint32_t pb[TILES][2][2];                      // probabilities as operand columns
+            uint32_t pb[S::kMats][TILES][2][2];            // probabilities as operand columns
             bool grow = false;
             float top[TILES][H], factor[TILES][H];
 #pragma unroll
@@ -723,9 +740,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float x = p[t][k][i][0], hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
-                        pb[t][k][i] = transpose8(h2_bits(TERMS == 2 ? __floats2half2_rn(hi, x - hi)
-                                                                    : __floats2half2_rn(x, p[t][k][i][H - 1])));
+                        const float x = p[t][k][i][0], y = p[t][k][i][H - 1];
+                        const float cx = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u), cy = __uint_as_float(__float_as_uint(y) & 0xFFFFE000u);
+                        pb[0][t][k][i] = transpose8(h2_bits(TERMS == kSide ? __floats2half2_rn(cx, x - cx)
+                                                            : TERMS == kTwice ? __floats2half2_rn(cx, cy) : __floats2half2_rn(x, y)));
+                        if (TERMS == kTwice) pb[S::kMats - 1][t][k][i] = transpose8(h2_bits(__floats2half2_rn(x - cx, y - cy)));
                     }
             }
 
@@ -796,11 +815,15 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
                         for (int t = 0; t < TILES; ++t) {
                             float acc[4];
-                            mma_f16(acc, a0, pb[t][0][0], pb[t][0][1], 0.0f, 0.0f);
-                            mma_f16(acc, a1, pb[t][1][0], pb[t][1][1]);
+                            mma_f16(acc, a0, pb[0][t][0][0], pb[0][t][0][1], 0.0f, 0.0f);
+                            mma_f16(acc, a1, pb[0][t][1][0], pb[0][t][1][1]);
+                            if (TERMS == kTwice) {
+                                mma_f16(acc, a0, pb[S::kMats - 1][t][0][0], pb[S::kMats - 1][t][0][1]);
+                                mma_f16(acc, a1, pb[S::kMats - 1][t][1][0], pb[S::kMats - 1][t][1][1]);
+                            }
                             float(&x)[H] = o[t][4 * (q * GI + i) + n];
                             float(&y)[H] = o[t][4 * (q * GI + i) + n + 1];
-                            if (TERMS == 2) {
+                            if (TERMS == kSide) {
                                 x[0] += acc[0] + acc[1];
                                 y[0] += acc[2] + acc[3];
                             } else {

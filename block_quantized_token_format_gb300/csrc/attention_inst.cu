@@ -7,12 +7,12 @@ namespace qg {
 #define QG_CAT2(a, b) a##b
 #define QG_CAT(a, b) QG_CAT2(a, b)
 
-AttnKernel QG_CAT(attention_lookup_, QG_ATTN_D)(int act, int tiles) {
+AttnKernel QG_CAT(attention_lookup_, QG_ATTN_D)(int act, int rows) {
     constexpr int D = QG_ATTN_D;
     if (act == QG_ACT_BF16)
-        return tiles == 1 ? attn_kernel<__nv_bfloat16, D, 1, 1>() : attn_kernel<__nv_bfloat16, D, 2, 1>();
-    return tiles == 1 ? attn_kernel<float, D, 1, 2>() : tiles == 2 ? attn_kernel<float, D, 2, 2>()
-         : tiles == 3 ? attn_kernel<float, D, 3, 2>() : attn_kernel<float, D, 4, 2>();
+        return rows <= 8 ? attn_kernel<__nv_bfloat16, D, 1, kOne>() : attn_kernel<__nv_bfloat16, D, 2, kOne>();
+    return rows <= 4 ? attn_kernel<float, D, 1, kSide>() : rows <= 8 ? attn_kernel<float, D, 1, kTwice>()
+         : rows <= 12 ? attn_kernel<float, D, 3, kSide>() : attn_kernel<float, D, 2, kTwice>();
 }
 
 }  // namespace qg
