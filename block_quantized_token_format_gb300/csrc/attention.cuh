@@ -261,6 +261,20 @@ __device__ __forceinline__ uint32_t ticket_add(uint32_t* p) {
     return old;
 }
 
+// A lane's V values of a row that another CTA wrote.
+template <int V> __device__ __forceinline__ void load_row_l2(const float* p, int lane, float (&x)[V]) {
+    if constexpr (V == 2) {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(p + 2 * lane));
+        x[0] = y.x; x[1] = y.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 32 * i + 4 * lane));
+            x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
+        }
+    }
+}
+
 // ------------------------------------------------------------------------------ work
 
 // A request's share of the work: its visible keys in units (from the first one a window
@@ -435,10 +449,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     // unit is two copies, and what they bring is masked or not valid anyway.
     uint32_t au = u0, next_rec = 0, cur_rec = 0;
     int ar = 0, next_count = 0, count = 0, at = 0, next_page = 0;
-    auto fetch = [&]() {
-        next_count = 0;
-        if (au >= u1) return;
-        const Item it = item_at<ROWS>(a, batch, ar, au);
+    auto fetch_from = [&](const Item& it) {
         ar = it.r;
         if (it.start >= u1) return;
         next_count = min(min(16, it.rq.units - it.unit), int(u1 - max(au, it.start)));
@@ -457,6 +468,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                                 i * (128 / int(sizeof(T))) % D);
             }
         }
+    };
+    auto fetch = [&]() {
+        next_count = 0;
+        if (au < u1) fetch_from(item_at<ROWS>(a, batch, ar, au));
     };
     auto turn_batch = [&]() {
         if (next_page < 0 || next_page >= a.n_pages) {
@@ -486,8 +501,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         ++issued;
         in_stage = in_stage + 1 == a.depth ? 0 : in_stage + 1;
     };
-    fetch();
-
     // ---- the warp's part, item by item
     const uint32_t mask = opaque(0x03C003C0u), magic = opaque(0x4C004C00u);
     bool dead = false;
@@ -495,6 +508,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     int r = 0;
     while (u < u1) {
         const Item it = item_at<ROWS>(a, batch, r, u);
+        if (u == u0) fetch_from(it);
         r = it.r;
         u = max(u, it.start);
         if (u >= u1) break;
@@ -890,19 +904,39 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     __syncthreads();
 
     // ---- join the warps' parts, in order.  Part i is warp i / 2's earlier (even) or last one; the
-    // parts of one item are neighbours.  Every warp reads the list for itself.
-    auto part = [&](int i) -> const float* {
-        return (i & 1) ? reinterpret_cast<const float*>(smem + lay.warp_off + (i >> 1) * lay.warp_bytes)
-                       : a.partial + (2ll * gridDim.x + (long long)blockIdx.x * W + (i >> 1)) * S::kPartial;
+    // parts of one item are neighbours.  Every warp reads the list for itself and takes rows.
+    constexpr int V = D / 32;                              // values of a row per lane
+    auto load_row = [&](const float* p, float (&x)[V]) {
+        if constexpr (V == 2) {
+            const float2 y = *reinterpret_cast<const float2*>(p + 2 * lane);
+            x[0] = y.x; x[1] = y.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(p + 32 * i + 4 * lane);
+                x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
+            }
+        }
     };
-    auto put = [&](const Item& it, int row, int col, float2 v, float m, float l) {
+    auto store_row = [&](float* p, const float (&x)[V]) {
+        if constexpr (V == 2) *reinterpret_cast<float2*>(p + 2 * lane) = make_float2(x[0], x[1]);
+        else
+#pragma unroll
+            for (int i = 0; i < V; i += 4) store4(p + 32 * i + 4 * lane, x[i], x[i + 1], x[i + 2], x[i + 3]);
+    };
+    auto put_row = [&](const Item& it, int row, const float (&x)[V], float m, float l) {
         int j, head;
         row_of<ROWS>(a, it, row, j, head);
         if (j < 0) return;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const long long tok = it.rq.first_tok + j;
-        store2(static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D + col, v.x * inv, v.y * inv);
-        if (a.lse && col == 0) a.lse[tok * a.n_heads + head] = (m + log2f(l) - kProbShift) * 0.693147180559945309f;
+        T* const dst = static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D;
+        if constexpr (V == 2) store2(dst + 2 * lane, x[0] * inv, x[1] * inv);
+        else
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                store4(dst + 32 * i + 4 * lane, x[i] * inv, x[i + 1] * inv, x[i + 2] * inv, x[i + 3] * inv);
+        if (a.lse && lane == 0) a.lse[tok * a.n_heads + head] = (m + log2f(l) - kProbShift) * 0.693147180559945309f;
     };
     auto unfinished = [&](int i) {
         const uint32_t* const m = meta + i * kMetaInts;
@@ -915,70 +949,64 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         it.tile = int(m[5]);
         return it;
     };
-    // Per row: the parts' weights, then by an item's first part its maximum and its sum; where
-    // the queries were.
-    auto weights = [&](int row) {
-        return reinterpret_cast<float*>(smem + lay.warp_off + (row % W) * lay.warp_bytes + lay.q_off) + row / W * 96;
-    };
+    float* const cta_parts = a.partial + 2ll * blockIdx.x * S::kPartial;
+    const float* const early_parts = a.partial + (2ll * gridDim.x + (long long)blockIdx.x * W) * S::kPartial;
     static_assert(2 * W <= 32, "a lane per part");
-    static_assert((ROWS + W - 1) / W * 384 <= S::kQBytes, "the weights fit where the queries were");
     const uint32_t my_start = lane < 2 * W ? meta[lane * kMetaInts] : kNoItem;
-    const uint32_t listed = __ballot_sync(kFull, my_start != kNoItem);
-    for (int row = warp; row < ROWS; row += W) {
-        const bool has = (listed >> lane) & 1u;
-        const float* const p = part(has ? lane : 1);
-        const float mi = has ? p[ROWS * D + row] : kNoRef, li = has ? p[ROWS * D + ROWS + row] : 0.0f;
-        for (uint32_t left = listed; left != 0;) {
-            const int head = __ffs(int(left)) - 1;
-            const uint32_t start = __shfl_sync(kFull, my_start, head);
-            const bool in = my_start == start;
-            left &= ~__ballot_sync(kFull, in);
-            float m = in ? mi : kNoRef;
+    // This lane's part (odd lanes: in the ring of a warp, even ones: in the workspace).
+    const float* const my_part = (lane & 1) ? reinterpret_cast<const float*>(smem + lay.warp_off + min(lane >> 1, W - 1) * lay.warp_bytes)
+                                            : early_parts + (long long)min(lane >> 1, W - 1) * S::kPartial;
+    uint32_t left = __ballot_sync(kFull, my_start != kNoItem);
+    int shared_item[2], n_shared = 0;
+    for (int turn = warp; left != 0; turn = (turn + W - ROWS % W) % W) {      // rows go round the warps, item after item
+        const int first_part = __ffs(int(left)) - 1;
+        const uint32_t parts = __ballot_sync(kFull, my_start == __shfl_sync(kFull, my_start, first_part));
+        left &= ~parts;
+        const Item it = unfinished(first_part);
+        const bool all = it.start >= c0 && it.end <= c1, has = (parts >> lane) & 1u;
+        if (!all && n_shared < 2) shared_item[n_shared++] = first_part;
+        for (int row = turn; row < ROWS; row += W) {
+            const float mi = has ? my_part[ROWS * D + row] : kNoRef, li = has ? my_part[ROWS * D + ROWS + row] : 0.0f;
+            float m = mi;
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
             const float f = exp2_fast(mi - m);
-            float l = in ? li * f : 0.0f;
+            float l = has ? li * f : 0.0f;
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(kFull, l, d);
-            float* const w = weights(row);
-            if (in) w[lane] = f;
-            if (lane == head) { w[32 + head] = m; w[64 + head] = l; }
-        }
-    }
-    __syncthreads();
-    int shared_item[2];
-    int n_shared = 0;
-    for (uint32_t left = listed; left != 0;) {
-        const int head = __ffs(int(left)) - 1;
-        const uint32_t parts = __ballot_sync(kFull, my_start == __shfl_sync(kFull, my_start, head));
-        left &= ~parts;
-        const Item it = unfinished(head);
-        const bool all = it.start >= c0 && it.end <= c1;
-        float* const dst = a.partial + (2ll * blockIdx.x + (it.start >= c0 ? 1 : 0)) * S::kPartial;
-        for (int e = tid; e < ROWS * D / 2; e += 32 * W) {
-            const int row = e / (D / 2), col = (e - row * (D / 2)) * 2;
-            const float* const w = weights(row);
-            float2 v = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-            for (uint32_t rest = parts; rest != 0; rest &= rest - 1) {
-                const int i = __ffs(int(rest)) - 1;
-                const float2 x = *reinterpret_cast<const float2*>(part(i) + row * D + col);
-                v.x = fmaf(x.x, w[i], v.x);
-                v.y = fmaf(x.y, w[i], v.y);
+            float v[V] = {};
+            for (uint32_t rest = parts; rest != 0;) {
+                // Four parts' loads at a time; beyond the last, the first again, unused.
+                float x[4][V], w[4];
+                bool in[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = rest != 0 ? __ffs(int(rest)) - 1 : first_part;
+                    w[k] = __shfl_sync(kFull, f, i);
+                    in[k] = rest != 0;
+                    rest &= rest - 1;
+                    if (i & 1) load_row(reinterpret_cast<const float*>(smem + lay.warp_off + (i >> 1) * lay.warp_bytes) + row * D, x[k]);
+                    else load_row(early_parts + (long long)(i >> 1) * S::kPartial + row * D, x[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = in[k] ? fmaf(x[k][i], w[k], v[i]) : v[i];
             }
-            const float m = w[32 + head], l = w[64 + head];
             if (all) {
-                put(it, row, col, v, m, l);
+                put_row(it, row, v, m, l);
             } else {
-                *reinterpret_cast<float2*>(dst + row * D + col) = v;
-                if (col == 0) { dst[ROWS * D + row] = m; dst[ROWS * D + ROWS + row] = l; }
+                float* const dst = cta_parts + (it.start >= c0 ? S::kPartial : 0);
+                store_row(dst + row * D, v);
+                if (lane == 0) { dst[ROWS * D + row] = m; dst[ROWS * D + ROWS + row] = l; }
             }
         }
-        if (!all && n_shared < 2) shared_item[n_shared++] = head;
     }
 
-    // ---- the last CTA of a shared item joins the CTAs' partials, in order
+    // ---- the last CTA of a shared item joins the CTAs' partials, in order: a warp per row, or
+    // several, which share the partials and add up what they have
     uint32_t* const flag = meta + 2 * W * kMetaInts;
+    constexpr int kSplit = W / ROWS > 1 ? W / ROWS : 1, kAhead = 8;
     for (int k = 0; k < n_shared; ++k) {
         const Item it = unfinished(shared_item[k]);
         const uint32_t first = it.start / share, last = (it.end - 1) / share;
@@ -991,66 +1019,65 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         }
         __syncthreads();
         if (*flag == 0) continue;
-        // Weights of the CTAs' partials, per row, then the row's maximum and sum; where the warps'
-        // parts were.
         auto cta_part = [&](int i) { return a.partial + (2ll * (first + i) + (i == 0 ? 1 : 0)) * S::kPartial; };
-        float* const wt = reinterpret_cast<float*>(smem + lay.warp_off);         // [ROWS][n + 2]
-        for (int row = warp; row < ROWS; row += W) {
-            float m = kNoRef, l = 0.0f;
+        float* const sums = reinterpret_cast<float*>(smem + lay.warp_off);       // [kSplit][ROWS][D]: the rings are done with
+        for (int job = warp; job < kSplit * ROWS; job += W) {
+            const int row = job % ROWS, mod = job / ROWS;
+            // The first partials' values are requested before their weights are known.
+            float x[kAhead][V];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (mod + i * kSplit < n) load_row_l2<V>(cta_part(mod + i * kSplit) + row * D, lane, x[i]);
+            float m = kNoRef, l = 0.0f, early_m = kNoRef;        // early_m: of partial `lane`
             for (int i = lane; i < n; i += 32) {
-                const float mi = __ldcg(cta_part(i) + ROWS * D + row);
-                wt[row * (n + 2) + i] = mi;
-                m = fmaxf(m, mi);
+                const float* const p = cta_part(i) + ROWS * D + row;
+                const float mi = __ldcg(p), li = __ldcg(p + ROWS), to = fmaxf(m, mi);
+                if (i == lane) early_m = mi;
+                l = l * exp2_fast(m - to) + li * exp2_fast(mi - to);
+                m = to;
             }
 #pragma unroll
-            for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-            for (int i = lane; i < n; i += 32) {
-                const float f = exp2_fast(wt[row * (n + 2) + i] - m);
-                wt[row * (n + 2) + i] = f;
-                l = fmaf(__ldcg(cta_part(i) + ROWS * D + ROWS + row), f, l);
+            for (int d = 16; d > 0; d /= 2) {
+                const float mo = __shfl_xor_sync(kFull, m, d), lo = __shfl_xor_sync(kFull, l, d), to = fmaxf(m, mo);
+                l = l * exp2_fast(m - to) + lo * exp2_fast(mo - to);
+                m = to;
             }
+            float v[V] = {};
+            for (int i0 = mod; i0 < n; i0 += kAhead * kSplit) {
+                if (i0 != mod) {
 #pragma unroll
-            for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(kFull, l, d);
-            if (lane == 0) { wt[row * (n + 2) + n] = m; wt[row * (n + 2) + n + 1] = l; }
-        }
-        __syncthreads();
-        // Four values a thread; where there are more threads than that takes, they share the
-        // partials and add up what they have.
-        constexpr int kQuads = ROWS * D / 4, kSplit = 32 * W / kQuads > 1 ? 32 * W / kQuads : 1;
-        float4* const sums = reinterpret_cast<float4*>(smem + lay.warp_off + 8192);
-        const int share_of = tid / kQuads;
-        for (int e = kSplit > 1 ? tid % kQuads : tid; e < kQuads && (kSplit == 1 || share_of < kSplit); e += kSplit > 1 ? kQuads : 32 * W) {
-            const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
-            const float* const w = wt + row * (n + 2);
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int i = kSplit > 1 ? share_of : 0; i < n; i += kSplit) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(cta_part(i) + row * D + col));
-                v.x = fmaf(x.x, w[i], v.x);
-                v.y = fmaf(x.y, w[i], v.y);
-                v.z = fmaf(x.z, w[i], v.z);
-                v.w = fmaf(x.w, w[i], v.w);
+                    for (int i = 0; i < kAhead; ++i)
+                        if (i0 + i * kSplit < n) load_row_l2<V>(cta_part(i0 + i * kSplit) + row * D, lane, x[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int at = i0 + i * kSplit;
+                    if (at >= n) break;
+                    const float w = exp2_fast((at < 32 ? __shfl_sync(kFull, early_m, at) : __ldcg(cta_part(at) + ROWS * D + row)) - m);
+#pragma unroll
+                    for (int q = 0; q < V; ++q) v[q] = fmaf(x[i][q], w, v[q]);
+                }
             }
             if (kSplit > 1) {
-                sums[share_of * kQuads + e] = v;
+                store_row(sums + (mod * ROWS + row) * D, v);
+                if (mod == 0 && lane == 0) { sums[kSplit * ROWS * D + row] = m; sums[kSplit * ROWS * D + ROWS + row] = l; }
             } else {
-                put(it, row, col, make_float2(v.x, v.y), w[n], w[n + 1]);
-                put(it, row, col + 2, make_float2(v.z, v.w), w[n], w[n + 1]);
+                put_row(it, row, v, m, l);
             }
         }
         if (kSplit > 1) {
             __syncthreads();
-            for (int e = tid; e < kQuads; e += 32 * W) {
-                const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
-                const float* const w = wt + row * (n + 2);
-                float4 v = sums[e];
+            for (int row = warp; row < ROWS; row += W) {
+                float v[V];
+                load_row(sums + row * D, v);
 #pragma unroll
                 for (int i = 1; i < kSplit; ++i) {
-                    const float4 x = sums[i * kQuads + e];
-                    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+                    float x[V];
+                    load_row(sums + (i * ROWS + row) * D, x);
+#pragma unroll
+                    for (int q = 0; q < V; ++q) v[q] += x[q];
                 }
-                put(it, row, col, make_float2(v.x, v.y), w[n], w[n + 1]);
-                put(it, row, col + 2, make_float2(v.z, v.w), w[n], w[n + 1]);
+                put_row(it, row, v, sums[kSplit * ROWS * D + row], sums[kSplit * ROWS * D + ROWS + row]);
             }
         }
     }
