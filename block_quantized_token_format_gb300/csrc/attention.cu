@@ -104,6 +104,8 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     a.n_kv = n_kv;
     a.group = group;
     a.page_records = cache->page_tokens / kRecordTokens;
+    a.group_inv = group == 1 ? 0xFFFFFFFFu : uint32_t((uint64_t(1) << 32) / uint32_t(group));
+    a.page_inv = a.page_records == 1 ? 0xFFFFFFFFu : uint32_t((uint64_t(1) << 32) / uint32_t(a.page_records));
     a.window = window;
     a.depth = depth;
     a.scale_log2 = scale == 0.0f ? 1.0f : float(std::fabs(double(scale)) * 1.4426950408889634);

@@ -66,6 +66,7 @@ struct AttnArgs {
     unsigned int* status;
     long long q_stride, out_stride, table_stride, n_tok, n_pages;
     int n_req, n_heads, n_kv, group, page_records, window, depth;
+    uint32_t group_inv, page_inv;    // floor(2^32 / x) (of 1: 2^32 - 1)
     float scale_log2;          // |scale| * log2(e) (1 where that is 0)
     float scale_sign;          // the scale's sign (0 for 0), which goes into the queries
     uint32_t wait_limit, drain_limit, test_extra_tx;
@@ -277,6 +278,12 @@ template <int V> __device__ __forceinline__ void load_row_l2(const float* p, int
 
 // ------------------------------------------------------------------------------ work
 
+// i / d with inv = floor(2^32 / d): the high product is the quotient or one less.
+__device__ __forceinline__ uint32_t divide(uint32_t i, uint32_t d, uint32_t inv) {
+    const uint32_t q = __umulhi(i, inv);
+    return q + (i - q * d >= d);
+}
+
 // A request's share of the work: its visible keys in units (from the first one a window
 // leaves) and its row tiles; 0 units for a request that does not fit the call.
 struct Request {
@@ -289,7 +296,7 @@ template <int ROWS> __device__ __forceinline__ Request request_of(const AttnArgs
     q.fresh = end - first_tok;
     q.first_unit = a.window > 0 ? max(0, seq - q.fresh + 1 - a.window) / kUnit : 0;
     q.units = max(1, int((unsigned(seq) + kUnit - 1) / kUnit) - q.first_unit);
-    q.tiles = int(((long long)q.fresh * a.group + ROWS - 1) / ROWS);
+    q.tiles = int((uint32_t(q.fresh) * uint32_t(a.group) + ROWS - 1) / ROWS);      // rows: below 2^32 (they are in memory)
     return q;
 }
 
@@ -318,7 +325,7 @@ template <int ROWS> __device__ __forceinline__ Item item_at(const AttnArgs& a, c
     it.r = r;
     it.rq = request_of<ROWS>(a, b.seq[r], b.first[r], b.first[r + 1]);
     const uint32_t length = uint32_t(it.rq.units + kItemCost), rem = u - b.cum[r], n = rem / length;
-    it.head = int(n / uint32_t(it.rq.tiles));
+    it.head = it.rq.tiles == 1 ? int(n) : int(n / uint32_t(it.rq.tiles));
     it.tile = int(n - uint32_t(it.head) * uint32_t(it.rq.tiles));
     it.start = b.cum[r] + n * length + kItemCost;
     it.end = it.start + uint32_t(it.rq.units);
@@ -338,7 +345,7 @@ struct Sight {
 // Row i of an item's tile: its token and head, or token -1.
 template <int ROWS> __device__ __forceinline__ void row_of(const AttnArgs& a, const Item& it, int row, int& j, int& head) {
     const int i = it.tile * ROWS + row;
-    j = i / a.group;
+    j = int(divide(uint32_t(i), uint32_t(a.group), a.group_inv));
     head = it.head * a.group + (i - j * a.group);
     if (j >= it.rq.fresh) j = -1;
 }
@@ -456,7 +463,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         au = max(au, it.start) + next_count;
         uint32_t rec = 2 * uint32_t(it.rq.first_unit + it.unit) + lane;
         if (rec * kRecordTokens >= unsigned(it.rq.seq)) rec = 0;
-        const uint32_t page = rec / uint32_t(a.page_records);
+        const uint32_t page = divide(rec, uint32_t(a.page_records), a.page_inv);
         next_rec = uint32_t(it.head) * uint32_t(a.page_records) + (rec - page * uint32_t(a.page_records));
         next_page = it.rq.seq > 0 ? a.table[(long long)ar * a.table_stride + page] : 0;
         if (it.unit == 0) {                    // the item's queries, for when it begins
@@ -590,10 +597,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         __syncwarp();
         // Keys that every row sees lie in (full_low, full_high]; any row's in (any_low, any_high].
         const int i0 = it.tile * ROWS, i1 = min(i0 + ROWS, it.rq.fresh * a.group) - 1;
-        const int any_high = begin + i1 / a.group;
-        const int full_high = a.span_mask ? min(begin + i0 / a.group, begin - 1) : begin + i0 / a.group;
+        const int low_pos = begin + int(divide(uint32_t(i0), uint32_t(a.group), a.group_inv));
+        const int any_high = begin + int(divide(uint32_t(i1), uint32_t(a.group), a.group_inv));
+        const int full_high = a.span_mask ? min(low_pos, begin - 1) : low_pos;
         const int full_low = a.window > 0 ? any_high - a.window : -1;
-        const int any_low = a.window > 0 ? begin + i0 / a.group - a.window : -1;
+        const int any_low = a.window > 0 ? low_pos - a.window : -1;
         // What this lane's row h of tile t may see (in units that need it).
         auto sight = [&](int t, int h) {
             int j, head;
@@ -871,25 +879,28 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 l += __shfl_xor_sync(kFull, l, 8);
                 l += __shfl_xor_sync(kFull, l, 16);
                 const int row = t * S::kTileRows + H * c4 + h;
+                if (!whole) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        store4(keep_at + row * D + 32 * g + 4 * r8, o[t][4 * g][h], o[t][4 * g + 1][h], o[t][4 * g + 2][h],
+                               o[t][4 * g + 3][h]);
+                    if (r8 == 0) {
+                        keep_at[ROWS * D + row] = ref[t][h];
+                        keep_at[ROWS * D + ROWS + row] = l;
+                    }
+                    continue;
+                }
                 int j, head;
                 row_of<ROWS>(a, it, row, j, head);
-                if (whole && j < 0) continue;
+                if (j < 0) continue;
                 const long long tok = it.rq.first_tok + j;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 T* const dst = static_cast<T*>(a.out) + tok * a.out_stride + (long long)head * D + 4 * r8;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float v0 = o[t][4 * g][h], v1 = o[t][4 * g + 1][h], v2 = o[t][4 * g + 2][h], v3 = o[t][4 * g + 3][h];
-                    if (whole) store4(dst + 32 * g, v0 * inv, v1 * inv, v2 * inv, v3 * inv);
-                    else store4(keep_at + row * D + 32 * g + 4 * r8, v0, v1, v2, v3);
-                }
-                if (r8 != 0) continue;
-                if (!whole) {
-                    keep_at[ROWS * D + row] = ref[t][h];
-                    keep_at[ROWS * D + ROWS + row] = l;
-                } else if (a.lse) {
-                    a.lse[tok * a.n_heads + head] = (ref[t][h] + log2f(l) - kProbShift) * 0.693147180559945309f;
-                }
+                for (int g = 0; g < NG; ++g)
+                    store4(dst + 32 * g, o[t][4 * g][h] * inv, o[t][4 * g + 1][h] * inv, o[t][4 * g + 2][h] * inv,
+                           o[t][4 * g + 3][h] * inv);
+                if (r8 == 0 && a.lse) a.lse[tok * a.n_heads + head] = (ref[t][h] + log2f(l) - kProbShift) * 0.693147180559945309f;
             }
         if (!whole && lane == 0) {
             uint32_t* const m = meta + (2 * warp + (last ? 1 : 0)) * kMetaInts;
@@ -1028,20 +1039,22 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
                 if (mod + i * kSplit < n) load_row_l2<V>(cta_part(mod + i * kSplit) + row * D, lane, x[i]);
-            float m = kNoRef, l = 0.0f, early_m = kNoRef;        // early_m: of partial `lane`
-            for (int i = lane; i < n; i += 32) {
+            // Maximum and sum over the partials, a lane each (round after round where there are more).
+            const bool in = lane < n;
+            const float early_m = in ? __ldcg(cta_part(lane) + ROWS * D + row) : kNoRef;
+            const float early_l = in ? __ldcg(cta_part(lane) + ROWS * D + ROWS + row) : 0.0f;
+            float m = early_m;
+            for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, __ldcg(cta_part(i) + ROWS * D + row));
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+            const float early_w = exp2_fast(early_m - m);
+            float l = early_l * early_w;
+            for (int i = lane + 32; i < n; i += 32) {
                 const float* const p = cta_part(i) + ROWS * D + row;
-                const float mi = __ldcg(p), li = __ldcg(p + ROWS), to = fmaxf(m, mi);
-                if (i == lane) early_m = mi;
-                l = l * exp2_fast(m - to) + li * exp2_fast(mi - to);
-                m = to;
+                l = fmaf(__ldcg(p + ROWS), exp2_fast(__ldcg(p) - m), l);
             }
 #pragma unroll
-            for (int d = 16; d > 0; d /= 2) {
-                const float mo = __shfl_xor_sync(kFull, m, d), lo = __shfl_xor_sync(kFull, l, d), to = fmaxf(m, mo);
-                l = l * exp2_fast(m - to) + lo * exp2_fast(mo - to);
-                m = to;
-            }
+            for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(kFull, l, d);
             float v[V] = {};
             for (int i0 = mod; i0 < n; i0 += kAhead * kSplit) {
                 if (i0 != mod) {
@@ -1053,7 +1066,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 for (int i = 0; i < kAhead; ++i) {
                     const int at = i0 + i * kSplit;
                     if (at >= n) break;
-                    const float w = exp2_fast((at < 32 ? __shfl_sync(kFull, early_m, at) : __ldcg(cta_part(at) + ROWS * D + row)) - m);
+                    const float w = at < 32 ? __shfl_sync(kFull, early_w, at) : exp2_fast(__ldcg(cta_part(at) + ROWS * D + row) - m);
 #pragma unroll
                     for (int q = 0; q < V; ++q) v[q] = fmaf(x[i][q], w, v[q]);
                 }
