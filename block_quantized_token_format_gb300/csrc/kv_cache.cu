@@ -272,7 +272,7 @@ __device__ __forceinline__ void quantize_block(const float (&x)[N], int lane, ui
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) code[i] = bad ? 8u : uint32_t(min(max(int(roundf(t[i])) + 8, 0), 15));
-    scale = !bad || d == 0.0f ? __float2half_rn(float(__float2bfloat16_rn(d))) : __ushort_as_half(0x7FFFu);
+    scale = d == 0.0f ? __ushort_as_half(0u) : bad ? __ushort_as_half(0x7E00u) : __float2half_rn(float(__float2bfloat16_rn(d)));
 }
 
 // One warp takes ROWS consecutive heads of one kind (queries, keys or values) of a token, a lane
