@@ -108,7 +108,7 @@ template <int D, int TILES, int TERMS> __host__ __device__ inline AttnSmem attn_
     p.seq_off = (n_req + 1) * 4;                     // after the prefix: lengths, then first new tokens
     p.new_off = p.seq_off + n_req * 4;
     p.meta_off = p.new_off + (n_req + 1) * 4;
-    p.warp_off = (p.meta_off + (S::kWarps + 2 * S::kWarps * kMetaInts + 1) * 4 + 127) / 128 * 128;
+    p.warp_off = (p.meta_off + (S::kWarps + 2 * S::kWarps * kMetaInts + 2) * 4 + 127) / 128 * 128;
     p.q_off = depth * S::kStage;                     // a warp's ring comes first
     p.init_off = p.q_off + S::kQBytes;
     p.bar_off = p.init_off + S::kInitBytes;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     int* const firsts = reinterpret_cast<int*>(smem + lay.new_off);
     const Batch batch{cum, seqs, firsts, a.n_req};
     uint32_t* const wsum = reinterpret_cast<uint32_t*>(smem + lay.meta_off);      // [W]
-    uint32_t* const meta = wsum + W;                                              // [W][2][kMetaInts], then a flag
+    uint32_t* const meta = wsum + W;                                              // [W][2][kMetaInts], then two flags
     const int tid = int(threadIdx.x), lane = tid & 31;
     // A warp's place in the CTA's share: neighbours in the share sit on different schedulers, so
     // that a share of few units is spread over all four.
@@ -541,8 +541,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 }
             }
         }
-        if (issued == 0)
-            for (int i = 0; i < a.depth; ++i) issue();
+        // The first stage of every warp before the others: all warps start on the first bytes to
+        // arrive, not on the last of a burst of whole rings.
+        const bool starting = issued == 0;
+        if (starting) issue();
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
             float top = 0.0f;
@@ -595,6 +597,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             }
         }
         __syncwarp();
+        if (starting)
+            for (int i = 1; i < a.depth; ++i) issue();
         // Keys that every row sees lie in (full_low, full_high]; any row's in (any_low, any_high].
         const int i0 = it.tile * ROWS, i1 = min(i0 + ROWS, it.rq.fresh * a.group) - 1;
         const int low_pos = begin + int(divide(uint32_t(i0), uint32_t(a.group), a.group_inv));
@@ -968,14 +972,18 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     const float* const my_part = (lane & 1) ? reinterpret_cast<const float*>(smem + lay.warp_off + min(lane >> 1, W - 1) * lay.warp_bytes)
                                             : early_parts + (long long)min(lane >> 1, W - 1) * S::kPartial;
     uint32_t left = __ballot_sync(kFull, my_start != kNoItem);
-    int shared_item[2], n_shared = 0;
+    int shared_item[2] = {0, 0}, n_shared = 0;
     for (int turn = warp; left != 0; turn = (turn + W - ROWS % W) % W) {      // rows go round the warps, item after item
         const int first_part = __ffs(int(left)) - 1;
         const uint32_t parts = __ballot_sync(kFull, my_start == __shfl_sync(kFull, my_start, first_part));
         left &= ~parts;
         const Item it = unfinished(first_part);
         const bool all = it.start >= c0 && it.end <= c1, has = (parts >> lane) & 1u;
-        if (!all && n_shared < 2) shared_item[n_shared++] = first_part;
+        if (!all) {                                        // at most two: the share's first item and its last
+            if (n_shared == 0) shared_item[0] = first_part;
+            else shared_item[1] = first_part;
+            n_shared = n_shared == 0 ? 1 : 2;
+        }
         for (int row = turn; row < ROWS; row += W) {
             const float mi = has ? my_part[ROWS * D + row] : kNoRef, li = has ? my_part[ROWS * D + ROWS + row] : 0.0f;
             float m = mi;
@@ -1016,20 +1024,23 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 
     // ---- the last CTA of a shared item joins the CTAs' partials, in order: a warp per row, or
     // several, which share the partials and add up what they have
-    uint32_t* const flag = meta + 2 * W * kMetaInts;
+    uint32_t* const flags = meta + 2 * W * kMetaInts;          // one per shared item
     constexpr int kSplit = W / ROWS > 1 ? W / ROWS : 1, kAhead = 8;
+    if (n_shared == 0) return;
+    __syncthreads();
+    if (tid < n_shared) {
+        const uint32_t* const m = meta + (tid == 0 ? shared_item[0] : shared_item[1]) * kMetaInts;
+        const uint32_t first = m[0] / share, n = (m[1] - 1) / share - first + 1;
+        const bool mine_last = ticket_add(a.tickets + first) == n - 1;
+        if (mine_last) a.tickets[first] = 0u;
+        flags[tid] = mine_last;
+    }
     for (int k = 0; k < n_shared; ++k) {
-        const Item it = unfinished(shared_item[k]);
-        const uint32_t first = it.start / share, last = (it.end - 1) / share;
-        const int n = int(last - first) + 1;
         __syncthreads();
-        if (tid == 0) {
-            const bool mine_last = ticket_add(a.tickets + first) == uint32_t(n - 1);
-            if (mine_last) a.tickets[first] = 0u;
-            *flag = mine_last;
-        }
-        __syncthreads();
-        if (*flag == 0) continue;
+        if (flags[k] == 0) continue;
+        const Item it = unfinished(k == 0 ? shared_item[0] : shared_item[1]);
+        const uint32_t first = it.start / share;
+        const int n = int((it.end - 1) / share - first) + 1;
         auto cta_part = [&](int i) { return a.partial + (2ll * (first + i) + (i == 0 ? 1 : 0)) * S::kPartial; };
         float* const sums = reinterpret_cast<float*>(smem + lay.warp_off);       // [kSplit][ROWS][D]: the rings are done with
         for (int job = warp; job < kSplit * ROWS; job += W) {
