@@ -494,15 +494,22 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     uint32_t issued = 0, consumed = 0;
     int in_stage = 0, out_stage = 0;
     uint32_t out_phase = 0;
-    auto issue = [&]() {
+    auto issue = [&](uint32_t extra_tx) {
         if (at == count) {
             if (next_count == 0) return;
             turn_batch();
         }
-        if ((lane >> 1) == at) {
-            const uint32_t bar = bars + 8 * in_stage;
-            if ((lane & 1) == 0) mbar_arrive_expect_tx(bar, S::kStage + (issued == 0 ? a.test_extra_tx : 0u));
-            bulk_load(ring + in_stage * S::kStage + (lane & 1) * S::kRec, a.data + uint64_t(cur_rec) * S::kRec, S::kRec, bar);
+        const uint32_t rec0 = __shfl_sync(kFull, cur_rec, 2 * at), rec1 = __shfl_sync(kFull, cur_rec, 2 * at + 1);
+        if (lane == 0) {
+            const uint32_t bar = bars + 8 * in_stage, to = ring + in_stage * S::kStage;
+            const uint8_t* const from = a.data + uint64_t(rec0) * S::kRec;
+            mbar_arrive_expect_tx(bar, S::kStage + extra_tx);
+            if (rec1 == rec0 + 1) {                        // neighbours in a page: one copy
+                bulk_load(to, from, S::kStage, bar);
+            } else {
+                bulk_load(to, from, S::kRec, bar);
+                bulk_load(to + S::kRec, a.data + uint64_t(rec1) * S::kRec, S::kRec, bar);
+            }
         }
         ++at;
         ++issued;
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         // The first stage of every warp before the others: all warps start on the first bytes to
         // arrive, not on the last of a burst of whole rings.
         const bool starting = issued == 0;
-        if (starting) issue();
+        if (starting) issue(a.test_extra_tx);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
             float top = 0.0f;
@@ -598,7 +605,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         }
         __syncwarp();
         if (starting)
-            for (int i = 1; i < a.depth; ++i) issue();
+            for (int i = 1; i < a.depth; ++i) issue(0u);
         // Keys that every row sees lie in (full_low, full_high]; any row's in (any_low, any_high].
         const int i0 = it.tile * ROWS, i1 = min(i0 + ROWS, it.rq.fresh * a.group) - 1;
         const int low_pos = begin + int(divide(uint32_t(i0), uint32_t(a.group), a.group_inv));
@@ -864,7 +871,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             ++consumed;
             out_stage = out_stage + 1 == a.depth ? 0 : out_stage + 1;
             if (out_stage == 0) out_phase ^= 1;
-            issue();
+            issue(0u);
         }
 
         // ---- the item's end: written out, or left for the join
