@@ -42,7 +42,7 @@ namespace qg {
 
 constexpr int kUnit = 32;                 // keys per unit: two records
 #ifndef QG_E
-#define QG_E 6
+#define QG_E 4
 #endif
 constexpr int kItemCost = QG_E;           // an item's own cost (its queries, its outputs), in units
 constexpr int kMaxAttnReq = 1024;
