@@ -5,32 +5,39 @@
 // Work.  A row is one (new token, query head); the rows of a request that read the same
 // key/value head are cut into tiles of ROWS, and an item is one (request, key/value head, row
 // tile) with its visible keys in units of 32.  All items' units form one sequence, dealt in
-// equal contiguous parts to the CTAs and, within a CTA, to its warps: a batch of any lengths
+// equal contiguous shares to the CTAs and, within a CTA, to its warps: a batch of any lengths
 // loads every SM alike, and a single long request is split over all of them.  Each warp runs
 // its part alone, with a running maximum and sum per row; parts of an item are joined in
 // order, first the warps' within the CTA, then the CTAs' by the last of them to finish (a
 // ticket; no CTA ever waits on another), so results do not change from run to run.
 //
-// Memory.  A unit's keys and values are two records of the cache, each one bulk copy into the
-// warp's own ring (mbarrier-counted, bounded waits), so the bytes in flight are set by shared
-// memory and every byte is read from HBM once per row tile.  Page numbers are fetched a batch
-// of 16 units ahead of their copies.
+// Memory.  A unit's keys and values are two records of the cache, one bulk copy (two where
+// they are not neighbours in a page) into the warp's own ring (mbarrier-counted, bounded
+// waits), so the bytes in flight are set by shared memory and every byte is read from HBM
+// once per row tile.  Page numbers are fetched a batch of 16 units ahead of their copies.
 //
-// Arithmetic.  The tensor cores' m16n8k16 (fp16 in, fp32 out) is the right size here: a
-// decode step has 1 to 32 rows per key/value head, far below the 64 or 128 rows of a tcgen05
-// tile, and operands that come out of nibbles in registers would have to go back through
-// shared memory for it.  Every operand is exact:
+// Arithmetic.  The tensor cores' m16n8k16 (fp16 in, fp32 out) fits: a decode step has 1 to 32
+// rows per key/value head, far below the 64 or 128 rows of a tcgen05 tile, and operands that
+// come out of nibbles in registers would have to go back through shared or tensor memory for
+// it.  Keys (then values, transposed) are the product's 16 rows, query rows its 8 columns.
+// Every operand of the cache is exact:
 //  * scores: a key's codes enter as they are, as fp16 subnormals (a shift and a mask per two
 //    codes, no arithmetic); the sum starts at -8 * sum(q) of its block, and the block's scale
 //    multiplies the fp32 result.  A query is scaled by a power of two to [2^14, 2^15) and split
 //    into two fp16 terms (22 bits; one term is exact for bf16 queries).
-//  * outputs: a value is (16 + code) * d - 24 * d in one fp16 FMA, which is exact because
-//    d has 8 significant bits; probabilities are two fp16 terms (one for bf16 outputs), scaled
-//    by 2^7 relative to a reference that follows the running maximum within 2^8, so that the
-//    outputs are rescaled rarely and no probability that counts becomes subnormal.
-// With at most 8 rows the two terms are the two halves of one 16-row operand (PACKED: the low
-// terms would-be padding rows, no extra work); with 16 rows they are two products into one
-// accumulator.
+//  * outputs: a value is (16 + code) * d - 24 * d in one fp16 FMA, exact because d has 8
+//    significant bits; probabilities are two fp16 terms (one for bf16 outputs, below its
+//    rounding), scaled by 2^7 relative to a reference that follows the running maximum within
+//    2^8, so that outputs are rescaled rarely and a probability counts down to 2^-31 of the
+//    row's largest.  Maxima, sums, outputs and joins are fp32.
+//
+// What bounds it (GB300, measured): per unit of a 128-wide head and 4 fp32 rows a warp issues
+// about 660 instructions, 208 of them for the values' codes, 136 for the keys', 32 tensor
+// products; on this tensor path a product (8 clocks per scheduler) does not overlap with fp32
+// FMAs, which share its register ports.  The loop takes 0.77 ns per unit and GPU (4608 bytes:
+// 6.0 TB/s; without its arithmetic 0.70 ns, 6.6 TB/s): memory bounds it, just.  With 12 rows it
+// takes about 980 instructions and the tensor path and the instruction issue bound it.
+// Around the loop a call costs about 11 us (launch, lengths, first copies; the joins).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,10 +48,12 @@
 namespace qg {
 
 constexpr int kUnit = 32;                 // keys per unit: two records
-#ifndef QG_E
-#define QG_E 4
-#endif
-constexpr int kItemCost = QG_E;           // an item's own cost (its queries, its outputs), in units
+// An item's own cost (its queries, its outputs) in units, for the division of work: without it
+// (0) a ragged batch of 64 took 133 us, with 2 it took 111; 3 to 9 measure alike.
+constexpr int kItemCost = 4;
+// The smallest share of a CTA, in units: 777 keys of 16 heads took 10.5 us with one unit per warp
+// (16), 8.4 with 4, whose warps sit on the four schedulers; 2 measures as 4.
+constexpr int kMinShare = 4;
 constexpr int kMaxAttnReq = 1024;
 constexpr int kAttnGrid = 160;             // most CTAs of a launch (one per SM; the workspace is sized by it)
 static_assert(kAttnGrid * 4 <= QG_ATTENTION_ZERO_BYTES, "one ticket per CTA");
@@ -72,24 +81,23 @@ struct AttnArgs {
     uint32_t wait_limit, drain_limit, test_extra_tx;
 };
 
-#ifndef QG_W2
-#define QG_W2 12
-#endif
-#ifndef QG_W
-#define QG_W 16
-#endif
 // How queries and probabilities enter the tensor core's fp16, in tiles of 8 columns:
 //  kOne    one term a row, 8 rows to a tile (bf16 activations)
 //  kSide   two terms side by side, 4 rows to a tile: for up to 4 rows half the products of kTwice
+//          (and for 9 to 12 three quarters: 3 tiles against 2 of twice the products)
 //  kTwice  two terms one after the other into one accumulator, 8 rows to a tile: as many products
-//          per row in full tiles, without kSide's sums of neighbouring columns
+//          per row in full tiles, without kSide's sums of neighbouring columns (8 rows of 32771
+//          keys and 8 heads: 24.6 us against 25.5)
 enum { kOne = 1, kSide = 2, kTwice = 3 };
 template <int D, int TILES, int TERMS> struct AttnShape {
     static constexpr int kLaneRows = TERMS == kSide ? 1 : 2;         // rows a lane holds per tile
     static constexpr int kTileRows = 4 * kLaneRows;
     static constexpr int kMats = TERMS == kTwice ? 2 : 1;            // operand matrices
     static constexpr int kRows = TILES * kTileRows;
-    static constexpr int kWarps = D == 256 ? 10 - kMats * TILES : kMats * TILES == 1 ? QG_W : QG_W2;
+    // One tile leaves 128 registers a thread enough: 16 warps (262,100 keys of 8 heads: 64 us
+    // against 68 with 12).  More tiles take 168 (12 warps; with 8 warps of 255, 12 rows of 32771
+    // keys took 49 us against 44).  Heads of 256 take what shared memory holds.
+    static constexpr int kWarps = D == 256 ? 10 - kMats * TILES : kMats * TILES == 1 ? 16 : 12;
     static constexpr float kCodeUnit = TERMS == kOne ? 1.0f / 16777216.0f : 1.0f / 1048576.0f;    // what a code of 1 stands for
     static constexpr float kOddScale = TERMS == kOne ? 0.0625f : 1.0f;
     static constexpr int kRec = kv_record_bytes(D);
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         if (!ok || !fits || end == first) return 0;
         const Request q = request_of<ROWS>(a, seq, first, end);
         const unsigned long long n = (unsigned long long)(q.units + kItemCost) * unsigned(q.tiles) * unsigned(a.n_kv);
-        const bool numbered = n < 0x7FFFFFFFull / kMaxAttnReq;       // more than the sequence can number
+        const bool numbered = n < 0x7FFFFFFFull / unsigned(a.n_req);       // the whole sequence stays below 2^31
         bad_len |= !numbered;
         return numbered ? uint32_t(n) : 0u;
     };
@@ -441,19 +449,17 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     if (blockIdx.x == 0 && bad_len) atomicOr(a.status, kStatusBadLength);
     if (blockIdx.x == 0 && bad_page) atomicOr(a.status, kStatusBadPage);
     const uint32_t total = run;
-#ifndef QG_MS
-#define QG_MS 4
-#endif
-    const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, uint32_t(QG_MS));
+    const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, uint32_t(kMinShare));
     const uint32_t c0 = min(share * blockIdx.x, total), c1 = min(c0 + share, total);
     if (c0 == c1) return;
     const uint32_t u0 = c0 + uint32_t((unsigned long long)(c1 - c0) * warp / W);
     const uint32_t u1 = c0 + uint32_t((unsigned long long)(c1 - c0) * (warp + 1) / W);
 
     // ---- records, found a batch (up to 16 units of one item) ahead of their copies: lanes 2 i
-    // and 2 i + 1 hold those of the batch's unit i.  A record past the request's last is replaced
-    // by its first, one of a page that does not exist by the cache's first (and reported): every
-    // unit is two copies, and what they bring is masked or not valid anyway.
+    // and 2 i + 1 hold those of the batch's unit i.  A record past the request's last, or wholly
+    // before its window (its page may be gone), is replaced by the unit's other one, a record of
+    // a page that does not exist by the cache's first (and reported): every unit is two records,
+    // and what a replacement brings is masked or not valid anyway.
     uint32_t au = u0, next_rec = 0, cur_rec = 0;
     int ar = 0, next_count = 0, count = 0, at = 0, next_page = 0;
     auto fetch_from = [&](const Item& it) {
@@ -461,8 +467,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         if (it.start >= u1) return;
         next_count = min(min(16, it.rq.units - it.unit), int(u1 - max(au, it.start)));
         au = max(au, it.start) + next_count;
-        uint32_t rec = 2 * uint32_t(it.rq.first_unit + it.unit) + lane;
-        if (rec * kRecordTokens >= unsigned(it.rq.seq)) rec = 0;
+        const uint32_t base = 2 * uint32_t(it.rq.first_unit + it.unit);
+        uint32_t rec = lane < 2 * next_count ? base + lane : base;
+        if (rec * kRecordTokens >= unsigned(it.rq.seq)) rec &= ~1u;
+        if (a.window > 0 && int(rec * kRecordTokens) + kRecordTokens <= it.rq.seq - it.rq.fresh + 1 - a.window) rec |= 1u;
         const uint32_t page = divide(rec, uint32_t(a.page_records), a.page_inv);
         next_rec = uint32_t(it.head) * uint32_t(a.page_records) + (rec - page * uint32_t(a.page_records));
         next_page = it.rq.seq > 0 ? a.table[(long long)ar * a.table_stride + page] : 0;
@@ -515,6 +523,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         ++issued;
         in_stage = in_stage + 1 == a.depth ? 0 : in_stage + 1;
     };
+
     // ---- the warp's part, item by item
     const uint32_t mask = opaque(0x03C003C0u), magic = opaque(0x4C004C00u);
     bool dead = false;

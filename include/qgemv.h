@@ -451,9 +451,12 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
  *                16 bytes.
  *   lse          device fp32 [n_tok][n_heads] (natural logarithm), or NULL.
  *   table        device int32 [n_req][table_stride], seq_len, cu_new: as qg_cache_pages leaves
- *                them.  Table entries past a request's tokens are not read.
+ *                them.  Entries of pages past a request's tokens, or wholly before what its
+ *                window leaves visible, are not used (such pages may have been given away).
  *   max_new      the largest number of new tokens of a request: chooses the kernel's row tile;
- *                results are right for any value.
+ *                results are right for any value.  Made for the few tokens of a decode or
+ *                verify step: rows (new tokens x n_heads / n_kv_heads) beyond 16 read the cache
+ *                again, through L2, so a long prompt costs a pass of the cache per 16 rows.
  *   n_tok        rows of q and out (tokens past cu_new[n_req] are not touched).
  *   workspace    device, >= qg_attention_workspace_bytes(n_heads, n_kv_heads, head_dim) bytes,
  *                16-byte aligned, its first QG_ATTENTION_ZERO_BYTES bytes ZEROED by the caller
@@ -461,9 +464,9 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
  *                After QG_DEVICE_WAIT_TIMEOUT zero them again.
  *   n_req <= 1024, n_heads a multiple of n_kv_heads.
  * fp32 activations: queries and probabilities enter the tensor cores as two fp16 terms (22
- * bits), sums are fp32; bf16: queries are exact, probabilities one fp16 term.  Outputs are the
- * same on every run; the order of a sum depends on the lengths of the whole batch and on the
- * GPU's number of SMs. */
+ * bits; a probability counts down to 2^-31 of its row's largest), sums are fp32; bf16: queries
+ * are exact, probabilities one fp16 term.  Outputs are the same on every run; the order of a sum
+ * depends on the lengths of the whole batch and on the GPU's number of SMs. */
 #define QG_ATTENTION_ZERO_BYTES 4096
 size_t    qg_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim);
 qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t q_stride, int64_t n_tok, int n_heads,

@@ -396,6 +396,19 @@ def test_attention_masks(D, heads, kv, page, new, window, tree, act):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("page", [16, 32, 48])
+def test_attention_window_does_not_need_older_pages(page):
+    """Pages wholly before the window may have been given away: their entries are not used."""
+    c = Case(41, 128, 6, 2, [200, 77, 1000], [3, 1, 2], page=page, window=40)
+    want = c.run()
+    c.check(want)
+    table = c.table.copy()
+    for r, (s, f) in enumerate(zip(c.seq, c.fresh)):
+        table[r, :max(0, s - f + 1 - c.window) // page] = -1
+    assert (table != c.table).sum() > 8
+    assert torch.equal(c.run(table=ints(table.ravel()).view(table.shape)), want) and qg.qg_device_status() == 0
+
+
 def test_attention_split_over_the_gpu():
     """Long caches: parts joined across warps and CTAs; one request, several, uneven ones."""
     for seed, (held, fresh, heads, kv) in enumerate([([6000], [1], 4, 1), ([3000], [4], 6, 2), ([9000, 0, 40], [1, 2, 3], 8, 2),
