@@ -3,7 +3,9 @@
 A thin ctypes layer over ``_lib/libqgemv.so`` (C ABI in ``include/qgemv.h``):
 the functions carry the C names and only marshal arguments.  Device buffers
 are torch CUDA tensors (or raw device addresses); host buffers for the packer
-are numpy arrays.  Every step of the mat-vec runs in the library's CUDA
+are numpy arrays.  The attention path's calls, which take torch tensors and run once per
+layer and step, go through a compiled module (``_lib/qg_torch.so``) that checks and marshals
+their arguments.  Every step of the mat-vec runs in the library's CUDA
 kernels; if the library is missing, every call raises.
 
     y[t, o] = sum_i dequant(W)[o, i] * x[t, i],  ntok = 1..4
@@ -11,6 +13,7 @@ kernels; if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import numpy as np
@@ -59,9 +62,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     if not os.path.exists(p):
         raise RuntimeError(f"CUDA library not built: {p} is missing (run __graft_entry__.build())")
     try:
-        import torch  # (loads torch's CUDA runtime first so one copy is shared)
-        _ACT.update({torch.float32: QG_ACT_F32, torch.bfloat16: QG_ACT_BF16})
-        _DTYPE.update(i32=torch.int32, i64=torch.int64, f32=torch.float32)
+        import torch  # noqa: F401  (loads torch's CUDA runtime first so one copy is shared)
     except ImportError:
         pass
     lib = ctypes.CDLL(p)
@@ -382,42 +383,23 @@ QG_DEVICE_BAD_LENGTH = 16
 QG_DEVICE_NO_PAGES = 32
 
 
-# The calls below run once per layer and step, where a few microseconds of Python count:
-# their checks look at each tensor once.
-_ACT: dict = {}      # torch dtype -> qg_act, and the dtypes by name; filled when the library loads
-_DTYPE: dict = {}
+_calls = None
 
 
-def _heads(t, dtype, name: str):
-    """(address, token stride, tokens, heads, head_dim) of ``[n_tok, heads, head_dim]``
-    activations whose heads are contiguous (a slice of a projection's row is)."""
-    n, h, d = t.shape
-    s, sh, sd = t.stride()
-    if (sh != d and h > 1) or sd != 1 or t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA [n_tok, heads, head_dim] tensor of one type, heads contiguous, is needed")
-    return t.data_ptr(), s if n > 1 else max(s, h * d), n, h, d
-
-
-def _typed(t, kind: str, name: str, numel: int = 0):
-    """Address of a contiguous CUDA tensor of type ``kind`` with at least ``numel`` entries."""
-    if t is None:
-        return None
-    if t.dtype is not _DTYPE[kind] or not t.is_contiguous() or t.numel() < numel or not t.is_cuda:
-        raise ValueError(f"{name}: a contiguous CUDA {kind} tensor of at least {numel} entries is needed")
-    return t.data_ptr()
-
-
-def _act(t) -> int:
-    a = _ACT.get(t.dtype)
-    if a is None:
-        raise TypeError(f"activations are float32 or bfloat16 tensors, not {t.dtype}")
-    return a
-
-
-def _table(table, n_req: int):
-    if table.dim() != 2 or table.shape[0] < n_req:
-        raise ValueError("table: a contiguous int32 [n_req, width] tensor is needed")
-    return _typed(table, "i32", "table"), table.shape[1]
+def _bound():
+    """The compiled module behind the four calls below, bound to the loaded library."""
+    global _calls
+    lib = load_library()
+    p = os.path.join(os.path.dirname(_LIB_PATH), "qg_torch.so")
+    if not os.path.exists(p):
+        raise RuntimeError(f"torch binding not built: {p} is missing (run __graft_entry__.build())")
+    spec = importlib.util.spec_from_file_location("qg_torch", p)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
+               for fn in (lib.qg_cache_pages, lib.qg_qk_norm_rope, lib.qg_cache_append, lib.qg_attention)))
+    _calls = mod
+    return mod
 
 
 def qg_cache_bytes(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
@@ -431,30 +413,10 @@ def qg_cache_pages(held, fresh, free_pages, table, seq_len, cu_new, slots, posit
     ``free_begin[0]``.  Writes the new entries of ``table`` (int32 ``[n_req, width]``),
     ``seq_len``, ``cu_new`` (int32 ``[n_req + 1]``), ``slots`` (int64) and ``positions`` (int32)
     of all new tokens, and ``free_end[0]`` (``free_begin`` itself may be passed)."""
-    lib = _lib or load_library()
-    n, n_tok = held.shape[0], slots.numel()
-    tp, width = _table(table, n)
-    st = lib.qg_cache_pages(
-        _typed(held, "i32", "held"), _typed(fresh, "i32", "fresh", n), n, page_tokens,
-        _typed(free_pages, "i32", "free_pages"), free_pages.numel(), _typed(free_begin, "i32", "free_begin", 1),
-        _typed(free_end, "i32", "free_end", 1), tp, width, _typed(seq_len, "i32", "seq_len", n),
-        _typed(cu_new, "i32", "cu_new", n + 1), _typed(slots, "i64", "slots"),
-        _typed(positions, "i32", "positions", n_tok), n_tok, _stream(stream))
+    st = (_calls or _bound()).cache_pages(held, fresh, free_pages, table, seq_len, cu_new, slots, positions, page_tokens,
+                                          free_begin, free_end, stream)
     if st != 0:
         raise QGError(st, "qg_cache_pages")
-
-
-def _rotation(cos_sin, positions, n_tok: int):
-    pos = _typed(positions, "i32", "positions", n_tok)
-    if cos_sin is None:
-        return None, 0, 0, pos
-    n_pos, rot = cos_sin.shape
-    return _typed(cos_sin, "f32", "cos_sin"), n_pos, rot, pos
-
-
-def _head_flags(norm: bool, unit_offset: bool, interleaved: bool) -> int:
-    return ((QG_ROPE_INTERLEAVED if interleaved else 0) | (QG_NORM_UNIT_OFFSET if unit_offset else 0)
-            | (0 if norm else QG_NORM_NONE))
 
 
 def qg_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -462,18 +424,8 @@ def qg_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=N
     """Enqueue the RMS norm of every query and key head (``[n_tok, heads, head_dim]``, float32 or
     bfloat16; slices of one projection's rows are taken as they are) and the rotation by
     ``cos_sin[positions]`` (``[n_pos, rot_dim]``: cosines, then sines) in one pass."""
-    lib = _lib or load_library()
-    act, dtype = _act(q), q.dtype
-    qp, qs, n, hq, d = _heads(q, dtype, "q")
-    kp, ks, nk, hk, dk = _heads(k, dtype, "k")
-    qo, qos, nqo, hqo, dqo = _heads(q_out, dtype, "q_out")
-    ko, kos, nko, hko, dko = _heads(k_out, dtype, "k_out")
-    if not (n == nk == nqo == nko and d == dk == dqo == dko and hq == hqo and hk == hko):
-        raise ValueError("qg_qk_norm_rope: q, k and their outputs differ in tokens, heads or head_dim")
-    cs, n_pos, rot, pos = _rotation(cos_sin, positions, n)
-    st = lib.qg_qk_norm_rope(act, qp, qs, kp, ks, n, hq, hk, d, _typed(q_weight, "f32", "q_weight", d),
-                             _typed(k_weight, "f32", "k_weight", d), eps, _head_flags(norm, unit_offset, interleaved),
-                             cs, n_pos, rot, pos, qo, qos, ko, kos, _stream(stream))
+    st = (_calls or _bound()).qk_norm_rope(q, k, q_out, k_out, positions, cos_sin, q_weight, k_weight, eps, norm,
+                                           unit_offset, interleaved, stream)
     if st != 0:
         raise QGError(st, "qg_qk_norm_rope")
 
@@ -484,27 +436,8 @@ def qg_cache_append(cache: qg_cache, k, v, slots, q=None, q_out=None, positions=
     """Enqueue qg_qk_norm_rope's norm and rotation with the keys and the values (``v``: as they
     are) quantized into ``cache`` at ``slots`` (int64 ``[n_tok]``, -1 = none); queries go to
     ``q_out``.  ``k_back`` / ``v_back`` receive the values the cache now stands for."""
-    lib = _lib or load_library()
-    act, dtype = _act(k), k.dtype
-    kp, ks, n, hk, d = _heads(k, dtype, "k")
-    vp, vs, nv, hv, dv = _heads(v, dtype, "v")
-    qp = qs = qo = qos = hq = 0
-    if q is not None:
-        qp, qs, nq, hq, dq = _heads(q, dtype, "q")
-        qo, qos, nqo, hqo, dqo = _heads(q_out, dtype, "q_out")
-        if not (nq == nqo == n and dq == dqo == d and hq == hqo):
-            raise ValueError("qg_cache_append: q and q_out differ from k in tokens or head_dim")
-    if not (nv == n and hk == hv == cache.n_kv_heads and d == dv == cache.head_dim):
-        raise ValueError("qg_cache_append: k and v do not fit the cache's heads")
-    for t, name in ((k_back, "k_back"), (v_back, "v_back")):
-        if t is not None and (t.dtype is not dtype or not t.is_contiguous() or t.numel() < n * hk * d or not t.is_cuda):
-            raise ValueError(f"{name}: a contiguous CUDA [n_tok, n_kv_heads, head_dim] tensor of k's type is needed")
-    cs, n_pos, rot, pos = _rotation(cos_sin, positions, n)
-    st = lib.qg_cache_append(cache.address, act, qp or None, qs, kp, ks, vp, vs, n, hq,
-                             _typed(q_weight, "f32", "q_weight", d), _typed(k_weight, "f32", "k_weight", d), eps,
-                             _head_flags(norm, unit_offset, interleaved), cs, n_pos, rot, pos,
-                             _typed(slots, "i64", "slots", n), qo or None, qos, None if k_back is None else k_back.data_ptr(),
-                             None if v_back is None else v_back.data_ptr(), _stream(stream))
+    st = (_calls or _bound()).cache_append(cache.address, k, v, slots, q, q_out, positions, cos_sin, q_weight, k_weight,
+                                           eps, norm, unit_offset, interleaved, k_back, v_back, stream)
     if st != 0:
         raise QGError(st, "qg_cache_append")
 
@@ -520,20 +453,8 @@ def qg_attention(cache: qg_cache, q, table, seq_len, cu_new, out, workspace, sca
     (``table``, ``seq_len``) into ``out``.  ``window`` > 0: a sliding window; ``span_mask`` (int32
     bits per new token): a draft tree's visibility among the request's new tokens.
     ``workspace``: uint8, ``qg_attention_workspace_bytes``, zeroed once."""
-    lib = _lib or load_library()
-    act, dtype = _act(q), q.dtype
-    qp, qs, n, hq, d = _heads(q, dtype, "q")
-    op, os_, no, ho, do = _heads(out, dtype, "out")
-    if not (n == no and hq == ho and d == do == cache.head_dim):
-        raise ValueError("qg_attention: q, out and the cache differ in tokens, heads or head_dim")
-    n_req = seq_len.shape[0]
-    tp, width = _table(table, n_req)
-    if not workspace.is_cuda:
-        raise ValueError("workspace: a CUDA tensor is needed")
-    st = lib.qg_attention(cache.address, act, qp, qs, n, hq, tp, width, _typed(seq_len, "i32", "seq_len"),
-                          _typed(cu_new, "i32", "cu_new", n_req + 1), n_req, max_new, window,
-                          _typed(span_mask, "i32", "span_mask", n), scale, op, os_, _typed(lse, "f32", "lse", n * hq),
-                          workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    st = (_calls or _bound()).attention(cache.address, q, table, seq_len, cu_new, out, workspace, scale, max_new, window,
+                                        span_mask, lse, stream)
     if st != 0:
         raise QGError(st, "qg_attention")
 

@@ -1,4 +1,5 @@
-"""Build the CUDA shared library ``_lib/libqgemv.so`` in-tree (sm_103a only).
+"""Build the CUDA shared library ``_lib/libqgemv.so`` in-tree (sm_103a only), and the Python
+binding of the attention path's calls, ``_lib/qg_torch.so``, where torch is installed.
 
 Compiles the per-format kernel units, the expert kernels, the attention path's units,
 the C ABI and the host packer in parallel with nvcc / g++, then links one shared library.  Object files go to
@@ -8,10 +9,12 @@ the work when nothing changed.
 from __future__ import annotations
 
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libqgemv.so")
+BINDING = os.path.join(LIBDIR, "qg_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off",
@@ -62,6 +66,23 @@ def _units():
     return cuda, nvcc, units
 
 
+def _binding(cuda: str):
+    """(object, compile command, link command) of the torch binding, None without torch."""
+    torch = importlib.util.find_spec("torch")
+    if torch is None or torch.origin is None:
+        return None
+    home = os.path.dirname(torch.origin)
+    inc, lib = os.path.join(home, "include"), os.path.join(home, "lib")
+    cxx = os.environ.get("CXX", "g++")
+    obj = os.path.join(BUILD, "torch_binding.o")
+    compile_ = [cxx, *CXX_FLAGS, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+                "-c", os.path.join(CSRC, "torch_binding.cpp")]
+    link = [cxx, "-shared", "-o", BINDING, obj, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+    return obj, compile_, link
+
+
 def _stamp(cmds) -> str:
     h = hashlib.sha256()
     files = sorted(os.listdir(CSRC)) + ["qgemv.h"]
@@ -83,9 +104,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     link = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", LIB, *[o for o, _ in units],
             "-Xlinker", f"-rpath,{os.path.join(cuda, 'lib64')}", "-lpthread"]
-    stamp = _stamp([c for _, c in units] + [link])
+    links = [link]
+    binding = _binding(cuda)
+    if binding is not None:
+        units.append(binding[:2])
+        links.append(binding[2])
+    stamp = _stamp([c for _, c in units] + links)
     stamp_file = os.path.join(BUILD, "libqgemv.stamp")
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_file):
+    if not force and os.path.exists(stamp_file) and all(os.path.exists(p) for p in (LIB, BINDING)[:len(links)]):
         with open(stamp_file) as fh:
             if fh.read().strip() == stamp:
                 return LIB
@@ -106,9 +132,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
         for log in logs:
             if log.strip():
                 print(log)
-    r = subprocess.run(link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
+    for link in links:
+        r = subprocess.run(link, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
     with open(stamp_file, "w") as fh:
         fh.write(stamp)
     return LIB
