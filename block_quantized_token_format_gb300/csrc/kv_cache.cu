@@ -152,6 +152,7 @@ struct HeadArgs {
     int n_q, n_k, n_v, page, rot;
     float eps;
     unsigned flags;
+    bool wide_rot, wide_weight;        // cos_sin, both weights: start on 16 bytes
     unsigned int* status;
 };
 
@@ -192,38 +193,30 @@ template <int N> __device__ __forceinline__ void store(__nv_bfloat16* at, const 
     *reinterpret_cast<Raw<__nv_bfloat16, N>*>(at) = raw;
 }
 
-// Sums of squares of G rows of a warp (G a power of two, N values of each per lane), as a tree
-// of adjacent pairs: pairs within the lane, then lanes 2i and 2i + 1, and so on.  The order is
-// part of the operator's definition (the sum then does not depend on the kernel); the first
-// steps halve the rows a lane still carries, so G rows cost G - 1 + 5 - log2(G) shuffles
-// instead of 5 G.  Returns the sum of row `sum_row<G>(lane)`.
-template <int G> __device__ __forceinline__ int sum_row(int lane) {
-    int r = 0;
-#pragma unroll
-    for (int m = G / 2, bit = 0; m >= 1; m /= 2, ++bit) r += ((lane >> bit) & 1) * m;
-    return r;
-}
-template <int G> __host__ __device__ constexpr int sum_lane(int row) {       // a lane that holds row's sum
+// Sums of squares of the S rows of D values that each D / 8 neighbouring lanes hold, a lane the
+// quads `sub` and D / 8 + `sub` of a row, as a tree of adjacent pairs: pairs and quads within
+// the lane, then lanes 2i and 2i + 1, and so on, the row's two halves last.  The order is part
+// of the operator's definition (the sum then does not depend on the kernel); the first steps
+// halve the sums a lane still carries, so 2 S of them cost 2 S - 1 + log2(D / 8 / S) + 1 shuffles.
+// A lane returns the sum of the row whose index its lane bits 1, 2 spell, high bit first (sum_lane).
+template <int S> __host__ __device__ constexpr int sum_lane(int row) {       // a lane that holds row's sum
     int l = 0;
-    for (int m = G / 2, bit = 0; m >= 1; m /= 2, ++bit) l |= ((row / m) & 1) << bit;
+    for (int m = S / 2, d = 2; m >= 1; m /= 2, d *= 2) l += ((row / m) & 1) * d;
     return l;
 }
-template <int N, int G> __device__ __forceinline__ float square_sums(const float (&x)[G][N], int lane) {
-    float s[G];
+template <int D, int S> __device__ __forceinline__ float square_sums(const float (&x)[S][2][4], int lane) {
+    float s[2 * S];
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-        float t[N];
+    for (int j = 0; j < S; ++j)
 #pragma unroll
-        for (int i = 0; i < N; ++i) t[i] = __fmul_rn(x[j][i], x[j][i]);
-#pragma unroll
-        for (int n = N; n > 1; n /= 2)
-#pragma unroll
-            for (int i = 0; i < n / 2; ++i) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
-        s[j] = t[0];
-    }
+        for (int q = 0; q < 2; ++q) {
+            const float* const v = x[j][q];
+            s[q * S + j] = __fadd_rn(__fadd_rn(__fmul_rn(v[0], v[0]), __fmul_rn(v[1], v[1])),
+                                     __fadd_rn(__fmul_rn(v[2], v[2]), __fmul_rn(v[3], v[3])));
+        }
     int d = 1;
 #pragma unroll
-    for (int m = G / 2; m >= 1; m /= 2, d *= 2) {
+    for (int m = S; m >= 1; m /= 2, d *= 2) {
 #pragma unroll
         for (int i = 0; i < m; ++i) {
             const bool up = (lane & d) != 0;
@@ -232,60 +225,67 @@ template <int N, int G> __device__ __forceinline__ float square_sums(const float
         }
     }
 #pragma unroll
-    for (; d < 32; d *= 2) s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], d));
-    return s[0];
+    for (; d < D / 8; d *= 2) s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], d));
+    return __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], 1));
 }
 
-// Codes and scale of the block this lane's N values belong to (32 / N lanes hold a block).
-template <int N>
-__device__ __forceinline__ void quantize_block(const float (&x)[N], int lane, uint32_t (&code)[N], __half& scale) {
+// Codes and scale of the block this lane's four values belong to (8 neighbouring lanes hold a block).
+__device__ __forceinline__ void quantize_block(const float (&x)[4], int lane, uint32_t (&code)[4], __half& scale) {
     float m = x[0];
     uint32_t top = __float_as_uint(x[0]) & 0x7FFFFFFFu;
 #pragma unroll
-    for (int i = 1; i < N; ++i) {                        // the first of the largest (NaN above all)
+    for (int i = 1; i < 4; ++i) {                        // the first of the largest (NaN above all)
         const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
         if (b > top) { top = b; m = x[i]; }
     }
     uint32_t all = top;
 #pragma unroll
-    for (int d = 1; d < 32 / N; d *= 2) all = max(all, __shfl_xor_sync(kAll, all, d));
-    constexpr int kLanes = 32 / N;
-    const uint32_t group = (kLanes == 32 ? kAll : ((1u << kLanes) - 1u)) << (lane & ~(kLanes - 1));
+    for (int d = 1; d < 8; d *= 2) all = max(all, __shfl_xor_sync(kAll, all, d));
+    const uint32_t group = 0xFFu << (lane & 24);
     const uint32_t who = __ballot_sync(kAll, top == all) & group;
     m = __shfl_sync(kAll, m, __ffs(int(who)) - 1);
     const float d = __fmul_rn(m, -0.125f);
     const bool bad = !(all <= __float_as_uint(QG_CACHE_MAX)) || d == 0.0f;
     // x / d through the reciprocal where that cannot change the code (the quotient, within 2^-20
     // of the true one, is not that near to a half), by the division itself elsewhere.
-    float t[N];
+    float t[4];
     const float inv = __frcp_rn(d);
     bool close = !(fabsf(inv) < 1e30f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 4; ++i) {
         t[i] = x[i] * inv;
         const float a = fabsf(t[i]);
         close |= !(fabsf(a - floorf(a) - 0.5f) > 1e-5f);
     }
     if (close) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) t[i] = __fdiv_rn(x[i], d);
+        for (int i = 0; i < 4; ++i) t[i] = __fdiv_rn(x[i], d);
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) code[i] = bad ? 8u : uint32_t(min(max(int(roundf(t[i])) + 8, 0), 15));
+    for (int i = 0; i < 4; ++i) code[i] = bad ? 8u : uint32_t(min(max(int(roundf(t[i])) + 8, 0), 15));
     scale = d == 0.0f ? __ushort_as_half(0u) : bad ? __ushort_as_half(0x7E00u) : __float2half_rn(float(__float2bfloat16_rn(d)));
 }
 
-// One warp takes ROWS consecutive heads of one kind (queries, keys or values) of a token, a lane
-// D / 32 neighbouring values of each: every load and store is one contiguous row of a warp, the
-// rows' loads are all issued before the first is used, and the token's cosines and sines and
-// the weights are read once for the ROWS heads.  Rows are normed G at a time, so that their
-// sums share shuffles and one lane of each computes the root.  Bound by memory (each element
-// read once and written once) at prompt sizes, by the launch and one load's latency at decode
-// sizes, where ROWS = 1 spreads the heads over more warps.
-template <int D, typename T, int ROWS>
-__global__ void __launch_bounds__(128, ROWS > 1 ? 8 : 4) heads_kernel(const HeadArgs a) {
-    constexpr int N = D / 32, G = ROWS < 4 ? ROWS : 4;
-    const int lane = int(threadIdx.x) & 31;
+// Four neighbouring floats, in one load where the array starts on 16 bytes.
+__device__ __forceinline__ void read_quad(const float* p, bool wide, float (&x)[4]) {
+    if (wide) {
+        const float4 r = *reinterpret_cast<const float4*>(p);
+        x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = p[i];
+    }
+}
+
+// One warp takes SETS * 256 / D consecutive heads of one kind (queries, keys or values) of a
+// token: D / 8 lanes a row, a lane the row's quads `sub` and D / 8 + `sub`, so that a
+// half-split rotation of the whole head pairs values of one lane, and a 32-value block of the
+// cache lies in 8 neighbouring lanes.  All rows' loads are issued before the first is used, and
+// the token's cosines and sines and the weights are read once for all of them.
+template <int D, typename T, int SETS>
+__global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const HeadArgs a) {
+    constexpr int L = D / 8, PER = 32 / L, ROWS = PER * SETS;
+    const int lane = int(threadIdx.x) & 31, sub = lane % L, row = lane / L;
     const int g_q = (a.n_q + ROWS - 1) / ROWS, g_k = (a.n_k + ROWS - 1) / ROWS, g_v = (a.n_v + ROWS - 1) / ROWS;
     const int per_tok = g_q + g_k + g_v;
     const uint32_t id = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);        // < 2^31 (host)
@@ -296,165 +296,195 @@ __global__ void __launch_bounds__(128, ROWS > 1 ? 8 : 4) heads_kernel(const Head
     const int group = int(id - tok32 * uint32_t(per_tok));
     const bool is_q = group < g_q, is_v = group >= g_q + g_k;
     const int h0 = (is_q ? group : is_v ? group - g_q - g_k : group - g_q) * ROWS;
-    const int heads = min(ROWS, (is_q ? a.n_q : is_v ? a.n_v : a.n_k) - h0);
+    const int heads = (is_q ? a.n_q : is_v ? a.n_v : a.n_k) - h0;          // rows from here on
+    const int ia = sub * 4, ib = D / 2 + ia;
 
     const T* const src = (is_q ? static_cast<const T*>(a.q) + tok * a.q_stride : is_v ? static_cast<const T*>(a.v) + tok * a.v_stride
                                                                                : static_cast<const T*>(a.k) + tok * a.k_stride) +
-                         (long long)h0 * D + lane * N;
-    Raw<T, N> raw[ROWS];
+                         (long long)(h0 + row) * D + ia;
+    Raw<T, 4> raw[SETS][2] = {};
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) if (j < heads) raw[j] = *reinterpret_cast<const Raw<T, N>*>(src + j * D);
+    for (int j = 0; j < SETS; ++j)
+        if (j * PER + row < heads) {
+            raw[j][0] = *reinterpret_cast<const Raw<T, 4>*>(src + j * PER * D);
+            raw[j][1] = *reinterpret_cast<const Raw<T, 4>*>(src + j * PER * D + D / 2);
+        }
 
-    // The token's rotation: of a lane's values the cosines and sines it needs (half-split: one
-    // per value; interleaved: one per pair).
-    const int half = a.rot / 2, i0 = lane * N;
+    // The token's rotation: the cosines and sines a lane's values need.  Half-split over the whole
+    // head: of its four pairs; over at most half of it: of its first quad, whose partner is the
+    // first quad of another lane; interleaved: of the pairs in its two quads.
+    const int half = a.rot / 2;
     const bool inter = (a.flags & QG_ROPE_INTERLEAVED) != 0, norm = !is_v && !(a.flags & QG_NORM_NONE);
-    float cs[N] = {}, sn[N] = {}, w[N];
-    bool dead = false, turn = false;
+    const bool turn = ia < a.rot, turn_b = ib < a.rot;
+    float cs[4] = {}, sn[4] = {}, w[2][4];
+    const float* angles = nullptr;
+    bool dead = false;
     if (a.positions) {
         const int pos = a.positions[tok];
         dead = pos < 0 || (a.rot > 0 && pos >= a.n_pos);
         if (pos >= 0 && dead && lane == 0) atomicOr(a.status, kStatusBadLength);
         if (!dead && a.rot > 0 && !is_v) {
-            const float* row = a.cos_sin + (long long)pos * a.rot;
-            turn = i0 < a.rot;
-            if (turn && inter) {
+            angles = a.cos_sin + (long long)pos * a.rot;
+            if (inter) {
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) { cs[i] = row[i0 / 2 + i]; sn[i] = row[half + i0 / 2 + i]; }
-            } else if (turn) {
-                const int at = i0 < half ? i0 : i0 - half;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {            // b' = b c + a s, a' = a c + b (-s)
-                    cs[i] = row[at + i];
-                    sn[i] = i0 < half ? -row[half + at + i] : row[half + at + i];
+                for (int i = 0; i < 2; ++i) {
+                    if (turn) { cs[i] = angles[ia / 2 + i]; sn[i] = angles[half + ia / 2 + i]; }
+                    if (turn_b) { cs[2 + i] = angles[ib / 2 + i]; sn[2 + i] = angles[half + ib / 2 + i]; }
                 }
+            } else if (turn) {
+                const int at = ia < half ? ia : ia - half;
+                read_quad(angles + at, a.wide_rot, cs);
+                read_quad(angles + half + at, a.wide_rot, sn);
             }
         }
     }
-    const int reach = half / N;                          // lanes from a value to its partner (half-split)
-    const int partner = !turn ? lane : lane < reach ? lane + reach : lane - reach;
     const float* const weight = is_q ? a.q_weight : a.k_weight;
     const bool weighted = norm && weight;
     if (weighted) {
+        read_quad(weight + ia, a.wide_weight, w[0]);
+        read_quad(weight + ib, a.wide_weight, w[1]);
+        if (a.flags & QG_NORM_UNIT_OFFSET) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = a.flags & QG_NORM_UNIT_OFFSET ? __fadd_rn(weight[i0 + i], 1.0f) : weight[i0 + i];
-    }
-
-    long long slot = -1;
-    if (a.data && !is_q) {
-        slot = a.slots[tok];
-        if (slot >= a.n_slots || slot < -1) {
-            if (lane == 0) atomicOr(a.status, kStatusBadPage);
-            slot = -1;
+            for (int i = 0; i < 4; ++i) { w[0][i] = __fadd_rn(w[0][i], 1.0f); w[1][i] = __fadd_rn(w[1][i], 1.0f); }
         }
     }
-    const long long page = slot >= 0 ? slot / a.page : 0;
-    const int in = slot >= 0 ? int(slot - page * a.page) : 0, t = in % kRecordTokens;
 
+    float x[SETS][2][4];
 #pragma unroll
-    for (int j0 = 0; j0 < ROWS; j0 += G) {
-        if (j0 >= heads) break;
-        float x[G][N];
+    for (int j = 0; j < SETS; ++j) { widen<4>(raw[j][0], x[j][0]); widen<4>(raw[j][1], x[j][1]); }
+    if (norm) {
+        const float mean = __fmul_rn(square_sums<D, SETS>(x, lane), 1.0f / D);
+        const float root = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, a.eps)));
 #pragma unroll
-        for (int j = 0; j < G; ++j) widen<N>(raw[j0 + j], x[j]);
-        if (norm) {
-            const float mean = __fmul_rn(square_sums<N, G>(x, lane), 1.0f / D);
-            const float root = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, a.eps)));
+        for (int j = 0; j < SETS; ++j) {
+            const float r = SETS == 1 ? root : __shfl_sync(kAll, root, (lane & ~(L - 1)) + sum_lane<SETS>(j));
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const float r = G == 1 ? root : __shfl_sync(kAll, root, sum_lane<G>(j));
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    x[j][i] = __fmul_rn(x[j][i], r);
-                    if (weighted) x[j][i] = __fmul_rn(x[j][i], w[i]);
-                }
-            }
+                for (int i = 0; i < 4; ++i) x[j][q][i] = __fmul_rn(x[j][q][i], r);
         }
-        if (a.rot > 0 && !dead && !is_v) {
+        if (weighted) {
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                if (inter) {
-                    if (turn) {
+            for (int j = 0; j < SETS; ++j)
 #pragma unroll
-                        for (int i = 0; i < N / 2; ++i) {
-                            const float u = x[j][2 * i], v = x[j][2 * i + 1];
-                            x[j][2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
-                            x[j][2 * i + 1] = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[j][q][i] = __fmul_rn(x[j][q][i], w[q][i]);
+        }
+    }
+    if (angles) {                                        // (the same for the whole warp)
+        if (inter) {
+#pragma unroll
+            for (int j = 0; j < SETS; ++j)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q ? turn_b : turn) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float u = x[j][q][2 * i], v = x[j][q][2 * i + 1], c = cs[2 * q + i], s = sn[2 * q + i];
+                            x[j][q][2 * i] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
+                            x[j][q][2 * i + 1] = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
                         }
                     }
-                } else {
+        } else if (a.rot == D) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const float p = __shfl_sync(kAll, x[j][i], partner);
-                        const float y = __fadd_rn(__fmul_rn(x[j][i], cs[i]), __fmul_rn(p, sn[i]));
-                        x[j][i] = turn ? y : x[j][i];
-                    }
+            for (int j = 0; j < SETS; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u = x[j][0][i], v = x[j][1][i];
+                    x[j][0][i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
+                    x[j][1][i] = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
                 }
+        } else {
+            // The partner of quad n of the rotated part is n +- half / 4; quads from L on are
+            // second quads, which only a rotation of more than half the head reaches.
+            const int hop = half / 4;
+            const int pa = !turn ? sub : sub < hop ? sub + hop : sub - hop;
+            const int pb = !turn_b ? L + sub : L + sub - hop;                    // (hop < L: a second quad is a high one)
+            const int base = lane & ~(L - 1), from_a = base + pa % L, from_b = base + pb % L;
+            float cb[4] = {}, sb[4] = {};
+            if (turn_b) {
+                read_quad(angles + ib - half, a.wide_rot, cb);
+                read_quad(angles + ib, a.wide_rot, sb);
             }
+#pragma unroll
+            for (int j = 0; j < SETS; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {            // b' = b c + a s, a' = a c - b s
+                    const float u = x[j][0][i], v = x[j][1][i];
+                    float p = __shfl_sync(kAll, u, from_a);
+                    if (a.rot > D / 2) {
+                        const float p1 = __shfl_sync(kAll, v, from_a), r0 = __shfl_sync(kAll, u, from_b), r1 = __shfl_sync(kAll, v, from_b);
+                        if (pa >= L) p = p1;
+                        const float y = __fadd_rn(__fmul_rn(v, cb[i]), __fmul_rn(pb >= L ? r1 : r0, sb[i]));
+                        if (turn_b) x[j][1][i] = y;
+                    }
+                    const float y = __fadd_rn(__fmul_rn(u, cs[i]), __fmul_rn(p, sub < hop ? -sn[i] : sn[i]));
+                    if (turn) x[j][0][i] = y;
+                }
         }
+    }
+    if (dead) {
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-            const int h = h0 + j0 + j;
-            if (j0 + j >= heads) break;
-            if (dead) {
+        for (int j = 0; j < SETS; ++j)
 #pragma unroll
-                for (int i = 0; i < N; ++i) x[j][i] = 0.0f;
-            }
-            if (is_q) {
-                store<N>(static_cast<T*>(a.q_out) + tok * a.q_out_stride + (long long)h * D + i0, x[j]);
-                continue;
-            }
-            if (!a.data) {
-                store<N>(static_cast<T*>(a.k_out) + tok * a.k_out_stride + (long long)h * D + i0, x[j]);
-                continue;
-            }
-            uint32_t code[N];
+            for (int i = 0; i < 4; ++i) x[j][0][i] = x[j][1][i] = 0.0f;
+    }
+    if (is_q || !a.data) {
+        T* const dst = (is_q ? static_cast<T*>(a.q_out) + tok * a.q_out_stride : static_cast<T*>(a.k_out) + tok * a.k_out_stride) +
+                       (long long)(h0 + row) * D + ia;
+#pragma unroll
+        for (int j = 0; j < SETS; ++j)
+            if (j * PER + row < heads) { store<4>(dst + j * PER * D, x[j][0]); store<4>(dst + j * PER * D + D / 2, x[j][1]); }
+        return;
+    }
+
+    long long slot = a.slots[tok];
+    if (slot >= a.n_slots || slot < -1) {
+        if (lane == 0) atomicOr(a.status, kStatusBadPage);
+        slot = -1;
+    }
+    const long long page = slot < 0 ? 0 : slot >> 31 ? slot / a.page : uint32_t(slot) / uint32_t(a.page);
+    const int in = slot >= 0 ? int(slot - page * a.page) : 0, t = in % kRecordTokens;
+    T* const back = static_cast<T*>(is_v ? a.v_back : a.k_out);
+#pragma unroll
+    for (int j = 0; j < SETS; ++j) {
+        if (j * PER >= heads) break;                     // (the same for the whole warp)
+        const int h = h0 + j * PER + row;
+        const bool there = j * PER + row < heads;
+        uint8_t* const rec = a.data + ((page * a.n_k + h) * (a.page / kRecordTokens) + in / kRecordTokens) * kv_record_bytes(D);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t code[4];
             __half scale;
-            quantize_block<N>(x[j], lane, code, scale);
-            if (slot >= 0) {
-                uint8_t* rec = a.data + ((page * a.n_k + h) * (a.page / kRecordTokens) + in / kRecordTokens) * kv_record_bytes(D);
-                const int g = i0 / 32, at = i0 % 32;
-                uint32_t bits = 0;                       // the lane's N nibbles, in order
-#pragma unroll
-                for (int i = 0; i < N; ++i) bits |= code[i] << (4 * i);
-                if (is_v) {
-                    uint8_t* p = rec + kv_v_codes(D) + at % 4 / 2;
-                    const int r = at / 4;
-                    if constexpr (N == 2) p[kv_value_half(D, t, r, g)] = uint8_t(bits);
-                    if constexpr (N == 4) *reinterpret_cast<uint16_t*>(p + kv_value_half(D, t, r, g)) = uint16_t(bits);
-                    if constexpr (N == 8) {
-                        *reinterpret_cast<uint16_t*>(p + kv_value_half(D, t, r, g)) = uint16_t(bits);
-                        *reinterpret_cast<uint16_t*>(p + kv_value_half(D, t, r + 1, g)) = uint16_t(bits >> 16);
-                    }
-                } else {
-                    uint8_t* p = rec + kv_key_word(D, t, at / 8, g) + at % 8 / 2;
-                    if constexpr (N == 2) *p = uint8_t(bits);
-                    if constexpr (N == 4) *reinterpret_cast<uint16_t*>(p) = uint16_t(bits);
-                    if constexpr (N == 8) *reinterpret_cast<uint32_t*>(p) = bits;
-                }
+            quantize_block(x[j][q], lane, code, scale);
+            const int i0 = q ? ib : ia, g = i0 / 32, at = i0 % 32;
+            if (there && slot >= 0) {
+                const uint16_t bits = uint16_t(code[0] | code[1] << 4 | code[2] << 8 | code[3] << 12);
+                uint8_t* const p = is_v ? rec + kv_v_codes(D) + kv_value_half(D, t, at / 4, g) : rec + kv_key_word(D, t, at / 8, g) + at % 8 / 2;
+                *reinterpret_cast<uint16_t*>(p) = bits;
                 if (at == 0)
                     *reinterpret_cast<__half*>(rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + kv_scale(D, t, g)) = scale;
             }
-            void* const out = is_v ? a.v_back : a.k_out;
-            if (!out) continue;
-            const float d = __half2float(scale);
+            if (there && back) {
+                const float d = __half2float(scale);
+                float y[4];
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[j][i] = __fmul_rn(float(int(code[i]) - 8), d);
-            store<N>(static_cast<T*>(out) + (tok * a.n_k + h) * D + i0, x[j]);
+                for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(float(int(code[i]) - 8), d);
+                store<4>(back + (tok * a.n_k + h) * D + i0, y);
+            }
         }
     }
 }
 
-// Heads per warp: 2 KB of rows (2 to 8; with 1 KB a chunk of 8191 bf16 tokens took 100 us, with
-// 2 KB 87, and 76 once eight CTAs of four warps fit an SM) once that still leaves every SM 32 warps; below, one, so
-// that a few tokens' heads run side by side.
-template <typename T, int D> struct HeadShape {
-    static constexpr int kFit = 2048 / (D * int(sizeof(T))), kWide = kFit > 8 ? 8 : kFit;
-};
+// Sets of rows per warp: 2 KB of rows once that still leaves every SM 32 warps; below, one set, so
+// that a few tokens' heads run side by side.  A chunk of 8191 bf16 tokens takes 64 us with 2 KB,
+// 77 with 1 and 71 with 4; one of 4100 fp32 tokens with the store 40 with 2 KB, 44 with 4.
+template <typename T> constexpr int kSets = 8 / int(sizeof(T));
 template <typename T, int D>
 const void* heads_fn(bool wide, int* rows) {
-    *rows = wide ? HeadShape<T, D>::kWide : 1;
-    return wide ? (const void*)&heads_kernel<D, T, HeadShape<T, D>::kWide> : (const void*)&heads_kernel<D, T, 1>;
+    *rows = 256 / D * (wide ? kSets<T> : 1);
+    return wide ? (const void*)&heads_kernel<D, T, kSets<T>> : (const void*)&heads_kernel<D, T, 1>;
 }
 
 template <typename T> const void* heads_fn(int D, bool wide, int* rows) {
@@ -465,6 +495,8 @@ qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
     int dev = 0, sms = 0, optin = 0;
     qg_status st = device_info(&dev, &sms, &optin, &a.status);
     if (st != QG_OK) return st;
+    a.wide_rot = aligned(a.cos_sin, 16);
+    a.wide_weight = aligned(a.q_weight, 16) && aligned(a.k_weight, 16);
     const long long heads = a.n_q + a.n_k + a.n_v;
     if (heads == 0 || a.n_tok == 0) return QG_OK;
     const bool wide = a.n_tok * heads >= 4ll * 32 * sms;
