@@ -156,41 +156,22 @@ struct HeadArgs {
     unsigned int* status;
 };
 
-template <typename T, int N> struct Raw;                 // N elements of a lane as one or two words
-template <> struct Raw<float, 2> { float2 v; };
-template <> struct Raw<float, 4> { float4 v; };
-template <> struct Raw<float, 8> { float4 v[2]; };
-template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
-template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
-template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
+template <typename T> struct Quad;                       // four elements of a lane
+template <> struct Quad<float> { float4 v; };
+template <> struct Quad<__nv_bfloat16> { uint2 v; };
 
-template <int N> __device__ __forceinline__ void widen(const Raw<float, N>& raw, float (&x)[N]) {
-    const float* e = reinterpret_cast<const float*>(&raw);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = e[i];
+__device__ __forceinline__ void widen(const Quad<float>& q, float (&x)[4]) { x[0] = q.v.x, x[1] = q.v.y, x[2] = q.v.z, x[3] = q.v.w; }
+__device__ __forceinline__ void widen(const Quad<__nv_bfloat16>& q, float (&x)[4]) {
+    x[0] = __uint_as_float(q.v.x << 16), x[1] = __uint_as_float(q.v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(q.v.y << 16), x[3] = __uint_as_float(q.v.y & 0xFFFF0000u);
 }
-template <int N> __device__ __forceinline__ void widen(const Raw<__nv_bfloat16, N>& raw, float (&x)[N]) {
-    const uint32_t* e = reinterpret_cast<const uint32_t*>(&raw);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        x[2 * i] = __uint_as_float(e[i] << 16);
-        x[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
-    }
-}
-
-template <int N> __device__ __forceinline__ void store(float* at, const float (&x)[N]) {
-    Raw<float, N> raw;
-    float* e = reinterpret_cast<float*>(&raw);
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = x[i];
-    *reinterpret_cast<Raw<float, N>*>(at) = raw;
-}
-template <int N> __device__ __forceinline__ void store(__nv_bfloat16* at, const float (&x)[N]) {
-    Raw<__nv_bfloat16, N> raw;
-    __nv_bfloat162* e = reinterpret_cast<__nv_bfloat162*>(&raw);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) e[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);      // nearest even
-    *reinterpret_cast<Raw<__nv_bfloat16, N>*>(at) = raw;
+__device__ __forceinline__ void store(float* at, const float (&x)[4]) { *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void store(__nv_bfloat16* at, const float (&x)[4]) {
+    Quad<__nv_bfloat16> q;
+    __nv_bfloat162* e = reinterpret_cast<__nv_bfloat162*>(&q);
+    e[0] = __floats2bfloat162_rn(x[0], x[1]);            // nearest even
+    e[1] = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<Quad<__nv_bfloat16>*>(at) = q;
 }
 
 // Sums of squares of the S rows of D values that each D / 8 neighbouring lanes hold, a lane the
@@ -282,6 +263,13 @@ __device__ __forceinline__ void read_quad(const float* p, bool wide, float (&x)[
 // half-split rotation of the whole head pairs values of one lane, and a 32-value block of the
 // cache lies in 8 neighbouring lanes.  All rows' loads are issued before the first is used, and
 // the token's cosines and sines and the weights are read once for all of them.
+//
+// Bounds (GB300, measured): norm and rotation of 8191 tokens of 72 bf16 heads of 128 take 64 us,
+// 4.7 TB/s (4 bytes an element and no more), 84 warp instructions a row at 2.7 a clock: memory
+// latency and instruction issue together.  With quads of neighbouring lanes exchanged for the
+// rotation and one row to a warp it was 115 instructions and 76 us; several tokens to a warp in a
+// loop made it 59 and the store below 46 instead of 40.  4100 tokens of 32 + 8 + 8 fp32 heads
+// with the store: 40 us, 5.2 TB/s.  At 4 tokens: 2.1 and 3.0 us, a launch and two latencies.
 template <int D, typename T, int SETS>
 __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const HeadArgs a) {
     constexpr int L = D / 8, PER = 32 / L, ROWS = PER * SETS;
@@ -302,12 +290,12 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
     const T* const src = (is_q ? static_cast<const T*>(a.q) + tok * a.q_stride : is_v ? static_cast<const T*>(a.v) + tok * a.v_stride
                                                                                : static_cast<const T*>(a.k) + tok * a.k_stride) +
                          (long long)(h0 + row) * D + ia;
-    Raw<T, 4> raw[SETS][2] = {};
+    Quad<T> raw[SETS][2] = {};
 #pragma unroll
     for (int j = 0; j < SETS; ++j)
         if (j * PER + row < heads) {
-            raw[j][0] = *reinterpret_cast<const Raw<T, 4>*>(src + j * PER * D);
-            raw[j][1] = *reinterpret_cast<const Raw<T, 4>*>(src + j * PER * D + D / 2);
+            raw[j][0] = *reinterpret_cast<const Quad<T>*>(src + j * PER * D);
+            raw[j][1] = *reinterpret_cast<const Quad<T>*>(src + j * PER * D + D / 2);
         }
 
     // The token's rotation: the cosines and sines a lane's values need.  Half-split over the whole
@@ -351,7 +339,7 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
 
     float x[SETS][2][4];
 #pragma unroll
-    for (int j = 0; j < SETS; ++j) { widen<4>(raw[j][0], x[j][0]); widen<4>(raw[j][1], x[j][1]); }
+    for (int j = 0; j < SETS; ++j) { widen(raw[j][0], x[j][0]); widen(raw[j][1], x[j][1]); }
     if (norm) {
         const float mean = __fmul_rn(square_sums<D, SETS>(x, lane), 1.0f / D);
         const float root = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, a.eps)));
@@ -435,7 +423,7 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
                        (long long)(h0 + row) * D + ia;
 #pragma unroll
         for (int j = 0; j < SETS; ++j)
-            if (j * PER + row < heads) { store<4>(dst + j * PER * D, x[j][0]); store<4>(dst + j * PER * D + D / 2, x[j][1]); }
+            if (j * PER + row < heads) { store(dst + j * PER * D, x[j][0]); store(dst + j * PER * D + D / 2, x[j][1]); }
         return;
     }
 
@@ -471,7 +459,7 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
                 float y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(float(int(code[i]) - 8), d);
-                store<4>(back + (tok * a.n_k + h) * D + i0, y);
+                store(back + (tok * a.n_k + h) * D + i0, y);
             }
         }
     }
