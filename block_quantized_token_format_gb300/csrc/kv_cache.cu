@@ -17,7 +17,7 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kMaxPageReq = 16384;      // requests of one qg_cache_pages call (two prefix arrays in shared memory)
-constexpr int kPageThreads = 512;
+constexpr int kPageThreads = 512;       // most
 
 __device__ __forceinline__ void grid_dependency() {
     // Let the next kernel start its prologue; this one's inputs may come from the previous.
@@ -49,19 +49,21 @@ struct PageArgs {
 // new token: a binary search for its request, its page from the table (a page the request
 // held) or from the free list, its slot and position; the first token of a page writes the
 // table's entry.  Working per token rather than per request spreads one long prompt over the
-// grid as evenly as many short ones.  Bound by latency at decode sizes (one launch, two
-// dependent loads) and by the 12 bytes written per token at prompt sizes.
+// grid as evenly as many short ones.
+// Bound by latency (GB300, measured): 48 requests with a token each 3.0 us, of which an empty
+// launch is 2; 40 prompts of up to 16001 tokens 4.8 us, 0.76 TB/s of its 3.6 MB: one launch,
+// the scan, a search in shared memory and two dependent loads.
 __global__ void __launch_bounds__(kPageThreads) cache_pages_kernel(const PageArgs a) {
     extern __shared__ int32_t prefix[];                  // [n_req + 1] tokens, then [n_req] pages
     __shared__ long long warp_tok[kPageThreads / 32], warp_pg[kPageThreads / 32];
     int32_t* const cu = prefix;
     int32_t* const off = prefix + a.n_req + 1;
-    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, threads = int(blockDim.x);
     grid_dependency();
     const long long begin = a.free_begin ? *a.free_begin : 0;
     bool bad = begin < 0;
     long long run_tok = 0, run_pg = 0;
-    for (int r0 = 0; r0 < a.n_req; r0 += kPageThreads) {
+    for (int r0 = 0; r0 < a.n_req; r0 += threads) {
         const int r = r0 + tid;
         long long tok = 0, pg = 0;
         if (r < a.n_req) {
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_pages_kernel(const PageArg
         if (lane == 31) { warp_tok[warp] = st; warp_pg[warp] = sp; }
         __syncthreads();
         long long bt = run_tok, bp = run_pg;
-        for (int w = 0; w < kPageThreads / 32; ++w) {
+        for (int w = 0; w < threads / 32; ++w) {
             if (w < warp) { bt += warp_tok[w]; bp += warp_pg[w]; }
             run_tok += warp_tok[w];
             run_pg += warp_pg[w];
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_pages_kernel(const PageArg
     if (tid == 0) cu[a.n_req] = int32_t(total);
     if (bad || run_tok > a.n_tok) atomicOr(a.status, kStatusBadLength);
     __syncthreads();
-    for (long long t = (long long)blockIdx.x * kPageThreads + tid; t < a.n_tok; t += (long long)gridDim.x * kPageThreads) {
+    for (long long t = (long long)blockIdx.x * threads + tid; t < a.n_tok; t += (long long)gridDim.x * threads) {
         long long slot = -1;
         int pos = -1;
         if (t < total) {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_pages_kernel(const PageArg
         __syncthreads();
     }
     if (blockIdx.x == 0) {
-        for (int r = tid; r <= a.n_req; r += kPageThreads) a.cu_new[r] = cu[r];
+        for (int r = tid; r <= a.n_req; r += threads) a.cu_new[r] = cu[r];
         if (tid == 0 && a.free_end) *a.free_end = int32_t(min(max(begin, 0ll) + run_pg, a.n_free));
     }
 }
@@ -596,12 +598,17 @@ qg_status qg_cache_pages(const int32_t* held, const int32_t* fresh, int n_req, i
     const size_t smem = (2 * size_t(n_req) + 1) * sizeof(int32_t);
     const void* fn = (const void*)&cache_pages_kernel;
     if (smem > 48 * 1024 && blocks_per_sm(fn, dev, optin, kPageThreads, smem) < 1) return QG_EUNSUPPORTED;
-    int64_t grid = std::max<int64_t>(1, std::min<int64_t>((n_tok + kPageThreads - 1) / kPageThreads, sms));
+    // CTAs of 256 threads, three to an SM, start and scan sooner than one of 512 (3.0 us against 3.5
+    // at 48 tokens, 4.8 against 5.7 at 300,000).  Where 256 threads would scan in two rounds (300
+    // requests: 4.3 us against 3.9), or a call in place, which has 8 CTAs, would take its tokens in
+    // two (32,000: 12.8 us against 9.3), CTAs have 512.
+    const int threads = n_req > 256 || (a.in_place && n_tok > 8 * 256) ? kPageThreads : 256;
+    int64_t grid = std::max<int64_t>(1, std::min<int64_t>((n_tok + threads - 1) / threads, threads == 256 ? 3 * sms : sms));
     // In place every CTA must have read free_begin before it is written: one cluster, which can wait for itself.
     const int cluster = a.in_place ? int(grid >= 8 ? 8 : grid) : 1;
     if (a.in_place) grid = cluster;
     void* params[] = {&a};
-    return launch_early(fn, int(grid), kPageThreads, smem, cluster, params, stream);
+    return launch_early(fn, int(grid), threads, smem, cluster, params, stream);
 }
 
 qg_status qg_qk_norm_rope(qg_act act, const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t n_tok,
