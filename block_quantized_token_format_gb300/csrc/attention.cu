@@ -19,6 +19,23 @@ AttnKernel lookup(int act, int D, int rows) {
                                                                : attention_lookup_256(act, rows);
 }
 
+// Rows of a tile for `rows` rows of a request and key/value head; a tile is one pass over the
+// keys.  Measured on 12 requests of up to 20000 keys, us:
+//   bf16: a pass of 16 rows costs 1.6 to 1.8 of 8, so 16, unless that leaves half a tile empty
+//     (24 rows: 128 wide 75 with three tiles of 8, 93 with two of 16; 32 rows: 98 and 93).
+//   fp32, 128 and 256 wide: a tile of 12 (three of one term beside the other) costs 1.5 of 8 and is
+//     the better one where it is enough (12 rows: 54 against 63 with two of 8; 24 rows: 94 and 90; heads
+//     of 256: 62 and 67; 102 and 92).  A tile of 16 cost more than two of 8 (70 and 63; 80 and 67).
+//   fp32, 64 wide: what a pass costs whatever its rows weighs more: as few passes of up to 16 as it
+//     takes, in equal shares (16 rows: 66, with two of 8 86; 24 rows: 103, with three of 8 125).
+int row_tile(int act, int D, int64_t rows) {
+    const int64_t eights = (rows + 7) / 8, passes = (rows + 15) / 16;
+    if (eights == 1) return int(rows);
+    if (act == QG_ACT_BF16) return eights % 2 != 0 && eights <= 5 ? 8 : 16;
+    if (D == 64) return int((rows + passes - 1) / passes);
+    return rows <= 12 ? 12 : 8;
+}
+
 // Floats of all partials of a grid of CTAs: two per CTA, one per warp.
 size_t partial_floats(const AttnKernel& k, int grid) { return size_t(grid) * size_t(2 + k.warps) * size_t(k.partial); }
 
@@ -67,15 +84,13 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     st = device_info(&dev, &sms, &optin, &a.status);
     if (st != QG_OK) return st;
     const int group = n_heads / n_kv;
-    // The rows of a request and key/value head, at most 16 at a time, and equal shares where there
-    // are more (24 rows are 12 and 12).
-    const int64_t all_rows = int64_t(max_new) * group, passes = (all_rows + 15) / 16;
+    const int64_t all_rows = int64_t(max_new) * group;
     AttnKernel k{};
     int depth = 0;
     auto fits = [&](int d) { return size_t(k.smem(n_req, d)) + kStaticSmemReserve <= size_t(optin); };
     // The deepest ring (2 to 8 stages per warp) that fits one CTA per SM; a long list of requests
     // may leave room only for fewer rows at a time.
-    for (int rows = int((all_rows + passes - 1) / passes); rows >= 1 && depth < 2; rows -= 4) {
+    for (int rows = row_tile(act, D, all_rows); rows >= 1 && depth < 2; rows -= 4) {
         k = lookup(act, D, rows);
         for (depth = 8; depth >= 2 && !fits(depth); --depth) {}
     }

@@ -96,8 +96,11 @@ template <int D, int TILES, int TERMS> struct AttnShape {
     static constexpr int kRows = TILES * kTileRows;
     // One tile leaves 128 registers a thread enough: 16 warps (262,100 keys of 8 heads: 64 us
     // against 68 with 12).  More tiles take 168 (12 warps; with 8 warps of 255, 12 rows of 32771
-    // keys took 49 us against 44).  Heads of 256 take what shared memory holds.
-    static constexpr int kWarps = D == 256 ? 10 - kMats * TILES : kMats * TILES == 1 ? 16 : 12;
+    // keys took 49 us against 44).  Heads of 256 have shared memory for 9 warps of one tile, but a
+    // ninth gives one scheduler a warp more than the others, and all wait for that one: 12 requests
+    // of up to 20000 keys took 42 us with 9 and 33 with 8 (bf16; fp32: 35 and 30).  Three tiles of
+    // them leave room for 7.
+    static constexpr int kWarps = D == 256 ? (kMats * TILES == 3 ? 7 : 8) : kMats * TILES == 1 ? 16 : 12;
     static constexpr float kCodeUnit = TERMS == kOne ? 1.0f / 16777216.0f : 1.0f / 1048576.0f;    // what a code of 1 stands for
     static constexpr float kOddScale = TERMS == kOne ? 0.0625f : 1.0f;
     static constexpr int kRec = kv_record_bytes(D);

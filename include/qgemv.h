@@ -455,8 +455,9 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
  *                window leaves visible, are not used (such pages may have been given away).
  *   max_new      the largest number of new tokens of a request: chooses the kernel's row tile;
  *                results are right for any value.  Made for the few tokens of a decode or
- *                verify step: rows (new tokens x n_heads / n_kv_heads) beyond 16 read the cache
- *                again, through L2, so a long prompt costs a pass of the cache per 16 rows.
+ *                verify step: rows (new tokens x n_heads / n_kv_heads) beyond a tile of 8 to 16
+ *                read the cache again, through L2, so a long prompt costs a pass of the cache per
+ *                tile.
  *   n_tok        rows of q and out (tokens past cu_new[n_req] are not touched).
  *   workspace    device, >= qg_attention_workspace_bytes(n_heads, n_kv_heads, head_dim) bytes,
  *                16-byte aligned, its first QG_ATTENTION_ZERO_BYTES bytes ZEROED by the caller
