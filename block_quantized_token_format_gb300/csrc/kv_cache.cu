@@ -232,7 +232,7 @@ __device__ __forceinline__ void quantize_block(const float (&x)[4], int lane, ui
     // x / d through the reciprocal where that cannot change the code (the quotient, within 2^-20
     // of the true one, is not that near to a half), by the division itself elsewhere.
     float t[4];
-    const float inv = __frcp_rn(d);
+    const float inv = d == 0.0f ? 0.0f : __frcp_rn(d);       // (a zero block, or a row that is not there, needs no division)
     bool close = !(fabsf(inv) < 1e30f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -467,18 +467,13 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
     }
 }
 
-// Sets of rows per warp: 2 KB of rows once that still leaves every SM 32 warps; below, one set, so
-// that a few tokens' heads run side by side.  A chunk of 8191 bf16 tokens takes 64 us with 2 KB,
-// 77 with 1 and 71 with 4; one of 4100 fp32 tokens with the store 40 with 2 KB, 44 with 4.
-template <typename T> constexpr int kSets = 8 / int(sizeof(T));
-template <typename T, int D>
-const void* heads_fn(bool wide, int* rows) {
-    *rows = 256 / D * (wide ? kSets<T> : 1);
-    return wide ? (const void*)&heads_kernel<D, T, kSets<T>> : (const void*)&heads_kernel<D, T, 1>;
+template <int D, typename T> const void* heads_fn(int sets) {
+    if constexpr (sizeof(T) == 2)
+        if (sets == 4) return (const void*)&heads_kernel<D, T, 4>;
+    return sets == 1 ? (const void*)&heads_kernel<D, T, 1> : (const void*)&heads_kernel<D, T, 2>;
 }
-
-template <typename T> const void* heads_fn(int D, bool wide, int* rows) {
-    return D == 64 ? heads_fn<T, 64>(wide, rows) : D == 128 ? heads_fn<T, 128>(wide, rows) : heads_fn<T, 256>(wide, rows);
+template <typename T> const void* heads_fn(int D, int sets) {
+    return D == 64 ? heads_fn<64, T>(sets) : D == 128 ? heads_fn<128, T>(sets) : heads_fn<256, T>(sets);
 }
 
 qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
@@ -489,11 +484,24 @@ qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
     a.wide_weight = aligned(a.q_weight, 16) && aligned(a.k_weight, 16);
     const long long heads = a.n_q + a.n_k + a.n_v;
     if (heads == 0 || a.n_tok == 0) return QG_OK;
-    const bool wide = a.n_tok * heads >= 4ll * 32 * sms;
-    int rows = 1;
-    const void* fn = act == QG_ACT_F32 ? heads_fn<float>(D, wide, &rows) : heads_fn<__nv_bfloat16>(D, wide, &rows);
-    const long long per_tok = (a.n_q + rows - 1) / rows + (a.n_k + rows - 1) / rows + (a.n_v + rows - 1) / rows;
-    const long long warps = a.n_tok * per_tok;
+    // Warps of a token when a warp takes so many sets.
+    auto warps_of = [&](int sets) {
+        const long long rows = 256 / D * sets;
+        return (a.n_q + rows - 1) / rows + (a.n_k + rows - 1) / rows + (a.n_v + rows - 1) / rows;
+    };
+    // More sets share a token's angles, weights and reductions, once there are enough warps without
+    // it, and where a kind's last warp does not idle too much of it (at most half as many sets
+    // again).  Norm and rotation of bf16 heads: with 1, 2 and 4 sets 64 + 8 heads of 128 take 4.9, 3.6
+    // and 3.9 us for 256 tokens, 60, 44 and 33 for 4096; 8 + 4 heads of 64 take 6.1, 5.4 and 7.0 for
+    // 4096.  fp32 and calls with a store have no registers for 4 (64 + 8 + 8 bf16 heads, 4096 tokens:
+    // 73, 53 and 55), and a store hides its latency with 64 warps an SM (48 + 16 + 16 heads of 64, 256
+    // tokens: 4.6 against 5.1 with two).
+    const long long enough = (a.data ? 64ll : 32ll) * sms;
+    const int most = act == QG_ACT_BF16 && !a.data ? 4 : 2;
+    int sets = 1;
+    while (sets < most && a.n_tok * warps_of(sets) > enough && 4 * sets * warps_of(2 * sets) <= 3 * warps_of(1)) sets *= 2;
+    const void* fn = act == QG_ACT_F32 ? heads_fn<float>(D, sets) : heads_fn<__nv_bfloat16>(D, sets);
+    const long long warps = a.n_tok * warps_of(sets);
     const int in_block = 4;
     const long long grid = (warps + in_block - 1) / in_block;
     if (warps > 0x7FFFFFFFll - 8) return QG_EUNSUPPORTED;
