@@ -16,6 +16,8 @@ namespace qg {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kMostSets = 4;            // of a call without a store (with one: 2)
+constexpr float kWhole = 12582912.0f;   // 1.5 * 2^23: adding it rounds a small number to a whole one
 constexpr int kMaxPageReq = 16384;      // requests of one qg_cache_pages call (two prefix arrays in shared memory)
 constexpr int kPageThreads = 512;       // most
 
@@ -212,8 +214,9 @@ template <int D, int S> __device__ __forceinline__ float square_sums(const float
     return __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], 1));
 }
 
-// Codes and scale of the block this lane's four values belong to (8 neighbouring lanes hold a block).
-__device__ __forceinline__ void quantize_block(const float (&x)[4], int lane, uint32_t (&code)[4], __half& scale) {
+// Levels (code - 8) and scale of the block this lane's four values belong to (8 neighbouring
+// lanes hold a block).
+__device__ __forceinline__ void quantize_block(const float (&x)[4], int lane, float (&level)[4], __half& scale) {
     float m = x[0];
     uint32_t top = __float_as_uint(x[0]) & 0x7FFFFFFFu;
 #pragma unroll
@@ -231,21 +234,20 @@ __device__ __forceinline__ void quantize_block(const float (&x)[4], int lane, ui
     const bool bad = !(all <= __float_as_uint(QG_CACHE_MAX)) || d == 0.0f;
     // x / d through the reciprocal where that cannot change the code (the quotient, within 2^-20
     // of the true one, is not that near to a half), by the division itself elsewhere.
-    float t[4];
     const float inv = d == 0.0f ? 0.0f : __frcp_rn(d);       // (a zero block, or a row that is not there, needs no division)
-    bool close = !(fabsf(inv) < 1e30f);
+    float off = fabsf(inv) < 1e30f ? 0.0f : 1.0f;        // the quotients' largest distance from a whole number
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        t[i] = x[i] * inv;
-        const float a = fabsf(t[i]);
-        close |= !(fabsf(a - floorf(a) - 0.5f) > 1e-5f);
+        const float t = __fmul_rn(x[i], inv);
+        level[i] = __fsub_rn(__fadd_rn(t, kWhole), kWhole);      // the nearest whole number (|t| is at most 8)
+        off = fmaxf(off, fabsf(__fsub_rn(t, level[i])));
     }
-    if (close) {
+    if (!(off < 0.49999f) && !bad) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = __fdiv_rn(x[i], d);
+        for (int i = 0; i < 4; ++i) level[i] = __fadd_rn(roundf(__fdiv_rn(x[i], d)), 0.0f);      // (no -0)
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) code[i] = bad ? 8u : uint32_t(min(max(int(roundf(t[i])) + 8, 0), 15));
+    for (int i = 0; i < 4; ++i) level[i] = bad ? 0.0f : fminf(level[i], 7.0f);
     scale = d == 0.0f ? __ushort_as_half(0u) : bad ? __ushort_as_half(0x7E00u) : __float2half_rn(float(__float2bfloat16_rn(d)));
 }
 
@@ -271,7 +273,8 @@ __device__ __forceinline__ void read_quad(const float* p, bool wide, float (&x)[
 // latency and instruction issue together.  With quads of neighbouring lanes exchanged for the
 // rotation and one row to a warp it was 115 instructions and 76 us; several tokens to a warp in a
 // loop made it 59 and the store below 46 instead of 40.  4100 tokens of 32 + 8 + 8 fp32 heads
-// with the store: 40 us, 5.2 TB/s.  At 4 tokens: 2.1 and 3.0 us, a launch and two latencies.
+// with the store: 39 us, 5.3 TB/s; a row stored costs about twice a row normed.  At 4 tokens: 2.1
+// and 2.9 us, a launch and two latencies.
 template <int D, typename T, int SETS>
 __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const HeadArgs a) {
     constexpr int L = D / 8, PER = 32 / L, ROWS = PER * SETS;
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[j][0][i] = x[j][1][i] = 0.0f;
     }
-    if (is_q || !a.data) {
+    if (SETS == kMostSets || is_q || !a.data) {
         T* const dst = (is_q ? static_cast<T*>(a.q_out) + tok * a.q_out_stride : static_cast<T*>(a.k_out) + tok * a.k_out_stride) +
                        (long long)(h0 + row) * D + ia;
 #pragma unroll
@@ -437,31 +440,38 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
     const long long page = slot < 0 ? 0 : slot >> 31 ? slot / a.page : uint32_t(slot) / uint32_t(a.page);
     const int in = slot >= 0 ? int(slot - page * a.page) : 0, t = in % kRecordTokens;
     T* const back = static_cast<T*>(is_v ? a.v_back : a.k_out);
+    // The lane's places in its first row's record, by quad; from set to set the record is PER heads on.
+    const long long per_head = (long long)(a.page / kRecordTokens) * kv_record_bytes(D);
+    uint8_t* rec = a.data + (page * a.n_k + h0 + row) * per_head + in / kRecordTokens * kv_record_bytes(D);
+    int codes_at[2], scale_at[2];
 #pragma unroll
-    for (int j = 0; j < SETS; ++j) {
+    for (int q = 0; q < 2; ++q) {
+        const int i0 = q ? ib : ia, g = i0 / 32, at = i0 % 32;
+        codes_at[q] = is_v ? kv_v_codes(D) + kv_value_half(D, t, at / 4, g) : kv_key_word(D, t, at / 8, g) + at % 8 / 2;
+        scale_at[q] = (is_v ? kv_v_scales(D) : kv_k_scales(D)) + kv_scale(D, t, g);
+    }
+#pragma unroll
+    for (int j = 0; j < SETS; ++j, rec += PER * per_head) {
         if (j * PER >= heads) break;                     // (the same for the whole warp)
-        const int h = h0 + j * PER + row;
         const bool there = j * PER + row < heads;
-        uint8_t* const rec = a.data + ((page * a.n_k + h) * (a.page / kRecordTokens) + in / kRecordTokens) * kv_record_bytes(D);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            uint32_t code[4];
+            float level[4];
             __half scale;
-            quantize_block(x[j][q], lane, code, scale);
-            const int i0 = q ? ib : ia, g = i0 / 32, at = i0 % 32;
+            quantize_block(x[j][q], lane, level, scale);
             if (there && slot >= 0) {
-                const uint16_t bits = uint16_t(code[0] | code[1] << 4 | code[2] << 8 | code[3] << 12);
-                uint8_t* const p = is_v ? rec + kv_v_codes(D) + kv_value_half(D, t, at / 4, g) : rec + kv_key_word(D, t, at / 8, g) + at % 8 / 2;
-                *reinterpret_cast<uint16_t*>(p) = bits;
-                if (at == 0)
-                    *reinterpret_cast<__half*>(rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + kv_scale(D, t, g)) = scale;
+                uint32_t c[4];                           // the codes are the last four bits
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__fadd_rn(level[i], kWhole + 8.0f)) & 15u;
+                *reinterpret_cast<uint16_t*>(rec + codes_at[q]) = uint16_t(c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12);
+                if (sub % 8 == 0) *reinterpret_cast<__half*>(rec + scale_at[q]) = scale;
             }
             if (there && back) {
                 const float d = __half2float(scale);
                 float y[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(float(int(code[i]) - 8), d);
-                store(back + (tok * a.n_k + h) * D + i0, y);
+                for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(level[i], d);
+                store(back + (tok * a.n_k + h0 + j * PER + row) * D + (q ? ib : ia), y);
             }
         }
     }
@@ -469,7 +479,7 @@ __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const Head
 
 template <int D, typename T> const void* heads_fn(int sets) {
     if constexpr (sizeof(T) == 2)
-        if (sets == 4) return (const void*)&heads_kernel<D, T, 4>;
+        if (sets == kMostSets) return (const void*)&heads_kernel<D, T, kMostSets>;
     return sets == 1 ? (const void*)&heads_kernel<D, T, 1> : (const void*)&heads_kernel<D, T, 2>;
 }
 template <typename T> const void* heads_fn(int D, int sets) {
@@ -497,7 +507,7 @@ qg_status launch_heads(HeadArgs& a, qg_act act, int D, void* stream) {
     // 73, 53 and 55), and a store hides its latency with 64 warps an SM (48 + 16 + 16 heads of 64, 256
     // tokens: 4.6 against 5.1 with two).
     const long long enough = (a.data ? 64ll : 32ll) * sms;
-    const int most = act == QG_ACT_BF16 && !a.data ? 4 : 2;
+    const int most = act == QG_ACT_BF16 && !a.data ? kMostSets : 2;
     int sets = 1;
     while (sets < most && a.n_tok * warps_of(sets) > enough && 4 * sets * warps_of(2 * sets) <= 3 * warps_of(1)) sets *= 2;
     const void* fn = act == QG_ACT_F32 ? heads_fn<float>(D, sets) : heads_fn<__nv_bfloat16>(D, sets);
