@@ -273,7 +273,7 @@ __device__ __forceinline__ void read_quad(const float* p, bool wide, float (&x)[
 // latency and instruction issue together.  With quads of neighbouring lanes exchanged for the
 // rotation and one row to a warp it was 115 instructions and 76 us; several tokens to a warp in a
 // loop made it 59 and the store below 46 instead of 40.  4100 tokens of 32 + 8 + 8 fp32 heads
-// with the store: 39 us, 5.3 TB/s; a row stored costs about twice a row normed.  At 4 tokens: 2.1
+// with the store: 39 us, 5.3 TB/s; a row stored takes about three times the instructions of one normed.  At 4 tokens: 2.1
 // and 2.9 us, a launch and two latencies.
 template <int D, typename T, int SETS>
 __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const HeadArgs a) {
