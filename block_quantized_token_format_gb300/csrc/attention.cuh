@@ -26,7 +26,8 @@
 //    multiplies the fp32 result.  A query is scaled by a power of two to [2^14, 2^15) and split
 //    into two fp16 terms (22 bits; one term is exact for bf16 queries).
 //  * outputs: a value is (16 + code) * d - 24 * d in one fp16 FMA, exact because d has 8
-//    significant bits; probabilities are two fp16 terms (one for bf16 outputs, below its
+//    significant bits (units with scales whose 24-fold fp16 does not hold take an addition and a
+//    product instead); probabilities are two fp16 terms (one for bf16 outputs, below its
 //    rounding), scaled by 2^7 relative to a reference that follows the running maximum within
 //    2^8, so that outputs are rescaled rarely and a probability counts down to 2^-31 of the
 //    row's largest.  Maxima, sums, outputs and joins are fp32.
@@ -200,15 +201,17 @@ template <bool COARSE> __device__ __forceinline__ void key_codes(uint32_t w, uin
 // The four value pairs of a word (nibble n of two tokens) times the tokens' scales d: with the
 // nibble in bits 6..9 under the exponent of 16, (16 + code) * d - 24 * d in one rounding, of
 // an exact result.  The mask and the exponent come in registers, so that one three-input
-// logic instruction places a pair.
-__device__ __forceinline__ void value_pairs(uint32_t w, uint32_t d, uint32_t mask, uint32_t magic, uint32_t (&v)[4]) {
-    const __half2 e = bits_h2(d), less = __hmul2(e, __float2half2_rn(-24.0f));
+// logic instruction places a pair.  24 * d is finite in fp16 for |d| <= 2720 (kFmaScale, blocks
+// of magnitudes up to 21760); LARGE is for any scale: (16 + code) - 24, then times d, both exact.
+constexpr uint32_t kFmaScale = 0x6950u;                  // 2720 in fp16
+template <bool LARGE> __device__ __forceinline__ void value_pairs(uint32_t w, uint32_t d, uint32_t mask, uint32_t magic, uint32_t (&v)[4]) {
+    const __half2 e = bits_h2(d), minus = __float2half2_rn(-24.0f), less = __hmul2(e, minus);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         const uint32_t t = n == 0 ? w << 6 : n == 1 ? w << 2 : n == 2 ? w >> 2 : w >> 6;
         uint32_t x;
         asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(t), "r"(mask), "r"(magic));
-        v[n] = h2_bits(__hfma2(bits_h2(x), e, less));
+        v[n] = h2_bits(LARGE ? __hmul2(__hadd2(bits_h2(x), minus), e) : __hfma2(bits_h2(x), e, less));
     }
 }
 // A value the compiler does not see through.
@@ -729,6 +732,17 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                     }
                 }
             }
+            // Whether any value scale of the unit's 32 NG (a lane looks at NG / 2 pairs) is above kFmaScale:
+            // its half of the sum reaches its top bit then.  The look and its branches cost 3.4% of 262,100 keys
+            // (65.2 -> 67.4 us) and 4% of a large batch (129.7 -> 134.9); LARGE in every unit costs 5 and 6%.
+            uint32_t above = 0;
+#pragma unroll
+            for (int i = 0; i < NG / 2; ++i) {
+                const int at = 32 * i + lane;
+                const uint32_t pair = lds32(stage + at / (8 * NG) * S::kRec + kv_v_scales(D) + at % (8 * NG) * 4);
+                above |= (pair & 0x7FFF7FFFu) + (0x7FFFu - kFmaScale) * 0x10001u;
+            }
+            const bool large = __any_sync(kFull, (above & 0x80008000u) != 0);
             const bool masked = key0 + kUnit - 1 > full_high || key0 <= full_low;
             uint32_t pb[S::kMats][TILES][2][2];            // probabilities as operand columns
             bool grow = false;
@@ -852,7 +866,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                 for (int i = 0; i < GI; ++i) {
                     uint32_t v[4][4];                      // [half][nibble]
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) value_pairs(w[k][i], d[k][i], mask, magic, v[k]);
+                    for (int k = 0; k < 4; ++k) value_pairs<false>(w[k][i], d[k][i], mask, magic, v[k]);
+                    if (large) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) value_pairs<true>(w[k][i], d[k][i], mask, magic, v[k]);
+                    }
 #pragma unroll
                     for (int n = 0; n < 4; n += 2) {
                         const uint4 a0 = make_uint4(v[0][n], v[0][n + 1], v[1][n], v[1][n + 1]);
