@@ -62,6 +62,7 @@ constexpr float kProbShift = 7.0f;        // probabilities are scaled by 2^7 ...
 constexpr float kRefSlack = 8.0f;         // ... and the reference follows the maximum within 2^8: below 2^15
 constexpr float kNoRef = -3.0e38f;        // the reference before the first visible key: any score is above it
 constexpr uint32_t kNoItem = 0xFFFFFFFFu;
+constexpr uint32_t kMostPlaces = 0x7FFFFFFFu;    // a call's work, in places (units and kItemCost an item), stays below
 constexpr int kMetaInts = 6;              // of an unfinished item: start, end, first token, new tokens, head, tile
 
 struct AttnArgs {
@@ -299,7 +300,7 @@ __device__ __forceinline__ uint32_t divide(uint32_t i, uint32_t d, uint32_t inv)
 }
 
 // A request's share of the work: its visible keys in units (from the first one a window
-// leaves) and its row tiles; 0 units for a request that does not fit the call.
+// leaves) and its row tiles.
 struct Request {
     int seq, first_tok, fresh, first_unit, units, tiles;
 };
@@ -409,9 +410,17 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         if (!ok || !fits || end == first) return 0;
         const Request q = request_of<ROWS>(a, seq, first, end);
         const unsigned long long n = (unsigned long long)(q.units + kItemCost) * unsigned(q.tiles) * unsigned(a.n_kv);
-        const bool numbered = n < 0x7FFFFFFFull / unsigned(a.n_req);       // the whole sequence stays below 2^31
-        bad_len |= !numbered;
-        return numbered ? uint32_t(n) : 0u;
+        bad_len |= n >= kMostPlaces;
+        return n < kMostPlaces ? uint32_t(n) : 0u;
+    };
+    // Sums of places stop at kMostPlaces, so a sequence that is too long shows in its total.
+    auto add = [](uint32_t x, uint32_t y) { return min(x + y, kMostPlaces); };
+    // Where it is: requests are taken in order, those that no longer fit are left out.
+    auto take = [&](uint32_t& used, uint32_t n) -> uint32_t {
+        const uint32_t at = used;
+        if (n < kMostPlaces - used) used += n;
+        else if (n > 0) bad_len = true;
+        return at;
     };
     if (lane < 2) meta[(2 * warp + lane) * kMetaInts] = kNoItem;
     if (a.n_req <= 32) {
@@ -421,10 +430,18 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const uint32_t up = __shfl_up_sync(kFull, run, d);
-            if (lane >= d) run += up;
+            if (lane >= d) run = add(run, up);
         }
-        if (lane < a.n_req) cum[lane] = run - n;
+        uint32_t at = run - n;
         run = __shfl_sync(kFull, run, 31);
+        if (run == kMostPlaces) {
+            run = 0;
+            for (int r = 0; r < a.n_req; ++r) {
+                const uint32_t before = take(run, __shfl_sync(kFull, n, r));
+                if (lane == r) at = before;
+            }
+        }
+        if (lane < a.n_req) cum[lane] = at;
         if (lane == 0) cum[a.n_req] = run;
         __syncwarp();
     } else {
@@ -435,7 +452,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
                 const uint32_t up = __shfl_up_sync(kFull, s, d);
-                if (lane >= d) s += up;
+                if (lane >= d) s = add(s, up);
             }
             if (lane == 31) wsum[tid >> 5] = s;
             __syncthreads();
@@ -443,11 +460,22 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 const uint32_t x = wsum[w];
-                if (w < (tid >> 5)) before += x;
-                run += x;
+                if (w < (tid >> 5)) before = add(before, x);
+                run = add(run, x);
             }
-            if (r < a.n_req) cum[r] = before + s - n;
+            if (r < a.n_req) cum[r] = add(before, s) - n;
             __syncthreads();
+        }
+        if (run == kMostPlaces) {                          // (the same for the whole CTA)
+            for (int r = tid; r < a.n_req; r += 32 * W) cum[r] = units_of(r);
+            __syncthreads();
+            if (tid == 0) {
+                run = 0;
+                for (int r = 0; r < a.n_req; ++r) cum[r] = take(run, cum[r]);
+                wsum[0] = run;
+            }
+            __syncthreads();
+            run = wsum[0];
         }
         if (tid == 0) cum[a.n_req] = run;
         __syncthreads();

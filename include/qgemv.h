@@ -463,7 +463,10 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
  *                16-byte aligned, its first QG_ATTENTION_ZERO_BYTES bytes ZEROED by the caller
  *                once; each call leaves them zeroed.  Calls that share one must be serialized.
  *                After QG_DEVICE_WAIT_TIMEOUT zero them again.
- *   n_req <= 1024, n_heads a multiple of n_kv_heads.
+ *   n_req <= 1024, n_heads a multiple of n_kv_heads.  A call's work, summed over requests, key/value
+ *   heads and tiles of 8 to 16 rows (4 for up to 4 fp32 rows) as visible keys / 32 + 4, is below 2^31:
+ *   requests are taken in order, and one that no longer fits sets QG_DEVICE_BAD_LENGTH, its rows of
+ *   out and lse are not written.
  * fp32 activations: queries and probabilities enter the tensor cores as two fp16 terms (22
  * bits; a probability counts down to 2^-31 of its row's largest), sums are fp32; bf16: queries
  * are exact, probabilities one fp16 term.  Outputs are the same on every run; the order of a sum

@@ -60,3 +60,101 @@ def test_large_values_stay_where_they_are_seen(act):
     want = np.zeros(tuple(big.shape), dtype=bool)
     want[1, 2:] = want[6, :2] = True
     assert np.array_equal(big.cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------------------------ the division of work
+
+def expect_row(c, tok, h):
+    """Output, its tolerance and the log-sum-exp of query head h of token tok (as Case.expect)."""
+    r = int(np.searchsorted(c.cu, tok, side="right")) - 1
+    s, j, hk = c.seq[r], tok - int(c.cu[r]), h // (c.heads // c.kv)
+    see = AO.visible(s, s, c.fresh[r], j, c.window)
+    if (r, hk) not in c.loaded:
+        c.loaded[r, hk] = AO.kv_load(c.pool.cpu().numpy(), c.slots[r], hk, c.page, c.kv, c.D)
+    K, V = c.loaded[r, hk]
+    d = np.abs(K).reshape(s, -1, 32).max(-1).repeat(32, -1) / 7.0
+    row = host(c.q)[tok, h]
+    o, l, p = AO.attention(row, K, V, see, c.scale)
+    ds = 2.0 ** -19 * abs(c.scale) * 23 * (d[see] @ np.abs(row)) + 2.0 ** -20
+    return o, (2 * ds.max() + 2.0 ** -19) * (p @ np.abs(V[see])) + 2.0 ** -32 * np.abs(V[see]).sum(0), l
+
+
+def test_a_long_chunk_in_a_large_batch():
+    """A chunk takes as much of a launch as it needs, whatever the number of requests beside it:
+    here 2.1 million places of work, more than 2^31 / 1024, beside 1023 single tokens."""
+    n = 1024
+    held, fresh = [5] * n, [1] * n
+    held[300], fresh[300] = 65600, 1024
+    c = Case(71, 64, 16, 2, held, fresh, page=64)
+    c.loaded = {}
+    got = host(c.run())
+    assert qg.qg_device_status() == 0
+    assert (2053 + 4) * (1024 * 8 // 16) * 2 > (1 << 31) // n
+    at = int(c.cu[300])
+    for tok in (0, 299, at, at + 1, at + 500, at + 1023, at + 1024, c.n_tok - 1):
+        for h in (0, 9, 15):
+            o, tol, _ = expect_row(c, tok, h)
+            assert np.all(np.abs(got[tok, h] - o) <= tol), (tok, h)
+
+
+def long_table(rows, width):
+    """Every page of every request is page 0: a cache of 65536 tokens stands for any length."""
+    return torch.zeros(rows, width, dtype=torch.int32, device=dev())
+
+
+class LongCase:
+    """One key/value head of 64 in a single page of 65536 tokens, which every entry of the tables names."""
+    D, PAGE = 64, 65536
+
+    def __init__(self, seed, rows):
+        self.rng = np.random.default_rng(seed)
+        pool = torch.zeros(qg.qg_cache_bytes(1, self.PAGE, 1, self.D), dtype=torch.uint8, device=dev())
+        self.pool, self.cache = pool, qg.qg_cache(pool, 1, self.PAGE, 1, self.D)
+        k, v = [torch.tensor(self.rng.standard_normal((self.PAGE, 1, self.D)).astype(np.float32), device=dev()) for _ in range(2)]
+        qg.qg_cache_append(self.cache, k, v, torch.arange(self.PAGE, device=dev()), norm=False)
+        self.q = torch.tensor(self.rng.standard_normal((rows, 1, self.D)).astype(np.float32), device=dev())
+        self.ws = torch.zeros(qg.qg_attention_workspace_bytes(1, 1, self.D), dtype=torch.uint8, device=dev())
+
+    def run(self, seq, cu, window=0, max_new=4):
+        out = torch.full_like(self.q, 7)
+        self.lse = torch.full((self.q.shape[0], 1), 7.0, device=dev())
+        qg.qg_attention(self.cache, self.q, long_table(len(seq), (max(seq) + self.PAGE - 1) // self.PAGE), ints(seq), ints(cu), out, self.ws,
+                        self.D ** -0.5, max_new=max_new, window=window, lse=self.lse)
+        return out
+
+    def check_row(self, got, tok, pos, window):
+        keys = np.arange(max(0, pos - window + 1), pos + 1, dtype=np.int64)
+        K, V = AO.kv_load(self.pool.cpu().numpy(), keys % self.PAGE, 0, self.PAGE, 1, self.D)
+        row = host(self.q)[tok, 0]
+        o, l, p = AO.attention(row, K, V, np.ones(len(keys), bool), self.D ** -0.5)
+        d = np.abs(K).reshape(len(keys), -1, 32).max(-1).repeat(32, -1) / 7.0
+        ds = 2.0 ** -19 * self.D ** -0.5 * 23 * (d @ np.abs(row)) + 2.0 ** -20
+        assert np.all(np.abs(host(got)[tok, 0] - o) <= (2 * ds.max() + 2.0 ** -19) * (p @ np.abs(V)) + 2.0 ** -32 * np.abs(V).sum(0)), (tok, pos)
+        assert abs(float(self.lse[tok, 0]) - l) <= ds.max() + 2.0 ** -20 * max(1.0, abs(l))
+
+
+def test_only_what_does_not_fit_a_launch_is_left_out():
+    """The work of a call is numbered with 31 bits: a request that no longer fits is reported and its
+    rows stay as they are; those before and after it are computed."""
+    last = (1 << 31) - 160                                   # (2^26 - 5 + 4) places a tile, 32 tiles of 4: 2^31 - 32
+    fresh = [1] * 8 + [128, 1, 2]
+    cu = np.concatenate([[0], np.cumsum(fresh)]).tolist()
+    seq = [10 * (i + 1) for i in range(8)] + [last, 33, 40]
+    c = LongCase(5, cu[-1])
+    got = c.run(seq, cu)
+    assert qg.qg_device_status() == qg.QG_DEVICE_BAD_LENGTH
+    assert bool((got[8:136] == 7).all()) and bool((c.lse[8:136] == 7).all())
+    for r in [0, 1, 7, 9, 10]:
+        for j in range(fresh[r]):
+            pos = seq[r] - fresh[r] + j
+            c.check_row(got, cu[r] + j, pos, pos + 1)
+    # The same in a batch of more requests than a warp has lanes.
+    fresh2, seq2 = [1] * 40 + fresh, [7] * 40 + seq
+    c2 = LongCase(6, 40 + cu[-1])
+    cu2 = np.concatenate([[0], np.cumsum(fresh2)]).tolist()
+    got = c2.run(seq2, cu2)
+    assert qg.qg_device_status(clear=True) == qg.QG_DEVICE_BAD_LENGTH
+    assert bool((got[48:176] == 7).all())
+    for tok, pos in ((0, 6), (39, 6), (40, 9), (176, 32), (178, 39)):
+        c2.check_row(got, tok, pos, pos + 1)
+    assert int(c.ws[:qg.QG_ATTENTION_ZERO_BYTES].max()) == 0 and int(c2.ws[:qg.QG_ATTENTION_ZERO_BYTES].max()) == 0
