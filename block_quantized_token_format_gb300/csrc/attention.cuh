@@ -399,7 +399,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
     // A request's units; its lengths go to shared memory for later decoding.
     auto units_of = [&](int r) -> uint32_t {
         const int seq = a.seq_len[r], first = a.cu_new[r], end = a.cu_new[r + 1];
-        const bool ok = seq >= 0 && first >= 0 && end >= first && end <= a.n_tok && !(a.span_mask && end - first > 32);
+        // (The new tokens are in the cache: with fewer tokens than those the positions would be negative.)
+        const bool ok = first >= 0 && end >= first && seq >= end - first && end <= a.n_tok && !(a.span_mask && end - first > 32);
         // Records beyond the table's row cannot be found: such a request is left out whole.
         const bool fits = ((long long)seq + kRecordTokens - 1) / kRecordTokens <= a.table_stride * a.page_records;
         bad_len |= !ok;

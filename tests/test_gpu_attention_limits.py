@@ -158,3 +158,17 @@ def test_only_what_does_not_fit_a_launch_is_left_out():
     for tok, pos in ((0, 6), (39, 6), (40, 9), (176, 32), (178, 39)):
         c2.check_row(got, tok, pos, pos + 1)
     assert int(c.ws[:qg.QG_ATTENTION_ZERO_BYTES].max()) == 0 and int(c2.ws[:qg.QG_ATTENTION_ZERO_BYTES].max()) == 0
+
+
+# ------------------------------------------------------------------------------------ lengths
+
+@pytest.mark.parametrize("window", [0, 5])
+def test_lengths_below_the_new_tokens_are_reported(window):
+    """A request cannot have fewer tokens in the cache than it adds: it is left out."""
+    c = Case(43, 128, 4, 2, [40, 20, 30], [3, 2, 1], page=16, window=window)
+    want = c.run()
+    for short in (0, 1, 2):
+        got = c.run(seq=ints([short, 22, 31]))
+        assert qg.qg_device_status() == qg.QG_DEVICE_BAD_LENGTH
+        assert bool((got[:3] == 7).all()) and torch.equal(got[3:], want[3:])
+    c.check(c.run())
