@@ -41,6 +41,8 @@
 // Around the loop a call costs about 11 us (launch, lengths, first copies; the joins).
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "kv_layout.h"
@@ -60,6 +62,7 @@ constexpr int kAttnGrid = 160;             // most CTAs of a launch (one per SM;
 static_assert(kAttnGrid * 4 <= QG_ATTENTION_ZERO_BYTES, "one ticket per CTA");
 constexpr float kProbShift = 7.0f;        // probabilities are scaled by 2^7 ...
 constexpr float kRefSlack = 8.0f;         // ... and the reference follows the maximum within 2^8: below 2^15
+constexpr float kFarRef = 4096.0f;        // above it the exponent's argument is rounded like the reference (below)
 constexpr float kNoRef = -3.0e38f;        // the reference before the first visible key: any score is above it
 constexpr uint32_t kNoItem = 0xFFFFFFFFu;
 constexpr uint32_t kMostPlaces = 0x7FFFFFFFu;    // a call's work, in places (units and kItemCost an item), stays below
@@ -671,6 +674,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 
         // Running outputs: of this lane's rows, value 4 r8 + n of block g.
         float o[TILES][4 * NG][H], ref[TILES][H], sum[TILES][H];
+        bool far = false;                                  // some row's reference is above kFarRef (the warp's)
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
 #pragma unroll
@@ -720,6 +724,15 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                     for (int i = 0; i < GI; ++i) kd[k][q * GI + i] = __byte_perm(d0[i], d1[i], (r8 & 1) ? 0x7632 : 0x5410);
                 }
             }
+            // Whether any value scale of the unit's 32 NG (a lane looks at NG / 2 pairs) is above kFmaScale:
+            // its half of the sum reaches its top bit then.
+            uint32_t above = 0;
+#pragma unroll
+            for (int i = 0; i < NG / 2; ++i) {
+                const int at = 32 * i + lane;
+                const uint32_t pair = lds32(stage + at / (8 * NG) * S::kRec + kv_v_scales(D) + at % (8 * NG) * 4);
+                above |= (pair & 0x7FFF7FFFu) + (0x7FFFu - kFmaScale) * 0x10001u;
+            }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 uint4 qb[TILES], ql[TILES];
@@ -761,17 +774,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                     }
                 }
             }
-            // Whether any value scale of the unit's 32 NG (a lane looks at NG / 2 pairs) is above kFmaScale:
-            // its half of the sum reaches its top bit then.  The look and its branches cost 3.4% of 262,100 keys
-            // (65.2 -> 67.4 us) and 4% of a large batch (129.7 -> 134.9); LARGE in every unit costs 5 and 6%.
-            uint32_t above = 0;
-#pragma unroll
-            for (int i = 0; i < NG / 2; ++i) {
-                const int at = 32 * i + lane;
-                const uint32_t pair = lds32(stage + at / (8 * NG) * S::kRec + kv_v_scales(D) + at % (8 * NG) * 4);
-                above |= (pair & 0x7FFF7FFFu) + (0x7FFFu - kFmaScale) * 0x10001u;
-            }
-            const bool large = __any_sync(kFull, (above & 0x80008000u) != 0);
             const bool masked = key0 + kUnit - 1 > full_high || key0 <= full_low;
             uint32_t pb[S::kMats][TILES][2][2];            // probabilities as operand columns
             bool grow = false;
@@ -794,32 +796,62 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                     m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-                    top[t][h] = m * factor[t][h];
-                    grow |= top[t][h] > ref[t][h] + kRefSlack;
+                    top[t][h] = __fmul_rn(m, factor[t][h]);
+                    grow |= __fsub_rn(top[t][h], ref[t][h]) > kRefSlack;
                 }
             }
-            // ---- running reference and sum
-            if (__any_sync(kFull, grow)) {
+            // ---- running reference and sum; what a unit seldom needs is behind one vote.  (Large values
+            // and far scores cost the units that have neither 3%: 262,100 keys 65.3 -> 67.2 us, a large
+            // batch 130 -> 134, a bf16 one 85.5 -> 88.3.  With a branch per block of values instead of a
+            // second body for them, and far scores behind a vote of their own, it was 5%.)
+            float base[TILES][H];
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                for (int h = 0; h < H; ++h) base[t][h] = kProbShift - ref[t][h];
+            bool large = false;
+            if (__any_sync(kFull, grow || far || (above & 0x80008000u) != 0)) {
+                large = __any_sync(kFull, (above & 0x80008000u) != 0);
+                far = false;
 #pragma unroll
                 for (int t = 0; t < TILES; ++t)
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         const float to = fmaxf(ref[t][h], top[t][h]), keep = exp2_fast(ref[t][h] - to);
                         ref[t][h] = to;
+                        base[t][h] = kProbShift - to;
+                        far |= fabsf(to) > kFarRef && to != kNoRef;
                         sum[t][h] *= keep;
 #pragma unroll
                         for (int n = 0; n < 4 * NG; ++n) o[t][n][h] *= keep;
                     }
+                // A reference is a rounded product, the fused argument below an exact one: by half a last bit
+                // of the reference apart (2^-12 at kFarRef, more than an exponent holds at 2^30).  Scores as
+                // large as that are rounded as the reference was and subtracted from it, which is exact.
+                far = __any_sync(kFull, far);
+                if (far) {
+#pragma unroll
+                    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    p[t][k][i][h] = __fsub_rn(__fmul_rn(p[t][k][i][h], factor[t][h]), ref[t][h]);
+                            factor[t][h] = 1.0f;
+                            base[t][h] = kProbShift;
+                        }
+                }
             }
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    const float base = kProbShift - ref[t][h];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) p[t][k][i][h] = exp2_fast(fmaf(p[t][k][i][h], factor[t][h], base));
+                        for (int i = 0; i < 2; ++i) p[t][k][i][h] = exp2_fast(fmaf(p[t][k][i][h], factor[t][h], base[t][h]));
                     sum[t][h] += (p[t][0][0][h] + p[t][0][1][h]) + (p[t][1][0][h] + p[t][1][1][h]);
                 }
                 // A key's row of operand columns is the transpose of what the product takes.  The
@@ -891,40 +923,40 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
                         }
                     }
                 }
+                auto products = [&](auto any_scale) {
 #pragma unroll
-                for (int i = 0; i < GI; ++i) {
-                    uint32_t v[4][4];                      // [half][nibble]
+                    for (int i = 0; i < GI; ++i) {
+                        uint32_t v[4][4];                      // [half][nibble]
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) value_pairs<false>(w[k][i], d[k][i], mask, magic, v[k]);
-                    if (large) {
+                        for (int k = 0; k < 4; ++k) value_pairs<decltype(any_scale)::value>(w[k][i], d[k][i], mask, magic, v[k]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) value_pairs<true>(w[k][i], d[k][i], mask, magic, v[k]);
-                    }
+                        for (int n = 0; n < 4; n += 2) {
+                            const uint4 a0 = make_uint4(v[0][n], v[0][n + 1], v[1][n], v[1][n + 1]);
+                            const uint4 a1 = make_uint4(v[2][n], v[2][n + 1], v[3][n], v[3][n + 1]);
 #pragma unroll
-                    for (int n = 0; n < 4; n += 2) {
-                        const uint4 a0 = make_uint4(v[0][n], v[0][n + 1], v[1][n], v[1][n + 1]);
-                        const uint4 a1 = make_uint4(v[2][n], v[2][n + 1], v[3][n], v[3][n + 1]);
+                            for (int t = 0; t < TILES; ++t) {
+                                float acc[4];
+                                mma_f16(acc, a0, pb[0][t][0][0], pb[0][t][0][1], 0.0f, 0.0f);
+                                mma_f16(acc, a1, pb[0][t][1][0], pb[0][t][1][1]);
+                                if (TERMS == kTwice) {
+                                    mma_f16(acc, a0, pb[S::kMats - 1][t][0][0], pb[S::kMats - 1][t][0][1]);
+                                    mma_f16(acc, a1, pb[S::kMats - 1][t][1][0], pb[S::kMats - 1][t][1][1]);
+                                }
+                                float(&x)[H] = o[t][4 * (q * GI + i) + n];
+                                float(&y)[H] = o[t][4 * (q * GI + i) + n + 1];
+                                if (TERMS == kSide) {
+                                    x[0] += acc[0] + acc[1];
+                                    y[0] += acc[2] + acc[3];
+                                } else {
 #pragma unroll
-                        for (int t = 0; t < TILES; ++t) {
-                            float acc[4];
-                            mma_f16(acc, a0, pb[0][t][0][0], pb[0][t][0][1], 0.0f, 0.0f);
-                            mma_f16(acc, a1, pb[0][t][1][0], pb[0][t][1][1]);
-                            if (TERMS == kTwice) {
-                                mma_f16(acc, a0, pb[S::kMats - 1][t][0][0], pb[S::kMats - 1][t][0][1]);
-                                mma_f16(acc, a1, pb[S::kMats - 1][t][1][0], pb[S::kMats - 1][t][1][1]);
-                            }
-                            float(&x)[H] = o[t][4 * (q * GI + i) + n];
-                            float(&y)[H] = o[t][4 * (q * GI + i) + n + 1];
-                            if (TERMS == kSide) {
-                                x[0] += acc[0] + acc[1];
-                                y[0] += acc[2] + acc[3];
-                            } else {
-#pragma unroll
-                                for (int h = 0; h < H; ++h) { x[h] += acc[h]; y[h] += acc[2 + h]; }
+                                    for (int h = 0; h < H; ++h) { x[h] += acc[h]; y[h] += acc[2 + h]; }
+                                }
                             }
                         }
                     }
-                }
+                };
+                if (large) products(std::true_type{});
+                else products(std::false_type{});
             }
             __syncwarp();                                   // every lane has read the stage
             ++consumed;

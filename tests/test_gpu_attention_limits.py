@@ -172,3 +172,51 @@ def test_lengths_below_the_new_tokens_are_reported(window):
         assert qg.qg_device_status() == qg.QG_DEVICE_BAD_LENGTH
         assert bool((got[:3] == 7).all()) and torch.equal(got[3:], want[3:])
     c.check(c.run())
+
+
+# ------------------------------------------------------------------------------------ scores
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("D,heads,new", [(64, 1, 1), (128, 2, 4), (128, 12, 1), (256, 3, 2)])
+@pytest.mark.parametrize("power", [12, 16, 22, 26, 27, 28, 30, 60, 100])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_far_apart(act, D, heads, new, power, sign):
+    """Scores that are whole multiples of 2^power, exact in every step: the keys with the largest share
+    the weight, all others have none (exp(-2^12) is 0 in any of the formats).  Error: two fp16 terms
+    of a probability and the sums, 2^-18 of the largest value; bf16: 2^-11 and the output's 2^-8."""
+    c = Case(power + D, D, heads, 1, [333, 2, 90], [new, 1, new], page=32, act=act, v_scale=1.0, scale=1.0)
+    c.k[:] = -8.0                                            # every block has the scale 1
+    c.k[:, :, 0] = c.rng.integers(-8, 8, c.k.shape[:2])
+    c.append()
+    c.q.zero_()
+    c.q[:, :, 0] = sign * 2.0 ** power
+    got = host(c.run())
+    want, _, lse, _ = c.expect()
+    assert np.all(np.isfinite(got))
+    assert np.abs(got - want).max() <= (2.0 ** -18 if act == "f32" else 2.0 ** -7) * np.abs(c.v).max()
+    gl = host(c.lse)[:c.n_tok]
+    assert np.all(np.abs(gl - lse) <= 2.0 ** -20 * np.abs(lse) + 2.0 ** -18)
+    assert qg.qg_device_status() == 0
+
+
+@pytest.mark.parametrize("q_scale", [1e3, 1e6, 3e7, 1e8, 1e9, 1e12])
+@pytest.mark.parametrize("spread", [0.0, 1e-4])
+def test_large_scores_weigh_no_more_than_one(q_scale, spread):
+    """Scores up to 10^13 that differ by a few of their own last bits (the keys are copies of one, but for
+    a small share): whatever the rounding, outputs are weighted means of the values."""
+    c = Case(57, 128, 6, 2, [700, 40], [2, 4], page=32, v_scale=1.0, scale=0.3, q_scale=q_scale)
+    c.k[:] = c.k[:1] + spread * c.k
+    c.append()
+    got = host(c.run())
+    V = AO.kv_load(c.pool.cpu().numpy(), np.concatenate(c.slots), 0, c.page, c.kv, c.D)[1]
+    V1 = AO.kv_load(c.pool.cpu().numpy(), np.concatenate(c.slots), 1, c.page, c.kv, c.D)[1]
+    top = max(np.abs(V).max(), np.abs(V1).max())
+    assert np.all(np.isfinite(got)) and np.abs(got).max() <= top * (1 + 2.0 ** -18)
+    if spread == 0.0:                                        # equal keys, equal scores: the plain mean of what a row sees
+        for r, (s, f) in enumerate(zip(c.seq, c.fresh)):
+            at = int(sum(c.seq[:r]))
+            for j in range(f):
+                n = s - f + j + 1
+                for h in range(6):
+                    want = (V, V1)[h // 3][at:at + n].mean(0)
+                    assert np.abs(got[int(c.cu[r]) + j, h] - want).max() <= 2.0 ** -18 * top
