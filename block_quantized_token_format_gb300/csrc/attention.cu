@@ -123,7 +123,7 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
     a.page_inv = a.page_records == 1 ? 0xFFFFFFFFu : uint32_t((uint64_t(1) << 32) / uint32_t(a.page_records));
     a.window = window;
     a.depth = depth;
-    a.scale_log2 = scale == 0.0f ? 1.0f : float(std::fabs(double(scale)) * 1.4426950408889634);
+    a.scale_log2 = float(std::frexp((scale == 0.0f ? 1.0 : std::fabs(double(scale))) * 1.4426950408889634, &a.scale_exp));
     a.scale_sign = scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f;
     a.wait_limit = wait_limit();
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);

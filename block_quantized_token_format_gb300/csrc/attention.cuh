@@ -81,7 +81,8 @@ struct AttnArgs {
     long long q_stride, out_stride, table_stride, n_tok, n_pages;
     int n_req, n_heads, n_kv, group, page_records, window, depth;
     uint32_t group_inv, page_inv;    // floor(2^32 / x) (of 1: 2^32 - 1)
-    float scale_log2;          // |scale| * log2(e) (1 where that is 0)
+    float scale_log2;          // |scale| * log2(e) is scale_log2 * 2^scale_exp, scale_log2 in [0.5, 1]
+    int scale_exp;             // (of a scale of 0: that of 1)
     float scale_sign;          // the scale's sign (0 for 0), which goes into the queries
     uint32_t wait_limit, drain_limit, test_extra_tx;
 };
@@ -106,7 +107,8 @@ template <int D, int TILES, int TERMS> struct AttnShape {
     // of up to 20000 keys took 42 us with 9 and 33 with 8 (bf16; fp32: 35 and 30).  Three tiles of
     // them leave room for 7.
     static constexpr int kWarps = D == 256 ? (kMats * TILES == 3 ? 7 : 8) : kMats * TILES == 1 ? 16 : 12;
-    static constexpr float kCodeUnit = TERMS == kOne ? 1.0f / 16777216.0f : 1.0f / 1048576.0f;    // what a code of 1 stands for
+    static constexpr int kCodeBits = TERMS == kOne ? 24 : 20;                    // a code of 1 stands for 2^-kCodeBits
+    static constexpr float kCodeUnit = 1.0f / (1 << kCodeBits);
     static constexpr float kOddScale = TERMS == kOne ? 0.0625f : 1.0f;
     static constexpr int kRec = kv_record_bytes(D);
     static constexpr int kStage = 2 * kRec;
@@ -612,10 +614,13 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
             // NaN or an infinity has NaN scores.
             const int e = int((__float_as_uint(top) & 0x7FFFFFFFu) >> 23);
             const int sh = min(141 - e, 126);
-            const float up = __uint_as_float(uint32_t(127 + sh) << 23) * a.scale_sign, down = __uint_as_float(uint32_t(127 - sh) << 23);
+            const float up = __uint_as_float(uint32_t(127 + sh) << 23) * a.scale_sign;
             const bool finite = e < 255;
             float* const init = reinterpret_cast<float*>(mine + lay.init_off) + t * (NG + 1) * 8;
-            if (c4 == 0) init[NG * 8 + r8] = finite ? a.scale_log2 * (1.0f / S::kCodeUnit) * down : __uint_as_float(0x7FFFFFFFu);
+            // The scores' factor in one step, so that no part of it leaves fp32's range; where the whole
+            // does, it stays positive and finite: a masked -infinity stays one and a zero a zero.
+            const float factor = fminf(fmaxf(ldexpf(a.scale_log2, a.scale_exp + S::kCodeBits - sh), 1.17549435e-38f), 3.40282347e38f);
+            if (c4 == 0) init[NG * 8 + r8] = finite ? factor : __uint_as_float(0x7FFFFFFFu);
             // The first of two terms is cut off at 11 bits, the second is the rest (kSide: in the odd column).
             const float rest = TERMS == kSide && (r8 & 1) ? 1.0f : 0.0f;
             const uint32_t minus = TERMS == kSide && (r8 & 1) ? 0x80000000u : 0u;

@@ -449,7 +449,8 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
  *   q            device act [n_tok][n_heads][head_dim], tokens q_stride elements apart;
  *   out          device act, likewise with out_stride.  16-byte aligned, strides a multiple of
  *                16 bytes.
- *   lse          device fp32 [n_tok][n_heads] (natural logarithm), or NULL.
+ *   lse          device fp32 [n_tok][n_heads] (natural logarithm), or NULL.  Of a row whose largest
+ *                |q| times |scale| is above 2^117 its magnitude may be too small.
  *   table        device int32 [n_req][table_stride], seq_len, cu_new: as qg_cache_pages leaves
  *                them.  Entries of pages past a request's tokens, or wholly before what its
  *                window leaves visible, are not used (such pages may have been given away).

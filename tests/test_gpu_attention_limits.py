@@ -220,3 +220,20 @@ def test_large_scores_weigh_no_more_than_one(q_scale, spread):
                 for h in range(6):
                     want = (V, V1)[h // 3][at:at + n].mean(0)
                     assert np.abs(got[int(c.cu[r]) + j, h] - want).max() <= 2.0 ** -18 * top
+
+
+@pytest.mark.parametrize("q_scale,scale", [(0.0, 1e-20), (0.0, 1.0), (0.0, 1e38), (1e-30, 1e-15), (1e-38, 1e-38), (1.0, 1e-38),
+                                           (1e-33, 1e33), (1e30, 1e-30), (1e-38, 3e38)])
+def test_scales_of_every_size(q_scale, scale):
+    """Masked units, rows of zeros and scales whose product with a query leaves fp32's range on the way."""
+    c = Case(61, 128, 6, 2, [90, 3, 0], [2, 1, 3], q_scale=q_scale, scale=scale)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_zero_scores_of_large_queries(act):
+    """Keys of zeros: every score is 0, however large a query times the scale is."""
+    c = Case(62, 128, 6, 2, [90, 3], [2, 1], q_scale=1e30, scale=1e10, act=act)
+    c.k[:] = 0
+    c.append()
+    c.check(c.run())
