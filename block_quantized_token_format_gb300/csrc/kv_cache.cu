@@ -615,7 +615,8 @@ qg_status qg_cache_pages(const int32_t* held, const int32_t* fresh, int n_req, i
     a.in_place = free_end && free_end == free_begin;
     const size_t smem = (2 * size_t(n_req) + 1) * sizeof(int32_t);
     const void* fn = (const void*)&cache_pages_kernel;
-    if (smem > 48 * 1024 && blocks_per_sm(fn, dev, optin, kPageThreads, smem) < 1) return QG_EUNSUPPORTED;
+    // (The kernel's own shared memory counts towards the 48 KB that need no opt-in.)
+    if (smem + kStaticSmemReserve > 48 * 1024 && blocks_per_sm(fn, dev, optin, kPageThreads, smem) < 1) return QG_EUNSUPPORTED;
     // CTAs of 256 threads, three to an SM, start and scan sooner than one of 512 (3.0 us against 3.5
     // at 48 tokens, 4.8 against 5.7 at 300,000).  Where 256 threads would scan in two rounds (300
     // requests: 4.3 us against 3.9), or a call in place, which has 8 CTAs, would take its tokens in

@@ -237,3 +237,36 @@ def test_zero_scores_of_large_queries(act):
     c.k[:] = 0
     c.append()
     c.check(c.run())
+
+
+# ------------------------------------------------------------------------------------ pages
+
+PAGES = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np
+from test_gpu_attention import AO, run_pages, qg
+for n in {sizes}:
+    rng = np.random.default_rng(n)
+    held, fresh = rng.integers(0, 40, n), rng.integers(0, 3, n)
+    table = np.full((n, 3), -1)
+    count = -(-held // 16)
+    for r in range(n):
+        table[r, :count[r]] = 100000 + 3 * r + np.arange(count[r])
+    free = rng.permutation(n + 5)
+    want = AO.cache_pages(held.tolist(), fresh.tolist(), free, 2, table, 16, int(fresh.sum()) + 1)
+    got = run_pages(held, fresh, free, table, 16, int(fresh.sum()) + 1, begin=2, in_place={in_place})
+    for w, g in zip(want, got):
+        assert np.array_equal(np.asarray(w).reshape(-1), g.reshape(-1)), n
+    assert qg.qg_device_status() == 0
+print("same")
+"""
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_of_every_number_of_requests(in_place):
+    """Where the prefix arrays and the kernel's own shared memory together pass 48 KB (in a process of its own:
+    a larger call before would raise the limit for the smaller ones)."""
+    code = PAGES.format(root=ROOT, tests=os.path.join(ROOT, "tests"), sizes=[6111, 6112, 6143, 6144, 16384], in_place=in_place)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
