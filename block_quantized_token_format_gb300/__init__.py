@@ -128,6 +128,7 @@ class qg_cache(ctypes.Structure):
             if need == 0 or data.numel() * data.element_size() < need or not data.is_contiguous():
                 raise ValueError("qg_cache: data must be a contiguous tensor of at least qg_cache_bytes() bytes")
         self.tensor, self.address = data, ctypes.addressof(self)
+        self.device = data.get_device() if hasattr(data, "numel") else -1
 
 
 def _ptr(t) -> int | None:
@@ -437,7 +438,8 @@ def qg_cache_append(cache: qg_cache, k, v, slots, q=None, q_out=None, positions=
     are) quantized into ``cache`` at ``slots`` (int64 ``[n_tok]``, -1 = none); queries go to
     ``q_out``.  ``k_back`` / ``v_back`` receive the values the cache now stands for."""
     st = (_calls or _bound()).cache_append(cache.address, k, v, slots, q, q_out, positions, cos_sin, q_weight, k_weight,
-                                           eps, norm, unit_offset, interleaved, k_back, v_back, stream)
+                                           eps, norm, unit_offset, interleaved, k_back, v_back, stream,
+                                           getattr(cache, "device", -1))
     if st != 0:
         raise QGError(st, "qg_cache_append")
 
@@ -454,7 +456,7 @@ def qg_attention(cache: qg_cache, q, table, seq_len, cu_new, out, workspace, sca
     bits per new token): a draft tree's visibility among the request's new tokens.
     ``workspace``: uint8, ``qg_attention_workspace_bytes``, zeroed once."""
     st = (_calls or _bound()).attention(cache.address, q, table, seq_len, cu_new, out, workspace, scale, max_new, window,
-                                        span_mask, lse, stream)
+                                        span_mask, lse, stream, getattr(cache, "device", -1))
     if st != 0:
         raise QGError(st, "qg_attention")
 

@@ -10,10 +10,9 @@
 #include <exception>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-
-
 
 #include "qgemv.h"
 
@@ -62,12 +61,21 @@ void* address(PyObject* o) {
     return p;
 }
 
+// Kernels are launched on the current device, so a call's tensors have to be there: looked up
+// at a call's first tensor (the interpreter's lock is held throughout), -1 before.
+int current_device = -1;
+void on_device(int device, const char* name) {
+    if (current_device < 0) current_device = c10::cuda::current_device();
+    if (device != current_device) refuse(PyExc_ValueError, name, "not on the current CUDA device");
+}
+
 // A contiguous CUDA tensor of one type with at least n entries (None gives null).
 template <typename T> T* typed(PyObject* o, at::ScalarType type, const char* name, int64_t n = 0) {
     const at::Tensor* t = tensor(o, name);
     if (!t) return nullptr;
     if (!t->is_cuda() || t->scalar_type() != type || !t->is_contiguous() || t->numel() < n)
         refuse(PyExc_ValueError, name, "a contiguous CUDA tensor of the documented type and size is needed");
+    on_device(t->device().index(), name);
     return static_cast<T*>(t->data_ptr());
 }
 int32_t* i32(PyObject* o, const char* name, int64_t n = 0) { return typed<int32_t>(o, at::kInt, name, n); }
@@ -85,6 +93,7 @@ Heads heads(PyObject* o, at::ScalarType type, const char* name) {
     if (t->dim() != 3 || !t->is_cuda() || t->scalar_type() != type || t->stride(2) != 1 ||
         (t->size(1) > 1 && t->stride(1) != t->size(2)))
         refuse(PyExc_ValueError, name, "a CUDA [n_tok, heads, head_dim] tensor of one type, heads contiguous, is needed");
+    on_device(t->device().index(), name);
     h.p = t->data_ptr();
     h.n = t->size(0);
     h.heads = t->size(1);
@@ -142,9 +151,12 @@ void* stream_of(PyObject* o) {
     if (PyErr_Occurred()) throw Refused{};
     return s;
 }
-const qg_cache& cache_at(PyObject* o) {
+// device: of the cache's tensor, -1 for one that is given by its address.
+const qg_cache& cache_at(PyObject* o, PyObject* device) {
     const qg_cache* const c = static_cast<const qg_cache*>(address(o));
     if (!c) refuse(PyExc_ValueError, "cache", "a qg_cache is needed");
+    const long long d = integer(device, "cache");
+    if (d >= 0) on_device(int(std::min<long long>(d, 1 << 30)), "cache");
     return *c;
 }
 
@@ -153,6 +165,7 @@ template <typename F> PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F f) {
         PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
         return nullptr;
     }
+    current_device = -1;
     try {
         return PyLong_FromLong(f());
     } catch (const Refused&) {
@@ -196,10 +209,10 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 }
 
 // cache address, k, v, slots, q, q_out, positions, cos_sin, q_weight, k_weight, eps, norm, unit_offset, interleaved,
-// k_back, v_back, stream
+// k_back, v_back, stream, cache device
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-    return guarded(n_args, 17, [&] {
-        const qg_cache& cache = cache_at(a[0]);
+    return guarded(n_args, 18, [&] {
+        const qg_cache& cache = cache_at(a[0], a[17]);
         const at::ScalarType type = act_type(a[1], "k");
         const Heads k = heads(a[1], type, "k"), v = heads(a[2], type, "v"), q = heads(a[4], type, "q"), qo = heads(a[5], type, "q_out");
         if (v.n != k.n || k.heads != cache.n_kv_heads || v.heads != k.heads || k.dim != cache.head_dim || v.dim != k.dim)
@@ -217,10 +230,10 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
-// cache address, q, table, seq_len, cu_new, out, workspace, scale, max_new, window, span_mask, lse, stream
+// cache address, q, table, seq_len, cu_new, out, workspace, scale, max_new, window, span_mask, lse, stream, cache device
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-    return guarded(n_args, 13, [&] {
-        const qg_cache& cache = cache_at(a[0]);
+    return guarded(n_args, 14, [&] {
+        const qg_cache& cache = cache_at(a[0], a[13]);
         const at::ScalarType type = act_type(a[1], "q");
         const Heads q = heads(a[1], type, "q"), out = heads(a[5], type, "out");
         if (!out.p || q.n != out.n || q.heads != out.heads || q.dim != cache.head_dim || out.dim != q.dim || q.heads > 65536)
@@ -229,6 +242,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const Table t = table(a[2], n_req);
         const at::Tensor* const ws = tensor(a[6], "workspace");
         if (ws && (!ws->is_cuda() || !ws->is_contiguous())) refuse(PyExc_ValueError, "workspace", "a contiguous CUDA tensor is needed");
+        if (ws) on_device(ws->device().index(), "workspace");
         return call_attention(&cache, act_of(type), q.p, q.stride, q.n, int(q.heads), t.p, t.width, i32(a[3], "seq_len"),
                             i32(a[4], "cu_new", n_req + 1), int(std::min<int64_t>(n_req, 1 << 30)), small(a[8], "max_new"),
                             small(a[9], "window"), reinterpret_cast<const uint32_t*>(i32(a[10], "span_mask", q.n)), real(a[7], "scale"),

@@ -270,3 +270,49 @@ def test_pages_of_every_number_of_requests(in_place):
     code = PAGES.format(root=ROOT, tests=os.path.join(ROOT, "tests"), sizes=[6111, 6112, 6143, 6144, 16384], in_place=in_place)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------------------------ tensors
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on another GPU; it has no memory, so nothing can be launched with it."""
+
+    @staticmethod
+    def __new__(cls, t):
+        return torch.Tensor._make_wrapper_subclass(cls, t.shape, strides=t.stride(), dtype=t.dtype,
+                                                   device=f"cuda:{torch.cuda.current_device() + 1}")
+
+    __torch_dispatch__ = None
+
+
+def test_tensors_of_another_device_are_refused():
+    """Kernels go to the current device: every tensor of a call has to be there."""
+    c = Case(63, 128, 4, 2, [40], [2], page=16)
+    cache = qg.qg_cache(c.pool, c.n_pages, 16, 2, 128)
+    n = c.seq[0]
+    f = lambda *s: torch.ones(*s, device=dev())  # noqa: E731
+    calls = [
+        (qg.qg_cache_pages, dict(held=ints([1]), fresh=ints([1]), free_pages=ints([0]), table=ints([0]).view(1, 1), seq_len=ints([0]),
+                                 cu_new=ints([0, 0]), slots=ints([0]).long(), positions=ints([0]), page_tokens=16, free_begin=ints([0]),
+                                 free_end=ints([0]))),
+        (qg.qg_qk_norm_rope, dict(q=c.q, k=c.q, q_out=f(2, 4, 128), k_out=f(2, 4, 128), positions=ints([0, 0]), cos_sin=f(4, 128),
+                                  q_weight=f(128), k_weight=f(128))),
+        (qg.qg_cache_append, dict(cache=cache, k=f(n, 2, 128), v=f(n, 2, 128), slots=torch.tensor(c.slots[0], device=dev()), q=f(n, 4, 128),
+                                  q_out=f(n, 4, 128), positions=ints([0] * n), cos_sin=f(4, 128), q_weight=f(128), k_weight=f(128),
+                                  k_back=f(n, 2, 128), v_back=f(n, 2, 128))),
+        (qg.qg_attention, dict(cache=cache, q=c.q, table=ints(c.table.ravel()).view(c.table.shape), seq_len=ints(c.seq), cu_new=ints(c.cu),
+                               out=f(2, 4, 128), workspace=torch.zeros(qg.qg_attention_workspace_bytes(4, 2, 128), dtype=torch.uint8, device=dev()),
+                               scale=0.1, span_mask=ints([1, 3]), lse=f(2, 4)))]
+    for call, good in calls:
+        call(**good)
+        for name, t in good.items():
+            if torch.is_tensor(t):
+                with pytest.raises(ValueError, match=f"{name}: not on the current CUDA device"):
+                    call(**{**good, name: Elsewhere(t)})
+        if "cache" in good:
+            other = qg.qg_cache(c.pool, c.n_pages, 16, 2, 128)
+            other.device += 1                                # as if its tensor were there
+            with pytest.raises(ValueError, match="cache: not on the current CUDA device"):
+                call(**{**good, "cache": other})
+            call(**{**good, "cache": qg.qg_cache(c.pool.data_ptr(), c.n_pages, 16, 2, 128)})
+    assert qg.qg_device_status() == 0
