@@ -121,8 +121,12 @@ __global__ void __launch_bounds__(kPageThreads) cache_pages_kernel(const PageArg
                 if (page < 0) atomicOr(a.status, kStatusBadPage);
             } else {
                 const long long i = begin + off[lo] + (pg - have);
-                if (begin >= 0 && i < a.n_free) page = a.free_pages[i];
-                else atomicOr(a.status, kStatusNoPages);
+                if (begin < 0 || i >= a.n_free) {
+                    atomicOr(a.status, kStatusNoPages);
+                } else {
+                    page = a.free_pages[i];
+                    if (page < 0) atomicOr(a.status, kStatusBadPage);
+                }
                 if (in == 0) *entry = page;
             }
             if (page >= 0) slot = (long long)page * a.page + in;

@@ -272,6 +272,15 @@ def test_pages_of_every_number_of_requests(in_place):
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_free_page_that_is_none_is_reported(in_place):
+    """A negative number in the list of free pages: its tokens have no slot, and the status says so."""
+    t, seq, cu, slots, pos, end = run_pages([0, 3], [20, 2], [5, -1, 6], [[-1, -1], [9, -1]], 16, 22, begin=0, in_place=in_place)
+    assert qg.qg_device_status() == qg.QG_DEVICE_BAD_PAGE
+    assert slots[:16].tolist() == list(range(80, 96)) and (slots[16:20] == -1).all() and slots[20:].tolist() == [147, 148]
+    assert cu.tolist() == [0, 20, 22] and seq.tolist() == [20, 5] and end[0] == 2
+
+
 # ------------------------------------------------------------------------------------ tensors
 
 class Elsewhere(torch.Tensor):
