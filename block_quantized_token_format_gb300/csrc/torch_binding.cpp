@@ -98,7 +98,7 @@ Heads heads(PyObject* o, at::ScalarType type, const char* name) {
     h.n = t->size(0);
     h.heads = t->size(1);
     h.dim = t->size(2);
-    h.stride = h.n > 1 ? t->stride(0) : std::max<int64_t>(t->stride(0), h.heads * h.dim);
+    h.stride = h.n > 1 ? t->stride(0) : h.heads * h.dim;      // (of one token it means nothing)
     return h;
 }
 at::ScalarType act_type(PyObject* o, const char* name) {

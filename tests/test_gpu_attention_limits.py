@@ -325,3 +325,30 @@ def test_tensors_of_another_device_are_refused():
                 call(**{**good, "cache": other})
             call(**{**good, "cache": qg.qg_cache(c.pool.data_ptr(), c.n_pages, 16, 2, 128)})
     assert qg.qg_device_status() == 0
+
+
+def test_one_token_may_have_any_stride():
+    """The distance of the next token means nothing where there is none."""
+    c = Case(67, 128, 4, 2, [50], [1], page=16)
+    want = c.run()
+    for extra in (1, 2, 130):
+        wide = torch.zeros(1, 4 * 128 + extra, device=dev())
+        wide[:, :512] = c.q.view(1, 512)
+        q = wide.as_strided((1, 4, 128), (4 * 128 + extra, 128, 1))
+        assert torch.equal(c.run(q=q), want)
+        out = torch.zeros(1, 4 * 128 + extra, device=dev()).as_strided((1, 4, 128), (4 * 128 + extra, 128, 1))
+        assert torch.equal(c.run(out=out), want)
+        k0, k1 = torch.empty_like(c.q), torch.empty_like(c.q)
+        qg.qg_qk_norm_rope(q, q, k0, k1)
+        a0, a1 = torch.empty_like(c.q), torch.empty_like(c.q)
+        qg.qg_qk_norm_rope(c.q, c.q, a0, a1)
+        assert torch.equal(k0, a0) and torch.equal(k1, a1)
+
+
+def test_one_token_as_a_bf16_row():
+    c = Case(67, 64, 2, 1, [50], [1], page=16, act="bf16")
+    want = c.run()
+    wide = torch.zeros(1, 2 * 64 + 3, device=dev(), dtype=torch.bfloat16)
+    q = wide.as_strided((1, 2, 64), (131, 64, 1))
+    q.copy_(c.q)
+    assert torch.equal(c.run(q=q), want)
