@@ -532,6 +532,12 @@ qg_status check_rows(const void* p, int64_t stride, int64_t heads, int D, qg_act
     return aligned(p, 16) && stride * size % 16 == 0 ? QG_OK : QG_EALIGN;
 }
 
+// Rows written over the rows they are made of need the same places: at another stride they would
+// cover rows that other warps have yet to read.
+bool in_place_ok(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int64_t n_tok) {
+    return in != out || in_stride == out_stride || n_tok <= 1;
+}
+
 qg_status check_heads(qg_act act, int64_t n_tok, int n_heads, int n_kv, int D, const float* qw, const float* kw,
                       float eps, unsigned flags, const float* cos_sin, int64_t n_pos, int rot,
                       const int32_t* positions) {
@@ -645,10 +651,12 @@ qg_status qg_qk_norm_rope(qg_act act, const void* q, int64_t q_stride, const voi
     if (n_tok > 0 && n_heads > 0) {
         if ((st = check_rows(q, q_stride, n_heads, head_dim, act)) != QG_OK) return st;
         if ((st = check_rows(q_out, q_out_stride, n_heads, head_dim, act)) != QG_OK) return st;
+        if (!in_place_ok(q, q_stride, q_out, q_out_stride, n_tok)) return QG_EINVAL;
     }
     if (n_tok > 0 && n_kv_heads > 0) {
         if ((st = check_rows(k, k_stride, n_kv_heads, head_dim, act)) != QG_OK) return st;
         if ((st = check_rows(k_out, k_out_stride, n_kv_heads, head_dim, act)) != QG_OK) return st;
+        if (!in_place_ok(k, k_stride, k_out, k_out_stride, n_tok)) return QG_EINVAL;
     }
     HeadArgs a{};
     a.q = q;
@@ -690,9 +698,12 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
         if (n_heads > 0) {
             if ((st = check_rows(q, q_stride, n_heads, D, act)) != QG_OK) return st;
             if ((st = check_rows(q_out, q_out_stride, n_heads, D, act)) != QG_OK) return st;
+            if (!in_place_ok(q, q_stride, q_out, q_out_stride, n_tok)) return QG_EINVAL;
         }
         if ((st = check_rows(k, k_stride, n_kv, D, act)) != QG_OK) return st;
         if ((st = check_rows(v, v_stride, n_kv, D, act)) != QG_OK) return st;
+        const int64_t row = int64_t(n_kv) * D;
+        if (!in_place_ok(k, k_stride, k_back, row, n_tok) || !in_place_ok(v, v_stride, v_back, row, n_tok)) return QG_EINVAL;
     }
     HeadArgs a{};
     a.q = q;

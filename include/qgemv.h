@@ -402,7 +402,8 @@ qg_status qg_cache_pages(const int32_t* held, const int32_t* fresh, int n_req, i
  *   q, k         device act [n_tok][heads][head_dim], tokens q_stride / k_stride elements
  *                apart (the slices of one projection's row may be passed as they are); q_out,
  *                k_out likewise.  16-byte aligned, strides a multiple of 16 bytes.  In place
- *                (q_out = q) is allowed.  n_heads or n_kv_heads may be 0 (its pointers unused).
+ *                (q_out = q) is allowed with q's stride; other than that outputs and inputs do
+ *                not overlap.  n_heads or n_kv_heads may be 0 (its pointers unused).
  *   q_weight,    device fp32 [head_dim], NULL for ones; QG_NORM_UNIT_OFFSET: the weight is
  *   k_weight     1 + w.  QG_NORM_NONE: no norm (y = x; weights and eps unused).
  *   cos_sin      device fp32 [n_pos][rot_dim], row p: the cosines c_i, then the sines s_i of

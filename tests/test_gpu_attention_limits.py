@@ -352,3 +352,23 @@ def test_one_token_as_a_bf16_row():
     q = wide.as_strided((1, 2, 64), (131, 64, 1))
     q.copy_(c.q)
     assert torch.equal(c.run(q=q), want)
+
+
+def test_append_over_its_inputs():
+    """What the cache now holds, written over the keys and values it was made of."""
+    rng = np.random.default_rng(68)
+    x = heads_input(rng, 40, 4, 2, 64, "f32", hv=2)
+    q, k, v = [t.contiguous() for t in (x[:, :4], x[:, 4:6], x[:, 6:])]
+    slots, pos, cs = torch.arange(40, device=dev()), ints(range(40)), torch.tensor(rotation(rng, 40, 64), device=dev())
+    pools, outs = [], []
+    for over in (False, True):
+        pool = torch.zeros(AO.pool_bytes(3, 16, 2, 64), dtype=torch.uint8, device=dev())
+        qq, kk, vv = q.clone(), k.clone(), v.clone()
+        qo, kb, vb = (qq, kk, vv) if over else [torch.empty_like(t) for t in (qq, kk, vv)]
+        qg.qg_cache_append(qg.qg_cache(pool, 3, 16, 2, 64), kk, vv, slots, q=qq, q_out=qo, positions=pos, cos_sin=cs, k_back=kb, v_back=vb)
+        pools.append(pool)
+        outs.append((qo, kb, vb))
+    assert torch.equal(*pools) and all(torch.equal(a, b) for a, b in zip(*outs))
+    wide = torch.randn(4, 6, 128, device=dev())
+    with pytest.raises(qg.QGError):                          # the same first row, tokens at another distance
+        qg.qg_qk_norm_rope(wide[:, :4], wide[:, 4:], wide.view(-1)[:4 * 4 * 128].view(4, 4, 128), torch.empty(4, 2, 128, device=dev()))
