@@ -510,7 +510,9 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
         const uint32_t base = 2 * uint32_t(it.rq.first_unit + it.unit);
         uint32_t rec = lane < 2 * next_count ? base + lane : base;
         if (rec * kRecordTokens >= unsigned(it.rq.seq)) rec &= ~1u;
-        if (a.window > 0 && int(rec * kRecordTokens) + kRecordTokens <= it.rq.seq - it.rq.fresh + 1 - a.window) rec |= 1u;
+        // (Records end at 2^31 at most: past int.)
+        const int visible = a.window > 0 ? max(0, it.rq.seq - it.rq.fresh + 1 - a.window) : 0;
+        if ((rec + 1) * kRecordTokens <= unsigned(visible)) rec |= 1u;
         const uint32_t page = divide(rec, uint32_t(a.page_records), a.page_inv);
         next_rec = uint32_t(it.head) * uint32_t(a.page_records) + (rec - page * uint32_t(a.page_records));
         next_page = it.rq.seq > 0 ? a.table[(long long)ar * a.table_stride + page] : 0;
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, TILES, TERMS>::kWarps, 1) at
 
         const uint32_t item_end = min(it.end, u1);
         int key0 = (it.rq.first_unit + it.unit) * kUnit;
-        for (; u < item_end; ++u, key0 += kUnit) {
+        for (; u < item_end; ++u, key0 = int(unsigned(key0) + kUnit)) {      // (past int after the last unit of 2^31 - 1 keys)
             const uint32_t stage = ring + out_stage * S::kStage;
             if (!__all_sync(kFull, mbar_try_wait(bars + 8 * out_stage, out_phase))) {
                 if (!dead) dead = __any_sync(kFull, !mbar_wait(bars + 8 * out_stage, out_phase, a.wait_limit));

@@ -174,6 +174,20 @@ def test_lengths_below_the_new_tokens_are_reported(window):
     c.check(c.run())
 
 
+def test_lengths_near_the_end_of_32_bits():
+    """Positions up to 2^31 - 2 through a table whose entries all name one page; windows up to 2^31 - 1."""
+    for last in ((1 << 31) - 1, (1 << 31) - 2, (1 << 31) - 16, (1 << 31) - 17, (1 << 31) - 33):
+        c = LongCase(last % 97, 5)
+        got = c.run([last, 900], [0, 3, 5], window=100)
+        assert qg.qg_device_status() == 0
+        for tok, pos in ((0, last - 3), (1, last - 2), (2, last - 1), (3, 898), (4, 899)):
+            c.check_row(got, tok, pos, 100)
+    got = c.run([700, 900], [0, 3, 5], window=(1 << 31) - 1)
+    assert qg.qg_device_status() == 0
+    for tok, pos in ((0, 697), (1, 698), (2, 699), (3, 898), (4, 899)):
+        c.check_row(got, tok, pos, (1 << 31) - 1)
+
+
 # ------------------------------------------------------------------------------------ scores
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
