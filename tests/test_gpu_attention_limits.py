@@ -386,3 +386,43 @@ def test_append_over_its_inputs():
     wide = torch.randn(4, 6, 128, device=dev())
     with pytest.raises(qg.QGError):                          # the same first row, tokens at another distance
         qg.qg_qk_norm_rope(wide[:, :4], wide[:, 4:], wide.view(-1)[:4 * 4 * 128].view(4, 4, 128), torch.empty(4, 2, 128, device=dev()))
+
+
+# ------------------------------------------------------------------------------------ branches that other tests do not reach
+
+@pytest.mark.parametrize("n,hq,hk,D,rot,act,norm", [
+    (3, 2, 1, 64, 48, "f32", True), (40, 6, 2, 128, 96, "f32", True), (5, 3, 3, 128, 112, "bf16", True), (7, 2, 1, 256, 144, "f32", False),
+    (2000, 9, 2, 128, 80, "bf16", True), (900, 21, 3, 256, 240, "f32", True), (1500, 12, 4, 64, 48, "bf16", True)])
+def test_rotation_of_more_than_half_the_head(n, hq, hk, D, rot, act, norm):
+    """Half-split pairs that lie in two lanes and in both halves of the row; the append computes the same bits."""
+    rng = np.random.default_rng(n + rot)
+    x = heads_input(rng, n, hq, hk, D, act, hv=hk)
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    cs, pos = rotation(rng, 50, rot), rng.integers(0, 50, n)
+    w = (1 + 0.3 * rng.standard_normal(D)).astype(np.float32)
+    up = lambda a: torch.tensor(a, device=dev())  # noqa: E731
+    qo, ko = torch.full_like(q, 7).contiguous(), torch.full_like(k, 7).contiguous()
+    qg.qg_qk_norm_rope(q, k, qo, ko, ints(pos), up(cs), up(w), up(w), 1e-5, norm)
+    page = 16
+    pool = torch.zeros(AO.pool_bytes(-(-n // page), page, hk, D), dtype=torch.uint8, device=dev())
+    qa, kb = torch.full_like(qo, 7), torch.full_like(ko, 7)
+    qg.qg_cache_append(qg.qg_cache(pool, -(-n // page), page, hk, D), k, v, torch.arange(n, device=dev()), q=q, q_out=qa, positions=ints(pos),
+                       cos_sin=up(cs), q_weight=up(w), k_weight=up(w), eps=1e-5, norm=norm, k_back=kb)
+    for src, out in ((q, qo), (k, ko)):
+        want = AO.norm_rope32(src.float().cpu().numpy(), w, 1e-5, pos, cs, norm=norm)
+        assert torch.equal(out.cpu(), torch.tensor(want).to(x.dtype))
+    assert torch.equal(qa, qo)
+    few = slice(0, 40)
+    want = AO.kv_values(*AO.kv_blocks(AO.norm_rope32(k[few].float().cpu().numpy(), w, 1e-5, pos[few], cs, norm=norm)))
+    assert torch.equal(kb[few].cpu(), torch.tensor(want.astype(np.float32)).to(x.dtype))
+    assert qg.qg_device_status() == 0
+
+
+@pytest.mark.parametrize("D,heads,new,act", [(256, 4, 3, "f32"), (256, 2, 4, "f32"), (256, 16, 1, "bf16"), (128, 12, 1, "f32")])
+def test_lists_of_requests_that_leave_room_for_fewer_rows(D, heads, new, act):
+    """1024 requests' lengths in shared memory: a shallower ring, or a tile of fewer rows."""
+    rng = np.random.default_rng(D + new)
+    held, fresh = rng.integers(0, 6, 1024), rng.integers(0, new + 1, 1024)
+    held[500], fresh[3] = 200, new
+    c = Case(D, D, heads, 1, held.tolist(), fresh.tolist(), page=16, act=act)
+    c.check(c.run())
