@@ -372,7 +372,7 @@ size_t qg_cache_bytes(int64_t n_pages, int page_tokens, int n_kv_heads, int head
 
 /* qg_cache_pages: block table, slots and positions of a step's new tokens.
  *   held, fresh  device int32 [n_req]: tokens a request has in the cache, tokens it adds.
- *   free_pages   device int32 [n_free]: pages to deal; free_begin: device int32, the first
+ *   free_pages   device int32 [n_free]: pages to deal (a negative one: QG_DEVICE_BAD_PAGE); free_begin: device int32, the first
  *                one not dealt yet, or NULL for 0; free_end: device int32, receives the one
  *                after the last dealt (may be free_begin itself), or NULL.
  *   table        device int32 [n_req][table_stride]: page i of a request's tokens; the first
@@ -430,7 +430,8 @@ qg_status qg_qk_norm_rope(qg_act act, const void* q, int64_t q_stride, const voi
  *   k_back,      device act [n_tok][n_kv_heads][head_dim], contiguous, 16-byte aligned, or
  *   v_back       NULL: what the cache now holds for these tokens, as values (a caller that
  *                attends within a prompt chunk then sees what later steps will read).
- *   cos_sin NULL: no rotation, positions may be NULL.  Other arguments as in qg_qk_norm_rope. */
+ *   cos_sin NULL: no rotation, positions may be NULL.  A token whose position is negative or not
+ *   below n_pos is stored as zeros where its slot is valid.  Other arguments as in qg_qk_norm_rope. */
 qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int64_t q_stride, const void* k,
                           int64_t k_stride, const void* v, int64_t v_stride, int64_t n_tok, int n_heads,
                           const float* q_weight, const float* k_weight, float eps, unsigned int flags,
@@ -465,13 +466,15 @@ qg_status qg_cache_append(const qg_cache* cache, qg_act act, const void* q, int6
  *                16-byte aligned, its first QG_ATTENTION_ZERO_BYTES bytes ZEROED by the caller
  *                once; each call leaves them zeroed.  Calls that share one must be serialized.
  *                After QG_DEVICE_WAIT_TIMEOUT zero them again.
- *   n_req <= 1024, n_heads a multiple of n_kv_heads.  A call's work, summed over requests, key/value
+ *   n_req <= 1024 (qg_cache_pages takes more: attend them in several calls, table, seq_len and
+ *   cu_new advanced, q and out as they are), n_heads a multiple of n_kv_heads.  A call's work, summed over requests, key/value
  *   heads and tiles of 8 to 16 rows (4 for up to 4 fp32 rows) as visible keys / 32 + 4, is below 2^31:
  *   requests are taken in order, and one that no longer fits sets QG_DEVICE_BAD_LENGTH, its rows of
  *   out and lse are not written.
  * fp32 activations: queries and probabilities enter the tensor cores as two fp16 terms (22
  * bits; a probability counts down to 2^-31 of its row's largest), sums are fp32; bf16: queries
- * are exact, probabilities one fp16 term.  Outputs are the same on every run; the order of a sum
+ * are exact, probabilities one fp16 term (11 bits), and a block's part of a score has 20 bits of
+ * its largest product, which lse shares although it is fp32.  Outputs are the same on every run; the order of a sum
  * depends on the lengths of the whole batch and on the GPU's number of SMs. */
 #define QG_ATTENTION_ZERO_BYTES 4096
 size_t    qg_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim);

@@ -160,6 +160,20 @@ def test_only_what_does_not_fit_a_launch_is_left_out():
     assert int(c.ws[:qg.QG_ATTENTION_ZERO_BYTES].max()) == 0 and int(c2.ws[:qg.QG_ATTENTION_ZERO_BYTES].max()) == 0
 
 
+def test_more_requests_than_a_call_takes():
+    """A batch in several calls: table, lengths and offsets advanced, queries and outputs as they are."""
+    rng = np.random.default_rng(72)
+    n = 1500
+    c = Case(72, 64, 2, 1, rng.integers(0, 20, n).tolist(), rng.integers(0, 3, n).tolist(), page=16)
+    cache = qg.qg_cache(c.pool, c.n_pages, 16, 1, 64)
+    table, seq, cu = ints(c.table.ravel()).view(c.table.shape), ints(c.seq), ints(c.cu)
+    out, c.lse = torch.full_like(c.q, 7), torch.full((c.n_tok, 2), 7.0, device=dev())
+    c.ws = torch.zeros(qg.qg_attention_workspace_bytes(2, 1, 64), dtype=torch.uint8, device=dev())
+    for r0, r1 in ((0, 1024), (1024, n)):
+        qg.qg_attention(cache, c.q, table[r0:r1], seq[r0:r1], cu[r0:r1 + 1], out, c.ws, c.scale, max_new=2, lse=c.lse)
+    c.check(out)
+
+
 # ------------------------------------------------------------------------------------ lengths
 
 @pytest.mark.parametrize("window", [0, 5])
@@ -386,6 +400,23 @@ def test_append_over_its_inputs():
     wide = torch.randn(4, 6, 128, device=dev())
     with pytest.raises(qg.QGError):                          # the same first row, tokens at another distance
         qg.qg_qk_norm_rope(wide[:, :4], wide[:, 4:], wide.view(-1)[:4 * 4 * 128].view(4, 4, 128), torch.empty(4, 2, 128, device=dev()))
+
+
+def test_append_of_positions_that_are_none():
+    """A negative position, or one past the table of angles, stores zeros; the latter is reported."""
+    rng = np.random.default_rng(69)
+    x = heads_input(rng, 3, 0, 1, 64, "f32", hv=1)
+    cs = torch.tensor(rotation(rng, 10, 64), device=dev())
+    for bad, status in ((-1, 0), (10, qg.QG_DEVICE_BAD_LENGTH)):
+        pool = torch.full((AO.pool_bytes(1, 16, 1, 64),), 0xFF, dtype=torch.uint8, device=dev())
+        kb, vb = [torch.full((3, 1, 64), 7.0, device=dev()) for _ in range(2)]
+        qg.qg_cache_append(qg.qg_cache(pool, 1, 16, 1, 64), x[:, :1], x[:, 1:], torch.arange(3, device=dev()), positions=ints([4, bad, 9]),
+                           cos_sin=cs, k_back=kb, v_back=vb)
+        assert qg.qg_device_status() == status
+        K, V = AO.kv_load(pool.cpu().numpy(), [0, 1, 2], 0, 16, 1, 64)
+        assert not K[1].any() and not V[1].any() and K[[0, 2]].any(1).all() and np.isfinite(K).all() and np.isfinite(V).all()
+        assert not bool(kb[1].any()) and not bool(vb[1].any())
+        assert np.array_equal(host(kb)[:, 0], K) and np.array_equal(host(vb)[:, 0], V)
 
 
 # ------------------------------------------------------------------------------------ branches that other tests do not reach
