@@ -33,12 +33,13 @@
 //    row's largest.  Maxima, sums, outputs and joins are fp32.
 //
 // What bounds it (GB300, measured): per unit of a 128-wide head and 4 fp32 rows a warp issues
-// about 660 instructions, 208 of them for the values' codes, 136 for the keys', 32 tensor
+// about 670 instructions, 208 of them for the values' codes, 136 for the keys', 32 tensor
 // products; on this tensor path a product (8 clocks per scheduler) does not overlap with fp32
-// FMAs, which share its register ports.  The loop takes 0.77 ns per unit and GPU (4608 bytes:
-// 6.0 TB/s; without its arithmetic 0.70 ns, 6.6 TB/s): memory bounds it, just.  With 12 rows it
-// takes about 980 instructions and the tensor path and the instruction issue bound it.
-// Around the loop a call costs about 11 us (launch, lengths, first copies; the joins).
+// FMAs, which share its register ports.  The loop takes 0.80 ns per unit and GPU (4608 bytes:
+// 5.8 TB/s; without its arithmetic 0.70 ns, 6.6 TB/s): memory and issue bound it together.  With
+// 12 rows it takes about 990 instructions; neither memory, issue nor one pipe is full then, and three
+// warps a scheduler do not cover the latencies that are left.
+// Around the loop a call costs about 12 us (launch, lengths, first copies; the joins).
 #pragma once
 
 #include <type_traits>

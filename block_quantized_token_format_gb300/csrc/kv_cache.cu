@@ -277,8 +277,9 @@ __device__ __forceinline__ void read_quad(const float* p, bool wide, float (&x)[
 // latency and instruction issue together.  With quads of neighbouring lanes exchanged for the
 // rotation and one row to a warp it was 115 instructions and 76 us; several tokens to a warp in a
 // loop made it 59 and the store below 46 instead of 40.  4100 tokens of 32 + 8 + 8 fp32 heads
-// with the store: 39 us, 5.3 TB/s; a row stored takes about three times the instructions of one normed.  At 4 tokens: 2.1
-// and 2.9 us, a launch and two latencies.
+// with the store: 39 us, 5.3 TB/s; 4096 of 64 + 8 + 8 bf16 heads with it: 51 us, 3.4 TB/s.  A row
+// stored takes about three times the instructions of one normed.  At 4 tokens: 2.1 and 3.1 us, a
+// launch and two latencies.
 template <int D, typename T, int SETS>
 __global__ void __launch_bounds__(128, SETS > 1 ? 8 : 4) heads_kernel(const HeadArgs a) {
     constexpr int L = D / 8, PER = 32 / L, ROWS = PER * SETS;
@@ -630,7 +631,9 @@ qg_status qg_cache_pages(const int32_t* held, const int32_t* fresh, int n_req, i
     // CTAs of 256 threads, three to an SM, start and scan sooner than one of 512 (3.0 us against 3.5
     // at 48 tokens, 4.8 against 5.7 at 300,000).  Where 256 threads would scan in two rounds (300
     // requests: 4.3 us against 3.9), or a call in place, which has 8 CTAs, would take its tokens in
-    // two (32,000: 12.8 us against 9.3), CTAs have 512.
+    // two (32,000: 12.8 us against 9.3), CTAs have 512.  A call in place has no more than its cluster's 8
+    // CTAs: 3.5 us for 48 tokens, 8.1 to 9.6 for 32,000 and 70 for 292,000, where the whole grid with a
+    // separate free_end takes 3.1, 2.8 and 5.1.
     const int threads = n_req > 256 || (a.in_place && n_tok > 8 * 256) ? kPageThreads : 256;
     int64_t grid = std::max<int64_t>(1, std::min<int64_t>((n_tok + threads - 1) / threads, threads == 256 ? 3 * sms : sms));
     // In place every CTA must have read free_begin before it is written: one cluster, which can wait for itself.
