@@ -32,6 +32,8 @@ __all__ = [
     "qg_cache", "qg_cache_bytes", "qg_cache_pages", "qg_qk_norm_rope", "qg_cache_append", "qg_attention",
     "qg_attention_workspace_bytes", "QG_CACHE_MAX", "QG_ATTENTION_ZERO_BYTES", "QG_DEVICE_BAD_PAGE",
     "QG_DEVICE_BAD_LENGTH", "QG_DEVICE_NO_PAGES", "QG_ACT_F32", "QG_ACT_BF16",
+    "qgemm", "qgemm_experts", "qgemm_workspace_bytes", "ACTIVATIONS", "qg_prompt_attention",
+    "qg_prompt_attention_workspace_bytes",
 ]
 
 QG_Q8_0, QG_Q4_0, QG_AFFINE4_G64, QG_BF16, QG_Q5_0 = 0, 1, 2, 3, 4
@@ -103,6 +105,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "qg_attention_workspace_bytes": (sz, [i32, i32, i32]),
         "qg_attention": (i32, [vp, i32, vp, i64, i64, i32, vp, i64, vp, vp, i32, i32, i32, vp, f32, vp, i64, vp, vp, sz,
                                vp]),
+        "qgemm_workspace_bytes": (sz, [i32, i32, i64, i64, i64, i64]),
+        "qgemm": (i32, [i32, vp, i64, i64, i32, vp, i64, i64, vp, i32, vp, i64, vp, i64, vp, sz, vp]),
+        "qgemm_experts": (i32, [i32, vp, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i32, vp, i64, vp, sz, vp]),
+        "qg_prompt_attention_workspace_bytes": (sz, [i32, i64, i32, i32, i32]),
+        "qg_prompt_attention": (i32, [i32, vp, i64, vp, i64, vp, i64, i64, i32, i32, i32, vp, i32, i32, i32, f32, vp, i64, vp, vp, sz,
+                                      vp]),
         "qgemv_expert_layer": (i32, [i32, vp, vp, i64, i64, i64, vp, i32, vp, i32, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -388,7 +396,7 @@ _calls = None
 
 
 def _bound():
-    """The compiled module behind the four calls below, bound to the loaded library."""
+    """The compiled module behind the attention path's and the prompt's calls, bound to the loaded library."""
     global _calls
     lib = load_library()
     p = os.path.join(os.path.dirname(_LIB_PATH), "qg_torch.so")
@@ -398,7 +406,8 @@ def _bound():
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
-               for fn in (lib.qg_cache_pages, lib.qg_qk_norm_rope, lib.qg_cache_append, lib.qg_attention)))
+               for fn in (lib.qg_cache_pages, lib.qg_qk_norm_rope, lib.qg_cache_append, lib.qg_attention, lib.qg_packed_bytes, lib.qgemm,
+                           lib.qgemm_experts, lib.qg_prompt_attention)))
     _calls = mod
     return mod
 
@@ -459,6 +468,59 @@ def qg_attention(cache: qg_cache, q, table, seq_len, cu_new, out, workspace, sca
                                         span_mask, lse, stream, getattr(cache, "device", -1))
     if st != 0:
         raise QGError(st, "qg_attention")
+
+
+# ------------------------------------------------------------------------- whole prompts
+
+ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "swiglu": 4}
+
+
+def _act(act) -> int:
+    """QG_ACT_F32 / QG_ACT_BF16 of a name, a torch type or the number itself."""
+    if isinstance(act, int):
+        return act
+    return {"f32": QG_ACT_F32, "bf16": QG_ACT_BF16, "torch.float32": QG_ACT_F32, "torch.bfloat16": QG_ACT_BF16}[str(act)]
+
+
+def qgemm_workspace_bytes(fmt, act, n_out: int, n_in: int, n_slots: int, n_experts: int = 0) -> int:
+    """Workspace of qgemm (``n_slots`` tokens) or qgemm_experts; ``act``: "f32", "bf16" or the torch type."""
+    return int(load_library().qgemm_workspace_bytes(_fmt(fmt), _act(act), int(n_out), int(n_in), int(n_slots), int(n_experts)))
+
+
+def qgemm(fmt, W, n_out: int, n_in: int, x, y, workspace, bias=None, activation: str | None = None, residual=None,
+          stream=None) -> None:
+    """Enqueue ``y[t] = f(W x[t] + bias) + residual[t]`` for any number of tokens: ``x`` ``[ntok, n_in]``
+    float32 or bfloat16, ``y`` and ``residual`` of its type (``residual`` may be ``y``), ``bias`` float32.
+    ``activation``: one of ACTIVATIONS; with "swiglu" W's rows pair up as (gate, up) and ``y`` is
+    ``[ntok, n_out / 2]``.  ``workspace``: uint8, ``qgemm_workspace_bytes``."""
+    st = (_calls or _bound()).gemm(_fmt(fmt), W, n_out, n_in, x, y, workspace, bias, ACTIVATIONS[activation], residual, stream)
+    if st != 0:
+        raise QGError(st, "qgemm")
+
+
+def qgemm_experts(fmt, W, n_experts: int, n_out: int, n_in: int, x, offsets, y, workspace, rows=None,
+                  activation: str | None = None, stream=None) -> None:
+    """Enqueue the product grouped by expert: slots ``offsets[e] .. offsets[e + 1]`` (int32
+    ``[n_experts + 1]``) are expert e's; ``y[s] = f(W_e x[rows[s]])``, or ``x[s]`` without ``rows`` (int32)."""
+    st = (_calls or _bound()).gemm_experts(_fmt(fmt), W, n_experts, n_out, n_in, x, offsets, y, workspace, rows,
+                                           ACTIVATIONS[activation], stream)
+    if st != 0:
+        raise QGError(st, "qgemm_experts")
+
+
+def qg_prompt_attention_workspace_bytes(act, n_tok: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(load_library().qg_prompt_attention_workspace_bytes(_act(act), int(n_tok), int(n_heads), int(n_kv_heads), int(head_dim)))
+
+
+def qg_prompt_attention(q, k, v, cu_seq, out, workspace, scale: float, longest: int, window: int = 0, lse=None, stream=None) -> None:
+    """Enqueue the causal attention of packed prompts: ``q``, ``out`` ``[n_tok, n_heads, head_dim]``,
+    ``k``, ``v`` ``[n_tok, n_kv_heads, head_dim]``, float32 or bfloat16 (slices of one projection's rows
+    are taken as they are); prompt r is rows ``cu_seq[r] .. cu_seq[r + 1]`` (int32), ``longest`` the most
+    tokens of one.  ``window`` > 0: a sliding window.  ``workspace``: uint8,
+    ``qg_prompt_attention_workspace_bytes``."""
+    st = (_calls or _bound()).prompt_attention(q, k, v, cu_seq, out, workspace, scale, longest, window, lse, stream)
+    if st != 0:
+        raise QGError(st, "qg_prompt_attention")
 
 
 QG_DEVICE_WAIT_TIMEOUT = 1

@@ -552,7 +552,7 @@ qg_status check_heads(qg_act act, int64_t n_tok, int n_heads, int n_kv, int D, c
 
 }  // namespace
 
-qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int cluster, void** params, void* stream) {
+static qg_status launch_with(bool early, const void* fn, int grid, int threads, size_t smem, int cluster, void** params, void* stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
@@ -560,7 +560,7 @@ qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int c
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (launch_flags() & QG_LAUNCH_EARLY_START) {
+    if (early) {
         attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[n++].val.programmaticStreamSerializationAllowed = 1;
     }
@@ -574,6 +574,14 @@ qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int c
     cfg.numAttrs = unsigned(n);
     if (cudaLaunchKernelExC(&cfg, fn, params) != cudaSuccess) { cudaGetLastError(); return QG_ECUDA; }
     return QG_OK;
+}
+
+qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int cluster, void** params, void* stream) {
+    return launch_with((launch_flags() & QG_LAUNCH_EARLY_START) != 0, fn, grid, threads, smem, cluster, params, stream);
+}
+
+qg_status launch_after(const void* fn, int grid, int threads, size_t smem, bool early, void** params, void* stream) {
+    return launch_with(early || (launch_flags() & QG_LAUNCH_EARLY_START) != 0, fn, grid, threads, smem, 1, params, stream);
 }
 
 }  // namespace qg

@@ -1,0 +1,393 @@
+// qgemm and qgemm_experts: argument checks, the kernel that stages the tokens, the choice of the
+// tile's tokens, the launch.  Formulas and argument rules are in include/qgemv.h; the product's
+// kernel in qgemm.cuh.
+#include <algorithm>
+#include <cmath>
+
+#include "qgemm.cuh"
+#include "qgemv_host.h"
+
+namespace qg {
+
+const void* qgemm_lookup_fmt0(bool);
+const void* qgemm_lookup_fmt1(bool);
+const void* qgemm_lookup_fmt2(bool);
+const void* qgemm_lookup_fmt3(bool);
+const void* qgemm_lookup_fmt4(bool);
+const void* qgemm_lookup(int fmt, bool f32) {
+    switch (fmt) {
+        case 0: return qgemm_lookup_fmt0(f32);
+        case 1: return qgemm_lookup_fmt1(f32);
+        case 2: return qgemm_lookup_fmt2(f32);
+        case 3: return qgemm_lookup_fmt3(f32);
+        default: return qgemm_lookup_fmt4(f32);
+    }
+}
+
+namespace {
+
+constexpr int kStageThreads = 256;
+constexpr int kMostExperts = 65536;
+
+struct StageArgs {
+    const void* x;
+    void* staged;                  // [terms][n_slots][n_in]; null: nothing to stage
+    float* xscale;
+    const int32_t* rows;           // experts: the token of each slot, or null
+    const int32_t* offsets;
+    int32_t* tile_start;
+    long long x_stride, n_x;
+    int n_slots, n_in, n_experts, bn, m_tiles;
+    unsigned int* status;
+};
+
+// Tiles of `bn` slots before each expert; offsets that do not grow from 0 on or pass n_slots leave
+// no tile at all.  One CTA.
+__device__ void plan_tiles(const StageArgs& a) {
+    __shared__ long long warp_sum[kStageThreads / 32];
+    __shared__ int bad;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    long long run = 0;
+    for (int e0 = 0; e0 < a.n_experts; e0 += kStageThreads) {
+        const int e = e0 + tid;
+        long long tiles = 0;
+        if (e < a.n_experts) {
+            const int lo = a.offsets[e], hi = a.offsets[e + 1];
+            if (lo < 0 || hi < lo || hi > a.n_slots) bad = 1;
+            else tiles = (hi - lo + a.bn - 1) / a.bn;
+        }
+        long long sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const long long up = __shfl_up_sync(tc::kFullMask, sum, d);
+            if (lane >= d) sum += up;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        long long before = run;
+        for (int w = 0; w < kStageThreads / 32; ++w) {
+            if (w < warp) before += warp_sum[w];
+            run += warp_sum[w];
+        }
+        if (e < a.n_experts) a.tile_start[e] = int32_t(min(before + sum - tiles, 0x7FFFFFFFll));
+        __syncthreads();
+    }
+    // (Tiles are numbered with 31 bits: the host has checked n_slots and n_experts for that.)
+    if (bad)
+        for (int e = tid; e <= a.n_experts; e += kStageThreads) a.tile_start[e] = 0;
+    else if (tid == 0)
+        a.tile_start[a.n_experts] = int32_t(run);
+    if (bad && tid == 0) atomicOr(a.status, 4u);         // QG_DEVICE_BAD_PLAN
+}
+
+// Eight neighbouring values of a row.
+__device__ __forceinline__ void read8(const float* p, float (&x)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void read8(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ bool finite_of(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+// The tokens' operand, one row per slot.  With quantized weights: fp16 terms of the row times the
+// power of two that takes its largest magnitude to [2^14, 2^15) (a second term holds what the
+// first one's rounding left: 22 bits together); with bf16 weights: the bf16 values, or three
+// bf16 terms of fp32 ones, each the next 8 bits (cut off, so that they add up exactly).  A value
+// that is not finite is its own first term.  `PER` threads take a row.  Bound by the launch for
+// few rows, else by memory.
+template <typename T, int FMT, int PER> __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a) {
+    constexpr bool kQuant = FMT != QG_BF16, kF32 = sizeof(T) == 4;
+    __shared__ uint32_t most[kStageThreads / 32];
+    tc::grid_launch_dependents();
+    tc::grid_wait();
+    if (a.n_experts && blockIdx.x == gridDim.x - 1) {
+        plan_tiles(a);
+        return;
+    }
+    const int tid = int(threadIdx.x), sub = tid % PER;
+    const long long slot = (long long)blockIdx.x * (kStageThreads / PER) + tid / PER;
+    const int used = a.n_experts ? max(0, min(a.offsets[a.n_experts], a.n_slots)) : a.n_slots;
+    if (slot >= used) return;                            // (PER = 256: the whole block)
+    long long at = a.rows ? (long long)a.rows[slot] : slot;
+    const bool bad = at < 0 || at >= a.n_x;
+    if (bad) {
+        if (sub == 0) atomicOr(a.status, 4u);            // QG_DEVICE_BAD_PLAN; the row counts as zeros
+        at = 0;
+    }
+    const T* const src = static_cast<const T*>(a.x) + at * a.x_stride;
+    float scale = 1.0f;
+    if constexpr (kQuant) {
+        uint32_t top = 0;                                // the largest finite magnitude's bits
+        for (int i = sub * 8; i < a.n_in; i += PER * 8) {
+            float x[8];
+            read8(src + i, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (finite_of(x[j])) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d /= 2) top = max(top, __shfl_xor_sync(tc::kFullMask, top, d));
+        if constexpr (PER > 32) {
+            if ((tid & 31) == 0) most[tid >> 5] = top;
+            __syncthreads();
+            for (int w = 0; w < kStageThreads / 32; ++w) top = max(top, most[w]);
+        }
+        if (bad) top = 0;
+        int e = 0;
+        if (top) e = min(14 - ilogbf(__uint_as_float(top)), 126);        // at least -113
+        scale = __int_as_float((e + 127) << 23);
+        if (sub == 0) a.xscale[slot] = __int_as_float((127 - e) << 23);
+    }
+    const size_t term = size_t(a.n_slots) * size_t(a.n_in);
+    uint16_t* const out = static_cast<uint16_t*>(a.staged) + size_t(slot) * size_t(a.n_in);
+    for (int i = sub * 8; i < a.n_in; i += PER * 8) {
+        float x[8];
+        read8(src + i, x);
+        uint16_t t0[8], t1[8], t2[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = bad ? 0.0f : x[pairs_by_four(FMT) ? j / 2 + j % 2 * 4 : j];
+            if constexpr (kQuant) {
+                const float s = v * scale;
+                const __half h = __float2half_rn(s);
+                t0[j] = __half_as_ushort(h);
+                t1[j] = finite_of(s) ? __half_as_ushort(__float2half_rn(s - __half2float(h))) : uint16_t(0);
+            } else {
+                const bool fine = finite_of(v);
+                const uint32_t b0 = __float_as_uint(v) & 0xFFFF0000u;
+                const float r1 = fine ? v - __uint_as_float(b0) : 0.0f;
+                const uint32_t b1 = __float_as_uint(r1) & 0xFFFF0000u;
+                const float r2 = r1 - __uint_as_float(b1);
+                // (A NaN whose bits would all be cut off stays one.)
+                t0[j] = fine || (b0 & 0x007F0000u) || !(__float_as_uint(v) & 0x007FFFFFu) ? uint16_t(b0 >> 16) : uint16_t(0x7FC0);
+                t1[j] = uint16_t(b1 >> 16);
+                t2[j] = uint16_t(__float_as_uint(r2) >> 16);
+            }
+        }
+        auto put = [&](uint16_t* to, const uint16_t (&t)[8]) {
+            *reinterpret_cast<uint4*>(to) = make_uint4(t[0] | uint32_t(t[1]) << 16, t[2] | uint32_t(t[3]) << 16, t[4] | uint32_t(t[5]) << 16,
+                                                       t[6] | uint32_t(t[7]) << 16);
+        };
+        put(out + i, t0);
+        if constexpr (kF32) put(out + term + i, t1);
+        if constexpr (kF32 && !kQuant) put(out + 2 * term + i, t2);
+    }
+}
+
+template <typename T, int PER> const void* stage_fn(int fmt) {
+    return fmt == QG_BF16 ? (const void*)&stage_kernel<T, QG_BF16, PER>
+           : fmt == QG_Q8_0 ? (const void*)&stage_kernel<T, QG_Q8_0, PER> : (const void*)&stage_kernel<T, QG_Q4_0, PER>;
+}
+const void* stage_fn(int fmt, bool f32, bool wide) {
+    return f32 ? (wide ? stage_fn<float, 256>(fmt) : stage_fn<float, 32>(fmt))
+               : (wide ? stage_fn<__nv_bfloat16, 256>(fmt) : stage_fn<__nv_bfloat16, 32>(fmt));
+}
+
+// What a call needs of its workspace: tiles per expert, powers of two, staged tokens.
+struct GemmSpace { size_t tile_start, xscale, staged, total; };
+GemmSpace gemm_space(int fmt, bool f32, bool gathers, int64_t n_in, int64_t n_slots, int64_t n_experts) {
+    GemmSpace s{};
+    auto take = [&](size_t bytes) { const size_t at = s.total; s.total = (at + bytes + 255) / 256 * 256; return at; };
+    const bool quant = fmt != QG_BF16;
+    s.tile_start = take(n_experts ? size_t(n_experts + 1) * 4 : 0);
+    s.xscale = take(quant ? size_t(n_slots) * 4 : 0);
+    s.staged = take(quant || f32 || gathers ? size_t(terms_x(fmt, f32)) * size_t(n_slots) * size_t(n_in) * 2 : 0);
+    return s;
+}
+
+struct GemmCall {
+    int fmt;
+    const void* W;
+    int64_t n_out, n_in, n_experts;
+    qg_act act;
+    const void* x;
+    int64_t x_stride, n_x, n_slots;
+    const int32_t *offsets, *rows;
+    const float* bias;
+    const void* residual;
+    int64_t residual_stride;
+    qg_activation f;
+    void* y;
+    int64_t y_stride;
+    void* workspace;
+    size_t workspace_bytes;
+    void* stream;
+};
+
+qg_status check(const GemmCall& c) {
+    const int64_t most = (int64_t(1) << 31) - 1;
+    if (!shape_valid(c.fmt, c.n_out, c.n_in) || (c.act != QG_ACT_F32 && c.act != QG_ACT_BF16)) return QG_EINVAL;
+    if (c.n_slots < 0 || c.n_slots > most - 1024 || c.n_x < 0 || c.n_x > most) return QG_EINVAL;
+    if (c.f < QG_F_NONE || c.f > QG_F_SWIGLU || (c.f == QG_F_SWIGLU && c.n_out % 2 != 0)) return QG_EINVAL;
+    const int64_t width = c.f == QG_F_SWIGLU ? c.n_out / 2 : c.n_out;
+    if (c.x_stride < c.n_in || c.y_stride < width || (c.residual && c.residual_stride < width)) return QG_EINVAL;
+    if (c.x_stride > most || c.y_stride > most || c.residual_stride > most) return QG_EINVAL;
+    if (c.n_slots == 0) return QG_OK;
+    if (!c.W || !c.x || !c.y || c.x == c.y) return QG_EINVAL;
+    const int64_t size = c.act == QG_ACT_F32 ? 4 : 2;
+    if (!aligned(c.W, 16) || !aligned(c.x, 16) || c.x_stride * size % 16 != 0 || !aligned(c.y, uintptr_t(size)) ||
+        !aligned(c.residual, uintptr_t(size)) || !aligned(c.bias, 4) || !aligned(c.offsets, 4) || !aligned(c.rows, 4))
+        return QG_EALIGN;
+    // Rows written over residual rows need the same places.
+    if (c.residual == c.y && c.residual_stride != c.y_stride && c.n_slots > 1) return QG_EINVAL;
+    return QG_OK;
+}
+
+// The tile's tokens.  A tile of bn tokens takes about max(2 bn, 190) clocks per step of 64 along K
+// (fp32: 6 bn, 400): the tensor cores' time, or the decoding of the codes; tiles run on all SMs in
+// rounds.
+int tile_tokens(bool f32, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms) {
+    int best = 32;
+    double least = 0;
+    for (int bn = 32; bn <= gemm_most_tokens(f32); bn *= 2) {
+        const double step = f32 ? std::max(6.0 * bn, 400.0) : std::max(2.0 * bn, 190.0);
+        double rounds;
+        if (n_experts == 0) {
+            rounds = double((m_tiles * ((n_slots + bn - 1) / bn) + sms - 1) / sms);
+        } else {
+            // Experts' rows spread around the mean: on average half a tile more than they fill.
+            const double used = double(std::min(n_experts, n_slots));
+            rounds = std::max(1.0, double(m_tiles) * std::max(used, double(n_slots) / bn + 0.5 * used) / sms);
+        }
+        const double cost = rounds * step;
+        if (bn == 32 || cost <= least) { best = bn; least = cost; }
+    }
+    return best;
+}
+
+qg_status encode(CUtensorMap* map, const void* p, int64_t inner, int64_t rows, int64_t terms, int64_t pitch, int box_rows) {
+    const EncodeTiledFn enc = encode_tiled();
+    if (!enc) return QG_ECUDA;
+    const cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(terms)};
+    const cuuint64_t strides[2] = {cuuint64_t(pitch), terms > 1 ? cuuint64_t(pitch) * cuuint64_t(rows) : cuuint64_t(pitch)};
+    const cuuint32_t box[3] = {kGemmK, cuuint32_t(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, terms > 0 ? 3 : 2, const_cast<void*>(p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QG_OK : QG_ECUDA;
+}
+
+qg_status launch_gemm(const GemmCall& c) {
+    const bool f32 = c.act == QG_ACT_F32, quant = c.fmt != QG_BF16;
+    const GemmSpace sp = gemm_space(c.fmt, f32, c.rows != nullptr, c.n_in, c.n_slots, c.n_experts);
+    if (sp.total > 0 && (!c.workspace || c.workspace_bytes < sp.total)) return QG_EWORKSPACE;
+    if (!aligned(c.workspace, 16)) return QG_EALIGN;
+    int dev = 0, sms = 0, optin = 0;
+    unsigned int* status = nullptr;
+    qg_status st = device_info(&dev, &sms, &optin, &status);
+    if (st != QG_OK) return st;
+    const int64_t m_tiles = (c.n_out + kGemmRows - 1) / kGemmRows;
+    const int bn = tile_tokens(f32, m_tiles, c.n_slots, c.n_experts, sms);
+    const int64_t n_tiles = (c.n_slots + bn - 1) / bn;
+    if ((n_tiles + c.n_experts) * m_tiles > (int64_t(1) << 31) - 4096) return QG_EUNSUPPORTED;
+    uint8_t* const ws = static_cast<uint8_t*>(c.workspace);
+    const bool stages_x = quant || f32 || c.rows;
+
+    GemmArgs a{};
+    a.W = static_cast<const uint8_t*>(c.W);
+    a.row_bytes = row_stride(c.fmt, c.n_in);
+    a.n_out = int(c.n_out);
+    a.n_in = int(c.n_in);
+    a.n_slots = int(c.n_slots);
+    a.n_experts = int(c.n_experts);
+    a.offsets = c.offsets;
+    a.tile_start = reinterpret_cast<const int32_t*>(ws + sp.tile_start);
+    a.xscale = quant ? reinterpret_cast<const float*>(ws + sp.xscale) : nullptr;
+    a.bias = c.bias;
+    a.residual = c.residual;
+    a.y = c.y;
+    a.residual_stride = c.residual_stride;
+    a.y_stride = c.y_stride;
+    a.f = int(c.f);
+    a.bn = bn;
+    a.m_tiles = int(m_tiles);
+    a.n_tiles = int(n_tiles);
+    a.status = status;
+    a.wait_limit = wait_limit();
+    a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
+    a.extra_tx = test_extra_tx();
+    const void* const fn = qgemm_lookup(c.fmt, f32);
+    const size_t stage = size_t(terms_w(c.fmt, f32)) * kOperandA + size_t(terms_x(c.fmt, f32)) * size_t(bn) * kGemmK * 2;
+    const size_t raw = size_t(kDecodeWarps) * kRawSlots * size_t(raw_bytes(c.fmt));
+    a.stages = int(std::min<size_t>(8, (size_t(optin) - kStaticSmemReserve - 1024 - raw) / stage));
+    const size_t smem = 1024 + raw + size_t(a.stages) * stage;
+    if (a.stages < 2 || blocks_per_sm(fn, dev, optin, kGemmThreads, smem) < 1) return QG_EUNSUPPORTED;
+    st = stages_x ? encode(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, bn)
+                  : encode(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, bn);
+    if (st == QG_OK && !quant) st = encode(&a.wmap, c.W, c.n_in, std::max<int64_t>(1, c.n_experts) * c.n_out, 0, a.row_bytes, kGemmRows);
+    if (st != QG_OK) return st;
+
+    const bool before = stages_x || c.n_experts > 0;
+    if (before) {
+        StageArgs s{};
+        s.x = c.x;
+        s.staged = ws + sp.staged;
+        s.xscale = reinterpret_cast<float*>(ws + sp.xscale);
+        s.rows = c.rows;
+        s.offsets = c.offsets;
+        s.tile_start = reinterpret_cast<int32_t*>(ws + sp.tile_start);
+        s.x_stride = c.x_stride;
+        s.n_x = c.n_x;
+        s.n_slots = int(c.n_slots);
+        s.n_in = int(c.n_in);
+        s.n_experts = int(c.n_experts);
+        s.bn = bn;
+        s.m_tiles = int(m_tiles);
+        s.status = status;
+        // A row takes a CTA where there are too few rows to fill the GPU with a warp each.
+        const bool wide = c.n_slots < 8 * sms;
+        const int64_t per = wide ? 1 : kStageThreads / 32;
+        const int64_t grid = (stages_x ? (c.n_slots + per - 1) / per : 0) + (c.n_experts > 0 ? 1 : 0);
+        void* params[] = {&s};
+        st = launch_early(stage_fn(c.fmt, f32, wide), int(grid), kStageThreads, 0, 1, params, c.stream);
+        if (st != QG_OK) return st;
+    }
+    const int64_t tiles = c.n_experts ? sms : n_tiles * m_tiles;
+    void* params[] = {&a};
+    return launch_after(fn, int(std::min<int64_t>(sms, tiles)), kGemmThreads, smem, before, params, c.stream);
+}
+
+}  // namespace
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" {
+
+size_t qgemm_workspace_bytes(qg_fmt fmt, qg_act act, int64_t n_out, int64_t n_in, int64_t n_slots, int64_t n_experts) {
+    if (!shape_valid(fmt, n_out, n_in) || (act != QG_ACT_F32 && act != QG_ACT_BF16) || n_slots < 0 ||
+        n_slots > (int64_t(1) << 31) - 1025 || n_experts < 0 || n_experts > kMostExperts)
+        return 0;
+    return std::max<size_t>(256, gemm_space(fmt, act == QG_ACT_F32, true, n_in, n_slots, n_experts).total);
+}
+
+qg_status qgemm(qg_fmt fmt, const void* W, int64_t n_out, int64_t n_in, qg_act act, const void* x, int64_t x_stride, int64_t ntok,
+                const float* bias, qg_activation f, const void* residual, int64_t residual_stride, void* y, int64_t y_stride,
+                void* workspace, size_t workspace_bytes, void* stream) {
+    GemmCall c{fmt, W, n_out, n_in, 0, act, x, x_stride, ntok, ntok, nullptr, nullptr, bias, residual, residual ? residual_stride : 0,
+               f, y, y_stride, workspace, workspace_bytes, stream};
+    const qg_status st = check(c);
+    if (st != QG_OK || ntok == 0) return st;
+    return launch_gemm(c);
+}
+
+qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_out, int64_t n_in, qg_act act, const void* x,
+                        int64_t x_stride, int64_t n_x, const int32_t* offsets, const int32_t* rows, int64_t n_slots, qg_activation f,
+                        void* y, int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    GemmCall c{fmt, W, n_out, n_in, n_experts, act, x, x_stride, n_x, n_slots, offsets, rows, nullptr, nullptr, 0,
+               f, y, y_stride, workspace, workspace_bytes, stream};
+    if (n_experts < 1 || n_experts > kMostExperts || n_experts * n_out > (int64_t(1) << 31) - 1024) return QG_EINVAL;
+    if (n_slots > 0 && (!offsets || n_x < 1 || (!rows && n_x < n_slots))) return QG_EINVAL;
+    const qg_status st = check(c);
+    if (st != QG_OK || n_slots == 0) return st;
+    return launch_gemm(c);
+}
+
+}  // extern "C"

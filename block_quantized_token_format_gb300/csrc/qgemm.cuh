@@ -1,0 +1,495 @@
+// The product of block-quantized weights with many tokens' activations (qgemm) and the same
+// grouped by expert (qgemm_experts): y = f(W x + bias) + residual.  Argument rules and formulas
+// are in include/qgemv.h.
+//
+// A tile is 128 rows of W times `bn` tokens; the products run on tcgen05 with W's rows as M (the
+// accumulators' lanes) and tokens as N, in steps of 64 along K:
+//   * eight warps turn W's codes into 16-bit floats: each keeps its own 16 rows' raw codes and
+//     scales a few steps ahead in shared memory (cp.async) and writes a step's 128 x 64 operand;
+//   * one thread copies the tokens' operand (staged by stage_kernel, below) with tensor copies;
+//   * one thread issues the products;
+//   * eight warps empty the accumulators, of which there are two sets, so that a tile's epilogue
+//     runs beside the next one's products.
+// A CTA takes tiles in turn; consecutive tiles share their tokens (which then come from L2).
+//
+// Numbers.  Quantized formats enter as fp16: a code times its fp16 scale has at most 19 bits.
+// bf16 activations, which a row's power of two moves into fp16's range exactly (but for values
+// 2^-29 and more below the row's largest), meet weights rounded to 11 bits: 2^-12 of a weight,
+// an eighth of what rounding the output to bf16 costs.  fp32 activations are two fp16 terms (22
+// bits), weights two (exact), in three products; the two small ones have accumulators of their
+// own, and every 256 values of K the sums move to fp32 registers: the tensor cores truncate what
+// they add, and a long chain of additions would lose what the terms keep.
+// bf16 weights meet bf16 activations as they are, fp32 ones as three bf16 terms (all 24 bits).
+#pragma once
+
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qg_layout.h"
+#include "umma.cuh"
+
+namespace qg {
+
+constexpr int kGemmRows = 128, kGemmK = 64;
+constexpr int kDecodeWarps = 8, kDrainWarps = 8;
+constexpr int kGemmThreads = 32 * (kDecodeWarps + kDrainWarps + 2);
+constexpr int kRawSlots = 3;                 // steps of raw codes a decoding warp holds
+constexpr int kChunkSteps = 4;               // fp32: steps of K between moves to registers
+constexpr int kOperandA = kGemmRows * kGemmK * 2;
+
+__host__ __device__ constexpr int raw_codes(int fmt) { return fmt == QG_Q8_0 ? 64 : fmt == QG_BF16 ? 0 : 32; }                        // bytes of 64 weights
+__host__ __device__ constexpr int raw_scales(int fmt) { return fmt == QG_BF16 ? 0 : fmt == QG_Q5_0 ? 12 : 4; }
+__host__ __device__ constexpr int raw_bytes(int fmt) { return 16 * (raw_codes(fmt) + raw_scales(fmt)); }                              // of a warp's 16 rows
+__host__ __device__ constexpr int terms_w(int fmt, bool f32) { return f32 && fmt != QG_BF16 ? 2 : 1; }
+__host__ __device__ constexpr int terms_x(int fmt, bool f32) { return !f32 ? 1 : fmt == QG_BF16 ? 3 : 2; }
+__host__ __device__ constexpr int gemm_most_tokens(bool f32) { return f32 ? 128 : 256; }                                              // of a tile
+
+struct GemmArgs {
+    CUtensorMap xmap, wmap;        // staged tokens [terms][n_slots][n_in]; bf16 weights
+    const uint8_t* W;
+    long long row_bytes;
+    int n_out, n_in, n_slots, n_experts;      // n_experts 0: one matrix
+    const int32_t* offsets;                   // experts: the caller's, and the tiles before each expert
+    const int32_t* tile_start;
+    const float* xscale;                      // a power of two per slot, or null
+    const float* bias;
+    const void* residual;
+    void* y;
+    long long residual_stride, y_stride;
+    int f, bn, stages, m_tiles, n_tiles;
+    unsigned int* status;
+    uint32_t wait_limit, drain_limit, extra_tx;
+};
+
+enum { kFNone = 0, kFSilu = 1, kFGelu = 2, kFGeluTanh = 3, kFSwiglu = 4 };
+
+__device__ __forceinline__ float silu_of(float v) { return v / (1.0f + expf(-v)); }
+__device__ __forceinline__ float activation_of(float v, int f) {
+    if (f == kFSilu) return silu_of(v);
+    if (f == kFGelu) return 0.5f * v * (1.0f + erff(v * 0.70710678f));
+    if (f == kFGeluTanh) return 0.5f * v * (1.0f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
+    return v;
+}
+
+struct GemmTile { int row0, w_row0, slot0, cols; };       // row0: in the expert's matrix; w_row0: in the stack
+
+__device__ __forceinline__ int gemm_tiles(const GemmArgs& a) {
+    return (a.n_experts ? a.tile_start[a.n_experts] : a.n_tiles) * a.m_tiles;
+}
+__device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& a, int t) {
+    GemmTile g;
+    const int nt = t / a.m_tiles;
+    g.row0 = (t - nt * a.m_tiles) * kGemmRows;
+    if (!a.n_experts) {
+        g.w_row0 = g.row0;
+        g.slot0 = nt * a.bn;
+        g.cols = min(a.bn, a.n_slots - g.slot0);
+        return g;
+    }
+    int lo = 0, hi = a.n_experts;                        // the last expert with tile_start <= nt
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.tile_start[mid] <= nt) lo = mid; else hi = mid;
+    }
+    g.slot0 = a.offsets[lo] + (nt - a.tile_start[lo]) * a.bn;
+    g.cols = min(a.bn, a.offsets[lo + 1] - g.slot0);
+    g.w_row0 = lo * a.n_out + g.row0;
+    return g;
+}
+
+// A position in the sequence of steps that a CTA's tiles make.
+struct StepWalk {
+    int tile, k;
+    GemmTile g;
+};
+
+// ------------------------------------------------------------------------- codes to fp16
+
+// The order of a step's values along K: eight nibbles of a word come as the pairs (0,4), (1,5),
+// (2,6), (3,7), which one mask each takes out of the word; the tokens are staged in that order.
+__host__ __device__ constexpr bool pairs_by_four(int fmt) { return fmt == QG_Q4_0 || fmt == QG_AFFINE4_G64 || fmt == QG_Q5_0; }
+
+__device__ __forceinline__ __half2 as_h2(uint32_t b) { return *reinterpret_cast<__half2*>(&b); }
+__device__ __forceinline__ uint32_t as_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// 32 weights of one row: codes (Q8_0: 8 words, else 4), fifth bits, scale (and bias) -> 16 pairs,
+// and with F32 the 16 pairs of what their rounding left.
+template <int FMT, bool F32>
+__device__ __forceinline__ void decode32(const uint32_t* code, uint32_t fifth, __half2 d, __half2 b, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+    constexpr uint32_t kThousand = 0x64006400u;          // 1024 in both halves: its last bits are a whole number
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        uint32_t u;
+        float off;
+        if constexpr (FMT == QG_Q8_0) {
+            u = __byte_perm(code[i / 2], 0x64646464u, i % 2 ? 0x4342 : 0x4140);
+            off = 1024.0f + 128.0f;
+        } else {
+            const int m = i % 4, j = i / 4;
+            u = ((code[j] >> (4 * m)) & 0x000F000Fu) | kThousand;
+            off = FMT == QG_Q4_0 ? 1024.0f + 8.0f : 1024.0f;
+            if constexpr (FMT == QG_Q5_0) {
+                const int s = 8 * (m / 2) + 2 * j + m % 2;           // element 8 j + m; m + 4 is 16 bits up
+                u |= (s >= 4 ? fifth >> (s - 4 < 0 ? 0 : s - 4) : fifth << (4 - s < 0 ? 0 : 4 - s)) & 0x00100010u;
+                off = 1024.0f + 16.0f;
+            }
+        }
+        const __half2 q = __hsub2(as_h2(u), __float2half2_rn(off));
+        if constexpr (FMT == QG_AFFINE4_G64) {
+            if constexpr (F32) {
+                const float2 w = make_float2(fmaf(__low2float(q), __low2float(d), __low2float(b)),
+                                             fmaf(__high2float(q), __low2float(d), __low2float(b)));
+                const __half2 h = __floats2half2_rn(w.x, w.y);
+                hi[i] = as_bits(h);
+                lo[i] = as_bits(__floats2half2_rn(w.x - __low2float(h), w.y - __high2float(h)));
+            } else {
+                hi[i] = as_bits(__hfma2(q, d, b));
+            }
+        } else {
+            const __half2 h = __hmul2_rn(q, d);
+            hi[i] = as_bits(h);
+            if constexpr (F32) lo[i] = as_bits(__hfma2(q, d, __hneg2(h)));       // exact
+        }
+    }
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// ------------------------------------------------------------------------------ the kernel
+
+template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) qgemm_kernel(const __grid_constant__ GemmArgs a) {
+    constexpr bool kQuant = FMT != QG_BF16;
+    constexpr int TW = terms_w(FMT, F32), TX = terms_x(FMT, F32);
+    constexpr int kStepWeights = FMT == QG_Q8_0 ? 512 : 1024;        // of a layout step
+    using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bar_mem[3 * 8 + 5];
+    __shared__ uint32_t tmem_at, dead;
+
+    const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t b_bytes = uint32_t(a.bn) * kGemmK * 2, stage_bytes = TW * kOperandA + TX * b_bytes;
+    const uint32_t raw0 = base + uint32_t(a.stages) * stage_bytes;
+    const uint32_t bars = smem_addr(bar_mem);
+    auto full_b = [&](int s) { return bars + 8u * uint32_t(s); };
+    auto full_a = [&](int s) { return bars + 8u * uint32_t(8 + s); };
+    auto empty = [&](int s) { return bars + 8u * uint32_t(16 + s); };
+    auto acc_full = [&](int b) { return bars + 8u * uint32_t(24 + b); };
+    auto acc_empty = [&](int b) { return bars + 8u * uint32_t(26 + b); };
+    const uint32_t drained = bars + 8u * 28u;
+    const uint32_t acc_cols = uint32_t(a.bn) * (F32 ? 2 : 1);                    // of one set
+    const uint32_t tmem_cols = max(32u, 2 * acc_cols);
+    const tc::Waits wait{&dead, a.status, a.wait_limit};
+    const int ksteps = (a.n_in + kGemmK - 1) / kGemmK;
+
+    if (tid == 0) {
+        dead = 0;
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(full_b(s), 1);
+            mbar_init(full_a(s), kDecodeWarps);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), kDrainWarps);
+        }
+        mbar_init(drained, 1);
+        mbar_fence_init();
+    }
+    if (warp == kDrainWarps + kDecodeWarps + 1) tc::tmem_alloc(smem_addr(&tmem_at), tmem_cols);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_at;
+    tc::grid_launch_dependents();
+
+    if (warp < kDrainWarps) {
+        // ---------------------------------------------------------------- accumulators to y
+        tc::grid_wait();
+        const int half = warp >> 2, hc = a.bn / 2;                   // its half of the columns
+        const uint32_t lanes = uint32_t(warp & 3) << 21;             // 32 (warp % 4) in the address's high half
+        const int chunks = F32 ? (ksteps + kChunkSteps - 1) / kChunkSteps : 1;
+        const int tiles = gemm_tiles(a);
+        uint32_t it = 0;
+        bool alive = true;
+        for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+            const GemmTile g = gemm_tile(a, t);
+            const int row = g.row0 + (warp & 3) * 32 + lane;
+            const bool there = row < a.n_out;
+            const float bias = a.bias && there ? a.bias[row] : 0.0f;
+            float sum[F32 ? 64 : 1];
+            uint32_t v[F32 ? 16 : 32];
+            auto put = [&](int u, const float* x) {                  // 16 columns of this lane's row
+                const int c0 = half * hc + u * 16;
+                const float mine = a.xscale && (lane & 15) + c0 < g.cols ? a.xscale[g.slot0 + c0 + (lane & 15)] : 1.0f;
+                const int col = a.f == kFSwiglu ? row >> 1 : row;
+                const bool writes = there && (a.f != kFSwiglu || (lane & 1) == 0);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    if (c0 + c >= g.cols) break;
+                    float y = x[c];
+                    if (a.xscale) y *= __shfl_sync(tc::kFullMask, mine, c);
+                    y += bias;
+                    if (a.f == kFSwiglu) {
+                        const float up = __shfl_xor_sync(tc::kFullMask, y, 1);
+                        y = silu_of(y) * up;
+                    } else if (a.f != kFNone) {
+                        y = activation_of(y, a.f);
+                    }
+                    if (!writes) continue;
+                    const long long slot = g.slot0 + c0 + c;
+                    if (a.residual) {
+                        const Out r = static_cast<const Out*>(a.residual)[slot * a.residual_stride + col];
+                        if constexpr (F32) y += r; else y += __bfloat162float(r);
+                    }
+                    if constexpr (F32) static_cast<float*>(a.y)[slot * a.y_stride + col] = y;
+                    else static_cast<__nv_bfloat16*>(a.y)[slot * a.y_stride + col] = __float2bfloat16_rn(y);
+                }
+            };
+            for (int ch = 0; ch < chunks; ++ch, ++it) {
+                const int b = int(it & 1);
+                if (!wait.warp(acc_full(b), (it >> 1) & 1)) { alive = false; break; }
+                tc::fence_after();
+                const uint32_t acc = tmem + lanes + uint32_t(b) * acc_cols + uint32_t(half * hc);
+                if constexpr (F32) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (u * 16 < hc) {
+                            tc::tmem_load16(acc + uint32_t(a.bn) + u * 16, v);
+                            tc::tmem_load_wait();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) sum[u * 16 + c] = ch == 0 ? __uint_as_float(v[c]) : sum[u * 16 + c] + __uint_as_float(v[c]);
+                            tc::tmem_load16(acc + u * 16, v);
+                            tc::tmem_load_wait();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) sum[u * 16 + c] += __uint_as_float(v[c]);
+                        }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty(b));
+                } else {
+                    for (int u = 0; u * 16 < hc; u += 2) {
+                        const bool two = (u + 1) * 16 < hc;
+                        tc::tmem_load16(acc + u * 16, v);
+                        if (two) tc::tmem_load16(acc + u * 16 + 16, v + 16);
+                        tc::tmem_load_wait();
+                        float x[32];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]);
+                        if ((u + 2) * 16 >= hc) {                    // the set is free before it is written out
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(acc_empty(b));
+                        }
+                        put(u, x);
+                        if (two) put(u + 1, x + 16);
+                    }
+                }
+            }
+            if constexpr (F32) {
+                if (alive) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (u * 16 < hc) put(u, sum + u * 16);
+                }
+            }
+        }
+    } else if (warp < kDrainWarps + kDecodeWarps) {
+        // --------------------------------------------------------------- codes to operand A
+        if constexpr (kQuant) {
+            constexpr int CB = raw_codes(FMT), SB = raw_scales(FMT);
+            if (a.n_experts) tc::grid_wait();
+            const int w = warp - kDrainWarps, r = lane >> 1, h = lane & 1, row = w * 16 + r;
+            const uint32_t raw = raw0 + uint32_t(w) * (kRawSlots * raw_bytes(FMT));
+            const int tiles = gemm_tiles(a);
+            const long long step_bytes = 512 + 512 / CB * SB;
+            const int last = (a.n_in - 1) / kStepWeights;
+            const int last_codes = (a.n_in - last * kStepWeights) * CB / 64;
+            // Requests raw step `n` (its place in the ring); always one group, empty past the end.
+            StepWalk f{int(blockIdx.x), 0, {}};
+            const uint8_t* src = a.W;
+            bool there = false;
+            auto enter = [&]() {
+                if (f.tile >= tiles) return;
+                f.g = gemm_tile(a, f.tile);
+                there = f.g.row0 + row < a.n_out;
+                src = a.W + (there ? (long long)(f.g.w_row0 + row) * a.row_bytes : 0ll);
+            };
+            enter();
+            auto fetch = [&](uint32_t n) {
+                if (f.tile < tiles) {
+                    const uint32_t slot = raw + (n % kRawSlots) * raw_bytes(FMT);
+                    const int k0 = f.k * kGemmK, step = k0 / kStepWeights, in = (k0 - step * kStepWeights) / 64;
+                    const uint8_t* const at = src + step * step_bytes;
+                    const int left = there ? a.n_in - k0 : 0;        // weights from here on
+                    constexpr int kPer = FMT == QG_Q8_0 ? 16 : 32;   // weights of 16 bytes
+#pragma unroll
+                    for (int i = 0; i < CB / 32; ++i) {
+                        const int c = 2 * i + h;
+                        const int place = CB == 64 ? c ^ ((r >> 1) & 1) : c;
+                        const bool some = c * kPer < left;
+                        tc::copy16(slot + r * CB + place * 16, some ? at + in * CB + c * 16 : a.W, some ? 16u : 0u);
+                    }
+                    const uint8_t* const sc = at + (step == last ? last_codes : 512) + in * SB;
+                    const uint32_t to = slot + 16 * CB + r * SB;
+                    if constexpr (FMT == QG_Q5_0) {
+                        const int valid = left >= 64 ? 12 : left > 0 ? 6 : 0;
+                        tc::copy4(to + 4 * h, valid ? sc + 4 * h : a.W, valid ? 4 * h + 4 <= valid ? 4u : 2u : 0u);
+                        if (h == 0) tc::copy4(to + 8, valid == 12 ? sc + 8 : a.W, valid == 12 ? 4u : 0u);
+                    } else if (h == 0) {
+                        tc::copy4(to, left > 0 ? sc : a.W, left <= 0 ? 0u : FMT == QG_AFFINE4_G64 || left >= 64 ? 4u : 2u);
+                    }
+                    if (++f.k == ksteps) {
+                        f.k = 0;
+                        f.tile += gridDim.x;
+                        enter();
+                    }
+                }
+                tc::copy_commit();
+            };
+#pragma unroll
+            for (int i = 0; i < kRawSlots - 1; ++i) fetch(i);
+            uint32_t n = 0;
+            int s = 0;
+            uint32_t phase = 0;
+            bool alive = true;
+            for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+                for (int k = 0; k < ksteps; ++k, ++n) {
+                    tc::copy_wait<kRawSlots - 2>();
+                    __syncwarp();
+                    const uint32_t slot = raw + (n % kRawSlots) * raw_bytes(FMT);
+                    uint32_t code[CB / 8];
+                    if constexpr (CB == 64) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 q = lds128(slot + r * CB + ((2 * h + i) ^ ((r >> 1) & 1)) * 16);
+                            code[4 * i] = q.x, code[4 * i + 1] = q.y, code[4 * i + 2] = q.z, code[4 * i + 3] = q.w;
+                        }
+                    } else {
+                        const uint4 q = lds128(slot + r * CB + h * 16);
+                        code[0] = q.x, code[1] = q.y, code[2] = q.z, code[3] = q.w;
+                    }
+                    uint32_t fifth = 0;
+                    __half2 d, b;
+                    const uint32_t sc = slot + 16 * CB + r * SB;
+                    if constexpr (FMT == QG_Q5_0) {
+                        const uint32_t w0 = lds32(sc), w1 = lds32(sc + 4), w2 = lds32(sc + 8);
+                        fifth = h ? (w1 >> 16) | (w2 << 16) : w0;
+                        d = __half2half2(__ushort_as_half(static_cast<unsigned short>(h ? w2 >> 16 : w1)));
+                        b = d;
+                    } else {
+                        const uint32_t w0 = lds32(sc);
+                        const __half l = __ushort_as_half(static_cast<unsigned short>(w0)), u = __ushort_as_half(static_cast<unsigned short>(w0 >> 16));
+                        d = __half2half2(FMT == QG_AFFINE4_G64 || !h ? l : u);
+                        b = __half2half2(u);
+                    }
+                    fetch(n + kRawSlots - 1);
+                    uint32_t hi[16], lo[16];
+                    decode32<FMT, F32>(code, fifth, d, b, hi, lo);
+                    if (!wait.warp(empty(s), phase ^ 1)) { alive = false; break; }
+                    const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(row) * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t at = to + uint32_t(((4 * h + c) ^ (row & 7)) * 16);
+                        sts128(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                        if constexpr (F32) sts128(at + kOperandA, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                    }
+                    tc::fence_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_a(s));
+                    if (++s == a.stages) { s = 0; phase ^= 1; }
+                }
+            }
+            tc::copy_wait<0>();
+        }
+    } else if (warp == kDrainWarps + kDecodeWarps) {
+        // ------------------------------------------------------------- tokens (and bf16 W)
+        if (lane == 0) {
+            tc::grid_wait();
+            const int tiles = gemm_tiles(a);
+            const uint32_t bytes = TX * b_bytes + (kQuant ? 0 : kOperandA);
+            uint32_t extra = a.extra_tx;
+            int s = 0;
+            uint32_t phase = 0, filled = 0;
+            bool alive = true;
+            for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+                const GemmTile g = gemm_tile(a, t);
+                for (int k = 0; k < ksteps; ++k) {
+                    if (!wait(empty(s), phase ^ 1)) { alive = false; break; }
+                    const uint32_t at = base + uint32_t(s) * stage_bytes;
+                    mbar_arrive_expect_tx(full_b(s), bytes + extra);
+                    extra = 0;
+                    if constexpr (!kQuant) tc::load_2d(at, &a.wmap, k * kGemmK, g.w_row0, full_b(s));
+#pragma unroll
+                    for (int x = 0; x < TX; ++x) tc::load_3d(at + TW * kOperandA + x * b_bytes, &a.xmap, k * kGemmK, g.slot0, x, full_b(s));
+                    ++filled;
+                    if (++s == a.stages) { s = 0; phase ^= 1; }
+                }
+            }
+            // Copies still on their way end before the CTA does: those of the last `stages` steps.
+            if (dead) {
+                for (uint32_t i = 0; i < uint32_t(a.stages) && i < filled; ++i) {
+                    const uint32_t n = filled - 1 - i;
+                    mbar_wait(full_b(int(n % a.stages)), (n / a.stages) & 1, a.drain_limit);
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------------- products
+        if (lane == 0) {
+            if (a.n_experts) tc::grid_wait();
+            const int tiles = gemm_tiles(a);
+            const uint32_t idesc = tc::instr(!kQuant, a.bn, false);
+            int s = 0;
+            uint32_t phase = 0, it = 0;
+            bool alive = true;
+            for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+                for (int k = 0; k < ksteps; ++k) {
+                    const bool first = F32 ? k % kChunkSteps == 0 : k == 0;
+                    const bool lastk = k + 1 == ksteps || (F32 && k % kChunkSteps == kChunkSteps - 1);
+                    const int b = int(it & 1);
+                    if (first && !wait(acc_empty(b), ((it >> 1) & 1) ^ 1)) { alive = false; break; }
+                    if (!wait(full_b(s), phase) || (kQuant && !wait(full_a(s), phase))) { alive = false; break; }
+                    tc::fence_after();
+                    const uint32_t acc = tmem + uint32_t(b) * acc_cols, cross = acc + uint32_t(a.bn);
+                    const uint32_t at = base + uint32_t(s) * stage_bytes, bt = at + TW * kOperandA;
+                    const uint64_t da = tc::desc_k(at), db = tc::desc_k(bt);
+#pragma unroll
+                    for (int j = 0; j < kGemmK / 16; ++j) {
+                        const bool add = !first || j > 0;
+                        const uint64_t aj = da + 2 * j, bj = db + 2 * j;             // 32 bytes along K
+                        if constexpr (F32) {
+                            const uint64_t term = b_bytes >> 4;
+                            tc::mma(cross, aj, bj + term, idesc, add);
+                            if constexpr (kQuant) tc::mma(cross, aj + (kOperandA >> 4), bj, idesc, true);
+                            else tc::mma(cross, aj, bj + 2 * term, idesc, true);
+                        }
+                        tc::mma(acc, aj, bj, idesc, add);
+                    }
+                    tc::commit(empty(s));
+                    if (lastk) {
+                        tc::commit(acc_full(b));
+                        ++it;
+                    }
+                    if (++s == a.stages) { s = 0; phase ^= 1; }
+                }
+            }
+            // Products still under way end before the accumulators are given back.
+            tc::commit(drained);
+            mbar_wait(drained, 0, a.drain_limit);
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == kDrainWarps + kDecodeWarps + 1) tc::tmem_free(tmem, tmem_cols);
+}
+
+const void* qgemm_lookup(int fmt, bool f32);
+
+}  // namespace qg

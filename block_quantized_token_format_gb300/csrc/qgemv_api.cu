@@ -270,12 +270,6 @@ qg_status plan_launch_cached(int fmt, int64_t n_out, int64_t n_in, int ntok, boo
 
 }  // namespace
 
-// cuTensorMapEncodeTiled, fetched from the driver through the runtime once
-// (the library links only the runtime).  Encoding is a host-only computation.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_tiled() {
     static const EncodeTiledFn fn = [] {
         void* f = nullptr;

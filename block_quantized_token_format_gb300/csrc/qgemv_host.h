@@ -33,6 +33,12 @@ int blocks_per_sm(const void* fn, int dev, int optin, int threads, size_t smem);
 // Threads per block the kernel allows (its launch bound).
 int max_threads(const void* fn);
 bool aligned(const void* p, uintptr_t a);
+// cuTensorMapEncodeTiled, fetched from the driver through the runtime once
+// (the library links only the runtime).  Encoding is a host-only computation.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
 // The packed matrix [n_out][row stride / 8] as a 2-D tensor map, box = one full step
 // x rpw rows, zero fill outside (cached per thread).
 qg_status encode_weight_map(CUtensorMap* map, int fmt, const void* W, int64_t n_out, int64_t n_in, int rpw);
@@ -45,6 +51,9 @@ uint32_t wait_limit();
 // A launch of `grid` CTAs (as clusters of `cluster`), with programmatic dependent launch
 // when it is on: the kernel waits for its predecessor before its first access.
 qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int cluster, void** params, void* stream);
+// The second launch of a call: with `early` it may start while the call's first kernel, which the
+// library has launched just before on the stream, still runs (and waits for it where it needs it).
+qg_status launch_after(const void* fn, int grid, int threads, size_t smem, bool early, void** params, void* stream);
 uint32_t test_extra_tx();
 
 }  // namespace qg

@@ -1,4 +1,4 @@
-// Python binding of the attention path's calls for torch tensors: a CPython module that checks
+// Python binding of the attention path's and the prompt's calls for torch tensors: a CPython module that checks
 // and marshals arguments and calls the C ABI through the addresses that bind() receives (the
 // library that the package has loaded).  These calls run once per layer and step, and at decode
 // sizes their host time is the call's time.  Measured per call on GB300's host: 2.7 to 3.0 us, of
@@ -22,6 +22,10 @@ decltype(&qg_cache_pages) call_cache_pages;
 decltype(&qg_qk_norm_rope) call_qk_norm_rope;
 decltype(&qg_cache_append) call_cache_append;
 decltype(&qg_attention) call_attention;
+decltype(&qg_packed_bytes) call_packed_bytes;
+decltype(&qgemm) call_gemm;
+decltype(&qgemm_experts) call_gemm_experts;
+decltype(&qg_prompt_attention) call_prompt_attention;
 
 struct Refused {};                       // a Python error is set
 
@@ -251,9 +255,102 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
-// The addresses of the four calls in the loaded library.
+// Rows [n, width] whose values are contiguous.
+struct Rows {
+    void* p = nullptr;
+    int64_t stride = 0, n = 0, width = 0;
+};
+Rows rows(PyObject* o, at::ScalarType type, const char* name) {
+    const at::Tensor* t = tensor(o, name);
+    Rows r;
+    if (!t) return r;
+    if (t->dim() != 2 || !t->is_cuda() || t->scalar_type() != type || (t->size(1) > 1 && t->stride(1) != 1))
+        refuse(PyExc_ValueError, name, "a CUDA matrix of one type, rows contiguous, is needed");
+    on_device(t->device().index(), name);
+    r.p = t->data_ptr();
+    r.n = t->size(0);
+    r.width = t->size(1);
+    r.stride = r.n > 1 ? t->stride(0) : r.width;              // (of one row it means nothing)
+    if (r.stride < 0) refuse(PyExc_ValueError, name, "rows go forward");
+    return r;
+}
+// Packed weights: a contiguous CUDA tensor that holds them all, or an address.
+const void* packed(PyObject* o, int fmt, int64_t n_rows, int64_t n_in) {
+    if (PyLong_Check(o)) return address(o);
+    const at::Tensor* t = tensor(o, "W");
+    if (!t || !t->is_cuda() || !t->is_contiguous() || size_t(t->nbytes()) < call_packed_bytes(qg_fmt(fmt), n_rows, n_in))
+        refuse(PyExc_ValueError, "W", "a contiguous CUDA tensor of qg_packed_bytes() bytes is needed");
+    on_device(t->device().index(), "W");
+    return t->data_ptr();
+}
+struct Space { void* p = nullptr; size_t bytes = 0; };
+Space space(PyObject* o) {
+    const at::Tensor* const t = tensor(o, "workspace");
+    if (!t) return {};
+    if (!t->is_cuda() || !t->is_contiguous()) refuse(PyExc_ValueError, "workspace", "a contiguous CUDA tensor is needed");
+    on_device(t->device().index(), "workspace");
+    return {t->data_ptr(), size_t(t->nbytes())};
+}
+
+// fmt, W, n_out, n_in, x, y, workspace, bias, activation, residual, stream
+PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded(n_args, 11, [&] {
+        const int fmt = small(a[0], "fmt"), f = small(a[8], "activation");
+        const int64_t n_out = integer(a[2], "n_out"), n_in = integer(a[3], "n_in"), width = f == QG_F_SWIGLU ? n_out / 2 : n_out;
+        const at::ScalarType type = act_type(a[4], "x");
+        const Rows x = rows(a[4], type, "x"), y = rows(a[5], type, "y"), r = rows(a[9], type, "residual");
+        if (!y.p && x.n > 0) refuse(PyExc_ValueError, "y", "a tensor is needed");
+        if (x.width != n_in || y.n != x.n || y.width != width) refuse(PyExc_ValueError, "qgemm", "x or y does not fit n_in, n_out or the tokens");
+        if (a[9] != Py_None && (r.n != x.n || r.width != width)) refuse(PyExc_ValueError, "residual", "a matrix like y is needed");
+        const Space ws = space(a[6]);
+        return call_gemm(qg_fmt(fmt), packed(a[1], fmt, n_out, n_in), n_out, n_in, act_of(type), x.p, x.stride, x.n, f32(a[7], "bias", n_out),
+                         qg_activation(f), r.p, r.stride, y.p, y.stride, ws.p, ws.bytes, stream_of(a[10]));
+    });
+}
+
+// fmt, W, n_experts, n_out, n_in, x, offsets, y, workspace, rows, activation, stream
+PyObject* gemm_experts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded(n_args, 12, [&] {
+        const int fmt = small(a[0], "fmt"), f = small(a[10], "activation"), n_experts = small(a[2], "n_experts");
+        const int64_t n_out = integer(a[3], "n_out"), n_in = integer(a[4], "n_in"), width = f == QG_F_SWIGLU ? n_out / 2 : n_out;
+        const at::ScalarType type = act_type(a[5], "x");
+        const Rows x = rows(a[5], type, "x"), y = rows(a[7], type, "y");
+        if (a[7] == Py_None) refuse(PyExc_ValueError, "y", "a tensor is needed");
+        if (x.width != n_in || y.width != width) refuse(PyExc_ValueError, "qgemm_experts", "x or y does not fit n_in or n_out");
+        if (n_experts < 1 || n_out < 1 || n_out > (int64_t(1) << 31)) refuse(PyExc_ValueError, "qgemm_experts", "n_experts and n_out are positive");
+        const int32_t* const offsets = i32(a[6], "offsets", int64_t(n_experts) + 1);
+        const int32_t* const which = i32(a[9], "rows", y.n);
+        const Space ws = space(a[8]);
+        return call_gemm_experts(qg_fmt(fmt), packed(a[1], fmt, int64_t(n_experts) * n_out, n_in), n_experts, n_out, n_in, act_of(type), x.p,
+                                 x.stride, x.n, offsets, which, y.n, qg_activation(f), y.p, y.stride, ws.p, ws.bytes, stream_of(a[11]));
+    });
+}
+
+// q, k, v, cu_seq, out, workspace, scale, longest, window, lse, stream
+PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded(n_args, 11, [&] {
+        const at::ScalarType type = act_type(a[0], "q");
+        const Heads q = heads(a[0], type, "q"), k = heads(a[1], type, "k"), v = heads(a[2], type, "v"), out = heads(a[4], type, "out");
+        if (a[1] == Py_None || a[2] == Py_None || a[4] == Py_None) refuse(PyExc_ValueError, "qg_prompt_attention", "k, v and out are tensors");
+        if (k.n != q.n || v.n != q.n || out.n != q.n || k.dim != q.dim || v.dim != q.dim || out.dim != q.dim || v.heads != k.heads ||
+            out.heads != q.heads || q.heads > 65535 || k.heads > 65535 || q.dim > 65536)
+            refuse(PyExc_ValueError, "qg_prompt_attention", "q, k, v and out differ in tokens, heads or head_dim");
+        const int64_t n_seq = length(a[3], "cu_seq") - 1;
+        if (n_seq < 0) refuse(PyExc_ValueError, "cu_seq", "n_seq + 1 entries are needed");
+        const Space ws = space(a[5]);
+        return call_prompt_attention(act_of(type), q.p, q.stride, k.p, k.stride, v.p, v.stride, q.n, int(q.heads), int(k.heads), int(q.dim),
+                                     i32(a[3], "cu_seq"), int(std::min<int64_t>(n_seq, 1 << 30)), small(a[7], "longest"), small(a[8], "window"),
+                                     real(a[6], "scale"), out.p, out.stride, f32(a[9], "lse", q.n * q.heads), ws.p, ws.bytes, stream_of(a[10]));
+    });
+}
+
+// The addresses of the calls in the loaded library.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-    return guarded(n_args, 4, [&] {
+    return guarded(n_args, 8, [&] {
+        call_packed_bytes = reinterpret_cast<decltype(call_packed_bytes)>(address(a[4]));
+        call_gemm = reinterpret_cast<decltype(call_gemm)>(address(a[5]));
+        call_gemm_experts = reinterpret_cast<decltype(call_gemm_experts)>(address(a[6]));
+        call_prompt_attention = reinterpret_cast<decltype(call_prompt_attention)>(address(a[7]));
         call_cache_pages = reinterpret_cast<decltype(call_cache_pages)>(address(a[0]));
         call_qk_norm_rope = reinterpret_cast<decltype(call_qk_norm_rope)>(address(a[1]));
         call_cache_append = reinterpret_cast<decltype(call_cache_append)>(address(a[2]));
@@ -268,6 +365,9 @@ PyMethodDef methods[] = {
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(cache_append)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attention)), METH_FASTCALL, nullptr},
+    {"gemm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(gemm)), METH_FASTCALL, nullptr},
+    {"gemm_experts", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(gemm_experts)), METH_FASTCALL, nullptr},
+    {"prompt_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prompt_attention)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "qg_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

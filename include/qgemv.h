@@ -483,6 +483,81 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
                        int n_req, int max_new, int window, const uint32_t* span_mask, float scale, void* out,
                        int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- whole prompts
+ * The products and the attention of a layer for prompts: any number of tokens in a pass, where
+ * the mat-vec, the experts' mat-vec and qg_attention above serve the few of a decode or verify
+ * step.  (The pages leave the prompt to the host program; these calls have no counterpart there.)
+ *
+ * qgemm: y[t] = f(W x[t] + bias) + residual[t],  t < ntok, W as in qgemv.
+ *   act          the type of x, residual and y: QG_ACT_F32 or QG_ACT_BF16.
+ *   x            device act [ntok][n_in], rows x_stride elements apart, 16-byte aligned, strides
+ *                a multiple of 16 bytes.
+ *   bias         device fp32 [n_out], or NULL.
+ *   f            none; silu(v) = v / (1 + exp(-v)); gelu(v) = v / 2 (1 + erf(v / sqrt 2)), or with
+ *                tanh: v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))); swiglu: rows 2j and 2j + 1
+ *                of W are gate j and up j (n_out even), silu(gate) * up, n_out / 2 outputs.
+ *   residual     device act, rows of y's width residual_stride elements apart, or NULL; may be y
+ *                itself, with y's stride.
+ *   y            device act [ntok][n_out] ([n_out / 2] with swiglu), rows y_stride elements apart;
+ *                aligned to an element.  Does not overlap x, W, bias, or (but for y itself) residual.
+ *   workspace    device, >= qgemm_workspace_bytes(fmt, act, n_out, n_in, ntok, 0) bytes, 16-byte
+ *                aligned; it need not be cleared.  Calls that share one must be serialized.
+ * Sums are fp32.  fp32 activations enter as two 16-bit terms each of x and W (22 bits of x below
+ * the row's largest value, all bits of W; bf16 weights: all 24 bits of x); bf16 ones as they are,
+ * weights of the quantized formats then rounded to 11 bits (2^-12 of each).  Quantized weights of
+ * magnitude 65520 and more count as infinite; values of x below 2^-39 of their row's largest as zero.
+ * Inputs that are not finite make the outputs they enter not finite.  A token's outputs do not depend
+ * on the other tokens' values; the order of a sum depends on n_in alone.
+ * n_out, n_in as in qgemv (n_in has no upper limit but 2^24); ntok >= 0, below 2^31 - 1024.
+ * Errors: QG_EINVAL (format, type, shape, null pointer, odd n_out with swiglu, y = x), QG_EALIGN,
+ * QG_EWORKSPACE, QG_EUNSUPPORTED (2^31 tiles of 128 rows and 32 tokens or more), QG_ECUDA.
+ *
+ * qgemm_experts: for every expert e and slot s, offsets[e] <= s < offsets[e + 1],
+ *     y[s] = f(W_e x_row(s)),  x_row(s) = x[rows[s]], or x[s] where rows is NULL,
+ *   W_e as in qgemv_experts (n_experts stacked n_out-row matrices).  x has n_x rows.
+ *   offsets      device int32 [n_experts + 1], growing, within 0..n_slots: the slots sorted by expert.
+ *                Slots outside offsets[0]..offsets[n_experts] are left as they are.  Offsets that
+ *                shrink or leave 0..n_slots set QG_DEVICE_BAD_PLAN and nothing is written.
+ *   rows         device int32 [n_slots]; one outside 0..n_x - 1 sets QG_DEVICE_BAD_PLAN, its slot is
+ *                computed as if x's row were zeros.
+ *   workspace    >= qgemm_workspace_bytes(fmt, act, n_out, n_in, n_slots, n_experts) bytes.
+ *   n_experts <= 65536.  Other arguments, numbers and errors as in qgemm. */
+typedef enum { QG_F_NONE = 0, QG_F_SILU = 1, QG_F_GELU = 2, QG_F_GELU_TANH = 3, QG_F_SWIGLU = 4 } qg_activation;
+size_t    qgemm_workspace_bytes(qg_fmt fmt, qg_act act, int64_t n_out, int64_t n_in, int64_t n_slots, int64_t n_experts);
+qg_status qgemm(qg_fmt fmt, const void* W, int64_t n_out, int64_t n_in, qg_act act, const void* x, int64_t x_stride,
+                int64_t ntok, const float* bias, qg_activation f, const void* residual, int64_t residual_stride, void* y,
+                int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);
+qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_out, int64_t n_in, qg_act act, const void* x,
+                        int64_t x_stride, int64_t n_x, const int32_t* offsets, const int32_t* rows, int64_t n_slots,
+                        qg_activation f, void* y, int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* qg_prompt_attention: causal attention within each of n_seq prompts whose tokens lie one after
+ * the other (packed): of prompt r, rows cu_seq[r] .. cu_seq[r + 1] of q, k and v,
+ *     s_j = scale * q_i . k_j,   out_i = sum_j softmax(s)_j v_j,   lse_i = log sum_j exp(s_j)
+ *   over the prompt's tokens j <= i, with window > 0 only those j > i - window; query head h reads
+ *   key/value head h / (n_heads / n_kv_heads).
+ *   q, out       device act [n_tok][n_heads][head_dim], tokens q_stride / out_stride elements apart;
+ *   k, v         device act [n_tok][n_kv_heads][head_dim] likewise (the slices of a projection's row, or
+ *                qg_cache_append's k_back and v_back, which are what later steps read from the cache).
+ *                head_dim 64, 128 or 256; 16-byte aligned, strides a multiple of 16 bytes.
+ *                out does not overlap q, k or v.
+ *   cu_seq       device int32 [n_seq + 1], as qg_cache_pages leaves cu_new where nothing was held.
+ *                Tokens outside cu_seq[0] .. cu_seq[n_seq] are neither read nor written.  Entries that
+ *                shrink or leave 0..n_tok set QG_DEVICE_BAD_LENGTH and nothing is written.
+ *   longest      a prompt's most tokens (at least 1): chooses the launch; results are right for any value.
+ *   lse          device fp32 [n_tok][n_heads] (natural logarithm), or NULL.
+ *   workspace    device, >= qg_prompt_attention_workspace_bytes(act, n_tok, n_heads, n_kv_heads, head_dim)
+ *                bytes, 16-byte aligned; it need not be cleared.  Calls that share one must be serialized.
+ *   n_seq <= 16384; n_heads a multiple of n_kv_heads, at most 128 to one key/value head.
+ * A masked key or value (of a later token, beyond the window, of another prompt) has no effect whatever
+ * it holds; a visible one that is not finite makes the outputs that see it not finite.
+ * Errors: QG_EINVAL, QG_EALIGN, QG_EWORKSPACE, QG_EUNSUPPORTED, QG_ECUDA. */
+size_t    qg_prompt_attention_workspace_bytes(qg_act act, int64_t n_tok, int n_heads, int n_kv_heads, int head_dim);
+qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, int64_t n_tok, int n_heads, int n_kv_heads, int head_dim, const int32_t* cu_seq,
+                              int n_seq, int longest, int window, float scale, void* out, int64_t out_stride, float* lse,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------- qgemv_argmax_noalloc
  * No counterpart on the source pages: an addition for callers that cannot call
  * cudaMalloc, such as a plugin inside a host framework that owns every device
