@@ -261,16 +261,29 @@ int tile_tokens(bool f32, int64_t m_tiles, int64_t n_slots, int64_t n_experts, i
     return best;
 }
 
-qg_status encode(CUtensorMap* map, const void* p, int64_t inner, int64_t rows, int64_t terms, int64_t pitch, int box_rows) {
+qg_status encode_tokens(CUtensorMap* map, const void* p, int64_t inner, int64_t rows, int64_t terms, int64_t pitch, int box_rows) {
     const EncodeTiledFn enc = encode_tiled();
     if (!enc) return QG_ECUDA;
     const cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(terms)};
     const cuuint64_t strides[2] = {cuuint64_t(pitch), terms > 1 ? cuuint64_t(pitch) * cuuint64_t(rows) : cuuint64_t(pitch)};
     const cuuint32_t box[3] = {kGemmK, cuuint32_t(box_rows), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, terms > 0 ? 3 : 2, const_cast<void*>(p), dims, strides, box, estr,
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QG_OK : QG_ECUDA;
+}
+// Boxes of 128 rows of W, `width` elements wide.
+qg_status encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* W, int64_t inner, int64_t rows, int64_t pitch, int width,
+                    CUtensorMapSwizzle swizzle) {
+    const EncodeTiledFn enc = encode_tiled();
+    if (!enc) return QG_ECUDA;
+    const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(pitch)};
+    const cuuint32_t box[2] = {cuuint32_t(width), kGemmRows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, type, 2, const_cast<void*>(W), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? QG_OK : QG_ECUDA;
 }
 
@@ -291,8 +304,6 @@ qg_status launch_gemm(const GemmCall& c) {
     const bool stages_x = quant || f32 || c.rows;
 
     GemmArgs a{};
-    a.W = static_cast<const uint8_t*>(c.W);
-    a.row_bytes = row_stride(c.fmt, c.n_in);
     a.n_out = int(c.n_out);
     a.n_in = int(c.n_in);
     a.n_slots = int(c.n_slots);
@@ -315,13 +326,26 @@ qg_status launch_gemm(const GemmCall& c) {
     a.extra_tx = test_extra_tx();
     const void* const fn = qgemm_lookup(c.fmt, f32);
     const size_t stage = size_t(terms_w(c.fmt, f32)) * kOperandA + size_t(terms_x(c.fmt, f32)) * size_t(bn) * kGemmK * 2;
-    const size_t raw = size_t(kDecodeWarps) * kRawSlots * size_t(raw_bytes(c.fmt));
-    a.stages = int(std::min<size_t>(8, (size_t(optin) - kStaticSmemReserve - 1024 - raw) / stage));
-    const size_t smem = 1024 + raw + size_t(a.stages) * stage;
+    // Four stages of operands (fewer if they do not fit), the rest of shared memory holds raw codes
+    // on their way: few tokens to a tile leave room for a deep ring, which is what they need.  An even
+    // number of raw steps: a slot then always belongs to the same four decoding warps, which wait for
+    // its fills one by one.
+    const size_t raw = size_t(kGemmRows) * size_t(raw_codes(c.fmt)), scales = size_t(kGemmRows) * kScaleSlots * size_t(raw_scales(c.fmt));
+    const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
+    a.stages = int(std::min<size_t>(quant ? 4 : 8, (room - 2 * raw) / stage));
+    a.raws = quant ? int(std::min<size_t>(kMostRaws, (room - size_t(a.stages) * stage) / raw)) / 2 * 2 : 0;
+    const size_t smem = 1024 + scales + size_t(a.raws) * raw + size_t(a.stages) * stage;
     if (a.stages < 2 || blocks_per_sm(fn, dev, optin, kGemmThreads, smem) < 1) return QG_EUNSUPPORTED;
-    st = stages_x ? encode(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, bn)
-                  : encode(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, bn);
-    if (st == QG_OK && !quant) st = encode(&a.wmap, c.W, c.n_in, std::max<int64_t>(1, c.n_experts) * c.n_out, 0, a.row_bytes, kGemmRows);
+    const int64_t rows = std::max<int64_t>(1, c.n_experts) * c.n_out, pitch = row_stride(c.fmt, c.n_in);
+    st = stages_x ? encode_tokens(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, bn)
+                  : encode_tokens(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, bn);
+    if (st == QG_OK && !quant)
+        st = encode_2d(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.W, c.n_in, rows, pitch, kGemmK, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st == QG_OK && quant)
+        st = encode_2d(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.W, pitch, rows, pitch, raw_codes(c.fmt),
+                       c.fmt == QG_Q8_0 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+    if (st == QG_OK && quant)
+        st = encode_2d(&a.smap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.W, pitch, rows, pitch, raw_scales(c.fmt), CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != QG_OK) return st;
 
     const bool before = stages_x || c.n_experts > 0;

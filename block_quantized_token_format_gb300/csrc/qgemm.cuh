@@ -4,9 +4,10 @@
 //
 // A tile is 128 rows of W times `bn` tokens; the products run on tcgen05 with W's rows as M (the
 // accumulators' lanes) and tokens as N, in steps of 64 along K:
-//   * eight warps turn W's codes into 16-bit floats: each keeps its own 16 rows' raw codes and
-//     scales a few steps ahead in shared memory (cp.async) and writes a step's 128 x 64 operand;
-//   * one thread copies the tokens' operand (staged by stage_kernel, below) with tensor copies;
+//   * one thread copies, with tensor copies, W's raw codes (each step) and scales (every fourth)
+//     into one ring and the tokens' operand (staged by stage_kernel, qgemm.cu) into another;
+//   * eight warps turn the codes into 16-bit floats, a lane a row: four of them one step, the other
+//     four the next;
 //   * one thread issues the products;
 //   * eight warps empty the accumulators, of which there are two sets, so that a tile's epilogue
 //     runs beside the next one's products.
@@ -34,22 +35,23 @@ namespace qg {
 
 constexpr int kGemmRows = 128, kGemmK = 64;
 constexpr int kDecodeWarps = 8, kDrainWarps = 8;
-constexpr int kGemmThreads = 32 * (kDecodeWarps + kDrainWarps + 2);
-constexpr int kRawSlots = 3;                 // steps of raw codes a decoding warp holds
+constexpr int kGemmThreads = 32 * (kDecodeWarps + kDrainWarps + 4);
 constexpr int kChunkSteps = 4;               // fp32: steps of K between moves to registers
+constexpr int kMostRaws = 16;
+
 constexpr int kOperandA = kGemmRows * kGemmK * 2;
 
-__host__ __device__ constexpr int raw_codes(int fmt) { return fmt == QG_Q8_0 ? 64 : fmt == QG_BF16 ? 0 : 32; }                        // bytes of 64 weights
-__host__ __device__ constexpr int raw_scales(int fmt) { return fmt == QG_BF16 ? 0 : fmt == QG_Q5_0 ? 12 : 4; }
-__host__ __device__ constexpr int raw_bytes(int fmt) { return 16 * (raw_codes(fmt) + raw_scales(fmt)); }                              // of a warp's 16 rows
+// Raw codes of a step (64 weights of 128 rows) and raw scales of four steps, as their copies' boxes
+// bring them: bytes of a row.
+constexpr int kScaleSteps = 4, kScaleSlots = 4;
+__host__ __device__ constexpr int raw_codes(int fmt) { return fmt == QG_Q8_0 ? 64 : fmt == QG_BF16 ? 0 : 32; }
+__host__ __device__ constexpr int raw_scales(int fmt) { return fmt == QG_BF16 ? 0 : fmt == QG_Q5_0 ? 48 : 16; }
 __host__ __device__ constexpr int terms_w(int fmt, bool f32) { return f32 && fmt != QG_BF16 ? 2 : 1; }
 __host__ __device__ constexpr int terms_x(int fmt, bool f32) { return !f32 ? 1 : fmt == QG_BF16 ? 3 : 2; }
 __host__ __device__ constexpr int gemm_most_tokens(bool f32) { return f32 ? 128 : 256; }                                              // of a tile
 
 struct GemmArgs {
-    CUtensorMap xmap, wmap;        // staged tokens [terms][n_slots][n_in]; bf16 weights
-    const uint8_t* W;
-    long long row_bytes;
+    CUtensorMap xmap, wmap, smap;  // staged tokens [terms][n_slots][n_in]; rows of W: codes (or bf16), scales
     int n_out, n_in, n_slots, n_experts;      // n_experts 0: one matrix
     const int32_t* offsets;                   // experts: the caller's, and the tiles before each expert
     const int32_t* tile_start;
@@ -58,7 +60,7 @@ struct GemmArgs {
     const void* residual;
     void* y;
     long long residual_stride, y_stride;
-    int f, bn, stages, m_tiles, n_tiles;
+    int f, bn, stages, raws, m_tiles, n_tiles;
     unsigned int* status;
     uint32_t wait_limit, drain_limit, extra_tx;
 };
@@ -98,12 +100,6 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& a, int t) {
     g.w_row0 = lo * a.n_out + g.row0;
     return g;
 }
-
-// A position in the sequence of steps that a CTA's tiles make.
-struct StepWalk {
-    int tile, k;
-    GemmTile g;
-};
 
 // ------------------------------------------------------------------------- codes to fp16
 
@@ -167,10 +163,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
     constexpr int kStepWeights = FMT == QG_Q8_0 ? 512 : 1024;        // of a layout step
     using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_mem[3 * 8 + 5];
+    __shared__ uint64_t bar_mem[3 * 8 + 5 + 2 * kMostRaws + 2 * kScaleSlots];
     __shared__ uint32_t tmem_at, dead;
 
-    const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t b_bytes = uint32_t(a.bn) * kGemmK * 2, stage_bytes = TW * kOperandA + TX * b_bytes;
     const uint32_t raw0 = base + uint32_t(a.stages) * stage_bytes;
@@ -181,6 +177,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
     auto acc_full = [&](int b) { return bars + 8u * uint32_t(24 + b); };
     auto acc_empty = [&](int b) { return bars + 8u * uint32_t(26 + b); };
     const uint32_t drained = bars + 8u * 28u;
+    auto raw_full = [&](int r) { return bars + 8u * uint32_t(29 + r); };
+    auto raw_empty = [&](int r) { return bars + 8u * uint32_t(29 + kMostRaws + r); };
+    auto sc_full = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + r); };
+    auto sc_empty = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + kScaleSlots + r); };
     const uint32_t acc_cols = uint32_t(a.bn) * (F32 ? 2 : 1);                    // of one set
     const uint32_t tmem_cols = max(32u, 2 * acc_cols);
     const tc::Waits wait{&dead, a.status, a.wait_limit};
@@ -190,12 +190,20 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
         dead = 0;
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(full_b(s), 1);
-            mbar_init(full_a(s), kDecodeWarps);
+            mbar_init(full_a(s), kDecodeWarps / 2);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
             mbar_init(acc_empty(b), kDrainWarps);
+        }
+        for (int r = 0; r < a.raws; ++r) {
+            mbar_init(raw_full(r), 1);
+            mbar_init(raw_empty(r), kDecodeWarps / 2);
+        }
+        for (int r = 0; r < kScaleSlots; ++r) {
+            mbar_init(sc_full(r), 1);
+            mbar_init(sc_empty(r), kDecodeWarps);
         }
         mbar_init(drained, 1);
         mbar_fence_init();
@@ -252,7 +260,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
             };
             for (int ch = 0; ch < chunks; ++ch, ++it) {
                 const int b = int(it & 1);
-                if (!wait.warp(acc_full(b), (it >> 1) & 1)) { alive = false; break; }
+                if (!wait(acc_full(b), (it >> 1) & 1)) { alive = false; break; }
                 tc::fence_after();
                 const uint32_t acc = tmem + lanes + uint32_t(b) * acc_cols + uint32_t(half * hc);
                 if constexpr (F32) {
@@ -260,11 +268,11 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                     for (int u = 0; u < 4; ++u)
                         if (u * 16 < hc) {
                             tc::tmem_load16(acc + uint32_t(a.bn) + u * 16, v);
-                            tc::tmem_load_wait();
+                            tc::tmem_load_wait16(v);
 #pragma unroll
                             for (int c = 0; c < 16; ++c) sum[u * 16 + c] = ch == 0 ? __uint_as_float(v[c]) : sum[u * 16 + c] + __uint_as_float(v[c]);
                             tc::tmem_load16(acc + u * 16, v);
-                            tc::tmem_load_wait();
+                            tc::tmem_load_wait16(v);
 #pragma unroll
                             for (int c = 0; c < 16; ++c) sum[u * 16 + c] += __uint_as_float(v[c]);
                         }
@@ -276,7 +284,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                         const bool two = (u + 1) * 16 < hc;
                         tc::tmem_load16(acc + u * 16, v);
                         if (two) tc::tmem_load16(acc + u * 16 + 16, v + 16);
-                        tc::tmem_load_wait();
+                        tc::tmem_load_wait32(v);
                         float x[32];
 #pragma unroll
                         for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]);
@@ -303,112 +311,83 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
         if constexpr (kQuant) {
             constexpr int CB = raw_codes(FMT), SB = raw_scales(FMT);
             if (a.n_experts) tc::grid_wait();
-            const int w = warp - kDrainWarps, r = lane >> 1, h = lane & 1, row = w * 16 + r;
-            const uint32_t raw = raw0 + uint32_t(w) * (kRawSlots * raw_bytes(FMT));
+            const int w = warp - kDrainWarps, row = (w & 3) * 32 + lane, which = w >> 2;
+            const uint32_t scales0 = raw0 + uint32_t(a.raws) * (kGemmRows * CB);
             const int tiles = gemm_tiles(a);
-            const long long step_bytes = 512 + 512 / CB * SB;
-            const int last = (a.n_in - 1) / kStepWeights;
-            const int last_codes = (a.n_in - last * kStepWeights) * CB / 64;
-            // Requests raw step `n` (its place in the ring); always one group, empty past the end.
-            StepWalk f{int(blockIdx.x), 0, {}};
-            const uint8_t* src = a.W;
-            bool there = false;
-            auto enter = [&]() {
-                if (f.tile >= tiles) return;
-                f.g = gemm_tile(a, f.tile);
-                there = f.g.row0 + row < a.n_out;
-                src = a.W + (there ? (long long)(f.g.w_row0 + row) * a.row_bytes : 0ll);
-            };
-            enter();
-            auto fetch = [&](uint32_t n) {
-                if (f.tile < tiles) {
-                    const uint32_t slot = raw + (n % kRawSlots) * raw_bytes(FMT);
-                    const int k0 = f.k * kGemmK, step = k0 / kStepWeights, in = (k0 - step * kStepWeights) / 64;
-                    const uint8_t* const at = src + step * step_bytes;
-                    const int left = there ? a.n_in - k0 : 0;        // weights from here on
-                    constexpr int kPer = FMT == QG_Q8_0 ? 16 : 32;   // weights of 16 bytes
-#pragma unroll
-                    for (int i = 0; i < CB / 32; ++i) {
-                        const int c = 2 * i + h;
-                        const int place = CB == 64 ? c ^ ((r >> 1) & 1) : c;
-                        const bool some = c * kPer < left;
-                        tc::copy16(slot + r * CB + place * 16, some ? at + in * CB + c * 16 : a.W, some ? 16u : 0u);
-                    }
-                    const uint8_t* const sc = at + (step == last ? last_codes : 512) + in * SB;
-                    const uint32_t to = slot + 16 * CB + r * SB;
-                    if constexpr (FMT == QG_Q5_0) {
-                        const int valid = left >= 64 ? 12 : left > 0 ? 6 : 0;
-                        tc::copy4(to + 4 * h, valid ? sc + 4 * h : a.W, valid ? 4 * h + 4 <= valid ? 4u : 2u : 0u);
-                        if (h == 0) tc::copy4(to + 8, valid == 12 ? sc + 8 : a.W, valid == 12 ? 4u : 0u);
-                    } else if (h == 0) {
-                        tc::copy4(to, left > 0 ? sc : a.W, left <= 0 ? 0u : FMT == QG_AFFINE4_G64 || left >= 64 ? 4u : 2u);
-                    }
-                    if (++f.k == ksteps) {
-                        f.k = 0;
-                        f.tile += gridDim.x;
-                        enter();
-                    }
-                }
-                tc::copy_commit();
-            };
-#pragma unroll
-            for (int i = 0; i < kRawSlots - 1; ++i) fetch(i);
-            uint32_t n = 0;
-            int s = 0;
-            uint32_t phase = 0;
+            int s = 0, r = 0, sr = 0;
+            uint32_t phase = 0, raw_phase = 0, n = 0, groups = 0;
             bool alive = true;
             for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
                 for (int k = 0; k < ksteps; ++k, ++n) {
-                    tc::copy_wait<kRawSlots - 2>();
-                    __syncwarp();
-                    const uint32_t slot = raw + (n % kRawSlots) * raw_bytes(FMT);
-                    uint32_t code[CB / 8];
-                    if constexpr (CB == 64) {
+                    if (k % kScaleSteps == 0) {          // the next four steps' scales
+                        if (groups && lane == 0) mbar_arrive(sc_empty(sr));
+                        sr = int(groups % kScaleSlots);
+                        if (!wait(sc_full(sr), groups / kScaleSlots & 1)) { alive = false; break; }
+                        ++groups;
+                    }
+                    if ((n & 1) == uint32_t(which)) {
+                        if (!wait(raw_full(r), raw_phase)) { alive = false; break; }
+                        uint32_t code[2][CB / 8];
+                        const uint32_t at = raw0 + uint32_t(r) * (kGemmRows * CB) + uint32_t(row) * CB;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 q = lds128(slot + r * CB + ((2 * h + i) ^ ((r >> 1) & 1)) * 16);
-                            code[4 * i] = q.x, code[4 * i + 1] = q.y, code[4 * i + 2] = q.z, code[4 * i + 3] = q.w;
+                        for (int c = 0; c < CB / 16; ++c) {          // the copy's swizzle: no two lanes of a phase in a bank
+                            const uint4 q = tc::lds128(at + uint32_t(c ^ (CB == 64 ? (row >> 1) & 3 : (row >> 2) & 1)) * 16);
+                            uint32_t* const to = &code[c * 16 / (CB / 2)][c * 4 % (CB / 8)];
+                            to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
                         }
-                    } else {
-                        const uint4 q = lds128(slot + r * CB + h * 16);
-                        code[0] = q.x, code[1] = q.y, code[2] = q.z, code[3] = q.w;
-                    }
-                    uint32_t fifth = 0;
-                    __half2 d, b;
-                    const uint32_t sc = slot + 16 * CB + r * SB;
-                    if constexpr (FMT == QG_Q5_0) {
-                        const uint32_t w0 = lds32(sc), w1 = lds32(sc + 4), w2 = lds32(sc + 8);
-                        fifth = h ? (w1 >> 16) | (w2 << 16) : w0;
-                        d = __half2half2(__ushort_as_half(static_cast<unsigned short>(h ? w2 >> 16 : w1)));
-                        b = d;
-                    } else {
-                        const uint32_t w0 = lds32(sc);
-                        const __half l = __ushort_as_half(static_cast<unsigned short>(w0)), u = __ushort_as_half(static_cast<unsigned short>(w0 >> 16));
-                        d = __half2half2(FMT == QG_AFFINE4_G64 || !h ? l : u);
-                        b = __half2half2(u);
-                    }
-                    fetch(n + kRawSlots - 1);
-                    uint32_t hi[16], lo[16];
-                    decode32<FMT, F32>(code, fifth, d, b, hi, lo);
-                    if (!wait.warp(empty(s), phase ^ 1)) { alive = false; break; }
-                    const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(row) * 128;
+                        const uint32_t sc = scales0 + uint32_t(sr) * (kGemmRows * SB) + uint32_t(row) * SB + uint32_t(k % kScaleSteps) * (SB / 4);
+                        uint32_t fifth[2] = {0, 0}, half[2];
+                        if constexpr (FMT == QG_Q5_0) {
+                            const uint32_t w0 = tc::lds32(sc), w1 = tc::lds32(sc + 4), w2 = tc::lds32(sc + 8);
+                            fifth[0] = w0, half[0] = w1 & 0xFFFFu;
+                            fifth[1] = (w1 >> 16) | (w2 << 16), half[1] = w2 >> 16;
+                        } else {
+                            const uint32_t w0 = tc::lds32(sc);
+                            half[0] = w0 & 0xFFFFu, half[1] = w0 >> 16;
+                        }
+                        const bool tail = k * kGemmK + 32 >= a.n_in;             // the second half is past the row's end
+                        const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(row) * 128;
+                        bool ready = false;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t at = to + uint32_t(((4 * h + c) ^ (row & 7)) * 16);
-                        sts128(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                        if constexpr (F32) sts128(at + kOperandA, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t hi[16], lo[16];
+                            __half2 d, b;
+                            if constexpr (FMT == QG_AFFINE4_G64) {
+                                d = __half2half2(__ushort_as_half(static_cast<unsigned short>(half[0])));
+                                b = __half2half2(__ushort_as_half(static_cast<unsigned short>(half[1])));
+                            } else {
+                                d = b = __half2half2(__ushort_as_half(static_cast<unsigned short>(h && tail ? 0u : half[h])));
+                            }
+                            decode32<FMT, F32>(code[h], fifth[h], d, b, hi, lo);
+                            if (h == 1 && FMT != QG_AFFINE4_G64 && tail) {       // codes there are other bytes of the row
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0;
+                            }
+                            if (h == 0 && !wait(empty(s), phase ^ 1)) { alive = false; break; }
+                            ready = true;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t p = to + uint32_t(((4 * h + c) ^ (row & 7)) * 16);
+                                sts128(p, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                                if constexpr (F32) sts128(p + kOperandA, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                            }
+                        }
+                        if (!ready) break;
+                        tc::fence_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(full_a(s));
+                            mbar_arrive(raw_empty(r));           // (what was read has been used: no load is still under way)
+                        }
                     }
-                    tc::fence_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full_a(s));
                     if (++s == a.stages) { s = 0; phase ^= 1; }
+                    if (++r == a.raws) { r = 0; raw_phase ^= 1; }
                 }
             }
-            tc::copy_wait<0>();
         }
     } else if (warp == kDrainWarps + kDecodeWarps) {
         // ------------------------------------------------------------- tokens (and bf16 W)
-        if (lane == 0) {
+        {
             tc::grid_wait();
             const int tiles = gemm_tiles(a);
             const uint32_t bytes = TX * b_bytes + (kQuant ? 0 : kOperandA);
@@ -421,11 +400,14 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                 for (int k = 0; k < ksteps; ++k) {
                     if (!wait(empty(s), phase ^ 1)) { alive = false; break; }
                     const uint32_t at = base + uint32_t(s) * stage_bytes;
-                    mbar_arrive_expect_tx(full_b(s), bytes + extra);
-                    extra = 0;
-                    if constexpr (!kQuant) tc::load_2d(at, &a.wmap, k * kGemmK, g.w_row0, full_b(s));
+                    if (tc::elect()) {
+                        mbar_arrive_expect_tx(full_b(s), bytes + extra);
+                        if constexpr (!kQuant) tc::load_2d(at, &a.wmap, k * kGemmK, g.w_row0, full_b(s));
 #pragma unroll
-                    for (int x = 0; x < TX; ++x) tc::load_3d(at + TW * kOperandA + x * b_bytes, &a.xmap, k * kGemmK, g.slot0, x, full_b(s));
+                        for (int x = 0; x < TX; ++x) tc::load_3d(at + TW * kOperandA + x * b_bytes, &a.xmap, k * kGemmK, g.slot0, x, full_b(s));
+                    }
+                    __syncwarp();
+                    extra = 0;
                     ++filled;
                     if (++s == a.stages) { s = 0; phase ^= 1; }
                 }
@@ -438,9 +420,59 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                 }
             }
         }
-    } else {
+    } else if (warp == kDrainWarps + kDecodeWarps + 2) {
+        // ------------------------------------------------------------- raw codes and scales
+        if constexpr (kQuant) {
+            {
+                constexpr int CB = raw_codes(FMT), SB = raw_scales(FMT), kSteps = kStepWeights / kGemmK;
+                if (a.n_experts) tc::grid_wait();
+                const int tiles = gemm_tiles(a);
+                const uint32_t scales0 = raw0 + uint32_t(a.raws) * (kGemmRows * CB);
+                constexpr int kStepBytes = 512 + kSteps / kScaleSteps * SB;
+                const int last = (a.n_in - 1) / kStepWeights, last_codes = (a.n_in - last * kStepWeights) * CB / kGemmK;
+                int r = 0;
+                uint32_t phase = 0, filled = 0, groups = 0;
+                bool alive = true;
+                for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+                    const GemmTile g = gemm_tile(a, t);
+                    for (int k = 0; k < ksteps; ++k) {
+                        if (!wait(raw_empty(r), phase ^ 1)) { alive = false; break; }
+                        const int step = k / kSteps, in = k % kSteps;
+                        if (k % kScaleSteps == 0) {
+                            const int sr = int(groups % kScaleSlots);
+                            if (!wait(sc_empty(sr), (groups / kScaleSlots & 1) ^ 1)) { alive = false; break; }
+                            ++groups;
+                            if (tc::elect()) {
+                                mbar_arrive_expect_tx(sc_full(sr), kGemmRows * SB);
+                                tc::load_2d(scales0 + uint32_t(sr) * (kGemmRows * SB), &a.smap,
+                                            step * kStepBytes + (step == last ? last_codes : 512) + in / kScaleSteps * SB, g.w_row0, sc_full(sr));
+                            }
+                            __syncwarp();
+                        }
+                        if (tc::elect()) {
+                            mbar_arrive_expect_tx(raw_full(r), kGemmRows * CB);
+                            tc::load_2d(raw0 + uint32_t(r) * (kGemmRows * CB), &a.wmap, step * kStepBytes + in * CB, g.w_row0, raw_full(r));
+                        }
+                        __syncwarp();
+                        ++filled;
+                        if (++r == a.raws) { r = 0; phase ^= 1; }
+                    }
+                }
+                if (dead) {
+                    for (uint32_t i = 0; i < uint32_t(a.raws) && i < filled; ++i) {
+                        const uint32_t n = filled - 1 - i;
+                        mbar_wait(raw_full(int(n % a.raws)), (n / a.raws) & 1, a.drain_limit);
+                    }
+                    for (uint32_t i = 0; i < uint32_t(kScaleSlots) && i < groups; ++i) {
+                        const uint32_t n = groups - 1 - i;
+                        mbar_wait(sc_full(int(n % kScaleSlots)), (n / kScaleSlots) & 1, a.drain_limit);
+                    }
+                }
+            }
+        }
+    } else if (warp == kDrainWarps + kDecodeWarps + 1) {
         // ---------------------------------------------------------------------- products
-        if (lane == 0) {
+        {
             if (a.n_experts) tc::grid_wait();
             const int tiles = gemm_tiles(a);
             const uint32_t idesc = tc::instr(!kQuant, a.bn, false);
@@ -458,6 +490,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                     const uint32_t acc = tmem + uint32_t(b) * acc_cols, cross = acc + uint32_t(a.bn);
                     const uint32_t at = base + uint32_t(s) * stage_bytes, bt = at + TW * kOperandA;
                     const uint64_t da = tc::desc_k(at), db = tc::desc_k(bt);
+                    if (tc::elect()) {
 #pragma unroll
                     for (int j = 0; j < kGemmK / 16; ++j) {
                         const bool add = !first || j > 0;
@@ -471,15 +504,16 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                         tc::mma(acc, aj, bj, idesc, add);
                     }
                     tc::commit(empty(s));
-                    if (lastk) {
-                        tc::commit(acc_full(b));
-                        ++it;
+                    if (lastk) tc::commit(acc_full(b));
                     }
+                    __syncwarp();
+                    if (lastk) ++it;
                     if (++s == a.stages) { s = 0; phase ^= 1; }
                 }
             }
             // Products still under way end before the accumulators are given back.
-            tc::commit(drained);
+            if (tc::elect()) tc::commit(drained);
+            __syncwarp();
             mbar_wait(drained, 0, a.drain_limit);
         }
     }

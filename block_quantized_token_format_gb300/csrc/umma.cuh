@@ -93,8 +93,27 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
 }
 #undef QG_R16
 #undef QG_R4
-__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the warp's loads; their values pass through, so that no use of them comes before.
+#define QG_R4(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3])
+#define QG_R16(v, i) QG_R4(v, i), QG_R4(v, i + 4), QG_R4(v, i + 8), QG_R4(v, i + 12)
+__device__ __forceinline__ void tmem_load_wait16(uint32_t* v) { asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_R16(v, 0) :: "memory"); }
+__device__ __forceinline__ void tmem_load_wait32(uint32_t* v) {
+    // (30 operands are the most that one statement takes both ways: a wait that is over costs nothing.)
+    tmem_load_wait16(v);
+    tmem_load_wait16(v + 16);
+}
+#undef QG_R16
+#undef QG_R4
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// True in one lane of a whole warp.  The loops that issue products and copies run in the whole warp
+// and only their instructions in this lane: what they take is then known to be the same in all
+// lanes, and stays in the registers that they read it from.
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
 
 // ---------------------------------------------------------------------------- copies
 
@@ -116,6 +135,18 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, uint32_t by
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
+// Shared-memory loads that stay between the barrier operations around them.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+    return r;
+}
+
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -127,19 +158,16 @@ struct Waits {
     volatile uint32_t* dead;       // shared memory
     unsigned int* status;
     uint32_t limit;
+    // The whole warp, with one result.
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
         for (uint32_t i = 0; i < limit; ++i) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if ((i & 31) == 31 && *dead) return false;
+            if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+            if ((i & 31) == 31 && __any_sync(kFullMask, *dead != 0)) return false;
         }
-        if (mbar_try_wait(bar, parity)) return true;
         *dead = 1;
         atomicOr(status, 1u);      // QG_DEVICE_WAIT_TIMEOUT
         return false;
-    }
-    // The whole warp, with one result.
-    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
-        return __all_sync(kFullMask, (*this)(bar, parity));
     }
 };
 
