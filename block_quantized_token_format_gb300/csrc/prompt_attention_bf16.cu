@@ -1,0 +1,320 @@
+// Causal attention of packed prompts, bf16: S = Q K^T and O += P V on tcgen05, softmax by a thread
+// a row.  Shapes and items in prompt_attention.cuh.
+//
+// One CTA is 128 rows.  Four warps hold a row each lane; one warp copies keys and values, one issues
+// the products.  S (fp32) and then P (bf16, over S) lie in tensor memory, P being the second
+// product's operand there, and O is summed there.  A row's reference is raised, and O scaled,
+// only where a tile's maximum is more than 2^8 above it: then rarely after the first tiles.
+// Heads of 64 and 128 take 256 columns of tensor memory and at most 96 KB, so that two CTAs share an
+// SM and the one's softmax runs beside the other's products; heads of 256 fill an SM with one CTA,
+// which issues the next tile's S before it waits for P.
+//
+// Numbers: products of bf16 values are exact, sums fp32; P is rounded to bf16 (2^-9 of each), its
+// sum is not.  A tile on an edge (some row does not see some key) may hold values of keys that
+// other rows, or none, see: one that is not finite would reach every row as 0 * inf.  Such tiles are looked
+// through, those values made zeros for the product, and the rows that see them get them afterwards.
+#include "prompt_attention.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kSoftWarps = 4, kPromptThreads = 32 * (kSoftWarps + 2);
+constexpr float kSlack = 8.0f;     // log2: P is at most 2^8
+
+template <int D> struct Shape {
+    static constexpr int KT = D == 256 ? 64 : 128, STAGES = D == 256 ? 2 : 1, SB = D == 256 ? 2 : 1;
+    static constexpr int CH = D / 64;                                // 64-wide pieces of a head
+    static constexpr int Q_BYTES = CH * 128 * 128, T_BYTES = CH * KT * 128;      // (T: a key or value tile)
+    static constexpr int SMEM = 1024 + Q_BYTES + 2 * STAGES * T_BYTES;
+    static constexpr uint32_t O_AT = SB * KT, COLS = D == 256 ? 512 : 256;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&p);
+}
+// Bits 15 and 31: the halves' exponents are all ones.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) prompt_bf16_kernel(const __grid_constant__ PromptArgs a) {
+    using S = Shape<D>;
+    constexpr int KT = S::KT, CH = S::CH;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bar_mem[16];
+    __shared__ uint32_t tmem_at, dead, odd;
+
+    const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
+    tc::grid_launch_dependents();
+    tc::grid_wait();
+    if (blockIdx.x == gridDim.x - 1) {
+        prompt_check(a);
+        return;
+    }
+    PromptItem it;
+    const int slots = (int(gridDim.x) - 1) / a.n_kv, b = int(blockIdx.x) / a.n_kv;
+    if (!prompt_item(a, slots - 1 - b, int(blockIdx.x) - b * a.n_kv, it)) return;
+    int first, tiles;
+    key_range<KT>(a, it, first, tiles);
+
+    const uint32_t q_at = (smem_addr(smem_raw) + 1023u) & ~1023u, k_at = q_at + S::Q_BYTES, v_at = k_at + S::STAGES * S::T_BYTES;
+    const uint32_t bars = smem_addr(bar_mem);
+    const uint32_t q_full = bars, o_full = bars + 8, pv_done = bars + 16;
+    auto k_full = [&](int s) { return bars + 24u + 8u * uint32_t(s); };
+    auto k_empty = [&](int s) { return bars + 40u + 8u * uint32_t(s); };
+    auto v_full = [&](int s) { return bars + 56u + 8u * uint32_t(s); };
+    auto v_empty = [&](int s) { return bars + 72u + 8u * uint32_t(s); };
+    auto s_full = [&](int s) { return bars + 88u + 8u * uint32_t(s); };
+    auto p_full = [&](int s) { return bars + 104u + 8u * uint32_t(s); };
+    const tc::Waits wait{&dead, a.status, a.wait_limit};
+
+    if (tid == 0) {
+        dead = odd = 0;
+        mbar_init(q_full, 1);
+        mbar_init(o_full, 1);
+        mbar_init(pv_done, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(k_full(s), 1);
+            mbar_init(k_empty(s), 1);
+            mbar_init(v_full(s), 1);
+            mbar_init(v_empty(s), 1);
+            mbar_init(s_full(s), 1);
+            mbar_init(p_full(s), kSoftWarps);
+        }
+        mbar_fence_init();
+    }
+    if (warp == kSoftWarps + 1) tc::tmem_alloc(smem_addr(&tmem_at), S::COLS);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_at;
+
+    if (warp < kSoftWarps) {
+        const int row = warp * 32 + lane, tok = it.t0 + row / a.group;
+        const bool there = row < a.tokens * a.group && tok < it.len;
+        const int pos = there ? tok : -1, low = there && a.window > 0 ? max(0, tok - a.window + 1) : 0;
+        const uint32_t mine = tmem + (uint32_t(warp) << 21);
+        float top = -INFINITY, sum = 0.0f;               // the row's reference (a score), sum of P
+        bool alive = true;
+        for (int j = 0; j < tiles; ++j) {
+            const int k0 = first + j * KT, sb = j % S::SB;
+            if (!wait(s_full(sb), j / S::SB & 1)) { alive = false; break; }
+            tc::fence_after();
+            uint32_t x[KT];
+            const uint32_t at = mine + uint32_t(sb * KT);
+#pragma unroll
+            for (int i = 0; i < KT; i += 32) tc::tmem_load32(at + i, x + i);
+#pragma unroll
+            for (int i = 0; i < KT; i += 16) tc::tmem_load_wait16(x + i);
+            const bool edge = on_edge<KT>(a, it, k0);
+            if (edge) {
+                const int hi = pos - k0, lo = low - k0;
+#pragma unroll
+                for (int i = 0; i < KT; ++i)
+                    if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < KT; i += 8)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) m4[n] = fmaxf(m4[n], fmaxf(__uint_as_float(x[i + 2 * n]), __uint_as_float(x[i + 2 * n + 1])));
+            const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            const bool raise = j == 0 ? most > -INFINITY : (most - top) * a.c > kSlack || (top == -INFINITY && most > -INFINITY);
+            float factor = 1.0f;
+            if (raise) {
+                factor = exp2_of((top - most) * a.c);    // (0 from -infinity)
+                if (top == -INFINITY) factor = 0.0f;
+                top = most;
+                sum *= factor;
+            }
+            if (j > 0 && __any_sync(tc::kFullMask, raise)) {
+                if (!wait(pv_done, (j - 1) & 1)) { alive = false; break; }
+                tc::fence_after();
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tc::tmem_load32(mine + S::O_AT + i, o);
+                    tc::tmem_load_wait32(o);
+#pragma unroll
+                    for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * factor);
+                    tc::tmem_store32(mine + S::O_AT + i, o);
+                }
+            }
+            const float shift = top == -INFINITY ? 0.0f : -top * a.c;
+            float s4[4] = {};
+#pragma unroll
+            for (int i = 0; i < KT; i += 4) {
+                float p[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    p[n] = exp2_of(fmaf(__uint_as_float(x[i + n]), a.c, shift));
+                    s4[n] += p[n];
+                }
+                x[i / 2] = pack_bf16(p[0], p[1]);
+                x[i / 2 + 1] = pack_bf16(p[2], p[3]);
+            }
+            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+#pragma unroll
+            for (int i = 0; i < KT / 2; i += 32) tc::tmem_store32(at + i, x + i);
+            if (edge) {                                  // values that are not finite
+                if (!wait(v_full(j % S::STAGES), j / S::STAGES & 1)) { alive = false; break; }
+                const uint32_t v = v_at + uint32_t(j % S::STAGES) * S::T_BYTES + uint32_t(tid) * 16;
+                uint32_t seen = 0;
+#pragma unroll 8
+                for (int i = 0; i < S::T_BYTES / 2048; ++i) {
+                    const uint4 w = tc::lds128(v + i * 2048);
+                    seen |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
+                }
+                if (seen) {
+                    odd = 1;
+                    for (int i = 0; i < S::T_BYTES / 2048; ++i) {
+                        const uint4 w = tc::lds128(v + i * 2048);
+                        uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) y[n] &= ~((not_finite(y[n]) >> 15) * 0xFFFFu);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v + i * 2048), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+                    }
+                    tc::fence_async();
+                }
+                __syncwarp();
+            }
+            tc::tmem_store_wait();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(sb));
+        }
+        if (alive && wait(o_full, 0)) {
+            tc::fence_after();
+            const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+            const long long token = it.seq0 + tok;
+            const int head = it.head * a.group + row % a.group;
+            const bool look = odd != 0;
+            __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride + (long long)head * D;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+                uint32_t o[32];
+                tc::tmem_load32(mine + S::O_AT + i, o);
+                tc::tmem_load_wait32(o);
+                float y[32];
+#pragma unroll
+                for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : __uint_as_float(o[n]) * inv;
+                if (look && there) {                     // visible values that were left out
+                    for (int j = 0; j < tiles; ++j) {
+                        const int k0 = first + j * KT;
+                        if (!on_edge<KT>(a, it, k0)) continue;
+                        for (int key = max(k0, low); key <= min(k0 + KT - 1, pos); ++key) {
+                            const __nv_bfloat16* const v = static_cast<const __nv_bfloat16*>(a.v) + (long long)(it.seq0 + key) * a.v_stride + it.head * D + i;
+#pragma unroll
+                            for (int n = 0; n < 32; ++n) {
+                                const float w = __bfloat162float(v[n]);
+                                if (!(fabsf(w) <= 3.4e38f)) y[n] += w;
+                            }
+                        }
+                    }
+                }
+                if (there) {
+#pragma unroll
+                    for (int n = 0; n < 32; n += 8)
+                        *reinterpret_cast<uint4*>(to + i + n) = make_uint4(pack_bf16(y[n], y[n + 1]), pack_bf16(y[n + 2], y[n + 3]),
+                                                                           pack_bf16(y[n + 4], y[n + 5]), pack_bf16(y[n + 6], y[n + 7]));
+                }
+            }
+            if (there && a.lse) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
+        }
+    } else if (warp == kSoftWarps) {
+        // --------------------------------------------------------------------- copies
+        const int n_q = a.tokens * a.group * 128;        // bytes of a 64-wide piece
+        if (tc::elect()) {
+            mbar_arrive_expect_tx(q_full, uint32_t(CH * n_q) + a.extra_tx);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) tc::load_3d(q_at + c * 16384, &a.qmap, c * 64, it.head * a.group, it.seq0 + it.t0, q_full);
+        }
+        __syncwarp();
+        int j = 0;
+        bool alive = true;
+        for (; j < tiles && alive; ++j) {
+            const int s = j % S::STAGES;
+            const uint32_t phase = (j / S::STAGES & 1) ^ 1;
+            const int key = it.seq0 + first + j * KT;
+            if (!wait(k_empty(s), phase)) { alive = false; break; }
+            if (tc::elect()) {
+                mbar_arrive_expect_tx(k_full(s), S::T_BYTES);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) tc::load_3d(k_at + s * S::T_BYTES + c * KT * 128, &a.kmap, c * 64, it.head, key, k_full(s));
+            }
+            __syncwarp();
+            if (!wait(v_empty(s), phase)) { alive = false; break; }
+            if (tc::elect()) {
+                mbar_arrive_expect_tx(v_full(s), S::T_BYTES);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) tc::load_3d(v_at + s * S::T_BYTES + c * KT * 128, &a.vmap, c * 64, it.head, key, v_full(s));
+            }
+            __syncwarp();
+        }
+        if (dead) {                                      // copies still on their way end before the CTA does
+            mbar_wait(q_full, 0, a.drain_limit);
+            for (int s = 0; s < S::STAGES; ++s) {
+                // (keys may have been requested for tile j where values were not)
+                for (int t = j; t >= 0 && t > j - S::STAGES - 1; --t)
+                    if (t % S::STAGES == s) {
+                        mbar_wait(k_full(s), t / S::STAGES & 1, min(a.drain_limit, 65536u));
+                        mbar_wait(v_full(s), t / S::STAGES & 1, min(a.drain_limit, 65536u));
+                    }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------- products
+        const uint32_t i_s = tc::instr(true, KT, false) | a.negate, i_o = tc::instr(true, D, true);
+        bool alive = wait(q_full, 0);
+        auto scores = [&](int j) {
+            const int s = j % S::STAGES, sb = j % S::SB;
+            if (!wait(k_full(s), j / S::STAGES & 1)) return false;
+            tc::fence_after();
+            if (tc::elect()) {
+                const uint64_t dq = tc::desc_k(q_at), dk = tc::desc_k(k_at + s * S::T_BYTES);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc::mma(tmem + uint32_t(sb * KT), dq + c * (16384 >> 4) + 2 * i, dk + c * (KT * 128 >> 4) + 2 * i, i_s, c + i > 0);
+                tc::commit(k_empty(s));
+                tc::commit(s_full(sb));
+            }
+            __syncwarp();
+            return true;
+        };
+        if (alive && S::SB == 2) alive = scores(0);
+        for (int j = 0; j < tiles && alive; ++j) {
+            const int s = j % S::STAGES, sb = j % S::SB;
+            if (S::SB == 1) alive = scores(j);
+            else if (j + 1 < tiles) alive = scores(j + 1);
+            if (!alive || !wait(v_full(s), j / S::STAGES & 1) || !wait(p_full(sb), j / S::SB & 1)) { alive = false; break; }
+            tc::fence_after();
+            if (tc::elect()) {
+                const uint64_t dv = tc::desc_mn(v_at + s * S::T_BYTES, KT * 128);
+#pragma unroll
+                for (int i = 0; i < KT / 16; ++i)
+                    tc::mma_ts(tmem + S::O_AT, tmem + uint32_t(sb * KT + i * 8), dv + i * (2048 >> 4), i_o, j > 0 || i > 0);
+                tc::commit(v_empty(s));
+                tc::commit(pv_done);
+                if (j + 1 == tiles) tc::commit(o_full);
+            }
+            __syncwarp();
+        }
+        if (!alive && tc::elect()) tc::commit(o_full);   // products under way end before the columns are given back
+        __syncwarp();
+        mbar_wait(o_full, 0, a.drain_limit);
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == kSoftWarps + 1) tc::tmem_free(tmem, S::COLS);
+}
+
+template <int D> PromptKernel kernel() { return {(const void*)&prompt_bf16_kernel<D>, kPromptThreads, Shape<D>::SMEM, Shape<D>::KT}; }
+
+}  // namespace
+
+PromptKernel prompt_bf16(int D) { return D == 64 ? kernel<64>() : D == 128 ? kernel<128>() : kernel<256>(); }
+
+}  // namespace qg
