@@ -57,7 +57,7 @@ def _units():
     for f in range(5):
         units.append((os.path.join(BUILD, f"qgemm_inst_fmt{f}.o"),
                       [nvcc, *ARCH, *NVCC_FLAGS, f"-DQG_INST_FMT={f}", "-c", os.path.join(CSRC, "qgemm_inst.cu")]))
-    for src in ("attention", "kv_cache", "qgemm", "prompt_attention", "prompt_attention_bf16"):
+    for src in ("attention", "kv_cache", "qgemm", "prompt_attention", "prompt_attention_bf16", "prompt_attention_f32"):
         units.append((os.path.join(BUILD, src + ".o"), [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src + ".cu")]))
     units.append((os.path.join(BUILD, "qgemv_experts.o"),
                   [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, "qgemv_experts.cu")]))

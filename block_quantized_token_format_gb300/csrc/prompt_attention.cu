@@ -6,11 +6,8 @@
 
 #include "kv_layout.h"
 #include "prompt_attention.cuh"
-#include "qgemv_host.h"
 
 namespace qg {
-
-PromptKernel prompt_bf16(int D);
 
 namespace {
 
@@ -29,6 +26,24 @@ qg_status encode_heads(CUtensorMap* map, const void* p, int64_t n_tok, int n_hea
                ? QG_OK : QG_ECUDA;
 }
 
+// What a call needs of its workspace: with fp32 the staged terms and their powers of two.
+struct PromptSpace { size_t q, k, v, qscale, kscale, vscale, total; };
+PromptSpace prompt_space(qg_act act, int64_t n_tok, int n_heads, int n_kv, int D) {
+    PromptSpace s{};
+    if (act == QG_ACT_F32) {
+        auto take = [&](size_t bytes) { const size_t at = s.total; s.total = (at + bytes + 255) / 256 * 256; return at; };
+        const size_t n = size_t(n_tok);
+        s.q = take(n * size_t(n_heads) * size_t(D) * 4);
+        s.k = take(n * size_t(n_kv) * size_t(D) * 4);
+        s.v = take(n * size_t(n_kv) * size_t(D) * 4);
+        s.qscale = take(n * size_t(n_heads) * 4);
+        s.kscale = take(n * size_t(n_kv) * 4);
+        s.vscale = take(n * size_t(n_kv) * 4);
+    }
+    s.total = std::max<size_t>(s.total, 256);
+    return s;
+}
+
 }  // namespace
 }  // namespace qg
 
@@ -40,7 +55,7 @@ size_t qg_prompt_attention_workspace_bytes(qg_act act, int64_t n_tok, int n_head
     if ((act != QG_ACT_F32 && act != QG_ACT_BF16) || n_tok < 0 || n_tok > (int64_t(1) << 31) - 1025 || n_kv_heads < 1 ||
         n_heads < 1 || n_heads > 65535 || n_heads % n_kv_heads != 0 || !kv_dim_ok(head_dim))
         return 0;
-    return 256;
+    return prompt_space(act, n_tok, n_heads, n_kv_heads, head_dim).total;
 }
 
 qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -65,18 +80,37 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
         k_stride * size % 16 != 0 || v_stride * size % 16 != 0 || out_stride * size % 16 != 0 || !aligned(cu_seq, 4) || !aligned(lse, 4))
         return QG_EALIGN;
     const int tokens = 128 / group;
-    const int64_t items = (n_tok / tokens + n_seq) * n_kv_heads;
-    if (items > most - 1) return QG_EUNSUPPORTED;
-    if (act == QG_ACT_F32) return QG_EUNSUPPORTED;
+    const bool f32 = act == QG_ACT_F32;
+    const PromptKernel kern = f32 ? prompt_f32(head_dim) : prompt_bf16(head_dim);
+    const int64_t items = (n_tok / tokens + n_seq) * n_kv_heads * kern.parts;
+    if (items > most - 1 || (f32 && 2 * n_tok > most)) return QG_EUNSUPPORTED;
     int dev = 0, sms = 0, optin = 0;
     PromptArgs a{};
     qg_status st = device_info(&dev, &sms, &optin, &a.status);
     if (st != QG_OK) return st;
-    const PromptKernel kern = prompt_bf16(head_dim);
     if (blocks_per_sm(kern.fn, dev, optin, kern.threads, size_t(kern.smem)) < 1) return QG_EUNSUPPORTED;
-    st = encode_heads(&a.qmap, q, n_tok, n_heads, head_dim, q_stride, group, tokens);
-    if (st == QG_OK) st = encode_heads(&a.kmap, k, n_tok, n_kv_heads, head_dim, k_stride, 1, kern.boxes_kt);
-    if (st == QG_OK) st = encode_heads(&a.vmap, v, n_tok, n_kv_heads, head_dim, v_stride, 1, kern.boxes_kt);
+    if (f32) {
+        const PromptSpace sp = prompt_space(act, n_tok, n_heads, n_kv_heads, head_dim);
+        uint8_t* const ws = static_cast<uint8_t*>(workspace);
+        PromptStage p{};
+        p.q = static_cast<const float*>(q), p.k = static_cast<const float*>(k), p.v = static_cast<const float*>(v);
+        p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
+        p.cu_seq = cu_seq;
+        p.q_out = reinterpret_cast<uint16_t*>(ws + sp.q), p.k_out = reinterpret_cast<uint16_t*>(ws + sp.k);
+        p.v_out = reinterpret_cast<uint16_t*>(ws + sp.v);
+        p.qscale = reinterpret_cast<float*>(ws + sp.qscale), p.kscale = reinterpret_cast<float*>(ws + sp.kscale);
+        p.vscale = reinterpret_cast<float*>(ws + sp.vscale);
+        p.n_tok = int(n_tok), p.n_seq = n_seq, p.n_heads = n_heads, p.n_kv = n_kv_heads;
+        a.qscale = p.qscale, a.kscale = p.kscale, a.vscale = p.vscale;
+        st = encode_heads(&a.qmap, p.q_out, 2 * n_tok, n_heads, head_dim, width, group, tokens);
+        if (st == QG_OK) st = encode_heads(&a.kmap, p.k_out, 2 * n_tok, n_kv_heads, head_dim, kv_width, 1, kern.tile_keys);
+        if (st == QG_OK) st = encode_heads(&a.vmap, p.v_out, 2 * n_tok, n_kv_heads, head_dim, kv_width, 1, kern.tile_keys);
+        if (st == QG_OK) st = prompt_stage(head_dim, p, stream);
+    } else {
+        st = encode_heads(&a.qmap, q, n_tok, n_heads, head_dim, q_stride, group, tokens);
+        if (st == QG_OK) st = encode_heads(&a.kmap, k, n_tok, n_kv_heads, head_dim, k_stride, 1, kern.tile_keys);
+        if (st == QG_OK) st = encode_heads(&a.vmap, v, n_tok, n_kv_heads, head_dim, v_stride, 1, kern.tile_keys);
+    }
     if (st != QG_OK) return st;
     a.k = k;
     a.v = v;
@@ -100,7 +134,7 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.extra_tx = test_extra_tx();
     void* params[] = {&a};
-    return launch_early(kern.fn, int(items) + 1, kern.threads, size_t(kern.smem), 1, params, stream);
+    return launch_after(kern.fn, int(items) + 1, kern.threads, size_t(kern.smem), f32, params, stream);
 }
 
 }  // extern "C"

@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "qgemv_host.h"
 #include "umma.cuh"
 
 namespace qg {
@@ -29,7 +30,7 @@ struct PromptArgs {
     int n_tok, n_seq, n_heads, n_kv, group, tokens, window;      // tokens: T
     float c;                       // |scale| log2 e
     uint32_t negate;               // of the instruction descriptor, where scale < 0
-    const float *kscale, *vscale;  // fp32: powers of two
+    const float *qscale, *kscale, *vscale;       // fp32: powers of two, per row, per token that begins a key tile
     unsigned int* status;
     uint32_t wait_limit, drain_limit, extra_tx;
 };
@@ -37,20 +38,19 @@ struct PromptArgs {
 // One item's place: prompt's first token and length, first query (of the prompt), key/value head.
 struct PromptItem { int seq0, len, t0, head; };
 
-// False: nothing to do.
-__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int slot, int head, PromptItem& it) {
-    int lo = 0, hi = a.n_seq;                            // the last prompt that begins at or before the slot
+// The piece of `per` tokens of a prompt that a slot is; false: nothing to do.
+__device__ __forceinline__ bool prompt_piece(const int32_t* cu_seq, int n_seq, int n_tok, int per, int slot, PromptItem& it) {
+    int lo = 0, hi = n_seq;                              // the last prompt that begins at or before the slot
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.cu_seq[mid] / a.tokens + mid <= slot) lo = mid; else hi = mid;
+        if (cu_seq[mid] / per + mid <= slot) lo = mid; else hi = mid;
     }
-    const int from = a.cu_seq[lo], to = a.cu_seq[lo + 1];
-    if (from < 0 || to < from || to > a.n_tok) return false;         // (reported by prompt_check)
-    const long long t0 = (long long)(slot - (from / a.tokens + lo)) * a.tokens;
+    const int from = cu_seq[lo], to = cu_seq[lo + 1];
+    if (from < 0 || to < from || to > n_tok) return false;           // (reported by prompt_check)
+    const long long t0 = (long long)(slot - (from / per + lo)) * per;
     it.seq0 = from;
     it.len = to - from;
     it.t0 = int(min(t0, 0x7FFFFFFFll));
-    it.head = head;
     return t0 >= 0 && t0 < it.len;
 }
 // Entries of cu_seq, checked by one CTA.
@@ -63,10 +63,12 @@ __device__ __forceinline__ void prompt_check(const PromptArgs& a) {
     if (bad) atomicOr(a.status, kPromptBadLength);
 }
 
-// Key tiles of an item: the first key (of the prompt) and their number.
-template <int KT> __device__ __forceinline__ void key_range(const PromptArgs& a, const PromptItem& it, int& first, int& tiles) {
+// Key tiles of an item: the first key (of the prompt) and their number.  `whole`: tiles begin at
+// multiples of KT.
+template <int KT> __device__ __forceinline__ void key_range(const PromptArgs& a, const PromptItem& it, bool whole, int& first, int& tiles) {
     const int last = min(it.t0 + a.tokens, it.len) - 1;
     first = a.window > 0 ? max(0, it.t0 - a.window + 1) : 0;
+    if (whole) first = first / KT * KT;
     tiles = (last - first) / KT + 1;
 }
 // Whether some row of the item does not see every key of the tile that begins at k0.
@@ -81,6 +83,77 @@ __device__ __forceinline__ float exp2_of(float x) {
     return y;
 }
 
-struct PromptKernel { const void* fn; int threads, smem, boxes_kt; };
+// One row's place in its item.
+struct PromptRow { bool there; int tok, pos, low; };     // of the prompt; last and first visible key
+__device__ __forceinline__ PromptRow prompt_row(const PromptArgs& a, const PromptItem& it, int row) {
+    PromptRow r;
+    r.tok = it.t0 + row / a.group;
+    r.there = row < a.tokens * a.group && r.tok < it.len;
+    r.pos = r.there ? r.tok : -1;
+    r.low = r.there && a.window > 0 ? max(0, r.tok - a.window + 1) : 0;
+    return r;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&y)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+}
+// Halves of a word whose exponents (mask) are all ones get bit 15 and 31.
+template <uint32_t MASK> __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return ((w & MASK) + (0x80008000u - MASK)) & 0x80008000u;
+}
+constexpr uint32_t kBf16Exp = 0x7F807F80u, kFp16Exp = 0x7C007C00u;
+// Makes zeros of the values of `bytes` at v that are not finite; 128 threads, each its own 16 bytes
+// of every 2048.  True if this thread met one.
+template <uint32_t MASK> __device__ __forceinline__ bool clear_not_finite(uint32_t v, int bytes, int tid) {
+    v += uint32_t(tid) * 16;
+    uint32_t seen = 0;
+#pragma unroll 8
+    for (int i = 0; i < bytes; i += 2048) {
+        const uint4 w = tc::lds128(v + i);
+        seen |= not_finite<MASK>(w.x) | not_finite<MASK>(w.y) | not_finite<MASK>(w.z) | not_finite<MASK>(w.w);
+    }
+    if (!seen) return false;
+    for (int i = 0; i < bytes; i += 2048) {
+        const uint4 w = tc::lds128(v + i);
+        uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) y[n] &= ~((not_finite<MASK>(y[n]) >> 15) * 0xFFFFu);
+        sts128(v + i, y);
+    }
+    tc::fence_async();
+    return true;
+}
+// What was left out: adds the values that are not finite, of the keys on edge tiles that the row
+// sees, to 32 outputs from `dim` on.
+template <int KT, typename T>
+__device__ __forceinline__ void add_not_finite(const PromptArgs& a, const PromptItem& it, const PromptRow& r, int first, int tiles, int dim, int D, float (&y)[32]) {
+    for (int j = 0; j < tiles; ++j) {
+        const int k0 = first + j * KT;
+        if (!on_edge<KT>(a, it, k0)) continue;
+        for (int key = max(k0, r.low); key <= min(k0 + KT - 1, r.pos); ++key) {
+            const T* const v = static_cast<const T*>(a.v) + (long long)(it.seq0 + key) * a.v_stride + it.head * D + dim;
+#pragma unroll
+            for (int n = 0; n < 32; ++n) {
+                const float w = float(v[n]);
+                if ((__float_as_uint(w) & 0x7F800000u) == 0x7F800000u) y[n] += w;
+            }
+        }
+    }
+}
+
+struct PromptKernel { const void* fn; int threads, smem, tile_keys, parts; };      // parts: CTAs of an item
+PromptKernel prompt_bf16(int D);
+PromptKernel prompt_f32(int D);
+
+// fp32: queries, keys and values as two fp16 terms each, with their powers of two.
+struct PromptStage {
+    const float *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* cu_seq;
+    uint16_t *q_out, *k_out, *v_out;
+    float *qscale, *kscale, *vscale;
+    int n_tok, n_seq, n_heads, n_kv;
+};
+qg_status prompt_stage(int D, const PromptStage& p, void* stream);
 
 }  // namespace qg

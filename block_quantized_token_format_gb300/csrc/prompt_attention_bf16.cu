@@ -33,8 +33,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&p);
 }
-// Bits 15 and 31: the halves' exponents are all ones.
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) prompt_bf16_kernel(const __grid_constant__ PromptArgs a) {
     using S = Shape<D>;
@@ -52,9 +50,10 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     }
     PromptItem it;
     const int slots = (int(gridDim.x) - 1) / a.n_kv, b = int(blockIdx.x) / a.n_kv;
-    if (!prompt_item(a, slots - 1 - b, int(blockIdx.x) - b * a.n_kv, it)) return;
+    if (!prompt_piece(a.cu_seq, a.n_seq, a.n_tok, a.tokens, slots - 1 - b, it)) return;
+    it.head = int(blockIdx.x) - b * a.n_kv;
     int first, tiles;
-    key_range<KT>(a, it, first, tiles);
+    key_range<KT>(a, it, false, first, tiles);
 
     const uint32_t q_at = (smem_addr(smem_raw) + 1023u) & ~1023u, k_at = q_at + S::Q_BYTES, v_at = k_at + S::STAGES * S::T_BYTES;
     const uint32_t bars = smem_addr(bar_mem);
@@ -89,9 +88,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     const uint32_t tmem = tmem_at;
 
     if (warp < kSoftWarps) {
-        const int row = warp * 32 + lane, tok = it.t0 + row / a.group;
-        const bool there = row < a.tokens * a.group && tok < it.len;
-        const int pos = there ? tok : -1, low = there && a.window > 0 ? max(0, tok - a.window + 1) : 0;
+        const PromptRow r = prompt_row(a, it, tid);
         const uint32_t mine = tmem + (uint32_t(warp) << 21);
         float top = -INFINITY, sum = 0.0f;               // the row's reference (a score), sum of P
         bool alive = true;
@@ -107,7 +104,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
             for (int i = 0; i < KT; i += 16) tc::tmem_load_wait16(x + i);
             const bool edge = on_edge<KT>(a, it, k0);
             if (edge) {
-                const int hi = pos - k0, lo = low - k0;
+                const int hi = r.pos - k0, lo = r.low - k0;
 #pragma unroll
                 for (int i = 0; i < KT; ++i)
                     if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
@@ -157,24 +154,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
             for (int i = 0; i < KT / 2; i += 32) tc::tmem_store32(at + i, x + i);
             if (edge) {                                  // values that are not finite
                 if (!wait(v_full(j % S::STAGES), j / S::STAGES & 1)) { alive = false; break; }
-                const uint32_t v = v_at + uint32_t(j % S::STAGES) * S::T_BYTES + uint32_t(tid) * 16;
-                uint32_t seen = 0;
-#pragma unroll 8
-                for (int i = 0; i < S::T_BYTES / 2048; ++i) {
-                    const uint4 w = tc::lds128(v + i * 2048);
-                    seen |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
-                }
-                if (seen) {
-                    odd = 1;
-                    for (int i = 0; i < S::T_BYTES / 2048; ++i) {
-                        const uint4 w = tc::lds128(v + i * 2048);
-                        uint32_t y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) y[n] &= ~((not_finite(y[n]) >> 15) * 0xFFFFu);
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v + i * 2048), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
-                    }
-                    tc::fence_async();
-                }
+                if (clear_not_finite<kBf16Exp>(v_at + uint32_t(j % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
                 __syncwarp();
             }
             tc::tmem_store_wait();
@@ -185,8 +165,8 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
         if (alive && wait(o_full, 0)) {
             tc::fence_after();
             const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-            const long long token = it.seq0 + tok;
-            const int head = it.head * a.group + row % a.group;
+            const long long token = it.seq0 + r.tok;
+            const int head = it.head * a.group + tid % a.group;
             const bool look = odd != 0;
             __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride + (long long)head * D;
 #pragma unroll 1
@@ -197,28 +177,15 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                 float y[32];
 #pragma unroll
                 for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : __uint_as_float(o[n]) * inv;
-                if (look && there) {                     // visible values that were left out
-                    for (int j = 0; j < tiles; ++j) {
-                        const int k0 = first + j * KT;
-                        if (!on_edge<KT>(a, it, k0)) continue;
-                        for (int key = max(k0, low); key <= min(k0 + KT - 1, pos); ++key) {
-                            const __nv_bfloat16* const v = static_cast<const __nv_bfloat16*>(a.v) + (long long)(it.seq0 + key) * a.v_stride + it.head * D + i;
-#pragma unroll
-                            for (int n = 0; n < 32; ++n) {
-                                const float w = __bfloat162float(v[n]);
-                                if (!(fabsf(w) <= 3.4e38f)) y[n] += w;
-                            }
-                        }
-                    }
-                }
-                if (there) {
+                if (look && r.there) add_not_finite<KT, __nv_bfloat16>(a, it, r, first, tiles, i, D, y);      // visible values that were left out
+                if (r.there) {
 #pragma unroll
                     for (int n = 0; n < 32; n += 8)
                         *reinterpret_cast<uint4*>(to + i + n) = make_uint4(pack_bf16(y[n], y[n + 1]), pack_bf16(y[n + 2], y[n + 3]),
                                                                            pack_bf16(y[n + 4], y[n + 5]), pack_bf16(y[n + 6], y[n + 7]));
                 }
             }
-            if (there && a.lse) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
+            if (r.there && a.lse) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
         }
     } else if (warp == kSoftWarps) {
         // --------------------------------------------------------------------- copies
@@ -311,7 +278,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     if (warp == kSoftWarps + 1) tc::tmem_free(tmem, S::COLS);
 }
 
-template <int D> PromptKernel kernel() { return {(const void*)&prompt_bf16_kernel<D>, kPromptThreads, Shape<D>::SMEM, Shape<D>::KT}; }
+template <int D> PromptKernel kernel() { return {(const void*)&prompt_bf16_kernel<D>, kPromptThreads, Shape<D>::SMEM, Shape<D>::KT, 1}; }
 
 }  // namespace
 
