@@ -325,14 +325,17 @@ qg_status launch_gemm(const GemmCall& c) {
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.extra_tx = test_extra_tx();
     const void* const fn = qgemm_lookup(c.fmt, f32);
-    const size_t stage = size_t(terms_w(c.fmt, f32)) * kOperandA + size_t(terms_x(c.fmt, f32)) * size_t(bn) * kGemmK * 2;
-    // Four stages of operands (fewer if they do not fit), the rest of shared memory holds raw codes
-    // on their way: few tokens to a tile leave room for a deep ring, which is what they need.  An even
-    // number of raw steps: a slot then always belongs to the same four decoding warps, which wait for
-    // its fills one by one.
+    const size_t sub = size_t(terms_w(c.fmt, f32)) * kOperandA + size_t(terms_x(c.fmt, f32)) * size_t(bn) * kGemmK * 2;
+    // Stages of one step of K, or of two where they are small (a stage's waits and bookkeeping take
+    // about 200 clocks of the thread that issues the products, a product's issue 60): four or three
+    // of them; the rest of shared memory holds raw codes on their way, which is what few tokens to a
+    // tile need.  An even number of raw steps: a slot then always belongs to the same four decoding
+    // warps, which wait for its fills one by one.
     const size_t raw = size_t(kGemmRows) * size_t(raw_codes(c.fmt)), scales = size_t(kGemmRows) * kScaleSlots * size_t(raw_scales(c.fmt));
     const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
-    a.stages = int(std::min<size_t>(quant ? 4 : 8, (room - 2 * raw) / stage));
+    a.subs = !f32 && bn <= 128 ? 2 : 1;
+    const size_t stage = size_t(a.subs) * sub;
+    a.stages = int(std::min<size_t>(quant ? (a.subs == 2 ? (bn == 128 ? 2 : 3) : 4) : 8, (room - 2 * raw) / stage));
     a.raws = quant ? int(std::min<size_t>(kMostRaws, (room - size_t(a.stages) * stage) / raw)) / 2 * 2 : 0;
     const size_t smem = 1024 + scales + size_t(a.raws) * raw + size_t(a.stages) * stage;
     if (a.stages < 2 || blocks_per_sm(fn, dev, optin, kGemmThreads, smem) < 1) return QG_EUNSUPPORTED;

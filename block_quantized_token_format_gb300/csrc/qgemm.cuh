@@ -60,19 +60,16 @@ struct GemmArgs {
     const void* residual;
     void* y;
     long long residual_stride, y_stride;
-    int f, bn, stages, raws, m_tiles, n_tiles;
+    int f, bn, subs, stages, raws, m_tiles, n_tiles;      // subs: steps of K in a stage
     unsigned int* status;
     uint32_t wait_limit, drain_limit, extra_tx;
 };
 
 enum { kFNone = 0, kFSilu = 1, kFGelu = 2, kFGeluTanh = 3, kFSwiglu = 4 };
 
-__device__ __forceinline__ float silu_of(float v) { return v / (1.0f + expf(-v)); }
-__device__ __forceinline__ float activation_of(float v, int f) {
-    if (f == kFSilu) return silu_of(v);
-    if (f == kFGelu) return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-    if (f == kFGeluTanh) return 0.5f * v * (1.0f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
-    return v;
+// (bf16 outputs: the fast exponential and division, 2^-20 of the value for |v| below 16.)
+template <bool F32> __device__ __forceinline__ float silu_of(float v) {
+    return F32 ? v / (1.0f + expf(-v)) : __fdividef(v, 1.0f + __expf(-v));
 }
 
 struct GemmTile { int row0, w_row0, slot0, cols; };       // row0: in the expert's matrix; w_row0: in the stack
@@ -168,11 +165,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
 
     const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t b_bytes = uint32_t(a.bn) * kGemmK * 2, stage_bytes = TW * kOperandA + TX * b_bytes;
+    const uint32_t b_bytes = uint32_t(a.bn) * kGemmK * 2, sub_bytes = TW * kOperandA + TX * b_bytes, stage_bytes = uint32_t(a.subs) * sub_bytes;
     const uint32_t raw0 = base + uint32_t(a.stages) * stage_bytes;
     const uint32_t bars = smem_addr(bar_mem);
-    auto full_b = [&](int s) { return bars + 8u * uint32_t(s); };
-    auto full_a = [&](int s) { return bars + 8u * uint32_t(8 + s); };
+    auto full = [&](int s) { return bars + 8u * uint32_t(s); };
     auto empty = [&](int s) { return bars + 8u * uint32_t(16 + s); };
     auto acc_full = [&](int b) { return bars + 8u * uint32_t(24 + b); };
     auto acc_empty = [&](int b) { return bars + 8u * uint32_t(26 + b); };
@@ -184,13 +180,13 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
     const uint32_t acc_cols = uint32_t(a.bn) * (F32 ? 2 : 1);                    // of one set
     const uint32_t tmem_cols = max(32u, 2 * acc_cols);
     const tc::Waits wait{&dead, a.status, a.wait_limit};
-    const int ksteps = (a.n_in + kGemmK - 1) / kGemmK;
+    // (A last stage that K does not fill gets zeros.)
+    const int ksteps = ((a.n_in + kGemmK - 1) / kGemmK + a.subs - 1) / a.subs * a.subs;
 
     if (tid == 0) {
         dead = 0;
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(full_b(s), 1);
-            mbar_init(full_a(s), kDecodeWarps / 2);
+            mbar_init(full(s), kQuant ? 1 + kDecodeWarps / 2 * a.subs : 1);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -229,33 +225,52 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
             const int row = g.row0 + (warp & 3) * 32 + lane;
             const bool there = row < a.n_out;
             const float bias = a.bias && there ? a.bias[row] : 0.0f;
+            const int col = a.f == kFSwiglu ? row >> 1 : row;
+            const bool writes = there && (a.f != kFSwiglu || (lane & 1) == 0);
             float sum[F32 ? 64 : 1];
             uint32_t v[F32 ? 16 : 32];
-            auto put = [&](int u, const float* x) {                  // 16 columns of this lane's row
-                const int c0 = half * hc + u * 16;
-                const float mine = a.xscale && (lane & 15) + c0 < g.cols ? a.xscale[g.slot0 + c0 + (lane & 15)] : 1.0f;
-                const int col = a.f == kFSwiglu ? row >> 1 : row;
-                const bool writes = there && (a.f != kFSwiglu || (lane & 1) == 0);
+            // 16 columns of this lane's row: one pass per part of the epilogue that the call has, so that
+            // none of them asks again for every column.
+            auto put = [&](int u, float* x) {
+                const int c0 = half * hc + u * 16, n = min(16, g.cols - c0);
+                if (n <= 0) return;
+                if (a.xscale) {
+                    const float mine = (lane & 15) < n ? a.xscale[g.slot0 + c0 + (lane & 15)] : 1.0f;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (c0 + c >= g.cols) break;
-                    float y = x[c];
-                    if (a.xscale) y *= __shfl_sync(tc::kFullMask, mine, c);
-                    y += bias;
-                    if (a.f == kFSwiglu) {
-                        const float up = __shfl_xor_sync(tc::kFullMask, y, 1);
-                        y = silu_of(y) * up;
-                    } else if (a.f != kFNone) {
-                        y = activation_of(y, a.f);
-                    }
-                    if (!writes) continue;
-                    const long long slot = g.slot0 + c0 + c;
-                    if (a.residual) {
-                        const Out r = static_cast<const Out*>(a.residual)[slot * a.residual_stride + col];
-                        if constexpr (F32) y += r; else y += __bfloat162float(r);
-                    }
-                    if constexpr (F32) static_cast<float*>(a.y)[slot * a.y_stride + col] = y;
-                    else static_cast<__nv_bfloat16*>(a.y)[slot * a.y_stride + col] = __float2bfloat16_rn(y);
+                    for (int c = 0; c < 16; ++c) x[c] *= __shfl_sync(tc::kFullMask, mine, c);
+                }
+                if (a.bias) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] += bias;
+                }
+                if (a.f == kFSwiglu) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] = silu_of<F32>(x[c]) * __shfl_xor_sync(tc::kFullMask, x[c], 1);
+                } else if (a.f == kFSilu) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] = silu_of<F32>(x[c]);
+                } else if (a.f == kFGelu) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] = 0.5f * x[c] * (1.0f + erff(x[c] * 0.70710678f));
+                } else if (a.f == kFGeluTanh) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] = 0.5f * x[c] * (1.0f + tanhf(0.79788456f * (x[c] + 0.044715f * x[c] * x[c] * x[c])));
+                }
+                if (!writes) return;
+                if (a.residual) {
+                    const Out* r = static_cast<const Out*>(a.residual) + (g.slot0 + c0) * a.residual_stride + col;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c, r += a.residual_stride)
+                        if (c < n) x[c] += float(*r);
+                }
+                Out* to = static_cast<Out*>(a.y) + (g.slot0 + c0) * a.y_stride + col;
+                if (n == 16) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c, to += a.y_stride) *to = Out(x[c]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c, to += a.y_stride)
+                        if (c < n) *to = Out(x[c]);
                 }
             };
             for (int ch = 0; ch < chunks; ++ch, ++it) {
@@ -314,7 +329,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
             const int w = warp - kDrainWarps, row = (w & 3) * 32 + lane, which = w >> 2;
             const uint32_t scales0 = raw0 + uint32_t(a.raws) * (kGemmRows * CB);
             const int tiles = gemm_tiles(a);
-            int s = 0, r = 0, sr = 0;
+            int s = 0, sub = 0, r = 0, sr = 0;
             uint32_t phase = 0, raw_phase = 0, n = 0, groups = 0;
             bool alive = true;
             for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
@@ -345,8 +360,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                             const uint32_t w0 = tc::lds32(sc);
                             half[0] = w0 & 0xFFFFu, half[1] = w0 >> 16;
                         }
-                        const bool tail = k * kGemmK + 32 >= a.n_in;             // the second half is past the row's end
-                        const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(row) * 128;
+                        const int left = a.n_in - k * kGemmK;                    // weights from here to the row's end
+                        const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(sub) * sub_bytes + uint32_t(row) * 128;
                         bool ready = false;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -356,10 +371,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                                 d = __half2half2(__ushort_as_half(static_cast<unsigned short>(half[0])));
                                 b = __half2half2(__ushort_as_half(static_cast<unsigned short>(half[1])));
                             } else {
-                                d = b = __half2half2(__ushort_as_half(static_cast<unsigned short>(h && tail ? 0u : half[h])));
+                                d = b = __half2half2(__ushort_as_half(static_cast<unsigned short>(half[h])));
                             }
                             decode32<FMT, F32>(code[h], fifth[h], d, b, hi, lo);
-                            if (h == 1 && FMT != QG_AFFINE4_G64 && tail) {       // codes there are other bytes of the row
+                            if (32 * h >= left) {                                // codes there are other bytes of the row
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0;
                             }
@@ -376,11 +391,14 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                         tc::fence_async();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(full_a(s));
+                            mbar_arrive(full(s));
                             mbar_arrive(raw_empty(r));           // (what was read has been used: no load is still under way)
                         }
                     }
-                    if (++s == a.stages) { s = 0; phase ^= 1; }
+                    if (++sub == a.subs) {
+                        sub = 0;
+                        if (++s == a.stages) { s = 0; phase ^= 1; }
+                    }
                     if (++r == a.raws) { r = 0; raw_phase ^= 1; }
                 }
             }
@@ -397,14 +415,16 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
             bool alive = true;
             for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
                 const GemmTile g = gemm_tile(a, t);
-                for (int k = 0; k < ksteps; ++k) {
+                for (int k = 0; k < ksteps; k += a.subs) {
                     if (!wait(empty(s), phase ^ 1)) { alive = false; break; }
-                    const uint32_t at = base + uint32_t(s) * stage_bytes;
+                    uint32_t at = base + uint32_t(s) * stage_bytes;
                     if (tc::elect()) {
-                        mbar_arrive_expect_tx(full_b(s), bytes + extra);
-                        if constexpr (!kQuant) tc::load_2d(at, &a.wmap, k * kGemmK, g.w_row0, full_b(s));
+                        mbar_arrive_expect_tx(full(s), uint32_t(a.subs) * bytes + extra);
+                        for (int u = 0; u < a.subs; ++u, at += sub_bytes) {
+                            if constexpr (!kQuant) tc::load_2d(at, &a.wmap, (k + u) * kGemmK, g.w_row0, full(s));
 #pragma unroll
-                        for (int x = 0; x < TX; ++x) tc::load_3d(at + TW * kOperandA + x * b_bytes, &a.xmap, k * kGemmK, g.slot0, x, full_b(s));
+                            for (int x = 0; x < TX; ++x) tc::load_3d(at + TW * kOperandA + x * b_bytes, &a.xmap, (k + u) * kGemmK, g.slot0, x, full(s));
+                        }
                     }
                     __syncwarp();
                     extra = 0;
@@ -412,11 +432,11 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                     if (++s == a.stages) { s = 0; phase ^= 1; }
                 }
             }
-            // Copies still on their way end before the CTA does: those of the last `stages` steps.
+            // Copies still on their way end before the CTA does: those of the last stages.
             if (dead) {
                 for (uint32_t i = 0; i < uint32_t(a.stages) && i < filled; ++i) {
                     const uint32_t n = filled - 1 - i;
-                    mbar_wait(full_b(int(n % a.stages)), (n / a.stages) & 1, a.drain_limit);
+                    mbar_wait(full(int(n % a.stages)), (n / a.stages) & 1, a.drain_limit);
                 }
             }
         }
@@ -475,36 +495,39 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
         {
             if (a.n_experts) tc::grid_wait();
             const int tiles = gemm_tiles(a);
-            const uint32_t idesc = tc::instr(!kQuant, a.bn, false);
+            // fp32: the tokens' first two terms are neighbours, and so are the sums of the large products
+            // and of the small ones.
+            const uint32_t idesc = tc::instr(!kQuant, F32 ? 2 * a.bn : a.bn, false), ione = tc::instr(!kQuant, a.bn, false);
             int s = 0;
             uint32_t phase = 0, it = 0;
             bool alive = true;
             for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
-                for (int k = 0; k < ksteps; ++k) {
+                for (int k = 0; k < ksteps; k += a.subs) {
                     const bool first = F32 ? k % kChunkSteps == 0 : k == 0;
-                    const bool lastk = k + 1 == ksteps || (F32 && k % kChunkSteps == kChunkSteps - 1);
+                    const bool lastk = k + a.subs == ksteps || (F32 && (k + a.subs) % kChunkSteps == 0);
                     const int b = int(it & 1);
                     if (first && !wait(acc_empty(b), ((it >> 1) & 1) ^ 1)) { alive = false; break; }
-                    if (!wait(full_b(s), phase) || (kQuant && !wait(full_a(s), phase))) { alive = false; break; }
+                    if (!wait(full(s), phase)) { alive = false; break; }
                     tc::fence_after();
-                    const uint32_t acc = tmem + uint32_t(b) * acc_cols, cross = acc + uint32_t(a.bn);
-                    const uint32_t at = base + uint32_t(s) * stage_bytes, bt = at + TW * kOperandA;
-                    const uint64_t da = tc::desc_k(at), db = tc::desc_k(bt);
+                    const uint32_t acc = tmem + uint32_t(b) * acc_cols;
+                    uint32_t at = base + uint32_t(s) * stage_bytes;
                     if (tc::elect()) {
+                        for (int u = 0; u < a.subs; ++u, at += sub_bytes) {
+                            const uint64_t da = tc::desc_k(at), db = tc::desc_k(at + TW * kOperandA);
 #pragma unroll
-                    for (int j = 0; j < kGemmK / 16; ++j) {
-                        const bool add = !first || j > 0;
-                        const uint64_t aj = da + 2 * j, bj = db + 2 * j;             // 32 bytes along K
-                        if constexpr (F32) {
-                            const uint64_t term = b_bytes >> 4;
-                            tc::mma(cross, aj, bj + term, idesc, add);
-                            if constexpr (kQuant) tc::mma(cross, aj + (kOperandA >> 4), bj, idesc, true);
-                            else tc::mma(cross, aj, bj + 2 * term, idesc, true);
+                            for (int j = 0; j < kGemmK / 16; ++j) {
+                                const bool add = j > 0 || u > 0 || !first;
+                                const uint64_t aj = da + 2 * j, bj = db + 2 * j;     // 32 bytes along K
+                                tc::mma(acc, aj, bj, idesc, add);                    // (fp32: the first two terms at once)
+                                if constexpr (F32) {
+                                    const uint32_t cross = acc + uint32_t(a.bn);
+                                    if constexpr (kQuant) tc::mma(cross, aj + (kOperandA >> 4), bj, ione, true);
+                                    else tc::mma(cross, aj, bj + 2 * (b_bytes >> 4), ione, true);
+                                }
+                            }
                         }
-                        tc::mma(acc, aj, bj, idesc, add);
-                    }
-                    tc::commit(empty(s));
-                    if (lastk) tc::commit(acc_full(b));
+                        tc::commit(empty(s));
+                        if (lastk) tc::commit(acc_full(b));
                     }
                     __syncwarp();
                     if (lastk) ++it;

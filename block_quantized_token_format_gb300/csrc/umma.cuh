@@ -34,7 +34,7 @@ __device__ __forceinline__ constexpr uint32_t instr(bool bf16, int n, bool b_alo
     return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_along_n ? 1u << 16 : 0u) | uint32_t(n >> 3) << 17 | uint32_t(128 >> 4) << 24;
 }
 
-// D[128][n] (+)= A[128][16] B[n][16]^T, one thread of the CTA issues.
+// D[128][n] += A[128][16] B[n][16]^T (or =, without `add`), one thread of the CTA issues.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
                  " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
