@@ -242,10 +242,11 @@ qg_status check(const GemmCall& c) {
 // The tile's tokens.  A tile of bn tokens takes about max(2 bn, 190) clocks per step of 64 along K
 // (fp32: 6 bn, 400): the tensor cores' time, or the decoding of the codes; tiles run on all SMs in
 // rounds.
-int tile_tokens(bool f32, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms) {
+int tile_tokens(int fmt, bool f32, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms) {
     int best = 32;
     double least = 0;
-    for (int bn = 32; bn <= gemm_most_tokens(f32); bn *= 2) {
+    for (int b = 32; b <= 256 && (f32 ? b <= 128 : true); b *= 2) {
+        const int bn = std::min(b, gemm_most_tokens(fmt, f32));
         const double step = f32 ? std::max(6.0 * bn, 400.0) : std::max(2.0 * bn, 190.0);
         double rounds;
         if (n_experts == 0) {
@@ -256,7 +257,7 @@ int tile_tokens(bool f32, int64_t m_tiles, int64_t n_slots, int64_t n_experts, i
             rounds = std::max(1.0, double(m_tiles) * std::max(used, double(n_slots) / bn + 0.5 * used) / sms);
         }
         const double cost = rounds * step;
-        if (bn == 32 || cost <= least) { best = bn; least = cost; }
+        if (b == 32 || cost <= least) { best = bn; least = cost; }
     }
     return best;
 }
@@ -297,7 +298,7 @@ qg_status launch_gemm(const GemmCall& c) {
     qg_status st = device_info(&dev, &sms, &optin, &status);
     if (st != QG_OK) return st;
     const int64_t m_tiles = (c.n_out + kGemmRows - 1) / kGemmRows;
-    const int bn = tile_tokens(f32, m_tiles, c.n_slots, c.n_experts, sms);
+    const int bn = tile_tokens(c.fmt, f32, m_tiles, c.n_slots, c.n_experts, sms);
     const int64_t n_tiles = (c.n_slots + bn - 1) / bn;
     if ((n_tiles + c.n_experts) * m_tiles > (int64_t(1) << 31) - 4096) return QG_EUNSUPPORTED;
     uint8_t* const ws = static_cast<uint8_t*>(c.workspace);
@@ -329,16 +330,18 @@ qg_status launch_gemm(const GemmCall& c) {
     // Stages of one step of K, or of two where they are small (a stage's waits and bookkeeping take
     // about 200 clocks of the thread that issues the products, a product's issue 60): four or three
     // of them; the rest of shared memory holds raw codes on their way, which is what few tokens to a
-    // tile need.  An even number of raw steps: a slot then always belongs to the same four decoding
-    // warps, which wait for its fills one by one.
+    // tile need.  Their slots are a multiple of the decoding groups: a slot then always belongs to the
+    // same group, which waits for its fills one by one.
     const size_t raw = size_t(kGemmRows) * size_t(raw_codes(c.fmt)), scales = size_t(kGemmRows) * kScaleSlots * size_t(raw_scales(c.fmt));
     const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
     a.subs = !f32 && bn <= 128 ? 2 : 1;
     const size_t stage = size_t(a.subs) * sub;
-    a.stages = int(std::min<size_t>(quant ? (a.subs == 2 ? (bn == 128 ? 2 : 3) : 4) : 8, (room - 2 * raw) / stage));
-    a.raws = quant ? int(std::min<size_t>(kMostRaws, (room - size_t(a.stages) * stage) / raw)) / 2 * 2 : 0;
+    const int groups = decode_groups(c.fmt, f32), threads = gemm_threads(c.fmt, f32);
+    a.stages = int(std::min<size_t>(quant ? (a.subs == 2 ? (bn == 128 ? 2 : 3) : 4) : 8, (room - size_t(groups) * raw) / stage));
+    a.raws = quant ? int(std::min<size_t>(kMostRaws, (room - size_t(a.stages) * stage) / std::max<size_t>(raw, 1))) / std::max(groups, 1) * groups : 0;
     const size_t smem = 1024 + scales + size_t(a.raws) * raw + size_t(a.stages) * stage;
-    if (a.stages < 2 || blocks_per_sm(fn, dev, optin, kGemmThreads, smem) < 1) return QG_EUNSUPPORTED;
+    if (a.stages < 2 || a.stages * a.subs < groups || (quant && a.raws < groups)) return QG_EUNSUPPORTED;
+    if (blocks_per_sm(fn, dev, optin, threads, smem) < 1) return QG_EUNSUPPORTED;
     const int64_t rows = std::max<int64_t>(1, c.n_experts) * c.n_out, pitch = row_stride(c.fmt, c.n_in);
     st = stages_x ? encode_tokens(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, bn)
                   : encode_tokens(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, bn);
@@ -378,7 +381,7 @@ qg_status launch_gemm(const GemmCall& c) {
     }
     const int64_t tiles = c.n_experts ? sms : n_tiles * m_tiles;
     void* params[] = {&a};
-    return launch_after(fn, int(std::min<int64_t>(sms, tiles)), kGemmThreads, smem, before, params, c.stream);
+    return launch_after(fn, int(std::min<int64_t>(sms, tiles)), threads, smem, before, params, c.stream);
 }
 
 }  // namespace

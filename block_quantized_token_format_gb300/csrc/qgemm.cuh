@@ -6,8 +6,7 @@
 // accumulators' lanes) and tokens as N, in steps of 64 along K:
 //   * one thread copies, with tensor copies, W's raw codes (each step) and scales (every fourth)
 //     into one ring and the tokens' operand (staged by stage_kernel, qgemm.cu) into another;
-//   * eight warps turn the codes into 16-bit floats, a lane a row: four of them one step, the other
-//     four the next;
+//   * groups of four warps turn the codes into 16-bit floats, a lane a row, a group a step;
 //   * one thread issues the products;
 //   * eight warps empty the accumulators, of which there are two sets, so that a tile's epilogue
 //     runs beside the next one's products.
@@ -34,8 +33,13 @@
 namespace qg {
 
 constexpr int kGemmRows = 128, kGemmK = 64;
-constexpr int kDecodeWarps = 8, kDrainWarps = 8;
-constexpr int kGemmThreads = 32 * (kDecodeWarps + kDrainWarps + 4);
+// Decoding warps: groups of four, each group a step of its own in turn.  A step's way through a group
+// (its codes' arrival, the arithmetic, the stage's release, the stores) takes 1500 clocks, its
+// products 512 or less, so bf16 has four groups; fp32, with three times the products and registers for
+// the sums, two.
+constexpr int kDrainWarps = 8;
+__host__ __device__ constexpr int decode_groups(int fmt, bool f32) { return fmt == QG_BF16 ? 0 : f32 ? 2 : 4; }
+__host__ __device__ constexpr int gemm_threads(int fmt, bool f32) { return 32 * (kDrainWarps + 4 * decode_groups(fmt, f32) + 3); }
 constexpr int kChunkSteps = 4;               // fp32: steps of K between moves to registers
 constexpr int kMostRaws = 16;
 
@@ -48,7 +52,8 @@ __host__ __device__ constexpr int raw_codes(int fmt) { return fmt == QG_Q8_0 ? 6
 __host__ __device__ constexpr int raw_scales(int fmt) { return fmt == QG_BF16 ? 0 : fmt == QG_Q5_0 ? 48 : 16; }
 __host__ __device__ constexpr int terms_w(int fmt, bool f32) { return f32 && fmt != QG_BF16 ? 2 : 1; }
 __host__ __device__ constexpr int terms_x(int fmt, bool f32) { return !f32 ? 1 : fmt == QG_BF16 ? 3 : 2; }
-__host__ __device__ constexpr int gemm_most_tokens(bool f32) { return f32 ? 128 : 256; }                                              // of a tile
+// Tokens of the largest tile: 240 leave room for four stages and four raw steps of any format.
+__host__ __device__ constexpr int gemm_most_tokens(int fmt, bool f32) { return f32 ? 128 : fmt == QG_BF16 ? 256 : 240; }
 
 struct GemmArgs {
     CUtensorMap xmap, wmap, smap;  // staged tokens [terms][n_slots][n_in]; rows of W: codes (or bf16), scales
@@ -154,8 +159,9 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 
 // ------------------------------------------------------------------------------ the kernel
 
-template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) qgemm_kernel(const __grid_constant__ GemmArgs a) {
+template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT, F32), 1) qgemm_kernel(const __grid_constant__ GemmArgs a) {
     constexpr bool kQuant = FMT != QG_BF16;
+    constexpr int kGroups = decode_groups(FMT, F32), kDecodeWarps = 4 * kGroups;
     constexpr int TW = terms_w(FMT, F32), TX = terms_x(FMT, F32);
     constexpr int kStepWeights = FMT == QG_Q8_0 ? 512 : 1024;        // of a layout step
     using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
@@ -178,7 +184,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
     auto sc_full = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + r); };
     auto sc_empty = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + kScaleSlots + r); };
     const uint32_t acc_cols = uint32_t(a.bn) * (F32 ? 2 : 1);                    // of one set
-    const uint32_t tmem_cols = max(32u, 2 * acc_cols);
+    const uint32_t tmem_cols = 2 * acc_cols <= 64 ? 64 : 2 * acc_cols <= 128 ? 128 : 2 * acc_cols <= 256 ? 256 : 512;
     const tc::Waits wait{&dead, a.status, a.wait_limit};
     // (A last stage that K does not fill gets zeros.)
     const int ksteps = ((a.n_in + kGemmK - 1) / kGemmK + a.subs - 1) / a.subs * a.subs;
@@ -186,7 +192,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
     if (tid == 0) {
         dead = 0;
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(full(s), kQuant ? 1 + kDecodeWarps / 2 * a.subs : 1);
+            mbar_init(full(s), kQuant ? 1 + 4 * a.subs : 1);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -195,11 +201,11 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
         }
         for (int r = 0; r < a.raws; ++r) {
             mbar_init(raw_full(r), 1);
-            mbar_init(raw_empty(r), kDecodeWarps / 2);
+            mbar_init(raw_empty(r), 4);
         }
         for (int r = 0; r < kScaleSlots; ++r) {
             mbar_init(sc_full(r), 1);
-            mbar_init(sc_empty(r), kDecodeWarps);
+            mbar_init(sc_empty(r), kQuant ? kDecodeWarps : 1);
         }
         mbar_init(drained, 1);
         mbar_fence_init();
@@ -214,7 +220,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
     if (warp < kDrainWarps) {
         // ---------------------------------------------------------------- accumulators to y
         tc::grid_wait();
-        const int half = warp >> 2, hc = a.bn / 2;                   // its half of the columns
+        const int half = warp >> 2, split = (a.bn / 2 + 15) / 16 * 16;       // its part of the columns
+        const int from = half * split, hc = half ? a.bn - split : split;
         const uint32_t lanes = uint32_t(warp & 3) << 21;             // 32 (warp % 4) in the address's high half
         const int chunks = F32 ? (ksteps + kChunkSteps - 1) / kChunkSteps : 1;
         const int tiles = gemm_tiles(a);
@@ -228,11 +235,11 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
             const int col = a.f == kFSwiglu ? row >> 1 : row;
             const bool writes = there && (a.f != kFSwiglu || (lane & 1) == 0);
             float sum[F32 ? 64 : 1];
-            uint32_t v[F32 ? 16 : 32];
+            uint32_t v[16];
             // 16 columns of this lane's row: one pass per part of the epilogue that the call has, so that
             // none of them asks again for every column.
             auto put = [&](int u, float* x) {
-                const int c0 = half * hc + u * 16, n = min(16, g.cols - c0);
+                const int c0 = from + u * 16, n = min(16, g.cols - c0);
                 if (n <= 0) return;
                 if (a.xscale) {
                     const float mine = (lane & 15) < n ? a.xscale[g.slot0 + c0 + (lane & 15)] : 1.0f;
@@ -277,7 +284,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                 const int b = int(it & 1);
                 if (!wait(acc_full(b), (it >> 1) & 1)) { alive = false; break; }
                 tc::fence_after();
-                const uint32_t acc = tmem + lanes + uint32_t(b) * acc_cols + uint32_t(half * hc);
+                const uint32_t acc = tmem + lanes + uint32_t(b) * acc_cols + uint32_t(from);
                 if constexpr (F32) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
@@ -295,21 +302,18 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                     __syncwarp();
                     if (lane == 0) mbar_arrive(acc_empty(b));
                 } else {
-                    for (int u = 0; u * 16 < hc; u += 2) {
-                        const bool two = (u + 1) * 16 < hc;
+                    for (int u = 0; u * 16 < hc; ++u) {
                         tc::tmem_load16(acc + u * 16, v);
-                        if (two) tc::tmem_load16(acc + u * 16 + 16, v + 16);
-                        tc::tmem_load_wait32(v);
-                        float x[32];
+                        tc::tmem_load_wait16(v);
+                        float x[16];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]);
-                        if ((u + 2) * 16 >= hc) {                    // the set is free before it is written out
+                        for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(v[c]);
+                        if ((u + 1) * 16 >= hc) {                    // the set is free before it is written out
                             tc::fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(acc_empty(b));
                         }
                         put(u, x);
-                        if (two) put(u + 1, x + 16);
                     }
                 }
             }
@@ -340,7 +344,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
                         if (!wait(sc_full(sr), groups / kScaleSlots & 1)) { alive = false; break; }
                         ++groups;
                     }
-                    if ((n & 1) == uint32_t(which)) {
+                    if (n % uint32_t(kGroups > 0 ? kGroups : 1) == uint32_t(which)) {
                         if (!wait(raw_full(r), raw_phase)) { alive = false; break; }
                         uint32_t code[2][CB / 8];
                         const uint32_t at = raw0 + uint32_t(r) * (kGemmRows * CB) + uint32_t(row) * CB;
@@ -378,6 +382,9 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(kGemmThreads, 1) 
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0;
                             }
+                            // (Two phases ahead a wait would pass too soon.  The group's last step was in a stage
+                            // filled since this one's last but one filling: there are at least as many stages
+                            // as groups, or half as many of two steps.)
                             if (h == 0 && !wait(empty(s), phase ^ 1)) { alive = false; break; }
                             ready = true;
 #pragma unroll
