@@ -102,18 +102,18 @@ template <uint32_t MASK> __device__ __forceinline__ uint32_t not_finite(uint32_t
     return ((w & MASK) + (0x80008000u - MASK)) & 0x80008000u;
 }
 constexpr uint32_t kBf16Exp = 0x7F807F80u, kFp16Exp = 0x7C007C00u;
-// Makes zeros of the values of `bytes` at v that are not finite; 128 threads, each its own 16 bytes
-// of every 2048.  True if this thread met one.
+// Makes zeros of the values of `bytes` at v that are not finite; 256 threads, each its own 16 bytes
+// of every 4096.  True if this thread met one.
 template <uint32_t MASK> __device__ __forceinline__ bool clear_not_finite(uint32_t v, int bytes, int tid) {
     v += uint32_t(tid) * 16;
     uint32_t seen = 0;
 #pragma unroll 8
-    for (int i = 0; i < bytes; i += 2048) {
+    for (int i = 0; i < bytes; i += 4096) {
         const uint4 w = tc::lds128(v + i);
         seen |= not_finite<MASK>(w.x) | not_finite<MASK>(w.y) | not_finite<MASK>(w.z) | not_finite<MASK>(w.w);
     }
     if (!seen) return false;
-    for (int i = 0; i < bytes; i += 2048) {
+    for (int i = 0; i < bytes; i += 4096) {
         const uint4 w = tc::lds128(v + i);
         uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -140,6 +140,52 @@ __device__ __forceinline__ void add_not_finite(const PromptArgs& a, const Prompt
         }
     }
 }
+
+// Two fp32 values in a register pair, as the packed instructions take them.
+__device__ __forceinline__ unsigned long long pair_of(uint32_t lo, uint32_t hi) {
+    unsigned long long d;
+    asm("mov.b64 %0, {%1,%2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 values_of(unsigned long long p) {
+    float2 v;
+    asm("mov.b64 {%0,%1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ unsigned long long pair_of(float x) { return pair_of(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ unsigned long long pair_fma(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long pair_add(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long pair_mul(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// The largest of N scores (NaN counts as none).
+template <int N> __device__ __forceinline__ float largest(const uint32_t (&x)[N]) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            asm("max.f32 %0, %0, %1, %2;" : "+f"(m[n]) : "f"(__uint_as_float(x[i + 2 * n])), "f"(__uint_as_float(x[i + 2 * n + 1])));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// The two warps that share 32 rows meet (`pair`: which of the four).  One whose wait has given up
+// leaves instead, so that the other, if it is in meet(), goes on; it then finds `dead` and leaves too.
+__device__ __forceinline__ bool meet(int pair, const volatile uint32_t& dead) {
+    if (__any_sync(tc::kFullMask, dead != 0)) return false;
+    asm volatile("bar.sync %0, 64;" :: "r"(pair + 1) : "memory");
+    return true;
+}
+__device__ __forceinline__ void leave(int pair) { asm volatile("bar.arrive %0, 64;" :: "r"(pair + 1) : "memory"); }
 
 struct PromptKernel { const void* fn; int threads, smem, tile_keys, parts; };      // parts: CTAs of an item
 PromptKernel prompt_bf16(int D);

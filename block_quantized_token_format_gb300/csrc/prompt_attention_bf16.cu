@@ -1,7 +1,8 @@
 // Causal attention of packed prompts, bf16: S = Q K^T and O += P V on tcgen05, softmax by a thread
 // a row.  Shapes and items in prompt_attention.cuh.
 //
-// One CTA is 128 rows.  Four warps hold a row each lane; one warp copies keys and values, one issues
+// One CTA is 128 rows.  Eight warps do the softmax, two lanes a row (each half of the tile's keys and
+// half of the output); one warp copies keys and values, one issues
 // the products.  S (fp32) and then P (bf16, over S) lie in tensor memory, P being the second
 // product's operand there, and O is summed there.  A row's reference is raised, and O scaled,
 // only where a tile's maximum is more than 2^8 above it: then rarely after the first tiles.
@@ -18,7 +19,7 @@
 namespace qg {
 namespace {
 
-constexpr int kSoftWarps = 4, kPromptThreads = 32 * (kSoftWarps + 2);
+constexpr int kSoftWarps = 8, kPromptThreads = 32 * (kSoftWarps + 2);
 constexpr float kSlack = 8.0f;     // log2: P is at most 2^8
 
 template <int D> struct Shape {
@@ -40,6 +41,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_mem[16];
     __shared__ uint32_t tmem_at, dead, odd;
+    __shared__ float most_of[2][256];                    // both lanes' maxima, of even and odd tiles
 
     const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     tc::grid_launch_dependents();
@@ -88,38 +90,38 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     const uint32_t tmem = tmem_at;
 
     if (warp < kSoftWarps) {
-        const PromptRow r = prompt_row(a, it, tid);
-        const uint32_t mine = tmem + (uint32_t(warp) << 21);
-        float top = -INFINITY, sum = 0.0f;               // the row's reference (a score), sum of P
+        constexpr int K2 = KT / 2, D2 = D / 2;
+        const int rows = warp & 3, half = warp >> 2, row = rows * 32 + lane;
+        const PromptRow r = prompt_row(a, it, row);
+        const uint32_t mine = tmem + (uint32_t(rows) << 21), o_mine = mine + S::O_AT + uint32_t(half * D2);
+        float top = -INFINITY, sum = 0.0f;               // the row's reference (a score), this lane's sum of P
         bool alive = true;
         for (int j = 0; j < tiles; ++j) {
             const int k0 = first + j * KT, sb = j % S::SB;
             if (!wait(s_full(sb), j / S::SB & 1)) { alive = false; break; }
             tc::fence_after();
-            uint32_t x[KT];
+            uint32_t x[K2];
             const uint32_t at = mine + uint32_t(sb * KT);
 #pragma unroll
-            for (int i = 0; i < KT; i += 32) tc::tmem_load32(at + i, x + i);
+            for (int i = 0; i < K2; i += 32) tc::tmem_load32(at + uint32_t(half * K2 + i), x + i);
 #pragma unroll
-            for (int i = 0; i < KT; i += 16) tc::tmem_load_wait16(x + i);
+            for (int i = 0; i < K2; i += 16) tc::tmem_load_wait16(x + i);
             const bool edge = on_edge<KT>(a, it, k0);
             if (edge) {
-                const int hi = r.pos - k0, lo = r.low - k0;
+                const int hi = r.pos - k0 - half * K2, lo = r.low - k0 - half * K2;
 #pragma unroll
-                for (int i = 0; i < KT; ++i)
+                for (int i = 0; i < K2; ++i)
                     if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
             }
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < KT; i += 8)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) m4[n] = fmaxf(m4[n], fmaxf(__uint_as_float(x[i + 2 * n]), __uint_as_float(x[i + 2 * n + 1])));
-            const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            const bool raise = j == 0 ? most > -INFINITY : (most - top) * a.c > kSlack || (top == -INFINITY && most > -INFINITY);
+            float most = largest<K2>(x);
+            float* const shared_most = most_of[j & 1];
+            shared_most[half * 128 + row] = most;
+            if (!meet(rows, dead)) { alive = false; break; }     // (both lanes have their S: P may lie over it now)
+            most = fmaxf(most, shared_most[(half ^ 1) * 128 + row]);
+            const bool raise = (most - top) * a.c > kSlack || (top == -INFINITY && most > -INFINITY);
             float factor = 1.0f;
             if (raise) {
-                factor = exp2_of((top - most) * a.c);    // (0 from -infinity)
-                if (top == -INFINITY) factor = 0.0f;
+                factor = top == -INFINITY ? 0.0f : exp2_of((top - most) * a.c);
                 top = most;
                 sum *= factor;
             }
@@ -127,31 +129,28 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                 if (!wait(pv_done, (j - 1) & 1)) { alive = false; break; }
                 tc::fence_after();
 #pragma unroll
-                for (int i = 0; i < D; i += 32) {
-                    uint32_t o[32];
-                    tc::tmem_load32(mine + S::O_AT + i, o);
-                    tc::tmem_load_wait32(o);
+                for (int i = 0; i < D2; i += 16) {
+                    uint32_t o[16];
+                    tc::tmem_load16(o_mine + i, o);
+                    tc::tmem_load_wait16(o);
 #pragma unroll
-                    for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * factor);
-                    tc::tmem_store32(mine + S::O_AT + i, o);
+                    for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * factor);
+                    tc::tmem_store16(o_mine + i, o);
                 }
             }
-            const float shift = top == -INFINITY ? 0.0f : -top * a.c;
-            float s4[4] = {};
+            const unsigned long long c2 = pair_of(a.c), shift = pair_of(top == -INFINITY ? 0.0f : -top * a.c);
+            unsigned long long s2[2] = {};
 #pragma unroll
-            for (int i = 0; i < KT; i += 4) {
-                float p[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    p[n] = exp2_of(fmaf(__uint_as_float(x[i + n]), a.c, shift));
-                    s4[n] += p[n];
-                }
-                x[i / 2] = pack_bf16(p[0], p[1]);
-                x[i / 2 + 1] = pack_bf16(p[2], p[3]);
+            for (int i = 0; i < K2; i += 2) {
+                const float2 t = values_of(pair_fma(pair_of(x[i], x[i + 1]), c2, shift));
+                const float p0 = exp2_of(t.x), p1 = exp2_of(t.y);
+                s2[i / 2 & 1] = pair_add(s2[i / 2 & 1], pair_of(__float_as_uint(p0), __float_as_uint(p1)));
+                x[i / 2] = pack_bf16(p0, p1);
             }
-            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-#pragma unroll
-            for (int i = 0; i < KT / 2; i += 32) tc::tmem_store32(at + i, x + i);
+            const float2 s = values_of(pair_add(s2[0], s2[1]));
+            sum += s.x + s.y;
+            if constexpr (K2 == 64) tc::tmem_store32(at + uint32_t(half * 32), x);
+            else tc::tmem_store16(at + uint32_t(half * 16), x);
             if (edge) {                                  // values that are not finite
                 if (!wait(v_full(j % S::STAGES), j / S::STAGES & 1)) { alive = false; break; }
                 if (clear_not_finite<kBf16Exp>(v_at + uint32_t(j % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
@@ -162,22 +161,28 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full(sb));
         }
-        if (alive && wait(o_full, 0)) {
+        float* const sums = most_of[tiles & 1];
+        sums[half * 128 + row] = sum;
+        alive = alive && wait(o_full, 0) && meet(rows, dead);
+        if (!alive) {
+            leave(rows);
+        } else {
             tc::fence_after();
-            const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+            sum += sums[(half ^ 1) * 128 + row];
+            const float inv = 1.0f / sum;
             const long long token = it.seq0 + r.tok;
-            const int head = it.head * a.group + tid % a.group;
+            const int head = it.head * a.group + row % a.group;
             const bool look = odd != 0;
-            __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride + (long long)head * D;
+            __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride + (long long)head * D + half * D2;
 #pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
+            for (int i = 0; i < D2; i += 32) {
                 uint32_t o[32];
-                tc::tmem_load32(mine + S::O_AT + i, o);
+                tc::tmem_load32(o_mine + i, o);
                 tc::tmem_load_wait32(o);
                 float y[32];
 #pragma unroll
                 for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : __uint_as_float(o[n]) * inv;
-                if (look && r.there) add_not_finite<KT, __nv_bfloat16>(a, it, r, first, tiles, i, D, y);      // visible values that were left out
+                if (look && r.there) add_not_finite<KT, __nv_bfloat16>(a, it, r, first, tiles, half * D2 + i, D, y);      // visible values that were left out
                 if (r.there) {
 #pragma unroll
                     for (int n = 0; n < 32; n += 8)
@@ -185,7 +190,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                                                                            pack_bf16(y[n + 4], y[n + 5]), pack_bf16(y[n + 6], y[n + 7]));
                 }
             }
-            if (r.there && a.lse) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
+            if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
         }
     } else if (warp == kSoftWarps) {
         // --------------------------------------------------------------------- copies
