@@ -83,7 +83,7 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     const bool f32 = act == QG_ACT_F32;
     const PromptKernel kern = f32 ? prompt_f32(head_dim) : prompt_bf16(head_dim);
     const int64_t items = (n_tok / tokens + n_seq) * n_kv_heads * kern.parts;
-    if (items > most - 1 || (f32 && 2 * n_tok > most)) return QG_EUNSUPPORTED;
+    if (items > most - 65536 || (f32 && 2 * n_tok > most)) return QG_EUNSUPPORTED;
     int dev = 0, sms = 0, optin = 0;
     PromptArgs a{};
     qg_status st = device_info(&dev, &sms, &optin, &a.status);
@@ -134,7 +134,8 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.extra_tx = test_extra_tx();
     void* params[] = {&a};
-    return launch_after(kern.fn, int(items) + 1, kern.threads, size_t(kern.smem), f32, params, stream);
+    const int64_t grid = kern.stay ? std::min<int64_t>(items, int64_t(kern.stay) * sms) : items + 1;
+    return launch_after(kern.fn, int(grid), kern.threads, size_t(kern.smem), f32, params, stream);
 }
 
 }  // extern "C"

@@ -3,7 +3,7 @@
 //
 // An item is 128 rows of the products: T = 128 / group tokens of one prompt times the `group` query
 // heads that read one key/value head (row = token * group + head), so short prompts fill rows with
-// heads and every key tile serves all of them.  A CTA takes one item, later tokens (more keys) first.
+// heads and every key tile serves all of them.  Later tokens (more keys) come first.
 // Items are numbered without a prefix sum: prompt r's begin at slot cu_seq[r] / T + r, which leaves
 // room for each prompt's last, partly filled item; a slot beyond a prompt's items has no work.
 #pragma once
@@ -35,15 +35,19 @@ struct PromptArgs {
     uint32_t wait_limit, drain_limit, extra_tx;
 };
 
-// One item's place: prompt's first token and length, first query (of the prompt), key/value head.
-struct PromptItem { int seq0, len, t0, head; };
+// One item's place: prompt's first token and length, first query (of the prompt), key/value head;
+// its first key and number of key tiles.
+struct PromptItem { int seq0, len, t0, head, first, tiles; };
 
-// The piece of `per` tokens of a prompt that a slot is; false: nothing to do.
+// The piece of `per` tokens of a prompt that a slot is; false: nothing to do.  Whole warps.
 __device__ __forceinline__ bool prompt_piece(const int32_t* cu_seq, int n_seq, int n_tok, int per, int slot, PromptItem& it) {
-    int lo = 0, hi = n_seq;                              // the last prompt that begins at or before the slot
+    int lo = 0, hi = n_seq;                              // the last prompt that begins at or before the slot,
+    const int lane = int(threadIdx.x) & 31;              // 32 probes at a time
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu_seq[mid] / per + mid <= slot) lo = mid; else hi = mid;
+        const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step;
+        const bool before = probe < hi && cu_seq[probe] / per + probe <= slot;
+        lo += __popc(__ballot_sync(tc::kFullMask, before)) * step;
+        hi = min(hi, lo + step);
     }
     const int from = cu_seq[lo], to = cu_seq[lo + 1];
     if (from < 0 || to < from || to > n_tok) return false;           // (reported by prompt_check)
@@ -65,11 +69,11 @@ __device__ __forceinline__ void prompt_check(const PromptArgs& a) {
 
 // Key tiles of an item: the first key (of the prompt) and their number.  `whole`: tiles begin at
 // multiples of KT.
-template <int KT> __device__ __forceinline__ void key_range(const PromptArgs& a, const PromptItem& it, bool whole, int& first, int& tiles) {
+template <int KT> __device__ __forceinline__ void key_range(const PromptArgs& a, PromptItem& it, bool whole) {
     const int last = min(it.t0 + a.tokens, it.len) - 1;
-    first = a.window > 0 ? max(0, it.t0 - a.window + 1) : 0;
-    if (whole) first = first / KT * KT;
-    tiles = (last - first) / KT + 1;
+    it.first = a.window > 0 ? max(0, it.t0 - a.window + 1) : 0;
+    if (whole) it.first = it.first / KT * KT;
+    it.tiles = (last - it.first) / KT + 1;
 }
 // Whether some row of the item does not see every key of the tile that begins at k0.
 template <int KT> __device__ __forceinline__ bool on_edge(const PromptArgs& a, const PromptItem& it, int k0) {
@@ -126,9 +130,9 @@ template <uint32_t MASK> __device__ __forceinline__ bool clear_not_finite(uint32
 // What was left out: adds the values that are not finite, of the keys on edge tiles that the row
 // sees, to 32 outputs from `dim` on.
 template <int KT, typename T>
-__device__ __forceinline__ void add_not_finite(const PromptArgs& a, const PromptItem& it, const PromptRow& r, int first, int tiles, int dim, int D, float (&y)[32]) {
-    for (int j = 0; j < tiles; ++j) {
-        const int k0 = first + j * KT;
+__device__ __forceinline__ void add_not_finite(const PromptArgs& a, const PromptItem& it, const PromptRow& r, int dim, int D, float (&y)[32]) {
+    for (int j = 0; j < it.tiles; ++j) {
+        const int k0 = it.first + j * KT;
         if (!on_edge<KT>(a, it, k0)) continue;
         for (int key = max(k0, r.low); key <= min(k0 + KT - 1, r.pos); ++key) {
             const T* const v = static_cast<const T*>(a.v) + (long long)(it.seq0 + key) * a.v_stride + it.head * D + dim;
@@ -138,6 +142,37 @@ __device__ __forceinline__ void add_not_finite(const PromptArgs& a, const Prompt
                 if ((__float_as_uint(w) & 0x7F800000u) == 0x7F800000u) y[n] += w;
             }
         }
+    }
+}
+
+// Stores a row's 32 16-bit values (16 words, this lane's row) from `to` on.  Four neighbouring lanes
+// first exchange their quarters, so that a store writes 64 bytes of a row and not 16 of each of 32
+// rows: a store takes the memory pipe once per 128-byte line that it touches.
+__device__ __forceinline__ void store_rows(uint16_t* to, bool there, const uint32_t (&w)[16], int lane) {
+    uint32_t q[4][4];                                    // piece p of the row, later of the rows of the four lanes
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) q[p][n] = w[4 * p + n];
+    // Lane i gives piece p and gets piece i of lane p's row: two exchanges, of bit 0 and of bit 1.
+#pragma unroll
+    for (int m = 1; m < 4; m *= 2) {
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (p & m) continue;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t got = __shfl_xor_sync(tc::kFullMask, up ? q[p][n] : q[p | m][n], m);
+                if (up) q[p][n] = got; else q[p | m][n] = got;
+            }
+        }
+    }
+    const unsigned long long mine = there ? reinterpret_cast<unsigned long long>(to) : 0ull;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {                        // (q[p] is now piece `lane % 4` of the row of lane p of the four)
+        const unsigned long long row = __shfl_sync(tc::kFullMask, mine, (lane & ~3) + p);
+        if (row) *reinterpret_cast<uint4*>(row + (lane & 3) * 16) = make_uint4(q[p][0], q[p][1], q[p][2], q[p][3]);
     }
 }
 
@@ -187,7 +222,8 @@ __device__ __forceinline__ bool meet(int pair, const volatile uint32_t& dead) {
 }
 __device__ __forceinline__ void leave(int pair) { asm volatile("bar.arrive %0, 64;" :: "r"(pair + 1) : "memory"); }
 
-struct PromptKernel { const void* fn; int threads, smem, tile_keys, parts; };      // parts: CTAs of an item
+// parts: CTAs of an item; stay: CTAs of an SM that take item after item (0: a CTA takes one, and one more checks cu_seq)
+struct PromptKernel { const void* fn; int threads, smem, tile_keys, parts, stay; };
 PromptKernel prompt_bf16(int D);
 PromptKernel prompt_f32(int D);
 

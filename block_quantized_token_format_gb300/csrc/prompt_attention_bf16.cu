@@ -6,7 +6,8 @@
 // the products.  S (fp32) and then P (bf16, over S) lie in tensor memory, P being the second
 // product's operand there, and O is summed there.  A row's reference is raised, and O scaled,
 // only where a tile's maximum is more than 2^8 above it: then rarely after the first tiles.
-// Heads of 64 and 128 take 256 columns of tensor memory and at most 96 KB, so that two CTAs share an
+// CTAs stay and take one item after another: the next one's queries and first keys are copied, and its
+// first S is made, while the last one's output is written.  Heads of 64 and 128 take 256 columns of tensor memory and at most 96 KB, so that two CTAs share an
 // SM and the one's softmax runs beside the other's products; heads of 256 fill an SM with one CTA,
 // which issues the next tile's S before it waits for P.
 //
@@ -20,6 +21,7 @@ namespace qg {
 namespace {
 
 constexpr int kSoftWarps = 8, kPromptThreads = 32 * (kSoftWarps + 2);
+constexpr int kItems = 4;          // that the copying warp may be ahead
 constexpr float kSlack = 8.0f;     // log2: P is at most 2^8
 
 template <int D> struct Shape {
@@ -39,40 +41,38 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     using S = Shape<D>;
     constexpr int KT = S::KT, CH = S::CH;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_mem[16];
+    __shared__ uint64_t bar_mem[18 + 2 * kItems];
+    __shared__ PromptItem item_mem[kItems];              // found by the copying warp, ahead of the others
     __shared__ uint32_t tmem_at, dead, odd;
-    __shared__ float most_of[2][256];                    // both lanes' maxima, of even and odd tiles
+    __shared__ float most_of[2][256], sum_of[256];       // both lanes' maxima, of even and odd tiles, and sums
 
     const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     tc::grid_launch_dependents();
     tc::grid_wait();
-    if (blockIdx.x == gridDim.x - 1) {
-        prompt_check(a);
-        return;
-    }
-    PromptItem it;
-    const int slots = (int(gridDim.x) - 1) / a.n_kv, b = int(blockIdx.x) / a.n_kv;
-    if (!prompt_piece(a.cu_seq, a.n_seq, a.n_tok, a.tokens, slots - 1 - b, it)) return;
-    it.head = int(blockIdx.x) - b * a.n_kv;
-    int first, tiles;
-    key_range<KT>(a, it, false, first, tiles);
+    if (blockIdx.x == 0) prompt_check(a);
+    const int slots = a.n_tok / a.tokens + a.n_seq, items = slots * a.n_kv;
 
     const uint32_t q_at = (smem_addr(smem_raw) + 1023u) & ~1023u, k_at = q_at + S::Q_BYTES, v_at = k_at + S::STAGES * S::T_BYTES;
     const uint32_t bars = smem_addr(bar_mem);
-    const uint32_t q_full = bars, o_full = bars + 8, pv_done = bars + 16;
-    auto k_full = [&](int s) { return bars + 24u + 8u * uint32_t(s); };
-    auto k_empty = [&](int s) { return bars + 40u + 8u * uint32_t(s); };
-    auto v_full = [&](int s) { return bars + 56u + 8u * uint32_t(s); };
-    auto v_empty = [&](int s) { return bars + 72u + 8u * uint32_t(s); };
-    auto s_full = [&](int s) { return bars + 88u + 8u * uint32_t(s); };
-    auto p_full = [&](int s) { return bars + 104u + 8u * uint32_t(s); };
+    const uint32_t q_full = bars, q_empty = bars + 8, o_full = bars + 16, o_empty = bars + 24, pv_done = bars + 32, drained = bars + 40;
+    auto k_full = [&](int s) { return bars + 48u + 8u * uint32_t(s); };
+    auto k_empty = [&](int s) { return bars + 64u + 8u * uint32_t(s); };
+    auto v_full = [&](int s) { return bars + 80u + 8u * uint32_t(s); };
+    auto v_empty = [&](int s) { return bars + 96u + 8u * uint32_t(s); };
+    auto s_full = [&](int s) { return bars + 112u + 8u * uint32_t(s); };
+    auto p_full = [&](int s) { return bars + 128u + 8u * uint32_t(s); };
+    auto i_full = [&](int s) { return bars + 144u + 8u * uint32_t(s); };
+    auto i_empty = [&](int s) { return bars + 144u + 8u * uint32_t(kItems + s); };
     const tc::Waits wait{&dead, a.status, a.wait_limit};
 
     if (tid == 0) {
         dead = odd = 0;
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         mbar_init(o_full, 1);
+        mbar_init(o_empty, kSoftWarps);
         mbar_init(pv_done, 1);
+        mbar_init(drained, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(k_full(s), 1);
             mbar_init(k_empty(s), 1);
@@ -81,6 +81,10 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
             mbar_init(s_full(s), 1);
             mbar_init(p_full(s), kSoftWarps);
         }
+        for (int s = 0; s < kItems; ++s) {
+            mbar_init(i_full(s), 1);
+            mbar_init(i_empty(s), kSoftWarps + 1);
+        }
         mbar_fence_init();
     }
     if (warp == kSoftWarps + 1) tc::tmem_alloc(smem_addr(&tmem_at), S::COLS);
@@ -88,158 +92,209 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tmem_at;
+    // The CTA's n-th item, which the copying warp has found; false: there is none, or a wait gave up.
+    auto next_item = [&](uint32_t n) { return wait(i_full(int(n % kItems)), n / kItems & 1) && item_mem[n % kItems].tiles > 0; };
+    auto give_back = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i_empty(int(n % kItems)));
+    };
 
     if (warp < kSoftWarps) {
         constexpr int K2 = KT / 2, D2 = D / 2;
         const int rows = warp & 3, half = warp >> 2, row = rows * 32 + lane;
-        const PromptRow r = prompt_row(a, it, row);
         const uint32_t mine = tmem + (uint32_t(rows) << 21), o_mine = mine + S::O_AT + uint32_t(half * D2);
-        float top = -INFINITY, sum = 0.0f;               // the row's reference (a score), this lane's sum of P
         bool alive = true;
-        for (int j = 0; j < tiles; ++j) {
-            const int k0 = first + j * KT, sb = j % S::SB;
-            if (!wait(s_full(sb), j / S::SB & 1)) { alive = false; break; }
-            tc::fence_after();
-            uint32_t x[K2];
-            const uint32_t at = mine + uint32_t(sb * KT);
-#pragma unroll
-            for (int i = 0; i < K2; i += 32) tc::tmem_load32(at + uint32_t(half * K2 + i), x + i);
-#pragma unroll
-            for (int i = 0; i < K2; i += 16) tc::tmem_load_wait16(x + i);
-            const bool edge = on_edge<KT>(a, it, k0);
-            if (edge) {
-                const int hi = r.pos - k0 - half * K2, lo = r.low - k0 - half * K2;
-#pragma unroll
-                for (int i = 0; i < K2; ++i)
-                    if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
+        uint32_t n = 0, g = 0;                           // items and key tiles so far
+        while (alive && next_item(n)) {
+            // What the loop over the tiles needs of the item: little, registers are what it lacks.
+            int tiles, inside_lo, inside_hi, pos, low;   // tiles inside: every row sees every key; visible keys from the first tile on
+            {
+                const PromptItem it = item_mem[n % kItems];
+                const PromptRow r = prompt_row(a, it, row);
+                const int last = min(it.t0 + a.tokens, it.len) - 1;
+                tiles = it.tiles;
+                pos = r.pos - it.first - half * K2;
+                low = r.low - it.first - half * K2;
+                inside_lo = a.window > 0 ? (max(0, last - a.window + 1 - it.first) + KT - 1) / KT : 0;
+                inside_hi = (it.t0 - it.first + 1) / KT;             // (exclusive)
             }
-            float most = largest<K2>(x);
-            float* const shared_most = most_of[j & 1];
-            shared_most[half * 128 + row] = most;
-            if (!meet(rows, dead)) { alive = false; break; }     // (both lanes have their S: P may lie over it now)
-            most = fmaxf(most, shared_most[(half ^ 1) * 128 + row]);
-            const bool raise = (most - top) * a.c > kSlack || (top == -INFINITY && most > -INFINITY);
-            float factor = 1.0f;
-            if (raise) {
-                factor = top == -INFINITY ? 0.0f : exp2_of((top - most) * a.c);
-                top = most;
-                sum *= factor;
-            }
-            if (j > 0 && __any_sync(tc::kFullMask, raise)) {
-                if (!wait(pv_done, (j - 1) & 1)) { alive = false; break; }
+            float top = -INFINITY, sum = 0.0f;           // the row's reference (a score), this lane's sum of P
+            for (int j = 0; j < tiles; ++j, ++g) {
+                const int sb = int(g % S::SB);
+                if (!wait(s_full(sb), g / S::SB & 1)) { alive = false; break; }
                 tc::fence_after();
+                uint32_t x[K2];
+                const uint32_t at = mine + uint32_t(sb * KT);
 #pragma unroll
-                for (int i = 0; i < D2; i += 16) {
-                    uint32_t o[16];
-                    tc::tmem_load16(o_mine + i, o);
-                    tc::tmem_load_wait16(o);
+                for (int i = 0; i < K2; i += 32) tc::tmem_load32(at + uint32_t(half * K2 + i), x + i);
 #pragma unroll
-                    for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * factor);
-                    tc::tmem_store16(o_mine + i, o);
+                for (int i = 0; i < K2; i += 16) tc::tmem_load_wait16(x + i);
+                const bool edge = j < inside_lo || j >= inside_hi;
+                if (edge) {
+                    const int hi = pos - j * KT, lo = low - j * KT;
+#pragma unroll
+                    for (int i = 0; i < K2; ++i)
+                        if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
                 }
-            }
-            const unsigned long long c2 = pair_of(a.c), shift = pair_of(top == -INFINITY ? 0.0f : -top * a.c);
-            unsigned long long s2[2] = {};
+                float most = largest<K2>(x);
+                float* const shared_most = most_of[g & 1];
+                shared_most[half * 128 + row] = most;
+                if (!meet(rows, dead)) { alive = false; break; }     // (both lanes have their S: P may lie over it now)
+                most = fmaxf(most, shared_most[(half ^ 1) * 128 + row]);
+                const bool raise = (most - top) * a.c > kSlack || (top == -INFINITY && most > -INFINITY);
+                float factor = 1.0f;
+                if (raise) {
+                    factor = top == -INFINITY ? 0.0f : exp2_of((top - most) * a.c);
+                    top = most;
+                    sum *= factor;
+                }
+                if (j > 0 && __any_sync(tc::kFullMask, raise)) {
+                    if (!wait(pv_done, (g - 1) & 1)) { alive = false; break; }
+                    tc::fence_after();
 #pragma unroll
-            for (int i = 0; i < K2; i += 2) {
-                const float2 t = values_of(pair_fma(pair_of(x[i], x[i + 1]), c2, shift));
-                const float p0 = exp2_of(t.x), p1 = exp2_of(t.y);
-                s2[i / 2 & 1] = pair_add(s2[i / 2 & 1], pair_of(__float_as_uint(p0), __float_as_uint(p1)));
-                x[i / 2] = pack_bf16(p0, p1);
-            }
-            const float2 s = values_of(pair_add(s2[0], s2[1]));
-            sum += s.x + s.y;
-            if constexpr (K2 == 64) tc::tmem_store32(at + uint32_t(half * 32), x);
-            else tc::tmem_store16(at + uint32_t(half * 16), x);
-            if (edge) {                                  // values that are not finite
-                if (!wait(v_full(j % S::STAGES), j / S::STAGES & 1)) { alive = false; break; }
-                if (clear_not_finite<kBf16Exp>(v_at + uint32_t(j % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
+                    for (int i = 0; i < D2; i += 16) {
+                        uint32_t o[16];
+                        tc::tmem_load16(o_mine + i, o);
+                        tc::tmem_load_wait16(o);
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * factor);
+                        tc::tmem_store16(o_mine + i, o);
+                    }
+                }
+                const unsigned long long c2 = pair_of(a.c), shift = pair_of(top == -INFINITY ? 0.0f : -top * a.c);
+                unsigned long long s2[2] = {};
+#pragma unroll
+                for (int i = 0; i < K2; i += 2) {
+                    const float2 t = values_of(pair_fma(pair_of(x[i], x[i + 1]), c2, shift));
+                    const float p0 = exp2_of(t.x), p1 = exp2_of(t.y);
+                    s2[i / 2 & 1] = pair_add(s2[i / 2 & 1], pair_of(__float_as_uint(p0), __float_as_uint(p1)));
+                    x[i / 2] = pack_bf16(p0, p1);
+                }
+                const float2 s = values_of(pair_add(s2[0], s2[1]));
+                sum += s.x + s.y;
+                if constexpr (K2 == 64) tc::tmem_store32(at + uint32_t(half * 32), x);
+                else tc::tmem_store16(at + uint32_t(half * 16), x);
+                if (edge) {                                  // values that are not finite
+                    if (!wait(v_full(int(g % S::STAGES)), g / S::STAGES & 1)) { alive = false; break; }
+                    if (clear_not_finite<kBf16Exp>(v_at + (g % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
+                    __syncwarp();
+                }
+                tc::tmem_store_wait();
+                tc::fence_before();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(sb));
             }
-            tc::tmem_store_wait();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(sb));
-        }
-        float* const sums = most_of[tiles & 1];
-        sums[half * 128 + row] = sum;
-        alive = alive && wait(o_full, 0) && meet(rows, dead);
-        if (!alive) {
-            leave(rows);
-        } else {
-            tc::fence_after();
-            sum += sums[(half ^ 1) * 128 + row];
-            const float inv = 1.0f / sum;
-            const long long token = it.seq0 + r.tok;
-            const int head = it.head * a.group + row % a.group;
-            const bool look = odd != 0;
-            __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride + (long long)head * D + half * D2;
+            sum_of[half * 128 + row] = sum;
+            alive = alive && wait(o_full, n & 1) && meet(rows, dead);
+            if (alive) {
+                tc::fence_after();
+                sum += sum_of[(half ^ 1) * 128 + row];
+                const float inv = 1.0f / sum;
+                const PromptItem it = item_mem[n % kItems];
+                const PromptRow r = prompt_row(a, it, row);
+                const long long token = it.seq0 + r.tok;
+                const int head = it.head * a.group + row % a.group;
+                const bool look = odd != 0;
+                uint16_t* const to = static_cast<uint16_t*>(a.out) + token * a.out_stride + (long long)head * D + half * D2;
 #pragma unroll 1
-            for (int i = 0; i < D2; i += 32) {
-                uint32_t o[32];
-                tc::tmem_load32(o_mine + i, o);
-                tc::tmem_load_wait32(o);
-                float y[32];
+                for (int d = 0; d < D2; d += 32) {
+                    uint32_t o[32];
+                    tc::tmem_load32(o_mine + d, o);
+                    tc::tmem_load_wait32(o);
+                    if (d + 32 >= D2) {                      // the next item's output may come
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_empty);
+                    }
+                    float y[32];
 #pragma unroll
-                for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : __uint_as_float(o[n]) * inv;
-                if (look && r.there) add_not_finite<KT, __nv_bfloat16>(a, it, r, first, tiles, half * D2 + i, D, y);      // visible values that were left out
-                if (r.there) {
+                    for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : __uint_as_float(o[n]) * inv;
+                    if (look && r.there) add_not_finite<KT, __nv_bfloat16>(a, it, r, half * D2 + d, D, y);      // visible values that were left out
+                    uint32_t w[16];
 #pragma unroll
-                    for (int n = 0; n < 32; n += 8)
-                        *reinterpret_cast<uint4*>(to + i + n) = make_uint4(pack_bf16(y[n], y[n + 1]), pack_bf16(y[n + 2], y[n + 3]),
-                                                                           pack_bf16(y[n + 4], y[n + 5]), pack_bf16(y[n + 6], y[n + 7]));
+                    for (int n = 0; n < 16; ++n) w[n] = pack_bf16(y[2 * n], y[2 * n + 1]);
+                    store_rows(to + d, r.there, w, lane);
                 }
+                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
             }
-            if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
+            give_back(n);
+            ++n;
         }
+        if (dead) leave(rows);
     } else if (warp == kSoftWarps) {
         // --------------------------------------------------------------------- copies
         const int n_q = a.tokens * a.group * 128;        // bytes of a 64-wide piece
-        if (tc::elect()) {
-            mbar_arrive_expect_tx(q_full, uint32_t(CH * n_q) + a.extra_tx);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) tc::load_3d(q_at + c * 16384, &a.qmap, c * 64, it.head * a.group, it.seq0 + it.t0, q_full);
-        }
-        __syncwarp();
-        int j = 0;
-        bool alive = true;
-        for (; j < tiles && alive; ++j) {
-            const int s = j % S::STAGES;
-            const uint32_t phase = (j / S::STAGES & 1) ^ 1;
-            const int key = it.seq0 + first + j * KT;
-            if (!wait(k_empty(s), phase)) { alive = false; break; }
-            if (tc::elect()) {
-                mbar_arrive_expect_tx(k_full(s), S::T_BYTES);
-#pragma unroll
-                for (int c = 0; c < CH; ++c) tc::load_3d(k_at + s * S::T_BYTES + c * KT * 128, &a.kmap, c * 64, it.head, key, k_full(s));
+        uint32_t n = 0, gk = 0, gv = 0;                  // items, key and value tiles requested
+        uint32_t extra = a.extra_tx;
+        PromptItem it;
+        auto hand_out = [&](uint32_t n) {                // the n-th item to the other warps
+            const int s = int(n % kItems);
+            if (!wait(i_empty(s), (n / kItems & 1) ^ 1)) return false;
+            if (lane == 0) {
+                item_mem[s] = it;
+                mbar_arrive(i_full(s));
             }
             __syncwarp();
-            if (!wait(v_empty(s), phase)) { alive = false; break; }
+            return true;
+        };
+        // Items in turn, every other round from the back: the rounds' shares of work even out.
+        for (int round = 0; !dead; ++round) {
+            const long long at = (long long)round * gridDim.x + ((round & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
+            if ((long long)round * gridDim.x >= items) break;
+            if (at >= items) continue;
+            const int b = int(at) / a.n_kv;
+            it.head = int(at) - b * a.n_kv;
+            if (!prompt_piece(a.cu_seq, a.n_seq, a.n_tok, a.tokens, slots - 1 - b, it)) continue;
+            key_range<KT>(a, it, false);
+            if (!hand_out(n)) break;
+            if (!wait(q_empty, (n & 1) ^ 1)) break;
             if (tc::elect()) {
-                mbar_arrive_expect_tx(v_full(s), S::T_BYTES);
+                mbar_arrive_expect_tx(q_full, uint32_t(CH * n_q) + extra);
 #pragma unroll
-                for (int c = 0; c < CH; ++c) tc::load_3d(v_at + s * S::T_BYTES + c * KT * 128, &a.vmap, c * 64, it.head, key, v_full(s));
+                for (int c = 0; c < CH; ++c) tc::load_3d(q_at + c * 16384, &a.qmap, c * 64, it.head * a.group, it.seq0 + it.t0, q_full);
             }
             __syncwarp();
+            extra = 0;
+            ++n;
+            for (int j = 0; j < it.tiles; ++j) {
+                const int s = int(gk % S::STAGES), key = it.seq0 + it.first + j * KT;
+                const uint32_t phase = (gk / S::STAGES & 1) ^ 1;
+                if (!wait(k_empty(s), phase)) break;
+                if (tc::elect()) {
+                    mbar_arrive_expect_tx(k_full(s), S::T_BYTES);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) tc::load_3d(k_at + s * S::T_BYTES + c * KT * 128, &a.kmap, c * 64, it.head, key, k_full(s));
+                }
+                __syncwarp();
+                ++gk;
+                if (!wait(v_empty(s), phase)) break;
+                if (tc::elect()) {
+                    mbar_arrive_expect_tx(v_full(s), S::T_BYTES);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) tc::load_3d(v_at + s * S::T_BYTES + c * KT * 128, &a.vmap, c * 64, it.head, key, v_full(s));
+                }
+                __syncwarp();
+                ++gv;
+            }
         }
+        it.tiles = 0;                                    // no more items
+        hand_out(n);
         if (dead) {                                      // copies still on their way end before the CTA does
-            mbar_wait(q_full, 0, a.drain_limit);
-            for (int s = 0; s < S::STAGES; ++s) {
-                // (keys may have been requested for tile j where values were not)
-                for (int t = j; t >= 0 && t > j - S::STAGES - 1; --t)
-                    if (t % S::STAGES == s) {
-                        mbar_wait(k_full(s), t / S::STAGES & 1, min(a.drain_limit, 65536u));
-                        mbar_wait(v_full(s), t / S::STAGES & 1, min(a.drain_limit, 65536u));
-                    }
+            if (n > 0) mbar_wait(q_full, (n - 1) & 1, a.drain_limit);
+            for (uint32_t i = 1; i <= S::STAGES; ++i) {
+                if (gk >= i) mbar_wait(k_full(int((gk - i) % S::STAGES)), (gk - i) / S::STAGES & 1, a.drain_limit);
+                if (gv >= i) mbar_wait(v_full(int((gv - i) % S::STAGES)), (gv - i) / S::STAGES & 1, a.drain_limit);
             }
         }
     } else {
         // ------------------------------------------------------------------- products
         const uint32_t i_s = tc::instr(true, KT, false) | a.negate, i_o = tc::instr(true, D, true);
-        bool alive = wait(q_full, 0);
-        auto scores = [&](int j) {
-            const int s = j % S::STAGES, sb = j % S::SB;
-            if (!wait(k_full(s), j / S::STAGES & 1)) return false;
+        bool alive = true;
+        uint32_t n = 0, g = 0;                           // items and key tiles so far
+        // S of the CTA's g-th tile.
+        auto scores = [&](uint32_t g, bool last) {
+            const int s = int(g % S::STAGES), sb = int(g % S::SB);
+            if (!wait(k_full(s), g / S::STAGES & 1)) return false;
             tc::fence_after();
             if (tc::elect()) {
                 const uint64_t dq = tc::desc_k(q_at), dk = tc::desc_k(k_at + s * S::T_BYTES);
@@ -250,31 +305,41 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                         tc::mma(tmem + uint32_t(sb * KT), dq + c * (16384 >> 4) + 2 * i, dk + c * (KT * 128 >> 4) + 2 * i, i_s, c + i > 0);
                 tc::commit(k_empty(s));
                 tc::commit(s_full(sb));
+                if (last) tc::commit(q_empty);
             }
             __syncwarp();
             return true;
         };
-        if (alive && S::SB == 2) alive = scores(0);
-        for (int j = 0; j < tiles && alive; ++j) {
-            const int s = j % S::STAGES, sb = j % S::SB;
-            if (S::SB == 1) alive = scores(j);
-            else if (j + 1 < tiles) alive = scores(j + 1);
-            if (!alive || !wait(v_full(s), j / S::STAGES & 1) || !wait(p_full(sb), j / S::SB & 1)) { alive = false; break; }
-            tc::fence_after();
-            if (tc::elect()) {
-                const uint64_t dv = tc::desc_mn(v_at + s * S::T_BYTES, KT * 128);
+        while (alive && next_item(n)) {
+            const int tiles = item_mem[n % kItems].tiles;
+            give_back(n);
+            alive = wait(q_full, n & 1);
+            if (alive && S::SB == 2) alive = scores(g, tiles == 1);
+            for (int j = 0; j < tiles && alive; ++j, ++g) {
+                const int s = int(g % S::STAGES), sb = int(g % S::SB);
+                if (S::SB == 1) alive = scores(g, j + 1 == tiles);
+                else if (j + 1 < tiles) alive = scores(g + 1, j + 2 == tiles);
+                if (!alive || (j == 0 && !wait(o_empty, (n & 1) ^ 1)) || !wait(v_full(s), g / S::STAGES & 1) || !wait(p_full(sb), g / S::SB & 1)) {
+                    alive = false;
+                    break;
+                }
+                tc::fence_after();
+                if (tc::elect()) {
+                    const uint64_t dv = tc::desc_mn(v_at + s * S::T_BYTES, KT * 128);
 #pragma unroll
-                for (int i = 0; i < KT / 16; ++i)
-                    tc::mma_ts(tmem + S::O_AT, tmem + uint32_t(sb * KT + i * 8), dv + i * (2048 >> 4), i_o, j > 0 || i > 0);
-                tc::commit(v_empty(s));
-                tc::commit(pv_done);
-                if (j + 1 == tiles) tc::commit(o_full);
+                    for (int i = 0; i < KT / 16; ++i)
+                        tc::mma_ts(tmem + S::O_AT, tmem + uint32_t(sb * KT + i * 8), dv + i * (2048 >> 4), i_o, j > 0 || i > 0);
+                    tc::commit(v_empty(s));
+                    tc::commit(pv_done);
+                    if (j + 1 == tiles) tc::commit(o_full);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            ++n;
         }
-        if (!alive && tc::elect()) tc::commit(o_full);   // products under way end before the columns are given back
+        if (tc::elect()) tc::commit(drained);            // products under way end before the columns are given back
         __syncwarp();
-        mbar_wait(o_full, 0, a.drain_limit);
+        mbar_wait(drained, 0, a.drain_limit);
     }
     __syncwarp();
     tc::fence_before();
@@ -283,7 +348,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     if (warp == kSoftWarps + 1) tc::tmem_free(tmem, S::COLS);
 }
 
-template <int D> PromptKernel kernel() { return {(const void*)&prompt_bf16_kernel<D>, kPromptThreads, Shape<D>::SMEM, Shape<D>::KT, 1}; }
+template <int D> PromptKernel kernel() { return {(const void*)&prompt_bf16_kernel<D>, kPromptThreads, Shape<D>::SMEM, Shape<D>::KT, 1, D == 256 ? 1 : 2}; }
 
 }  // namespace
 

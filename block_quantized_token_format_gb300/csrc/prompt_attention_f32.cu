@@ -156,8 +156,8 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
     if (!prompt_piece(a.cu_seq, a.n_seq, a.n_tok, a.tokens, slots - 1 - b, it)) return;
     const int part = int(blockIdx.x) - b * parts, half = part % S::HALVES;
     it.head = part / S::HALVES;
-    int first, tiles;
-    key_range<KT>(a, it, true, first, tiles);
+    key_range<KT>(a, it, true);
+    const int first = it.first, tiles = it.tiles;
 
     const uint32_t q_at = (smem_addr(smem_raw) + 1023u) & ~1023u, k_at = q_at + 2 * S::Q_TERM, v_at = k_at + 2 * S::STAGES * S::K_TERM;
     const uint32_t bars = smem_addr(bar_mem);
@@ -311,7 +311,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
                     float y[32];
 #pragma unroll
                     for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : o[i + n] * inv;
-                    if (look) add_not_finite<KT, float>(a, it, r, first, tiles, half * DV + i, D, y);      // visible values that were left out
+                    if (look) add_not_finite<KT, float>(a, it, r, half * DV + i, D, y);      // visible values that were left out
 #pragma unroll
                     for (int n = 0; n < 32; n += 4) *reinterpret_cast<float4*>(to + i + n) = make_float4(y[n], y[n + 1], y[n + 2], y[n + 3]);
                 }
@@ -428,7 +428,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
 }
 
 template <int D> PromptKernel kernel() {
-    return {(const void*)&prompt_f32_kernel<D>, kPromptThreads, Shape<D>::SMEM, kTileKeys, Shape<D>::HALVES};
+    return {(const void*)&prompt_f32_kernel<D>, kPromptThreads, Shape<D>::SMEM, kTileKeys, Shape<D>::HALVES, 0};
 }
 
 }  // namespace
