@@ -25,7 +25,7 @@ constexpr int kItems = 4;          // that the copying warp may be ahead
 constexpr float kSlack = 8.0f;     // log2: P is at most 2^8
 
 template <int D> struct Shape {
-    static constexpr int KT = D == 256 ? 64 : 128, STAGES = D == 256 ? 2 : 1, SB = D == 256 ? 2 : 1;
+    static constexpr int KT = 64, STAGES = 2, SB = 2;
     static constexpr int CH = D / 64;                                // 64-wide pieces of a head
     static constexpr int Q_BYTES = CH * 128 * 128, T_BYTES = CH * KT * 128;      // (T: a key or value tile)
     static constexpr int SMEM = 1024 + Q_BYTES + 2 * STAGES * T_BYTES;
