@@ -106,18 +106,18 @@ template <uint32_t MASK> __device__ __forceinline__ uint32_t not_finite(uint32_t
     return ((w & MASK) + (0x80008000u - MASK)) & 0x80008000u;
 }
 constexpr uint32_t kBf16Exp = 0x7F807F80u, kFp16Exp = 0x7C007C00u;
-// Makes zeros of the values of `bytes` at v that are not finite; 256 threads, each its own 16 bytes
-// of every 4096.  True if this thread met one.
-template <uint32_t MASK> __device__ __forceinline__ bool clear_not_finite(uint32_t v, int bytes, int tid) {
+// Makes zeros of the values of `bytes` at v that are not finite; 128 * SIDES threads, each its own 16
+// bytes of every 2048 * SIDES.  True if this thread met one.
+template <uint32_t MASK, int SIDES> __device__ __forceinline__ bool clear_not_finite(uint32_t v, int bytes, int tid) {
     v += uint32_t(tid) * 16;
     uint32_t seen = 0;
 #pragma unroll 8
-    for (int i = 0; i < bytes; i += 4096) {
+    for (int i = 0; i < bytes; i += 2048 * SIDES) {
         const uint4 w = tc::lds128(v + i);
         seen |= not_finite<MASK>(w.x) | not_finite<MASK>(w.y) | not_finite<MASK>(w.z) | not_finite<MASK>(w.w);
     }
     if (!seen) return false;
-    for (int i = 0; i < bytes; i += 4096) {
+    for (int i = 0; i < bytes; i += 2048 * SIDES) {
         const uint4 w = tc::lds128(v + i);
         uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

@@ -176,7 +176,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                 else tc::tmem_store16(at + uint32_t(half * 16), x);
                 if (edge) {                                  // values that are not finite
                     if (!wait(v_full(int(g % S::STAGES)), g / S::STAGES & 1)) { alive = false; break; }
-                    if (clear_not_finite<kBf16Exp>(v_at + (g % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
+                    if (clear_not_finite<kBf16Exp, 2>(v_at + (g % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
                     __syncwarp();
                 }
                 tc::tmem_store_wait();

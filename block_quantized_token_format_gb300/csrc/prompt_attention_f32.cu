@@ -8,7 +8,8 @@
 // P is 2^7 times the exponential, so that two terms of it reach 2^-31 of the row's largest; each
 // tile's P V goes to fresh accumulators and is added in fp32 registers.
 //
-// One CTA is 128 rows, a thread a row; S and the tiles' P V have two buffers each, so that the next
+// One CTA is 128 rows, two lanes a row (each half of a tile's keys and half of the output; one with heads
+// of 256, whose operands leave no shared memory for the lanes' maxima); S and the tiles' P V have two buffers each, so that the next
 // tile's S and this tile's P V run beside the softmax.  Heads of 256 take two CTAs, each 128 values of
 // the output.
 #include "prompt_attention.cuh"
@@ -16,12 +17,13 @@
 namespace qg {
 namespace {
 
-constexpr int kSoftWarps = 4, kPromptThreads = 32 * (kSoftWarps + 2), kStageThreads = 256;
+constexpr int kStageThreads = 256;
 constexpr float kSlack = 8.0f, kLift = 7.0f;     // log2: P is 2^7 times the exponential, at most 2^15
 constexpr int kTileKeys = 64;
 
 template <int D> struct Shape {
     static constexpr int KT = kTileKeys, DV = D < 128 ? D : 128, HALVES = D / DV, STAGES = D == 256 ? 1 : 2;
+    static constexpr int SIDES = D == 256 ? 1 : 2, WARPS = 4 * SIDES;        // lanes of a row, warps of the softmax
     static constexpr int CH = D / 64, CV = DV / 64;
     static constexpr int Q_TERM = CH * 128 * 128, K_TERM = CH * KT * 128, V_TERM = CV * KT * 128;
     static constexpr int SMEM = 1024 + 2 * Q_TERM + 2 * STAGES * (K_TERM + V_TERM);
@@ -135,14 +137,13 @@ template <int D> __global__ void __launch_bounds__(kStageThreads) stage_kernel(c
     }
 }
 
-__device__ __forceinline__ uint32_t pack_half(__half lo, __half hi) { return __half_as_ushort(lo) | uint32_t(__half_as_ushort(hi)) << 16; }
-
-template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32_kernel(const __grid_constant__ PromptArgs a) {
+template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1) prompt_f32_kernel(const __grid_constant__ PromptArgs a) {
     using S = Shape<D>;
-    constexpr int KT = S::KT, CH = S::CH, CV = S::CV, DV = S::DV;
+    constexpr int KT = S::KT, CH = S::CH, CV = S::CV, DV = S::DV, SIDES = S::SIDES, kSoftWarps = S::WARPS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_mem[18];
     __shared__ uint32_t tmem_at, dead, odd;
+    __shared__ float most_of[2][SIDES == 2 ? 256 : 1], sum_of[SIDES == 2 ? 256 : 1];       // both lanes' maxima, of even and odd tiles, and sums
 
     const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     tc::grid_launch_dependents();
@@ -195,19 +196,21 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
     const uint32_t tmem = tmem_at;
 
     if (warp < kSoftWarps) {
-        const PromptRow r = prompt_row(a, it, tid);
-        const uint32_t mine = tmem + (uint32_t(warp) << 21);
-        const int head = it.head * a.group + tid % a.group;
+        constexpr int K2 = KT / SIDES, D2 = DV / SIDES;
+        const int rows = warp & 3, side = warp >> 2, row = rows * 32 + lane;
+        const PromptRow r = prompt_row(a, it, row);
+        const uint32_t mine = tmem + (uint32_t(rows) << 21);
+        const int head = it.head * a.group + row % a.group;
         const long long token = it.seq0 + r.tok;
         const float c = r.there ? a.c * a.qscale[token * a.n_heads + head] : 0.0f;
         const float* const ks = a.kscale + (long long)(it.seq0 + first) * a.n_kv + it.head;
         const float* const vs = a.vscale + (long long)(it.seq0 + first) * a.n_kv + it.head;
         const long long hop = (long long)KT * a.n_kv;
         float k_next = ks[0], v_next = vs[0], v_mine = 0.0f;
-        float top = -INFINITY, sum = 0.0f;               // the row's reference (log2 of an exponential), sum of P
-        float o[DV];
+        float top = -INFINITY, sum = 0.0f;               // the row's reference (log2 of an exponential), this lane's sum of P
+        float o[D2];
 #pragma unroll
-        for (int i = 0; i < DV; ++i) o[i] = 0.0f;
+        for (int i = 0; i < D2; ++i) o[i] = 0.0f;
         bool alive = true;
         // Adds the part of the output that tile j made, times its factor.
         auto gather = [&](int j) {
@@ -215,9 +218,9 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
             if (!wait(o_full(ob), j >> 1 & 1)) return false;
             tc::fence_after();
 #pragma unroll
-            for (int i = 0; i < DV; i += 32) {
+            for (int i = 0; i < D2; i += 32) {
                 uint32_t x[32];
-                tc::tmem_load32(mine + S::O_AT + uint32_t(ob * DV + i), x);
+                tc::tmem_load32(mine + S::O_AT + uint32_t(ob * DV + side * D2 + i), x);
                 tc::tmem_load_wait32(x);
 #pragma unroll
                 for (int n = 0; n < 32; ++n) o[i + n] = fmaf(__uint_as_float(x[n]), v_mine, o[i + n]);
@@ -236,25 +239,26 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
             }
             if (!wait(s_full(sb), j >> 1 & 1)) { alive = false; break; }
             tc::fence_after();
-            uint32_t x[KT];
+            uint32_t x[K2];
             const uint32_t at = mine + uint32_t(sb * KT);
 #pragma unroll
-            for (int i = 0; i < KT; i += 32) tc::tmem_load32(at + i, x + i);
+            for (int i = 0; i < K2; i += 32) tc::tmem_load32(at + uint32_t(side * K2 + i), x + i);
 #pragma unroll
-            for (int i = 0; i < KT; i += 16) tc::tmem_load_wait16(x + i);
+            for (int i = 0; i < K2; i += 32) tc::tmem_load_wait32(x + i);
             const bool edge = on_edge<KT>(a, it, k0);
             if (edge) {
-                const int hi = r.pos - k0, lo = r.low - k0;
+                const int hi = r.pos - k0 - side * K2, lo = r.low - k0 - side * K2;
 #pragma unroll
-                for (int i = 0; i < KT; ++i)
+                for (int i = 0; i < K2; ++i)
                     if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
             }
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < KT; i += 8)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) m4[n] = fmaxf(m4[n], fmaxf(__uint_as_float(x[i + 2 * n]), __uint_as_float(x[i + 2 * n + 1])));
-            const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
+            float most = largest<K2>(x);
+            if constexpr (SIDES == 2) {
+                most_of[sb][side * 128 + row] = most;
+                if (!meet(rows, dead)) { alive = false; break; }     // (both lanes have their S: P may lie over it now)
+                most = fmaxf(most, most_of[sb][(side ^ 1) * 128 + row]);
+            }
+            most *= f;
             const bool raise = most - top > kSlack || (top == -INFINITY && most > -INFINITY);
             float factor = 1.0f;
             if (raise) {
@@ -262,30 +266,30 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
                 top = most;
                 sum *= factor;
             }
-            const float shift = top == -INFINITY ? 0.0f : kLift - top;
-            float s4[4] = {};
-            uint32_t lo32[KT / 2];
+            const unsigned long long f2 = pair_of(f), shift = pair_of(top == -INFINITY ? 0.0f : kLift - top);
+            unsigned long long s2[2] = {};
+            uint32_t lo16[K2 / 2];
 #pragma unroll
-            for (int i = 0; i < KT; i += 4) {
-                __half h[4], l[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float p = exp2_of(fmaf(__uint_as_float(x[i + n]), f, shift));
-                    s4[n] += p;
-                    h[n] = __float2half_rn(p);
-                    l[n] = __float2half_rn(p - __half2float(h[n]));
-                }
-                x[i / 2] = pack_half(h[0], h[1]);
-                x[i / 2 + 1] = pack_half(h[2], h[3]);
-                lo32[i / 2] = pack_half(l[0], l[1]);
-                lo32[i / 2 + 1] = pack_half(l[2], l[3]);
+            for (int i = 0; i < K2; i += 2) {
+                const float2 t = values_of(pair_fma(pair_of(x[i], x[i + 1]), f2, shift));
+                const float p0 = exp2_of(t.x), p1 = exp2_of(t.y);
+                s2[i / 2 & 1] = pair_add(s2[i / 2 & 1], pair_of(__float_as_uint(p0), __float_as_uint(p1)));
+                const __half2 h = __floats2half2_rn(p0, p1);
+                const float2 back = __half22float2(h);
+                const __half2 l = __floats2half2_rn(p0 - back.x, p1 - back.y);
+                x[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                lo16[i / 2] = *reinterpret_cast<const uint32_t*>(&l);
             }
-            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            tc::tmem_store32(at, x);
-            tc::tmem_store32(at + KT / 2, lo32);
+            const float2 s = values_of(pair_add(s2[0], s2[1]));
+            sum += s.x + s.y;
+#pragma unroll
+            for (int i = 0; i < K2 / 2; i += 16) {
+                tc::tmem_store16(at + uint32_t(side * (K2 / 2) + i), x + i);
+                tc::tmem_store16(at + KT / 2 + uint32_t(side * (K2 / 2) + i), lo16 + i);
+            }
             if (edge) {                                  // values that are not finite
                 if (!wait(v_full(j % S::STAGES), j / S::STAGES & 1)) { alive = false; break; }
-                if (clear_not_finite<kFp16Exp>(v_at + uint32_t(j % S::STAGES) * 2 * S::V_TERM, 2 * S::V_TERM, tid)) odd = 1;
+                if (clear_not_finite<kFp16Exp, SIDES>(v_at + uint32_t(j % S::STAGES) * 2 * S::V_TERM, 2 * S::V_TERM, tid)) odd = 1;
                 __syncwarp();
             }
             tc::tmem_store_wait();
@@ -296,28 +300,31 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
                 if (!gather(j - 1)) { alive = false; break; }
                 if (__any_sync(tc::kFullMask, raise)) {
 #pragma unroll
-                    for (int i = 0; i < DV; ++i) o[i] *= factor;
+                    for (int i = 0; i < D2; ++i) o[i] *= factor;
                 }
             }
             v_mine = v_this;
         }
-        if (alive && gather(tiles - 1)) {
+        if constexpr (SIDES == 2) sum_of[side * 128 + row] = sum;
+        if (alive && gather(tiles - 1) && (SIDES == 1 || meet(rows, dead))) {
+            if constexpr (SIDES == 2) sum += sum_of[(side ^ 1) * 128 + row];
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const bool look = odd != 0;
-            float* const to = static_cast<float*>(a.out) + token * a.out_stride + (long long)head * D + half * DV;
+            float* const to = static_cast<float*>(a.out) + token * a.out_stride + (long long)head * D + half * DV + side * D2;
             if (r.there) {
 #pragma unroll
-                for (int i = 0; i < DV; i += 32) {
+                for (int i = 0; i < D2; i += 32) {
                     float y[32];
 #pragma unroll
                     for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : o[i + n] * inv;
-                    if (look) add_not_finite<KT, float>(a, it, r, half * DV + i, D, y);      // visible values that were left out
+                    if (look) add_not_finite<KT, float>(a, it, r, half * DV + side * D2 + i, D, y);      // visible values that were left out
 #pragma unroll
                     for (int n = 0; n < 32; n += 4) *reinterpret_cast<float4*>(to + i + n) = make_float4(y[n], y[n + 1], y[n + 2], y[n + 3]);
                 }
-                if (a.lse && half == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : (top - kLift) * kLn2 + logf(sum);
+                if (a.lse && half == 0 && side == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : (top - kLift) * kLn2 + logf(sum);
             }
         }
+        if (SIDES == 2 && dead) leave(rows);
     } else if (warp == kSoftWarps) {
         // --------------------------------------------------------------------- copies
         const int n_q = a.tokens * a.group * 128;        // bytes of a 64-wide piece
@@ -428,7 +435,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, 1) prompt_f32
 }
 
 template <int D> PromptKernel kernel() {
-    return {(const void*)&prompt_f32_kernel<D>, kPromptThreads, Shape<D>::SMEM, kTileKeys, Shape<D>::HALVES, 0};
+    return {(const void*)&prompt_f32_kernel<D>, 32 * (Shape<D>::WARPS + 2), Shape<D>::SMEM, kTileKeys, Shape<D>::HALVES, 0};
 }
 
 }  // namespace
