@@ -580,8 +580,8 @@ qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int c
     return launch_with((launch_flags() & QG_LAUNCH_EARLY_START) != 0, fn, grid, threads, smem, cluster, params, stream);
 }
 
-qg_status launch_after(const void* fn, int grid, int threads, size_t smem, bool early, void** params, void* stream) {
-    return launch_with(early || (launch_flags() & QG_LAUNCH_EARLY_START) != 0, fn, grid, threads, smem, 1, params, stream);
+qg_status launch_after(const void* fn, int grid, int threads, size_t smem, int cluster, bool early, void** params, void* stream) {
+    return launch_with(early || (launch_flags() & QG_LAUNCH_EARLY_START) != 0, fn, grid, threads, smem, cluster, params, stream);
 }
 
 }  // namespace qg

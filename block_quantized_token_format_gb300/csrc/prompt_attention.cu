@@ -135,7 +135,7 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     a.extra_tx = test_extra_tx();
     void* params[] = {&a};
     const int64_t grid = kern.stay ? std::min<int64_t>(items, int64_t(kern.stay) * sms) : items + 1;
-    return launch_after(kern.fn, int(grid), kern.threads, size_t(kern.smem), f32, params, stream);
+    return launch_after(kern.fn, int(grid), kern.threads, size_t(kern.smem), 1, f32, params, stream);
 }
 
 }  // extern "C"

@@ -3,6 +3,8 @@
 // kernel in qgemm.cuh.
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
 
 #include "qgemm.cuh"
 #include "qgemv_host.h"
@@ -239,25 +241,83 @@ qg_status check(const GemmCall& c) {
     return QG_OK;
 }
 
-// The tile's tokens.  A tile of bn tokens takes about max(2 bn, 190) clocks per step of 64 along K
-// (fp32: 6 bn, 400): the tensor cores' time, or the decoding of the codes; tiles run on all SMs in
-// rounds.
-int tile_tokens(int fmt, bool f32, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms) {
-    int best = 32;
+// Clusters of `parts` CTAs, an SM each, that run at once (cached: every geometry of these kernels
+// fills an SM).
+int clusters_at_once(const void* fn, int dev, int threads, size_t smem, int parts) {
+    static std::mutex mu;
+    static std::map<std::pair<int, int>, int> cache;
+    std::lock_guard<std::mutex> lk(mu);
+    const auto key = std::make_pair(dev, parts);
+    const auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(parts));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(parts);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) { cudaGetLastError(); n = 0; }
+    cache[key] = n;
+    return n;
+}
+
+// A kernel's shared memory for tiles of bn tokens.
+struct Geometry { int subs, stages, raws; size_t smem; };
+Geometry geometry(int fmt, bool f32, int bn, int optin) {
+    // Stages of one step of K, or of two where they are small (a stage's waits and bookkeeping take
+    // about 200 clocks of the warp that issues the products): four or three of them; the rest of
+    // shared memory holds raw codes on their way, which is what few tokens to a tile need.  Their slots
+    // are a multiple of the decoding groups: a slot then always belongs to the same group, which waits
+    // for its fills one by one.
+    const bool quant = fmt != QG_BF16;
+    const int groups = decode_groups(fmt, f32);
+    const size_t raw = size_t(kGemmRows) * size_t(raw_codes(fmt)), scales = size_t(kGemmRows) * kScaleSlots * size_t(raw_scales(fmt));
+    const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
+    Geometry g{};
+    g.subs = !f32 && bn <= 128 ? 2 : 1;
+    const size_t stage = size_t(g.subs) * (size_t(terms_w(fmt, f32)) * kOperandA + size_t(terms_x(fmt, f32)) * size_t(bn) * kGemmK * 2);
+    g.stages = int(std::min<size_t>(quant ? (g.subs == 2 ? 3 : 4) : 8, (room - size_t(groups) * raw) / stage));
+    g.raws = quant ? int(std::min<size_t>(kMostRaws, (room - size_t(g.stages) * stage) / raw)) / groups * groups : 0;
+    g.smem = 1024 + scales + size_t(g.raws) * raw + size_t(g.stages) * stage;
+    return g;
+}
+
+// The tile's tokens, and the CTAs that share its K.  Measured on GB300 (128 rows, 64 of K, all SMs): a
+// step takes 265 to 330 ns whatever the tokens, until 1.85 ns a token are more (240: 440 ns); with bf16
+// weights 160 ns or 1.55 a token; in fp32 330 ns and 3.2 a token (bf16 weights 300 and 2.75).  Tiles run
+// on all SMs in rounds, each with about 1.5 us of its own; a cluster's join takes 2.5 us.
+struct Shape { int bn, parts; };
+template <typename Clusters>
+Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms, Clusters clusters) {
+    Shape best{32, 1};
     double least = 0;
-    for (int b = 32; b <= 256 && (f32 ? b <= 128 : true); b *= 2) {
-        const int bn = std::min(b, gemm_most_tokens(fmt, f32));
-        const double step = f32 ? std::max(6.0 * bn, 400.0) : std::max(2.0 * bn, 190.0);
-        double rounds;
-        if (n_experts == 0) {
-            rounds = double((m_tiles * ((n_slots + bn - 1) / bn) + sms - 1) / sms);
-        } else {
-            // Experts' rows spread around the mean: on average half a tile more than they fill.
-            const double used = double(std::min(n_experts, n_slots));
-            rounds = std::max(1.0, double(m_tiles) * std::max(used, double(n_slots) / bn + 0.5 * used) / sms);
+    const double ksteps = double((n_in + kGemmK - 1) / kGemmK);
+    for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
+        const bool quant = fmt != QG_BF16;
+        const double step = f32 ? (quant ? 330.0 + 3.2 * bn : 300.0 + 2.75 * bn) : quant ? std::max(290.0, 1.85 * bn) : std::max(160.0, 1.55 * bn);
+        for (int parts = 1; parts <= 8; parts *= 2) {
+            double rounds;
+            if (n_experts == 0) {
+                const int64_t tiles = m_tiles * ((n_slots + bn - 1) / bn);
+                if (parts > 1 && (tiles * parts > sms || ksteps < 8 * parts || clusters(parts) < tiles)) break;
+                rounds = double((tiles + sms - 1) / sms);
+            } else {
+                // Experts' rows spread around the mean: on average half a tile more than they fill.
+                if (parts > 1) break;
+                const double used = double(std::min(n_experts, n_slots));
+                rounds = std::max(1.0, double(m_tiles) * std::max(used, double(n_slots) / bn + 0.5 * used) / sms);
+            }
+            const double cost = rounds * (ksteps / parts * step + 1500.0) + (parts > 1 ? 2500.0 : 0.0);
+            if (least == 0 || cost < least) {
+                best = {bn, parts};
+                least = cost;
+            }
         }
-        const double cost = rounds * step;
-        if (b == 32 || cost <= least) { best = bn; least = cost; }
     }
     return best;
 }
@@ -298,7 +358,13 @@ qg_status launch_gemm(const GemmCall& c) {
     qg_status st = device_info(&dev, &sms, &optin, &status);
     if (st != QG_OK) return st;
     const int64_t m_tiles = (c.n_out + kGemmRows - 1) / kGemmRows;
-    const int bn = tile_tokens(c.fmt, f32, m_tiles, c.n_slots, c.n_experts, sms);
+    const void* const fn = qgemm_lookup(c.fmt, f32);
+    const int threads = gemm_threads(c.fmt, f32);
+    const Shape shape = tile_shape(c.fmt, f32, c.n_in, m_tiles, c.n_slots, c.n_experts, sms, [&](int parts) {
+        const size_t smem = geometry(c.fmt, f32, 32, optin).smem;
+        return blocks_per_sm(fn, dev, optin, threads, smem) < 1 ? 0 : clusters_at_once(fn, dev, threads, smem, parts);
+    });
+    const int bn = shape.bn;
     const int64_t n_tiles = (c.n_slots + bn - 1) / bn;
     if ((n_tiles + c.n_experts) * m_tiles > (int64_t(1) << 31) - 4096) return QG_EUNSUPPORTED;
     uint8_t* const ws = static_cast<uint8_t*>(c.workspace);
@@ -325,23 +391,14 @@ qg_status launch_gemm(const GemmCall& c) {
     a.wait_limit = wait_limit();
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.extra_tx = test_extra_tx();
-    const void* const fn = qgemm_lookup(c.fmt, f32);
-    const size_t sub = size_t(terms_w(c.fmt, f32)) * kOperandA + size_t(terms_x(c.fmt, f32)) * size_t(bn) * kGemmK * 2;
-    // Stages of one step of K, or of two where they are small (a stage's waits and bookkeeping take
-    // about 200 clocks of the thread that issues the products, a product's issue 60): four or three
-    // of them; the rest of shared memory holds raw codes on their way, which is what few tokens to a
-    // tile need.  Their slots are a multiple of the decoding groups: a slot then always belongs to the
-    // same group, which waits for its fills one by one.
-    const size_t raw = size_t(kGemmRows) * size_t(raw_codes(c.fmt)), scales = size_t(kGemmRows) * kScaleSlots * size_t(raw_scales(c.fmt));
-    const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
-    a.subs = !f32 && bn <= 128 ? 2 : 1;
-    const size_t stage = size_t(a.subs) * sub;
-    const int groups = decode_groups(c.fmt, f32), threads = gemm_threads(c.fmt, f32);
-    a.stages = int(std::min<size_t>(quant ? (a.subs == 2 ? (bn == 128 ? 2 : 3) : 4) : 8, (room - size_t(groups) * raw) / stage));
-    a.raws = quant ? int(std::min<size_t>(kMostRaws, (room - size_t(a.stages) * stage) / std::max<size_t>(raw, 1))) / std::max(groups, 1) * groups : 0;
-    const size_t smem = 1024 + scales + size_t(a.raws) * raw + size_t(a.stages) * stage;
+    const Geometry geo = geometry(c.fmt, f32, bn, optin);
+    const int groups = decode_groups(c.fmt, f32);
+    a.subs = geo.subs;
+    a.stages = geo.stages;
+    a.raws = geo.raws;
+    a.parts = shape.parts;
     if (a.stages < 2 || a.stages * a.subs < groups || (quant && a.raws < groups)) return QG_EUNSUPPORTED;
-    if (blocks_per_sm(fn, dev, optin, threads, smem) < 1) return QG_EUNSUPPORTED;
+    if (blocks_per_sm(fn, dev, optin, threads, geo.smem) < 1) return QG_EUNSUPPORTED;
     const int64_t rows = std::max<int64_t>(1, c.n_experts) * c.n_out, pitch = row_stride(c.fmt, c.n_in);
     st = stages_x ? encode_tokens(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, bn)
                   : encode_tokens(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, bn);
@@ -381,7 +438,8 @@ qg_status launch_gemm(const GemmCall& c) {
     }
     const int64_t tiles = c.n_experts ? sms : n_tiles * m_tiles;
     void* params[] = {&a};
-    return launch_after(fn, int(std::min<int64_t>(sms, tiles)), threads, smem, before, params, c.stream);
+    return launch_after(fn, shape.parts > 1 ? int(tiles) * shape.parts : int(std::min<int64_t>(sms, tiles)), threads, geo.smem, shape.parts, before,
+                        params, c.stream);
 }
 
 }  // namespace

@@ -66,6 +66,7 @@ struct GemmArgs {
     void* y;
     long long residual_stride, y_stride;
     int f, bn, subs, stages, raws, m_tiles, n_tiles;      // subs: steps of K in a stage
+    int parts;                                            // CTAs of a cluster that share a tile's K
     unsigned int* status;
     uint32_t wait_limit, drain_limit, extra_tx;
 };
@@ -188,6 +189,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
     const tc::Waits wait{&dead, a.status, a.wait_limit};
     // (A last stage that K does not fill gets zeros.)
     const int ksteps = ((a.n_in + kGemmK - 1) / kGemmK + a.subs - 1) / a.subs * a.subs;
+    // Its steps of K: all, or this CTA's part of a cluster's (in units of the scales' four).
+    const int units = (ksteps + kScaleSteps - 1) / kScaleSteps, rank = a.parts > 1 ? int(blockIdx.x) % a.parts : 0;
+    const int kb = units * rank / a.parts * kScaleSteps, ke = min(ksteps, units * (rank + 1) / a.parts * kScaleSteps);
+    const int tile0 = int(blockIdx.x) / a.parts, tile_step = int(gridDim.x) / a.parts;
 
     if (tid == 0) {
         dead = 0;
@@ -223,11 +228,11 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
         const int half = warp >> 2, split = (a.bn / 2 + 15) / 16 * 16;       // its part of the columns
         const int from = half * split, hc = half ? a.bn - split : split;
         const uint32_t lanes = uint32_t(warp & 3) << 21;             // 32 (warp % 4) in the address's high half
-        const int chunks = F32 ? (ksteps + kChunkSteps - 1) / kChunkSteps : 1;
+        const int chunks = F32 ? (ke - kb + kChunkSteps - 1) / kChunkSteps : 1;
         const int tiles = gemm_tiles(a);
         uint32_t it = 0;
         bool alive = true;
-        for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+        for (int t = tile0; t < tiles && alive; t += tile_step) {
             const GemmTile g = gemm_tile(a, t);
             const int row = g.row0 + (warp & 3) * 32 + lane;
             const bool there = row < a.n_out;
@@ -238,8 +243,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             uint32_t v[16];
             // 16 columns of this lane's row: one pass per part of the epilogue that the call has, so that
             // none of them asks again for every column.
-            auto put = [&](int u, float* x) {
-                const int c0 = from + u * 16, n = min(16, g.cols - c0);
+            auto put = [&](int c0, float* x) {
+                const int n = min(16, g.cols - c0);
                 if (n <= 0) return;
                 if (a.xscale) {
                     const float mine = (lane & 15) < n ? a.xscale[g.slot0 + c0 + (lane & 15)] : 1.0f;
@@ -280,6 +285,12 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                         if (c < n) *to = Out(x[c]);
                 }
             };
+            // The CTA's part of the sums, in the operands' memory (all products are done): [column][row].
+            auto stash = [&](int c0, const float* x) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    asm volatile("st.shared.f32 [%0], %1;" :: "r"(base + uint32_t(((c0 + c) * kGemmRows + (warp & 3) * 32 + lane) * 4)), "f"(x[c]) : "memory");
+            };
             for (int ch = 0; ch < chunks; ++ch, ++it) {
                 const int b = int(it & 1);
                 if (!wait(acc_full(b), (it >> 1) & 1)) { alive = false; break; }
@@ -313,7 +324,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                             __syncwarp();
                             if (lane == 0) mbar_arrive(acc_empty(b));
                         }
-                        put(u, x);
+                        if (a.parts == 1) put(from + u * 16, x); else stash(from + u * 16, x);
                     }
                 }
             }
@@ -321,8 +332,27 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                 if (alive) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        if (u * 16 < hc) put(u, sum + u * 16);
+                        if (u * 16 < hc) {
+                            if (a.parts == 1) put(from + u * 16, sum + u * 16); else stash(from + u * 16, sum + u * 16);
+                        }
                 }
+            }
+            if (a.parts > 1) {                           // (one tile)
+                tc::cluster_sync();
+                // Every CTA of the cluster joins and writes some of the tile's columns; the parts are
+                // added in the order of K.
+                if (alive)
+                    for (int c0 = (rank + (warp >> 2) * a.parts) * 16; c0 < a.bn; c0 += 2 * a.parts * 16) {
+                        float x[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) x[c] = 0.0f;
+                        for (int p = 0; p < a.parts; ++p) {
+                            const uint32_t at = tc::of_cluster(base + uint32_t((c0 * kGemmRows + (warp & 3) * 32 + lane) * 4), p);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) x[c] += tc::load_cluster(at + uint32_t(c * kGemmRows * 4));
+                        }
+                        put(c0, x);
+                    }
             }
         }
     } else if (warp < kDrainWarps + kDecodeWarps) {
@@ -336,8 +366,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             int s = 0, sub = 0, r = 0, sr = 0;
             uint32_t phase = 0, raw_phase = 0, n = 0, groups = 0;
             bool alive = true;
-            for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
-                for (int k = 0; k < ksteps; ++k, ++n) {
+            for (int t = tile0; t < tiles && alive; t += tile_step) {
+                for (int k = kb; k < ke; ++k, ++n) {
                     if (k % kScaleSteps == 0) {          // the next four steps' scales
                         if (groups && lane == 0) mbar_arrive(sc_empty(sr));
                         sr = int(groups % kScaleSlots);
@@ -347,10 +377,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                     if (n % uint32_t(kGroups > 0 ? kGroups : 1) == uint32_t(which)) {
                         if (!wait(raw_full(r), raw_phase)) { alive = false; break; }
                         uint32_t code[2][CB / 8];
-                        const uint32_t at = raw0 + uint32_t(r) * (kGemmRows * CB) + uint32_t(row) * CB;
+                        const uint32_t at = raw0 + uint32_t(r) * (kGemmRows * CB) + uint32_t(row) * CB + uint32_t(CB == 64 ? (row >> 1) & 3 : (row >> 2) & 1) * 16;
 #pragma unroll
                         for (int c = 0; c < CB / 16; ++c) {          // the copy's swizzle: no two lanes of a phase in a bank
-                            const uint4 q = tc::lds128(at + uint32_t(c ^ (CB == 64 ? (row >> 1) & 3 : (row >> 2) & 1)) * 16);
+                            const uint4 q = tc::lds128(at ^ uint32_t(c * 16));
                             uint32_t* const to = &code[c * 16 / (CB / 2)][c * 4 % (CB / 8)];
                             to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
                         }
@@ -365,7 +395,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                             half[0] = w0 & 0xFFFFu, half[1] = w0 >> 16;
                         }
                         const int left = a.n_in - k * kGemmK;                    // weights from here to the row's end
-                        const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(sub) * sub_bytes + uint32_t(row) * 128;
+                        const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(sub) * sub_bytes + uint32_t(row) * 128 + uint32_t(row & 7) * 16;
                         bool ready = false;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -389,7 +419,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                             ready = true;
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                const uint32_t p = to + uint32_t(((4 * h + c) ^ (row & 7)) * 16);
+                                const uint32_t p = to ^ uint32_t((4 * h + c) * 16);
                                 sts128(p, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
                                 if constexpr (F32) sts128(p + kOperandA, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
                             }
@@ -420,9 +450,9 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             int s = 0;
             uint32_t phase = 0, filled = 0;
             bool alive = true;
-            for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+            for (int t = tile0; t < tiles && alive; t += tile_step) {
                 const GemmTile g = gemm_tile(a, t);
-                for (int k = 0; k < ksteps; k += a.subs) {
+                for (int k = kb; k < ke; k += a.subs) {
                     if (!wait(empty(s), phase ^ 1)) { alive = false; break; }
                     uint32_t at = base + uint32_t(s) * stage_bytes;
                     if (tc::elect()) {
@@ -460,9 +490,9 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                 int r = 0;
                 uint32_t phase = 0, filled = 0, groups = 0;
                 bool alive = true;
-                for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
+                for (int t = tile0; t < tiles && alive; t += tile_step) {
                     const GemmTile g = gemm_tile(a, t);
-                    for (int k = 0; k < ksteps; ++k) {
+                    for (int k = kb; k < ke; ++k) {
                         if (!wait(raw_empty(r), phase ^ 1)) { alive = false; break; }
                         const int step = k / kSteps, in = k % kSteps;
                         if (k % kScaleSteps == 0) {
@@ -508,10 +538,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             int s = 0;
             uint32_t phase = 0, it = 0;
             bool alive = true;
-            for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
-                for (int k = 0; k < ksteps; k += a.subs) {
-                    const bool first = F32 ? k % kChunkSteps == 0 : k == 0;
-                    const bool lastk = k + a.subs == ksteps || (F32 && (k + a.subs) % kChunkSteps == 0);
+            for (int t = tile0; t < tiles && alive; t += tile_step) {
+                for (int k = kb; k < ke; k += a.subs) {
+                    const bool first = F32 ? k % kChunkSteps == 0 : k == kb;
+                    const bool lastk = k + a.subs == ke || (F32 && (k + a.subs) % kChunkSteps == 0);
                     const int b = int(it & 1);
                     if (first && !wait(acc_empty(b), ((it >> 1) & 1) ^ 1)) { alive = false; break; }
                     if (!wait(full(s), phase)) { alive = false; break; }
@@ -546,6 +576,10 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             __syncwarp();
             mbar_wait(drained, 0, a.drain_limit);
         }
+    }
+    if (a.parts > 1) {
+        if (warp >= kDrainWarps) tc::cluster_sync();         // the drain warps' first (each of them has had its tile)
+        tc::cluster_sync();                                  // no CTA ends while another reads its sums
     }
     __syncwarp();
     tc::fence_before();

@@ -53,7 +53,7 @@ uint32_t wait_limit();
 qg_status launch_early(const void* fn, int grid, int threads, size_t smem, int cluster, void** params, void* stream);
 // The second launch of a call: with `early` it may start while the call's first kernel, which the
 // library has launched just before on the stream, still runs (and waits for it where it needs it).
-qg_status launch_after(const void* fn, int grid, int threads, size_t smem, bool early, void** params, void* stream);
+qg_status launch_after(const void* fn, int grid, int threads, size_t smem, int cluster, bool early, void** params, void* stream);
 uint32_t test_extra_tx();
 
 }  // namespace qg
