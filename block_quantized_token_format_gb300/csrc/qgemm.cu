@@ -281,25 +281,33 @@ Geometry geometry(int fmt, bool f32, int bn, int optin) {
     Geometry g{};
     g.subs = !f32 && bn <= 128 ? 2 : 1;
     const size_t stage = size_t(g.subs) * (size_t(terms_w(fmt, f32)) * kOperandA + size_t(terms_x(fmt, f32)) * size_t(bn) * kGemmK * 2);
+    auto slots = [&](int stages) { return int(std::min<size_t>(kMostRaws, (room - size_t(stages) * stage) / std::max<size_t>(raw, 1))) / std::max(groups, 1) * groups; };
     g.stages = int(std::min<size_t>(quant ? (g.subs == 2 ? 3 : 4) : 8, (room - size_t(groups) * raw) / stage));
-    g.raws = quant ? int(std::min<size_t>(kMostRaws, (room - size_t(g.stages) * stage) / raw)) / groups * groups : 0;
+    if (quant && g.subs == 2 && g.stages == 3 && slots(3) < 8) g.stages = 2;
+    g.raws = quant ? slots(g.stages) : 0;
     g.smem = 1024 + scales + size_t(g.raws) * raw + size_t(g.stages) * stage;
     return g;
 }
 
 // The tile's tokens, and the CTAs that share its K.  Measured on GB300 (128 rows, 64 of K, all SMs): a
-// step takes 265 to 330 ns whatever the tokens, until 1.85 ns a token are more (240: 440 ns); with bf16
-// weights 160 ns or 1.55 a token; in fp32 330 ns and 3.2 a token (bf16 weights 300 and 2.75).  Tiles run
-// on all SMs in rounds, each with about 1.5 us of its own; a cluster's join takes 2.5 us.
+// step takes 270 ns with three stages and 310 with two whatever the tokens, until 1.85 ns a token are
+// more (240: 440 ns); with bf16 weights 160 ns or 1.55 a token; in fp32 330 ns and 3.2 a token (bf16
+// weights 300 and 2.75).  Tiles run on all SMs in rounds, each with about 1.5 us of its own; a cluster's
+// join takes 2.5 us.
 struct Shape { int bn, parts; };
 template <typename Clusters>
-Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms, Clusters clusters) {
+Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms, int optin, Clusters clusters) {
     Shape best{32, 1};
     double least = 0;
     const double ksteps = double((n_in + kGemmK - 1) / kGemmK);
+    // Experts' rows: spread like independent choices, and by half their mean for the experts' popularity
+    // (of 20,480 rows and 512 experts in tiles of 64 that makes 577 tiles; a routing had 568).
+    const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
     for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
         const bool quant = fmt != QG_BF16;
-        const double step = f32 ? (quant ? 330.0 + 3.2 * bn : 300.0 + 2.75 * bn) : quant ? std::max(290.0, 1.85 * bn) : std::max(160.0, 1.55 * bn);
+        const Geometry g = geometry(fmt, f32, bn, optin);
+        const double step = f32 ? (quant ? 330.0 + 3.2 * bn : 300.0 + 2.75 * bn)
+                            : quant ? std::max(g.subs == 2 && g.stages >= 3 ? 270.0 : 310.0, 1.85 * bn) : std::max(160.0, 1.55 * bn);
         for (int parts = 1; parts <= 8; parts *= 2) {
             double rounds;
             if (n_experts == 0) {
@@ -307,10 +315,11 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
                 if (parts > 1 && (tiles * parts > sms || ksteps < 8 * parts || clusters(parts) < tiles)) break;
                 rounds = double((tiles + sms - 1) / sms);
             } else {
-                // Experts' rows spread around the mean: on average half a tile more than they fill.
                 if (parts > 1) break;
-                const double used = double(std::min(n_experts, n_slots));
-                rounds = std::max(1.0, double(m_tiles) * std::max(used, double(n_slots) / bn + 0.5 * used) / sms);
+                double per_expert = 1.0 - std::exp(-mean);               // the mean of a count's tiles
+                for (int j = 1; j * bn < mean + 4.0 * spread && j < 1000; ++j)
+                    per_expert += 0.5 * std::erfc((j * bn - mean) / (spread * 1.41421356));
+                rounds = std::max(1.0, double(m_tiles) * double(n_experts) * per_expert / sms);
             }
             const double cost = rounds * (ksteps / parts * step + 1500.0) + (parts > 1 ? 2500.0 : 0.0);
             if (least == 0 || cost < least) {
@@ -360,7 +369,7 @@ qg_status launch_gemm(const GemmCall& c) {
     const int64_t m_tiles = (c.n_out + kGemmRows - 1) / kGemmRows;
     const void* const fn = qgemm_lookup(c.fmt, f32);
     const int threads = gemm_threads(c.fmt, f32);
-    const Shape shape = tile_shape(c.fmt, f32, c.n_in, m_tiles, c.n_slots, c.n_experts, sms, [&](int parts) {
+    const Shape shape = tile_shape(c.fmt, f32, c.n_in, m_tiles, c.n_slots, c.n_experts, sms, optin, [&](int parts) {
         const size_t smem = geometry(c.fmt, f32, 32, optin).smem;
         return blocks_per_sm(fn, dev, optin, threads, smem) < 1 ? 0 : clusters_at_once(fn, dev, threads, smem, parts);
     });
