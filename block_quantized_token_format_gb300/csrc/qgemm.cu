@@ -114,8 +114,8 @@ template <typename T, int FMT, int PER> __global__ void __launch_bounds__(kStage
     }
     const int tid = int(threadIdx.x), sub = tid % PER;
     const long long slot = (long long)blockIdx.x * (kStageThreads / PER) + tid / PER;
-    const int used = a.n_experts ? max(0, min(a.offsets[a.n_experts], a.n_slots)) : a.n_slots;
-    if (slot >= used) return;                            // (PER = 256: the whole block)
+    const int unused = a.n_experts ? a.offsets[0] : 0, used = a.n_experts ? min(a.offsets[a.n_experts], a.n_slots) : a.n_slots;
+    if (slot < unused || slot >= used) return;           // of no expert (PER = 256: the whole block)
     long long at = a.rows ? (long long)a.rows[slot] : slot;
     const bool bad = at < 0 || at >= a.n_x;
     if (bad) {

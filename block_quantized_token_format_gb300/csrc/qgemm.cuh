@@ -14,7 +14,7 @@
 //
 // Numbers.  Quantized formats enter as fp16: a code times its fp16 scale has at most 19 bits.
 // bf16 activations, which a row's power of two moves into fp16's range exactly (but for values
-// 2^-29 and more below the row's largest), meet weights rounded to 11 bits: 2^-12 of a weight,
+// 2^-29 and more below the row's largest), meet weights rounded to 11 bits: 2^-11 of a weight at most,
 // an eighth of what rounding the output to bf16 costs.  fp32 activations are two fp16 terms (22
 // bits), weights two (exact), in three products; the two small ones have accumulators of their
 // own, and every 256 values of K the sums move to fp32 registers: the tensor cores truncate what

@@ -10,8 +10,8 @@ A batch of sequences runs through the calls a serving program makes per step:
     qg_attention       the new tokens over the cache
     qgemv              output projection, 6144 -> 2560
 
-The prompt goes in 4 tokens at a time (the mat-vec's largest step); weights and inputs are random.
-The decode step is captured once as a CUDA graph and replayed: nothing in it reads back to the
+The prompts go in whole, with qgemm for qgemv and qg_prompt_attention over the keys and values as the
+cache has stored them; weights and inputs are random.  The decode step is captured once as a CUDA graph and replayed: nothing in it reads back to the
 host, and the lengths live on the device.
 """
 from __future__ import annotations
@@ -63,6 +63,25 @@ class AttentionLayer:
         return y
 
 
+    def prompt(self, x, step):
+        """The same for whole prompts, packed: x fp32 ``[n_tok, 2560]``; the cache holds nothing of them before."""
+        n = x.shape[0]
+        work = max(qg.qgemm_workspace_bytes("q8_0", "f32", QKV, D_MODEL, n), qg.qgemm_workspace_bytes("q8_0", "f32", D_MODEL, HEADS * DIM, n),
+                   qg.qg_prompt_attention_workspace_bytes("f32", n, HEADS, KV, DIM))
+        work = torch.empty(work, dtype=torch.uint8, device="cuda")               # one after the other: one workspace
+        qkv = torch.empty(n, HEADS + 2 * KV, DIM, device="cuda")
+        qg.qgemm("q8_0", self.w_qkv, QKV, D_MODEL, x, qkv.view(n, QKV), work)
+        q, k, v = qkv[:, :HEADS], qkv[:, HEADS:HEADS + KV], qkv[:, HEADS + KV:]
+        k_back, v_back = [torch.empty(n, KV, DIM, device="cuda") for _ in range(2)]
+        qg.qg_cache_append(self.cache, k, v, step.slots, q=q, q_out=q, positions=step.positions, cos_sin=self.cos_sin,
+                           q_weight=self.q_weight, k_weight=self.k_weight, k_back=k_back, v_back=v_back)
+        out = torch.empty(n, HEADS, DIM, device="cuda")
+        qg.qg_prompt_attention(q, k_back, v_back, step.cu_new, out, work, DIM ** -0.5, longest=step.max_new)
+        y = torch.empty_like(x)
+        qg.qgemm("q8_0", self.w_out, D_MODEL, HEADS * DIM, out.view(n, HEADS * DIM), y, work)
+        return y
+
+
 class Step:
     """Device state of a batch: lengths, block table, free pages, and the current step's tokens."""
 
@@ -91,12 +110,11 @@ class Step:
 def main(prompt: int = 40, decode: int = 8) -> dict:
     torch.manual_seed(0)
     n_pages = 64
-    layer, step = AttentionLayer(1, n_pages), Step(2, n_pages, 16, [2, 2])
-    # Prompt: two sequences, two tokens each per step.
-    for _ in range(prompt // 2):
-        step.begin_step()
-        layer(torch.randn(4, D_MODEL, device="cuda"), step)
-        step.end_step()
+    layer, step = AttentionLayer(1, n_pages), Step(2, n_pages, 16, [prompt, prompt])
+    # Prompt: two sequences in one pass.
+    step.begin_step()
+    prompts = layer.prompt(torch.randn(2 * prompt, D_MODEL, device="cuda"), step)
+    step.end_step()
     # Decode: one token each, as one graph.
     step.set_fresh([1, 1])
     x = torch.randn(2, D_MODEL, device="cuda")
@@ -120,7 +138,7 @@ def main(prompt: int = 40, decode: int = 8) -> dict:
     step.end_step()
     torch.cuda.synchronize()
     assert qg.qg_device_status() == 0
-    return {"lengths": step.seq_len.tolist(), "pages": int(step.begin), "decode": y, "verify": z}
+    return {"lengths": step.seq_len.tolist(), "pages": int(step.begin), "prompt": prompts, "decode": y, "verify": z}
 
 
 if __name__ == "__main__":

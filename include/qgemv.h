@@ -504,10 +504,11 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
  *                aligned; it need not be cleared.  Calls that share one must be serialized.
  * Sums are fp32.  fp32 activations enter as two 16-bit terms each of x and W (22 bits of x below
  * the row's largest value, all bits of W; bf16 weights: all 24 bits of x); bf16 ones as they are,
- * weights of the quantized formats then rounded to 11 bits (2^-12 of each).  Quantized weights of
- * magnitude 65520 and more count as infinite; values of x below 2^-39 of their row's largest as zero.
+ * weights of the quantized formats then rounded to 11 bits (2^-11 of each at most).  Quantized weights
+ * of magnitude 65520 and more count as infinite; values of x below 2^-39 of their row's largest as zero.
  * Inputs that are not finite make the outputs they enter not finite.  A token's outputs do not depend
- * on the other tokens' values; the order of a sum depends on n_in alone.
+ * on the other tokens' values; the order of a sum depends on the call's sizes and the GPU's number of SMs; outputs are the same on
+ * every run.
  * n_out, n_in as in qgemv (n_in has no upper limit but 2^24); ntok >= 0, below 2^31 - 1024.
  * Errors: QG_EINVAL (format, type, shape, null pointer, odd n_out with swiglu, y = x), QG_EALIGN,
  * QG_EWORKSPACE, QG_EUNSUPPORTED (2^31 tiles of 128 rows and 32 tokens or more), QG_ECUDA.
@@ -543,12 +544,16 @@ qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_
  *                out does not overlap q, k or v.
  *   cu_seq       device int32 [n_seq + 1], as qg_cache_pages leaves cu_new where nothing was held.
  *                Tokens outside cu_seq[0] .. cu_seq[n_seq] are neither read nor written.  Entries that
- *                shrink or leave 0..n_tok set QG_DEVICE_BAD_LENGTH and nothing is written.
- *   longest      a prompt's most tokens (at least 1): chooses the launch; results are right for any value.
+ *                shrink or leave 0..n_tok set QG_DEVICE_BAD_LENGTH; out and lse are then not valid.
+ *   longest      a prompt's most tokens (at least 1): a hint; results are right for any value.
  *   lse          device fp32 [n_tok][n_heads] (natural logarithm), or NULL.
  *   workspace    device, >= qg_prompt_attention_workspace_bytes(act, n_tok, n_heads, n_kv_heads, head_dim)
  *                bytes, 16-byte aligned; it need not be cleared.  Calls that share one must be serialized.
  *   n_seq <= 16384; n_heads a multiple of n_kv_heads, at most 128 to one key/value head.
+ * bf16: products are exact, sums fp32, probabilities rounded to bf16 (their sum and lse are not).  fp32:
+ * queries, keys and values as two fp16 terms, 22 bits below the largest of the query, and of the head's keys or
+ * values in a tile of 64 tokens; probabilities as two terms, down to 2^-31 of the row's largest.  Outputs are
+ * the same on every run, and do not depend on the other prompts of the call.
  * A masked key or value (of a later token, beyond the window, of another prompt) has no effect whatever
  * it holds; a visible one that is not finite makes the outputs that see it not finite.
  * Errors: QG_EINVAL, QG_EALIGN, QG_EWORKSPACE, QG_EUNSUPPORTED, QG_ECUDA. */
