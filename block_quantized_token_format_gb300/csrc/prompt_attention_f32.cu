@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kStageThreads = 256;
 constexpr float kSlack = 8.0f, kLift = 7.0f;     // log2: P is 2^7 times the exponential, at most 2^15
-constexpr int kTileKeys = 64;
+constexpr int kTileKeys = 64, kStageRows = 4;
 
 template <int D> struct Shape {
     static constexpr int KT = kTileKeys, DV = D < 128 ? D : 128, HALVES = D / DV, STAGES = D == 256 ? 1 : 2;
@@ -65,35 +65,45 @@ template <int D> __global__ void __launch_bounds__(kStageThreads) stage_kernel(c
     tc::grid_launch_dependents();
     tc::grid_wait();
     const int tid = int(threadIdx.x), lane = tid & 31;
-    if (blockIdx.x >= a.tile_blocks) {                   // queries, a warp a row
-        const long long row = (long long)(blockIdx.x - a.tile_blocks) * (kStageThreads / 32) + (tid >> 5);
-        if (row >= (long long)a.n_tok * a.n_heads) return;
-        const long long tok = row / a.n_heads;
-        if (tok < a.cu_seq[0] || tok >= a.cu_seq[a.n_seq]) return;
-        const float* const src = a.q + tok * a.q_stride + (row - tok * a.n_heads) * D;
+    if (blockIdx.x >= a.tile_blocks) {                   // queries, a warp four rows at a time
+        const long long row0 = ((long long)(blockIdx.x - a.tile_blocks) * (kStageThreads / 32) + (tid >> 5)) * kStageRows;
+        const long long from = (long long)a.cu_seq[0] * a.n_heads, to = min((long long)a.cu_seq[a.n_seq], (long long)a.n_tok) * a.n_heads;
         constexpr int N = (D + 127) / 128;
-        float4 x[N];
-        uint32_t top = 0;
+        float4 x[kStageRows][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = (i * 32 + lane) * 4;
-            x[i] = at < D ? *reinterpret_cast<const float4*>(src + at) : make_float4(0, 0, 0, 0);
-            top = max(max(max(top, finite_bits(x[i].x)), finite_bits(x[i].y)), max(finite_bits(x[i].z), finite_bits(x[i].w)));
+        for (int k = 0; k < kStageRows; ++k) {
+            const long long row = row0 + k;
+            const long long tok = row / a.n_heads;
+            const float* const src = a.q + tok * a.q_stride + (row - tok * a.n_heads) * D;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = (i * 32 + lane) * 4;
+                x[k][i] = at < D && row >= from && row < to && row >= 0 ? *reinterpret_cast<const float4*>(src + at) : make_float4(0, 0, 0, 0);
+            }
         }
-        top = __reduce_max_sync(tc::kFullMask, top);
-        float inverse;
-        const float lift = lift_of(top, inverse);
-        if (lane == 0) a.qscale[row] = inverse;
-        uint16_t* const to = a.q_out + row * D;
-        const size_t term = size_t(a.n_tok) * a.n_heads * D;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = (i * 32 + lane) * 4;
-            if (at >= D) break;
-            uint2 hi, lo;
-            terms4(x[i], lift, hi, lo);
-            *reinterpret_cast<uint2*>(to + at) = hi;
-            *reinterpret_cast<uint2*>(to + term + at) = lo;
+        for (int k = 0; k < kStageRows; ++k) {
+            const long long row = row0 + k;
+            if (row < from || row >= to || row < 0) continue;
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                top = max(max(max(top, finite_bits(x[k][i].x)), finite_bits(x[k][i].y)), max(finite_bits(x[k][i].z), finite_bits(x[k][i].w)));
+            top = __reduce_max_sync(tc::kFullMask, top);
+            float inverse;
+            const float lift = lift_of(top, inverse);
+            if (lane == 0) a.qscale[row] = inverse;
+            uint16_t* const out = a.q_out + row * D;
+            const size_t term = size_t(a.n_tok) * a.n_heads * D;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = (i * 32 + lane) * 4;
+                if (at >= D) break;
+                uint2 hi, lo;
+                terms4(x[k][i], lift, hi, lo);
+                *reinterpret_cast<uint2*>(out + at) = hi;
+                *reinterpret_cast<uint2*>(out + term + at) = lo;
+            }
         }
         return;
     }
@@ -451,7 +461,7 @@ qg_status prompt_stage(int D, const PromptStage& p, void* stream) {
     a.qscale = p.qscale, a.kscale = p.kscale, a.vscale = p.vscale;
     a.n_tok = p.n_tok, a.n_seq = p.n_seq, a.n_heads = p.n_heads, a.n_kv = p.n_kv;
     const int64_t tiles = 2 * (int64_t(p.n_tok) / kTileKeys + p.n_seq) * p.n_kv;
-    const int64_t rows = (int64_t(p.n_tok) * p.n_heads + kStageThreads / 32 - 1) / (kStageThreads / 32);
+    const int64_t per = kStageThreads / 32 * kStageRows, rows = (int64_t(p.n_tok) * p.n_heads + per - 1) / per;
     if (tiles + rows > (int64_t(1) << 31) - 1) return QG_EUNSUPPORTED;
     a.tile_blocks = uint32_t(tiles);
     void* params[] = {&a};
