@@ -280,10 +280,10 @@ Geometry geometry(int fmt, bool f32, int bn, int optin) {
     const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
     Geometry g{};
     g.subs = !f32 && bn <= 128 ? 2 : 1;
-    const size_t stage = size_t(g.subs) * (size_t(terms_w(fmt, f32)) * kOperandA + size_t(terms_x(fmt, f32)) * size_t(bn) * kGemmK * 2);
+    const size_t stage = size_t(g.subs) * ((quant ? 0 : size_t(kOperandA)) + size_t(terms_x(fmt, f32)) * size_t(bn) * kGemmK * 2);
     auto slots = [&](int stages) { return int(std::min<size_t>(kMostRaws, (room - size_t(stages) * stage) / std::max<size_t>(raw, 1))) / std::max(groups, 1) * groups; };
     g.stages = int(std::min<size_t>(quant ? (g.subs == 2 ? 3 : 4) : 8, (room - size_t(groups) * raw) / stage));
-    if (quant && g.subs == 2 && g.stages == 3 && slots(3) < 8) g.stages = 2;
+    if (quant) g.stages = std::min(g.stages, (512 - 2 * bn * (f32 ? 2 : 1)) / (g.subs * w_columns(fmt, f32)));
     g.raws = quant ? slots(g.stages) : 0;
     g.smem = 1024 + scales + size_t(g.raws) * raw + size_t(g.stages) * stage;
     return g;

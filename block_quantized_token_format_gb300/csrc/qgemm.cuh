@@ -6,7 +6,10 @@
 // accumulators' lanes) and tokens as N, in steps of 64 along K:
 //   * one thread copies, with tensor copies, W's raw codes (each step) and scales (every fourth)
 //     into one ring and the tokens' operand (staged by stage_kernel, qgemm.cu) into another;
-//   * groups of four warps turn the codes into 16-bit floats, a lane a row, a group a step;
+//   * groups of four warps turn the codes into 16-bit floats, a lane a row, a group a step, and put
+//     them into tensor memory, from where the products take them: through shared memory a step's
+//     operand would be written and, for every 16 of K, read there, which bounded the kernel (32
+//     tokens: 58 of its 90 KB a step; 270 ns against XXX);
 //   * one thread issues the products;
 //   * eight warps empty the accumulators, of which there are two sets, so that a tile's epilogue
 //     runs beside the next one's products.
@@ -50,10 +53,11 @@ constexpr int kOperandA = kGemmRows * kGemmK * 2;
 constexpr int kScaleSteps = 4, kScaleSlots = 4;
 __host__ __device__ constexpr int raw_codes(int fmt) { return fmt == QG_Q8_0 ? 64 : fmt == QG_BF16 ? 0 : 32; }
 __host__ __device__ constexpr int raw_scales(int fmt) { return fmt == QG_BF16 ? 0 : fmt == QG_Q5_0 ? 48 : 16; }
-__host__ __device__ constexpr int terms_w(int fmt, bool f32) { return f32 && fmt != QG_BF16 ? 2 : 1; }
 __host__ __device__ constexpr int terms_x(int fmt, bool f32) { return !f32 ? 1 : fmt == QG_BF16 ? 3 : 2; }
-// Tokens of the largest tile: 240 leave room for four stages and four raw steps of any format.
-__host__ __device__ constexpr int gemm_most_tokens(int fmt, bool f32) { return f32 ? 128 : fmt == QG_BF16 ? 256 : 240; }
+// Tokens of the largest tile: two sets of sums and the stages of W's operand share tensor memory's
+// 512 columns.
+__host__ __device__ constexpr int gemm_most_tokens(int fmt, bool f32) { return fmt == QG_BF16 ? (f32 ? 128 : 256) : f32 ? 96 : 192; }
+__host__ __device__ constexpr int w_columns(int fmt, bool f32) { return fmt == QG_BF16 ? 0 : f32 ? 64 : 32; }      // of a step
 
 struct GemmArgs {
     CUtensorMap xmap, wmap, smap;  // staged tokens [terms][n_slots][n_in]; rows of W: codes (or bf16), scales
@@ -154,16 +158,12 @@ __device__ __forceinline__ void decode32(const uint32_t* code, uint32_t fifth, _
     }
 }
 
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
 // ------------------------------------------------------------------------------ the kernel
 
 template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT, F32), 1) qgemm_kernel(const __grid_constant__ GemmArgs a) {
     constexpr bool kQuant = FMT != QG_BF16;
     constexpr int kGroups = decode_groups(FMT, F32), kDecodeWarps = 4 * kGroups;
-    constexpr int TW = terms_w(FMT, F32), TX = terms_x(FMT, F32);
+    constexpr int TX = terms_x(FMT, F32);
     constexpr int kStepWeights = FMT == QG_Q8_0 ? 512 : 1024;        // of a layout step
     using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
     extern __shared__ uint8_t smem_raw[];
@@ -172,7 +172,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
 
     const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t b_bytes = uint32_t(a.bn) * kGemmK * 2, sub_bytes = TW * kOperandA + TX * b_bytes, stage_bytes = uint32_t(a.subs) * sub_bytes;
+    constexpr uint32_t a_bytes = kQuant ? 0 : kOperandA;             // (quantized weights' operand is in tensor memory)
+    const uint32_t b_bytes = uint32_t(a.bn) * kGemmK * 2, sub_bytes = a_bytes + TX * b_bytes, stage_bytes = uint32_t(a.subs) * sub_bytes;
     const uint32_t raw0 = base + uint32_t(a.stages) * stage_bytes;
     const uint32_t bars = smem_addr(bar_mem);
     auto full = [&](int s) { return bars + 8u * uint32_t(s); };
@@ -185,7 +186,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
     auto sc_full = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + r); };
     auto sc_empty = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + kScaleSlots + r); };
     const uint32_t acc_cols = uint32_t(a.bn) * (F32 ? 2 : 1);                    // of one set
-    const uint32_t tmem_cols = 2 * acc_cols <= 64 ? 64 : 2 * acc_cols <= 128 ? 128 : 2 * acc_cols <= 256 ? 256 : 512;
+    const uint32_t tmem_cols = kQuant ? 512 : 2 * acc_cols <= 64 ? 64 : 2 * acc_cols <= 128 ? 128 : 2 * acc_cols <= 256 ? 256 : 512;
     const tc::Waits wait{&dead, a.status, a.wait_limit};
     // (A last stage that K does not fill gets zeros.)
     const int ksteps = ((a.n_in + kGemmK - 1) / kGemmK + a.subs - 1) / a.subs * a.subs;
@@ -239,7 +240,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             const float bias = a.bias && there ? a.bias[row] : 0.0f;
             const int col = a.f == kFSwiglu ? row >> 1 : row;
             const bool writes = there && (a.f != kFSwiglu || (lane & 1) == 0);
-            float sum[F32 ? 64 : 1];
+            constexpr int kSums = !F32 ? 1 : gemm_most_tokens(FMT, true) / 32;   // fp32: sets of 16 sums of a lane
+            float sum[F32 ? 16 * kSums : 1];
             uint32_t v[16];
             // 16 columns of this lane's row: one pass per part of the epilogue that the call has, so that
             // none of them asks again for every column.
@@ -298,7 +300,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                 const uint32_t acc = tmem + lanes + uint32_t(b) * acc_cols + uint32_t(from);
                 if constexpr (F32) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < kSums; ++u)
                         if (u * 16 < hc) {
                             tc::tmem_load16(acc + uint32_t(a.bn) + u * 16, v);
                             tc::tmem_load_wait16(v);
@@ -331,7 +333,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             if constexpr (F32) {
                 if (alive) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < kSums; ++u)
                         if (u * 16 < hc) {
                             if (a.parts == 1) put(from + u * 16, sum + u * 16); else stash(from + u * 16, sum + u * 16);
                         }
@@ -395,7 +397,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                             half[0] = w0 & 0xFFFFu, half[1] = w0 >> 16;
                         }
                         const int left = a.n_in - k * kGemmK;                    // weights from here to the row's end
-                        const uint32_t to = base + uint32_t(s) * stage_bytes + uint32_t(sub) * sub_bytes + uint32_t(row) * 128 + uint32_t(row & 7) * 16;
+                        const uint32_t to = tmem + (uint32_t(w & 3) << 21) + 2 * acc_cols + uint32_t((s * a.subs + sub) * w_columns(FMT, F32));
                         bool ready = false;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -415,17 +417,17 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                             // (Two phases ahead a wait would pass too soon.  The group's last step was in a stage
                             // filled since this one's last but one filling: there are at least as many stages
                             // as groups, or half as many of two steps.)
-                            if (h == 0 && !wait(empty(s), phase ^ 1)) { alive = false; break; }
-                            ready = true;
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t p = to ^ uint32_t((4 * h + c) * 16);
-                                sts128(p, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                                if constexpr (F32) sts128(p + kOperandA, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                            if (h == 0) {
+                                if (!wait(empty(s), phase ^ 1)) { alive = false; break; }
+                                tc::fence_after();
                             }
+                            ready = true;
+                            tc::tmem_store16(to + uint32_t(16 * h), hi);
+                            if constexpr (F32) tc::tmem_store16(to + uint32_t(32 + 16 * h), lo);
                         }
                         if (!ready) break;
-                        tc::fence_async();
+                        tc::tmem_store_wait();
+                        tc::fence_before();
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(full(s));
@@ -445,7 +447,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
         {
             tc::grid_wait();
             const int tiles = gemm_tiles(a);
-            const uint32_t bytes = TX * b_bytes + (kQuant ? 0 : kOperandA);
+            const uint32_t bytes = TX * b_bytes + a_bytes;
             uint32_t extra = a.extra_tx;
             int s = 0;
             uint32_t phase = 0, filled = 0;
@@ -460,7 +462,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                         for (int u = 0; u < a.subs; ++u, at += sub_bytes) {
                             if constexpr (!kQuant) tc::load_2d(at, &a.wmap, (k + u) * kGemmK, g.w_row0, full(s));
 #pragma unroll
-                            for (int x = 0; x < TX; ++x) tc::load_3d(at + TW * kOperandA + x * b_bytes, &a.xmap, (k + u) * kGemmK, g.slot0, x, full(s));
+                            for (int x = 0; x < TX; ++x) tc::load_3d(at + a_bytes + x * b_bytes, &a.xmap, (k + u) * kGemmK, g.slot0, x, full(s));
                         }
                     }
                     __syncwarp();
@@ -549,17 +551,20 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                     const uint32_t acc = tmem + uint32_t(b) * acc_cols;
                     uint32_t at = base + uint32_t(s) * stage_bytes;
                     if (tc::elect()) {
-                        for (int u = 0; u < a.subs; ++u, at += sub_bytes) {
-                            const uint64_t da = tc::desc_k(at), db = tc::desc_k(at + TW * kOperandA);
+                        uint32_t wt = tmem + 2 * acc_cols + uint32_t(s * a.subs * w_columns(FMT, F32));
+                        for (int u = 0; u < a.subs; ++u, at += sub_bytes, wt += w_columns(FMT, F32)) {
+                            const uint64_t da = tc::desc_k(at), db = tc::desc_k(at + a_bytes);
 #pragma unroll
                             for (int j = 0; j < kGemmK / 16; ++j) {
                                 const bool add = j > 0 || u > 0 || !first;
-                                const uint64_t aj = da + 2 * j, bj = db + 2 * j;     // 32 bytes along K
-                                tc::mma(acc, aj, bj, idesc, add);                    // (fp32: the first two terms at once)
-                                if constexpr (F32) {
-                                    const uint32_t cross = acc + uint32_t(a.bn);
-                                    if constexpr (kQuant) tc::mma(cross, aj + (kOperandA >> 4), bj, ione, true);
-                                    else tc::mma(cross, aj, bj + 2 * (b_bytes >> 4), ione, true);
+                                const uint64_t bj = db + 2 * j;                      // 32 bytes along K
+                                const uint32_t cross = acc + uint32_t(a.bn);
+                                if constexpr (kQuant) {                              // (fp32: the tokens' two terms at once)
+                                    tc::mma_ts(acc, wt + 8 * j, bj, idesc, add);
+                                    if constexpr (F32) tc::mma_ts(cross, wt + 32 + 8 * j, bj, ione, true);
+                                } else {
+                                    tc::mma(acc, da + 2 * j, bj, idesc, add);
+                                    if constexpr (F32) tc::mma(cross, da + 2 * j, bj + 2 * (b_bytes >> 4), ione, true);
                                 }
                             }
                         }
