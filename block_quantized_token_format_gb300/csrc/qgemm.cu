@@ -2,9 +2,8 @@
 // tile's tokens, the launch.  Formulas and argument rules are in include/qgemv.h; the product's
 // kernel in qgemm.cuh.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
-#include <map>
-#include <mutex>
 
 #include "qgemm.cuh"
 #include "qgemv_host.h"
@@ -244,12 +243,10 @@ qg_status check(const GemmCall& c) {
 // Clusters of `parts` CTAs, an SM each, that run at once (cached: every geometry of these kernels
 // fills an SM).
 int clusters_at_once(const void* fn, int dev, int threads, size_t smem, int parts) {
-    static std::mutex mu;
-    static std::map<std::pair<int, int>, int> cache;
-    std::lock_guard<std::mutex> lk(mu);
-    const auto key = std::make_pair(dev, parts);
-    const auto it = cache.find(key);
-    if (it != cache.end()) return it->second;
+    static std::atomic<int> cache[64][9];                // one more than the number; 0: not known yet
+    if (dev < 0 || dev >= 64) return 0;
+    const int known = cache[dev][parts].load(std::memory_order_relaxed);
+    if (known) return known - 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(parts));
     cfg.blockDim = dim3(unsigned(threads));
@@ -262,7 +259,7 @@ int clusters_at_once(const void* fn, int dev, int threads, size_t smem, int part
     cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) { cudaGetLastError(); n = 0; }
-    cache[key] = n;
+    cache[dev][parts].store(n + 1, std::memory_order_relaxed);
     return n;
 }
 
@@ -279,7 +276,7 @@ Geometry geometry(int fmt, bool f32, int bn, int optin) {
     const size_t raw = size_t(kGemmRows) * size_t(raw_codes(fmt)), scales = size_t(kGemmRows) * kScaleSlots * size_t(raw_scales(fmt));
     const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
     Geometry g{};
-    g.subs = !f32 && bn <= 128 ? 2 : 1;
+    g.subs = bn <= (quant ? (f32 ? 64 : 160) : f32 ? 0 : 128) ? 2 : 1;
     const size_t stage = size_t(g.subs) * ((quant ? 0 : size_t(kOperandA)) + size_t(terms_x(fmt, f32)) * size_t(bn) * kGemmK * 2);
     auto slots = [&](int stages) { return int(std::min<size_t>(kMostRaws, (room - size_t(stages) * stage) / std::max<size_t>(raw, 1))) / std::max(groups, 1) * groups; };
     g.stages = int(std::min<size_t>(quant ? (g.subs == 2 ? 3 : 4) : 8, (room - size_t(groups) * raw) / stage));
@@ -289,14 +286,19 @@ Geometry geometry(int fmt, bool f32, int bn, int optin) {
     return g;
 }
 
-// The tile's tokens, and the CTAs that share its K.  Measured on GB300 (128 rows, 64 of K, all SMs): a
-// step takes 270 ns with three stages and 310 with two whatever the tokens, until 1.85 ns a token are
-// more (240: 440 ns); with bf16 weights 160 ns or 1.55 a token; in fp32 330 ns and 3.2 a token (bf16
-// weights 300 and 2.75).  Tiles run on all SMs in rounds, each with about 1.5 us of its own; a cluster's
-// join takes 2.5 us.
+// Nanoseconds of a step of K (64) of a tile of bn tokens, all SMs at work, as measured on GB300: the
+// decoding of the codes, or from some size on the tokens' way from L2 and the products.
+double step_ns(int fmt, bool f32, int bn) {
+    if (fmt == QG_BF16) return f32 ? 300.0 + 2.75 * bn : std::max(160.0, 1.55 * bn);
+    if (!f32) return std::max(fmt == QG_Q8_0 ? 215.0 : fmt == QG_Q5_0 ? 300.0 : 255.0, 1.8 * bn);
+    return std::max(fmt == QG_Q8_0 ? 0.0 : fmt == QG_Q4_0 ? 375.0 : fmt == QG_Q5_0 ? 450.0 : 535.0, 290.0 + 1.8 * bn + (bn > 80 ? 70.0 : 0.0));      // (two stages)
+}
+
+// The tile's tokens, and the CTAs that share its K.  Tiles run on all SMs in rounds, each with about
+// 1.5 us of its own (fp32 2.5); a cluster's join takes 2.5 us.
 struct Shape { int bn, parts; };
 template <typename Clusters>
-Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms, int optin, Clusters clusters) {
+Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slots, int64_t n_experts, int sms, Clusters clusters) {
     Shape best{32, 1};
     double least = 0;
     const double ksteps = double((n_in + kGemmK - 1) / kGemmK);
@@ -304,10 +306,7 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
     // (of 20,480 rows and 512 experts in tiles of 64 that makes 577 tiles; a routing had 568).
     const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
     for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
-        const bool quant = fmt != QG_BF16;
-        const Geometry g = geometry(fmt, f32, bn, optin);
-        const double step = f32 ? (quant ? 330.0 + 3.2 * bn : 300.0 + 2.75 * bn)
-                            : quant ? std::max(g.subs == 2 && g.stages >= 3 ? 270.0 : 310.0, 1.85 * bn) : std::max(160.0, 1.55 * bn);
+        const double step = step_ns(fmt, f32, bn);
         for (int parts = 1; parts <= 8; parts *= 2) {
             double rounds;
             if (n_experts == 0) {
@@ -321,7 +320,7 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
                     per_expert += 0.5 * std::erfc((j * bn - mean) / (spread * 1.41421356));
                 rounds = std::max(1.0, double(m_tiles) * double(n_experts) * per_expert / sms);
             }
-            const double cost = rounds * (ksteps / parts * step + 1500.0) + (parts > 1 ? 2500.0 : 0.0);
+            const double cost = rounds * (ksteps / parts * step + (f32 ? 2500.0 : 1500.0)) + (parts > 1 ? 2500.0 : 0.0);
             if (least == 0 || cost < least) {
                 best = {bn, parts};
                 least = cost;
@@ -369,7 +368,7 @@ qg_status launch_gemm(const GemmCall& c) {
     const int64_t m_tiles = (c.n_out + kGemmRows - 1) / kGemmRows;
     const void* const fn = qgemm_lookup(c.fmt, f32);
     const int threads = gemm_threads(c.fmt, f32);
-    const Shape shape = tile_shape(c.fmt, f32, c.n_in, m_tiles, c.n_slots, c.n_experts, sms, optin, [&](int parts) {
+    const Shape shape = tile_shape(c.fmt, f32, c.n_in, m_tiles, c.n_slots, c.n_experts, sms, [&](int parts) {
         const size_t smem = geometry(c.fmt, f32, 32, optin).smem;
         return blocks_per_sm(fn, dev, optin, threads, smem) < 1 ? 0 : clusters_at_once(fn, dev, threads, smem, parts);
     });

@@ -7,9 +7,8 @@
 //   * one thread copies, with tensor copies, W's raw codes (each step) and scales (every fourth)
 //     into one ring and the tokens' operand (staged by stage_kernel, qgemm.cu) into another;
 //   * groups of four warps turn the codes into 16-bit floats, a lane a row, a group a step, and put
-//     them into tensor memory, from where the products take them: through shared memory a step's
-//     operand would be written and, for every 16 of K, read there, which bounded the kernel (32
-//     tokens: 58 of its 90 KB a step; 270 ns against XXX);
+//     them into tensor memory, from where the products take them: through shared memory, which
+//     bounded the kernel, it was 32 of a step's 58 KB there (Q8_0, 32 tokens: 270 ns a step, now 204);
 //   * one thread issues the products;
 //   * eight warps empty the accumulators, of which there are two sets, so that a tile's epilogue
 //     runs beside the next one's products.
@@ -240,7 +239,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             const float bias = a.bias && there ? a.bias[row] : 0.0f;
             const int col = a.f == kFSwiglu ? row >> 1 : row;
             const bool writes = there && (a.f != kFSwiglu || (lane & 1) == 0);
-            constexpr int kSums = !F32 ? 1 : gemm_most_tokens(FMT, true) / 32;   // fp32: sets of 16 sums of a lane
+            constexpr int kSums = !F32 ? 1 : (gemm_most_tokens(FMT, true) / 2 + 15) / 16;   // fp32: sets of 16 sums of a lane
             float sum[F32 ? 16 * kSums : 1];
             uint32_t v[16];
             // 16 columns of this lane's row: one pass per part of the epilogue that the call has, so that
