@@ -88,7 +88,8 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     PromptArgs a{};
     qg_status st = device_info(&dev, &sms, &optin, &a.status);
     if (st != QG_OK) return st;
-    if (blocks_per_sm(kern.fn, dev, optin, kern.threads, size_t(kern.smem)) < 1) return QG_EUNSUPPORTED;
+    const int resident = blocks_per_sm(kern.fn, dev, optin, kern.threads, size_t(kern.smem));
+    if (resident < 1) return QG_EUNSUPPORTED;
     if (f32) {
         const PromptSpace sp = prompt_space(act, n_tok, n_heads, n_kv_heads, head_dim);
         uint8_t* const ws = static_cast<uint8_t*>(workspace);
@@ -112,9 +113,7 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
         if (st == QG_OK) st = encode_heads(&a.vmap, v, n_tok, n_kv_heads, head_dim, v_stride, 1, kern.tile_keys);
     }
     if (st != QG_OK) return st;
-    a.k = k;
     a.v = v;
-    a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.cu_seq = cu_seq;
     a.out = out;
@@ -127,6 +126,7 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     a.group = group;
     a.tokens = tokens;
     a.window = window;
+    a.asks = items > int64_t(resident) * sms;
     // (Zero: the smallest factor instead, which leaves masked scores at -infinity.)
     a.c = std::max(std::fabs(scale) * kLog2e, FLT_MIN);
     a.negate = scale < 0.0f ? 1u << 13 : 0u;
@@ -134,8 +134,7 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.extra_tx = test_extra_tx();
     void* params[] = {&a};
-    const int64_t grid = kern.stay ? std::min<int64_t>(items, int64_t(kern.stay) * sms) : items + 1;
-    return launch_after(kern.fn, int(grid), kern.threads, size_t(kern.smem), 1, f32, params, stream);
+    return launch_after(kern.fn, int(items), kern.threads, size_t(kern.smem), 1, f32, params, stream);
 }
 
 }  // extern "C"

@@ -21,13 +21,14 @@ constexpr unsigned kPromptBadLength = 16u;       // QG_DEVICE_BAD_LENGTH
 
 struct PromptArgs {
     CUtensorMap qmap, kmap, vmap;
-    const void *k, *v;
-    long long k_stride, v_stride;
+    const void* v;
+    long long v_stride;
     const int32_t* cu_seq;
     void* out;
     float* lse;
     long long out_stride;
     int n_tok, n_seq, n_heads, n_kv, group, tokens, window;      // tokens: T
+    int asks;                      // the grid does not run at once: CTAs take on what others would
     float c;                       // |scale| log2 e
     uint32_t negate;               // of the instruction descriptor, where scale < 0
     const float *qscale, *kscale, *vscale;       // fp32: powers of two, per row, per token that begins a key tile
@@ -57,14 +58,12 @@ __device__ __forceinline__ bool prompt_piece(const int32_t* cu_seq, int n_seq, i
     it.t0 = int(min(t0, 0x7FFFFFFFll));
     return t0 >= 0 && t0 < it.len;
 }
-// Entries of cu_seq, checked by one CTA.
-__device__ __forceinline__ void prompt_check(const PromptArgs& a) {
-    bool bad = false;
-    for (int r = int(threadIdx.x); r < a.n_seq; r += int(blockDim.x)) {
-        const int from = a.cu_seq[r], to = a.cu_seq[r + 1];
-        bad |= from < 0 || to < from || to > a.n_tok;
-    }
-    if (bad) atomicOr(a.status, kPromptBadLength);
+// Entries of cu_seq, 32 by the warp that has the item `at` (there are as many items as prompts).
+__device__ __forceinline__ void prompt_check(const PromptArgs& a, int at) {
+    const long long r = (long long)at * 32 + (int(threadIdx.x) & 31);
+    if (r >= a.n_seq) return;
+    const int from = a.cu_seq[r], to = a.cu_seq[r + 1];
+    if (from < 0 || to < from || to > a.n_tok) atomicOr(a.status, kPromptBadLength);
 }
 
 // Key tiles of an item: the first key (of the prompt) and their number.  `whole`: tiles begin at
@@ -198,11 +197,6 @@ __device__ __forceinline__ unsigned long long pair_add(unsigned long long a, uns
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ unsigned long long pair_mul(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 // The largest of N scores (NaN counts as none).
 template <int N> __device__ __forceinline__ float largest(const uint32_t (&x)[N]) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -213,17 +207,31 @@ template <int N> __device__ __forceinline__ float largest(const uint32_t (&x)[N]
             asm("max.f32 %0, %0, %1, %2;" : "+f"(m[n]) : "f"(__uint_as_float(x[i + 2 * n])), "f"(__uint_as_float(x[i + 2 * n + 1])));
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-// The two warps that share 32 rows meet (`pair`: which of the four).  One whose wait has given up
-// leaves instead, so that the other, if it is in meet(), goes on; it then finds `dead` and leaves too.
-__device__ __forceinline__ bool meet(int pair, const volatile uint32_t& dead) {
+// The SIDES warps that share 32 rows meet (`rows`: which of the four).  One whose wait has given up
+// leaves instead, so that the others, if they are in meet(), go on; they then find `dead` and leave too.
+template <int SIDES> __device__ __forceinline__ bool meet(int rows, const volatile uint32_t& dead) {
     if (__any_sync(tc::kFullMask, dead != 0)) return false;
-    asm volatile("bar.sync %0, 64;" :: "r"(pair + 1) : "memory");
+    asm volatile("bar.sync %0, %1;" :: "r"(rows + 1), "n"(32 * SIDES) : "memory");
     return true;
 }
-__device__ __forceinline__ void leave(int pair) { asm volatile("bar.arrive %0, 64;" :: "r"(pair + 1) : "memory"); }
+template <int SIDES> __device__ __forceinline__ void leave(int rows) {
+    asm volatile("bar.arrive %0, %1;" :: "r"(rows + 1), "n"(32 * SIDES) : "memory");
+}
+// The largest of the row's lanes' maxima, and the sum of their sums (in the same order in each).
+template <int SIDES> __device__ __forceinline__ float largest_of(const float* shared, int row) {
+    float m = shared[row];
+#pragma unroll
+    for (int s = 1; s < SIDES; ++s) m = fmaxf(m, shared[s * 128 + row]);
+    return m;
+}
+template <int SIDES> __device__ __forceinline__ float sum_of_lanes(const float* shared, int row) {
+    float m = shared[row];
+#pragma unroll
+    for (int s = 1; s < SIDES; ++s) m += shared[s * 128 + row];
+    return m;
+}
 
-// parts: CTAs of an item; stay: CTAs of an SM that take item after item (0: a CTA takes one, and one more checks cu_seq)
-struct PromptKernel { const void* fn; int threads, smem, tile_keys, parts, stay; };
+struct PromptKernel { const void* fn; int threads, smem, tile_keys, parts; };       // parts: CTAs of an item
 PromptKernel prompt_bf16(int D);
 PromptKernel prompt_f32(int D);
 

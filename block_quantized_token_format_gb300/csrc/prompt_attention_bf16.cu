@@ -6,12 +6,23 @@
 // the products.  S (fp32) and then P (bf16, over S) lie in tensor memory, P being the second
 // product's operand there, and O is summed there.  A row's reference is raised, and O scaled,
 // only where a tile's maximum is more than 2^8 above it: then rarely after the first tiles.
-// CTAs stay and take one item after another: the next one's queries and first keys are copied, and its
-// first S is made, while the last one's output is written.  Heads of 64 and 128 take 256 columns of tensor memory and at most 96 KB, so that two CTAs share an
-// SM and the one's softmax runs beside the other's products; heads of 256 fill an SM with one CTA,
-// which issues the next tile's S before it waits for P.
+// CTAs stay and take one item after another, asking for the next that no CTA has begun: the next one's queries and first keys are copied, and its
+// first S is made, while the last one's output is written.  Heads of 64 and 128 take 256 columns of
+// tensor memory and at most 97 KB, so that two CTAs share an SM and the one's softmax runs beside the
+// other's products; heads of 256 fill an SM with one CTA.  The next tile's S is issued before P is
+// waited for.
 //
-// Numbers: products of bf16 values are exact, sums fp32; P is rounded to bf16 (2^-9 of each), its
+// Bound by a tile's softmax, one dependent chain of tensor-memory load, maximum over two lanes,
+// exponentials and store, which the two CTAs' tiles cover only in part, and by the scores' products,
+// which read 6 KB of operands from shared memory in the 32 clocks that they would take: heads of
+// 128 keep the tensor cores busy 70 % of the time and issue instructions in 49 % of the clocks, DRAM is
+// at 8 %.  8191 tokens, 48 heads of 128 on 16: 566 us, 1455 TFLOP/s of visible keys' products; 60 packed prompts
+// of up to 1500 tokens, 32 heads on 8: 285 us; 5 prompts of up to 5000, 24 heads of 256 on 4, window
+// 1024: 191 us.  Steps: one lane a row to two and packed arithmetic 875 -> 707 us (8191 tokens); CTAs that
+// stay 524 -> 425 (packed prompts); tiles of 64 keys, not 128, with two buffers of S 425 -> 352; items
+// taken as CTAs come free, not in turn, 349 -> 285.  Four lanes a row with heads of 256: 203 -> 210, not kept.
+//
+// Numbers: products of bf16 values are exact, sums fp32; P is rounded to bf16 (2^-8 of each), its
 // sum is not.  A tile on an edge (some row does not see some key) may hold values of keys that
 // other rows, or none, see: one that is not finite would reach every row as 0 * inf.  Such tiles are looked
 // through, those values made zeros for the product, and the rows that see them get them afterwards.
@@ -20,12 +31,13 @@
 namespace qg {
 namespace {
 
-constexpr int kSoftWarps = 8, kPromptThreads = 32 * (kSoftWarps + 2);
 constexpr int kItems = 4;          // that the copying warp may be ahead
 constexpr float kSlack = 8.0f;     // log2: P is at most 2^8
 
 template <int D> struct Shape {
     static constexpr int KT = 64, STAGES = 2, SB = 2;
+    static constexpr int SIDES = 2, WARPS = 4 * SIDES;    // lanes of a row, warps of the softmax
+    static constexpr int THREADS = 32 * (WARPS + 2);
     static constexpr int CH = D / 64;                                // 64-wide pieces of a head
     static constexpr int Q_BYTES = CH * 128 * 128, T_BYTES = CH * KT * 128;      // (T: a key or value tile)
     static constexpr int SMEM = 1024 + Q_BYTES + 2 * STAGES * T_BYTES;
@@ -37,20 +49,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&p);
 }
 
-template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) prompt_bf16_kernel(const __grid_constant__ PromptArgs a) {
+template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ? 1 : 2) prompt_bf16_kernel(const __grid_constant__ PromptArgs a) {
     using S = Shape<D>;
-    constexpr int KT = S::KT, CH = S::CH;
+    constexpr int KT = S::KT, CH = S::CH, SIDES = S::SIDES, kSoftWarps = S::WARPS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_mem[18 + 2 * kItems];
+    __shared__ uint64_t bar_mem[19 + 2 * kItems];
+    __shared__ uint4 answer_mem;                         // the grid's next item
     __shared__ PromptItem item_mem[kItems];              // found by the copying warp, ahead of the others
     __shared__ uint32_t tmem_at, dead, odd;
-    __shared__ float most_of[2][256], sum_of[256];       // both lanes' maxima, of even and odd tiles, and sums
+    __shared__ float most_of[2][SIDES * 128], sum_of[SIDES * 128];       // the lanes' maxima, of even and odd tiles, and sums
 
     const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     tc::grid_launch_dependents();
     tc::grid_wait();
-    if (blockIdx.x == 0) prompt_check(a);
-    const int slots = a.n_tok / a.tokens + a.n_seq, items = slots * a.n_kv;
+    const int slots = a.n_tok / a.tokens + a.n_seq;      // (a CTA for each slot and key/value head)
 
     const uint32_t q_at = (smem_addr(smem_raw) + 1023u) & ~1023u, k_at = q_at + S::Q_BYTES, v_at = k_at + S::STAGES * S::T_BYTES;
     const uint32_t bars = smem_addr(bar_mem);
@@ -63,6 +75,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     auto p_full = [&](int s) { return bars + 128u + 8u * uint32_t(s); };
     auto i_full = [&](int s) { return bars + 144u + 8u * uint32_t(s); };
     auto i_empty = [&](int s) { return bars + 144u + 8u * uint32_t(kItems + s); };
+    const uint32_t answered = bars + 144u + 16u * uint32_t(kItems), answer = smem_addr(&answer_mem);
     const tc::Waits wait{&dead, a.status, a.wait_limit};
 
     if (tid == 0) {
@@ -73,6 +86,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
         mbar_init(o_empty, kSoftWarps);
         mbar_init(pv_done, 1);
         mbar_init(drained, 1);
+        mbar_init(answered, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(k_full(s), 1);
             mbar_init(k_empty(s), 1);
@@ -100,7 +114,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     };
 
     if (warp < kSoftWarps) {
-        constexpr int K2 = KT / 2, D2 = D / 2;
+        constexpr int K2 = KT / SIDES, D2 = D / SIDES;
         const int rows = warp & 3, half = warp >> 2, row = rows * 32 + lane;
         const uint32_t mine = tmem + (uint32_t(rows) << 21), o_mine = mine + S::O_AT + uint32_t(half * D2);
         bool alive = true;
@@ -125,10 +139,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                 tc::fence_after();
                 uint32_t x[K2];
                 const uint32_t at = mine + uint32_t(sb * KT);
-#pragma unroll
-                for (int i = 0; i < K2; i += 32) tc::tmem_load32(at + uint32_t(half * K2 + i), x + i);
-#pragma unroll
-                for (int i = 0; i < K2; i += 16) tc::tmem_load_wait16(x + i);
+                tc::tmem_load(at + uint32_t(half * K2), x);
                 const bool edge = j < inside_lo || j >= inside_hi;
                 if (edge) {
                     const int hi = pos - j * KT, lo = low - j * KT;
@@ -139,8 +150,8 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                 float most = largest<K2>(x);
                 float* const shared_most = most_of[g & 1];
                 shared_most[half * 128 + row] = most;
-                if (!meet(rows, dead)) { alive = false; break; }     // (both lanes have their S: P may lie over it now)
-                most = fmaxf(most, shared_most[(half ^ 1) * 128 + row]);
+                if (!meet<SIDES>(rows, dead)) { alive = false; break; }      // (all lanes have their S: P may lie over it now)
+                most = largest_of<SIDES>(shared_most, row);
                 const bool raise = (most - top) * a.c > kSlack || (top == -INFINITY && most > -INFINITY);
                 float factor = 1.0f;
                 if (raise) {
@@ -172,11 +183,10 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                 }
                 const float2 s = values_of(pair_add(s2[0], s2[1]));
                 sum += s.x + s.y;
-                if constexpr (K2 == 64) tc::tmem_store32(at + uint32_t(half * 32), x);
-                else tc::tmem_store16(at + uint32_t(half * 16), x);
+                tc::tmem_store<K2 / 2>(at + uint32_t(half * (K2 / 2)), x);
                 if (edge) {                                  // values that are not finite
                     if (!wait(v_full(int(g % S::STAGES)), g / S::STAGES & 1)) { alive = false; break; }
-                    if (clear_not_finite<kBf16Exp, 2>(v_at + (g % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
+                    if (clear_not_finite<kBf16Exp, SIDES>(v_at + (g % S::STAGES) * S::T_BYTES, S::T_BYTES, tid)) odd = 1;
                     __syncwarp();
                 }
                 tc::tmem_store_wait();
@@ -185,10 +195,10 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
                 if (lane == 0) mbar_arrive(p_full(sb));
             }
             sum_of[half * 128 + row] = sum;
-            alive = alive && wait(o_full, n & 1) && meet(rows, dead);
+            alive = alive && wait(o_full, n & 1) && meet<SIDES>(rows, dead);
             if (alive) {
                 tc::fence_after();
-                sum += sum_of[(half ^ 1) * 128 + row];
+                sum = sum_of_lanes<SIDES>(sum_of, row);
                 const float inv = 1.0f / sum;
                 const PromptItem it = item_mem[n % kItems];
                 const PromptRow r = prompt_row(a, it, row);
@@ -220,7 +230,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
             give_back(n);
             ++n;
         }
-        if (dead) leave(rows);
+        if (dead) leave<SIDES>(rows);
     } else if (warp == kSoftWarps) {
         // --------------------------------------------------------------------- copies
         const int n_q = a.tokens * a.group * 128;        // bytes of a 64-wide piece
@@ -237,13 +247,30 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
             __syncwarp();
             return true;
         };
-        // Items in turn, every other round from the back: the rounds' shares of work even out.
-        for (int round = 0; !dead; ++round) {
-            const long long at = (long long)round * gridDim.x + ((round & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
-            if ((long long)round * gridDim.x >= items) break;
-            if (at >= items) continue;
-            const int b = int(at) / a.n_kv;
-            it.head = int(at) - b * a.n_kv;
+        // After its own item those of CTAs that have not begun, one asked for ahead: items differ in their
+        // tiles by far (in equal turns the most loaded CTA of 60 packed prompts had 1.32 times the mean).
+        uint32_t asked = 0, heard = 0;
+        auto ask = [&]() {
+            tc::fence_async();                           // the last answer has been read
+            if (tc::elect()) {
+                mbar_arrive_expect_tx(answered, 16);
+                tc::ask_block(answer, answered);
+            }
+            __syncwarp();
+            ++asked;
+        };
+        auto next_block = [&]() {
+            if (dead || !wait(answered, heard & 1)) return -1;
+            ++heard;
+            const int block = tc::block_of(answer);
+            __syncwarp();
+            return block;
+        };
+        for (int at = int(blockIdx.x); at >= 0; at = a.asks ? next_block() : -1) {
+            if (a.asks) ask();
+            const int b = at / a.n_kv;
+            it.head = at - b * a.n_kv;
+            prompt_check(a, at);
             if (!prompt_piece(a.cu_seq, a.n_seq, a.n_tok, a.tokens, slots - 1 - b, it)) continue;
             key_range<KT>(a, it, false);
             if (!hand_out(n)) break;
@@ -280,6 +307,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
         it.tiles = 0;                                    // no more items
         hand_out(n);
         if (dead) {                                      // copies still on their way end before the CTA does
+            if (heard < asked) mbar_wait(answered, heard & 1, a.drain_limit);
             if (n > 0) mbar_wait(q_full, (n - 1) & 1, a.drain_limit);
             for (uint32_t i = 1; i <= S::STAGES; ++i) {
                 if (gk >= i) mbar_wait(k_full(int((gk - i) % S::STAGES)), (gk - i) / S::STAGES & 1, a.drain_limit);
@@ -314,11 +342,10 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
             const int tiles = item_mem[n % kItems].tiles;
             give_back(n);
             alive = wait(q_full, n & 1);
-            if (alive && S::SB == 2) alive = scores(g, tiles == 1);
+            if (alive) alive = scores(g, tiles == 1);
             for (int j = 0; j < tiles && alive; ++j, ++g) {
                 const int s = int(g % S::STAGES), sb = int(g % S::SB);
-                if (S::SB == 1) alive = scores(g, j + 1 == tiles);
-                else if (j + 1 < tiles) alive = scores(g + 1, j + 2 == tiles);
+                if (j + 1 < tiles) alive = scores(g + 1, j + 2 == tiles);
                 if (!alive || (j == 0 && !wait(o_empty, (n & 1) ^ 1)) || !wait(v_full(s), g / S::STAGES & 1) || !wait(p_full(sb), g / S::SB & 1)) {
                     alive = false;
                     break;
@@ -348,7 +375,7 @@ template <int D> __global__ void __launch_bounds__(kPromptThreads, D == 256 ? 1 
     if (warp == kSoftWarps + 1) tc::tmem_free(tmem, S::COLS);
 }
 
-template <int D> PromptKernel kernel() { return {(const void*)&prompt_bf16_kernel<D>, kPromptThreads, Shape<D>::SMEM, Shape<D>::KT, 1, D == 256 ? 1 : 2}; }
+template <int D> PromptKernel kernel() { return {(const void*)&prompt_bf16_kernel<D>, Shape<D>::THREADS, Shape<D>::SMEM, Shape<D>::KT, 1}; }
 
 }  // namespace
 

@@ -153,17 +153,14 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_mem[18];
     __shared__ uint32_t tmem_at, dead, odd;
-    __shared__ float most_of[2][SIDES == 2 ? 256 : 1], sum_of[SIDES == 2 ? 256 : 1];       // both lanes' maxima, of even and odd tiles, and sums
+    __shared__ float most_of[2][SIDES > 1 ? SIDES * 128 : 1], sum_of[SIDES > 1 ? SIDES * 128 : 1];      // the lanes' maxima, of even and odd tiles, and sums
 
     const int tid = int(threadIdx.x), warp = __shfl_sync(tc::kFullMask, tid >> 5, 0), lane = tid & 31;
     tc::grid_launch_dependents();
     tc::grid_wait();
-    if (blockIdx.x == gridDim.x - 1) {
-        prompt_check(a);
-        return;
-    }
+    if (warp == 0) prompt_check(a, int(blockIdx.x));
     PromptItem it;
-    const int parts = a.n_kv * S::HALVES, slots = (int(gridDim.x) - 1) / parts, b = int(blockIdx.x) / parts;
+    const int parts = a.n_kv * S::HALVES, slots = int(gridDim.x) / parts, b = int(blockIdx.x) / parts;
     if (!prompt_piece(a.cu_seq, a.n_seq, a.n_tok, a.tokens, slots - 1 - b, it)) return;
     const int part = int(blockIdx.x) - b * parts, half = part % S::HALVES;
     it.head = part / S::HALVES;
@@ -251,10 +248,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             tc::fence_after();
             uint32_t x[K2];
             const uint32_t at = mine + uint32_t(sb * KT);
-#pragma unroll
-            for (int i = 0; i < K2; i += 32) tc::tmem_load32(at + uint32_t(side * K2 + i), x + i);
-#pragma unroll
-            for (int i = 0; i < K2; i += 32) tc::tmem_load_wait32(x + i);
+            tc::tmem_load(at + uint32_t(side * K2), x);
             const bool edge = on_edge<KT>(a, it, k0);
             if (edge) {
                 const int hi = r.pos - k0 - side * K2, lo = r.low - k0 - side * K2;
@@ -263,10 +257,10 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                     if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
             }
             float most = largest<K2>(x);
-            if constexpr (SIDES == 2) {
+            if constexpr (SIDES > 1) {
                 most_of[sb][side * 128 + row] = most;
-                if (!meet(rows, dead)) { alive = false; break; }     // (both lanes have their S: P may lie over it now)
-                most = fmaxf(most, most_of[sb][(side ^ 1) * 128 + row]);
+                if (!meet<SIDES>(rows, dead)) { alive = false; break; }      // (all lanes have their S: P may lie over it now)
+                most = largest_of<SIDES>(most_of[sb], row);
             }
             most *= f;
             const bool raise = most - top > kSlack || (top == -INFINITY && most > -INFINITY);
@@ -292,11 +286,8 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             }
             const float2 s = values_of(pair_add(s2[0], s2[1]));
             sum += s.x + s.y;
-#pragma unroll
-            for (int i = 0; i < K2 / 2; i += 16) {
-                tc::tmem_store16(at + uint32_t(side * (K2 / 2) + i), x + i);
-                tc::tmem_store16(at + KT / 2 + uint32_t(side * (K2 / 2) + i), lo16 + i);
-            }
+            tc::tmem_store<K2 / 2>(at + uint32_t(side * (K2 / 2)), x);
+            tc::tmem_store<K2 / 2>(at + KT / 2 + uint32_t(side * (K2 / 2)), lo16);
             if (edge) {                                  // values that are not finite
                 if (!wait(v_full(j % S::STAGES), j / S::STAGES & 1)) { alive = false; break; }
                 if (clear_not_finite<kFp16Exp, SIDES>(v_at + uint32_t(j % S::STAGES) * 2 * S::V_TERM, 2 * S::V_TERM, tid)) odd = 1;
@@ -315,9 +306,9 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             }
             v_mine = v_this;
         }
-        if constexpr (SIDES == 2) sum_of[side * 128 + row] = sum;
-        if (alive && gather(tiles - 1) && (SIDES == 1 || meet(rows, dead))) {
-            if constexpr (SIDES == 2) sum += sum_of[(side ^ 1) * 128 + row];
+        if constexpr (SIDES > 1) sum_of[side * 128 + row] = sum;
+        if (alive && gather(tiles - 1) && (SIDES == 1 || meet<SIDES>(rows, dead))) {
+            if constexpr (SIDES > 1) sum = sum_of_lanes<SIDES>(sum_of, row);
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const bool look = odd != 0;
             float* const to = static_cast<float*>(a.out) + token * a.out_stride + (long long)head * D + half * DV + side * D2;
@@ -334,7 +325,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                 if (a.lse && half == 0 && side == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : (top - kLift) * kLn2 + logf(sum);
             }
         }
-        if (SIDES == 2 && dead) leave(rows);
+        if (SIDES > 1 && dead) leave<SIDES>(rows);
     } else if (warp == kSoftWarps) {
         // --------------------------------------------------------------------- copies
         const int n_q = a.tokens * a.group * 128;        // bytes of a 64-wide piece
@@ -445,7 +436,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
 }
 
 template <int D> PromptKernel kernel() {
-    return {(const void*)&prompt_f32_kernel<D>, 32 * (Shape<D>::WARPS + 2), Shape<D>::SMEM, kTileKeys, Shape<D>::HALVES, 0};
+    return {(const void*)&prompt_f32_kernel<D>, 32 * (Shape<D>::WARPS + 2), Shape<D>::SMEM, kTileKeys, Shape<D>::HALVES};
 }
 
 }  // namespace

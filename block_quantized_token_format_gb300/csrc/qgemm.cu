@@ -38,7 +38,7 @@ struct StageArgs {
     const int32_t* offsets;
     int32_t* tile_start;
     long long x_stride, n_x;
-    int n_slots, n_in, n_experts, bn, m_tiles;
+    int n_slots, n_in, n_experts, bn;
     unsigned int* status;
 };
 
@@ -105,8 +105,9 @@ __device__ __forceinline__ bool finite_of(float x) { return (__float_as_uint(x) 
 template <typename T, int FMT, int PER> __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a) {
     constexpr bool kQuant = FMT != QG_BF16, kF32 = sizeof(T) == 4;
     __shared__ uint32_t most[kStageThreads / 32];
-    tc::grid_launch_dependents();
+    // What ran before is done, W's writer among it, when the product's kernel begins to copy W.
     tc::grid_wait();
+    tc::grid_launch_dependents();
     if (a.n_experts && blockIdx.x == gridDim.x - 1) {
         plan_tiles(a);
         return;
@@ -316,8 +317,11 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
             } else {
                 if (parts > 1) break;
                 double per_expert = 1.0 - std::exp(-mean);               // the mean of a count's tiles
-                for (int j = 1; j * bn < mean + 4.0 * spread && j < 1000; ++j)
-                    per_expert += 0.5 * std::erfc((j * bn - mean) / (spread * 1.41421356));
+                if (mean > 16.0 * bn)
+                    per_expert = mean / bn + 0.5;                        // (the sum below comes to that)
+                else
+                    for (int j = 1; j * bn < mean + 4.0 * spread; ++j)
+                        per_expert += 0.5 * std::erfc((j * bn - mean) / (spread * 1.41421356));
                 rounds = std::max(1.0, double(m_tiles) * double(n_experts) * per_expert / sms);
             }
             const double cost = rounds * (ksteps / parts * step + (f32 ? 2500.0 : 1500.0)) + (parts > 1 ? 2500.0 : 0.0);
@@ -434,7 +438,6 @@ qg_status launch_gemm(const GemmCall& c) {
         s.n_in = int(c.n_in);
         s.n_experts = int(c.n_experts);
         s.bn = bn;
-        s.m_tiles = int(m_tiles);
         s.status = status;
         // A row takes a CTA where there are too few rows to fill the GPU with a warp each.
         const bool wide = c.n_slots < 8 * sms;

@@ -86,11 +86,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
                  :: QG_R16(v, 0), "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-                 :: QG_R16(v, 0), QG_R16(v, 16), "r"(addr) : "memory");
-}
 #undef QG_R16
 #undef QG_R4
 // Waits for the warp's loads; their values pass through, so that no use of them comes before.
@@ -104,6 +99,19 @@ __device__ __forceinline__ void tmem_load_wait32(uint32_t* v) {
 }
 #undef QG_R16
 #undef QG_R4
+template <int N> __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[N]) {
+    static_assert(N % 32 == 0, "columns");
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_load32(addr + uint32_t(i), v + i);
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_load_wait32(v + i);
+}
+// (of a larger array's first N)
+template <int N> __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* v) {
+    static_assert(N % 16 == 0, "columns");
+#pragma unroll
+    for (int i = 0; i < N; i += 16) tmem_store16(addr + uint32_t(i), v + i);
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // True in one lane of a whole warp.  The loops that issue products and copies run in the whole warp
@@ -125,15 +133,6 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const void* map, int x, in
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
-// `bytes` of 16 are copied, the rest are zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 // Shared-memory loads that stay between the barrier operations around them.
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -149,6 +148,26 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------- the grid's next block
+
+// Asks for a CTA of the grid that has not begun, to do its work instead of it: the answer's 16 bytes
+// arrive on `bar`.  Not asked again after an answer that there is none.
+__device__ __forceinline__ void ask_block(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 :: "r"(answer), "r"(bar) : "memory");
+}
+// The block's x, or -1.
+__device__ __forceinline__ int block_of(uint32_t answer) {
+    uint32_t x, got;
+    asm volatile("{\n .reg .pred p;\n .reg .b128 h;\n .reg .b64 lo, hi;\n"
+                 " ld.shared.v2.b64 {lo, hi}, [%2];\n mov.b128 h, {lo, hi};\n"
+                 " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+                 " selp.u32 %1, 1, 0, p;\n mov.u32 %0, 0;\n"
+                 " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n}"
+                 : "=r"(x), "=r"(got) : "r"(answer) : "memory");
+    return got ? int(x) : -1;
+}
 
 // ---------------------------------------------------------------------------- clusters
 
