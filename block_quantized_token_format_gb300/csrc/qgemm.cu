@@ -308,11 +308,12 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
     const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
     for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
         const double step = step_ns(fmt, f32, bn);
-        for (int parts = 1; parts <= 8; parts *= 2) {
+        for (int parts = 1; parts <= 8; ++parts) {
             double rounds;
             if (n_experts == 0) {
                 const int64_t tiles = m_tiles * ((n_slots + bn - 1) / bn);
-                if (parts > 1 && (tiles * parts > sms || ksteps < 8 * parts || clusters(parts) < tiles)) break;
+                if (parts > 1 && (tiles * parts > sms || ksteps < 8 * parts)) break;
+                if (parts > 1 && clusters(parts) < tiles) continue;
                 rounds = double((tiles + sms - 1) / sms);
             } else {
                 if (parts > 1) break;
@@ -324,7 +325,8 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
                         per_expert += 0.5 * std::erfc((j * bn - mean) / (spread * 1.41421356));
                 rounds = std::max(1.0, double(m_tiles) * double(n_experts) * per_expert / sms);
             }
-            const double cost = rounds * (ksteps / parts * step + (f32 ? 2500.0 : 1500.0)) + (parts > 1 ? 2500.0 : 0.0);
+            const double steps = parts > 1 ? kScaleSteps * std::ceil(std::ceil(ksteps / kScaleSteps) / parts) : ksteps;      // of a CTA
+            const double cost = rounds * (steps * step + (f32 ? 2500.0 : 1500.0)) + (parts > 1 ? 2500.0 : 0.0);
             if (least == 0 || cost < least) {
                 best = {bn, parts};
                 least = cost;

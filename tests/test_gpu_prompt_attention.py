@@ -238,6 +238,47 @@ def test_a_wait_that_runs_out_is_reported(act, D):
     assert torch.equal(out, want) and qg.qg_device_status() == 0
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_more_items_than_run_at_once(act, D):
+    """CTAs take items that others would have had: hundreds of short prompts around a longer one, some
+    empty; the same bits every time, and a wait that runs out in such a call ends all of it."""
+    rng = np.random.default_rng(31)
+    lens = list(rng.integers(0, 8, 500))
+    lens[200] = 300
+    cu = [int(sum(lens[:i])) for i in range(len(lens) + 1)]
+    q, k, v = inputs(rng, cu[-1], 4, 2, D, act)
+    out, lse = run(q, k, v, cu, D ** -0.5)
+    check(q, k, v, cu, D ** -0.5, 0, out, lse)
+    for _ in range(3):
+        again, l2 = run(q, k, v, cu, D ** -0.5)
+        assert torch.equal(again, out) and torch.equal(l2, lse)
+    assert qg.qg_device_status() == 0
+    qg.qg_set_wait_limit(2000, 16)
+    run(q, k, v, cu, D ** -0.5)
+    torch.cuda.synchronize()
+    assert qg.qg_device_status() == qg.QG_DEVICE_WAIT_TIMEOUT
+    qg.qg_set_wait_limit(0, 0)
+    again, _ = run(q, k, v, cu, D ** -0.5)
+    assert torch.equal(again, out) and qg.qg_device_status() == 0
+
+
+@pytest.mark.parametrize("at", [0, 31, 32, 400])
+def test_one_wrong_length_among_many_prompts(at):
+    """It is reported wherever it stands."""
+    rng = np.random.default_rng(32)
+    cu = list(range(0, 2 * 402, 2))
+    q, k, v = inputs(rng, cu[-1], 2, 2, 64, "bf16")
+    run(q, k, v, cu, 0.1)
+    torch.cuda.synchronize()
+    assert qg.qg_device_status() == 0
+    bad = list(cu)
+    bad[at + 1] = -7
+    run(q, k, v, bad, 0.1)
+    torch.cuda.synchronize()
+    assert qg.qg_device_status() & qg.QG_DEVICE_BAD_LENGTH
+
+
 def test_binding_refuses():
     rng = np.random.default_rng(28)
     q, k, v = inputs(rng, 20, 4, 2, 64, "bf16")

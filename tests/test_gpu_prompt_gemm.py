@@ -312,6 +312,29 @@ def test_experts(fmt, act, n_experts, n_out, n_in, most, gather, f):
     assert qg.qg_device_status() == 0
 
 
+@pytest.mark.parametrize("fmt,act", [("q8_0", "bf16"), ("q4_0", "f32"), ("bf16", "bf16")])
+def test_few_experts_with_thousands_of_rows(fmt, act):
+    rng = np.random.default_rng(33)
+    n_out, n_in, n_x, off = 130, 64, 29, [0, 15001, 15001, 20000]
+    c, W = packed(rng, fmt, 3 * n_out, n_in)
+    x = tokens(rng, n_x, n_in, act)
+    rows = rng.integers(0, n_x, off[-1])
+    y = torch.zeros(off[-1], n_out, dtype=DT[act], device="cuda")
+    qg.qgemm_experts(fmt, W, 3, n_out, n_in, x, torch.tensor(off, dtype=torch.int32, device="cuda"), y,
+                     space(fmt, act, n_out, n_in, off[-1], 3), rows=torch.tensor(rows, dtype=torch.int32, device="cuda"))
+    got = host(y)
+    for e in (0, 2):                                                 # equal rows of an expert are equal
+        first = {}
+        for s in range(off[e], off[e + 1]):
+            assert (got[s] == got[first.setdefault(rows[s], s)]).all()
+        slots = sorted(first.values())
+        args = (fmt, c, 3, n_out, n_in, host(x), [0] * (e + 1) + [len(slots)] * (3 - e), rows[slots])
+        v, S = PO.gemm_experts(*args), PO.gemm_experts(*args, product=PO.gemm_abs)
+        for i, s in enumerate(slots):
+            assert (np.abs(got[s] - v[i]) <= tolerance(S[i], v[i], v[i], n_in, act, "none")).all()
+    assert qg.qg_device_status() == 0
+
+
 @pytest.mark.parametrize("off", [[0, 5, 3, 9], [-1, 2, 4, 6], [0, 4, 8, 11], [0, 2, 1, 0]])
 def test_offsets_that_are_no_offsets(off):
     rng = np.random.default_rng(13)
