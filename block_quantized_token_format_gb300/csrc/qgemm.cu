@@ -100,8 +100,9 @@ __device__ __forceinline__ bool finite_of(float x) { return (__float_as_uint(x) 
 // power of two that takes its largest magnitude to [2^14, 2^15) (a second term holds what the
 // first one's rounding left: 22 bits together); with bf16 weights: the bf16 values, or three
 // bf16 terms of fp32 ones, each the next 8 bits (cut off, so that they add up exactly).  A value
-// that is not finite is its own first term.  `PER` threads take a row.  Bound by the launch for
-// few rows, else by memory.
+// that is not finite is its own first term.  `PER` threads take a row: a warp, or a CTA where rows are
+// too few to fill the GPU with warps (17 tokens of 6144: the row's latency, not its bytes).  Bound by
+// the launch for few rows, else by memory (a bf16 row is read twice, out of L2 the second time).
 template <typename T, int FMT, int PER> __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a) {
     constexpr bool kQuant = FMT != QG_BF16, kF32 = sizeof(T) == 4;
     __shared__ uint32_t most[kStageThreads / 32];

@@ -13,6 +13,17 @@
 //   * eight warps empty the accumulators, of which there are two sets, so that a tile's epilogue
 //     runs beside the next one's products.
 // A CTA takes tiles in turn; consecutive tiles share their tokens (which then come from L2).
+// Where tiles are few, a cluster of up to eight CTAs shares each tile's K; they join their sums through
+// one another's shared memory, in the order of K (2560 x 6144, 17 tokens fp32: 61 -> 17 us).
+//
+// What bounds it.  Quantized weights with many tokens: the decoding (Q8_0: 215 ns a step whatever
+// the tokens; instructions are issued in 64 % of the clocks, the tensor cores work in 60 %), and for tiles of
+// 128 tokens and more the way of the operands into the SM, about 60 bytes a clock: Q8_0, bf16, 10240 x 2560,
+// 8191 tokens 317 to 339 us, 1270 to 1355 TFLOP/s; bf16 weights, which need no decoding, 2560 x 6144, 8191
+// tokens 155 us, 1654 TFLOP/s.  fp32: its three products and the sums' moves to registers, 2047 tokens of
+// 2560 x 12288 with swiglu 332 us.  Experts with few rows each: their weights' way from memory (61 tokens of
+// 512 experts, 1.22 GB: 226 us, 5.4 TB/s), and with 40 rows each (2048 tokens, 421 us) decoding again.  A few tokens: two launches, the
+// first copies and the join.
 //
 // Numbers.  Quantized formats enter as fp16: a code times its fp16 scale has at most 19 bits.
 // bf16 activations, which a row's power of two moves into fp16's range exactly (but for values
