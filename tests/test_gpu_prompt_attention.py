@@ -253,6 +253,10 @@ def test_more_items_than_run_at_once(act, D):
     for _ in range(3):
         again, l2 = run(q, k, v, cu, D ** -0.5)
         assert torch.equal(again, out) and torch.equal(l2, lse)
+    qg.qg_set_launch_options(qg.QG_LAUNCH_EARLY_START)
+    many = [run(q, k, v, cu, D ** -0.5)[0] for _ in range(4)]
+    qg.qg_set_launch_options(0)
+    assert all(torch.equal(m, out) for m in many)
     assert qg.qg_device_status() == 0
     qg.qg_set_wait_limit(2000, 16)
     run(q, k, v, cu, D ** -0.5)
