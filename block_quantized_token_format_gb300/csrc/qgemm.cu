@@ -308,7 +308,8 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
     // (of 20,480 rows and 512 experts in tiles of 64 that makes 577 tiles; a routing had 568).
     const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
     for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
-        const double step = step_ns(fmt, f32, bn);
+        // (An expert's tile has no more tokens than the expert.)
+        const double step = step_ns(fmt, f32, n_experts ? std::min(bn, int(mean + spread) / 16 * 16 + 16) : bn);
         for (int parts = 1; parts <= 8; ++parts) {
             double rounds;
             if (n_experts == 0) {
@@ -400,6 +401,7 @@ qg_status launch_gemm(const GemmCall& c) {
     a.y_stride = c.y_stride;
     a.f = int(c.f);
     a.bn = bn;
+    a.box = c.n_experts ? 16 : bn;
     a.m_tiles = int(m_tiles);
     a.n_tiles = int(n_tiles);
     a.status = status;
@@ -415,8 +417,8 @@ qg_status launch_gemm(const GemmCall& c) {
     if (a.stages < 2 || a.stages * a.subs < groups || (quant && a.raws < groups)) return QG_EUNSUPPORTED;
     if (blocks_per_sm(fn, dev, optin, threads, geo.smem) < 1) return QG_EUNSUPPORTED;
     const int64_t rows = std::max<int64_t>(1, c.n_experts) * c.n_out, pitch = row_stride(c.fmt, c.n_in);
-    st = stages_x ? encode_tokens(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, bn)
-                  : encode_tokens(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, bn);
+    st = stages_x ? encode_tokens(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, a.box)
+                  : encode_tokens(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, a.box);
     if (st == QG_OK && !quant)
         st = encode_2d(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.W, c.n_in, rows, pitch, kGemmK, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == QG_OK && quant)

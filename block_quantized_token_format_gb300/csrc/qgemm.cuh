@@ -79,7 +79,7 @@ struct GemmArgs {
     const void* residual;
     void* y;
     long long residual_stride, y_stride;
-    int f, bn, subs, stages, raws, m_tiles, n_tiles;      // subs: steps of K in a stage
+    int f, bn, box, subs, stages, raws, m_tiles, n_tiles;      // box: tokens of a copy; subs: steps of K in a stage
     int parts;                                            // CTAs of a cluster that share a tile's K
     unsigned int* status;
     uint32_t wait_limit, drain_limit, extra_tx;
@@ -92,7 +92,9 @@ template <bool F32> __device__ __forceinline__ float silu_of(float v) {
     return F32 ? v / (1.0f + expf(-v)) : __fdividef(v, 1.0f + __expf(-v));
 }
 
-struct GemmTile { int row0, w_row0, slot0, cols; };       // row0: in the expert's matrix; w_row0: in the stack
+// row0: in the expert's matrix; w_row0: in the stack.  n: tokens that are copied and multiplied (experts: no more
+// than the tile has, in sixteens, so that a tile for an expert's most rows costs no more where it has few).
+struct GemmTile { int row0, w_row0, slot0, cols, n; };
 
 __device__ __forceinline__ int gemm_tiles(const GemmArgs& a) {
     return (a.n_experts ? a.tile_start[a.n_experts] : a.n_tiles) * a.m_tiles;
@@ -105,6 +107,7 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& a, int t) {
         g.w_row0 = g.row0;
         g.slot0 = nt * a.bn;
         g.cols = min(a.bn, a.n_slots - g.slot0);
+        g.n = a.bn;
         return g;
     }
     int lo = 0, hi = a.n_experts;                        // the last expert with tile_start <= nt
@@ -114,6 +117,7 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& a, int t) {
     }
     g.slot0 = a.offsets[lo] + (nt - a.tile_start[lo]) * a.bn;
     g.cols = min(a.bn, a.offsets[lo + 1] - g.slot0);
+    g.n = (g.cols + 15) / 16 * 16;
     g.w_row0 = lo * a.n_out + g.row0;
     return g;
 }
@@ -236,8 +240,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
     if (warp < kDrainWarps) {
         // ---------------------------------------------------------------- accumulators to y
         tc::grid_wait();
-        const int half = warp >> 2, split = (a.bn / 2 + 15) / 16 * 16;       // its part of the columns
-        const int from = half * split, hc = half ? a.bn - split : split;
+        const int half = warp >> 2;
         const uint32_t lanes = uint32_t(warp & 3) << 21;             // 32 (warp % 4) in the address's high half
         const int chunks = F32 ? (ke - kb + kChunkSteps - 1) / kChunkSteps : 1;
         const int tiles = gemm_tiles(a);
@@ -245,6 +248,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
         bool alive = true;
         for (int t = tile0; t < tiles && alive; t += tile_step) {
             const GemmTile g = gemm_tile(a, t);
+            const int split = (g.n / 2 + 15) / 16 * 16, from = half * split, hc = half ? g.n - split : split;      // its part of the columns
             const int row = g.row0 + (warp & 3) * 32 + lane;
             const bool there = row < a.n_out;
             const float bias = a.bias && there ? a.bias[row] : 0.0f;
@@ -312,7 +316,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
 #pragma unroll
                     for (int u = 0; u < kSums; ++u)
                         if (u * 16 < hc) {
-                            tc::tmem_load16(acc + uint32_t(a.bn) + u * 16, v);
+                            tc::tmem_load16(acc + uint32_t(g.n) + u * 16, v);
                             tc::tmem_load_wait16(v);
 #pragma unroll
                             for (int c = 0; c < 16; ++c) sum[u * 16 + c] = ch == 0 ? __uint_as_float(v[c]) : sum[u * 16 + c] + __uint_as_float(v[c]);
@@ -325,6 +329,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                     __syncwarp();
                     if (lane == 0) mbar_arrive(acc_empty(b));
                 } else {
+                    if (hc == 0 && lane == 0) mbar_arrive(acc_empty(b));     // (16 tokens: all in the first half)
                     for (int u = 0; u * 16 < hc; ++u) {
                         tc::tmem_load16(acc + u * 16, v);
                         tc::tmem_load_wait16(v);
@@ -354,7 +359,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                 // Every CTA of the cluster joins and writes some of the tile's columns; the parts are
                 // added in the order of K.
                 if (alive)
-                    for (int c0 = (rank + (warp >> 2) * a.parts) * 16; c0 < a.bn; c0 += 2 * a.parts * 16) {
+                    for (int c0 = (rank + (warp >> 2) * a.parts) * 16; c0 < g.n; c0 += 2 * a.parts * 16) {
                         float x[16];
 #pragma unroll
                         for (int c = 0; c < 16; ++c) x[c] = 0.0f;
@@ -457,13 +462,13 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
         {
             tc::grid_wait();
             const int tiles = gemm_tiles(a);
-            const uint32_t bytes = TX * b_bytes + a_bytes;
             uint32_t extra = a.extra_tx;
             int s = 0;
             uint32_t phase = 0, filled = 0;
             bool alive = true;
             for (int t = tile0; t < tiles && alive; t += tile_step) {
                 const GemmTile g = gemm_tile(a, t);
+                const uint32_t term = uint32_t(g.n) * kGemmK * 2, bytes = TX * term + a_bytes;
                 for (int k = kb; k < ke; k += a.subs) {
                     if (!wait(empty(s), phase ^ 1)) { alive = false; break; }
                     uint32_t at = base + uint32_t(s) * stage_bytes;
@@ -472,7 +477,9 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                         for (int u = 0; u < a.subs; ++u, at += sub_bytes) {
                             if constexpr (!kQuant) tc::load_2d(at, &a.wmap, (k + u) * kGemmK, g.w_row0, full(s));
 #pragma unroll
-                            for (int x = 0; x < TX; ++x) tc::load_3d(at + a_bytes + x * b_bytes, &a.xmap, (k + u) * kGemmK, g.slot0, x, full(s));
+                            for (int x = 0; x < TX; ++x)
+                                for (int c = 0; c < g.n; c += a.box)
+                                    tc::load_3d(at + a_bytes + x * term + uint32_t(c) * kGemmK * 2, &a.xmap, (k + u) * kGemmK, g.slot0 + c, x, full(s));
                         }
                     }
                     __syncwarp();
@@ -546,11 +553,12 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
             const int tiles = gemm_tiles(a);
             // fp32: the tokens' first two terms are neighbours, and so are the sums of the large products
             // and of the small ones.
-            const uint32_t idesc = tc::instr(!kQuant, F32 ? 2 * a.bn : a.bn, false), ione = tc::instr(!kQuant, a.bn, false);
             int s = 0;
             uint32_t phase = 0, it = 0;
             bool alive = true;
             for (int t = tile0; t < tiles && alive; t += tile_step) {
+                const int n = a.n_experts ? gemm_tile(a, t).n : a.bn;
+                const uint32_t idesc = tc::instr(!kQuant, F32 ? 2 * n : n, false), ione = tc::instr(!kQuant, n, false);
                 for (int k = kb; k < ke; k += a.subs) {
                     const bool first = F32 ? k % kChunkSteps == 0 : k == kb;
                     const bool lastk = k + a.subs == ke || (F32 && (k + a.subs) % kChunkSteps == 0);
@@ -568,13 +576,13 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                             for (int j = 0; j < kGemmK / 16; ++j) {
                                 const bool add = j > 0 || u > 0 || !first;
                                 const uint64_t bj = db + 2 * j;                      // 32 bytes along K
-                                const uint32_t cross = acc + uint32_t(a.bn);
+                                const uint32_t cross = acc + uint32_t(n);
                                 if constexpr (kQuant) {                              // (fp32: the tokens' two terms at once)
                                     tc::mma_ts(acc, wt + 8 * j, bj, idesc, add);
                                     if constexpr (F32) tc::mma_ts(cross, wt + 32 + 8 * j, bj, ione, true);
                                 } else {
                                     tc::mma(acc, da + 2 * j, bj, idesc, add);
-                                    if constexpr (F32) tc::mma(cross, da + 2 * j, bj + 2 * (b_bytes >> 4), ione, true);
+                                    if constexpr (F32) tc::mma(cross, da + 2 * j, bj + 2 * (uint32_t(n) * kGemmK * 2 >> 4), ione, true);
                                 }
                             }
                         }

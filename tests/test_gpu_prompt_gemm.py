@@ -335,6 +335,26 @@ def test_few_experts_with_thousands_of_rows(fmt, act):
     assert qg.qg_device_status() == 0
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_experts_with_rows_around_sixteens(fmt, act):
+    """A tile takes its expert's rows in sixteens: one more, one less and just as many."""
+    rng = np.random.default_rng(34)
+    counts = [16, 1, 0, 15, 17, 31, 32, 33, 48, 49, 64, 100, 192, 193]
+    n_experts, n_out, n_in, off = len(counts), 130, 576, [0] + list(np.cumsum(counts))
+    c, W = packed(rng, fmt, n_experts * n_out, n_in)
+    x = tokens(rng, int(off[-1]), n_in, act)
+    y = torch.zeros(int(off[-1]), n_out, dtype=DT[act], device="cuda")
+    qg.qgemm_experts(fmt, W, n_experts, n_out, n_in, x, torch.tensor(off, dtype=torch.int32, device="cuda"), y,
+                     space(fmt, act, n_out, n_in, int(off[-1]), n_experts))
+    args = (fmt, c, n_experts, n_out, n_in, host(x), off)
+    v, S = PO.gemm_experts(*args), PO.gemm_experts(*args, product=PO.gemm_abs)
+    got = host(y)
+    for s in range(int(off[-1])):
+        assert (np.abs(got[s] - v[s]) <= tolerance(S[s], v[s], v[s], n_in, act, "none")).all()
+    assert qg.qg_device_status() == 0
+
+
 @pytest.mark.parametrize("off", [[0, 5, 3, 9], [-1, 2, 4, 6], [0, 4, 8, 11], [0, 2, 1, 0]])
 def test_offsets_that_are_no_offsets(off):
     rng = np.random.default_rng(13)
