@@ -99,6 +99,7 @@ struct GemmTile { int row0, w_row0, slot0, cols, n; };
 __device__ __forceinline__ int gemm_tiles(const GemmArgs& a) {
     return (a.n_experts ? a.tile_start[a.n_experts] : a.n_tiles) * a.m_tiles;
 }
+// (Whole warps.)
 __device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& a, int t) {
     GemmTile g;
     const int nt = t / a.m_tiles;
@@ -110,10 +111,13 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& a, int t) {
         g.n = a.bn;
         return g;
     }
-    int lo = 0, hi = a.n_experts;                        // the last expert with tile_start <= nt
+    int lo = 0, hi = a.n_experts;                        // the last expert with tile_start <= nt, 32 probes at a time
+    const int lane = int(threadIdx.x) & 31;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.tile_start[mid] <= nt) lo = mid; else hi = mid;
+        const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step;
+        const bool before = probe < hi && a.tile_start[probe] <= nt;
+        lo += __popc(__ballot_sync(tc::kFullMask, before)) * step;
+        hi = min(hi, lo + step);
     }
     g.slot0 = a.offsets[lo] + (nt - a.tile_start[lo]) * a.bn;
     g.cols = min(a.bn, a.offsets[lo + 1] - g.slot0);
