@@ -305,7 +305,8 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
     double least = 0;
     const double ksteps = double((n_in + kGemmK - 1) / kGemmK);
     // Experts' rows: spread like independent choices, and by half their mean for the experts' popularity
-    // (of 20,480 rows and 512 experts in tiles of 64 that makes 577 tiles; a routing had 568).
+    // (of 20,480 rows and 512 experts in tiles of 64 that makes 577 tiles; a routing had 568).  A larger tile
+    // costs no more where an expert has few rows, so it is the one that holds most experts' rows.
     const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
     for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
         // (An expert's tile has no more tokens than the expert.)

@@ -21,9 +21,12 @@
 // 128 tokens and more the way of the operands into the SM, about 60 bytes a clock: Q8_0, bf16, 10240 x 2560,
 // 8191 tokens 317 to 339 us, 1270 to 1355 TFLOP/s; bf16 weights, which need no decoding, 2560 x 6144, 8191
 // tokens 155 us, 1654 TFLOP/s.  fp32: its three products and the sums' moves to registers, 2047 tokens of
-// 2560 x 12288 with swiglu 332 us.  Experts with few rows each: their weights' way from memory (61 tokens of
-// 512 experts, 1.22 GB: 226 us, 5.4 TB/s), and with 40 rows each (2048 tokens, 421 us) decoding again.  A few tokens: two launches, the
-// first copies and the join.
+// 2560 x 12288 with swiglu 328 us.  Experts: their weights' way from memory (61 tokens of ten experts out of 512,
+// 1.22 GB: 221 us, 5.5 TB/s; 2048 tokens, 1.82 GB: 375 us, 4.8 TB/s), with 40 rows each and more beside the
+// decoding.  A few tokens: two launches, the first copies and the join.
+//
+// Tried and not kept: five decoding groups (10240 x 2560, 8191 tokens 320 -> 333 us); raw codes in rows of 128
+// bytes, two or four steps to a copy (320 -> 332, 2048 tokens' experts 404 -> 434).
 //
 // Numbers.  Quantized formats enter as fp16: a code times its fp16 scale has at most 19 bits.
 // bf16 activations, which a row's power of two moves into fp16's range exactly (but for values
