@@ -310,7 +310,7 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
     const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
     for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
         // (An expert's tile has no more tokens than the expert.)
-        const double step = step_ns(fmt, f32, n_experts ? std::min(bn, int(mean + spread) / 16 * 16 + 16) : bn);
+        const double step = step_ns(fmt, f32, n_experts && mean + spread < bn ? std::min(bn, int(mean + spread) / 16 * 16 + 16) : bn);
         for (int parts = 1; parts <= 8; ++parts) {
             double rounds;
             if (n_experts == 0) {
