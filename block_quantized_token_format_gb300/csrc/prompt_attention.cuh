@@ -31,7 +31,7 @@ struct PromptArgs {
     int asks;                      // the grid does not run at once: CTAs take on what others would
     float c;                       // |scale| log2 e
     uint32_t negate;               // of the instruction descriptor, where scale < 0
-    const float *qscale, *kscale, *vscale;       // fp32: powers of two, per row, per token that begins a key tile
+    const float *qscale, *kscale, *vscale;       // fp32: powers of two, [n_tok][n_heads], [n_tok][n_kv]
     unsigned int* status;
     uint32_t wait_limit, drain_limit, extra_tx;
 };
@@ -99,6 +99,10 @@ __device__ __forceinline__ PromptRow prompt_row(const PromptArgs& a, const Promp
 
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&y)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    const uint4 w = tc::lds128(a);
+    return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
 }
 // Halves of a word whose exponents (mask) are all ones get bit 15 and 31.
 template <uint32_t MASK> __device__ __forceinline__ uint32_t not_finite(uint32_t w) {

@@ -1,9 +1,13 @@
 // Causal attention of packed prompts, fp32: as the bf16 kernel, on two fp16 terms of every operand.
 //
-// stage_kernel writes, for every query row and for every key tile (64 tokens of one prompt) of a head,
-// the values times a power of two that takes the largest finite magnitude to [2^14, 2^15), as an fp16
-// value and another of what its rounding left: 22 bits below the largest of the row or tile.  A
-// score's factor is then one product per tile, and a tile's part of the output has one factor.
+// stage_kernel writes, for every query, key and value of a head, its values times a power of two that
+// takes their largest finite magnitude to [2^7, 2^15), as an fp16 value and another of what its
+// rounding left: 22 bits of the largest and, of smaller ones, what is above 2^-32 of it.  The powers are a
+// token's own: one for several tokens would take bits of a token for the size of another, which a row may
+// not see.  Their exponents are multiples of 8, so that tokens of similar size have the same one: a tile in which all
+// do, as the copying warp finds, has one factor for its scores and one for its part of the output.  In another
+// tile the scores' columns and P's are multiplied by the powers, relative to the largest that the
+// row sees, which gives the rows of both kinds the same bits.
 // Three products of 16-bit terms (small ones first: the tensor cores truncate what they add) make S;
 // P is 2^7 times the exponential, so that two terms of it reach 2^-31 of the row's largest; each
 // tile's P V goes to fresh accumulators and is added in fp32 registers.
@@ -29,6 +33,7 @@ constexpr int kTileKeys = 64, kStageRows = 4;
 template <int D> struct Shape {
     static constexpr int KT = kTileKeys, DV = D < 128 ? D : 128, HALVES = D / DV, STAGES = D == 256 ? 1 : 2;
     static constexpr int SIDES = D == 256 ? 1 : 2, WARPS = 4 * SIDES;        // lanes of a row, warps of the softmax
+    static constexpr int SLOTS = STAGES + 1;             // tiles whose powers of two wait in shared memory
     static constexpr int CH = D / 64, CV = DV / 64;
     static constexpr int Q_TERM = CH * 128 * 128, K_TERM = CH * KT * 128, V_TERM = CV * KT * 128;
     static constexpr int SMEM = 1024 + 2 * Q_TERM + 2 * STAGES * (K_TERM + V_TERM);
@@ -37,9 +42,10 @@ template <int D> struct Shape {
 
 __device__ __forceinline__ bool finite_of(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 __device__ __forceinline__ uint32_t finite_bits(float x) { return finite_of(x) ? __float_as_uint(x) & 0x7FFFFFFFu : 0u; }
-// The power of two that takes a magnitude (its bits) to [2^14, 2^15), and its inverse.
+// The power of two, its exponent a multiple of 8, that takes a magnitude (its bits) to [2^7, 2^15), and its
+// inverse; of zero the one of the smallest, which is nobody's largest.
 __device__ __forceinline__ float lift_of(uint32_t top, float& inverse) {
-    const int e = top ? min(14 - ilogbf(__uint_as_float(top)), 126) : 0;
+    const int e = top ? min((14 - ilogbf(__uint_as_float(top))) & ~7, 120) : 120;
     inverse = __int_as_float((127 - e) << 23);
     return __int_as_float((e + 127) << 23);
 }
@@ -56,107 +62,96 @@ __device__ __forceinline__ void terms4(float4 x, float lift, uint2& hi, uint2& l
     lo = make_uint2(__half_as_ushort(l[0]) | uint32_t(__half_as_ushort(l[1])) << 16, __half_as_ushort(l[2]) | uint32_t(__half_as_ushort(l[3])) << 16);
 }
 
+// One tensor's rows, [n_tok][heads][D].
+struct StageRows {
+    const float* x;
+    long long stride;
+    uint16_t* out;                               // [2 terms][n_tok][heads][D]
+    float* scale;                                // [n_tok][heads]
+    int heads;
+};
 struct StageArgs {
-    const float *q, *k, *v;
-    long long q_stride, k_stride, v_stride;
+    StageRows q, k, v;
     const int32_t* cu_seq;
-    uint16_t *q_out, *k_out, *v_out;             // [2 terms][n_tok][heads][D]
-    float *qscale, *kscale, *vscale;             // [n_tok][heads]
-    int n_tok, n_seq, n_heads, n_kv;
-    uint32_t tile_blocks;                        // key tiles times heads, for keys and for values
+    int n_tok, n_seq;
+    uint32_t q_blocks, kv_blocks;                // blocks of the queries, of the keys, of the values
 };
 
-template <int D> __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a) {
+// A warp four rows at a time.
+template <int D> __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_constant__ StageArgs a) {
     tc::grid_launch_dependents();
     tc::grid_wait();
     const int tid = int(threadIdx.x), lane = tid & 31;
-    if (blockIdx.x >= a.tile_blocks) {                   // queries, a warp four rows at a time
-        const long long row0 = ((long long)(blockIdx.x - a.tile_blocks) * (kStageThreads / 32) + (tid >> 5)) * kStageRows;
-        const long long from = (long long)a.cu_seq[0] * a.n_heads, to = min((long long)a.cu_seq[a.n_seq], (long long)a.n_tok) * a.n_heads;
-        constexpr int N = (D + 127) / 128;
-        float4 x[kStageRows][N];
-#pragma unroll
-        for (int k = 0; k < kStageRows; ++k) {
-            const long long row = row0 + k;
-            const long long tok = row / a.n_heads;
-            const float* const src = a.q + tok * a.q_stride + (row - tok * a.n_heads) * D;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = (i * 32 + lane) * 4;
-                x[k][i] = at < D && row >= from && row < to && row >= 0 ? *reinterpret_cast<const float4*>(src + at) : make_float4(0, 0, 0, 0);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kStageRows; ++k) {
-            const long long row = row0 + k;
-            if (row < from || row >= to || row < 0) continue;
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                top = max(max(max(top, finite_bits(x[k][i].x)), finite_bits(x[k][i].y)), max(finite_bits(x[k][i].z), finite_bits(x[k][i].w)));
-            top = __reduce_max_sync(tc::kFullMask, top);
-            float inverse;
-            const float lift = lift_of(top, inverse);
-            if (lane == 0) a.qscale[row] = inverse;
-            uint16_t* const out = a.q_out + row * D;
-            const size_t term = size_t(a.n_tok) * a.n_heads * D;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = (i * 32 + lane) * 4;
-                if (at >= D) break;
-                uint2 hi, lo;
-                terms4(x[k][i], lift, hi, lo);
-                *reinterpret_cast<uint2*>(out + at) = hi;
-                *reinterpret_cast<uint2*>(out + term + at) = lo;
-            }
-        }
-        return;
-    }
-    __shared__ uint32_t most[kStageThreads / 32];
     uint32_t b = blockIdx.x;
-    const bool values = b >= a.tile_blocks / 2;
-    if (values) b -= a.tile_blocks / 2;
-    const int slot = int(b / uint32_t(a.n_kv)), head = int(b - uint32_t(slot) * uint32_t(a.n_kv));
-    PromptItem it;
-    if (!prompt_piece(a.cu_seq, a.n_seq, a.n_tok, kTileKeys, slot, it)) return;
-    const long long tok0 = it.seq0 + it.t0, stride = values ? a.v_stride : a.k_stride;
-    const int rows = min(kTileKeys, it.len - it.t0);
-    const float* const src = (values ? a.v : a.k) + tok0 * stride + (long long)head * D;
-    constexpr int N = kTileKeys * D / 4 / kStageThreads, PER = D / 4;        // quads of a thread, of a row
-    float4 x[N];
-    uint32_t top = 0;
+    const bool queries = b < a.q_blocks;
+    if (!queries) b -= a.q_blocks;
+    const bool values = !queries && b >= a.kv_blocks;
+    if (values) b -= a.kv_blocks;
+    const StageRows& t = queries ? a.q : values ? a.v : a.k;
+    const long long row0 = ((long long)b * (kStageThreads / 32) + (tid >> 5)) * kStageRows;
+    const long long from = (long long)a.cu_seq[0] * t.heads, to = min((long long)a.cu_seq[a.n_seq], (long long)a.n_tok) * t.heads;
+    constexpr int N = (D + 127) / 128;
+    float4 x[kStageRows][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int n = i * kStageThreads + tid, row = n / PER;
-        x[i] = row < rows ? *reinterpret_cast<const float4*>(src + row * stride + (n % PER) * 4) : make_float4(0, 0, 0, 0);
-        top = max(max(max(top, finite_bits(x[i].x)), finite_bits(x[i].y)), max(finite_bits(x[i].z), finite_bits(x[i].w)));
-    }
-    top = __reduce_max_sync(tc::kFullMask, top);
-    if (lane == 0) most[tid >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < kStageThreads / 32; ++w) top = max(top, most[w]);
-    float inverse;
-    const float lift = lift_of(top, inverse);
-    if (tid == 0) (values ? a.vscale : a.kscale)[tok0 * a.n_kv + head] = inverse;
-    uint16_t* const out = values ? a.v_out : a.k_out;
-    const size_t term = size_t(a.n_tok) * a.n_kv * D;
+    for (int k = 0; k < kStageRows; ++k) {
+        const long long row = row0 + k;
+        const long long tok = row / t.heads;
+        const float* const src = t.x + tok * t.stride + (row - tok * t.heads) * D;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int n = i * kStageThreads + tid, row = n / PER;
-        if (row >= rows) break;
-        uint2 hi, lo;
-        terms4(x[i], lift, hi, lo);
-        uint16_t* const to = out + ((tok0 + row) * a.n_kv + head) * D + (n % PER) * 4;
-        *reinterpret_cast<uint2*>(to) = hi;
-        *reinterpret_cast<uint2*>(to + term) = lo;
+        for (int i = 0; i < N; ++i) {
+            const int at = (i * 32 + lane) * 4;
+            x[k][i] = at < D && row >= from && row < to && row >= 0 ? *reinterpret_cast<const float4*>(src + at) : make_float4(0, 0, 0, 0);
+        }
     }
+#pragma unroll
+    for (int k = 0; k < kStageRows; ++k) {
+        const long long row = row0 + k;
+        if (row < from || row >= to || row < 0) continue;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            top = max(max(max(top, finite_bits(x[k][i].x)), finite_bits(x[k][i].y)), max(finite_bits(x[k][i].z), finite_bits(x[k][i].w)));
+        top = __reduce_max_sync(tc::kFullMask, top);
+        float inverse;
+        const float lift = lift_of(top, inverse);
+        if (lane == 0) t.scale[row] = inverse;
+        uint16_t* const out = t.out + row * D;
+        const size_t term = size_t(a.n_tok) * t.heads * D;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = (i * 32 + lane) * 4;
+            if (at >= D) break;
+            uint2 hi, lo;
+            terms4(x[k][i], lift, hi, lo);
+            *reinterpret_cast<uint2*>(out + at) = hi;
+            *reinterpret_cast<uint2*>(out + term + at) = lo;
+        }
+    }
+}
+
+// The inverse of a power of two from 2^-120 to 2^120 (of zero: 2^127).
+__device__ __forceinline__ float inverse_of(float x) { return __int_as_float(0x7F000000 - __float_as_int(x)); }
+
+// The largest of a tile's powers (in shared memory) from `lo` to `hi`; 0: none.
+__device__ __forceinline__ float most_seen(uint32_t powers, int lo, int hi) {
+    float most = 0.0f;
+#pragma unroll 2
+    for (int i = 0; i < kTileKeys; i += 4) {
+        const float4 p = lds4(powers + i * 4);
+        if (i >= lo && i <= hi) most = fmaxf(most, p.x);
+        if (i + 1 >= lo && i + 1 <= hi) most = fmaxf(most, p.y);
+        if (i + 2 >= lo && i + 2 <= hi) most = fmaxf(most, p.z);
+        if (i + 3 >= lo && i + 3 <= hi) most = fmaxf(most, p.w);
+    }
+    return most;
 }
 
 template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1) prompt_f32_kernel(const __grid_constant__ PromptArgs a) {
     using S = Shape<D>;
     constexpr int KT = S::KT, CH = S::CH, CV = S::CV, DV = S::DV, SIDES = S::SIDES, kSoftWarps = S::WARPS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_mem[18];
+    __shared__ uint64_t bar_mem[18 + S::SLOTS];
+    __shared__ alignas(16) float scale_mem[S::SLOTS][2 * KT + 4];        // a tile's powers of keys and of values, their largest, whether they differ
     __shared__ uint32_t tmem_at, dead, odd;
     __shared__ float most_of[2][SIDES > 1 ? SIDES * 128 : 1], sum_of[SIDES > 1 ? SIDES * 128 : 1];      // the lanes' maxima, of even and odd tiles, and sums
 
@@ -183,6 +178,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
     auto p_full = [&](int s) { return bars + 96u + 8u * uint32_t(s); };
     auto o_full = [&](int s) { return bars + 112u + 8u * uint32_t(s); };
     auto o_empty = [&](int s) { return bars + 128u + 8u * uint32_t(s); };
+    auto scales_full = [&](int s) { return bars + 144u + 8u * uint32_t(s); };
     const tc::Waits wait{&dead, a.status, a.wait_limit};
 
     if (tid == 0) {
@@ -199,6 +195,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             mbar_init(o_full(s), 1);
             mbar_init(o_empty(s), kSoftWarps);
         }
+        for (int s = 0; s < S::SLOTS; ++s) mbar_init(scales_full(s), 1);
         mbar_fence_init();
     }
     if (warp == kSoftWarps + 1) tc::tmem_alloc(smem_addr(&tmem_at), S::COLS);
@@ -215,10 +212,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
         const int head = it.head * a.group + row % a.group;
         const long long token = it.seq0 + r.tok;
         const float c = r.there ? a.c * a.qscale[token * a.n_heads + head] : 0.0f;
-        const float* const ks = a.kscale + (long long)(it.seq0 + first) * a.n_kv + it.head;
-        const float* const vs = a.vscale + (long long)(it.seq0 + first) * a.n_kv + it.head;
-        const long long hop = (long long)KT * a.n_kv;
-        float k_next = ks[0], v_next = vs[0], v_mine = 0.0f;
+        float v_mine = 0.0f;                             // what the last tile's powers of values were divided by
         float top = -INFINITY, sum = 0.0f;               // the row's reference (log2 of an exponential), this lane's sum of P
         float o[D2];
 #pragma unroll
@@ -244,23 +238,40 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
         };
         for (int j = 0; j < tiles; ++j) {
             const int k0 = first + j * KT, sb = j & 1;
-            const float f = fmaxf(c * k_next, 1.17549435e-38f), v_this = v_next;
-            if (j + 1 < tiles) {
-                k_next = ks[(j + 1) * hop];
-                v_next = vs[(j + 1) * hop];
-            }
+            if (!wait(scales_full(j % S::SLOTS), j / S::SLOTS & 1)) { alive = false; break; }
+            const float* const scales = scale_mem[j % S::SLOTS];
+            const uint32_t powers = smem_addr(scales), k_pow = powers + uint32_t(side * K2 * 4), v_pow = k_pow + KT * 4;
+            float k_this = scales[2 * KT], v_this = scales[2 * KT + 1], v_inverse = 1.0f;
+            const bool edge = on_edge<KT>(a, it, k0), uneven = scales[2 * KT + 2] != 0.0f;
             if (!wait(s_full(sb), j >> 1 & 1)) { alive = false; break; }
             tc::fence_after();
             uint32_t x[K2];
             const uint32_t at = mine + uint32_t(sb * KT);
             tc::tmem_load(at + uint32_t(side * K2), x);
-            const bool edge = on_edge<KT>(a, it, k0);
+            const int hi = r.pos - k0 - side * K2, lo = r.low - k0 - side * K2;      // visible keys of this lane's
+            if (uneven) {
+                float k_inverse = 1.0f;
+                if (edge) {                                  // the powers are as they are: relative to the largest that is seen
+                    k_this = most_seen(powers, r.low - k0, r.pos - k0);
+                    v_this = most_seen(powers + KT * 4, r.low - k0, r.pos - k0);
+                    k_inverse = inverse_of(k_this);
+                    v_inverse = inverse_of(v_this);
+                }
+#pragma unroll
+                for (int i = 0; i < K2; i += 4) {
+                    const float4 p = lds4(k_pow + i * 4);
+                    x[i] = __float_as_uint(__uint_as_float(x[i]) * (p.x * k_inverse));
+                    x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * (p.y * k_inverse));
+                    x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * (p.z * k_inverse));
+                    x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * (p.w * k_inverse));
+                }
+            }
             if (edge) {
-                const int hi = r.pos - k0 - side * K2, lo = r.low - k0 - side * K2;
 #pragma unroll
                 for (int i = 0; i < K2; ++i)
                     if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
             }
+            const float f = fmaxf(c * k_this, 1.17549435e-38f);
             float most = largest<K2>(x);
             if constexpr (SIDES > 1) {
                 most_of[sb][side * 128 + row] = most;
@@ -278,16 +289,35 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             const unsigned long long f2 = pair_of(f), shift = pair_of(top == -INFINITY ? 0.0f : kLift - top);
             unsigned long long s2[2] = {};
             uint32_t lo16[K2 / 2];
-#pragma unroll
-            for (int i = 0; i < K2; i += 2) {
-                const float2 t = values_of(pair_fma(pair_of(x[i], x[i + 1]), f2, shift));
-                const float p0 = exp2_of(t.x), p1 = exp2_of(t.y);
-                s2[i / 2 & 1] = pair_add(s2[i / 2 & 1], pair_of(__float_as_uint(p0), __float_as_uint(p1)));
-                const __half2 h = __floats2half2_rn(p0, p1);
+            auto terms = [&](int i, float2 p) {
+                const __half2 h = __floats2half2_rn(p.x, p.y);
                 const float2 back = __half22float2(h);
-                const __half2 l = __floats2half2_rn(p0 - back.x, p1 - back.y);
+                const __half2 l = __floats2half2_rn(p.x - back.x, p.y - back.y);
                 x[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
                 lo16[i / 2] = *reinterpret_cast<const uint32_t*>(&l);
+            };
+            auto weights = [&](int i) {
+                const float2 t = values_of(pair_fma(pair_of(x[i], x[i + 1]), f2, shift));
+                const float2 p = make_float2(exp2_of(t.x), exp2_of(t.y));
+                s2[i / 2 & 1] = pair_add(s2[i / 2 & 1], pair_of(__float_as_uint(p.x), __float_as_uint(p.y)));
+                return p;
+            };
+            if (!uneven) {
+#pragma unroll
+                for (int i = 0; i < K2; i += 2) terms(i, weights(i));
+            } else {
+#pragma unroll
+                for (int i = 0; i < K2; i += 4) {
+                    const float4 w = lds4(v_pow + i * 4);
+                    float2 p = weights(i), q = weights(i + 2);
+                    // (A power of a token that the row does not see may be anything.)
+                    p.x = p.x == 0.0f ? 0.0f : p.x * (w.x * v_inverse);
+                    p.y = p.y == 0.0f ? 0.0f : p.y * (w.y * v_inverse);
+                    q.x = q.x == 0.0f ? 0.0f : q.x * (w.z * v_inverse);
+                    q.y = q.y == 0.0f ? 0.0f : q.y * (w.w * v_inverse);
+                    terms(i, p);
+                    terms(i + 2, q);
+                }
             }
             const float2 s = values_of(pair_add(s2[0], s2[1]));
             sum += s.x + s.y;
@@ -343,6 +373,41 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                     tc::load_3d(q_at + t * S::Q_TERM + n * 16384, &a.qmap, n * 64, it.head * a.group, t * a.n_tok + it.seq0 + it.t0, q_full);
         }
         __syncwarp();
+        // The powers of two of a tile's keys and values, two of each to a lane: read ahead, and put into a
+        // slot once the tile that had it has made its part of the output (which comes after v_empty).
+        float k_pow[2], v_pow[2];
+        auto fetch = [&](int t) {
+            if (t >= tiles) return;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int tok = it.seq0 + first + t * KT + n * 32 + lane;
+                const long long row = (long long)tok * a.n_kv + it.head;
+                k_pow[n] = tok < a.n_tok ? a.kscale[row] : 1.0f;
+                v_pow[n] = tok < a.n_tok ? a.vscale[row] : 1.0f;
+            }
+        };
+        auto hand_out = [&](int t) {
+            if (t >= tiles) return;
+            float* const to = scale_mem[t % S::SLOTS];
+            const uint32_t k_most = __reduce_max_sync(tc::kFullMask, max(__float_as_uint(k_pow[0]), __float_as_uint(k_pow[1])));
+            const uint32_t v_most = __reduce_max_sync(tc::kFullMask, max(__float_as_uint(v_pow[0]), __float_as_uint(v_pow[1])));
+            const bool even = __all_sync(tc::kFullMask, __float_as_uint(k_pow[0]) == k_most && __float_as_uint(k_pow[1]) == k_most &&
+                                                            __float_as_uint(v_pow[0]) == v_most && __float_as_uint(v_pow[1]) == v_most);
+            if (lane == 0) {
+                to[2 * KT] = __uint_as_float(k_most);
+                to[2 * KT + 1] = __uint_as_float(v_most);
+                to[2 * KT + 2] = even ? 0.0f : 1.0f;
+            }
+            if (!even) {
+                const bool edge = on_edge<KT>(a, it, first + t * KT);            // (there the rows see different ones)
+                const float k_inverse = edge ? 1.0f : inverse_of(__uint_as_float(k_most)), v_inverse = edge ? 1.0f : inverse_of(__uint_as_float(v_most));
+#pragma unroll
+                for (int n = 0; n < 2; ++n) to[n * 32 + lane] = k_pow[n] * k_inverse, to[KT + n * 32 + lane] = v_pow[n] * v_inverse;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(scales_full(t % S::SLOTS));
+        };
+        fetch(0);
         int j = 0;
         for (; j < tiles; ++j) {
             const int s = j % S::STAGES;
@@ -368,6 +433,12 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                         tc::load_3d(v_at + (2 * s + t) * S::V_TERM + n * KT * 128, &a.vmap, half * DV + n * 64, it.head, t * a.n_tok + key, v_full(s));
             }
             __syncwarp();
+            if (j == 0) {
+                hand_out(0);
+                fetch(1);
+            }
+            hand_out(j + 1);
+            fetch(j + 2);
         }
         if (dead) {                                      // copies still on their way end before the CTA does
             mbar_wait(q_full, 0, a.drain_limit);
@@ -450,19 +521,19 @@ PromptKernel prompt_f32(int D) { return D == 64 ? kernel<64>() : D == 128 ? kern
 
 qg_status prompt_stage(int D, const PromptStage& p, void* stream) {
     StageArgs a{};
-    a.q = p.q, a.k = p.k, a.v = p.v;
-    a.q_stride = p.q_stride, a.k_stride = p.k_stride, a.v_stride = p.v_stride;
+    a.q = {p.q, p.q_stride, p.q_out, p.qscale, p.n_heads};
+    a.k = {p.k, p.k_stride, p.k_out, p.kscale, p.n_kv};
+    a.v = {p.v, p.v_stride, p.v_out, p.vscale, p.n_kv};
     a.cu_seq = p.cu_seq;
-    a.q_out = p.q_out, a.k_out = p.k_out, a.v_out = p.v_out;
-    a.qscale = p.qscale, a.kscale = p.kscale, a.vscale = p.vscale;
-    a.n_tok = p.n_tok, a.n_seq = p.n_seq, a.n_heads = p.n_heads, a.n_kv = p.n_kv;
-    const int64_t tiles = 2 * (int64_t(p.n_tok) / kTileKeys + p.n_seq) * p.n_kv;
-    const int64_t per = kStageThreads / 32 * kStageRows, rows = (int64_t(p.n_tok) * p.n_heads + per - 1) / per;
-    if (tiles + rows > (int64_t(1) << 31) - 1) return QG_EUNSUPPORTED;
-    a.tile_blocks = uint32_t(tiles);
+    a.n_tok = p.n_tok, a.n_seq = p.n_seq;
+    const int64_t per = kStageThreads / 32 * kStageRows;
+    const int64_t q_blocks = (int64_t(p.n_tok) * p.n_heads + per - 1) / per, kv_blocks = (int64_t(p.n_tok) * p.n_kv + per - 1) / per;
+    if (q_blocks + 2 * kv_blocks > (int64_t(1) << 31) - 1) return QG_EUNSUPPORTED;
+    a.q_blocks = uint32_t(q_blocks);
+    a.kv_blocks = uint32_t(kv_blocks);
     void* params[] = {&a};
     const void* fn = D == 64 ? (const void*)&stage_kernel<64> : D == 128 ? (const void*)&stage_kernel<128> : (const void*)&stage_kernel<256>;
-    return launch_early(fn, int(tiles + rows), kStageThreads, 0, 1, params, stream);
+    return launch_early(fn, int(q_blocks + 2 * kv_blocks), kStageThreads, 0, 1, params, stream);
 }
 
 }  // namespace qg

@@ -551,9 +551,9 @@ qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_
  *                bytes, 16-byte aligned; it need not be cleared.  Calls that share one must be serialized.
  *   n_seq <= 16384; n_heads a multiple of n_kv_heads, at most 128 to one key/value head.
  * bf16: products are exact, sums fp32, probabilities rounded to bf16 (their sum and lse are not).  fp32:
- * queries, keys and values as two fp16 terms, 22 bits below the largest of the query, and of the head's keys or
- * values in a tile of 64 tokens; probabilities as two terms, down to 2^-31 of the row's largest.  Outputs are
- * the same on every run, and do not depend on the other prompts of the call.
+ * a token's query, key or value of a head as two fp16 terms, 22 bits of its largest element and nothing below 2^-32 of
+ * it; probabilities as two terms, down to 2^-31 of the row's largest, times the largest value that the row sees among 64
+ * tokens.  Outputs are the same on every run, and do not depend on the other prompts of the call.
  * A masked key or value (of a later token, beyond the window, of another prompt) has no effect whatever
  * it holds; a visible one that is not finite makes the outputs that see it not finite.
  * Errors: QG_EINVAL, QG_EALIGN, QG_EWORKSPACE, QG_EUNSUPPORTED, QG_ECUDA. */
