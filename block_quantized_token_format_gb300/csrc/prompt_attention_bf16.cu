@@ -199,7 +199,7 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
             if (alive) {
                 tc::fence_after();
                 sum = sum_of_lanes<SIDES>(sum_of, row);
-                const float inv = 1.0f / sum;
+                const float inv = 1.0f / sum;                // (all scores -infinity: the sum is 0, the average NaN)
                 const PromptItem it = item_mem[n % kItems];
                 const PromptRow r = prompt_row(a, it, row);
                 const long long token = it.seq0 + r.tok;
@@ -218,14 +218,14 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                     }
                     float y[32];
 #pragma unroll
-                    for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : __uint_as_float(o[n]) * inv;
+                    for (int n = 0; n < 32; ++n) y[n] = __uint_as_float(o[n]) * inv;
                     if (look && r.there) add_not_finite<KT, __nv_bfloat16>(a, it, r, half * D2 + d, D, y);      // visible values that were left out
                     uint32_t w[16];
 #pragma unroll
                     for (int n = 0; n < 16; ++n) w[n] = pack_bf16(y[2 * n], y[2 * n + 1]);
                     store_rows(to + d, r.there, w, lane);
                 }
-                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : top * a.c * kLn2 + logf(sum);
+                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = top * a.c * kLn2 + logf(sum);
             }
             give_back(n);
             ++n;

@@ -114,6 +114,11 @@ template <int D> __global__ void __launch_bounds__(kStageThreads) stage_kernel(c
         top = __reduce_max_sync(tc::kFullMask, top);
         float inverse;
         const float lift = lift_of(top, inverse);
+        bool fine = true;
+#pragma unroll
+        for (int i = 0; i < N; ++i) fine = fine && finite_of(x[k][i].x) && finite_of(x[k][i].y) && finite_of(x[k][i].z) && finite_of(x[k][i].w);
+        // Two terms of a query or key that is not finite are no score: its power makes one that is NaN.
+        if (!__all_sync(tc::kFullMask, fine) && !values) inverse = __int_as_float(0x7FC00000);
         if (lane == 0) t.scale[row] = inverse;
         uint16_t* const out = t.out + row * D;
         const size_t term = size_t(a.n_tok) * t.heads * D;
@@ -271,7 +276,8 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                 for (int i = 0; i < K2; ++i)
                     if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
             }
-            const float f = fmaxf(c * k_this, 1.17549435e-38f);
+            float f = c * k_this;
+            if (f < 1.17549435e-38f) f = 1.17549435e-38f;        // (NaN stays)
             float most = largest<K2>(x);
             if constexpr (SIDES > 1) {
                 most_of[sb][side * 128 + row] = most;
@@ -344,7 +350,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
         if constexpr (SIDES > 1) sum_of[side * 128 + row] = sum;
         if (alive && gather(tiles - 1) && (SIDES == 1 || meet<SIDES>(rows, dead))) {
             if constexpr (SIDES > 1) sum = sum_of_lanes<SIDES>(sum_of, row);
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = 1.0f / sum;
             const bool look = odd != 0;
             float* const to = static_cast<float*>(a.out) + token * a.out_stride + (long long)head * D + half * DV + side * D2;
             if (r.there) {
@@ -352,12 +358,12 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                 for (int i = 0; i < D2; i += 32) {
                     float y[32];
 #pragma unroll
-                    for (int n = 0; n < 32; ++n) y[n] = sum == 0.0f ? 0.0f : o[i + n] * inv;
+                    for (int n = 0; n < 32; ++n) y[n] = o[i + n] * inv;
                     if (look) add_not_finite<KT, float>(a, it, r, half * DV + side * D2 + i, D, y);      // visible values that were left out
 #pragma unroll
                     for (int n = 0; n < 32; n += 4) *reinterpret_cast<float4*>(to + i + n) = make_float4(y[n], y[n + 1], y[n + 2], y[n + 3]);
                 }
-                if (a.lse && half == 0 && side == 0) a.lse[token * a.n_heads + head] = sum == 0.0f ? -INFINITY : (top - kLift) * kLn2 + logf(sum);
+                if (a.lse && half == 0 && side == 0) a.lse[token * a.n_heads + head] = (top - kLift) * kLn2 + logf(sum);
             }
         }
         if (SIDES > 1 && dead) leave<SIDES>(rows);
@@ -391,7 +397,8 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             float* const to = scale_mem[t % S::SLOTS];
             const uint32_t k_most = __reduce_max_sync(tc::kFullMask, max(__float_as_uint(k_pow[0]), __float_as_uint(k_pow[1])));
             const uint32_t v_most = __reduce_max_sync(tc::kFullMask, max(__float_as_uint(v_pow[0]), __float_as_uint(v_pow[1])));
-            const bool even = __all_sync(tc::kFullMask, __float_as_uint(k_pow[0]) == k_most && __float_as_uint(k_pow[1]) == k_most &&
+            const bool even = k_most < 0x7F800000u &&            // (NaN is for the rows that see it)
+                              __all_sync(tc::kFullMask, __float_as_uint(k_pow[0]) == k_most && __float_as_uint(k_pow[1]) == k_most &&
                                                             __float_as_uint(v_pow[0]) == v_most && __float_as_uint(v_pow[1]) == v_most);
             if (lane == 0) {
                 to[2 * KT] = __uint_as_float(k_most);

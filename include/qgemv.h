@@ -555,7 +555,9 @@ qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_
  * it; probabilities as two terms, down to 2^-31 of the row's largest, times the largest value that the row sees among 64
  * tokens.  Outputs are the same on every run, and do not depend on the other prompts of the call.
  * A masked key or value (of a later token, beyond the window, of another prompt) has no effect whatever
- * it holds; a visible one that is not finite makes the outputs that see it not finite.
+ * it holds; a visible value that is not finite makes the outputs that see it not finite.  A visible key, or a query, that is
+ * not: bf16 as the formula has it (a score of -infinity has weight 0, a row of no others is NaN with lse -infinity; one
+ * of +infinity or NaN leaves nothing finite); fp32: NaN.
  * Errors: QG_EINVAL, QG_EALIGN, QG_EWORKSPACE, QG_EUNSUPPORTED, QG_ECUDA. */
 size_t    qg_prompt_attention_workspace_bytes(qg_act act, int64_t n_tok, int n_heads, int n_kv_heads, int head_dim);
 qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

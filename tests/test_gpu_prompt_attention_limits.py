@@ -1,4 +1,5 @@
-"""qg_prompt_attention where values leave the ordinary range: large finite values that a row does not see.
+"""qg_prompt_attention where values leave the ordinary range: large finite values that a row does not
+see, scores that are not finite.
 
 Tolerances (derived from the arithmetic, before any run), with A = |scale| sum |q| |k| of a score, the
 largest of those that the row sees, V = sum p |v| and M the largest |v| that the row sees in the head:
@@ -129,3 +130,41 @@ def test_values_that_grow_along_a_prompt():
     v *= torch.tensor(1e-10 * 1.3 ** np.arange(300), device="cuda").float()[:, None, None]
     out, lse = run(q, k, v, [0, 300], 0.1)
     check(q, k, v, [0, 300], 0.1, 0, out, lse)
+
+
+# ----------------------------------------------------------------- scores that are not finite
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_keys_that_are_not_finite_bf16(D):
+    """A score of -infinity has weight 0; a row of nothing else has no average; one of +infinity or NaN none either."""
+    rng = np.random.default_rng(45)
+    q, k, v = inputs(rng, 200, 2, 1, D, "bf16")
+    q[:, 0, 5], q[:, 1, 5] = 1.0, -1.0
+    q[:100, :, 6] = 1.0
+    k[0, 0, 5] = float("-inf")                                       # head 0: -infinity, head 1: +infinity
+    k[100, 0, 6] = float("nan")
+    out, lse = run(q, k, v, [0, 70, 200], 0.1)
+    o, l = host(out), host(lse)
+    assert np.isnan(o[0, 0]).all() and l[0, 0] == -np.inf
+    assert np.isnan(o[:70, 1]).all() and not np.isfinite(l[:70, 1]).any()
+    assert np.isnan(o[100:]).all() and np.isnan(l[100:]).all()
+    k[0, 0, 5] = -3e38                                               # finite, and as little weight
+    want, wl = run(q, k, v, [0, 70, 200], 0.1)
+    assert np.array_equal(o[1:70, 0], host(want)[1:70, 0]) and np.array_equal(l[1:70, 0], host(wl)[1:70, 0])
+    assert np.isfinite(o[70:100]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("-inf"), float("inf"), float("nan")])
+def test_keys_and_queries_that_are_not_finite_fp32(D, bad):
+    """The rows that see one are NaN, the others keep every bit."""
+    rng = np.random.default_rng(46)
+    q, k, v = inputs(rng, 300, 4, 2, D, "f32")
+    clean, lse_clean = run(q, k, v, [0, 70, 300], 0.1)
+    k[0, 0, 5] = k[150, 1, 6] = q[290, 0, 7] = bad
+    out, lse = run(q, k, v, [0, 70, 300], 0.1)
+    nan = np.zeros((300, 4), bool)
+    nan[:70, :2] = nan[150:, 2:] = nan[290, 0] = True
+    o, l = host(out), host(lse)
+    assert np.isnan(o[nan]).all() and np.isnan(l[nan]).all()
+    assert np.array_equal(o[~nan], host(clean)[~nan]) and np.array_equal(l[~nan], host(lse_clean)[~nan])
