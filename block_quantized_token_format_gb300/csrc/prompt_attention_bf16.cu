@@ -5,7 +5,8 @@
 // half of the output); one warp copies keys and values, one issues
 // the products.  S (fp32) and then P (bf16, over S) lie in tensor memory, P being the second
 // product's operand there, and O is summed there.  A row's reference is raised, and O scaled,
-// only where a tile's maximum is more than 2^8 above it: then rarely after the first tiles.
+// only where a tile's maximum is more than 2^8 above it: then rarely after the first tiles.  P is 2^-8 times the
+// exponential, so that it stays below 1 and O below the sum of the values: they may be as large as that allows.
 // CTAs stay and take one item after another, asking for the next that no CTA has begun: the next one's queries and first keys are copied, and its
 // first S is made, while the last one's output is written.  Heads of 64 and 128 take 256 columns of
 // tensor memory and at most 97 KB, so that two CTAs share an SM and the one's softmax runs beside the
@@ -32,7 +33,7 @@ namespace qg {
 namespace {
 
 constexpr int kItems = 4;          // that the copying warp may be ahead
-constexpr float kSlack = 8.0f;     // log2: P is at most 2^8
+constexpr float kSlack = 8.0f;     // log2: how far scores may pass the reference; P is 2^-8 times the exponential, at most 1
 
 template <int D> struct Shape {
     static constexpr int KT = 64, STAGES = 2, SB = 2;
@@ -172,7 +173,7 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                         tc::tmem_store16(o_mine + i, o);
                     }
                 }
-                const unsigned long long c2 = pair_of(a.c), shift = pair_of(top == -INFINITY ? 0.0f : -top * a.c);
+                const unsigned long long c2 = pair_of(a.c), shift = pair_of(top == -INFINITY ? 0.0f : -top * a.c - kSlack);
                 unsigned long long s2[2] = {};
 #pragma unroll
                 for (int i = 0; i < K2; i += 2) {
@@ -225,7 +226,7 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                     for (int n = 0; n < 16; ++n) w[n] = pack_bf16(y[2 * n], y[2 * n + 1]);
                     store_rows(to + d, r.there, w, lane);
                 }
-                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = top * a.c * kLn2 + logf(sum);
+                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = (top * a.c + kSlack) * kLn2 + logf(sum);
             }
             give_back(n);
             ++n;

@@ -10,7 +10,8 @@
 // row sees, which gives the rows of both kinds the same bits.
 // Three products of 16-bit terms (small ones first: the tensor cores truncate what they add) make S;
 // P is 2^7 times the exponential, so that two terms of it reach 2^-31 of the row's largest; each
-// tile's P V goes to fresh accumulators and is added in fp32 registers.
+// tile's P V goes to fresh accumulators and is added in fp32 registers, in units of the largest power of values that the
+// row has met, so that outputs next to the largest fp32 number do not pass it on the way.
 //
 // One CTA is 128 rows, two lanes a row (each half of a tile's keys and half of the output; one with heads
 // of 256, whose operands leave no shared memory for the lanes' maxima); S and the tiles' P V have two buffers each, so that the next
@@ -217,7 +218,8 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
         const int head = it.head * a.group + row % a.group;
         const long long token = it.seq0 + r.tok;
         const float c = r.there ? a.c * a.qscale[token * a.n_heads + head] : 0.0f;
-        float v_mine = 0.0f;                             // what the last tile's powers of values were divided by
+        // The output is in units of the largest power of values so far: v_mine is the last tile's in these.
+        float v_mine = 0.0f, v_unit = 0.0f;
         float top = -INFINITY, sum = 0.0f;               // the row's reference (log2 of an exponential), this lane's sum of P
         float o[D2];
 #pragma unroll
@@ -241,6 +243,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             if (lane == 0) mbar_arrive(o_empty(ob));
             return true;
         };
+
         for (int j = 0; j < tiles; ++j) {
             const int k0 = first + j * KT, sb = j & 1;
             if (!wait(scales_full(j % S::SLOTS), j / S::SLOTS & 1)) { alive = false; break; }
@@ -292,6 +295,11 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                 top = most;
                 sum *= factor;
             }
+            const bool grows = v_this > v_unit;
+            if (grows) {
+                factor *= v_unit * inverse_of(v_this);
+                v_unit = v_this;
+            }
             const unsigned long long f2 = pair_of(f), shift = pair_of(top == -INFINITY ? 0.0f : kLift - top);
             unsigned long long s2[2] = {};
             uint32_t lo16[K2 / 2];
@@ -340,12 +348,12 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
             if (lane == 0) mbar_arrive(p_full(sb));
             if (j > 0) {
                 if (!gather(j - 1)) { alive = false; break; }
-                if (__any_sync(tc::kFullMask, raise)) {
+                if (__any_sync(tc::kFullMask, raise || grows)) {
 #pragma unroll
                     for (int i = 0; i < D2; ++i) o[i] *= factor;
                 }
             }
-            v_mine = v_this;
+            v_mine = v_this * inverse_of(v_unit);
         }
         if constexpr (SIDES > 1) sum_of[side * 128 + row] = sum;
         if (alive && gather(tiles - 1) && (SIDES == 1 || meet<SIDES>(rows, dead))) {
@@ -358,7 +366,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                 for (int i = 0; i < D2; i += 32) {
                     float y[32];
 #pragma unroll
-                    for (int n = 0; n < 32; ++n) y[n] = o[i + n] * inv;
+                    for (int n = 0; n < 32; ++n) y[n] = o[i + n] * inv * v_unit;
                     if (look) add_not_finite<KT, float>(a, it, r, half * DV + side * D2 + i, D, y);      // visible values that were left out
 #pragma unroll
                     for (int n = 0; n < 32; n += 4) *reinterpret_cast<float4*>(to + i + n) = make_float4(y[n], y[n + 1], y[n + 2], y[n + 3]);

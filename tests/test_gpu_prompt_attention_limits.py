@@ -1,5 +1,5 @@
 """qg_prompt_attention where values leave the ordinary range: large finite values that a row does not
-see, scores that are not finite.
+see, scores that are not finite, values next to the largest number.
 
 Tolerances (derived from the arithmetic, before any run), with A = |scale| sum |q| |k| of a score, the
 largest of those that the row sees, V = sum p |v| and M the largest |v| that the row sees in the head:
@@ -168,3 +168,34 @@ def test_keys_and_queries_that_are_not_finite_fp32(D, bad):
     o, l = host(out), host(lse)
     assert np.isnan(o[nan]).all() and np.isnan(l[nan]).all()
     assert np.array_equal(o[~nan], host(clean)[~nan]) and np.array_equal(l[~nan], host(lse_clean)[~nan])
+
+
+# ------------------------------------------------------------------------- the range's end
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_fp32_values_next_to_the_largest(D, n):
+    """Outputs are averages: they are finite where the values are."""
+    rng = np.random.default_rng(44)
+    q, k, v = inputs(rng, n, 2, 1, D, "f32")
+    v = torch.tensor(rng.uniform(0.5, 0.99, (n, 1, D)) * 2.0 ** 128, dtype=torch.float32, device="cuda")
+    q[:, 1] = 0.0                                                    # even weights
+    out, lse = run(q, k, v, [0, n], 0.1)
+    assert torch.isfinite(out).all()
+    check(q, k, v, [0, n], 0.1, 0, out, lse)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_that_rise_under_large_values(act, D):
+    """Weights grow 2^7 from the first 64 keys to the next: sums of weights times values stay within what the
+    weights' largest being 1 allows."""
+    n = 128
+    q = torch.zeros(n, 1, D, dtype=DT[act], device="cuda")
+    k, v = torch.zeros_like(q), torch.full_like(q, 1e36)
+    q[:, 0, 0] = 7.0
+    k[64:, 0, 0] = 1.0
+    scale = float(np.log(2.0))
+    out, lse = run(q, k, v, [0, n], scale)
+    assert torch.isfinite(out).all()
+    check(q, k, v, [0, n], scale, 0, out, lse)
