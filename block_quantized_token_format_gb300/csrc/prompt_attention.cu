@@ -127,8 +127,9 @@ qg_status qg_prompt_attention(qg_act act, const void* q, int64_t q_stride, const
     a.tokens = tokens;
     a.window = window;
     a.asks = items > int64_t(resident) * sms;
-    // (Zero: the smallest factor instead, which leaves masked scores at -infinity.)
-    a.c = std::max(std::fabs(scale) * kLog2e, FLT_MIN);
+    // (bf16, zero: the smallest number instead, which leaves masked scores at -infinity and others, the
+    // largest fp32 number among them, below 2^-21.)
+    a.c = std::max(std::fabs(scale) * kLog2e, f32 ? 0.0f : FLT_TRUE_MIN);
     a.negate = scale < 0.0f ? 1u << 13 : 0u;
     a.wait_limit = wait_limit();
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);

@@ -133,7 +133,7 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                 inside_lo = a.window > 0 ? (max(0, last - a.window + 1 - it.first) + KT - 1) / KT : 0;
                 inside_hi = (it.t0 - it.first + 1) / KT;             // (exclusive)
             }
-            float top = -INFINITY, sum = 0.0f;           // the row's reference (a score), this lane's sum of P
+            float top = -INFINITY, sum = 0.0f;           // the row's reference (log2 of an exponential), this lane's sum of P
             for (int j = 0; j < tiles; ++j, ++g) {
                 const int sb = int(g % S::SB);
                 if (!wait(s_full(sb), g / S::SB & 1)) { alive = false; break; }
@@ -152,11 +152,11 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                 float* const shared_most = most_of[g & 1];
                 shared_most[half * 128 + row] = most;
                 if (!meet<SIDES>(rows, dead)) { alive = false; break; }      // (all lanes have their S: P may lie over it now)
-                most = largest_of<SIDES>(shared_most, row);
-                const bool raise = (most - top) * a.c > kSlack || (top == -INFINITY && most > -INFINITY);
+                most = largest_of<SIDES>(shared_most, row) * a.c;
+                const bool raise = most - top > kSlack || (top == -INFINITY && most > -INFINITY);
                 float factor = 1.0f;
                 if (raise) {
-                    factor = top == -INFINITY ? 0.0f : exp2_of((top - most) * a.c);
+                    factor = top == -INFINITY ? 0.0f : exp2_of(top - most);
                     top = most;
                     sum *= factor;
                 }
@@ -173,7 +173,7 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                         tc::tmem_store16(o_mine + i, o);
                     }
                 }
-                const unsigned long long c2 = pair_of(a.c), shift = pair_of(top == -INFINITY ? 0.0f : -top * a.c - kSlack);
+                const unsigned long long c2 = pair_of(a.c), shift = pair_of(top == -INFINITY ? 0.0f : -top - kSlack);
                 unsigned long long s2[2] = {};
 #pragma unroll
                 for (int i = 0; i < K2; i += 2) {
@@ -226,7 +226,7 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                     for (int n = 0; n < 16; ++n) w[n] = pack_bf16(y[2 * n], y[2 * n + 1]);
                     store_rows(to + d, r.there, w, lane);
                 }
-                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = (top * a.c + kSlack) * kLn2 + logf(sum);
+                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = (top + kSlack) * kLn2 + logf(sum);
             }
             give_back(n);
             ++n;

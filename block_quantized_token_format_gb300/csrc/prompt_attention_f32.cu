@@ -280,7 +280,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
                     if (i > hi || i < lo) x[i] = 0xFF800000u;        // -infinity
             }
             float f = c * k_this;
-            if (f < 1.17549435e-38f) f = 1.17549435e-38f;        // (NaN stays)
+            if (f < 1e-45f) f = 1e-45f;                          // (NaN stays; zero would make NaN of -infinity)
             float most = largest<K2>(x);
             if constexpr (SIDES > 1) {
                 most_of[sb][side * 128 + row] = most;

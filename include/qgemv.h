@@ -553,7 +553,8 @@ qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_
  * bf16: products are exact, sums fp32, probabilities rounded to bf16 (their sum and lse are not).  fp32:
  * a token's query, key or value of a head as two fp16 terms, 22 bits of its largest element and nothing below 2^-32 of
  * it; probabilities as two terms, down to 2^-31 of the row's largest, times the largest value that the row sees among 64
- * tokens.  Values may be any finite ones; in bf16 a row's largest times the number of its keys is below 2^128.  Outputs are the same on every run, and do not depend on the other prompts of the call.
+ * tokens.  Values may be any finite ones; in bf16 a row's largest times the number of its keys is below 2^128.
+ * Outputs are the same on every run, and do not depend on the other prompts of the call.
  * A masked key or value (of a later token, beyond the window, of another prompt) has no effect whatever
  * it holds; a visible value that is not finite makes the outputs that see it not finite.  A visible key, or a query, that is
  * not: bf16 as the formula has it (a score of -infinity has weight 0, a row of no others is NaN with lse -infinity; one

@@ -1,5 +1,5 @@
 """qg_prompt_attention where values leave the ordinary range: large finite values that a row does not
-see, scores that are not finite, values next to the largest number.
+see, scores that are not finite, values next to the largest number, a factor of zero.
 
 Tolerances (derived from the arithmetic, before any run), with A = |scale| sum |q| |k| of a score, the
 largest of those that the row sees, V = sum p |v| and M the largest |v| that the row sees in the head:
@@ -199,3 +199,20 @@ def test_scores_that_rise_under_large_values(act, D):
     out, lse = run(q, k, v, [0, n], scale)
     assert torch.isfinite(out).all()
     check(q, k, v, [0, n], scale, 0, out, lse)
+
+
+# ------------------------------------------------------------------------------ factors
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_factor_of_zero(act, D):
+    """Every score is zero, however large the products are: averages of the values."""
+    rng = np.random.default_rng(47)
+    q, k, v = inputs(rng, 200, 2, 1, D, act)
+    q[:], k[:] = 0.0, 0.0
+    big = 1.6e19 if act == "bf16" else 1e35                          # (bf16: the products are fp32 numbers)
+    q[:, :, 0] = big
+    k[:, 0, 0] = torch.tensor(rng.choice([-big, big], 200), device="cuda").to(DT[act])
+    out, lse = run(q, k, v, [0, 200], 0.0)
+    assert np.abs(host(lse) - np.log(np.arange(1, 201))[:, None]).max() <= 2.0 ** -18
+    check(q, k, v, [0, 200], 0.0, 0, out, lse)
