@@ -10,18 +10,18 @@
 
 namespace qg {
 
-const void* qgemm_lookup_fmt0(bool);
-const void* qgemm_lookup_fmt1(bool);
-const void* qgemm_lookup_fmt2(bool);
-const void* qgemm_lookup_fmt3(bool);
-const void* qgemm_lookup_fmt4(bool);
-const void* qgemm_lookup(int fmt, bool f32) {
+const void* qgemm_lookup_fmt0(bool, bool);
+const void* qgemm_lookup_fmt1(bool, bool);
+const void* qgemm_lookup_fmt2(bool, bool);
+const void* qgemm_lookup_fmt3(bool, bool);
+const void* qgemm_lookup_fmt4(bool, bool);
+const void* qgemm_lookup(int fmt, bool f32, bool chains) {
     switch (fmt) {
-        case 0: return qgemm_lookup_fmt0(f32);
-        case 1: return qgemm_lookup_fmt1(f32);
-        case 2: return qgemm_lookup_fmt2(f32);
-        case 3: return qgemm_lookup_fmt3(f32);
-        default: return qgemm_lookup_fmt4(f32);
+        case 0: return qgemm_lookup_fmt0(f32, chains);
+        case 1: return qgemm_lookup_fmt1(f32, chains);
+        case 2: return qgemm_lookup_fmt2(f32, chains);
+        case 3: return qgemm_lookup_fmt3(f32, chains);
+        default: return qgemm_lookup_fmt4(f32, chains);
     }
 }
 
@@ -267,7 +267,7 @@ int clusters_at_once(const void* fn, int dev, int threads, size_t smem, int part
 
 // A kernel's shared memory for tiles of bn tokens.
 struct Geometry { int subs, stages, raws; size_t smem; };
-Geometry geometry(int fmt, bool f32, int bn, int optin) {
+Geometry geometry(int fmt, bool f32, int bn, int sets, int optin) {
     // Stages of one step of K, or of two where they are small (a stage's waits and bookkeeping take
     // about 200 clocks of the warp that issues the products): four or three of them; the rest of
     // shared memory holds raw codes on their way, which is what few tokens to a tile need.  Their slots
@@ -278,11 +278,11 @@ Geometry geometry(int fmt, bool f32, int bn, int optin) {
     const size_t raw = size_t(kGemmRows) * size_t(raw_codes(fmt)), scales = size_t(kGemmRows) * kScaleSlots * size_t(raw_scales(fmt));
     const size_t room = size_t(optin) - kStaticSmemReserve - 1024 - scales;
     Geometry g{};
-    g.subs = bn <= (quant ? (f32 ? 64 : 160) : f32 ? 0 : 128) ? 2 : 1;
+    g.subs = bn <= (quant ? (f32 ? 64 : sets == 3 ? 96 : 160) : f32 ? 0 : 128) ? 2 : 1;
     const size_t stage = size_t(g.subs) * ((quant ? 0 : size_t(kOperandA)) + size_t(terms_x(fmt, f32)) * size_t(bn) * kGemmK * 2);
     auto slots = [&](int stages) { return int(std::min<size_t>(kMostRaws, (room - size_t(stages) * stage) / std::max<size_t>(raw, 1))) / std::max(groups, 1) * groups; };
     g.stages = int(std::min<size_t>(quant ? (g.subs == 2 ? 3 : 4) : 8, (room - size_t(groups) * raw) / stage));
-    if (quant) g.stages = std::min(g.stages, (512 - 2 * bn * (f32 ? 2 : 1)) / (g.subs * w_columns(fmt, f32)));
+    if (quant) g.stages = std::min(g.stages, (512 - sets * bn * (f32 ? 2 : 1)) / (g.subs * w_columns(fmt, f32)));
     g.raws = quant ? slots(g.stages) : 0;
     g.smem = 1024 + scales + size_t(g.raws) * raw + size_t(g.stages) * stage;
     return g;
@@ -308,7 +308,7 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
     // (of 20,480 rows and 512 experts in tiles of 64 that makes 577 tiles; a routing had 568).  A larger tile
     // costs no more where an expert has few rows, so it is the one that holds most experts' rows.
     const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
-    for (int bn = 32; bn <= gemm_most_tokens(fmt, f32); bn += 16) {
+    for (int bn = 32; bn <= gemm_most_tokens(fmt, f32, gemm_sets(f32, int(n_in))); bn += 16) {
         // (An expert's tile has no more tokens than the expert.)
         const double step = step_ns(fmt, f32, n_experts && mean + spread < bn ? std::min(bn, int(mean + spread) / 16 * 16 + 16) : bn);
         for (int parts = 1; parts <= 8; ++parts) {
@@ -375,10 +375,11 @@ qg_status launch_gemm(const GemmCall& c) {
     qg_status st = device_info(&dev, &sms, &optin, &status);
     if (st != QG_OK) return st;
     const int64_t m_tiles = (c.n_out + kGemmRows - 1) / kGemmRows;
-    const void* const fn = qgemm_lookup(c.fmt, f32);
+    const int sets = gemm_sets(f32, int(c.n_in));
+    const void* const fn = qgemm_lookup(c.fmt, f32, sets == 3);
     const int threads = gemm_threads(c.fmt, f32);
     const Shape shape = tile_shape(c.fmt, f32, c.n_in, m_tiles, c.n_slots, c.n_experts, sms, [&](int parts) {
-        const size_t smem = geometry(c.fmt, f32, 32, optin).smem;
+        const size_t smem = geometry(c.fmt, f32, 32, sets, optin).smem;
         return blocks_per_sm(fn, dev, optin, threads, smem) < 1 ? 0 : clusters_at_once(fn, dev, threads, smem, parts);
     });
     const int bn = shape.bn;
@@ -409,7 +410,7 @@ qg_status launch_gemm(const GemmCall& c) {
     a.wait_limit = wait_limit();
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.extra_tx = test_extra_tx();
-    const Geometry geo = geometry(c.fmt, f32, bn, optin);
+    const Geometry geo = geometry(c.fmt, f32, bn, sets, optin);
     const int groups = decode_groups(c.fmt, f32);
     a.subs = geo.subs;
     a.stages = geo.stages;

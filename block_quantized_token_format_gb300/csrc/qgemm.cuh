@@ -57,6 +57,10 @@ constexpr int kDrainWarps = 8;
 __host__ __device__ constexpr int decode_groups(int fmt, bool f32) { return fmt == QG_BF16 ? 0 : f32 ? 2 : 4; }
 __host__ __device__ constexpr int gemm_threads(int fmt, bool f32) { return 32 * (kDrainWarps + 4 * decode_groups(fmt, f32) + 3); }
 constexpr int kChunkSteps = 4;               // fp32: steps of K between moves to registers
+// bf16: rows of W of more than kChainValues are summed in chains of kChainSteps steps of K (512 additions on the
+// tensor cores, which cut off a bit: 2^-14 of the sum), whose sums are added in fp32 in a third set of columns.
+// One chain for 4 million products of one sign lost more than the output's rounding.
+constexpr int kChainValues = 16384, kChainSteps = 128;
 constexpr int kMostRaws = 16;
 
 constexpr int kOperandA = kGemmRows * kGemmK * 2;
@@ -67,9 +71,12 @@ constexpr int kScaleSteps = 4, kScaleSlots = 4;
 __host__ __device__ constexpr int raw_codes(int fmt) { return fmt == QG_Q8_0 ? 64 : fmt == QG_BF16 ? 0 : 32; }
 __host__ __device__ constexpr int raw_scales(int fmt) { return fmt == QG_BF16 ? 0 : fmt == QG_Q5_0 ? 48 : 16; }
 __host__ __device__ constexpr int terms_x(int fmt, bool f32) { return !f32 ? 1 : fmt == QG_BF16 ? 3 : 2; }
-// Tokens of the largest tile: two sets of sums and the stages of W's operand share tensor memory's
-// 512 columns.
-__host__ __device__ constexpr int gemm_most_tokens(int fmt, bool f32) { return fmt == QG_BF16 ? (f32 ? 128 : 256) : f32 ? 96 : 192; }
+// Tokens of the largest tile: two sets of sums (three with chains) and the stages of W's operand share
+// tensor memory's 512 columns.
+__host__ __device__ constexpr int gemm_sets(bool f32, int n_in) { return !f32 && n_in > kChainValues ? 3 : 2; }
+__host__ __device__ constexpr int gemm_most_tokens(int fmt, bool f32, int sets = 2) {
+    return fmt == QG_BF16 ? (f32 ? 128 : sets == 3 ? 160 : 256) : f32 ? 96 : sets == 3 ? 128 : 192;
+}
 __host__ __device__ constexpr int w_columns(int fmt, bool f32) { return fmt == QG_BF16 ? 0 : f32 ? 64 : 32; }      // of a step
 
 struct GemmArgs {
@@ -181,7 +188,7 @@ __device__ __forceinline__ void decode32(const uint32_t* code, uint32_t fifth, _
 
 // ------------------------------------------------------------------------------ the kernel
 
-template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT, F32), 1) qgemm_kernel(const __grid_constant__ GemmArgs a) {
+template <int FMT, bool F32, bool CHAINS> __global__ void __launch_bounds__(gemm_threads(FMT, F32), 1) qgemm_kernel(const __grid_constant__ GemmArgs a) {
     constexpr bool kQuant = FMT != QG_BF16;
     constexpr int kGroups = decode_groups(FMT, F32), kDecodeWarps = 4 * kGroups;
     constexpr int TX = terms_x(FMT, F32);
@@ -207,7 +214,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
     auto sc_full = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + r); };
     auto sc_empty = [&](int r) { return bars + 8u * uint32_t(29 + 2 * kMostRaws + kScaleSlots + r); };
     const uint32_t acc_cols = uint32_t(a.bn) * (F32 ? 2 : 1);                    // of one set
-    const uint32_t tmem_cols = kQuant ? 512 : 2 * acc_cols <= 64 ? 64 : 2 * acc_cols <= 128 ? 128 : 2 * acc_cols <= 256 ? 256 : 512;
+    const uint32_t sums_cols = (CHAINS ? 3 : 2) * acc_cols;                      // of all sets; behind them W's operand
+    const uint32_t tmem_cols = kQuant ? 512 : sums_cols <= 64 ? 64 : sums_cols <= 128 ? 128 : sums_cols <= 256 ? 256 : 512;
     const tc::Waits wait{&dead, a.status, a.wait_limit};
     // (A last stage that K does not fill gets zeros.)
     const int ksteps = ((a.n_in + kGemmK - 1) / kGemmK + a.subs - 1) / a.subs * a.subs;
@@ -249,7 +257,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
         tc::grid_wait();
         const int half = warp >> 2;
         const uint32_t lanes = uint32_t(warp & 3) << 21;             // 32 (warp % 4) in the address's high half
-        const int chunks = F32 ? (ke - kb + kChunkSteps - 1) / kChunkSteps : 1;
+        const int chunks = F32 ? (ke - kb + kChunkSteps - 1) / kChunkSteps : CHAINS ? (ke - kb + kChainSteps - 1) / kChainSteps : 1;
         const int tiles = gemm_tiles(a);
         uint32_t it = 0;
         bool alive = true;
@@ -336,6 +344,30 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                     __syncwarp();
                     if (lane == 0) mbar_arrive(acc_empty(b));
                 } else {
+                    if constexpr (CHAINS) {              // the sum so far, in the third set; of the last chain, in its own
+                        for (int u = 0; u * 16 < hc; ++u) {
+                            const uint32_t so_far = tmem + lanes + 2 * acc_cols + uint32_t(from + u * 16);
+                            float x[16];
+                            tc::tmem_load16(acc + u * 16, v);
+                            tc::tmem_load_wait16(v);
+                            if (ch > 0) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(v[c]);
+                                tc::tmem_load16(so_far, v);
+                                tc::tmem_load_wait16(v);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(x[c] + __uint_as_float(v[c]));
+                            }
+                            tc::tmem_store16(ch + 1 < chunks ? so_far : acc + u * 16, v);
+                        }
+                        tc::tmem_store_wait();
+                        if (ch + 1 < chunks) {
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(acc_empty(b));
+                            continue;
+                        }
+                    }
                     if (hc == 0 && lane == 0) mbar_arrive(acc_empty(b));     // (16 tokens: all in the first half)
                     for (int u = 0; u * 16 < hc; ++u) {
                         tc::tmem_load16(acc + u * 16, v);
@@ -419,7 +451,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                             half[0] = w0 & 0xFFFFu, half[1] = w0 >> 16;
                         }
                         const int left = a.n_in - k * kGemmK;                    // weights from here to the row's end
-                        const uint32_t to = tmem + (uint32_t(w & 3) << 21) + 2 * acc_cols + uint32_t((s * a.subs + sub) * w_columns(FMT, F32));
+                        const uint32_t to = tmem + (uint32_t(w & 3) << 21) + sums_cols + uint32_t((s * a.subs + sub) * w_columns(FMT, F32));
                         bool ready = false;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -567,8 +599,8 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                 const int n = a.n_experts ? gemm_tile(a, t).n : a.bn;
                 const uint32_t idesc = tc::instr(!kQuant, F32 ? 2 * n : n, false), ione = tc::instr(!kQuant, n, false);
                 for (int k = kb; k < ke; k += a.subs) {
-                    const bool first = F32 ? k % kChunkSteps == 0 : k == kb;
-                    const bool lastk = k + a.subs == ke || (F32 && (k + a.subs) % kChunkSteps == 0);
+                    const bool first = F32 ? k % kChunkSteps == 0 : k == kb || (CHAINS && (k - kb) % kChainSteps == 0);
+                    const bool lastk = k + a.subs == ke || (F32 && (k + a.subs) % kChunkSteps == 0) || (CHAINS && (k + a.subs - kb) % kChainSteps == 0);
                     const int b = int(it & 1);
                     if (first && !wait(acc_empty(b), ((it >> 1) & 1) ^ 1)) { alive = false; break; }
                     if (!wait(full(s), phase)) { alive = false; break; }
@@ -576,7 +608,7 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
                     const uint32_t acc = tmem + uint32_t(b) * acc_cols;
                     uint32_t at = base + uint32_t(s) * stage_bytes;
                     if (tc::elect()) {
-                        uint32_t wt = tmem + 2 * acc_cols + uint32_t(s * a.subs * w_columns(FMT, F32));
+                        uint32_t wt = tmem + sums_cols + uint32_t(s * a.subs * w_columns(FMT, F32));
                         for (int u = 0; u < a.subs; ++u, at += sub_bytes, wt += w_columns(FMT, F32)) {
                             const uint64_t da = tc::desc_k(at), db = tc::desc_k(at + a_bytes);
 #pragma unroll
@@ -618,6 +650,6 @@ template <int FMT, bool F32> __global__ void __launch_bounds__(gemm_threads(FMT,
     if (warp == kDrainWarps + kDecodeWarps + 1) tc::tmem_free(tmem, tmem_cols);
 }
 
-const void* qgemm_lookup(int fmt, bool f32);
+const void* qgemm_lookup(int fmt, bool f32, bool chains);
 
 }  // namespace qg

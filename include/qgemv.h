@@ -502,8 +502,9 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
  *                aligned to an element.  Does not overlap x, W, bias, or (but for y itself) residual.
  *   workspace    device, >= qgemm_workspace_bytes(fmt, act, n_out, n_in, ntok, 0) bytes, 16-byte
  *                aligned; it need not be cleared.  Calls that share one must be serialized.
- * Sums are fp32.  fp32 activations enter as two 16-bit terms each of x and W (22 bits of x below
- * the row's largest value, all bits of W; bf16 weights: all 24 bits of x); bf16 ones as they are,
+ * Sums are fp32; the tensor cores cut off a bit (2^-23 of the sum) with every 16 products that they add, in chains of 256
+ * products with fp32 activations (2^-19 at most), of 16384 at most with bf16 ones (2^-13).  fp32
+ * activations enter as two 16-bit terms each of x and W (22 bits of x below the row's largest value, all bits of W; bf16 weights: all 24 bits of x); bf16 ones as they are,
  * weights of the quantized formats then rounded to 11 bits (2^-11 of each at most).  Quantized weights
  * of magnitude 65520 and more count as infinite; values of x below 2^-39 of their row's largest as zero.
  * Inputs that are not finite make the outputs they enter not finite.  A token's outputs do not depend
