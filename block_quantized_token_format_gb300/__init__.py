@@ -516,7 +516,7 @@ def qg_prompt_attention(q, k, v, cu_seq, out, workspace, scale: float, longest: 
     """Enqueue the causal attention of packed prompts: ``q``, ``out`` ``[n_tok, n_heads, head_dim]``,
     ``k``, ``v`` ``[n_tok, n_kv_heads, head_dim]``, float32 or bfloat16 (slices of one projection's rows
     are taken as they are); prompt r is rows ``cu_seq[r] .. cu_seq[r + 1]`` (int32), ``longest`` the most
-    tokens of one.  ``window`` > 0: a sliding window.  ``workspace``: uint8,
+    tokens of one (a hint; nothing depends on it).  ``window`` > 0: a sliding window.  ``workspace``: uint8,
     ``qg_prompt_attention_workspace_bytes``."""
     st = (_calls or _bound()).prompt_attention(q, k, v, cu_seq, out, workspace, scale, longest, window, lse, stream)
     if st != 0:

@@ -32,7 +32,7 @@
 // bf16 activations, which a row's power of two moves into fp16's range exactly (but for values
 // 2^-29 and more below the row's largest), meet weights rounded to 11 bits: 2^-11 of a weight at most,
 // an eighth of what rounding the output to bf16 costs.  fp32 activations are two fp16 terms (22
-// bits), weights two (exact), in three products; the two small ones have accumulators of their
+// bits), weights two (exact; affine 22 bits), in three products; the two small ones have accumulators of their
 // own, and every 256 values of K the sums move to fp32 registers: the tensor cores truncate what
 // they add, and a long chain of additions would lose what the terms keep.
 // bf16 weights meet bf16 activations as they are, fp32 ones as three bf16 terms (all 24 bits).

@@ -504,12 +504,13 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
  *                aligned; it need not be cleared.  Calls that share one must be serialized.
  * Sums are fp32; the tensor cores cut off a bit (2^-23 of the sum) with every 16 products that they add, in chains of 256
  * products with fp32 activations (2^-19 at most), of 16384 at most with bf16 ones (2^-13).  fp32
- * activations enter as two 16-bit terms each of x and W (22 bits of x below the row's largest value, all bits of W; bf16 weights: all 24 bits of x); bf16 ones as they are,
- * weights of the quantized formats then rounded to 11 bits (2^-11 of each at most).  Quantized weights
- * of magnitude 65520 and more count as infinite; values of x below 2^-39 of their row's largest as zero.
- * Inputs that are not finite make the outputs they enter not finite.  A token's outputs do not depend
- * on the other tokens' values; the order of a sum depends on the call's sizes and the GPU's number of SMs; outputs are the same on
- * every run.
+ * activations enter as two 16-bit terms each of x and W (22 bits of x below the row's largest value; all bits of
+ * W, of affine weights 22; bf16 weights: all 24 bits of x); bf16 ones as they are, weights of the quantized formats then
+ * rounded to 11 bits (2^-11 of each at most).  Values of x below 2^-39 of their row's largest count as zero.  Quantized
+ * weights of magnitude 65520 and more, which qgemv multiplies, are beyond fp16: their outputs are infinite or NaN.
+ * Inputs that are not finite make the outputs they enter not finite.  A token's outputs do not depend on the other
+ * tokens' values; the order of a sum depends on the call's sizes and the GPU's number of SMs; outputs are the
+ * same on every run.
  * n_out, n_in as in qgemv (n_in has no upper limit but 2^24); ntok >= 0, below 2^31 - 1024.
  * Errors: QG_EINVAL (format, type, shape, null pointer, odd n_out with swiglu, y = x), QG_EALIGN,
  * QG_EWORKSPACE, QG_EUNSUPPORTED (2^31 tiles of 128 rows and 32 tokens or more), QG_ECUDA.
@@ -546,7 +547,8 @@ qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_
  *   cu_seq       device int32 [n_seq + 1], as qg_cache_pages leaves cu_new where nothing was held.
  *                Tokens outside cu_seq[0] .. cu_seq[n_seq] are neither read nor written.  Entries that
  *                shrink or leave 0..n_tok set QG_DEVICE_BAD_LENGTH; out and lse are then not valid.
- *   longest      a prompt's most tokens (at least 1): a hint; results are right for any value.
+ *   longest      a prompt's most tokens (at least 1).  A hint that the present kernels do not need: nothing
+ *                depends on it.
  *   lse          device fp32 [n_tok][n_heads] (natural logarithm), or NULL.
  *   workspace    device, >= qg_prompt_attention_workspace_bytes(act, n_tok, n_heads, n_kv_heads, head_dim)
  *                bytes, 16-byte aligned; it need not be cleared.  Calls that share one must be serialized.
