@@ -1,6 +1,6 @@
 """One attention sublayer served with the library: a prompt, then decode and verify steps.
 
-    python examples/attention_step.py
+    python examples/attention_step.py [--steps]
 
 A batch of sequences runs through the calls a serving program makes per step:
 
@@ -11,8 +11,9 @@ A batch of sequences runs through the calls a serving program makes per step:
     qgemv              output projection, 6144 -> 2560
 
 The prompts go in whole, with qgemm for qgemv and qg_prompt_attention over the keys and values as the
-cache has stored them; weights and inputs are random.  The decode step is captured once as a CUDA graph and replayed: nothing in it reads back to the
-host, and the lengths live on the device.
+cache has stored them, or (--steps) two tokens of each at a time through the same calls as the decode
+step; weights and inputs are random.  The decode step is captured once as a CUDA graph and replayed:
+nothing in it reads back to the host, and the lengths live on the device.
 """
 from __future__ import annotations
 
@@ -107,14 +108,25 @@ class Step:
         self.held.copy_(self.seq_len)
 
 
-def main(prompt: int = 40, decode: int = 8) -> dict:
+def main(prompt: int = 40, decode: int = 8, whole: bool = True) -> dict:
     torch.manual_seed(0)
     n_pages = 64
     layer, step = AttentionLayer(1, n_pages), Step(2, n_pages, 16, [prompt, prompt])
-    # Prompt: two sequences in one pass.
-    step.begin_step()
-    prompts = layer.prompt(torch.randn(2 * prompt, D_MODEL, device="cuda"), step)
-    step.end_step()
+    tokens = torch.randn(2, prompt, D_MODEL, device="cuda")
+    if whole:
+        # Prompt: two sequences in one pass.
+        step.begin_step()
+        prompts = layer.prompt(tokens.view(2 * prompt, D_MODEL), step).view(2, prompt, D_MODEL)
+        step.end_step()
+    else:
+        # Prompt: two sequences, two tokens each per step.
+        prompts = torch.empty_like(tokens)
+        for at in range(0, prompt, 2):
+            now = tokens[:, at:at + 2].contiguous()
+            step.set_fresh([now.shape[1]] * 2)
+            step.begin_step()
+            prompts[:, at:at + 2] = layer(now.view(-1, D_MODEL), step).view_as(now)
+            step.end_step()
     # Decode: one token each, as one graph.
     step.set_fresh([1, 1])
     x = torch.randn(2, D_MODEL, device="cuda")
@@ -142,5 +154,5 @@ def main(prompt: int = 40, decode: int = 8) -> dict:
 
 
 if __name__ == "__main__":
-    r = main()
+    r = main(whole="--steps" not in sys.argv[1:])
     print("lengths", r["lengths"], "pages dealt", r["pages"], "output rms", float(r["verify"].square().mean().sqrt()))
