@@ -33,7 +33,7 @@ __all__ = [
     "qg_attention_workspace_bytes", "QG_CACHE_MAX", "QG_ATTENTION_ZERO_BYTES", "QG_DEVICE_BAD_PAGE",
     "QG_DEVICE_BAD_LENGTH", "QG_DEVICE_NO_PAGES", "QG_ACT_F32", "QG_ACT_BF16",
     "qgemm", "qgemm_experts", "qgemm_workspace_bytes", "ACTIVATIONS", "qg_prompt_attention",
-    "qg_prompt_attention_workspace_bytes",
+    "qg_prompt_attention_workspace_bytes", "qg_describe_gemm_tile",
 ]
 
 QG_Q8_0, QG_Q4_0, QG_AFFINE4_G64, QG_BF16, QG_Q5_0 = 0, 1, 2, 3, 4
@@ -108,6 +108,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "qgemm_workspace_bytes": (sz, [i32, i32, i64, i64, i64, i64]),
         "qgemm": (i32, [i32, vp, i64, i64, i32, vp, i64, i64, vp, i32, vp, i64, vp, i64, vp, sz, vp]),
         "qgemm_experts": (i32, [i32, vp, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i32, vp, i64, vp, sz, vp]),
+        "qg_describe_gemm_tile": (i32, [i32, i32, i64, i64, i64, i64, ctypes.c_char_p, sz]),
         "qg_prompt_attention_workspace_bytes": (sz, [i32, i64, i32, i32, i32]),
         "qg_prompt_attention": (i32, [i32, vp, i64, vp, i64, vp, i64, i64, i32, i32, i32, vp, i32, i32, i32, f32, vp, i64, vp, vp, sz,
                                       vp]),
@@ -506,6 +507,13 @@ def qgemm_experts(fmt, W, n_experts: int, n_out: int, n_in: int, x, offsets, y, 
                                            ACTIVATIONS[activation], stream)
     if st != 0:
         raise QGError(st, "qgemm_experts")
+
+
+def qg_describe_gemm_tile(fmt, act, n_out: int, n_in: int, n_slots: int, n_experts: int = 0) -> str:
+    """The tile that qgemm (``n_experts`` 0) or qgemm_experts would use on the current device."""
+    buf = ctypes.create_string_buffer(128)
+    _check(load_library().qg_describe_gemm_tile(_fmt(fmt), _act(act), n_out, n_in, n_slots, n_experts, buf, 128), "qg_describe_gemm_tile")
+    return buf.value.decode()
 
 
 def qg_prompt_attention_workspace_bytes(act, n_tok: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdio>
 
 #include "qgemm.cuh"
 #include "qgemv_host.h"
@@ -365,26 +366,43 @@ qg_status encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* W, i
                ? QG_OK : QG_ECUDA;
 }
 
+// A call's kernel, tile and shared memory on the current device.
+struct Choice {
+    int dev, sms, optin;
+    unsigned int* status;
+    const void* fn;
+    int threads;
+    int64_t m_tiles, n_tiles;
+    Shape shape;
+    Geometry geo;
+};
+qg_status choose(int fmt, bool f32, int64_t n_out, int64_t n_in, int64_t n_slots, int64_t n_experts, Choice* ch) {
+    qg_status st = device_info(&ch->dev, &ch->sms, &ch->optin, &ch->status);
+    if (st != QG_OK) return st;
+    const int sets = gemm_sets(f32, int(n_in)), groups = decode_groups(fmt, f32);
+    ch->fn = qgemm_lookup(fmt, f32, sets == 3);
+    ch->threads = gemm_threads(fmt, f32);
+    ch->m_tiles = (n_out + kGemmRows - 1) / kGemmRows;
+    ch->shape = tile_shape(fmt, f32, n_in, ch->m_tiles, n_slots, n_experts, ch->sms, [&](int parts) {
+        const size_t smem = geometry(fmt, f32, 32, sets, ch->optin).smem;
+        return blocks_per_sm(ch->fn, ch->dev, ch->optin, ch->threads, smem) < 1 ? 0 : clusters_at_once(ch->fn, ch->dev, ch->threads, smem, parts);
+    });
+    ch->n_tiles = (n_slots + ch->shape.bn - 1) / ch->shape.bn;
+    if ((ch->n_tiles + n_experts) * ch->m_tiles > (int64_t(1) << 31) - 4096) return QG_EUNSUPPORTED;
+    const Geometry& g = ch->geo = geometry(fmt, f32, ch->shape.bn, sets, ch->optin);
+    if (g.stages < 2 || g.stages * g.subs < groups || g.raws < groups) return QG_EUNSUPPORTED;
+    return blocks_per_sm(ch->fn, ch->dev, ch->optin, ch->threads, g.smem) < 1 ? QG_EUNSUPPORTED : QG_OK;
+}
+
 qg_status launch_gemm(const GemmCall& c) {
     const bool f32 = c.act == QG_ACT_F32, quant = c.fmt != QG_BF16;
     const GemmSpace sp = gemm_space(c.fmt, f32, c.rows != nullptr, c.n_in, c.n_slots, c.n_experts);
     if (sp.total > 0 && (!c.workspace || c.workspace_bytes < sp.total)) return QG_EWORKSPACE;
     if (!aligned(c.workspace, 16)) return QG_EALIGN;
-    int dev = 0, sms = 0, optin = 0;
-    unsigned int* status = nullptr;
-    qg_status st = device_info(&dev, &sms, &optin, &status);
+    Choice ch{};
+    qg_status st = choose(c.fmt, f32, c.n_out, c.n_in, c.n_slots, c.n_experts, &ch);
     if (st != QG_OK) return st;
-    const int64_t m_tiles = (c.n_out + kGemmRows - 1) / kGemmRows;
-    const int sets = gemm_sets(f32, int(c.n_in));
-    const void* const fn = qgemm_lookup(c.fmt, f32, sets == 3);
-    const int threads = gemm_threads(c.fmt, f32);
-    const Shape shape = tile_shape(c.fmt, f32, c.n_in, m_tiles, c.n_slots, c.n_experts, sms, [&](int parts) {
-        const size_t smem = geometry(c.fmt, f32, 32, sets, optin).smem;
-        return blocks_per_sm(fn, dev, optin, threads, smem) < 1 ? 0 : clusters_at_once(fn, dev, threads, smem, parts);
-    });
-    const int bn = shape.bn;
-    const int64_t n_tiles = (c.n_slots + bn - 1) / bn;
-    if ((n_tiles + c.n_experts) * m_tiles > (int64_t(1) << 31) - 4096) return QG_EUNSUPPORTED;
+    const int bn = ch.shape.bn, parts = ch.shape.parts;
     uint8_t* const ws = static_cast<uint8_t*>(c.workspace);
     const bool stages_x = quant || f32 || c.rows;
 
@@ -404,20 +422,16 @@ qg_status launch_gemm(const GemmCall& c) {
     a.f = int(c.f);
     a.bn = bn;
     a.box = c.n_experts ? 16 : bn;
-    a.m_tiles = int(m_tiles);
-    a.n_tiles = int(n_tiles);
-    a.status = status;
+    a.m_tiles = int(ch.m_tiles);
+    a.n_tiles = int(ch.n_tiles);
+    a.status = ch.status;
     a.wait_limit = wait_limit();
     a.drain_limit = std::max<uint32_t>(a.wait_limit, 1u << 16);
     a.extra_tx = test_extra_tx();
-    const Geometry geo = geometry(c.fmt, f32, bn, sets, optin);
-    const int groups = decode_groups(c.fmt, f32);
-    a.subs = geo.subs;
-    a.stages = geo.stages;
-    a.raws = geo.raws;
-    a.parts = shape.parts;
-    if (a.stages < 2 || a.stages * a.subs < groups || (quant && a.raws < groups)) return QG_EUNSUPPORTED;
-    if (blocks_per_sm(fn, dev, optin, threads, geo.smem) < 1) return QG_EUNSUPPORTED;
+    a.subs = ch.geo.subs;
+    a.stages = ch.geo.stages;
+    a.raws = ch.geo.raws;
+    a.parts = parts;
     const int64_t rows = std::max<int64_t>(1, c.n_experts) * c.n_out, pitch = row_stride(c.fmt, c.n_in);
     st = stages_x ? encode_tokens(&a.xmap, ws + sp.staged, c.n_in, c.n_slots, terms_x(c.fmt, f32), c.n_in * 2, a.box)
                   : encode_tokens(&a.xmap, c.x, c.n_in, c.n_x, 1, c.x_stride * 2, a.box);
@@ -445,19 +459,19 @@ qg_status launch_gemm(const GemmCall& c) {
         s.n_in = int(c.n_in);
         s.n_experts = int(c.n_experts);
         s.bn = bn;
-        s.status = status;
+        s.status = ch.status;
         // A row takes a CTA where there are too few rows to fill the GPU with a warp each.
-        const bool wide = c.n_slots < 8 * sms;
+        const bool wide = c.n_slots < 8 * ch.sms;
         const int64_t per = wide ? 1 : kStageThreads / 32;
         const int64_t grid = (stages_x ? (c.n_slots + per - 1) / per : 0) + (c.n_experts > 0 ? 1 : 0);
         void* params[] = {&s};
         st = launch_early(stage_fn(c.fmt, f32, wide), int(grid), kStageThreads, 0, 1, params, c.stream);
         if (st != QG_OK) return st;
     }
-    const int64_t tiles = c.n_experts ? sms : n_tiles * m_tiles;
+    const int64_t tiles = c.n_experts ? ch.sms : ch.n_tiles * ch.m_tiles;
     void* params[] = {&a};
-    return launch_after(fn, shape.parts > 1 ? int(tiles) * shape.parts : int(std::min<int64_t>(sms, tiles)), threads, geo.smem, shape.parts, before,
-                        params, c.stream);
+    return launch_after(ch.fn, parts > 1 ? int(tiles) * parts : int(std::min<int64_t>(ch.sms, tiles)), ch.threads, ch.geo.smem, parts, before, params,
+                        c.stream);
 }
 
 }  // namespace
@@ -494,6 +508,16 @@ qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_
     const qg_status st = check(c);
     if (st != QG_OK || n_slots == 0) return st;
     return launch_gemm(c);
+}
+
+qg_status qg_describe_gemm_tile(qg_fmt fmt, qg_act act, int64_t n_out, int64_t n_in, int64_t n_slots, int64_t n_experts, char* buf, size_t len) {
+    if (!buf || len == 0 || !shape_valid(fmt, n_out, n_in) || (act != QG_ACT_F32 && act != QG_ACT_BF16)) return QG_EINVAL;
+    if (n_slots < 1 || n_slots > (int64_t(1) << 31) - 1025 || n_experts < 0 || n_experts > kMostExperts) return QG_EINVAL;
+    Choice ch{};
+    const qg_status st = choose(fmt, act == QG_ACT_F32, n_out, n_in, n_slots, n_experts, &ch);
+    if (st != QG_OK) return st;
+    std::snprintf(buf, len, "tokens=%d,parts=%d,steps=%d,stages=%d,raws=%d", ch.shape.bn, ch.shape.parts, ch.geo.subs, ch.geo.stages, ch.geo.raws);
+    return QG_OK;
 }
 
 }  // extern "C"

@@ -524,7 +524,11 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
  *   rows         device int32 [n_slots]; one outside 0..n_x - 1 sets QG_DEVICE_BAD_PLAN, its slot is
  *                computed as if x's row were zeros.
  *   workspace    >= qgemm_workspace_bytes(fmt, act, n_out, n_in, n_slots, n_experts) bytes.
- *   n_experts <= 65536.  Other arguments, numbers and errors as in qgemm. */
+ *   n_experts <= 65536.  Other arguments, numbers and errors as in qgemm.
+ *
+ * qg_describe_gemm_tile: writes the tile that a call would use on the current device (n_experts 0: qgemm)
+ * into buf as "tokens=..,parts=..,steps=..,stages=..,raws=..": tokens of a tile, CTAs that share its K, steps of K in a
+ * stage, stages, slots of raw codes (NUL-terminated, truncated to len).  n_slots >= 1. */
 typedef enum { QG_F_NONE = 0, QG_F_SILU = 1, QG_F_GELU = 2, QG_F_GELU_TANH = 3, QG_F_SWIGLU = 4 } qg_activation;
 size_t    qgemm_workspace_bytes(qg_fmt fmt, qg_act act, int64_t n_out, int64_t n_in, int64_t n_slots, int64_t n_experts);
 qg_status qgemm(qg_fmt fmt, const void* W, int64_t n_out, int64_t n_in, qg_act act, const void* x, int64_t x_stride,
@@ -533,6 +537,8 @@ qg_status qgemm(qg_fmt fmt, const void* W, int64_t n_out, int64_t n_in, qg_act a
 qg_status qgemm_experts(qg_fmt fmt, const void* W, int64_t n_experts, int64_t n_out, int64_t n_in, qg_act act, const void* x,
                         int64_t x_stride, int64_t n_x, const int32_t* offsets, const int32_t* rows, int64_t n_slots,
                         qg_activation f, void* y, int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);
+qg_status qg_describe_gemm_tile(qg_fmt fmt, qg_act act, int64_t n_out, int64_t n_in, int64_t n_slots, int64_t n_experts, char* buf,
+                                size_t len);
 
 /* qg_prompt_attention: causal attention within each of n_seq prompts whose tokens lie one after
  * the other (packed): of prompt r, rows cu_seq[r] .. cu_seq[r + 1] of q, k and v,

@@ -1,9 +1,11 @@
-"""qgemm and qgemm_experts at the ends of their range: long sums.
+"""qgemm and qgemm_experts at the ends of their range: long sums, tiles of every width.
 
 Tolerances (derived from the arithmetic, before any run), with S = sum |w x|: the tensor cores may cut off the
 last bit of a sum that they add to, 2^-23 of S for each addition of 16 products.
 """
 from __future__ import annotations
+
+import functools
 
 import numpy as np
 import pytest
@@ -93,4 +95,100 @@ def test_sums_around_a_chain(fmt, n_in):
     got = host(y)
     for s in range(off[-1]):
         assert (np.abs(got[s] - v[s]) <= (2.0 ** -11 + 2.0 ** -13) * S[s] + 2.0 ** -8 * np.abs(v[s])).all()
+    assert qg.qg_device_status() == 0
+
+
+# --------------------------------------------------------------------------- wide tiles
+
+QUANT = ["q8_0", "q4_0", "affine4_g64", "q5_0"]
+N_IN = {"q8_0": 1120, "q4_0": 1120, "q5_0": 1120, "affine4_g64": 1152, "bf16": 1136}      # half a step, or two, at the end
+LONG = {"q8_0": 4640, "q4_0": 4640, "q5_0": 4640, "affine4_g64": 4672, "bf16": 4656}
+
+
+def tile(*a):
+    return {k: int(v) for k, v in (p.split("=") for p in qg.qg_describe_gemm_tile(*a).split(","))}
+
+
+@functools.lru_cache(maxsize=2)
+def weights(fmt, rows, n_in):
+    """Canonical bytes, packed bytes and the weights themselves in 64 bits."""
+    c = oracle.quantize(fmt, (np.random.default_rng(rows).standard_normal((rows, n_in)) * 0.02).astype(np.float32))
+    return c, torch.from_numpy(qg.qg_to_device_layout(fmt, c, rows, n_in)).cuda(), torch.from_numpy(oracle.dequantize(fmt, c, rows, n_in)).cuda()
+
+
+def tokens(rng, n, n_in, act):
+    return torch.tensor(rng.standard_normal((n, n_in)) * rng.uniform(0.5, 2.0, (n, 1)), dtype=torch.float32, device="cuda").to(DT[act])
+
+
+def check(x, W, y, act):
+    """bf16: a weight rounded to fp16 2^-11 of S, n_in / 16 additions that may cut off a bit, the output's rounding
+    2^-8 of it.  fp32: terms 2^-21, chains of 256 and their small products' 2^-18, their sums in fp32."""
+    want, S, n_in = x.double() @ W.t(), x.double().abs() @ W.abs().t(), x.shape[1]
+    if act == "bf16":
+        t = S * (2.0 ** -11 + n_in / 16 * 2.0 ** -23) + 2.0 ** -8 * want.abs()
+    else:
+        t = S * (2.0 ** -21 + 2.0 ** -18 + (n_in / 256 + 8) * 2.0 ** -24)
+    assert bool(((y.double() - want).abs() <= t).all())
+
+
+WIDE = ([(f, "bf16", *c) for f in QUANT for c in ((96, 3967, 776), (112, 3967, 875), (128, 3583, 1139), (144, 3967, 1172), (160, 3967, 1304),
+                                                  (176, 3583, 1601), (192, 3583, 1766))] +
+        [(f, "f32", *c) for f in QUANT for c in ((48, 2815, 578), (64, 3967, 446), (80, 3967, 578), (96, 3583, 809))] +
+        [("bf16", "bf16", *c) for c in ((128, 3967, 1040), (144, 3967, 1172), (176, 3583, 1601), (208, 3967, 1733), (240, 3967, 2030), (256, 3967, 2162))] +
+        [("bf16", "f32", *c) for c in ((64, 3327, 644), (80, 3967, 578), (96, 3583, 809), (112, 3967, 875), (128, 3583, 1139))])
+
+
+@pytest.mark.parametrize("fmt,act,width,n_out,ntok", sorted(WIDE))
+def test_tiles_of_every_width(fmt, act, width, n_out, ntok):
+    """More tiles than SMs, so that CTAs take a second one; the last ones partly filled in both directions."""
+    n_in = N_IN[fmt]
+    got = tile(fmt, act, n_out, n_in, ntok)
+    assert got["tokens"] == width and got["parts"] == 1 and -(-n_out // 128) * -(-ntok // width) > 152
+    _, packed, W = weights(fmt, n_out, n_in)
+    x = tokens(np.random.default_rng(width), ntok, n_in, act)
+    y = torch.zeros(ntok, n_out, dtype=DT[act], device="cuda")
+    qg.qgemm(fmt, packed, n_out, n_in, x, y, space(fmt, act, n_out, n_in, ntok))
+    check(x, W, y, act)
+    assert qg.qg_device_status() == 0
+
+
+@pytest.mark.parametrize("n_out,ntok", [(127, 1), (1023, 53), (1023, 66), (1919, 105), (1919, 183), (2047, 92), (2431, 105), (2431, 196)])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", QUANT + ["bf16"])
+def test_clusters(fmt, act, n_out, ntok):
+    """CTAs that share K, in numbers that do not divide it, with tiles of one width and another."""
+    n_in = LONG[fmt]
+    assert tile(fmt, act, n_out, n_in, ntok)["parts"] > 1
+    _, packed, W = weights(fmt, n_out, n_in)
+    x = tokens(np.random.default_rng(ntok), ntok, n_in, act)
+    y = torch.zeros(ntok, n_out, dtype=DT[act], device="cuda")
+    qg.qgemm(fmt, packed, n_out, n_in, x, y, space(fmt, act, n_out, n_in, ntok))
+    check(x, W, y, act)
+    assert qg.qg_device_status() == 0
+
+
+def test_clusters_of_many_sizes():
+    """The cases above are of several numbers of CTAs and widths."""
+    for act, fmts in (("bf16", QUANT + ["bf16"]), ("f32", QUANT + ["bf16"])):
+        got = [tile(f, act, n_out, LONG[f], ntok) for f in fmts for n_out, ntok in
+               ((127, 1), (1023, 53), (1023, 66), (1919, 105), (1919, 183), (2047, 92), (2431, 105), (2431, 196))]
+        assert len({g["parts"] for g in got}) >= 3 and len({g["tokens"] for g in got}) >= 4 and max(g["tokens"] for g in got) >= 96
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", QUANT + ["bf16"])
+def test_experts_in_wide_tiles(fmt, act):
+    """Experts' rows around every multiple of sixteen that a tile takes, some more than a tile has; more tiles than SMs."""
+    counts = [16, 1, 0, 15, 17, 31, 32, 33, 48, 49, 64, 100, 192, 193, 95, 96, 97, 111, 112, 113, 127, 128, 129, 143, 144, 145, 159, 160, 161, 175, 176,
+              177, 191, 208, 255, 256, 257]
+    n_experts, n_out, n_in, off = len(counts), 515, 1152, [0] + list(np.cumsum(counts))
+    width = tile(fmt, act, n_out, n_in, int(off[-1]), n_experts)["tokens"]
+    assert width >= (80 if act == "f32" else 128) and 5 * sum(-(-k // width) for k in counts) > 152
+    _, packed, W = weights(fmt, n_experts * n_out, n_in)
+    x = tokens(np.random.default_rng(3), int(off[-1]), n_in, act)
+    y = torch.zeros(int(off[-1]), n_out, dtype=DT[act], device="cuda")
+    qg.qgemm_experts(fmt, packed, n_experts, n_out, n_in, x, torch.tensor(off, dtype=torch.int32, device="cuda"), y,
+                     space(fmt, act, n_out, n_in, int(off[-1]), n_experts))
+    for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+        check(x[a:b], W[e * n_out:(e + 1) * n_out], y[a:b], act)
     assert qg.qg_device_status() == 0

@@ -97,3 +97,10 @@ def test_binding_refuses_without_a_gpu():
         qg.qg_prompt_attention(torch.zeros(4, 2, 64), None, None, None, None, None, 1.0, 4)
     with pytest.raises(TypeError):
         qg.qgemm_experts("q8_0", A, 8, 100, 64, np.zeros((4, 64), np.float32), None, None, None)
+
+
+def test_tile_description_refuses():
+    for bad in (("q8_0", "bf16", 0, 64, 1), ("q8_0", "bf16", 8, 33, 1), ("q8_0", "bf16", 8, 64, 0), ("q8_0", "bf16", 8, 64, 1, -1),
+                ("q8_0", "bf16", 8, 64, 1, 70000), ("q8_0", 2, 8, 64, 1)):
+        with pytest.raises(qg.QGError):
+            qg.qg_describe_gemm_tile(*bad)
