@@ -16,10 +16,10 @@
 // Bound by a tile's softmax, one dependent chain of tensor-memory load, maximum over two lanes,
 // exponentials and store, which the two CTAs' tiles cover only in part, and by the scores' products,
 // which read 6 KB of operands from shared memory in the 32 clocks that they would take: heads of
-// 128 keep the tensor cores busy 70 % of the time and issue instructions in 49 % of the clocks, DRAM is
-// at 8 %.  Back to back (single calls): 8191 tokens, 48 heads of 128 on 16: 615 us (566), 1340 TFLOP/s of
-// visible keys' products; 60 packed prompts of up to 1500 tokens, 32 heads on 8: 303 us (287); 5 prompts of
-// up to 5000, 24 heads of 256 on 4, window 1024: 196 us (191).  Steps: one lane a row to two and packed arithmetic 875 -> 707 us (8191 tokens); CTAs that
+// 128 keep the tensor cores busy 71 % of the time and issue instructions in 52 % of the clocks, DRAM is
+// at 8 %.  Back to back: 8191 tokens, 48 heads of 128 on 16: 614 us, 1340 TFLOP/s of
+// visible keys' products; 60 packed prompts of up to 1500 tokens, 32 heads on 8: 299 us; 5 prompts of
+// up to 5000, 24 heads of 256 on 4, window 1024: 193 us.  Steps (single calls): one lane a row to two and packed arithmetic 875 -> 707 us (8191 tokens); CTAs that
 // stay 524 -> 425 (packed prompts); tiles of 64 keys, not 128, with two buffers of S 425 -> 352; items
 // taken as CTAs come free, not in turn, 349 -> 287.  Four lanes a row with heads of 256: 203 -> 210, not kept.
 //

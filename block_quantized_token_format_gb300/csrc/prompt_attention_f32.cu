@@ -20,8 +20,10 @@
 //
 // Bound by the tensor cores, which work 68 % of the time on three products for each that counts as
 // work, and by the softmax with its two terms in what is left: two prompts of up to 3500 tokens, 32
-// heads of 128 on 8: 291 us with the staging (there four query rows to a warp; one row to a warp took 12 us
-// more).  Two lanes a row instead of one: 377 to 306 us; four: 303 where two took 292, not kept.
+// heads of 128 on 8: 292 us with the staging (there four rows to a warp; one row to a warp took 12 us
+// more); tokens of sizes from 1e-3 to 1, whose tiles are scaled by column, 331 us.  Heads of 64 209 us (283), 16
+// heads of 256 on 4 525 us.  Two lanes a row instead of one: 377 to 306 us; four: 303 where two took 292, not kept.
+// Powers of two in steps of 8: in single steps every tile was scaled by column, 340 us and heads of 64 283.
 #include "prompt_attention.cuh"
 
 namespace qg {

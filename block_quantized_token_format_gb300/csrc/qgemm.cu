@@ -289,8 +289,11 @@ Geometry geometry(int fmt, bool f32, int bn, int sets, int optin) {
     return g;
 }
 
-// Nanoseconds of a step of K (64) of a tile of bn tokens, all SMs at work, as measured on GB300: the
-// decoding of the codes, or from some size on the tokens' way from L2 and the products.
+// Nanoseconds of a step of K (64) of a tile of bn tokens, all SMs at work: the decoding of the codes, or from
+// some size on the tokens' way from L2 and the products.  Fitted to measurements on GB300, in calls short enough that
+// the clocks stay up; calls of 150 steps to a tile measured, in ns, at 32 / 96 / 192 tokens (bf16) and 32 / 64 / 96
+// (fp32): Q8_0 209 / 213 / 472 and 350 / 364 / 548, Q4_0 246 / 253 / 451 and 372 / 393 / 534, affine 252 / 255 / 452 and
+// 531 / 555 / 566, Q5_0 298 / 311 / 489 and 454 / 473 / 581, bf16 166 / 188 / 301 and 388 / 455 / 525.
 double step_ns(int fmt, bool f32, int bn) {
     if (fmt == QG_BF16) return f32 ? 300.0 + 2.75 * bn : std::max(160.0, 1.55 * bn);
     if (!f32) return std::max(fmt == QG_Q8_0 ? 215.0 : fmt == QG_Q5_0 ? 300.0 : 255.0, 1.8 * bn);
@@ -305,9 +308,12 @@ Shape tile_shape(int fmt, bool f32, int64_t n_in, int64_t m_tiles, int64_t n_slo
     Shape best{32, 1};
     double least = 0;
     const double ksteps = double((n_in + kGemmK - 1) / kGemmK);
-    // Experts' rows: spread like independent choices, and by half their mean for the experts' popularity
-    // (of 20,480 rows and 512 experts in tiles of 64 that makes 577 tiles; a routing had 568).  A larger tile
-    // costs no more where an expert has few rows, so it is the one that holds most experts' rows.
+    // Experts' rows: spread like independent choices, and by half their mean for the experts' popularity, which the
+    // host does not know.  A larger tile costs little more where an expert has few rows, so the guess matters little:
+    // with popularities exp(sigma N(0, 1)), sigma 0 / 0.5 / 1 / 1.5, 512 experts of Q8_0 1280 x 2560 took, in us (in
+    // parentheses the best of all widths), 20,480 rows 372 / 372 / 388 / 392 (372 / 370 / 388 / 392), 5120 rows
+    // 319 / 318 / 310 / 285 (319 / 318 / 306 / 279), 60,000 rows 582 / 639 / 658 / 663 (535 / 617 / 634 / 663); of
+    // 2560 x 640 in fp32 7000 rows 269 / 269 / 270 / 262 (268 / 268 / 266 / 253).
     const double mean = n_experts ? double(n_slots) / double(n_experts) : 0.0, spread = std::sqrt(mean + 0.25 * mean * mean);
     for (int bn = 32; bn <= gemm_most_tokens(fmt, f32, gemm_sets(f32, int(n_in))); bn += 16) {
         // (An expert's tile has no more tokens than the expert.)

@@ -8,7 +8,7 @@
 //     into one ring and the tokens' operand (staged by stage_kernel, qgemm.cu) into another;
 //   * groups of four warps turn the codes into 16-bit floats, a lane a row, a group a step, and put
 //     them into tensor memory, from where the products take them: through shared memory, which
-//     bounded the kernel, it was 32 of a step's 58 KB there (Q8_0, 32 tokens: 270 ns a step, now 204);
+//     bounded the kernel, it was 32 of a step's 58 KB there (Q8_0, 32 tokens: 270 ns a step, now 209);
 //   * one thread issues the products;
 //   * eight warps empty the accumulators, of which there are two sets, so that a tile's epilogue
 //     runs beside the next one's products.
@@ -16,13 +16,14 @@
 // Where tiles are few, a cluster of up to eight CTAs shares each tile's K; they join their sums through
 // one another's shared memory, in the order of K (2560 x 6144, 17 tokens fp32: 61 -> 17 us).
 //
-// What bounds it.  Quantized weights with many tokens: the decoding (Q8_0: 215 ns a step whatever
-// the tokens; instructions are issued in 64 % of the clocks, the tensor cores work in 60 %), and for tiles of
-// 128 tokens and more the way of the operands into the SM, about 60 bytes a clock: Q8_0, bf16, 10240 x 2560,
-// 8191 tokens 317 to 339 us, 1270 to 1355 TFLOP/s; bf16 weights, which need no decoding, 2560 x 6144, 8191
-// tokens 155 us, 1654 TFLOP/s.  fp32: its three products and the sums' moves to registers, 2047 tokens of
-// 2560 x 12288 with swiglu 328 us.  Experts: their weights' way from memory (61 tokens of ten experts out of 512,
-// 1.22 GB: 221 us, 5.5 TB/s; 2048 tokens, 1.82 GB: 375 us, 4.8 TB/s), with 40 rows each and more beside the
+// What bounds it.  Quantized weights with many tokens: the decoding (Q8_0: 209 to 213 ns a step up to 96
+// tokens; instructions are issued in 69 % of the clocks, the tensor cores work in 60 %), which every tile
+// of tokens does anew, and for tiles of 128 tokens and more the way of the operands into the SM, about 60 bytes
+// a clock: Q8_0, bf16, 10240 x 2560, 8191 tokens 340 us, 1260 TFLOP/s (318 us, 1350 TFLOP/s where the same
+// buffers come again); bf16 weights, which need no decoding, 262 us, 1640 TFLOP/s, 2560 x 6144 158 us (the same buffers
+// again).  fp32: its three products and the sums' moves to registers, 2047 tokens of
+// 2560 x 12288 with swiglu 327 us.  Experts: their weights' way from memory (61 tokens of ten experts out of 512,
+// 1.22 GB: 221 us, 5.5 TB/s; 2048 tokens, 1.82 GB: 378 us, 4.8 TB/s), with 40 rows each and more beside the
 // decoding.  A few tokens: two launches, the first copies and the join.
 //
 // Tried and not kept: five decoding groups (10240 x 2560, 8191 tokens 320 -> 333 us); raw codes in rows of 128

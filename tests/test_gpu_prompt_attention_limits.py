@@ -216,3 +216,20 @@ def test_a_factor_of_zero(act, D):
     out, lse = run(q, k, v, [0, 200], 0.0)
     assert np.abs(host(lse) - np.log(np.arange(1, 201))[:, None]).max() <= 2.0 ** -18
     check(q, k, v, [0, 200], 0.0, 0, out, lse)
+
+
+# ------------------------------------------------------------------------------ lengths
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_bad_prompts_are_reported_fp32(D):
+    """Lengths that shrink or leave the tokens, whose powers of two nobody has written, are reported."""
+    rng = np.random.default_rng(48)
+    q, k, v = inputs(rng, 40, 2, 1, D, "f32")
+    out, ws = torch.zeros(40, 2, D, device="cuda"), torch.full((qg.qg_prompt_attention_workspace_bytes("f32", 40, 2, 1, D),), 0xFF,
+                                                               dtype=torch.uint8, device="cuda")
+    for cu in ([0, 20, 10, 40], [-1, 20, 40], [0, 20, 41], [30, 10], [0, 1 << 30]):
+        qg.qg_prompt_attention(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), out, ws, 0.1, 40)
+        torch.cuda.synchronize()
+        assert qg.qg_device_status(clear=True) == qg.QG_DEVICE_BAD_LENGTH
+    good, lse = run(q, k, v, [0, 40], 0.1)
+    check(q, k, v, [0, 40], 0.1, 0, good, lse)
