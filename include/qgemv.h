@@ -505,9 +505,10 @@ qg_status qg_attention(const qg_cache* cache, qg_act act, const void* q, int64_t
  * Sums are fp32; the tensor cores cut off a bit (2^-23 of the sum) with every 16 products that they add, in chains of 256
  * products with fp32 activations (2^-19 at most), of 16384 at most with bf16 ones (2^-13).  fp32
  * activations enter as two 16-bit terms each of x and W (22 bits of x below the row's largest value; all bits of
- * W, of affine weights 22; bf16 weights: all 24 bits of x); bf16 ones as they are, weights of the quantized formats then
- * rounded to 11 bits (2^-11 of each at most).  Values of x below 2^-39 of their row's largest count as zero.  Quantized
- * weights of magnitude 65520 and more, which qgemv multiplies, are beyond fp16: their outputs are infinite or NaN.
+ * W, of affine weights 22), with bf16 weights as three (all 24 bits of x; of values below 2^-109 those above
+ * 2^-133); bf16 ones as they are, weights of the quantized formats then rounded to 11 bits (2^-11 of each at most).
+ * Values of x below 2^-39 of their row's largest count as zero with quantized weights.  Quantized weights of
+ * magnitude 65520 and more, which qgemv multiplies, are beyond fp16: their outputs are infinite or NaN.
  * Inputs that are not finite make the outputs they enter not finite.  A token's outputs do not depend on the other
  * tokens' values; the order of a sum depends on the call's sizes and the GPU's number of SMs; outputs are the
  * same on every run.
@@ -561,7 +562,7 @@ qg_status qg_describe_gemm_tile(qg_fmt fmt, qg_act act, int64_t n_out, int64_t n
  *   n_seq <= 16384; n_heads a multiple of n_kv_heads, at most 128 to one key/value head.
  * bf16: products are exact, sums fp32, probabilities rounded to bf16 (their sum and lse are not).  fp32:
  * a token's query, key or value of a head as two fp16 terms, 22 bits of its largest element and nothing below 2^-32 of
- * it; probabilities as two terms, down to 2^-31 of the row's largest, times the largest value that the row sees among 64
+ * it or 2^-145; probabilities as two terms, down to 2^-31 of the row's largest, times the largest value that the row sees among 64
  * tokens.  Values may be any finite ones; in bf16 a row's largest times the number of its keys is below 2^128.
  * Outputs are the same on every run, and do not depend on the other prompts of the call.
  * A masked key or value (of a later token, beyond the window, of another prompt) has no effect whatever
