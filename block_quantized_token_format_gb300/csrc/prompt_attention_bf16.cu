@@ -33,7 +33,7 @@ namespace qg {
 namespace {
 
 constexpr int kItems = 4;          // that the copying warp may be ahead
-constexpr float kSlack = 8.0f;     // log2: how far scores may pass the reference; P is 2^-8 times the exponential, at most 1
+constexpr float kSlack = 8.0f, kUnslack = 256.0f;     // log2: how far scores may pass the reference; P is 2^-8 times the exponential, at most 1
 
 template <int D> struct Shape {
     static constexpr int KT = 64, STAGES = 2, SB = 2;
@@ -226,7 +226,7 @@ template <int D> __global__ void __launch_bounds__(Shape<D>::THREADS, D == 256 ?
                     for (int n = 0; n < 16; ++n) w[n] = pack_bf16(y[2 * n], y[2 * n + 1]);
                     store_rows(to + d, r.there, w, lane);
                 }
-                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = (top + kSlack) * kLn2 + logf(sum);
+                if (r.there && a.lse && half == 0) a.lse[token * a.n_heads + head] = top * kLn2 + logf(sum * kUnslack);
             }
             give_back(n);
             ++n;

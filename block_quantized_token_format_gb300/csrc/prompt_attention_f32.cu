@@ -30,7 +30,7 @@ namespace qg {
 namespace {
 
 constexpr int kStageThreads = 256;
-constexpr float kSlack = 8.0f, kLift = 7.0f;     // log2: P is 2^7 times the exponential, at most 2^15
+constexpr float kSlack = 8.0f, kLift = 7.0f, kUnlift = 0.0078125f;     // log2: P is 2^7 times the exponential, at most 2^15
 constexpr int kTileKeys = 64, kStageRows = 4;
 
 template <int D> struct Shape {
@@ -373,7 +373,7 @@ template <int D> __global__ void __launch_bounds__(32 * (Shape<D>::WARPS + 2), 1
 #pragma unroll
                     for (int n = 0; n < 32; n += 4) *reinterpret_cast<float4*>(to + i + n) = make_float4(y[n], y[n + 1], y[n + 2], y[n + 3]);
                 }
-                if (a.lse && half == 0 && side == 0) a.lse[token * a.n_heads + head] = (top - kLift) * kLn2 + logf(sum);
+                if (a.lse && half == 0 && side == 0) a.lse[token * a.n_heads + head] = top * kLn2 + logf(sum * kUnlift);
             }
         }
         if (SIDES > 1 && dead) leave<SIDES>(rows);
