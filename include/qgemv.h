@@ -560,10 +560,12 @@ qg_status qg_describe_gemm_tile(qg_fmt fmt, qg_act act, int64_t n_out, int64_t n
  *   workspace    device, >= qg_prompt_attention_workspace_bytes(act, n_tok, n_heads, n_kv_heads, head_dim)
  *                bytes, 16-byte aligned; it need not be cleared.  Calls that share one must be serialized.
  *   n_seq <= 16384; n_heads a multiple of n_kv_heads, at most 128 to one key/value head.
- * bf16: products are exact, sums fp32, probabilities rounded to bf16 (their sum and lse are not).  fp32:
- * a token's query, key or value of a head as two fp16 terms, 22 bits of its largest element and nothing below 2^-32 of
- * it or 2^-145; probabilities as two terms, down to 2^-31 of the row's largest, times the largest value that the row sees among 64
- * tokens.  Values may be any finite ones; in bf16 a row's largest times the number of its keys is below 2^128.
+ * bf16: products are exact, probabilities rounded to bf16 (their sum and lse are not); sums are fp32, of which the tensor
+ * cores cut off a bit (2^-23 of sum p |v| at most) with every 16 keys: a few 2^-13 over 131072 keys.  fp32: a token's
+ * query, key or value of a head as two fp16 terms, 22 bits of its largest element and nothing below 2^-32 of it or
+ * 2^-145; probabilities as two terms, down to 2^-31 of the row's largest, times the largest value that the row sees
+ * among 64 tokens; sums in fp32 registers.  Values may be any finite ones; in bf16 a row's largest times the number of
+ * its keys is below 2^128.
  * Outputs are the same on every run, and do not depend on the other prompts of the call.
  * A masked key or value (of a later token, beyond the window, of another prompt) has no effect whatever
  * it holds; a visible value that is not finite makes the outputs that see it not finite.  A visible key, or a query, that is
